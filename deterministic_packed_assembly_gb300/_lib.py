@@ -1,7 +1,8 @@
-"""ctypes binding of ``libnspack.so`` (declared in ``include/nspack.h``).
+"""ctypes binding of ``libnspack.so`` (declared in ``include/nspack.h`` and, for
+the training operators, ``include/nstrain.h``).
 
-Argument marshalling only: every step of the packing path runs in the
-library's CUDA kernels.  There is no fallback: if the library is missing or
+Argument marshalling only: every step of the packing path and every operator
+runs in the library's CUDA kernels.  There is no fallback: if the library is missing or
 fails to load, importing this module raises.
 """
 from __future__ import annotations
@@ -26,6 +27,10 @@ NS_PACK_SHUFFLE_ROWS = 4
 NS_PACK_WRAP = 8
 NS_PACK_HOST_CORPUS = 16
 NS_PACK_ORDERED_FREE = 32
+NS_F32 = 0
+NS_BF16 = 1
+NS_F16 = 2
+NS_SCAN_TILE = 64
 NS_MAX_T = 1 << 24
 NS_MAX_TOKENS = 1 << 47
 
@@ -100,11 +105,63 @@ class ns_pack_info_t(C.Structure):
     ]
 
 
-# Every symbol the header declares, for the load check.
+class ns_scan_inputs(C.Structure):
+    _fields_ = [
+        ("z", C.c_void_p),
+        ("f", C.c_void_p),
+        ("z_row", C.c_int64),
+        ("z_time", C.c_int64),
+        ("f_row", C.c_int64),
+        ("f_time", C.c_int64),
+        ("bias", C.c_void_p),
+        ("pos", C.c_void_p),
+        ("doc", C.c_void_p),
+        ("B", C.c_uint32),
+        ("T", C.c_uint32),
+        ("D", C.c_uint32),
+        ("dtype", C.c_int32),
+    ]
+
+
+class ns_distill_inputs(C.Structure):
+    _fields_ = [
+        ("logits", C.c_void_p),
+        ("logits_row", C.c_int64),
+        ("top_logits", C.c_void_p),
+        ("top_ids", C.c_void_p),
+        ("teacher_lse", C.c_void_p),
+        ("mask", C.c_void_p),
+        ("weight", C.c_void_p),
+        ("N", C.c_uint32),
+        ("V", C.c_uint32),
+        ("K", C.c_uint32),
+        ("dtype", C.c_int32),
+        ("top_dtype", C.c_int32),
+        ("ids_64", C.c_int32),
+        ("temperature", C.c_float),
+    ]
+
+
+class ns_route_inputs(C.Structure):
+    _fields_ = [
+        ("logits", C.c_void_p),
+        ("logits_row", C.c_int64),
+        ("doc", C.c_void_p),
+        ("N", C.c_uint32),
+        ("E", C.c_uint32),
+        ("k", C.c_uint32),
+        ("dtype", C.c_int32),
+        ("normalize", C.c_int32),
+    ]
+
+
+# Every symbol the headers declare, for the load check.
 SYMBOLS = ("ns_pack_init", "ns_pack_step", "ns_pack_fingerprint", "ns_pack_batch_fp",
            "ns_pack_step_learned", "ns_pack_info", "ns_pack_stream_windows",
            "ns_pack_quota_table", "ns_pack_check", "ns_pack_free", "ns_pack_strerror",
-           "ns_pack_quota_noalloc", "ns_pack_probe_hash_terms")
+           "ns_pack_quota_noalloc", "ns_pack_probe_hash_terms",
+           "ns_scan_forward", "ns_scan_workspace", "ns_scan_backward", "ns_distill",
+           "ns_route_workspace", "ns_route_forward", "ns_route_backward")
 
 
 def _load() -> C.CDLL:
@@ -140,6 +197,23 @@ def _load() -> C.CDLL:
     L.ns_pack_probe_hash_terms.argtypes = [u32, u32, vp, vp]
     L.ns_pack_quota_noalloc.restype = i32
     L.ns_pack_quota_noalloc.argtypes = [vp, u32, vp, vp, u32, u32, u32, vp, vp, vp]
+    i64 = C.c_int64
+    scan, distill, route = (C.POINTER(t) for t in
+                            (ns_scan_inputs, ns_distill_inputs, ns_route_inputs))
+    L.ns_scan_forward.restype = i32
+    L.ns_scan_forward.argtypes = [scan, vp, vp, vp, vp, vp]
+    L.ns_scan_workspace.restype = u64
+    L.ns_scan_workspace.argtypes = [u32, u32, u32]
+    L.ns_scan_backward.restype = i32
+    L.ns_scan_backward.argtypes = [scan, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+    L.ns_distill.restype = i32
+    L.ns_distill.argtypes = [distill, vp, vp, i64, vp]
+    L.ns_route_workspace.restype = u64
+    L.ns_route_workspace.argtypes = [u32, u32]
+    L.ns_route_forward.restype = i32
+    L.ns_route_forward.argtypes = [route, vp, vp, vp, vp, vp, vp, vp]
+    L.ns_route_backward.restype = i32
+    L.ns_route_backward.argtypes = [route, vp, vp, vp, vp, vp, vp, vp, vp]
     return L
 
 
@@ -243,3 +317,38 @@ def ns_pack_probe_hash_terms(blocks: int, terms_per_thread: int, sum_dev: int,
     include/nspack_probe.h); adds its sum to the device u64 at sum_dev."""
     check(lib.ns_pack_probe_hash_terms(blocks, terms_per_thread, sum_dev, stream or None),
           "ns_pack_probe_hash_terms")
+
+
+# ---- training operators (include/nstrain.h) -----------------------------------
+def ns_scan_forward(inputs: ns_scan_inputs, h0, y, h_last, states, stream) -> None:
+    check(lib.ns_scan_forward(C.byref(inputs), h0, y, h_last, states, stream), "ns_scan_forward")
+
+
+def ns_scan_workspace(B: int, T: int, D: int) -> int:
+    return lib.ns_scan_workspace(B, T, D)
+
+
+def ns_scan_backward(inputs: ns_scan_inputs, states, dy, dy_row: int, dy_time: int, dh_last, dz,
+                     df, dbias, dh0, workspace, stream) -> None:
+    check(lib.ns_scan_backward(C.byref(inputs), states, dy, dy_row, dy_time, dh_last, dz, df, dbias,
+                               dh0, workspace, stream), "ns_scan_backward")
+
+
+def ns_distill(inputs: ns_distill_inputs, loss, dlogits, dlogits_row: int, stream) -> None:
+    check(lib.ns_distill(C.byref(inputs), loss, dlogits, dlogits_row, stream), "ns_distill")
+
+
+def ns_route_workspace(N: int, E: int) -> int:
+    return lib.ns_route_workspace(N, E)
+
+
+def ns_route_forward(inputs: ns_route_inputs, ids, weights, counts, tokens, loss, workspace,
+                     stream) -> None:
+    check(lib.ns_route_forward(C.byref(inputs), ids, weights, counts, tokens, loss, workspace,
+                               stream), "ns_route_forward")
+
+
+def ns_route_backward(inputs: ns_route_inputs, ids, weights, counts, tokens, d_weights, d_loss,
+                      dlogits, stream) -> None:
+    check(lib.ns_route_backward(C.byref(inputs), ids, weights, counts, tokens, d_weights, d_loss,
+                                dlogits, stream), "ns_route_backward")
