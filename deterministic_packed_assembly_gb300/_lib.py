@@ -30,7 +30,7 @@ NS_PACK_ORDERED_FREE = 32
 NS_F32 = 0
 NS_BF16 = 1
 NS_F16 = 2
-NS_SCAN_TILE = 64
+NS_SCAN_TILE = 32
 NS_MAX_T = 1 << 24
 NS_MAX_TOKENS = 1 << 47
 

@@ -3,26 +3,25 @@
 //   a_t = sigmoid(f_t + bias), h_t = a_t p_t + (1 - a_t) z_t,
 //   p_t = 0 where a sequence starts (pos 0), else h_{t-1}
 //
-// Each channel of each row is a chain of T steps.  A run of steps is the
-// affine map h -> A h + H of the state before it, and two runs compose, so a
-// chain is cut into segments of kSteps steps: a warp takes one segment of 32
-// (or 64) channels, a lane one (or two) channels of it, all kSteps steps in
-// registers; the block's eight warps take the eight segments of a tile, put
-// their (A, H) in shared memory, and each one composes those before its own.
-// Then it runs its steps again from the state it found (two multiply-adds a
-// step) and writes them, so every input is read once.  Blocks walk along
-// time; the loads of the next tile are in flight while a tile is computed.
-// Where rows and channels are too few to fill the GPU, a cluster of up to
-// eight blocks takes consecutive tiles and composes them through distributed
-// shared memory: no block waits for another outside its cluster.
+// Each channel of each row is a chain of T steps.  A run of steps is the affine
+// map h -> A h + H of the state before it, and two runs compose, so a chain is
+// cut into segments of kSteps steps: a warp takes one segment of 64 channels (32
+// of 32 bits), a lane two (one) of them, all kSteps steps in registers; the
+// block's eight warps take the eight segments of a tile, put their runs in shared
+// memory, and each one finds the state before its own.  Then it runs its steps
+// again from that state and writes them: every input is read once.  Blocks walk
+// along time, with asynchronous copies of the next two tiles in flight.  Where
+// rows and channels are too few to fill the GPU, a cluster of up to eight blocks
+// takes consecutive tiles and exchanges their runs through distributed shared
+// memory.
 //
-// A segment in which a sequence starts does not depend on the state before
-// it.  Its A is -0.0: the sign says so (a product of gates has none), and the
-// state before is then not used at all, so that a NaN of one document does
-// not reach the next.
+// A segment in which a sequence starts does not depend on the state before it;
+// that state is then not used at all (not even times 0), so that a NaN of one
+// document does not reach the next.
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -37,7 +36,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = kSteps * kWarps;
 constexpr int kMaxCluster = 8;
-static_assert(kTile == NS_SCAN_TILE, "states are saved at every tile");
+constexpr int kShortThreads = 256;
+constexpr int kBiasWarps = 8;
+constexpr uint64_t kEnough = 304;  // blocks: two on each of 152 SMs
+static_assert(NS_SCAN_TILE % kSteps == 0, "states are saved at the start of a segment");
+constexpr int kSaveEvery = NS_SCAN_TILE / kSteps;  // segments between two saved states
 
 struct ScanParams {
   const void *z, *f;
@@ -47,6 +50,7 @@ struct ScanParams {
   uint32_t B, T, D;
   uint32_t groups;  // of 32 lanes' channels
   uint32_t split;   // blocks of a cluster, along time
+  bool wide;        // rows are copied 16 bytes at a time
   // forward
   const float *h0;
   void *y;
@@ -61,219 +65,581 @@ struct ScanParams {
   float *partial, *dh0;
 };
 
-// a = sigmoid(x) and c = 1 - a = sigmoid(-x), neither by a subtraction that
-// cancels: the small one of the two is exp(-|x|) / (1 + exp(-|x|)).
-__device__ __forceinline__ void gate(float x, float &a, float &c) {
-  const float e = exp2_sfu(-fabsf(x) * kLog2e);
-  const float r = rcp_sfu(1.0f + e);
-  const float small = e * r;
-  const float large = 1.0f - small;  // the exact sum of both is 1
-  const bool up = x >= 0.0f;
-  a = up ? large : small;
-  c = up ? small : large;
+// A lane's one or two channels; two are computed by the packed instructions.
+template <int CH>
+struct Ch;
+template <>
+struct Ch<1> {
+  float v[1];
+};
+template <>
+struct alignas(8) Ch<2> {
+  float v[2];
+};
+__device__ __forceinline__ uint64_t bits(Ch<2> a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.v[0]), "f"(a.v[1]));
+  return r;
 }
-
-// The state after a run (A, H) that found the state h.
-__device__ __forceinline__ float run_state(float A, float H, float h) {
-  return __float_as_int(A) < 0 ? H : fmaf(A, h, H);
+__device__ __forceinline__ Ch<2> unbits(uint64_t r) {
+  Ch<2> a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.v[0]), "=f"(a.v[1]) : "l"(r));
+  return a;
 }
-
-// One warp's segment of a tile as it lies in memory.
+__device__ __forceinline__ Ch<1> fma(Ch<1> a, Ch<1> b, Ch<1> c) {
+  return {fmaf(a.v[0], b.v[0], c.v[0])};
+}
+__device__ __forceinline__ Ch<2> fma(Ch<2> a, Ch<2> b, Ch<2> c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return unbits(r);
+}
+__device__ __forceinline__ Ch<1> operator*(Ch<1> a, Ch<1> b) { return {a.v[0] * b.v[0]}; }
+__device__ __forceinline__ Ch<2> operator*(Ch<2> a, Ch<2> b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return unbits(r);
+}
+__device__ __forceinline__ Ch<1> operator+(Ch<1> a, Ch<1> b) { return {a.v[0] + b.v[0]}; }
+__device__ __forceinline__ Ch<2> operator+(Ch<2> a, Ch<2> b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return unbits(r);
+}
+template <int CH>
+__device__ __forceinline__ Ch<CH> splat(float x) {
+  Ch<CH> r;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) r.v[k] = x;
+  return r;
+}
+// a - b, as a + (-1) b: exact as a subtraction
+template <int CH>
+__device__ __forceinline__ Ch<CH> sub(Ch<CH> a, Ch<CH> b) {
+  return fma(b, splat<CH>(-1.0f), a);
+}
+template <int CH>
+__device__ __forceinline__ Ch<CH> pick(bool first, Ch<CH> a, Ch<CH> b) {
+  Ch<CH> r;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) r.v[k] = first ? a.v[k] : b.v[k];
+  return r;
+}
+// A lane's channels of one step as they lie in memory: a pair of 16-bit ones in
+// one register.  (A 32-bit lane takes one channel: its bytes are the same, and the
+// registers of a second one are worth more than the packed instructions.)
 template <class E, int CH>
-struct Segment {
-  Vec<E, CH> z[kSteps], f[kSteps];
-  int posv, docv;  // of step `lane`
-  int n;           // steps inside the row
+struct RawOf;
+template <class E>
+struct RawOf<E, 1> {
+  using type = E;
+};
+template <>
+struct RawOf<__nv_bfloat16, 2> {
+  using type = uint32_t;
+};
+template <>
+struct RawOf<__half, 2> {
+  using type = uint32_t;
+};
+template <class E, int CH>
+using Raw = typename RawOf<E, CH>::type;
+
+template <class E, int CH>
+__device__ __forceinline__ Ch<CH> widen(Raw<E, CH> x) {
+  if constexpr (CH == 1) {
+    return {to_f32(x)};
+  } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+    return {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
+  } else {
+    const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&x));
+    return {v.x, v.y};
+  }
+}
+template <class E, int CH>
+__device__ __forceinline__ Raw<E, CH> narrow(Ch<CH> x) {
+  if constexpr (CH == 1) {
+    return from_f32<E>(x.v[0]);
+  } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x.v[0], x.v[1]);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(x.v[0], x.v[1]);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+}
+template <int CH>
+__device__ __forceinline__ Ch<CH> load_channels(const float *src, int64_t off, bool live) {
+  Ch<CH> r = splat<CH>(0.0f);
+  if (src && live) r = *reinterpret_cast<const Ch<CH> *>(src + off);
+  return r;
+}
+template <int CH>
+__device__ __forceinline__ void store_channels(float *dst, int64_t off, bool live, Ch<CH> v) {
+  if (dst && live) *reinterpret_cast<Ch<CH> *>(dst + off) = v;
+}
+
+// With x = f + bias and e = exp(-x): r = 1 / (1 + e) = sigmoid(x), c = e r =
+// sigmoid(-x), both to 2 ulp whatever x is, and a = 1 - c, so that a and c add
+// up to 1 to the last bit: an error of r near 1 would build up over 1 / c steps.
+// nb = -bias log2 e.  e is kept finite (at most 2^120) where it would not be;
+// a NaN stays one.
+template <int CH>
+__device__ __forceinline__ void gate(Ch<CH> f, Ch<CH> nb, Ch<CH> &r, Ch<CH> &c, Ch<CH> &a) {
+  const Ch<CH> t = fma(f, splat<CH>(-kLog2e), nb);
+  Ch<CH> e;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    float m;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(t.v[k]), "f"(120.0f));
+    e.v[k] = exp2_sfu(m);
+  }
+  const Ch<CH> d = e + splat<CH>(1.0f);
+#pragma unroll
+  for (int k = 0; k < CH; ++k) r.v[k] = rcp_sfu(d.v[k]);
+  c = e * r;
+  a = sub(splat<CH>(1.0f), c);
+}
+
+// A warp's ring of segments in shared memory, filled by asynchronous copies that
+// run kRing - 1 tiles ahead: A arrays (z, f and, backward, dy) of kSteps rows.
+// (Prefetched into registers instead, the backward kernel spilled at 128 of them
+// and ran 16 warps an SM.)
+constexpr int kRing = 3;
+template <class E, int CH, int A>
+struct alignas(16) Stage {
+  Raw<E, CH> v[A][kSteps][32];
 };
 
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
+}
+
+// One array's copies: a lane's part of the segment that is copied next.  `wide`:
+// rows, strides and widths are multiples of 16 bytes, and a lane copies 16 bytes
+// of every fourth row; else its own channels of every row (a single 16-bit one,
+// which no asynchronous copy takes, by way of a register).
 template <class E, int CH>
-__device__ __forceinline__ void load_segment(const ScanParams &p, uint32_t b, int64_t t0,
-                                             uint32_t c0, bool live, int lane,
-                                             Segment<E, CH> &s) {
-  const int64_t left = (int64_t)p.T - t0;
-  s.n = left < 0 ? 0 : left > kSteps ? kSteps : (int)left;
-  s.posv = 1;
-  s.docv = 0;
-  if (lane < s.n) {
-    const int64_t i = (int64_t)b * p.T + t0 + lane;
-    if (p.pos) s.posv = __ldg(p.pos + i);
-    if (p.doc) s.docv = __ldg(p.doc + i);
-  }
-  const E *z = static_cast<const E *>(p.z) + (int64_t)b * p.z_row + t0 * p.z_time + c0;
-  const E *f = static_cast<const E *>(p.f) + (int64_t)b * p.f_row + t0 * p.f_time + c0;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    if (live && i < s.n) {
-      s.z[i] = *reinterpret_cast<const Vec<E, CH> *>(z + i * p.z_time);
-      s.f[i] = *reinterpret_cast<const Vec<E, CH> *>(f + i * p.f_time);
-    }
-  }
-}
+struct Copier {
+  static constexpr int kN = 16 / sizeof(E), kPerRow = 32 * CH / kN;
+  static constexpr int kRows = kPerRow <= 32 ? 32 / kPerRow : 1;
+  const E *from;
+  int64_t time, step;  // elements to the next row, and to the next segment
+  bool in;             // this lane has channels to copy
 
-// Bit i: a sequence starts at step i / step i is padding or past the row.
-template <class E, int CH>
-__device__ __forceinline__ void segment_flags(const Segment<E, CH> &s, int lane, uint32_t &reset,
-                                              uint32_t &skip) {
-  skip = __ballot_sync(0xffffffffu, lane >= s.n || s.docv < 0);
-  reset = __ballot_sync(0xffffffffu, s.posv == 0) & ~skip;
-}
-
-// Gates and inputs of a segment; at skipped steps a = 1, c = 0, z = 0.
-template <class E, int CH>
-__device__ __forceinline__ void segment_gates(const Segment<E, CH> &s, const float (&bias)[CH],
-                                              uint32_t skip, float (&a)[kSteps][CH],
-                                              float (&c)[kSteps][CH], float (&z)[kSteps][CH]) {
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const bool out = (skip >> i) & 1u;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      gate(to_f32(s.f[i].v[k]) + bias[k], a[i][k], c[i][k]);
-      z[i][k] = to_f32(s.z[i].v[k]);
-      if (out) a[i][k] = 1.0f, c[i][k] = 0.0f, z[i][k] = 0.0f;
-    }
+  // src: the group's first channel at the first segment's first step.
+  __device__ __forceinline__ void set(const E *src, int64_t row_time, int64_t to_next,
+                                      uint32_t width, bool wide, int lane) {
+    const int row = wide ? lane / kPerRow : 0, at = wide ? lane % kPerRow * kN : lane * CH;
+    from = src + row * row_time + at;
+    time = row_time;
+    step = to_next * row_time;
+    in = (uint32_t)at < width;
   }
-}
-
-template <int CH>
-__device__ __forceinline__ void load_channels(const float *src, int64_t off, bool live,
-                                              float (&v)[CH]) {
+  // Copy steps [0, n) and move on.
+  __device__ __forceinline__ void copy(int n, bool wide, int lane, Raw<E, CH> (&dst)[kSteps][32]) {
+    if (wide) {
+      const int row = lane / kPerRow;
+      E *to = reinterpret_cast<E *>(dst) + lane * kN;
 #pragma unroll
-  for (int k = 0; k < CH; ++k) v[k] = 0.0f;
-  if (src && live) {
-    const Vec<float, CH> x = *reinterpret_cast<const Vec<float, CH> *>(src + off);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) v[k] = x.v[k];
-  }
-}
-template <int CH>
-__device__ __forceinline__ void store_channels(float *dst, int64_t off, bool live,
-                                               const float (&v)[CH]) {
-  if (!dst || !live) return;
-  Vec<float, CH> x;
-#pragma unroll
-  for (int k = 0; k < CH; ++k) x.v[k] = v[k];
-  *reinterpret_cast<Vec<float, CH> *>(dst + off) = x;
-}
-
-// The runs of a tile's segments, or of a cluster's tiles, of 32 * CH channels.
-template <int CH>
-using Runs = float2[32 * CH];
-
-template <class E, int CH, bool kCluster>
-__global__ void __launch_bounds__(kThreads) scan_forward_kernel(const ScanParams p) {
-  __shared__ Runs<CH> seg[2][kWarps];
-  __shared__ Runs<CH> tile[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t rank = kCluster ? blockIdx.x % p.split : 0;
-  const uint32_t unit = kCluster ? blockIdx.x / p.split : blockIdx.x;
-  const uint32_t b = unit / p.groups, c0 = (unit % p.groups) * 32 * CH + lane * CH;
-  const bool live = c0 < p.D;
-  const int64_t nt = ((int64_t)p.T + kTile - 1) / kTile;
-  if (kCluster) {  // the other blocks' shared memory is written to: they run
-    cluster_arrive();
-    cluster_wait();
-  }
-  float bias[CH], h[CH];
-  load_channels<CH>(p.bias, c0, live, bias);
-  load_channels<CH>(p.h0, (int64_t)b * p.D + c0, live, h);
-  Segment<E, CH> next;
-  load_segment<E, CH>(p, b, (int64_t)rank * kTile + warp * kSteps, c0, live, lane, next);
-  int buf = 0;
-  for (int64_t i = 0; i < nt; i += kCluster ? p.split : 1, buf ^= 1) {
-    const int64_t j = i + rank;  // this block's tile: may lie past the last one
-    const int64_t t0 = j * kTile + warp * kSteps;
-    uint32_t reset, skip;
-    float a[kSteps][CH], c[kSteps][CH], z[kSteps][CH];
-    segment_flags<E, CH>(next, lane, reset, skip);
-    segment_gates<E, CH>(next, bias, skip, a, c, z);
-    const int n = next.n;
-    load_segment<E, CH>(p, b, t0 + (int64_t)(kCluster ? p.split : 1) * kTile, c0, live, lane,
-                        next);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      float A = 1.0f, H = 0.0f;
+      for (int s = 0; s < kSteps; s += kRows)
+        if (in && s + row < n) copy_async<16>(to + s * 32 * CH, from + s * time);
+    } else {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const bool start = (reset >> s) & 1u;
-        H = fmaf(a[s][k], start ? 0.0f : H, c[s][k] * z[s][k]);
-        A = start ? -0.0f : A * a[s][k];
+        if (in && s < n) {
+          if constexpr (sizeof(E) * CH == 4)
+            copy_async<4>(&dst[s][lane], from + s * time);
+          else
+            dst[s][lane] = from[s * time];
+        }
       }
-      seg[buf][warp][lane * CH + k] = make_float2(A, H);
     }
+    from += step;
+  }
+};
+
+// Steps inside the row from t on, at most kSteps.
+__device__ __forceinline__ int steps_at(int T, int t) {
+  return t < 0 ? 0 : min(max(T - t, 0), kSteps);
+}
+
+// Where sequences start and what is skipped (padding, steps past the row), for
+// the segments that a warp takes one after the other, `step` apart: bits of four
+// segments are read at once, a byte each, and four segments ahead.
+struct Flags {
+  const int32_t *pos, *doc;  // of the row
+  int T, t, step;            // t: the first step of the next four segments, in this lane
+  int posv, docv;
+  uint32_t start, skip;
+
+  __device__ __forceinline__ void load() {
+    const bool in = t >= 0 && t < T;
+    posv = in && pos ? __ldg(pos + t) : 1;
+    docv = in ? (doc ? __ldg(doc + t) : 0) : -1;
+    t += 4 * step;
+  }
+  __device__ __forceinline__ void set(const ScanParams &p, uint32_t b, int t0, int to_next,
+                                      int lane) {
+    pos = p.pos ? p.pos + (int64_t)b * p.T : nullptr;
+    doc = p.doc ? p.doc + (int64_t)b * p.T : nullptr;
+    T = (int)p.T;
+    step = to_next;
+    t = t0 + lane / kSteps * to_next + lane % kSteps;
+    load();
+  }
+  // Before segment i of the walk.
+  __device__ __forceinline__ void next(int i) {
+    if ((i & 3) == 0) {
+      skip = __ballot_sync(0xffffffffu, docv < 0);
+      start = __ballot_sync(0xffffffffu, posv == 0) & ~skip;
+      load();
+    } else {
+      skip >>= kSteps;
+      start >>= kSteps;
+    }
+  }
+};
+static_assert(kSteps == 8, "a segment's flags are a byte");
+
+// A run of steps maps the state h before it to A h + H, or, where a sequence
+// starts inside (`cut`), to H alone.
+template <int CH>
+struct alignas(8 * CH) Run {
+  Ch<CH> A, H;
+};
+template <int CH>
+__device__ __forceinline__ Ch<CH> after(const Run<CH> &r, bool cut, Ch<CH> h) {
+  return cut ? r.H : fma(r.A, h, r.H);
+}
+// Runs that warps or blocks exchange, N of them for every lane's channels.
+template <int CH, int N>
+struct Exchange {
+  Run<CH> run[N][32];
+  uint32_t cut[N];
+};
+
+// A quad is four consecutive segments: NS_SCAN_TILE steps from a multiple of
+// them, between two saved states.  The states at these boundaries are chained by
+// the quads' runs, whichever blocks computed them, and the states inside follow
+// from the one at the quad's start.  So a row's results do not depend on how
+// its quads were shared out, nor on the other rows of the call.
+constexpr int kQuad = kSaveEvery;
+constexpr int kQuads = kWarps / kQuad;  // of a tile
+
+template <int CH>
+__device__ __forceinline__ Run<CH> quad_run(const Exchange<CH, kWarps> &x, int quad, int lane,
+                                            uint32_t cuts) {
+  Run<CH> all = x.run[quad * kQuad][lane];
+  if (cuts == 0) {
+#pragma unroll
+    for (int k = 1; k < kQuad; ++k) {
+      const Run<CH> r = x.run[quad * kQuad + k][lane];
+      all.H = fma(r.A, all.H, r.H);
+      all.A = all.A * r.A;
+    }
+  } else {
+#pragma unroll
+    for (int k = 1; k < kQuad; ++k) {
+      const Run<CH> r = x.run[quad * kQuad + k][lane];
+      all.H = after(r, x.cut[quad * kQuad + k] != 0, all.H);
+    }
+  }
+  return all;
+}
+// Nonzero where a sequence starts in the quad.
+template <int CH>
+__device__ __forceinline__ uint32_t quad_cuts(const Exchange<CH, kWarps> &x, int quad) {
+  const uint4 c = *reinterpret_cast<const uint4 *>(&x.cut[quad * kQuad]);
+  return c.x | c.y | c.z | c.w;
+}
+// The state before this warp's segment, from the one before its quad.
+template <int CH>
+__device__ __forceinline__ Ch<CH> inside_quad(const Exchange<CH, kWarps> &x, int lane, int warp,
+                                              uint32_t cuts, Ch<CH> h) {
+  const int first = warp / kQuad * kQuad;
+#pragma unroll
+  for (int k = 0; k < kQuad - 1; ++k)
+    if (first + k < warp)  // the same for the warp
+      h = after(x.run[first + k][lane], cuts != 0 && x.cut[first + k] != 0, h);
+  return h;
+}
+
+// The state before this warp's segment, and h moved on past the tile: in a
+// block alone ...
+template <int CH>
+__device__ __forceinline__ Ch<CH> pass_block(const Exchange<CH, kWarps> &x, int lane, int warp,
+                                             Ch<CH> &h) {
+  Ch<CH> mine = h;
+  uint32_t my_cuts = 0;
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const uint32_t cuts = quad_cuts(x, q);
+    if (q == warp / kQuad) mine = h, my_cuts = cuts;
+    h = after(quad_run(x, q, lane, cuts), cuts != 0, h);
+  }
+  return inside_quad(x, lane, warp, my_cuts, mine);
+}
+
+// ... and in a cluster whose blocks took consecutive tiles, where every quad's run
+// is stored into every block, asynchronously: the stores themselves count down
+// the barrier that the receiving block's warps wait at.  (A cluster barrier in
+// its place has each warp wait for its earlier stores to global memory: a quarter
+// of the stalls.)  A block sends for round i + 2 when it has everything of round
+// i + 1, which the others sent after they had read round i: two buffers do.
+template <int CH>
+struct Quads {
+  Exchange<CH, kMaxCluster * kQuads> x;
+  uint64_t arrived;  // an mbarrier
+};
+
+__device__ __forceinline__ void barrier_init(uint64_t *bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(bar))
+               : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// Wait for the phase of this parity; false if it has not come after about a second.
+__device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(bar);
+  for (int i = 0; i < 100000; ++i) {  // each try suspends for some microseconds at most
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+template <int CH>
+__device__ __forceinline__ void send_run(uint32_t to, uint32_t bar, Run<CH> r) {
+  if constexpr (CH == 2) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+        "[%5];" ::"r"(to),
+        "f"(r.A.v[0]), "f"(r.A.v[1]), "f"(r.H.v[0]), "f"(r.H.v[1]), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+            to),
+        "f"(r.A.v[0]), "f"(r.H.v[0]), "r"(bar)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void send_word(uint32_t to, uint32_t bar, uint32_t v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                   to),
+               "r"(v), "r"(bar)
+               : "memory");
+}
+
+template <int CH>
+__device__ __forceinline__ Ch<CH> pass_cluster(const Exchange<CH, kWarps> &x, Quads<CH> &quads,
+                                               uint32_t parity, bool &lost, uint32_t rank,
+                                               uint32_t split, int lane, int warp, Ch<CH> &h) {
+  const int quad = warp / kQuad;
+  const uint32_t cuts = quad_cuts(x, quad);
+  const Run<CH> all = quad_run(x, quad, lane, cuts);
+  const uint32_t self = rank * kQuads + quad, count = split * kQuads;
+  if (threadIdx.x == 0) barrier_expect(&quads.arrived, count * (32 * sizeof(Run<CH>) + 4));
+  for (uint32_t to = warp % kQuad; to < split; to += kQuad) {
+    const uint32_t bar = remote_smem(&quads.arrived, to);
+    send_run<CH>(remote_smem(&quads.x.run[self][lane], to), bar, all);
+    if (lane == 0) send_word(remote_smem(&quads.x.cut[self], to), bar, cuts);
+  }
+  if (!lost && !barrier_wait(&quads.arrived, parity)) lost = true;
+  const uint32_t any =
+      __ballot_sync(0xffffffffu, (uint32_t)lane < count && quads.x.cut[lane] != 0);
+  Ch<CH> mine = h;
+  if (any == 0) {
+#pragma unroll 4
+    for (uint32_t q = 0; q < count; ++q) {
+      if (q == self) mine = h;
+      const Run<CH> r = quads.x.run[q][lane];
+      h = fma(r.A, h, r.H);
+    }
+  } else {
+    for (uint32_t q = 0; q < count; ++q) {
+      if (q == self) mine = h;
+      h = after(quads.x.run[q][lane], (any >> q) & 1u, h);
+    }
+  }
+  if (lost) mine = h = splat<CH>(__int_as_float(0x7fffffff));  // shows in every output
+  return inside_quad(x, lane, warp, cuts, mine);
+}
+
+// Blocks of an SM: 24 warps forward (80 registers), 16 backward (128).
+constexpr int kForwardBlocks = 24 / kWarps, kBackwardBlocks = 16 / kWarps;
+
+// Where a block works: a group of 32 lanes' channels of a row, and with others of
+// its cluster every split-th tile.
+struct Place {
+  int lane, warp;
+  uint32_t rank, b, cg, c0;
+  bool live;
+};
+template <int CH, bool kCluster>
+__device__ __forceinline__ Place place_of(const ScanParams &p) {
+  Place at;
+  at.lane = threadIdx.x & 31, at.warp = threadIdx.x >> 5;
+  at.rank = kCluster ? blockIdx.x % p.split : 0;
+  const uint32_t unit = kCluster ? blockIdx.x / p.split : blockIdx.x;
+  at.b = unit / p.groups, at.cg = (unit % p.groups) * 32 * CH, at.c0 = at.cg + at.lane * CH;
+  at.live = at.c0 < p.D;
+  return at;
+}
+
+template <int CH>
+__device__ __forceinline__ void cluster_begin(Quads<CH> (&quads)[2]) {
+  if (threadIdx.x == 0) {
+    barrier_init(&quads[0].arrived);
+    barrier_init(&quads[1].arrived);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_arrive();  // the others' barriers are there before anything is sent
+  cluster_wait();
+}
+
+template <class E, int CH, bool kCluster>
+__global__ void __launch_bounds__(kThreads, kForwardBlocks)
+    scan_forward_kernel(const ScanParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) Exchange<CH, kWarps> seg[2];
+  __shared__ __align__(16) unsigned char quads_mem[kCluster ? 2 * sizeof(Quads<CH>) : 16];
+  Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
+  const Place at = place_of<CH, kCluster>(p);
+  const int lane = at.lane, warp = at.warp;
+  Stage<E, CH, 2> *ring = reinterpret_cast<Stage<E, CH, 2> *>(smem) + warp * kRing;
+  if (kCluster) cluster_begin<CH>(quads);
+  const int T = (int)p.T, stride = kCluster ? (int)p.split : 1, step = stride * kTile;
+  const int rounds = ((T + kTile - 1) / kTile + stride - 1) / stride;
+  int t = (int)at.rank * kTile + warp * kSteps;  // may lie past the row
+  Copier<E, CH> cz_in, cf_in;
+  cz_in.set(static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg, p.z_time,
+            step, p.D - at.cg, p.wide, lane);
+  cf_in.set(static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg, p.f_time,
+            step, p.D - at.cg, p.wide, lane);
+  auto fetch = [&](int at_step, Stage<E, CH, 2> &to) {
+    const int n = steps_at(T, at_step);
+    cz_in.copy(n, p.wide, lane, to.v[0]);
+    cf_in.copy(n, p.wide, lane, to.v[1]);
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kRing - 1; ++k) fetch(t + k * step, ring[k]);
+  Flags flags;
+  flags.set(p, at.b, t, step, lane);
+  const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
+  Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
+  E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
+  float *state = nullptr;  // the state before a quad is its first warp's to save
+  if (p.states && warp % kQuad == 0)
+    state = p.states + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
+                        t / NS_SCAN_TILE) * p.D + at.c0;
+  int slot = 0;
+  bool lost = false;
+  for (int i = 0; i < rounds; ++i, t += step) {
+    __syncwarp();  // the slot that is filled now was read in the last round
+    fetch(t + (kRing - 1) * step, ring[slot == 0 ? kRing - 1 : slot - 1]);
+    flags.next(i);
+    const uint32_t start = flags.start & 0xffu, skip = flags.skip & 0xffu;
+    const bool plain = (start | skip) == 0;  // the same for the warp
+    copy_wait<kRing - 1>();
+    __syncwarp();
+    const Stage<E, CH, 2> &in_smem = ring[slot];
+    slot = slot == kRing - 1 ? 0 : slot + 1;
+    Ch<CH> a[kSteps], cz[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      Ch<CH> r, c;
+      gate<CH>(widen<E, CH>(in_smem.v[1][s][lane]), nb, r, c, a[s]);
+      cz[s] = c * widen<E, CH>(in_smem.v[0][s][lane]);
+    }
+    Run<CH> run;
+    if (plain) {
+      run.H = cz[0], run.A = a[0];
+#pragma unroll
+      for (int s = 1; s < kSteps; ++s) {
+        run.H = fma(a[s], run.H, cz[s]);
+        run.A = run.A * a[s];
+      }
+    } else {
+      run.H = splat<CH>(0.0f), run.A = splat<CH>(1.0f);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const bool out = (skip >> s) & 1u;
+        a[s] = pick(out, splat<CH>(1.0f), a[s]);
+        cz[s] = pick(out, splat<CH>(0.0f), cz[s]);
+        run.H = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), run.H), cz[s]);
+        run.A = run.A * a[s];
+      }
+    }
+    Exchange<CH, kWarps> &x = seg[i & 1];
+    x.run[warp][lane] = run;
+    if (lane == 0) x.cut[warp] = start;
     __syncthreads();
-    float in[CH];  // the state before this warp's segment
-    if (kCluster) {
-      float A[CH], H[CH], Aw[CH], Hw[CH];
+    Ch<CH> in;
+    if constexpr (kCluster)
+      in = pass_cluster<CH>(x, quads[i & 1], (i >> 1) & 1, lost, at.rank, p.split, lane, warp, h);
+    else
+      in = pass_block<CH>(x, lane, warp, h);
+    if (state) {
+      store_channels<CH>(state, 0, at.live && t < T, in);
+      state += (int64_t)(step / (int)NS_SCAN_TILE) * p.D;
+    }
+    E *to = y;
+    if (plain) {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        A[k] = 1.0f, H[k] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w == warp) Aw[k] = A[k], Hw[k] = H[k];
-          const float2 r = seg[buf][w][lane * CH + k];
-          H[k] = run_state(r.x, r.y, H[k]);
-          A[k] = __float_as_int(r.x) < 0 ? r.x : A[k] * r.x;
-        }
-      }
-      if (warp < p.split) {  // warp w writes this tile's run into block w
-        const uint32_t to = remote_smem(&tile[buf][rank][lane * CH], warp);
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-          remote_store(to + k * sizeof(float2), make_float2(A[k], H[k]));
-      }
-      cluster_arrive();
-      cluster_wait();
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        float mine = 0.0f;
-        for (uint32_t r = 0; r < p.split; ++r) {
-          if (r == rank) mine = h[k];
-          const float2 x = tile[buf][r][lane * CH + k];
-          h[k] = run_state(x.x, x.y, h[k]);
-        }
-        in[k] = run_state(Aw[k], Hw[k], mine);
+      for (int s = 0; s < kSteps; ++s, to += p.D) {
+        in = fma(a[s], in, cz[s]);
+        if (at.live) *reinterpret_cast<Raw<E, CH> *>(to) = narrow<E, CH>(in);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w == warp) in[k] = h[k];
-          const float2 r = seg[buf][w][lane * CH + k];
-          h[k] = run_state(r.x, r.y, h[k]);
-        }
+      for (int s = 0; s < kSteps; ++s, to += p.D) {
+        in = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), in), cz[s]);
+        if (at.live && t + s < T)
+          *reinterpret_cast<Raw<E, CH> *>(to) =
+              narrow<E, CH>(pick((skip >> s) & 1u, splat<CH>(0.0f), in));
       }
     }
-    if (warp == 0 && j < nt)
-      store_channels<CH>(p.states, ((int64_t)b * nt + j) * p.D + c0, live, in);
-    E *y = static_cast<E *>(p.y) + ((int64_t)b * p.T + t0) * p.D + c0;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      Vec<E, CH> out;
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const float before = (reset >> s) & 1u ? 0.0f : in[k];
-        in[k] = fmaf(a[s][k], before, c[s][k] * z[s][k]);
-        out.v[k] = from_f32<E>((skip >> s) & 1u ? 0.0f : in[k]);
-      }
-      if (live && s < n) *reinterpret_cast<Vec<E, CH> *>(y + (int64_t)s * p.D) = out;
-    }
+    y += (int64_t)step * p.D;
   }
-  if (rank == 0 && warp == 0) store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, live, h);
+  copy_wait<0>();
+  if (at.rank == 0 && warp == 0)
+    store_channels<CH>(p.h_last, (int64_t)at.b * p.D + at.c0, at.live, h);
 }
 
 // Rows of at most kSteps steps: a thread takes a row's channels alone, one
 // segment, no exchange.
 template <class E, int CH>
-__global__ void __launch_bounds__(kThreads) scan_forward_short_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const ScanParams p) {
   const uint32_t per_row = (p.D + CH - 1) / CH;
-  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  const uint64_t i = (uint64_t)blockIdx.x * kShortThreads + threadIdx.x;
   if (i >= (uint64_t)p.B * per_row) return;
   const uint32_t b = (uint32_t)(i / per_row), c0 = (uint32_t)(i % per_row) * CH;
-  float bias[CH], h[CH];
-  load_channels<CH>(p.bias, c0, true, bias);
-  load_channels<CH>(p.h0, (int64_t)b * p.D + c0, true, h);
+  const Ch<CH> nb = load_channels<CH>(p.bias, c0, true) * splat<CH>(-kLog2e);
+  Ch<CH> h = load_channels<CH>(p.h0, (int64_t)b * p.D + c0, true);
   store_channels<CH>(p.states, (int64_t)b * p.D + c0, p.T > 0, h);
   const E *z = static_cast<const E *>(p.z) + (int64_t)b * p.z_row + c0;
   const E *f = static_cast<const E *>(p.f) + (int64_t)b * p.f_row + c0;
@@ -282,211 +648,208 @@ __global__ void __launch_bounds__(kThreads) scan_forward_short_kernel(const Scan
   for (uint32_t t = 0; t < p.T; ++t) {
     const int64_t at = (int64_t)b * p.T + t;
     const bool start = p.pos && __ldg(p.pos + at) == 0, skip = p.doc && __ldg(p.doc + at) < 0;
-    const Vec<E, CH> zv = *reinterpret_cast<const Vec<E, CH> *>(z + t * p.z_time);
-    const Vec<E, CH> fv = *reinterpret_cast<const Vec<E, CH> *>(f + t * p.f_time);
-    Vec<E, CH> out;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      float a, c;
-      gate(to_f32(fv.v[k]) + bias[k], a, c);
-      const float to = fmaf(a, start ? 0.0f : h[k], c * to_f32(zv.v[k]));
-      if (!skip) h[k] = to;
-      out.v[k] = from_f32<E>(skip ? 0.0f : to);
-    }
-    *reinterpret_cast<Vec<E, CH> *>(y + (int64_t)t * p.D) = out;
+    const Raw<E, CH> zv = *reinterpret_cast<const Raw<E, CH> *>(z + t * p.z_time);
+    const Raw<E, CH> fv = *reinterpret_cast<const Raw<E, CH> *>(f + t * p.f_time);
+    Ch<CH> r, c, a;
+    gate<CH>(widen<E, CH>(fv), nb, r, c, a);
+    const Ch<CH> to = fma(a, pick(start, splat<CH>(0.0f), h), c * widen<E, CH>(zv));
+    h = pick(skip, h, to);
+    *reinterpret_cast<Raw<E, CH> *>(y + (int64_t)t * p.D) =
+        narrow<E, CH>(pick(skip, splat<CH>(0.0f), to));
   }
   store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, true, h);
 }
 
-// The backward pass walks the tiles from the last one.  Inside a tile the
-// states are run again from the saved one, forward in time, while
+// The backward pass walks the tiles from the last one, and a warp's segments
+// with them: warp w takes the segment that is w-th from the tile's end.
 //   d_t = dy_t + u_t,  u_{t-1} = a_t d_t  (0 where a sequence starts)
-// runs backward: both maps of a segment have the same A, and one exchange
-// serves both.  Warp w takes the segment that is w-th from the tile's end.
+// is a run in the other direction with the same A, exchanged as in the forward
+// pass.  The states inside a quad are run again from the saved one before it,
+// by the segments' forward runs, which are exchanged too.
 template <class E, int CH, bool kCluster>
-__global__ void __launch_bounds__(kThreads) scan_backward_kernel(const ScanParams p) {
-  __shared__ Runs<CH> seg[2][kWarps];         // (A, H)
-  __shared__ float seg_u[2][kWarps][32 * CH];  // U of the same segment
-  __shared__ Runs<CH> tile[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1];  // (A, U)
-  __shared__ float sums[kWarps][32 * CH];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t rank = kCluster ? blockIdx.x % p.split : 0;
-  const uint32_t unit = kCluster ? blockIdx.x / p.split : blockIdx.x;
-  const uint32_t b = unit / p.groups, c0 = (unit % p.groups) * 32 * CH + lane * CH;
-  const bool live = c0 < p.D;
-  const int64_t nt = ((int64_t)p.T + kTile - 1) / kTile;
-  const int64_t stride = kCluster ? p.split : 1;
-  if (kCluster) {
-    cluster_arrive();
-    cluster_wait();
-  }
-  const E *dy = static_cast<const E *>(p.dy) + (int64_t)b * p.dy_row + c0;
-  float bias[CH], u[CH], sum[CH];
-  load_channels<CH>(p.bias, c0, live, bias);
-  load_channels<CH>(p.dh_last, (int64_t)b * p.D + c0, live, u);
-#pragma unroll
-  for (int k = 0; k < CH; ++k) sum[k] = 0.0f;
-
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks)
+    scan_backward_kernel(const ScanParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) Exchange<CH, kWarps> seg[2];  // (A, U)
+  __shared__ Ch<CH> ahead[2][kWarps][32];                // H of the same segments
+  __shared__ __align__(16) unsigned char quads_mem[kCluster ? 2 * sizeof(Quads<CH>) : 16];
+  Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
+  const Place at = place_of<CH, kCluster>(p);
+  const int lane = at.lane, warp = at.warp;
+  Stage<E, CH, 3> *ring = reinterpret_cast<Stage<E, CH, 3> *>(smem) + warp * kRing;
+  if (kCluster) cluster_begin<CH>(quads);
+  const int T = (int)p.T, stride = kCluster ? (int)p.split : 1, step = stride * kTile;
+  const int tiles = (T + kTile - 1) / kTile, rounds = (tiles + stride - 1) / stride;
   const int back = kWarps - 1 - warp;  // this warp's segment of a tile
-  Segment<E, CH> next;
-  Vec<E, CH> next_dy[kSteps];
-  float next_h[CH];  // the saved state before the tile
-  auto fetch = [&](int64_t j) {
-    // a tile before the first one (past the last of the walk) has no steps
-    const int64_t t0 = j < 0 ? (int64_t)p.T : j * kTile + back * kSteps;
-    load_segment<E, CH>(p, b, t0, c0, live, lane, next);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      if (live && s < next.n)
-        next_dy[s] = *reinterpret_cast<const Vec<E, CH> *>(dy + (t0 + s) * p.dy_time);
-    load_channels<CH>(p.saved, ((int64_t)b * nt + j) * p.D + c0, live && j >= 0, next_h);
+  // negative in a tile before the first one, past the end of the walk
+  int t = (tiles - 1 - (int)at.rank) * kTile + back * kSteps;
+  Copier<E, CH> z_in, f_in, g_in;
+  z_in.set(static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg, p.z_time,
+           -step, p.D - at.cg, p.wide, lane);
+  f_in.set(static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg, p.f_time,
+           -step, p.D - at.cg, p.wide, lane);
+  g_in.set(static_cast<const E *>(p.dy) + (int64_t)at.b * p.dy_row + t * p.dy_time + at.cg,
+           p.dy_time, -step, p.D - at.cg, p.wide, lane);
+  auto fetch = [&](int at_step, Stage<E, CH, 3> &to) {
+    const int n = steps_at(T, at_step);
+    z_in.copy(n, p.wide, lane, to.v[0]);
+    f_in.copy(n, p.wide, lane, to.v[1]);
+    g_in.copy(n, p.wide, lane, to.v[2]);
+    copy_commit();
   };
-  fetch(nt - 1 - rank);
-  int buf = 0;
-  for (int64_t i = 0; i < nt; i += stride, buf ^= 1) {
-    const int64_t j = nt - 1 - i - rank;  // may be negative
-    const int64_t t0 = j * kTile + back * kSteps;
-    uint32_t reset, skip;
-    float a[kSteps][CH], c[kSteps][CH], z[kSteps][CH], g[kSteps][CH], h[CH];
-    segment_flags<E, CH>(next, lane, reset, skip);
-    segment_gates<E, CH>(next, bias, skip, a, c, z);
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+  for (int k = 0; k < kRing - 1; ++k) fetch(t - k * step, ring[k]);
+  Flags flags;
+  flags.set(p, at.b, t, -step, lane);
+  const Ch<CH> zero = splat<CH>(0.0f);
+  // the saved state before the segment's quad
+  const float *saved = p.saved + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
+                                  t / (int)NS_SCAN_TILE) * p.D + at.c0;
+  Ch<CH> next_h = load_channels<CH>(saved, 0, at.live && t >= 0 && t < T);
+  const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
+  Ch<CH> u = load_channels<CH>(p.dh_last, (int64_t)at.b * p.D + at.c0, at.live), sum = zero;
+  const int64_t out = ((int64_t)at.b * p.T + t) * p.D + at.c0;
+  E *dz = static_cast<E *>(p.dz) + out, *df = static_cast<E *>(p.df) + out;
+  int slot = 0;
+  bool lost = false;
+  for (int i = 0; i < rounds; ++i, t -= step) {
+    __syncwarp();
+    fetch(t - (kRing - 1) * step, ring[slot == 0 ? kRing - 1 : slot - 1]);
+    flags.next(i);
+    const uint32_t start = flags.start & 0xffu, skip = flags.skip & 0xffu;
+    const bool plain = (start | skip) == 0;
+    Ch<CH> h = next_h;
+    saved -= (int64_t)(step / (int)NS_SCAN_TILE) * p.D;
+    next_h = load_channels<CH>(saved, 0, at.live && t - step >= 0 && t - step < T);
+    copy_wait<kRing - 1>();
+    __syncwarp();
+    const Stage<E, CH, 3> &in = ring[slot];
+    slot = slot == kRing - 1 ? 0 : slot + 1;
+    Ch<CH> a[kSteps], c[kSteps], q[kSteps], H = zero;  // q = a c, from the unrounded gate
+    Run<CH> run = {splat<CH>(1.0f), zero};
 #pragma unroll
-      for (int k = 0; k < CH; ++k) g[s][k] = (skip >> s) & 1u ? 0.0f : to_f32(next_dy[s].v[k]);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) h[k] = next_h[k];
-    const int n = next.n;
-    fetch(j - stride);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      float A = 1.0f, H = 0.0f, U = 0.0f;
+    for (int s = 0; s < kSteps; ++s) {
+      Ch<CH> r;
+      gate<CH>(widen<E, CH>(in.v[1][s][lane]), nb, r, c[s], a[s]);
+      q[s] = r * c[s];
+    }
+    if (plain) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const bool start = (reset >> s) & 1u;
-        H = fmaf(a[s][k], start ? 0.0f : H, c[s][k] * z[s][k]);
-        A = start ? -0.0f : A * a[s][k];
+        H = fma(a[s], H, c[s] * widen<E, CH>(in.v[0][s][lane]));
+        run.A = run.A * a[s];
       }
 #pragma unroll
       for (int s = kSteps - 1; s >= 0; --s)
-        U = (reset >> s) & 1u ? 0.0f : a[s][k] * (g[s][k] + U);
-      seg[buf][warp][lane * CH + k] = make_float2(A, H);
-      seg_u[buf][warp][lane * CH + k] = U;
+        run.H = a[s] * (widen<E, CH>(in.v[2][s][lane]) + run.H);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const bool gone = (skip >> s) & 1u;
+        a[s] = pick(gone, splat<CH>(1.0f), a[s]);
+        c[s] = pick(gone, zero, c[s]);
+        const Ch<CH> cz = pick(gone, zero, c[s] * widen<E, CH>(in.v[0][s][lane]));
+        H = fma(a[s], pick((start >> s) & 1u, zero, H), cz);
+        run.A = run.A * a[s];
+      }
+#pragma unroll
+      for (int s = kSteps - 1; s >= 0; --s) {
+        const Ch<CH> g = pick((skip >> s) & 1u, zero, widen<E, CH>(in.v[2][s][lane]));
+        run.H = pick((start >> s) & 1u, zero, a[s] * (g + run.H));
+      }
     }
+    Exchange<CH, kWarps> &x = seg[i & 1];
+    x.run[warp][lane] = run;
+    ahead[i & 1][warp][lane] = H;
+    if (lane == 0) x.cut[warp] = start;
     __syncthreads();
-    float ui[CH];  // u after this warp's segment, that is from its right
+    // the state before this segment: through the quad's earlier ones, which
+    // later warps hold
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      // the state before this segment: through the segments earlier in time
-#pragma unroll
-      for (int w = kWarps - 1; w > 0; --w) {
-        const float2 r = seg[buf][w][lane * CH + k];
-        if (w > warp) h[k] = run_state(r.x, r.y, h[k]);
+    for (int k = kQuad - 1; k > 0; --k) {
+      if (back % kQuad >= k) {
+        const Run<CH> r = {x.run[warp + k][lane].A, ahead[i & 1][warp + k][lane]};
+        h = after(r, x.cut[warp + k] != 0, h);
       }
     }
-    if (kCluster) {
-      float A[CH], U[CH], Aw[CH], Uw[CH];
+    Ch<CH> ui;
+    if constexpr (kCluster)
+      ui = pass_cluster<CH>(x, quads[i & 1], (i >> 1) & 1, lost, at.rank, p.split, lane, warp, u);
+    else
+      ui = pass_block<CH>(x, lane, warp, u);
+    E *to_z = dz + (int64_t)(kSteps - 1) * p.D, *to_f = df + (int64_t)(kSteps - 1) * p.D;
+    if (plain) {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        A[k] = 1.0f, U[k] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w == warp) Aw[k] = A[k], Uw[k] = U[k];
-          const float ra = seg[buf][w][lane * CH + k].x;
-          U[k] = run_state(ra, seg_u[buf][w][lane * CH + k], U[k]);
-          A[k] = __float_as_int(ra) < 0 ? ra : A[k] * ra;
-        }
+      for (int s = 0; s < kSteps; ++s) {  // q takes p_t - z_t in
+        const Ch<CH> z = widen<E, CH>(in.v[0][s][lane]);
+        q[s] = q[s] * sub(h, z);
+        h = fma(a[s], h, c[s] * z);
       }
-      if (warp < p.split) {
-        const uint32_t to = remote_smem(&tile[buf][rank][lane * CH], warp);
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
-          remote_store(to + k * sizeof(float2), make_float2(A[k], U[k]));
-      }
-      cluster_arrive();
-      cluster_wait();
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        float mine = 0.0f;
-        for (uint32_t r = 0; r < p.split; ++r) {
-          if (r == rank) mine = u[k];
-          const float2 x = tile[buf][r][lane * CH + k];
-          u[k] = run_state(x.x, x.y, u[k]);
+      for (int s = kSteps - 1; s >= 0; --s, to_z -= p.D, to_f -= p.D) {
+        const Ch<CH> d = widen<E, CH>(in.v[2][s][lane]) + ui, vf = q[s] * d;
+        ui = a[s] * d;
+        sum = sum + vf;
+        if (at.live) {
+          *reinterpret_cast<Raw<E, CH> *>(to_z) = narrow<E, CH>(c[s] * d);
+          *reinterpret_cast<Raw<E, CH> *>(to_f) = narrow<E, CH>(vf);
         }
-        ui[k] = run_state(Aw[k], Uw[k], mine);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
+      for (int s = 0; s < kSteps; ++s) {
+        const bool gone = (skip >> s) & 1u;
+        const Ch<CH> z = pick(gone, zero, widen<E, CH>(in.v[0][s][lane]));
+        const Ch<CH> before = pick((start >> s) & 1u, zero, h);
+        q[s] = q[s] * sub(before, z);
+        h = fma(a[s], before, c[s] * z);
+      }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w == warp) ui[k] = u[k];
-          u[k] = run_state(seg[buf][w][lane * CH + k].x, seg_u[buf][w][lane * CH + k], u[k]);
+      for (int s = kSteps - 1; s >= 0; --s, to_z -= p.D, to_f -= p.D) {
+        const bool gone = (skip >> s) & 1u;
+        const Ch<CH> d = pick(gone, zero, widen<E, CH>(in.v[2][s][lane])) + ui;
+        const Ch<CH> vf = pick(gone, zero, q[s] * d);
+        ui = pick((start >> s) & 1u, zero, a[s] * d);
+        sum = sum + vf;
+        if (at.live && t + s < T && t >= 0) {
+          *reinterpret_cast<Raw<E, CH> *>(to_z) = narrow<E, CH>(pick(gone, zero, c[s] * d));
+          *reinterpret_cast<Raw<E, CH> *>(to_f) = narrow<E, CH>(vf);
         }
       }
     }
-    // z becomes p_t - z_t, the rest of df's factors
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const float before = (reset >> s) & 1u ? 0.0f : h[k];
-        h[k] = fmaf(a[s][k], before, c[s][k] * z[s][k]);
-        z[s][k] = before - z[s][k];
-      }
-    }
-    const int64_t at = ((int64_t)b * p.T + t0) * p.D + c0;
-#pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s) {
-      Vec<E, CH> oz, of;
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const bool out = (skip >> s) & 1u;
-        const float d = g[s][k] + ui[k], ad = a[s][k] * d;
-        const float vz = out ? 0.0f : c[s][k] * d, vf = out ? 0.0f : c[s][k] * ad * z[s][k];
-        ui[k] = (reset >> s) & 1u ? 0.0f : ad;
-        oz.v[k] = from_f32<E>(vz);
-        of.v[k] = from_f32<E>(vf);
-        sum[k] += vf;
-      }
-      if (live && s < n) {
-        *reinterpret_cast<Vec<E, CH> *>(static_cast<E *>(p.dz) + at + (int64_t)s * p.D) = oz;
-        *reinterpret_cast<Vec<E, CH> *>(static_cast<E *>(p.df) + at + (int64_t)s * p.D) = of;
-      }
-    }
+    dz -= (int64_t)step * p.D, df -= (int64_t)step * p.D;
   }
-  if (rank == 0 && warp == 0) store_channels<CH>(p.dh0, (int64_t)b * p.D + c0, live, u);
+  copy_wait<0>();
+  if (at.rank == 0 && warp == 0)
+    store_channels<CH>(p.dh0, (int64_t)at.b * p.D + at.c0, at.live, u);
   if (p.partial) {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) sums[warp][lane * CH + k] = sum[k];
+    __syncthreads();
+    ahead[0][warp][lane] = sum;
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w)
-#pragma unroll
-        for (int k = 0; k < CH; ++k) sum[k] += sums[w][lane * CH + k];
-      store_channels<CH>(p.partial, ((int64_t)b * stride + rank) * p.D + c0, live, sum);
+      for (int w = 1; w < kWarps; ++w) sum = sum + ahead[0][w][lane];
+      store_channels<CH>(p.partial, ((int64_t)at.b * stride + at.rank) * p.D + at.c0, at.live,
+                         sum);
     }
   }
 }
 
 template <class E, int CH>
-__global__ void __launch_bounds__(kThreads) scan_backward_short_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(const ScanParams p) {
   const uint32_t per_row = (p.D + CH - 1) / CH;
-  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  const uint64_t i = (uint64_t)blockIdx.x * kShortThreads + threadIdx.x;
   if (i >= (uint64_t)p.B * per_row) return;
   const uint32_t b = (uint32_t)(i / per_row), c0 = (uint32_t)(i % per_row) * CH;
   const int64_t bc = (int64_t)b * p.D + c0;
-  float bias[CH], h[CH], u[CH], sum[CH];
-  load_channels<CH>(p.bias, c0, true, bias);
-  load_channels<CH>(p.saved, bc, p.T > 0, h);
-  load_channels<CH>(p.dh_last, bc, true, u);
-#pragma unroll
-  for (int k = 0; k < CH; ++k) sum[k] = 0.0f;
+  const Ch<CH> zero = splat<CH>(0.0f);
+  const Ch<CH> nb = load_channels<CH>(p.bias, c0, true) * splat<CH>(-kLog2e);
+  Ch<CH> h = load_channels<CH>(p.saved, bc, p.T > 0);
+  Ch<CH> u = load_channels<CH>(p.dh_last, bc, true), sum = zero;
   const E *z = static_cast<const E *>(p.z) + (int64_t)b * p.z_row + c0;
   const E *f = static_cast<const E *>(p.f) + (int64_t)b * p.f_row + c0;
   const E *dy = static_cast<const E *>(p.dy) + (int64_t)b * p.dy_row + c0;
-  float a[kSteps][CH], c[kSteps][CH], q[kSteps][CH];  // q: p_t - z_t
+  Ch<CH> a[kSteps], c[kSteps], q[kSteps], e[kSteps];  // e: p_t - z_t
   uint32_t start = 0, skip = 0;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
@@ -494,35 +857,28 @@ __global__ void __launch_bounds__(kThreads) scan_backward_short_kernel(const Sca
       const int64_t at = (int64_t)b * p.T + s;
       if (p.pos && __ldg(p.pos + at) == 0) start |= 1u << s;
       if (p.doc && __ldg(p.doc + at) < 0) skip |= 1u << s;
-      const Vec<E, CH> zv = *reinterpret_cast<const Vec<E, CH> *>(z + s * p.z_time);
-      const Vec<E, CH> fv = *reinterpret_cast<const Vec<E, CH> *>(f + s * p.f_time);
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        gate(to_f32(fv.v[k]) + bias[k], a[s][k], c[s][k]);
-        const float before = (start >> s) & 1u ? 0.0f : h[k], zk = to_f32(zv.v[k]);
-        q[s][k] = before - zk;
-        if (!((skip >> s) & 1u)) h[k] = fmaf(a[s][k], before, c[s][k] * zk);
-      }
+      const Raw<E, CH> zv = *reinterpret_cast<const Raw<E, CH> *>(z + s * p.z_time);
+      const Raw<E, CH> fv = *reinterpret_cast<const Raw<E, CH> *>(f + s * p.f_time);
+      Ch<CH> r;
+      gate<CH>(widen<E, CH>(fv), nb, r, c[s], a[s]);
+      q[s] = r * c[s];
+      const Ch<CH> before = pick((start >> s) & 1u, zero, h);
+      e[s] = sub(before, widen<E, CH>(zv));
+      h = pick((skip >> s) & 1u, h, fma(a[s], before, c[s] * widen<E, CH>(zv)));
     }
   }
 #pragma unroll
   for (int s = kSteps - 1; s >= 0; --s) {
     if (s < (int)p.T) {
       const bool out = (skip >> s) & 1u;
-      const Vec<E, CH> gv = *reinterpret_cast<const Vec<E, CH> *>(dy + s * p.dy_time);
-      Vec<E, CH> oz, of;
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const float d = to_f32(gv.v[k]) + u[k], ad = a[s][k] * d;
-        const float vz = out ? 0.0f : c[s][k] * d, vf = out ? 0.0f : c[s][k] * ad * q[s][k];
-        if (!out) u[k] = (start >> s) & 1u ? 0.0f : ad;
-        oz.v[k] = from_f32<E>(vz);
-        of.v[k] = from_f32<E>(vf);
-        sum[k] += vf;
-      }
+      const Ch<CH> d = widen<E, CH>(*reinterpret_cast<const Raw<E, CH> *>(dy + s * p.dy_time)) + u;
+      const Ch<CH> vf = pick(out, zero, q[s] * d * e[s]);
+      u = pick(out, u, pick((start >> s) & 1u, zero, a[s] * d));
+      sum = sum + vf;
       const int64_t at = ((int64_t)b * p.T + s) * p.D + c0;
-      *reinterpret_cast<Vec<E, CH> *>(static_cast<E *>(p.dz) + at) = oz;
-      *reinterpret_cast<Vec<E, CH> *>(static_cast<E *>(p.df) + at) = of;
+      *reinterpret_cast<Raw<E, CH> *>(static_cast<E *>(p.dz) + at) =
+          narrow<E, CH>(pick(out, zero, c[s] * d));
+      *reinterpret_cast<Raw<E, CH> *>(static_cast<E *>(p.df) + at) = narrow<E, CH>(vf);
     }
   }
   store_channels<CH>(p.dh0, bc, true, u);
@@ -531,43 +887,52 @@ __global__ void __launch_bounds__(kThreads) scan_backward_short_kernel(const Sca
 
 // dbias[c] = the sum of the partial rows, in a fixed order: 32 channels a
 // block, warp w the rows w, w + 8, ..., then the warps in order.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kBiasWarps)
     scan_bias_kernel(const float *__restrict__ partial, uint64_t rows, uint32_t D, float *dbias) {
   pdl_wait_then_release();
-  __shared__ float sums[kWarps][32];
+  __shared__ float sums[kBiasWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t c = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (c < D) {
 #pragma unroll 8
-    for (uint64_t r = warp; r < rows; r += kWarps) s += partial[r * D + c];
+    for (uint64_t r = warp; r < rows; r += kBiasWarps) s += partial[r * D + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < D) {
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += sums[w][lane];
+    for (int w = 1; w < kBiasWarps; ++w) s += sums[w][lane];
     dbias[c] = s;
   }
 }
 
-// Blocks along time: doubled while the grid holds fewer than three blocks a
-// SM and every block of the cluster still has a tile.  The groups of 64
-// channels count also where lanes take one channel each, so that the order of
-// the sums depends on the sizes alone.
+// Blocks of a cluster, along time: doubled while the grid holds fewer than kEnough
+// blocks and every block still has a tile.  It follows from the sizes alone, with
+// groups of 64 channels also where a lane takes one, so that the order of the
+// bias's sums does too.
 uint32_t split_of(uint32_t B, uint32_t T, uint32_t D) {
-  const uint64_t units = (uint64_t)B * ((D + 63) / 64), nt = (T + (uint64_t)kTile - 1) / kTile;
+  const uint64_t units = (uint64_t)B * ((D + 63) / 64), tiles = (T + (uint64_t)kTile - 1) / kTile;
   uint32_t s = 1;
-  while (s < kMaxCluster && units * s < 456 && nt >= 2 * s) s *= 2;
+  while (s < kMaxCluster && units * s < kEnough && tiles >= 2 * s) s *= 2;
   return s;
 }
 
 template <class... KArgs>
-cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, uint32_t cluster, cudaStream_t st,
-                   const ScanParams &p) {
+cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint32_t cluster,
+                   size_t smem, cudaStream_t st, const ScanParams &p) {
+  if (smem > 0) {  // with the static part it may be beyond what needs no leave
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -582,30 +947,21 @@ cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, uint32_t cluster, cudaS
   return e != cudaSuccess ? e : last;
 }
 
-template <class E, int CH>
-cudaError_t run_forward(ScanParams &p, cudaStream_t st) {
+template <class E, int CH, bool kForward>
+cudaError_t run_as(ScanParams &p, cudaStream_t st) {
   if (p.T <= (uint32_t)kSteps) {
     const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
-    return launch(scan_forward_short_kernel<E, CH>, (n + kThreads - 1) / kThreads, 1, st, p);
+    return launch(kForward ? scan_forward_short_kernel<E, CH> : scan_backward_short_kernel<E, CH>,
+                  (n + kShortThreads - 1) / kShortThreads, kShortThreads, 1, 0, st, p);
   }
   p.groups = (p.D + 32 * CH - 1) / (32 * CH);
   p.split = split_of(p.B, p.T, p.D);
   const uint64_t blocks = (uint64_t)p.B * p.groups * p.split;
-  return p.split > 1 ? launch(scan_forward_kernel<E, CH, true>, blocks, p.split, st, p)
-                     : launch(scan_forward_kernel<E, CH, false>, blocks, 1, st, p);
-}
-
-template <class E, int CH>
-cudaError_t run_backward(ScanParams &p, cudaStream_t st) {
-  if (p.T <= (uint32_t)kSteps) {
-    const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
-    return launch(scan_backward_short_kernel<E, CH>, (n + kThreads - 1) / kThreads, 1, st, p);
-  }
-  p.groups = (p.D + 32 * CH - 1) / (32 * CH);
-  p.split = split_of(p.B, p.T, p.D);
-  const uint64_t blocks = (uint64_t)p.B * p.groups * p.split;
-  return p.split > 1 ? launch(scan_backward_kernel<E, CH, true>, blocks, p.split, st, p)
-                     : launch(scan_backward_kernel<E, CH, false>, blocks, 1, st, p);
+  const size_t smem = sizeof(Stage<E, CH, kForward ? 2 : 3>) * kRing * kWarps;
+#define NSK_SCAN(C) (kForward ? scan_forward_kernel<E, CH, C> : scan_backward_kernel<E, CH, C>)
+  return p.split == 1 ? launch(NSK_SCAN(false), blocks, kThreads, 1, smem, st, p)
+                      : launch(NSK_SCAN(true), blocks, kThreads, p.split, smem, st, p);
+#undef NSK_SCAN
 }
 
 // Two channels a lane need rows, strides and addresses of whole pairs.
@@ -619,6 +975,13 @@ bool pairs(const ScanParams &p, size_t es) {
   return e % (2 * es) == 0 && s % 8 == 0 && st % 2 == 0;
 }
 
+// 16 bytes at a time need addresses, strides and widths of whole 16 bytes.
+bool sixteens(const ScanParams &p, size_t es) {
+  const uintptr_t e = (uintptr_t)p.z | (uintptr_t)p.f | (uintptr_t)p.dy;
+  const int64_t st = p.z_row | p.z_time | p.f_row | p.f_time | p.dy_row | p.dy_time | p.D;
+  return e % 16 == 0 && st % (int64_t)(16 / es) == 0;
+}
+
 ScanParams params_of(const ns_scan_inputs &in) {
   ScanParams p = {};
   p.z = in.z, p.f = in.f;
@@ -630,15 +993,17 @@ ScanParams params_of(const ns_scan_inputs &in) {
 
 template <bool kForward>
 cudaError_t run(ScanParams &p, int dtype, cudaStream_t st) {
-  const bool two = pairs(p, dtype == NS_F32 ? 4 : 2);
-#define NSK_RUN(E, CH) \
-  (kForward ? run_forward<E, CH>(p, st) : run_backward<E, CH>(p, st))
+  const size_t es = dtype == NS_F32 ? 4 : 2;
+  const bool two = pairs(p, es);
+  p.wide = (two || es == 4) && sixteens(p, es);
   switch (dtype) {
-    case NS_F32: return two ? NSK_RUN(float, 2) : NSK_RUN(float, 1);
-    case NS_BF16: return two ? NSK_RUN(__nv_bfloat16, 2) : NSK_RUN(__nv_bfloat16, 1);
-    default: return two ? NSK_RUN(__half, 2) : NSK_RUN(__half, 1);
+    case NS_F32: return run_as<float, 1, kForward>(p, st);
+    case NS_BF16:
+      return two ? run_as<__nv_bfloat16, 2, kForward>(p, st)
+                 : run_as<__nv_bfloat16, 1, kForward>(p, st);
+    default:
+      return two ? run_as<__half, 2, kForward>(p, st) : run_as<__half, 1, kForward>(p, st);
   }
-#undef NSK_RUN
 }
 
 }  // namespace
@@ -664,7 +1029,7 @@ cudaError_t launch_scan_backward(const ns_scan_inputs &in, const float *states, 
   const cudaError_t e = in.B ? run<false>(p, in.dtype, st) : cudaSuccess;
   if (e != cudaSuccess || !dbias) return e;  // without rows dbias is 0
   ++launch_counter();
-  pdl_launch(scan_bias_kernel, dim3((in.D + 31) / 32), dim3(kThreads), 0, st,
+  pdl_launch(scan_bias_kernel, dim3((in.D + 31) / 32), dim3(32 * kBiasWarps), 0, st,
              (const float *)partial, scan_partial_rows(in.B, in.T, in.D), in.D, dbias);
   return cudaGetLastError();
 }

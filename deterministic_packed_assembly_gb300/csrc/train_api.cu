@@ -31,7 +31,7 @@ int done(cudaError_t e) { return e == cudaSuccess ? NS_OK : NS_ERR_CUDA; }
 
 bool check_scan(const ns_scan_inputs *in) {
   if (!in || !size_of(in->dtype)) return false;
-  if (in->B >= (1u << 31) || in->T >= (1u << 31) || in->D >= (1u << 31)) return false;
+  if (in->B >= (1u << 31) || in->T > NS_SCAN_MAX_T || in->D >= (1u << 31)) return false;
   // blocks of a launch: at most eight along time for each 32 channels of a row
   if ((uint64_t)in->B * ((in->D + 31) / 32) >= (1ull << 31) / 8) return false;
   // a stride that reaches past the address space cannot be one

@@ -114,7 +114,7 @@ def gated_scan_forward(z: torch.Tensor, f: torch.Tensor, bias: Optional[torch.Te
                        pos: Optional[torch.Tensor] = None, doc: Optional[torch.Tensor] = None,
                        h0: Optional[torch.Tensor] = None):
     """``gated_scan`` without autograd: (y, h_last, states), where ``states``
-    (the state before every 64 steps) is for ``gated_scan_backward``."""
+    (the state before every NS_SCAN_TILE steps) is for ``gated_scan_backward``."""
     return _scan(z, f, bias, pos, doc, h0, True)
 
 

@@ -28,7 +28,8 @@
  *    statistics and losses are 32-bit floats; an output of 16 bits is rounded
  *    once, from 32 bits.
  *  - Every sum is taken in an order fixed by the sizes alone: the same
- *    arguments give the same bits, on every call and every stream.
+ *    arguments give the same bits, on every call and every stream.  What a row
+ *    (of a scan, of logits) gets does not depend on the other rows of the call.
  *  - Values at padded or unlearned positions are never used, whatever they
  *    are (NaN and infinities among them); the outputs there are 0 (-1 for
  *    expert ids).
@@ -50,7 +51,8 @@ extern "C" {
 #define NS_F16 2
 
 /* ---- limits ---------------------------------------------------------------- */
-#define NS_SCAN_TILE 64u         /* time steps between two saved states */
+#define NS_SCAN_TILE 32u         /* time steps between two saved states */
+#define NS_SCAN_MAX_T (1u << 30) /* time steps of a row */
 #define NS_DISTILL_MAX_TOP 1024u /* teacher logits a row */
 #define NS_DISTILL_MAX_ROW (8u * 200u * 1024u) /* bytes of a row of logits */
 #define NS_ROUTE_MAX_EXPERTS 1024u
@@ -81,7 +83,7 @@ typedef struct {
   const float *bias;     /* [D] or NULL */
   const int32_t *pos;    /* [B][T] or NULL */
   const int32_t *doc;    /* [B][T] or NULL */
-  uint32_t B, T, D;      /* T < 2^31; B, D < 2^31; any may be 0 */
+  uint32_t B, T, D;      /* T <= NS_SCAN_MAX_T; any may be 0 */
   int32_t dtype;         /* of z, f, y and their gradients */
 } ns_scan_inputs;
 

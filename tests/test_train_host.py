@@ -124,7 +124,7 @@ def test_structures_match_the_header(nsp):
 def test_workspaces(nsp):
     assert nsp.ns_scan_workspace(3, 5, 10) == 3 * 10 * 4
     assert nsp.ns_scan_workspace(0, 5, 10) == 0
-    assert nsp.ns_scan_workspace(1, 64, 64) == 64 * 4
+    assert nsp.ns_scan_workspace(1, 32, 64) == 64 * 4
     assert nsp.ns_scan_workspace(1, 10_000, 64) == 8 * 64 * 4  # eight blocks share the row
     assert nsp.ns_route_workspace(0, 16) >= 4
     assert nsp.ns_route_workspace(1 << 20, 64) >= nsp.ns_route_workspace(64, 64)
