@@ -5,15 +5,17 @@
 //   dl_nj = p_nj (g_j - sum_e p_ne g_e) + the chosen weights' part,
 //   g_e = d_loss E / (k M^2) counts_e
 //
-// L lanes of a warp take a token, R consecutive experts each, all in
-// registers: one read of the logits, shuffles of log2 L steps for the row's
-// maximum and sum and for each of the k choices.  A choice is the maximum of
-// keys that order the logits and, of equal ones, put the lowest index first.
-// Each lane adds its experts' probabilities up over all of its tokens; blocks
-// write rows of partial sums and counts, and a second kernel adds them in a
-// fixed order (no floating-point atomics: the loss has the same bits every
-// time).  The backward pass reads the logits again and computes the softmax
-// again, which costs less than keeping it.
+// Forward, a thread takes a token (or LP threads a token of more than 128 experts):
+// its logits lie in shared memory, in groups of S whose maxima it keeps in
+// registers.  A choice is the largest group's, found again among that group's S
+// logits alone; of equal ones the first group and the first place win.  Then the
+// logits are replaced by their exponentials, and the threads turn round: each
+// takes an expert and adds its probabilities up over the tile's tokens.  Blocks
+// write rows of partial sums and counts, and a second kernel adds them in a fixed
+// order (no floating-point atomics: the loss has the same bits every time).
+//
+// Backward, L lanes take a token, R consecutive experts each, in registers; the
+// softmax is computed again, which costs less than keeping it.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -29,7 +31,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr uint32_t kMaxBlocks = 456;  // three blocks on each of 152 SMs
+constexpr int kForwardThreads = 128;
+constexpr uint32_t kSMs = 152;
 
 struct RouteParams {
   const void *logits;
@@ -40,6 +43,8 @@ struct RouteParams {
   int32_t *ids;
   float *weights;
   // forward
+  int32_t dtype;
+  uint32_t lanes;   // threads of a token
   float *mass;      // [blocks][E]
   int32_t *chosen;  // [blocks][E]
   int32_t *real;    // [blocks]
@@ -49,45 +54,6 @@ struct RouteParams {
   // backward
   const float *d_weights, *d_loss;
   void *dlogits;
-};
-
-// Keys: unsigned numbers in the order of (logit, then lowest index first), 0
-// for an expert that cannot be chosen (-inf, NaN).  A 16-bit type's value and the index
-// fit 32 bits together; a float needs 64.
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 and 0 are equal
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-}
-template <class E>
-struct KeyOf {
-  using type = uint32_t;
-  // bits below the value's: bfloat16 has 16 significant ones as a float, half 19
-  static constexpr uint32_t kLow = sizeof(E) == 4 ? 0u
-                                   : std::is_same<E, __half>::value ? 0x1fffu : 0xffffu;
-  static __device__ __forceinline__ uint32_t make(float x, uint32_t i) {
-    return (ordered(x) & ~kLow) | (kLow - i);
-  }
-  static __device__ __forceinline__ uint32_t index(uint32_t key) { return kLow - (key & kLow); }
-  static __device__ __forceinline__ float value(uint32_t key) {
-    const uint32_t hi = key & ~kLow;
-    return unordered(hi & 0x80000000u ? hi : hi | kLow);
-  }
-};
-template <>
-struct KeyOf<float> {
-  using type = uint64_t;
-  static __device__ __forceinline__ uint64_t make(float x, uint32_t i) {
-    return (uint64_t)ordered(x) << 32 | (0xffffffffu - i);
-  }
-  static __device__ __forceinline__ uint32_t index(uint64_t key) {
-    return 0xffffffffu - (uint32_t)key;
-  }
-  static __device__ __forceinline__ float value(uint64_t key) {
-    return unordered((uint32_t)(key >> 32));
-  }
 };
 
 template <int L>
@@ -102,26 +68,6 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-template <int L>
-__device__ __forceinline__ uint64_t group_best(uint64_t v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = w > v ? w : v;
-  }
-  return v;
-}
-template <int L>
-__device__ __forceinline__ uint32_t group_best(uint32_t v) {
-  if constexpr (L == 32) {
-    return __reduce_max_sync(0xffffffffu, v);
-  } else {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-  }
-}
-
 // Elements of one access of at most 16 bytes.
 template <class E, int R>
 constexpr int kMove = R * sizeof(E) <= 16 ? R : 16 / sizeof(E);
@@ -136,9 +82,9 @@ __device__ __forceinline__ void load_logits(const RouteParams &p, uint32_t n, ui
   if (!real) return;
   const E *src = static_cast<const E *>(p.logits) + (int64_t)n * p.logits_row + i0;
   if (p.wide) {
-    if (i0 < p.E) {
 #pragma unroll
-      for (int r = 0; r < R; r += kN) {
+    for (int r = 0; r < R; r += kN) {
+      if (i0 + r < p.E) {
         const Vec<E, kN> v = *reinterpret_cast<const Vec<E, kN> *>(src + r);
 #pragma unroll
         for (int q = 0; q < kN; ++q) x[r + q] = to_f32(v.v[q]);
@@ -174,84 +120,227 @@ __device__ __forceinline__ float balance(uint32_t E, uint32_t k, int32_t M) {
   return M == 0 ? 0.0f : (float)E / (float)k / ((float)M * (float)M);
 }
 
-template <class E, int L, int R>
-__global__ void __launch_bounds__(kThreads) route_forward_kernel(const RouteParams p) {
-  using Key = typename KeyOf<E>::type;
-  constexpr int G = 32 / L, kExperts = L * R, kTop = kExperts < 32 ? kExperts : 32;
-  __shared__ float mass[kWarps][kExperts];
-  __shared__ int chosen[kExperts];
-  __shared__ int top_id[kWarps][G][kTop];
-  __shared__ float top_e[kWarps][G][kTop];
-  __shared__ int real_tokens;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / L, gl = lane % L;
-  const uint32_t i0 = gl * R;
-  for (int e = threadIdx.x; e < kExperts; e += kThreads) chosen[e] = 0;
-  if (threadIdx.x == 0) real_tokens = 0;
-  __syncthreads();
-  float sum[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) sum[r] = 0.0f;
-  int counted = 0;
-  int *my_id = top_id[warp][group];
-  float *my_e = top_e[warp][group];
-  const uint64_t step = (uint64_t)gridDim.x * kWarps * G;
-  for (uint64_t n0 = ((uint64_t)blockIdx.x * kWarps + warp) * G; n0 < p.N; n0 += step) {
-    const bool in = n0 + group < p.N;
-    const uint32_t n = in ? (uint32_t)(n0 + group) : 0;
-    const bool real = in && !(p.doc && __ldg(p.doc + n) < 0);
-    float x[R], base;
-    load_logits<E, R>(p, n, i0, real, x);
-    Key key[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) key[r] = x[r] > kNegInf ? KeyOf<E>::make(x[r], i0 + r) : 0;
-    const float s = exponentials<L, R>(x, base);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-    for (int r = 0; r < R; ++r) sum[r] += s == 0.0f ? 0.0f : x[r] * inv;
-    if (gl == 0 && s != 0.0f) ++counted;
-    for (uint32_t j = 0; j < p.k; ++j) {
-      Key best = key[0];
-#pragma unroll
-      for (int r = 1; r < R; ++r) best = key[r] > best ? key[r] : best;
-      best = group_best<L>(best);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (key[r] == best) key[r] = 0;
-      if (gl == 0) {
-        my_id[j] = best == 0 ? -1 : (int)KeyOf<E>::index(best);
-        my_e[j] = best == 0 ? 0.0f : exp2_sfu((KeyOf<E>::value(best) - base) * kLog2e);
-      }
-    }
-    __syncwarp();
-    float total = 0.0f;
-    if (p.normalize) {
-      for (uint32_t j = gl; j < p.k; j += L) total += my_e[j];
-      total = group_sum<L>(total);
-    }
-    // a NaN logit is never chosen, but makes s and so the token's weights NaN
-    const float by = p.normalize ? (total == 0.0f ? 0.0f : 1.0f / total) + (s - s) : inv;
-    for (uint32_t j = gl; in && j < p.k; j += L) {
-      const int id = my_id[j];
-      p.ids[(int64_t)n * p.k + j] = id;
-      p.weights[(int64_t)n * p.k + j] = id < 0 ? 0.0f : my_e[j] * by;
-      if (id >= 0) atomicAdd(&chosen[id], 1);
-    }
-    __syncwarp();
+// ---- forward ------------------------------------------------------------------
+// Walks the (row, place) pairs of a tile with `per` places a row, a thread's every
+// kForwardThreads-th, without a division a step.
+struct Walk {
+  uint32_t row, at, rows_a_step, rest, per;
+  __device__ __forceinline__ explicit Walk(uint32_t per_row) : per(per_row) {
+    row = threadIdx.x / per, at = threadIdx.x % per;
+    rows_a_step = kForwardThreads / per, rest = kForwardThreads % per;
   }
+  __device__ __forceinline__ void next() {
+    row += rows_a_step, at += rest;
+    if (at >= per) at -= per, ++row;
+  }
+};
+
+// A tile's logits into shared memory, as floats: token n0 + row's expert e at
+// row `row * lanes + e / SG`, place e % SG.  -inf for tokens that do not count.
+template <class E, int SG, int kPitch>
+__device__ __forceinline__ void load_tile(const RouteParams &p, uint64_t n0, uint32_t tokens,
+                                          float *tile) {
+  auto real = [&](uint32_t row) {
+    const uint64_t n = n0 + row;
+    return n < p.N && !(p.doc && __ldg(p.doc + n) < 0);
+  };
+  if (p.wide) {
+    constexpr int kN = 16 / sizeof(E);
+    for (Walk w(p.E / kN); w.row < tokens; w.next()) {
+      const uint32_t e = w.at * kN;
+      float *to = tile + (w.row * p.lanes + e / SG) * kPitch + e % SG;
+      float x[kN];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+      for (int q = 0; q < kN; ++q) x[q] = kNegInf;
+      if (real(w.row)) {
+        const Vec<E, kN> v = *reinterpret_cast<const Vec<E, kN> *>(
+            static_cast<const E *>(p.logits) + (int64_t)(n0 + w.row) * p.logits_row + e);
 #pragma unroll
-    for (int o = L; o < 32; o <<= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
-    if (group == 0) mass[warp][i0 + r] = sum[r];
+        for (int q = 0; q < kN; ++q) x[q] = to_f32(v.v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kN; q += 4)
+        *reinterpret_cast<float4 *>(to + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+    }
+  } else {
+    for (Walk w(p.E); w.row < tokens; w.next())
+      tile[(w.row * p.lanes + w.at / SG) * kPitch + w.at % SG] =
+          real(w.row) ? to_f32(static_cast<const E *>(
+                            p.logits)[(int64_t)(n0 + w.row) * p.logits_row + w.at])
+                      : kNegInf;
+  }
+}
+
+template <int S>
+__device__ __forceinline__ void load_group(const float *at, float (&v)[S]) {
+#pragma unroll
+  for (int q = 0; q < S; q += 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(at + q);
+    v[q] = x.x, v[q + 1] = x.y, v[q + 2] = x.z, v[q + 3] = x.w;
+  }
+}
+
+// G groups of S experts a thread.  Its row of shared memory is S * G floats and
+// four more, an odd number of 16 bytes: eight threads' 16-byte accesses then use
+// all banks.
+template <int S, int G>
+__global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forward_kernel(const RouteParams p) {
+  constexpr int SG = S * G, kPitch = SG + 4, kMaxColumns = NS_ROUTE_MAX_EXPERTS / kForwardThreads;
+  extern __shared__ __align__(16) float tile[];
+  const uint32_t LP = p.lanes, tokens = kForwardThreads / LP, columns = LP * SG;
+  float *inv = tile + kForwardThreads * kPitch;                     // [tokens]
+  int *chosen = reinterpret_cast<int *>(inv + kForwardThreads);     // [columns]
+  float *top_x = reinterpret_cast<float *>(chosen + columns);       // [tokens][k]: logit, weight
+  int *top_id = reinterpret_cast<int *>(top_x + tokens * p.k);      // [tokens][k]
+  __shared__ int real_tokens;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, token = tid / LP, lp = tid % LP;
+  float *mine = tile + tid * kPitch;
+  for (uint32_t e = tid; e < columns; e += kForwardThreads) chosen[e] = 0;
+  if (tid == 0) real_tokens = 0;
+  // an expert's (or several's, 128 apart) sum over every `parts`-th token
+  const uint32_t side = columns < kForwardThreads ? columns : kForwardThreads;
+  const uint32_t parts = kForwardThreads / side, my_part = tid / side, per_thread = columns / side;
+  float sum[kMaxColumns];
+  uint32_t place[kMaxColumns];
+#pragma unroll
+  for (int i = 0; i < kMaxColumns; ++i) {
+    const uint32_t e = tid % side + i * kForwardThreads;
+    sum[i] = 0.0f;
+    place[i] = e / SG * kPitch + e % SG;
+  }
+  int counted = 0;
+  const uint64_t tiles = ((uint64_t)p.N + tokens - 1) / tokens;
+  for (uint64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const uint64_t n0 = t * tokens;
+    __syncthreads();  // the last tile is done with
+    if (p.dtype == NS_F32) load_tile<float, SG, kPitch>(p, n0, tokens, tile);
+    else if (p.dtype == NS_BF16) load_tile<__nv_bfloat16, SG, kPitch>(p, n0, tokens, tile);
+    else load_tile<__half, SG, kPitch>(p, n0, tokens, tile);
+    for (int i = (int)p.E > (int)(lp * SG) ? (int)(p.E - lp * SG) : 0; i < SG; ++i)
+      mine[i] = kNegInf;  // places beyond the last expert
+    __syncthreads();
+
+    // The k largest: by groups.  NaN is below everything (a maximum leaves it out).
+    float top[G];
+    float m = kNegInf;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float v[S];
+      load_group<S>(mine + g * S, v);
+      top[g] = kNegInf;
+#pragma unroll
+      for (int q = 0; q < S; ++q) top[g] = fmaxf(top[g], v[q]);
+      m = fmaxf(m, top[g]);
+    }
+    for (uint32_t o = LP / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float last_x = kNegInf;  // which is never chosen
+    int last = 0;  // this thread's last choice
+    for (uint32_t j = 0; j < p.k; ++j) {
+      float own = top[0];
+#pragma unroll
+      for (int g = 1; g < G; ++g) own = fmaxf(own, top[g]);
+      float best = own;
+      for (uint32_t o = LP / 2; o > 0; o >>= 1)
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      // the first of the token's threads that has it
+      bool me = true;
+      if (LP > 1) {
+        const uint32_t have = __ballot_sync(0xffffffffu, own == best) >> (lane - lp);
+        me = (uint32_t)__ffs(have) == lp + 1;
+      }
+      if (!me) continue;
+      if (best == kNegInf) {
+        top_id[token * p.k + j] = -1;
+        top_x[token * p.k + j] = kNegInf;
+        continue;
+      }
+      int g = 0;
+#pragma unroll
+      for (int i = G - 1; i > 0; --i)
+        if (top[i] == best) g = i;
+      if (top[0] == best) g = 0;
+      float v[S];
+      load_group<S>(mine + g * S, v);
+      uint32_t equal = 0;
+      float less = kNegInf;
+#pragma unroll
+      for (int q = 0; q < S; ++q) {
+        if (v[q] == best) equal |= 1u << q;
+        if (v[q] < best) less = fmaxf(less, v[q]);
+      }
+      // equal ones up to the last choice were chosen before
+      if (best == last_x && last / S == g) equal &= 0xfffffffeu << (last % S);
+      last = g * S + __ffs(equal) - 1;
+      last_x = best;
+      const float left = equal & (equal - 1) ? best : less;
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        if (i == g) top[i] = left;
+      const int id = lp * SG + last;
+      top_id[token * p.k + j] = id;
+      top_x[token * p.k + j] = best;
+      atomicAdd(&chosen[id], 1);
+    }
+
+    // Exponentials in the logits' place, and their sum.  The difference is taken
+    // before the change of base, which overflows near the type's lowest value.
+    const float base = m == kNegInf ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < SG; i += 4) {
+      float4 x = *reinterpret_cast<const float4 *>(mine + i);
+      x.x = exp2_sfu((x.x - base) * kLog2e), x.y = exp2_sfu((x.y - base) * kLog2e);
+      x.z = exp2_sfu((x.z - base) * kLog2e), x.w = exp2_sfu((x.w - base) * kLog2e);
+      s += (x.x + x.y) + (x.z + x.w);
+      *reinterpret_cast<float4 *>(mine + i) = x;
+    }
+    for (uint32_t o = LP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float by_all = s == 0.0f ? 0.0f : 1.0f / s;
+    if (lp == 0) {
+      inv[token] = by_all;
+      counted += s != 0.0f;
+    }
+    __syncwarp();  // the token's threads have written their choices
+    float total = 0.0f;
+    for (uint32_t j = lp; j < p.k; j += LP)
+      total += exp2_sfu((top_x[token * p.k + j] - base) * kLog2e);
+    for (uint32_t o = LP / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // a NaN logit is never chosen, but makes s and so the token's weights NaN
+    const float by =
+        p.normalize ? (total == 0.0f ? 0.0f : 1.0f / total) + (s - s) : by_all;
+    for (uint32_t j = lp; j < p.k; j += LP) {
+      const float e = exp2_sfu((top_x[token * p.k + j] - base) * kLog2e);
+      top_x[token * p.k + j] = top_id[token * p.k + j] < 0 ? 0.0f : e * by;
+    }
+    __syncthreads();
+
+    const uint64_t left = p.N - n0;
+    const uint32_t here = left < tokens ? (uint32_t)left : tokens;
+    for (uint32_t i = tid; i < here * p.k; i += kForwardThreads) {
+      p.ids[n0 * p.k + i] = top_id[i];
+      p.weights[n0 * p.k + i] = top_x[i];
+    }
+#pragma unroll 4
+    for (uint32_t r = my_part; r < tokens; r += parts) {
+      const float by_token = inv[r];
+      const float *row = tile + r * LP * kPitch;
+#pragma unroll
+      for (int i = 0; i < kMaxColumns; ++i)
+        if (i < (int)per_thread) sum[i] = fmaf(row[place[i]], by_token, sum[i]);
+    }
   }
   counted = warp_sum_i32(counted);
   if (lane == 0) atomicAdd(&real_tokens, counted);
   __syncthreads();
-  float part = 0.0f;
-  for (uint32_t e = threadIdx.x; e < p.E; e += kThreads) {
-    float v = mass[0][e];
+  // the parts of an expert's sum, in order
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) v += mass[w][e];
+  for (int i = 0; i < kMaxColumns; ++i)
+    if (i < (int)per_thread) tile[my_part * columns + tid % side + i * kForwardThreads] = sum[i];
+  __syncthreads();
+  float part = 0.0f;
+  for (uint32_t e = tid; e < p.E; e += kForwardThreads) {
+    float v = tile[e];
+    for (uint32_t q = 1; q < parts; ++q) v += tile[q * columns + e];
     if (p.blocks == 1) {
       p.counts[e] = chosen[e];
       part += v * (float)chosen[e];
@@ -262,15 +351,14 @@ __global__ void __launch_bounds__(kThreads) route_forward_kernel(const RoutePara
   }
   if (p.blocks == 1) {  // few tokens: this block has all of them
     part = group_sum<32>(part);
+    if (lane == 0) inv[tid / 32] = part;
     __syncthreads();
-    if (lane == 0) mass[warp][0] = part;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) part += mass[w][0];
+    if (tid == 0) {
+      for (int w = 1; w < kForwardThreads / 32; ++w) part += inv[w];
       p.tokens[0] = real_tokens;
       p.loss[0] = part * balance(p.E, p.k, real_tokens);
     }
-  } else if (threadIdx.x == 0) {
+  } else if (tid == 0) {
     p.real[blockIdx.x] = real_tokens;
   }
 }
@@ -278,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) route_forward_kernel(const RoutePara
 // The blocks' partial sums, added up by one cluster: block c of it takes a
 // share of the experts, `width` lanes side by side and the rest of its threads
 // down the rows.
-constexpr int kFinalThreads = 512;
+constexpr int kFinalThreads = 1024;
 constexpr int kFinalBlocks = 8;
 __global__ void __launch_bounds__(kFinalThreads) __cluster_dims__(kFinalBlocks, 1, 1)
     route_total_kernel(const RouteParams p) {
@@ -298,7 +386,7 @@ __global__ void __launch_bounds__(kFinalThreads) __cluster_dims__(kFinalBlocks, 
   float v = 0.0f;
   int n = 0;
   if (col < share && e < p.E) {
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t b = first; b < p.blocks; b += rows) {
       v += p.mass[(uint64_t)b * p.E + e];
       n += p.chosen[(uint64_t)b * p.E + e];
@@ -367,31 +455,30 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RoutePar
     float x[R], base;
     load_logits<E, R>(p, n, i0, real, x);
     const float s = exponentials<L, R>(x, base);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s);
     float dot = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       x[r] *= inv;
       dot += x[r] * g[r];
     }
-    dot = group_sum<L>(dot);
+    const uint32_t at = n * p.k;  // below 2^31
     if (p.d_weights) {
       // w = p at the chosen ones: dl_j = w_j dw_j - p_j t at them, t = sum w dw;
       // normalised, w is their own softmax: dl_j = w_j (dw_j - t)
       float t = 0.0f;
       for (uint32_t j = gl; real && j < p.k; j += L)
-        if (p.ids[(int64_t)n * p.k + j] >= 0)  // else there is no such choice
-          t += p.weights[(int64_t)n * p.k + j] * p.d_weights[(int64_t)n * p.k + j];
+        if (p.ids[at + j] >= 0) t += p.weights[at + j] * p.d_weights[at + j];
       t = group_sum<L>(t);
       for (uint32_t j = gl; real && j < p.k; j += L) {
-        const int id = p.ids[(int64_t)n * p.k + j];
-        const float w = p.weights[(int64_t)n * p.k + j];
+        const int id = p.ids[at + j];  // -1: there is no such choice
         if (id >= 0 && id < (int)p.E)
-          my_add[id] = w * (p.d_weights[(int64_t)n * p.k + j] - (p.normalize ? t : 0.0f));
+          my_add[id] = p.weights[at + j] * (p.d_weights[at + j] - (p.normalize ? t : 0.0f));
       }
-      if (!p.normalize) dot += t;
+      dot += p.normalize || gl > 0 ? 0.0f : t;
       __syncwarp();
     }
+    dot = group_sum<L>(dot);
     if (in) {
       constexpr int kN = kMove<E, R>;
       E *dst = static_cast<E *>(p.dlogits) + (int64_t)n * p.E + i0;
@@ -403,9 +490,9 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RoutePar
         if (s == 0.0f) d[r] = 0.0f;
       }
       if (p.wide) {
-        if (i0 < p.E) {
 #pragma unroll
-          for (int r = 0; r < R; r += kN) {
+        for (int r = 0; r < R; r += kN) {
+          if (i0 + r < p.E) {
             Vec<E, kN> v;
 #pragma unroll
             for (int q = 0; q < kN; ++q) v.v[q] = from_f32<E>(d[r + q]);
@@ -421,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RoutePar
     if (p.d_weights) {
       __syncwarp();
       for (uint32_t j = gl; real && j < p.k; j += L) {
-        const int id = p.ids[(int64_t)n * p.k + j];
+        const int id = p.ids[at + j];
         if (id >= 0 && id < (int)p.E) my_add[id] = 0.0f;
       }
       __syncwarp();
@@ -429,73 +516,99 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RoutePar
   }
 }
 
-// Lanes of a token: as many as hold its experts, eight each.
-int lanes_of(uint32_t E) {
-  int L = 2;
-  while (L < 32 && (uint32_t)L * 8 < E) L *= 2;
-  return L;
+// The forward kernel's groups and threads a token: groups of eight for up to 64
+// experts, of 16 beyond, 128 experts a thread at most.
+struct Shape {
+  int S, G;
+  uint32_t lanes;
+};
+Shape shape_of(uint32_t E) {
+  if (E <= 8) return {8, 1, 1};
+  if (E <= 16) return {8, 2, 1};
+  if (E <= 32) return {8, 4, 1};
+  if (E <= 64) return {8, 8, 1};
+  uint32_t lanes = 1;
+  while (lanes * 128 < E) lanes *= 2;
+  return {16, 8, lanes};
 }
 
-template <class E, int L, int R, bool kForward>
-cudaError_t launch(RouteParams &p, uint32_t blocks, cudaStream_t st) {
+template <int S, int G>
+cudaError_t launch_forward(RouteParams &p, cudaStream_t st) {
+  const size_t tokens = kForwardThreads / p.lanes;
+  const size_t smem = 4 * (kForwardThreads * (size_t)(S * G + 4) + kForwardThreads +
+                           p.lanes * S * G + 2 * tokens * p.k);
+  auto *k = route_forward_kernel<S, G>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
   ++launch_counter();
-  if (kForward)
-    route_forward_kernel<E, L, R><<<blocks, kThreads, 0, st>>>(p);
-  else
-    route_backward_kernel<E, L, R><<<blocks, kThreads, 0, st>>>(p);
+  k<<<p.blocks, kForwardThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-template <class E, bool kForward>
-cudaError_t by_experts(RouteParams &p, uint32_t blocks, cudaStream_t st) {
-  if (p.E <= 16) return launch<E, 2, 8, kForward>(p, blocks, st);
-  if (p.E <= 32) return launch<E, 4, 8, kForward>(p, blocks, st);
-  if (p.E <= 64) return launch<E, 8, 8, kForward>(p, blocks, st);
-  if (p.E <= 128) return launch<E, 16, 8, kForward>(p, blocks, st);
-  if (p.E <= 256) return launch<E, 32, 8, kForward>(p, blocks, st);
-  if (p.E <= 512) return launch<E, 32, 16, kForward>(p, blocks, st);
-  return launch<E, 32, 32, kForward>(p, blocks, st);
+// A token's lanes backward, R experts each.
+template <class E, int L, int R>
+cudaError_t launch_backward(RouteParams &p, cudaStream_t st) {
+  constexpr uint32_t kTokens = kWarps * (32 / L);  // a block takes at once
+  const uint32_t blocks = (uint32_t)(((uint64_t)p.N + kTokens - 1) / kTokens);
+  ++launch_counter();
+  route_backward_kernel<E, L, R>
+      <<<blocks < 8 * kSMs ? blocks : 8 * kSMs, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
-template <bool kForward>
-cudaError_t by_type(RouteParams &p, int dtype, uint32_t blocks, cudaStream_t st) {
-  const size_t es = dtype == NS_F32 ? 4 : 2;
-  const uint32_t R = p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
-  p.wide = p.E % R == 0 && (uintptr_t)p.logits % 16 == 0 && (p.logits_row * es) % 16 == 0 &&
-           (uintptr_t)p.dlogits % 16 == 0;
-  switch (dtype) {
-    case NS_F32: return by_experts<float, kForward>(p, blocks, st);
-    case NS_BF16: return by_experts<__nv_bfloat16, kForward>(p, blocks, st);
-    default: return by_experts<__half, kForward>(p, blocks, st);
-  }
+template <class E>
+cudaError_t backward_of(RouteParams &p, cudaStream_t st) {
+  if (p.E <= 16) return launch_backward<E, 1, 16>(p, st);
+  if (p.E <= 32) return launch_backward<E, 2, 16>(p, st);
+  if (p.E <= 64) return launch_backward<E, 4, 16>(p, st);
+  if (p.E <= 128) return launch_backward<E, 8, 16>(p, st);
+  if (p.E <= 256) return launch_backward<E, 16, 16>(p, st);
+  if (p.E <= 512) return launch_backward<E, 32, 16>(p, st);
+  return launch_backward<E, 32, 32>(p, st);
 }
 
 RouteParams params_of(const ns_route_inputs &in) {
   RouteParams p = {};
-  p.logits = in.logits, p.logits_row = in.logits_row, p.doc = in.doc;
+  p.logits = in.logits, p.logits_row = in.logits_row, p.doc = in.doc, p.dtype = in.dtype;
   p.N = in.N, p.E = in.E, p.k = in.k, p.normalize = in.normalize != 0;
   return p;
+}
+
+// Whether rows of `experts` can be moved 16 bytes at a time.
+bool whole_sixteens(const ns_route_inputs &in) {
+  const size_t es = in.dtype == NS_F32 ? 4 : 2;
+  return (uintptr_t)in.logits % 16 == 0 && (in.logits_row * es) % 16 == 0 && in.E * es % 16 == 0;
 }
 
 }  // namespace
 
 uint32_t route_blocks(uint32_t N, uint32_t E) {
-  const uint32_t per = kWarps * (32 / lanes_of(E));  // tokens a block takes at once
-  const uint64_t blocks = ((uint64_t)N + per - 1) / per;
-  // up to four rounds of one block are quicker than a second kernel
-  return blocks <= 4 ? 1 : blocks < kMaxBlocks ? (uint32_t)blocks : kMaxBlocks;
+  const uint32_t tokens = kForwardThreads / shape_of(E).lanes;
+  const uint64_t tiles = ((uint64_t)N + tokens - 1) / tokens;
+  // up to two tiles, one block does without the second kernel
+  return tiles <= 2 ? 1 : tiles < 3 * kSMs ? (uint32_t)tiles : 3 * kSMs;
 }
 
 cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float *weights,
                                  int32_t *counts, int32_t *tokens, float *loss, void *workspace,
                                  cudaStream_t st) {
   RouteParams p = params_of(in);
+  const Shape shape = shape_of(in.E);
+  p.wide = whole_sixteens(in), p.lanes = shape.lanes;
   p.ids = ids, p.weights = weights, p.counts = counts, p.tokens = tokens, p.loss = loss;
   p.blocks = route_blocks(in.N, in.E);
   p.mass = static_cast<float *>(workspace);
   p.chosen = reinterpret_cast<int32_t *>(p.mass + (uint64_t)p.blocks * in.E);
   p.real = p.chosen + (uint64_t)p.blocks * in.E;
-  const cudaError_t e = by_type<true>(p, in.dtype, p.blocks, st);
+  const cudaError_t e = shape.S == 16  ? launch_forward<16, 8>(p, st)
+                        : shape.G == 8 ? launch_forward<8, 8>(p, st)
+                        : shape.G == 4 ? launch_forward<8, 4>(p, st)
+                        : shape.G == 2 ? launch_forward<8, 2>(p, st)
+                                       : launch_forward<8, 1>(p, st);
   if (e != cudaSuccess || p.blocks == 1) return e;
   ++launch_counter();
   pdl_launch(route_total_kernel, dim3(kFinalBlocks), dim3(kFinalThreads), 0, st, p);
@@ -510,10 +623,13 @@ cudaError_t launch_route_backward(const ns_route_inputs &in, const int32_t *ids,
   p.ids = const_cast<int32_t *>(ids), p.weights = const_cast<float *>(weights);
   p.counts = const_cast<int32_t *>(counts), p.tokens = const_cast<int32_t *>(tokens);
   p.d_weights = d_weights, p.d_loss = d_loss, p.dlogits = dlogits;
-  const uint32_t per = kWarps * (32 / lanes_of(in.E));
-  const uint64_t blocks = ((uint64_t)in.N + per - 1) / per;
-  return by_type<false>(p, in.dtype, blocks < 4 * kMaxBlocks ? (uint32_t)blocks : 4 * kMaxBlocks,
-                        st);
+  // a lane's experts are whole pieces of 16 bytes, or none
+  p.wide = whole_sixteens(in) && (uintptr_t)dlogits % 16 == 0;
+  switch (in.dtype) {
+    case NS_F32: return backward_of<float>(p, st);
+    case NS_BF16: return backward_of<__nv_bfloat16>(p, st);
+    default: return backward_of<__half>(p, st);
+  }
 }
 
 }  // namespace nsk
