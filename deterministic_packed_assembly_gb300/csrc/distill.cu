@@ -50,17 +50,6 @@ struct DistillParams {
   int64_t dlogits_row;
 };
 
-__device__ __forceinline__ void copy16(void *smem, const void *gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(smem)),
-               "l"(gmem)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
 __device__ __forceinline__ void copy_wait_left(int left) {
   if (left == 3) copy_wait<3>();
   else if (left == 2) copy_wait<2>();
@@ -195,7 +184,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillParam
       if (c < mine) {
         const int64_t i = e0 + (int64_t)c * kN;
         if (i >= 0 && i + kN <= (int64_t)p.V) {
-          copy16(slice + (size_t)c * kN, src + i);
+          copy_async<16>(slice + (size_t)c * kN, src + i);
         } else {  // the row's ends
 #pragma unroll
           for (int k = 0; k < kN; ++k)

@@ -68,107 +68,45 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Elements of one access of at most 16 bytes.
-template <class E, int R>
-constexpr int kMove = R * sizeof(E) <= 16 ? R : 16 / sizeof(E);
-
-// The lane's experts of token n (-inf where there is none or `real` is false).
-template <class E, int R>
-__device__ __forceinline__ void load_logits(const RouteParams &p, uint32_t n, uint32_t i0,
-                                            bool real, float (&x)[R]) {
-  constexpr int kN = kMove<E, R>;
-#pragma unroll
-  for (int r = 0; r < R; ++r) x[r] = kNegInf;
-  if (!real) return;
-  const E *src = static_cast<const E *>(p.logits) + (int64_t)n * p.logits_row + i0;
-  if (p.wide) {
-#pragma unroll
-    for (int r = 0; r < R; r += kN) {
-      if (i0 + r < p.E) {
-        const Vec<E, kN> v = *reinterpret_cast<const Vec<E, kN> *>(src + r);
-#pragma unroll
-        for (int q = 0; q < kN; ++q) x[r + q] = to_f32(v.v[q]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i0 + r < p.E) x[r] = to_f32(src[r]);
-  }
-}
-
-// Softmax of a token: x becomes exp(x - max), and their sum is returned (0 for
-// a token that counts for nothing).  The difference is taken before the change
-// of base, which overflows for logits near the type's lowest value.
-template <int L, int R>
-__device__ __forceinline__ float exponentials(float (&x)[R], float &base) {
-  float m = x[0];
-#pragma unroll
-  for (int r = 1; r < R; ++r) m = fmaxf(m, x[r]);
-  m = group_max<L>(m);
-  base = m == kNegInf ? 0.0f : m;
-  float s = 0.0f;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    x[r] = exp2_sfu((x[r] - base) * kLog2e);
-    s += x[r];
-  }
-  return group_sum<L>(s);
-}
-
 __device__ __forceinline__ float balance(uint32_t E, uint32_t k, int32_t M) {
   return M == 0 ? 0.0f : (float)E / (float)k / ((float)M * (float)M);
 }
 
 // ---- forward ------------------------------------------------------------------
-// Walks the (row, place) pairs of a tile with `per` places a row, a thread's every
-// kForwardThreads-th, without a division a step.
-struct Walk {
-  uint32_t row, at, rows_a_step, rest, per;
-  __device__ __forceinline__ explicit Walk(uint32_t per_row) : per(per_row) {
-    row = threadIdx.x / per, at = threadIdx.x % per;
-    rows_a_step = kForwardThreads / per, rest = kForwardThreads % per;
-  }
-  __device__ __forceinline__ void next() {
-    row += rows_a_step, at += rest;
-    if (at >= per) at -= per, ++row;
-  }
-};
-
 // A tile's logits into shared memory, as floats: token n0 + row's expert e at
-// row `row * lanes + e / SG`, place e % SG.  -inf for tokens that do not count.
+// row `row * lanes + e / SG`, place e % SG.  `tokens` of them are inside the call.
 template <class E, int SG, int kPitch>
 __device__ __forceinline__ void load_tile(const RouteParams &p, uint64_t n0, uint32_t tokens,
                                           float *tile) {
-  auto real = [&](uint32_t row) {
-    const uint64_t n = n0 + row;
-    return n < p.N && !(p.doc && __ldg(p.doc + n) < 0);
-  };
-  if (p.wide) {
-    constexpr int kN = 16 / sizeof(E);
-    for (Walk w(p.E / kN); w.row < tokens; w.next()) {
-      const uint32_t e = w.at * kN;
-      float *to = tile + (w.row * p.lanes + e / SG) * kPitch + e % SG;
-      float x[kN];
-#pragma unroll
-      for (int q = 0; q < kN; ++q) x[q] = kNegInf;
-      if (real(w.row)) {
-        const Vec<E, kN> v = *reinterpret_cast<const Vec<E, kN> *>(
-            static_cast<const E *>(p.logits) + (int64_t)(n0 + w.row) * p.logits_row + e);
-#pragma unroll
-        for (int q = 0; q < kN; ++q) x[q] = to_f32(v.v[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < kN; q += 4)
-        *reinterpret_cast<float4 *>(to + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+  // A thread's pieces are kForwardThreads apart: the row and the place move on
+  // without a division.
+  constexpr int kN = 16 / sizeof(E);
+  const uint32_t per = p.wide ? p.E / kN : p.E, size = p.wide ? kN : 1;  // pieces a row
+  const uint32_t rows = kForwardThreads / per, rest = kForwardThreads % per;
+  uint32_t row = threadIdx.x / per, at = threadIdx.x % per;
+  const E *from =
+      static_cast<const E *>(p.logits) + (int64_t)(n0 + row) * p.logits_row + at * size;
+  const int64_t step = (int64_t)rows * p.logits_row + rest * size,
+                wrap = p.logits_row - (int64_t)per * size;
+  while (row < tokens) {
+    const uint32_t e = at * size;
+    float *to = tile + row * (p.lanes * kPitch) + e + e / SG * (kPitch - SG);
+    if (!p.wide) {
+      *to = to_f32(*from);
+    } else if constexpr (sizeof(E) == 4) {
+      copy_async<16>(to, from);
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4 *>(from);
+      const Ch<2> a = widen_pair<E>(v.x), b = widen_pair<E>(v.y), c = widen_pair<E>(v.z),
+                  d = widen_pair<E>(v.w);
+      reinterpret_cast<float4 *>(to)[0] = make_float4(a.v[0], a.v[1], b.v[0], b.v[1]);
+      reinterpret_cast<float4 *>(to)[1] = make_float4(c.v[0], c.v[1], d.v[0], d.v[1]);
     }
-  } else {
-    for (Walk w(p.E); w.row < tokens; w.next())
-      tile[(w.row * p.lanes + w.at / SG) * kPitch + w.at % SG] =
-          real(w.row) ? to_f32(static_cast<const E *>(
-                            p.logits)[(int64_t)(n0 + w.row) * p.logits_row + w.at])
-                      : kNegInf;
+    row += rows, at += rest, from += step;
+    if (at >= per) at -= per, ++row, from += wrap;
   }
+  copy_commit();
+  copy_wait<0>();
 }
 
 template <int S>
@@ -177,6 +115,22 @@ __device__ __forceinline__ void load_group(const float *at, float (&v)[S]) {
   for (int q = 0; q < S; q += 4) {
     const float4 x = *reinterpret_cast<const float4 *>(at + q);
     v[q] = x.x, v[q + 1] = x.y, v[q + 2] = x.z, v[q + 3] = x.w;
+  }
+}
+
+// Add the probabilities of a thread's n experts, kForwardThreads (a row or more of
+// SG) apart, up over every `parts`-th token.
+template <int n, int SG, int kPitch, int kMax>
+__device__ __forceinline__ void add_columns(const float *column, const float *inv, uint32_t first,
+                                            uint32_t tokens, uint32_t parts, uint32_t lanes,
+                                            float (&sum)[kMax]) {
+  const float *at = column + first * lanes * kPitch;
+#pragma unroll 4
+  for (uint32_t r = first; r < tokens; r += parts, at += parts * lanes * kPitch) {
+    const float by = inv[r];
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      sum[i] = fmaf(at[i * (kForwardThreads / SG) * kPitch], by, sum[i]);
   }
 }
 
@@ -201,24 +155,22 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
   const uint32_t side = columns < kForwardThreads ? columns : kForwardThreads;
   const uint32_t parts = kForwardThreads / side, my_part = tid / side, per_thread = columns / side;
   float sum[kMaxColumns];
-  uint32_t place[kMaxColumns];
 #pragma unroll
-  for (int i = 0; i < kMaxColumns; ++i) {
-    const uint32_t e = tid % side + i * kForwardThreads;
-    sum[i] = 0.0f;
-    place[i] = e / SG * kPitch + e % SG;
-  }
+  for (int i = 0; i < kMaxColumns; ++i) sum[i] = 0.0f;
   int counted = 0;
   const uint64_t tiles = ((uint64_t)p.N + tokens - 1) / tokens;
   for (uint64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const uint64_t n0 = t * tokens;
     __syncthreads();  // the last tile is done with
-    if (p.dtype == NS_F32) load_tile<float, SG, kPitch>(p, n0, tokens, tile);
-    else if (p.dtype == NS_BF16) load_tile<__nv_bfloat16, SG, kPitch>(p, n0, tokens, tile);
-    else load_tile<__half, SG, kPitch>(p, n0, tokens, tile);
-    for (int i = (int)p.E > (int)(lp * SG) ? (int)(p.E - lp * SG) : 0; i < SG; ++i)
-      mine[i] = kNegInf;  // places beyond the last expert
+    const uint32_t here = p.N - n0 < tokens ? (uint32_t)(p.N - n0) : tokens;
+    if (p.dtype == NS_F32) load_tile<float, SG, kPitch>(p, n0, here, tile);
+    else if (p.dtype == NS_BF16) load_tile<__nv_bfloat16, SG, kPitch>(p, n0, here, tile);
+    else load_tile<__half, SG, kPitch>(p, n0, here, tile);
+    const bool real = token < here && !(p.doc && __ldg(p.doc + n0 + token) < 0);
     __syncthreads();
+    // places beyond the last expert, and all of a token that does not count
+    const int used = !real || p.E <= lp * SG ? 0 : (int)min(p.E - lp * SG, (uint32_t)SG);
+    for (int i = used; i < SG; ++i) mine[i] = kNegInf;
 
     // The k largest: by groups.  NaN is below everything (a maximum leaves it out).
     float top[G];
@@ -285,15 +237,18 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     // Exponentials in the logits' place, and their sum.  The difference is taken
     // before the change of base, which overflows near the type's lowest value.
     const float base = m == kNegInf ? 0.0f : m;
-    float s = 0.0f;
+    Ch<2> s2 = splat<2>(0.0f);
 #pragma unroll 4
     for (int i = 0; i < SG; i += 4) {
-      float4 x = *reinterpret_cast<const float4 *>(mine + i);
-      x.x = exp2_sfu((x.x - base) * kLog2e), x.y = exp2_sfu((x.y - base) * kLog2e);
-      x.z = exp2_sfu((x.z - base) * kLog2e), x.w = exp2_sfu((x.w - base) * kLog2e);
-      s += (x.x + x.y) + (x.z + x.w);
-      *reinterpret_cast<float4 *>(mine + i) = x;
+      const float4 x = *reinterpret_cast<const float4 *>(mine + i);
+      Ch<2> a = (Ch<2>{x.x, x.y} + splat<2>(-base)) * splat<2>(kLog2e);
+      Ch<2> b = (Ch<2>{x.z, x.w} + splat<2>(-base)) * splat<2>(kLog2e);
+      a = {exp2_sfu(a.v[0]), exp2_sfu(a.v[1])};
+      b = {exp2_sfu(b.v[0]), exp2_sfu(b.v[1])};
+      s2 = s2 + (a + b);
+      *reinterpret_cast<float4 *>(mine + i) = make_float4(a.v[0], a.v[1], b.v[0], b.v[1]);
     }
+    float s = s2.v[0] + s2.v[1];
     for (uint32_t o = LP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float by_all = s == 0.0f ? 0.0f : 1.0f / s;
     if (lp == 0) {
@@ -314,20 +269,19 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     }
     __syncthreads();
 
-    const uint64_t left = p.N - n0;
-    const uint32_t here = left < tokens ? (uint32_t)left : tokens;
     for (uint32_t i = tid; i < here * p.k; i += kForwardThreads) {
       p.ids[n0 * p.k + i] = top_id[i];
       p.weights[n0 * p.k + i] = top_x[i];
     }
-#pragma unroll 4
-    for (uint32_t r = my_part; r < tokens; r += parts) {
-      const float by_token = inv[r];
-      const float *row = tile + r * LP * kPitch;
-#pragma unroll
-      for (int i = 0; i < kMaxColumns; ++i)
-        if (i < (int)per_thread) sum[i] = fmaf(row[place[i]], by_token, sum[i]);
-    }
+    const float *column = tile + (tid % side) / SG * kPitch + (tid % side) % SG;
+    if (SG < kForwardThreads || per_thread == 1)
+      add_columns<1, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
+    else if (per_thread == 2)
+      add_columns<2, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
+    else if (per_thread == 4)
+      add_columns<4, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
+    else
+      add_columns<8, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
   }
   counted = warp_sum_i32(counted);
   if (lane == 0) atomicAdd(&real_tokens, counted);
@@ -431,85 +385,147 @@ __global__ void __launch_bounds__(kFinalThreads) __cluster_dims__(kFinalBlocks, 
   }
 }
 
+// ---- backward -------------------------------------------------------------------
+// A lane's R experts of a token from `src`, in pairs; -inf where there is none.
+template <class E, int R>
+__device__ __forceinline__ void load_logits(const E *src, uint32_t i0, uint32_t experts, bool wide,
+                                            Ch<2> (&x)[R / 2]) {
+  constexpr int kN = 16 / sizeof(E);
+  if (wide) {
+#pragma unroll
+    for (int r = 0; r < R; r += kN) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const bool in = i0 + r < experts;
+      if (in) v = *reinterpret_cast<const uint4 *>(src + r);
+      if constexpr (sizeof(E) == 4) {
+        x[r / 2] = {__uint_as_float(v.x), __uint_as_float(v.y)};
+        x[r / 2 + 1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
+      } else {
+        x[r / 2] = widen_pair<E>(v.x), x[r / 2 + 1] = widen_pair<E>(v.y);
+        x[r / 2 + 2] = widen_pair<E>(v.z), x[r / 2 + 3] = widen_pair<E>(v.w);
+      }
+      if (!in) {
+#pragma unroll
+        for (int q = 0; q < kN; ++q) x[(r + q) / 2].v[(r + q) % 2] = kNegInf;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      x[r / 2].v[r % 2] = i0 + r < experts ? to_f32(src[r]) : kNegInf;
+  }
+}
+template <class E, int R>
+__device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t experts, bool wide,
+                                             const Ch<2> (&d)[R / 2]) {
+  constexpr int kN = 16 / sizeof(E);
+  if (wide) {
+#pragma unroll
+    for (int r = 0; r < R; r += kN) {
+      uint4 v;
+      if constexpr (sizeof(E) == 4)
+        v = make_uint4(__float_as_uint(d[r / 2].v[0]), __float_as_uint(d[r / 2].v[1]),
+                       __float_as_uint(d[r / 2 + 1].v[0]), __float_as_uint(d[r / 2 + 1].v[1]));
+      else
+        v = make_uint4(narrow_pair<E>(d[r / 2]), narrow_pair<E>(d[r / 2 + 1]),
+                       narrow_pair<E>(d[r / 2 + 2]), narrow_pair<E>(d[r / 2 + 3]));
+      if (i0 + r < experts) *reinterpret_cast<uint4 *>(dst + r) = v;
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i0 + r < experts) dst[r] = from_f32<E>(d[r / 2].v[r % 2]);
+  }
+}
+
 template <class E, int L, int R>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteParams p) {
-  constexpr int G = 32 / L, kExperts = L * R;
-  __shared__ __align__(16) float add[kWarps][G][kExperts];  // the weights' part, 0 elsewhere
+  constexpr int G = 32 / L, kExperts = L * R, kP = R / 2;
+  // the weights' part of a token's gradient, 0 but where it has one; four floats
+  // more a token keep the lanes' 16-byte reads off each other's banks
+  __shared__ __align__(16) float add[kWarps][G][kExperts + 4 * L];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / L, gl = lane % L;
   const uint32_t i0 = gl * R;
   float *my_add = add[warp][group];
-  float g[R];
-  const float coef =
-      p.d_loss ? p.d_loss[0] * balance(p.E, p.k, p.tokens[0]) : 0.0f;
+  auto place = [](uint32_t e) { return e + e / R * 4; };
+  Ch<2> g[kP];
+  const float coef = p.d_loss ? p.d_loss[0] * balance(p.E, p.k, p.tokens[0]) : 0.0f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    g[r] = p.d_loss && i0 + r < p.E ? coef * (float)p.counts[i0 + r] : 0.0f;
-    my_add[i0 + r] = 0.0f;
+    g[r / 2].v[r % 2] = p.d_loss && i0 + r < p.E ? coef * (float)p.counts[i0 + r] : 0.0f;
+    my_add[place(i0 + r)] = 0.0f;
   }
   __syncwarp();
-  const uint64_t step = (uint64_t)gridDim.x * kWarps * G;
-  for (uint64_t n0 = ((uint64_t)blockIdx.x * kWarps + warp) * G; n0 < p.N; n0 += step) {
+  const uint32_t step = gridDim.x * kWarps * G;
+  uint64_t n0 = ((uint64_t)blockIdx.x * kWarps + warp) * G;
+  const E *src = static_cast<const E *>(p.logits) + (int64_t)(n0 + group) * p.logits_row + i0;
+  E *dst = static_cast<E *>(p.dlogits) + (int64_t)(n0 + group) * p.E + i0;
+  for (; n0 < p.N; n0 += step, src += (int64_t)step * p.logits_row, dst += (int64_t)step * p.E) {
     const bool in = n0 + group < p.N;
-    const uint32_t n = in ? (uint32_t)(n0 + group) : 0;
+    const uint32_t n = in ? (uint32_t)n0 + group : 0;
     const bool real = in && !(p.doc && __ldg(p.doc + n) < 0);
-    float x[R], base;
-    load_logits<E, R>(p, n, i0, real, x);
-    const float s = exponentials<L, R>(x, base);
-    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s);
-    float dot = 0.0f;
+    Ch<2> x[kP];
+    if (real) {
+      load_logits<E, R>(src, i0, p.E, p.wide, x);
+    } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      x[r] *= inv;
-      dot += x[r] * g[r];
+      for (int r = 0; r < kP; ++r) x[r] = splat<2>(kNegInf);
     }
     const uint32_t at = n * p.k;  // below 2^31
+    // w = p at the chosen ones: dl_j = w_j dw_j - p_j t at them, t = sum w dw;
+    // normalised, w is their own softmax: dl_j = w_j (dw_j - t)
+    float t = 0.0f;
     if (p.d_weights) {
-      // w = p at the chosen ones: dl_j = w_j dw_j - p_j t at them, t = sum w dw;
-      // normalised, w is their own softmax: dl_j = w_j (dw_j - t)
-      float t = 0.0f;
       for (uint32_t j = gl; real && j < p.k; j += L)
-        if (p.ids[at + j] >= 0) t += p.weights[at + j] * p.d_weights[at + j];
-      t = group_sum<L>(t);
+        if (p.ids[at + j] >= 0) t += p.weights[at + j] * p.d_weights[at + j];  // -1: no choice
+    }
+    float m = kNegInf;
+#pragma unroll
+    for (int r = 0; r < kP; ++r) m = fmaxf(m, fmaxf(x[r].v[0], x[r].v[1]));
+    m = group_max<L>(m);
+    const Ch<2> base = splat<2>(m == kNegInf ? 0.0f : -m);
+    Ch<2> s2 = splat<2>(0.0f), dot2 = s2;
+#pragma unroll
+    for (int r = 0; r < kP; ++r) {
+      const Ch<2> y = (x[r] + base) * splat<2>(kLog2e);
+      x[r] = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+      s2 = s2 + x[r];
+      dot2 = fma(x[r], g[r], dot2);
+    }
+    float s = s2.v[0] + s2.v[1], dot = dot2.v[0] + dot2.v[1];
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (p.d_weights) t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    if (p.d_weights) {
       for (uint32_t j = gl; real && j < p.k; j += L) {
-        const int id = p.ids[at + j];  // -1: there is no such choice
+        const int id = p.ids[at + j];
         if (id >= 0 && id < (int)p.E)
-          my_add[id] = p.weights[at + j] * (p.d_weights[at + j] - (p.normalize ? t : 0.0f));
+          my_add[place(id)] = p.weights[at + j] * (p.d_weights[at + j] - (p.normalize ? t : 0.0f));
       }
-      dot += p.normalize || gl > 0 ? 0.0f : t;
       __syncwarp();
     }
-    dot = group_sum<L>(dot);
-    if (in) {
-      constexpr int kN = kMove<E, R>;
-      E *dst = static_cast<E *>(p.dlogits) + (int64_t)n * p.E + i0;
-      float d[R];
+    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s);
+    dot = fmaf(dot, inv, p.normalize ? 0.0f : t);
+    const Ch<2> inv2 = splat<2>(inv), minus = splat<2>(-dot);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        d[r] = x[r] * (g[r] - dot);
-        if (p.d_weights) d[r] += my_add[i0 + r];
-        if (s == 0.0f) d[r] = 0.0f;
-      }
-      if (p.wide) {
-#pragma unroll
-        for (int r = 0; r < R; r += kN) {
-          if (i0 + r < p.E) {
-            Vec<E, kN> v;
-#pragma unroll
-            for (int q = 0; q < kN; ++q) v.v[q] = from_f32<E>(d[r + q]);
-            *reinterpret_cast<Vec<E, kN> *>(dst + r) = v;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (i0 + r < p.E) dst[r] = from_f32<E>(d[r]);
-      }
+    for (int r = 0; r < kP; r += 2) {
+      const float4 w = *reinterpret_cast<const float4 *>(my_add + place(i0) + 2 * r);
+      x[r] = fma(x[r] * inv2, g[r] + minus, Ch<2>{w.x, w.y});
+      x[r + 1] = fma(x[r + 1] * inv2, g[r + 1] + minus, Ch<2>{w.z, w.w});
     }
+    if (s == 0.0f) {  // the token counts for nothing
+#pragma unroll
+      for (int r = 0; r < kP; ++r) x[r] = splat<2>(0.0f);
+    }
+    if (in) store_logits<E, R>(dst, i0, p.E, p.wide, x);
     if (p.d_weights) {
       __syncwarp();
       for (uint32_t j = gl; real && j < p.k; j += L) {
         const int id = p.ids[at + j];
-        if (id >= 0 && id < (int)p.E) my_add[id] = 0.0f;
+        if (id >= 0 && id < (int)p.E) my_add[place(id)] = 0.0f;
       }
       __syncwarp();
     }

@@ -69,54 +69,6 @@ struct ScanParams {
   float *partial, *dh0;
 };
 
-// A lane's one or two channels; two are computed by the packed instructions.
-template <int CH>
-struct Ch;
-template <>
-struct Ch<1> {
-  float v[1];
-};
-template <>
-struct alignas(8) Ch<2> {
-  float v[2];
-};
-__device__ __forceinline__ uint64_t bits(Ch<2> a) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.v[0]), "f"(a.v[1]));
-  return r;
-}
-__device__ __forceinline__ Ch<2> unbits(uint64_t r) {
-  Ch<2> a;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.v[0]), "=f"(a.v[1]) : "l"(r));
-  return a;
-}
-__device__ __forceinline__ Ch<1> fma(Ch<1> a, Ch<1> b, Ch<1> c) {
-  return {fmaf(a.v[0], b.v[0], c.v[0])};
-}
-__device__ __forceinline__ Ch<2> fma(Ch<2> a, Ch<2> b, Ch<2> c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return unbits(r);
-}
-__device__ __forceinline__ Ch<1> operator*(Ch<1> a, Ch<1> b) { return {a.v[0] * b.v[0]}; }
-__device__ __forceinline__ Ch<2> operator*(Ch<2> a, Ch<2> b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return unbits(r);
-}
-__device__ __forceinline__ Ch<1> operator+(Ch<1> a, Ch<1> b) { return {a.v[0] + b.v[0]}; }
-__device__ __forceinline__ Ch<2> operator+(Ch<2> a, Ch<2> b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return unbits(r);
-}
-template <int CH>
-__device__ __forceinline__ Ch<CH> splat(float x) {
-  Ch<CH> r;
-#pragma unroll
-  for (int k = 0; k < CH; ++k) r.v[k] = x;
-  return r;
-}
 // a - b, as a + (-1) b: exact as a subtraction
 template <int CH>
 __device__ __forceinline__ Ch<CH> sub(Ch<CH> a, Ch<CH> b) {
@@ -153,23 +105,16 @@ template <class E, int CH>
 __device__ __forceinline__ Ch<CH> widen(Raw<E, CH> x) {
   if constexpr (CH == 1) {
     return {to_f32(x)};
-  } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
-    return {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
   } else {
-    const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&x));
-    return {v.x, v.y};
+    return widen_pair<E>(x);
   }
 }
 template <class E, int CH>
 __device__ __forceinline__ Raw<E, CH> narrow(Ch<CH> x) {
   if constexpr (CH == 1) {
     return from_f32<E>(x.v[0]);
-  } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x.v[0], x.v[1]);
-    return *reinterpret_cast<const uint32_t *>(&v);
   } else {
-    const __half2 v = __floats2half2_rn(x.v[0], x.v[1]);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    return narrow_pair<E>(x);
   }
 }
 template <int CH>
@@ -214,20 +159,6 @@ template <class E, int CH, int A>
 struct alignas(16) Stage {
   Raw<E, CH> v[A][kSteps][32];
 };
-
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
-  const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
-}
 
 // Copies of a segment's rows.  `wide`: rows, strides and widths are multiples of 16
 // bytes, and a lane copies 16 bytes of every fourth row; else its own channels of
