@@ -121,14 +121,15 @@ static bool check_route(const ns_route_inputs *in) {
 
 uint64_t ns_route_workspace(uint32_t N, uint32_t E) {
   const uint64_t blocks = nsk::route_blocks(N, E);
-  return blocks * (8ull * E + 4);
+  return blocks == 1 ? 0 : blocks * (8ull * E + 4);
 }
 
 int ns_route_forward(const ns_route_inputs *in, int32_t *ids, float *weights, int32_t *counts,
                      int32_t *tokens, float *loss, void *workspace, void *cuda_stream) {
   if (!check_route(in)) return NS_ERR_INVALID_ARG;
   if (!usable(ids, 4, in->N == 0) || !usable(weights, 4, in->N == 0) || !usable(counts, 4) ||
-      !usable(tokens, 4) || !usable(loss, 4) || !usable(workspace, 4))
+      !usable(tokens, 4) || !usable(loss, 4) ||
+      !usable(workspace, 4, ns_route_workspace(in->N, in->E) == 0))
     return NS_ERR_INVALID_ARG;
   return done(nsk::launch_route_forward(*in, ids, weights, counts, tokens, loss, workspace,
                                         static_cast<cudaStream_t>(cuda_stream)));

@@ -43,8 +43,10 @@ def _optional(t, name: str, dtype: torch.dtype, shape: tuple, device) -> Optiona
     """The address of an optional contiguous tensor."""
     if t is None:
         return None
-    _need(t, name, dtype, device)
-    _shape(t, name, shape)
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
+            and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, device)  # says which of them it is
+        _shape(t, name, shape)
     return t.data_ptr()
 
 
@@ -54,59 +56,61 @@ def _rows(t: torch.Tensor, name: str) -> None:
         _refuse(f"{name}: strides {t.stride()}, the last dimension has to be contiguous")
 
 
-class _On:
-    """The device of a call, made current if it is not; the current stream there."""
+def _elsewhere(t) -> bool:
+    """Whether a CUDA tensor is on another device than the current one."""
+    return t.device.index != torch.cuda.current_device()
 
-    def __init__(self, device):
-        self.device, self.other = device, None
 
-    def __enter__(self) -> int:
-        if self.device.index != torch.cuda.current_device():
-            self.other = torch.cuda.device(self.device)
-            self.other.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
+# The current stream's handle; building a torch.cuda.Stream for it takes 3 us.
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                return True
+    return False
 
 
 # ---- gated linear recurrence ---------------------------------------------------
 def _scan_inputs(z, f, bias, pos, doc) -> L.ns_scan_inputs:
     code = _floats(z, "z")
-    if z.dim() != 3:
-        _refuse(f"z: shape {tuple(z.shape)}, expected [B, T, D]")
-    if not isinstance(f, torch.Tensor) or f.dtype != z.dtype or f.device != z.device:
+    shape = z.shape
+    if len(shape) != 3:
+        _refuse(f"z: shape {tuple(shape)}, expected [B, T, D]")
+    device = z.device
+    if not isinstance(f, torch.Tensor) or f.dtype != z.dtype or f.device != device:
         _refuse("f: expected a tensor of z's dtype on z's device")
-    _shape(f, "f", z.shape)
-    _rows(z, "z")
-    _rows(f, "f")
-    B, T, D = z.shape
+    if f.shape != shape:
+        _shape(f, "f", shape)
+    B, T, D = shape
     zs, fs = z.stride(), f.stride()
+    if (zs[2] != 1 or fs[2] != 1) and D > 1:
+        _rows(z, "z")
+        _rows(f, "f")
     return L.ns_scan_inputs(
         z.data_ptr(), f.data_ptr(), zs[0], zs[1], fs[0], fs[1],
-        _optional(bias, "bias", torch.float32, (D,), z.device),
-        _optional(pos, "pos", torch.int32, (B, T), z.device),
-        _optional(doc, "doc", torch.int32, (B, T), z.device), B, T, D, code)
+        _optional(bias, "bias", torch.float32, (D,), device),
+        _optional(pos, "pos", torch.int32, (B, T), device),
+        _optional(doc, "doc", torch.int32, (B, T), device), B, T, D, code)
 
 
 def _scan(z, f, bias, pos, doc, h0, keep: bool):
     inputs = _scan_inputs(z, f, bias, pos, doc)
-    B, T, D = z.shape
-    h0_ptr = _optional(h0, "h0", torch.float32, (B, D), z.device)
-    with _On(z.device) as stream:
-        y = torch.empty((B, T, D), dtype=z.dtype, device=z.device)
-        h_last = torch.empty((B, D), dtype=torch.float32, device=z.device)
-        states = None
-        if keep:
-            states = torch.empty((B, -(-T // L.NS_SCAN_TILE), D), dtype=torch.float32,
-                                 device=z.device)
-        L.ns_scan_forward(inputs, h0_ptr, y.data_ptr(), h_last.data_ptr(),
-                          states.data_ptr() if keep else None, stream)
+    if _elsewhere(z):
+        with torch.cuda.device(z.device):
+            return _scan(z, f, bias, pos, doc, h0, keep)
+    B, T, D = shape = z.shape
+    device = z.device
+    h0_ptr = _optional(h0, "h0", torch.float32, (B, D), device)
+    y = torch.empty(shape, dtype=z.dtype, device=device)
+    h_last = torch.empty((B, D), dtype=torch.float32, device=device)
+    states = None
+    if keep:
+        states = torch.empty((B, -(-T // L.NS_SCAN_TILE), D), dtype=torch.float32, device=device)
+    L.ns_scan_forward(inputs, h0_ptr, y.data_ptr(), h_last.data_ptr(),
+                      states.data_ptr() if keep else None, _stream(device.index))
     return y, h_last, states
 
 
@@ -125,29 +129,30 @@ def gated_scan_backward(dy: torch.Tensor, dh_last: Optional[torch.Tensor], z: to
     None), with the forward pass's inputs and ``states``; dbias is None where
     ``bias`` is."""
     inputs = _scan_inputs(z, f, bias, pos, doc)
-    B, T, D = z.shape
-    if not isinstance(dy, torch.Tensor) or dy.dtype != z.dtype or dy.device != z.device:
+    if _elsewhere(z):
+        with torch.cuda.device(z.device):
+            return gated_scan_backward(dy, dh_last, z, f, bias, states, pos=pos, doc=doc)
+    B, T, D = shape = z.shape
+    device = z.device
+    if not isinstance(dy, torch.Tensor) or dy.dtype != z.dtype or dy.device != device:
         _refuse("dy: expected a tensor of z's dtype on z's device")
-    _shape(dy, "dy", z.shape)
+    _shape(dy, "dy", shape)
     _rows(dy, "dy")
-    dh_ptr = _optional(dh_last, "dh_last", torch.float32, (B, D), z.device)
+    dh_ptr = _optional(dh_last, "dh_last", torch.float32, (B, D), device)
     if states is None:
         _refuse("states: expected what gated_scan_forward returned")
-    states_ptr = _optional(states, "states", torch.float32, (B, -(-T // L.NS_SCAN_TILE), D),
-                           z.device)
-    with _On(z.device) as stream:
-        dz = torch.empty((B, T, D), dtype=z.dtype, device=z.device)
-        df = torch.empty((B, T, D), dtype=z.dtype, device=z.device)
-        dh0 = torch.empty((B, D), dtype=torch.float32, device=z.device)
-        dbias = work = None
-        if bias is not None:
-            dbias = torch.empty(D, dtype=torch.float32, device=z.device)
-            work = torch.empty(L.ns_scan_workspace(B, T, D) // 4, dtype=torch.float32,
-                               device=z.device)
-        L.ns_scan_backward(inputs, states_ptr, dy.data_ptr(), dy.stride(0), dy.stride(1), dh_ptr,
-                           dz.data_ptr(), df.data_ptr(),
-                           None if dbias is None else dbias.data_ptr(), dh0.data_ptr(),
-                           None if work is None else work.data_ptr(), stream)
+    states_ptr = _optional(states, "states", torch.float32, (B, -(-T // L.NS_SCAN_TILE), D), device)
+    dz = torch.empty(shape, dtype=z.dtype, device=device)
+    df = torch.empty(shape, dtype=z.dtype, device=device)
+    dh0 = torch.empty((B, D), dtype=torch.float32, device=device)
+    dbias = work = None
+    if bias is not None:
+        dbias = torch.empty(D, dtype=torch.float32, device=device)
+        work = torch.empty(L.ns_scan_workspace(B, T, D) // 4, dtype=torch.float32, device=device)
+    dys = dy.stride()
+    L.ns_scan_backward(inputs, states_ptr, dy.data_ptr(), dys[0], dys[1], dh_ptr, dz.data_ptr(),
+                       df.data_ptr(), None if dbias is None else dbias.data_ptr(), dh0.data_ptr(),
+                       None if work is None else work.data_ptr(), _stream(device.index))
     return dz, df, dbias, dh0
 
 
@@ -201,41 +206,46 @@ def _distill(logits, top_logits, top_ids, mask, temperature, teacher_lse, weight
     code = _floats(logits, "logits")
     if logits.dim() != 2:
         _refuse(f"logits: shape {tuple(logits.shape)}, expected [N, V]")
-    _rows(logits, "logits")
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return _distill(logits, top_logits, top_ids, mask, temperature, teacher_lse, weight,
+                            out, grad)
     N, V = logits.shape
-    dev = logits.device
+    row, column = logits.stride()
+    if column != 1:
+        _rows(logits, "logits")
+    device = logits.device
     top_code = _floats(top_logits, "top_logits")
-    _need(top_logits, "top_logits", top_logits.dtype, dev)
-    if top_logits.dim() != 2 or top_logits.shape[0] != N:
-        _refuse(f"top_logits: shape {tuple(top_logits.shape)}, expected [{N}, K]")
+    shape = top_logits.shape
+    if len(shape) != 2 or shape[0] != N:
+        _refuse(f"top_logits: shape {tuple(shape)}, expected [{N}, K]")
     ids_64 = isinstance(top_ids, torch.Tensor) and top_ids.dtype == torch.int64
-    _need(top_ids, "top_ids", torch.int64 if ids_64 else torch.int32, dev)
-    _shape(top_ids, "top_ids", top_logits.shape)
-    if mask is not None and isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+    if top_ids is None:
+        _refuse("top_ids: expected a tensor")
+    if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
         mask = mask.view(torch.uint8)
     inputs = L.ns_distill_inputs(
-        logits.data_ptr(), max(logits.stride(0), V) if N == 1 else logits.stride(0),
-        top_logits.data_ptr(), top_ids.data_ptr(),
-        _optional(teacher_lse, "teacher_lse", torch.float32, (N,), dev),
-        _optional(mask, "mask", torch.uint8, (N,), dev),
-        _optional(weight, "weight", torch.float32, (N,), dev),
-        N, V, top_logits.shape[1], code, top_code, ids_64, float(temperature))
-    with _On(dev) as stream:
-        loss = torch.empty(N, dtype=torch.float32, device=dev)
-        dlogits = None
-        if grad:
-            dlogits = out
-            if out is None:
-                dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
-            elif (not isinstance(out, torch.Tensor) or out.dtype != logits.dtype
-                  or out.device != dev):
-                _refuse("out: expected a tensor of the logits' dtype on their device")
-            _shape(dlogits, "out", (N, V))
-            _rows(dlogits, "out")
-        L.ns_distill(inputs, loss.data_ptr(), None if dlogits is None else dlogits.data_ptr(),
-                     0 if dlogits is None else
-                     max(dlogits.stride(0), V) if N == 1 else dlogits.stride(0), stream)
-    return loss, dlogits
+        logits.data_ptr(), row if N > 1 else max(row, V),
+        _optional(top_logits, "top_logits", top_logits.dtype, shape, device),
+        _optional(top_ids, "top_ids", torch.int64 if ids_64 else torch.int32, shape, device),
+        _optional(teacher_lse, "teacher_lse", torch.float32, (N,), device),
+        _optional(mask, "mask", torch.uint8, (N,), device),
+        _optional(weight, "weight", torch.float32, (N,), device),
+        N, V, shape[1], code, top_code, ids_64, float(temperature))
+    loss = torch.empty(N, dtype=torch.float32, device=device)
+    if not grad:
+        L.ns_distill(inputs, loss.data_ptr(), None, 0, _stream(device.index))
+        return loss, None
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=device)
+    elif not isinstance(out, torch.Tensor) or out.dtype != logits.dtype or out.device != device:
+        _refuse("out: expected a tensor of the logits' dtype on their device")
+    _shape(out, "out", (N, V))
+    _rows(out, "out")
+    out_row = out.stride(0)
+    L.ns_distill(inputs, loss.data_ptr(), out.data_ptr(), out_row if N > 1 else max(out_row, V),
+                 _stream(device.index))
+    return loss, out
 
 
 def distill_grad(logits: torch.Tensor, top_logits: torch.Tensor, top_ids: torch.Tensor, *,
@@ -303,10 +313,12 @@ def _route_inputs(logits, k, doc, normalize) -> L.ns_route_inputs:
     code = _floats(logits, "logits")
     if logits.dim() != 2:
         _refuse(f"logits: shape {tuple(logits.shape)}, expected [N, E]")
-    _rows(logits, "logits")
     N, E = logits.shape
+    row, column = logits.stride()
+    if column != 1:
+        _rows(logits, "logits")
     return L.ns_route_inputs(
-        logits.data_ptr(), max(logits.stride(0), E) if N == 1 else logits.stride(0),
+        logits.data_ptr(), row if N > 1 else max(row, E),
         _optional(doc, "doc", torch.int32, (N,), logits.device), N, E, int(k), code,
         1 if normalize else 0)
 
@@ -315,17 +327,21 @@ def _route(logits, k, doc, normalize) -> Routing:
     if not isinstance(k, int) or k < 1:
         _refuse(f"k: {k!r}, expected a positive integer")
     inputs = _route_inputs(logits, k, doc, normalize)
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return _route(logits, k, doc, normalize)
     N, E = logits.shape
-    dev = logits.device
-    with _On(dev) as stream:
-        ids = torch.empty((N, k), dtype=torch.int32, device=dev)
-        weights = torch.empty((N, k), dtype=torch.float32, device=dev)
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
-        tokens = torch.empty((), dtype=torch.int32, device=dev)
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        work = torch.empty(L.ns_route_workspace(N, E) // 4, dtype=torch.int32, device=dev)
-        L.ns_route_forward(inputs, ids.data_ptr(), weights.data_ptr(), counts.data_ptr(),
-                           tokens.data_ptr(), loss.data_ptr(), work.data_ptr(), stream)
+    device = logits.device
+    ids = torch.empty((N, k), dtype=torch.int32, device=device)
+    weights = torch.empty((N, k), dtype=torch.float32, device=device)
+    counts = torch.empty(E, dtype=torch.int32, device=device)
+    tokens = torch.empty((), dtype=torch.int32, device=device)
+    loss = torch.empty((), dtype=torch.float32, device=device)
+    size = L.ns_route_workspace(N, E)
+    work = torch.empty(size // 4, dtype=torch.int32, device=device) if size else None
+    L.ns_route_forward(inputs, ids.data_ptr(), weights.data_ptr(), counts.data_ptr(),
+                       tokens.data_ptr(), loss.data_ptr(), work.data_ptr() if size else None,
+                       _stream(device.index))
     return Routing(ids, weights, counts, tokens, loss)
 
 
@@ -342,9 +358,12 @@ def route_backward(logits: torch.Tensor, routing: Routing, d_weights: Optional[t
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         _refuse("routing.ids: expected [N, k]")
     inputs = _route_inputs(logits, ids.shape[1], doc, normalize)
+    if _elsewhere(logits):
+        with torch.cuda.device(dev):
+            return route_backward(logits, routing, d_weights, d_loss, doc=doc, normalize=normalize)
     N, E = logits.shape
-    shape = (N, ids.shape[1])
-    pointers = [_optional(ids, "routing.ids", torch.int32, shape, dev),
+    shape = ids.shape
+    pointers = [_optional(ids, "routing.ids", torch.int32, (N, shape[1]), dev),
                 _optional(weights, "routing.weights", torch.float32, shape, dev),
                 _optional(counts, "routing.counts", torch.int32, (E,), dev),
                 _optional(tokens, "routing.tokens", torch.int32, (), dev),
@@ -353,10 +372,9 @@ def route_backward(logits: torch.Tensor, routing: Routing, d_weights: Optional[t
         _need(d_loss, "d_loss", torch.float32, dev)
         if d_loss.numel() != 1:
             _refuse(f"d_loss: shape {tuple(d_loss.shape)}, expected one element")
-    with _On(dev) as stream:
-        dlogits = torch.empty((N, E), dtype=logits.dtype, device=dev)
-        L.ns_route_backward(inputs, *pointers, None if d_loss is None else d_loss.data_ptr(),
-                            dlogits.data_ptr(), stream)
+    dlogits = torch.empty((N, E), dtype=logits.dtype, device=dev)
+    L.ns_route_backward(inputs, *pointers, None if d_loss is None else d_loss.data_ptr(),
+                        dlogits.data_ptr(), _stream(dev.index))
     return dlogits
 
 

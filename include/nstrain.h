@@ -164,10 +164,10 @@ typedef struct {
   int32_t normalize;
 } ns_route_inputs;
 
-/* Bytes of the workspace of ns_route_forward for these sizes. */
+/* Bytes of the workspace of ns_route_forward for these sizes (0: none). */
 uint64_t ns_route_workspace(uint32_t N, uint32_t E);
 
-/* workspace: ns_route_workspace bytes, 4-byte aligned.  Errors: INVALID_ARG (a
+/* workspace: ns_route_workspace bytes, 4-byte aligned, or NULL for none.  Errors: INVALID_ARG (a
  * needed pointer NULL or misaligned, an unknown type, sizes out of range), CUDA. */
 int ns_route_forward(const ns_route_inputs *in, int32_t *ids, float *weights, int32_t *counts,
                      int32_t *tokens, float *loss, void *workspace, void *cuda_stream);

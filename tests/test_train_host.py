@@ -101,7 +101,7 @@ def route(nsp, back=False, **kw):
     dict(logits=None), dict(logits=AT + 2), dict(logits_row=15), dict(doc=AT + 1), dict(E=0),
     dict(E=1025, logits_row=1025), dict(k=0), dict(k=17), dict(E=64, logits_row=64, k=33),
     dict(dtype=4), dict(N=1 << 30), dict(ids=None), dict(ids=AT + 1), dict(weights=None),
-    dict(counts=None), dict(tokens=AT + 2), dict(loss=None), dict(workspace=None),
+    dict(counts=None), dict(tokens=AT + 2), dict(loss=None), dict(workspace=None, N=4096), dict(workspace=AT + 2),
     dict(back=True, ids=None), dict(back=True, weights=AT + 1), dict(back=True, counts=None),
     dict(back=True, tokens=None), dict(back=True, d_weights=AT + 2), dict(back=True, d_loss=AT + 1),
     dict(back=True, dlogits=None), dict(back=True, dlogits=AT + 2)])
@@ -126,5 +126,5 @@ def test_workspaces(nsp):
     assert nsp.ns_scan_workspace(0, 5, 10) == 0
     assert nsp.ns_scan_workspace(1, 32, 64) == 64 * 4
     assert nsp.ns_scan_workspace(1, 10_000, 64) == 8 * 64 * 4  # eight blocks share the row
-    assert nsp.ns_route_workspace(0, 16) >= 4
+    assert nsp.ns_route_workspace(0, 16) == 0 and nsp.ns_route_workspace(8, 16) == 0
     assert nsp.ns_route_workspace(1 << 20, 64) >= nsp.ns_route_workspace(64, 64)
