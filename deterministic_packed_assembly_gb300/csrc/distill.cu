@@ -6,12 +6,18 @@
 //
 // The gradient needs the row's softmax sum before its first element can be
 // written, and a row (256 KB for a vocabulary of 128K in 16 bits) is read from
-// memory once: a cluster of C blocks keeps the row in its shared memory, a
-// slice each, copied in with asynchronous 16-byte copies; every thread reduces
-// the chunks that it copied itself to a running maximum and sum, the blocks
-// exchange theirs through distributed shared memory, and each thread turns its
-// chunks into the gradient.  The K entries of the teacher, which are few, are
-// then written over what that put at their ids.
+// memory once: a cluster of C blocks keeps the row in its shared memory, a slice
+// each, copied in with asynchronous 16-byte copies; every thread reduces the chunks
+// that it copied itself to a running maximum and sum, the blocks exchange theirs
+// through distributed shared memory, and each thread turns its chunks into the
+// gradient.  The teacher's K entries are few: one warp of each block has them.  It
+// adds up the loss of those whose ids lie in its slice before the exchange, so that
+// one is enough:
+//   sum_k p_k (log p_k - log q_k) = sum over the slices r of
+//     part_r + pm_r (log S + (M - m_r) / temp),
+//   part_r = sum of p_k (log p_k - (s_k - m_r) / temp), pm_r = sum of p_k there,
+// with M, S the row's maximum and sum and m_r the slice's maximum (which keeps the
+// terms small).  After the gradient is written it writes the entries' own over it.
 //
 // Logits are kept as they came.  An exponential is 2^((s - max) log2 e / temp):
 // the difference is taken first, so that it is exact where it matters, near the
@@ -79,11 +85,15 @@ __device__ __forceinline__ float load_top(const void *top, int dtype, int64_t i)
 
 // The row's K entries in shared memory, one array each.
 struct Entries {
-  int *id;      // -1: absent
+  int *id;      // -1: absent, or (later) in another block's slice
   float *p;     // probability
   float *logp;  // its natural logarithm
-  float *x;     // the student's logit there, where this block holds it
+  float *x;     // the student's logit there
 };
+
+// What an entry's number is kept in, over a logit.
+template <class E>
+using Tag = typename std::conditional<sizeof(E) == 2, uint16_t, uint32_t>::type;
 
 // Warp 0: the teacher's probabilities; returns their sum m (1 unless the
 // teacher's own normaliser is given, 0 if no entry is left).
@@ -128,14 +138,13 @@ __device__ float teacher_entries(const DistillParams &p, uint32_t row, int lane,
 }
 
 template <class E, bool kGrad>
-__global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillParams p) {
   constexpr int kN = 16 / sizeof(E);  // elements of a chunk
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float2 stats[kMaxCluster];   // (maximum, sum) of every block's slice
-  __shared__ float losses[kMaxCluster];   // in block 0: every block's part of the loss
+  // every slice's maximum, sum, part_r and pm_r
+  __shared__ __align__(16) float4 stats[kMaxCluster];
   __shared__ float2 warp_stats[kMaxThreads / 32];
-  __shared__ float warp_loss[kMaxThreads / 32];
-  __shared__ float mass;
+  __shared__ float mass_of_row;
   const uint32_t rank = cluster_rank(), C = cluster_size();
   const uint32_t row = blockIdx.x / C;
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
@@ -145,53 +154,56 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillParam
   const int mis = (int)(((uintptr_t)src & 15) / sizeof(E));
   const uint32_t chunks = (uint32_t)(((uint64_t)mis + p.V + kN - 1) / kN);
   const uint32_t first = min(rank * p.slice, chunks), mine = min(p.slice, chunks - first);
-  const int64_t e0 = (int64_t)first * kN - mis;  // index of this slice's first element
+  const int e0 = (int)(first * kN) - mis;  // index of this slice's first element
+  // chunks [whole, whole + wholes) lie inside the row, at most one on either side does not
+  const uint32_t whole = e0 < 0 ? 1 : 0;
+  const uint32_t wholes =
+      mine - whole - (mine > whole && e0 + (int)mine * kN > (int)p.V ? 1 : 0);
   E *dst = kGrad ? static_cast<E *>(p.dlogits) + (int64_t)row * p.dlogits_row : nullptr;
   // whole chunks of the gradient can be stored at once
   const bool wide = kGrad && ((uintptr_t)(dst - mis) & 15) == 0;
-  auto store_chunk = [&](uint32_t c, const Vec<E, kN> &v) {
-    const int64_t i = e0 + (int64_t)c * kN;
-    if (wide && i >= 0 && i + kN <= (int64_t)p.V) {
-      *reinterpret_cast<Vec<E, kN> *>(dst + i) = v;
+  auto store_chunk = [&](uint32_t c, uint4 v) {
+    E *to = dst + e0 + (int)(c * kN);
+    if (wide && c - whole < wholes) {
+      *reinterpret_cast<uint4 *>(to) = v;
     } else {
+      E x[kN];
+      *reinterpret_cast<uint4 *>(x) = v;
 #pragma unroll
-      for (int k = 0; k < kN; ++k)
-        if (i + k >= 0 && i + k < (int64_t)p.V) dst[i + k] = v.v[k];
+      for (int k = 0; k < kN; ++k) {
+        const int i = e0 + (int)(c * kN) + k;
+        if (i >= 0 && i < (int)p.V) to[k] = x[k];
+      }
     }
   };
 
   if (p.mask && p.mask[row] == 0) {  // the same for every block of the cluster
-    if (kGrad) {
-      Vec<E, kN> zero;
-#pragma unroll
-      for (int k = 0; k < kN; ++k) zero.v[k] = from_f32<E>(0.0f);
-      for (uint32_t c = tid; c < mine; c += nthr) store_chunk(c, zero);
-    }
+    if (kGrad)
+      for (uint32_t c = tid; c < mine; c += nthr) store_chunk(c, make_uint4(0, 0, 0, 0));
     if (rank == 0 && tid == 0) p.loss[row] = 0.0f;
     return;
   }
-  cluster_arrive();  // waited for before the first write to another block
+  cluster_arrive_relaxed();  // waited for before the first write to another block
 
   // Copies of this thread's chunks, in kGroups groups.
-  E *slice = reinterpret_cast<E *>(smem);
+  uint4 *slice = reinterpret_cast<uint4 *>(smem);
   const uint32_t per = (mine + nthr - 1) / nthr;  // chunks of a thread
-  uint32_t j = 0;
+  uint32_t c = tid;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    const uint32_t end = (per * (g + 1) + kGroups - 1) / kGroups;
-    for (; j < end; ++j) {
-      const uint32_t c = j * nthr + tid;
-      if (c < mine) {
-        const int64_t i = e0 + (int64_t)c * kN;
-        if (i >= 0 && i + kN <= (int64_t)p.V) {
-          copy_async<16>(slice + (size_t)c * kN, src + i);
-        } else {  // the row's ends
+    const uint32_t end = min((per * (g + 1) + kGroups - 1) / kGroups * nthr, mine);
+    for (; c < end; c += nthr) {
+      const E *from = src + e0 + (int)(c * kN);
+      if (c - whole < wholes) {
+        copy_async<16>(slice + c, from);
+      } else {  // the row's ends
+        E x[kN];
 #pragma unroll
-          for (int k = 0; k < kN; ++k)
-            slice[(size_t)c * kN + k] = i + k >= 0 && i + k < (int64_t)p.V
-                                            ? src[i + k]
-                                            : from_f32<E>(kNegInf);
+        for (int k = 0; k < kN; ++k) {
+          const int i = e0 + (int)(c * kN) + k;
+          x[k] = i >= 0 && i < (int)p.V ? from[k] : from_f32<E>(kNegInf);
         }
+        slice[c] = *reinterpret_cast<const uint4 *>(x);
       }
     }
     copy_commit();
@@ -204,33 +216,37 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillParam
   e.id = reinterpret_cast<int *>(e.x + p.K);
   if (warp == 0) {
     const float m = teacher_entries(p, row, lane, e);
-    if (lane == 0) mass = m;
+    if (lane == 0) mass_of_row = m;
   }
 
   // Maximum and sum of this thread's chunks, as they arrive.
   MaxSum acc = {kNegInf, 0.0f};
-  j = 0;
+  const Ch<2> scale = splat<2>(p.scale);
+  c = tid;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    const uint32_t end = (per * (g + 1) + kGroups - 1) / kGroups;
+    const uint32_t end = min((per * (g + 1) + kGroups - 1) / kGroups * nthr, mine);
     copy_wait_left(kGroups - 1 - g);
-    for (; j < end; ++j) {
-      const uint32_t c = j * nthr + tid;
-      if (c < mine) {
-        const Vec<E, kN> v = *reinterpret_cast<const Vec<E, kN> *>(slice + (size_t)c * kN);
-        float x[kN], top = to_f32(v.v[0]);
+#pragma unroll 2
+    for (; c < end; c += nthr) {
+      Ch<2> x[kN / 2];
+      widen_chunk<E>(slice[c], x);
+      float top = fmaxf(x[0].v[0], x[0].v[1]);
 #pragma unroll
-        for (int k = 0; k < kN; ++k) x[k] = to_f32(v.v[k]);
-#pragma unroll
-        for (int k = 1; k < kN; ++k) top = fmaxf(top, x[k]);
-        if (top > acc.m) {
-          acc.s *= exp2_sfu((acc.m - top) * p.scale);
-          acc.m = top;
-        }
-        const float base = base_of(acc.m);
-#pragma unroll
-        for (int k = 0; k < kN; ++k) acc.s += exp2_sfu((x[k] - base) * p.scale);
+      for (int k = 1; k < kN / 2; ++k) top = fmaxf(top, fmaxf(x[k].v[0], x[k].v[1]));
+      if (top > acc.m) {
+        acc.s *= exp2_sfu((acc.m - top) * p.scale);
+        acc.m = top;
       }
+      const Ch<2> base = splat<2>(-base_of(acc.m));
+      Ch<2> sum;
+#pragma unroll
+      for (int k = 0; k < kN / 2; ++k) {
+        const Ch<2> y = (x[k] + base) * scale;
+        const Ch<2> v = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+        sum = k == 0 ? v : sum + v;
+      }
+      acc.s += sum.v[0] + sum.v[1];
     }
   }
 #pragma unroll
@@ -240,88 +256,107 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillParam
     acc = join(acc, other, p.scale);
   }
   if (lane == 0) warp_stats[warp] = make_float2(acc.m, acc.s);
-  __syncthreads();  // also: the slice and the entries are in shared memory
-  cluster_wait();   // every block of the cluster has started
-  if (tid < (int)C) {
-    acc = {warp_stats[0].x, warp_stats[0].y};
-    for (int w = 1; w < nthr / 32; ++w)
-      acc = join(acc, {warp_stats[w].x, warp_stats[w].y}, p.scale);
-    remote_store(remote_smem(&stats[rank], tid), make_float2(acc.m, acc.s));
+  __syncthreads();  // also: the slice is in shared memory
+  if (warp == 0) {
+    acc = {kNegInf, 0.0f};
+    if (lane < nthr / 32) acc = {warp_stats[lane].x, warp_stats[lane].y};
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const MaxSum other = {__shfl_xor_sync(0xffffffffu, acc.m, o),
+                            __shfl_xor_sync(0xffffffffu, acc.s, o)};
+      acc = join(acc, other, p.scale);
+    }
+    // lanes 16 and up joined nothing: lane 0 has the slice's
+    acc = {__shfl_sync(0xffffffffu, acc.m, 0), __shfl_sync(0xffffffffu, acc.s, 0)};
+    const float base = base_of(acc.m);
+    float part = 0.0f, pm = 0.0f;
+    for (uint32_t k = lane; k < p.K; k += 32) {
+      const int at = e.id[k] - e0;
+      if (e.id[k] >= 0 && at >= 0 && at < (int)(mine * kN)) {
+        const float x = to_f32(reinterpret_cast<const E *>(slice)[at]), pk = e.p[k];
+        e.x[k] = x;
+        if (pk != 0.0f) {
+          part += pk * (x == kNegInf ? -kNegInf : fmaf(base - x, p.inv_temp, e.logp[k]));
+          pm += pk;
+        }
+      } else {
+        e.id[k] = -1;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      part += __shfl_xor_sync(0xffffffffu, part, o);
+      pm += __shfl_xor_sync(0xffffffffu, pm, o);
+    }
+    if (kGrad) {
+      // Of entries with the same id, one writes the sum of their p: the one whose
+      // number is left in the slice at that id.  (What the gradient's loop makes of
+      // the numbers is written over.)
+      __syncwarp();
+      for (uint32_t k = lane; k < p.K; k += 32)
+        if (e.id[k] >= 0) reinterpret_cast<Tag<E> *>(slice)[e.id[k] - e0] = (Tag<E>)k;
+    }
+    cluster_wait();  // every block of the cluster has started
+    if (lane < (int)C)
+      remote_store(remote_smem(&stats[rank], lane), make_float4(acc.m, acc.s, part, pm));
+  } else {
+    cluster_wait();
   }
   cluster_arrive();
   cluster_wait();
   acc = {stats[0].x, stats[0].y};
   for (uint32_t r = 1; r < C; ++r) acc = join(acc, {stats[r].x, stats[r].y}, p.scale);
-  const float base = base_of(acc.m), m = mass;
-  const float log_s = logf(acc.s);
-
-  // The entries whose ids lie in this slice: their student logits, and their
-  // part of the loss.
-  float part = 0.0f;
-  for (uint32_t k = tid; k < p.K; k += nthr) {
-    const int64_t at = (int64_t)e.id[k] - e0;
-    if (e.id[k] >= 0 && at >= 0 && at < (int64_t)mine * kN) {
-      const float x = to_f32(slice[at]), pk = e.p[k];
-      e.x[k] = x;
-      const float log_q = x == kNegInf ? kNegInf : fmaf(x - base, p.inv_temp, -log_s);
-      if (pk != 0.0f) part += pk * (e.logp[k] - log_q);
-    } else {
-      e.id[k] = -1;  // another block's, or absent
+  const float mass = mass_of_row;
+  if (rank == 0 && tid == 0) {
+    const float log_s = logf(acc.s);
+    float loss = 0.0f;
+    for (uint32_t r = 0; r < C; ++r) {
+      const float4 v = stats[r];
+      if (v.w != 0.0f)
+        loss += v.z + v.w * fmaf(base_of(acc.m) - base_of(v.x), p.inv_temp, log_s);
     }
+    // a student without any logit above -inf gives the teacher's entries probability 0
+    if (acc.s == 0.0f) loss = mass == 0.0f ? 0.0f : -kNegInf;
+    p.loss[row] = loss * p.temp * p.temp;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  if (lane == 0) warp_loss[warp] = part;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < nthr / 32; ++w) part += warp_loss[w];
-    remote_store(remote_smem(&losses[rank], 0), part);
-  }
-  cluster_arrive();
+  if (!kGrad) return;
 
-  if (kGrad) {
-    const float w = (p.weight ? p.weight[row] : 1.0f) * p.temp;
-    const float f = m == 0.0f || acc.s == 0.0f ? 0.0f : w * m / acc.s;  // of the exponentials
-    const bool none = m == 0.0f;
-    for (uint32_t c = tid; c < mine; c += nthr) {
-      const Vec<E, kN> v = *reinterpret_cast<const Vec<E, kN> *>(slice + (size_t)c * kN);
-      Vec<E, kN> out;
+  const float w = (p.weight ? p.weight[row] : 1.0f) * p.temp;
+  const float f = acc.s == 0.0f ? 0.0f : w * mass / acc.s;  // of the exponentials
+  const Ch<2> base = splat<2>(-base_of(acc.m)), by = splat<2>(f);
+  if (mass == 0.0f) {  // no entry: nothing to learn, whatever the logits are
+    for (uint32_t i = tid; i < mine; i += nthr) store_chunk(i, make_uint4(0, 0, 0, 0));
+    return;
+  }
+#pragma unroll 2
+  for (uint32_t i = tid; i < mine; i += nthr) {
+    Ch<2> x[kN / 2];
+    widen_chunk<E>(slice[i], x);
 #pragma unroll
-      for (int k = 0; k < kN; ++k) {
-        const float g = f * exp2_sfu((to_f32(v.v[k]) - base) * p.scale);
-        out.v[k] = from_f32<E>(none ? 0.0f : g);
-      }
-      store_chunk(c, out);
+    for (int k = 0; k < kN / 2; ++k) {
+      const Ch<2> y = (x[k] + base) * scale;
+      x[k] = by * Ch<2>{exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
     }
-    __syncthreads();  // the slice is read, the gradient is written
-    // Of entries with the same id, one writes the sum of their p: the one
-    // whose number is left in the slice at that id.
-    using Tag = typename std::conditional<sizeof(E) == 2, uint16_t, uint32_t>::type;
-    Tag *tags = reinterpret_cast<Tag *>(smem);
-    for (uint32_t k = tid; k < p.K; k += nthr)
-      if (e.id[k] >= 0) tags[e.id[k] - e0] = (Tag)k;
-    __syncthreads();
+    store_chunk(i, narrow_chunk<E>(x));
+  }
+  __syncthreads();  // the gradient is written
+  if (warp == 0) {
+    const Tag<E> *tags = reinterpret_cast<const Tag<E> *>(slice);
     bool twice = false;
-    for (uint32_t k = tid; k < p.K; k += nthr)
-      if (e.id[k] >= 0 && tags[e.id[k] - e0] != (Tag)k) twice = true;
-    twice = __syncthreads_or(twice);
-    for (uint32_t k = tid; k < p.K; k += nthr) {
-      if (e.id[k] < 0 || tags[e.id[k] - e0] != (Tag)k) continue;
+    for (uint32_t k = lane; k < p.K; k += 32)
+      if (e.id[k] >= 0 && tags[e.id[k] - e0] != (Tag<E>)k) twice = true;
+    twice = __any_sync(0xffffffffu, twice);
+    for (uint32_t k = lane; k < p.K; k += 32) {
+      if (e.id[k] < 0 || tags[e.id[k] - e0] != (Tag<E>)k) continue;
       float pk = e.p[k];
       if (twice) {  // in the entries' order
         pk = 0.0f;
         for (uint32_t i = 0; i < p.K; ++i)
           if (e.id[i] == e.id[k]) pk += e.p[i];
       }
-      const float g = f * exp2_sfu((e.x[k] - base) * p.scale);
-      dst[e.id[k]] = from_f32<E>(none ? 0.0f : fmaf(-w, pk, g));
+      const float g = f * exp2_sfu((e.x[k] - base_of(acc.m)) * p.scale);
+      dst[e.id[k]] = from_f32<E>(fmaf(-w, pk, g));
     }
-  }
-  cluster_wait();  // every block's part of the loss is in block 0
-  if (rank == 0 && tid == 0) {
-    float loss = losses[0];
-    for (uint32_t r = 1; r < C; ++r) loss += losses[r];
-    p.loss[row] = loss * p.temp * p.temp;
   }
 }
 

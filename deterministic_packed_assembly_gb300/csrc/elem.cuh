@@ -131,6 +131,27 @@ __device__ __forceinline__ uint32_t narrow_pair(Ch<2> x) {
   }
 }
 
+// 16 bytes of elements as pairs of floats, and back.
+template <class E>
+__device__ __forceinline__ void widen_chunk(uint4 v, Ch<2> (&x)[8 / sizeof(E)]) {
+  if constexpr (sizeof(E) == 4) {
+    x[0] = {__uint_as_float(v.x), __uint_as_float(v.y)};
+    x[1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
+  } else {
+    x[0] = widen_pair<E>(v.x), x[1] = widen_pair<E>(v.y);
+    x[2] = widen_pair<E>(v.z), x[3] = widen_pair<E>(v.w);
+  }
+}
+template <class E>
+__device__ __forceinline__ uint4 narrow_chunk(const Ch<2> (&x)[8 / sizeof(E)]) {
+  if constexpr (sizeof(E) == 4)
+    return make_uint4(__float_as_uint(x[0].v[0]), __float_as_uint(x[0].v[1]),
+                      __float_as_uint(x[1].v[0]), __float_as_uint(x[1].v[1]));
+  else
+    return make_uint4(narrow_pair<E>(x[0]), narrow_pair<E>(x[1]), narrow_pair<E>(x[2]),
+                      narrow_pair<E>(x[3]));
+}
+
 // ---- thread-block clusters --------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -150,6 +171,10 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
+// As cluster_arrive, with nothing to be seen: only that this thread got here.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
 // The address, in block `rank` of the cluster, of this block's shared `p`.
 __device__ __forceinline__ uint32_t remote_smem(const void *p, uint32_t rank) {
   uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
@@ -158,6 +183,11 @@ __device__ __forceinline__ uint32_t remote_smem(const void *p, uint32_t rank) {
 }
 __device__ __forceinline__ void remote_store(uint32_t addr, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y)
+               : "memory");
+}
+__device__ __forceinline__ void remote_store(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
+               "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
 }
 __device__ __forceinline__ void remote_store(uint32_t addr, float v) {
