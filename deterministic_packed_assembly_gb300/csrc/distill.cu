@@ -7,17 +7,19 @@
 // The gradient needs the row's softmax sum before its first element can be
 // written, and a row (256 KB for a vocabulary of 128K in 16 bits) is read from
 // memory once: a cluster of C blocks keeps the row in its shared memory, a slice
-// each, copied in with asynchronous 16-byte copies; every thread reduces the chunks
-// that it copied itself to a running maximum and sum, the blocks exchange theirs
-// through distributed shared memory, and each thread turns its chunks into the
-// gradient.  The teacher's K entries are few: one warp of each block has them.  It
-// adds up the loss of those whose ids lie in its slice before the exchange, so that
-// one is enough:
-//   sum_k p_k (log p_k - log q_k) = sum over the slices r of
-//     part_r + pm_r (log S + (M - m_r) / temp),
-//   part_r = sum of p_k (log p_k - (s_k - m_r) / temp), pm_r = sum of p_k there,
-// with M, S the row's maximum and sum and m_r the slice's maximum (which keeps the
-// terms small).  After the gradient is written it writes the entries' own over it.
+// each.  A thread has its own 16-byte chunks of the slice: it copies them in
+// asynchronously, reduces them to a running maximum and sum as they arrive, and,
+// once the blocks have exchanged theirs, turns each into the gradient and starts
+// the copy of the cluster's next row into its place.  So the copies of a row run
+// beside the stores of the one before.  The teacher's K entries are few: a warp of
+// their own in each block has them, a row ahead.  With c the student's logit at the
+// teacher's first choice, M and S the row's maximum and sum,
+//   sum_k p_k (log p_k - log q_k) = sum_k p_k (log p_k - (s_k - c) / temp)
+//                                   + m (log S + (M - c) / temp),
+// whose first sum each block takes over the ids in its slice, without the row's
+// statistics, so that one exchange is enough; its terms are small, as the
+// teacher's choices are near c.  After the gradient is written the warp writes the
+// entries' own over it.
 //
 // Logits are kept as they came.  An exponential is 2^((s - max) log2 e / temp):
 // the difference is taken first, so that it is exact where it matters, near the
@@ -35,7 +37,7 @@
 namespace nsk {
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 288;  // eight warps for the row, one for the entries
 constexpr int kMaxCluster = 8;
 constexpr int kGroups = 4;  // of asynchronous copies, waited for in order
 
@@ -51,6 +53,7 @@ struct DistillParams {
   int32_t top_dtype, ids_64;
   float temp, inv_temp, scale;  // scale = log2 e / temp
   uint32_t slice;               // 16-byte chunks of a block's slice
+  uint32_t slots;               // of the dictionary of its entries
   float *loss;
   void *dlogits;
   int64_t dlogits_row;
@@ -91,27 +94,91 @@ struct Entries {
   float *x;     // the student's logit there
 };
 
-// What an entry's number is kept in, over a logit.
+// A row of logits: `head` elements, then whole chunks of 16 bytes from a 16-byte
+// boundary on, then the rest, which is shorter than a chunk.  This block's slice is
+// `mine` of the chunks; the first one starts at element `from`.  The elements at
+// both ends are the first block's entry warp's, one or none a lane.
 template <class E>
-using Tag = typename std::conditional<sizeof(E) == 2, uint16_t, uint32_t>::type;
+struct RowSlice {
+  static constexpr int kN = 16 / sizeof(E);  // elements of a chunk
+  int head, tail;  // the tail's first element
+  int from;
+  uint32_t mine;
+  __device__ __forceinline__ RowSlice(const DistillParams &p, uint32_t row, uint32_t rank) {
+    const uintptr_t at = (uintptr_t)(static_cast<const E *>(p.logits) + (int64_t)row * p.logits_row);
+    head = min((int)(((16 - (at & 15)) & 15) / sizeof(E)), (int)p.V);
+    const uint32_t chunks = (p.V - head) / kN;
+    const uint32_t first = min(rank * p.slice, chunks);
+    mine = min(p.slice, chunks - first);
+    from = head + (int)(first * kN);
+    tail = head + (int)(chunks * kN);
+  }
+  // The element at the row's ends that a lane of the entry warp has, -1 for none.
+  __device__ __forceinline__ int end_of(const DistillParams &p, uint32_t rank, int lane) const {
+    const int i = lane < kN ? lane : tail + lane - kN;
+    return rank == 0 && (lane < kN ? i < head : lane < 2 * kN && i < (int)p.V) ? i : -1;
+  }
+};
 
-// Warp 0: the teacher's probabilities; returns their sum m (1 unless the
-// teacher's own normaliser is given, 0 if no entry is left).
-__device__ float teacher_entries(const DistillParams &p, uint32_t row, int lane,
-                                 const Entries &e) {
+// The entries' warp: the teacher's probabilities and the student's logits at the
+// entries of this block's slice [from, to).
+struct EntrySums {
+  float mass;  // sum of p over the row: 1 unless the teacher's own normaliser is given
+  float c;     // the student's logit at the teacher's first choice
+  float part;  // sum of p (log p - (s - c) / temp) over the slice
+};
+template <class E>
+__device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uint32_t row,
+                                                     const E *logits, const RowSlice<E> &s,
+                                                     uint32_t rank, int lane, const Entries &e) {
+  // an id is this block's: in its chunks, or at the row's ends for the first block
+  const int last = s.from + (int)s.mine * (16 / (int)sizeof(E));
+  auto ours = [&](int id) {
+    return (id >= s.from && id < last) || (rank == 0 && id >= 0 && (id < s.head || id >= s.tail));
+  };
   const int64_t base = (int64_t)row * p.K;
   float m = kNegInf;
-  for (uint32_t k = lane; k < p.K; k += 32) {
-    const int64_t id = p.ids_64 ? static_cast<const int64_t *>(p.ids)[base + k]
-                                : (int64_t)static_cast<const int32_t *>(p.ids)[base + k];
-    const float t = load_top(p.top, p.top_dtype, base + k);
-    const bool in = id >= 0 && id < (int64_t)p.V;
-    e.id[k] = in ? (int)id : -1;
-    e.logp[k] = in ? t : kNegInf;
-    if (in) m = fmaxf(m, t);
+  uint32_t top = 0xffffffffu;  // the first entry of the largest logit, and its id
+  int top_id = 0;
+  constexpr int kBatch = 4;  // loads in flight
+  for (uint32_t k0 = lane; k0 < p.K; k0 += 32 * kBatch) {
+    int id[kBatch];
+    float t[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint32_t k = k0 + 32 * i;
+      id[i] = -1;
+      if (k < p.K) {
+        const int64_t v = p.ids_64 ? static_cast<const int64_t *>(p.ids)[base + k]
+                                   : (int64_t)static_cast<const int32_t *>(p.ids)[base + k];
+        if (v >= 0 && v < (int64_t)p.V) id[i] = (int)v;
+        t[i] = load_top(p.top, p.top_dtype, base + k);
+      }
+    }
+    float x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (ours(id[i])) x[i] = to_f32(logits[id[i]]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint32_t k = k0 + 32 * i;
+      if (k >= p.K) continue;
+      e.id[k] = id[i];
+      e.logp[k] = id[i] >= 0 ? t[i] : kNegInf;
+      if (id[i] >= 0 && t[i] > m) m = t[i], top = k, top_id = id[i];
+      if (ours(id[i])) e.x[k] = x[i];
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o);
+    const uint32_t ok = __shfl_xor_sync(0xffffffffu, top, o);
+    const int oi = __shfl_xor_sync(0xffffffffu, top_id, o);
+    if (om > m || (om == m && ok < top)) m = om, top = ok, top_id = oi;
+  }
+  EntrySums r = {0.0f, 0.0f, 0.0f};
+  if (top != 0xffffffffu) r.c = to_f32(logits[top_id]);
+  if (r.c == kNegInf) r.c = 0.0f;
   const float base_m = base_of(m);
   const float lse = p.teacher_lse ? p.teacher_lse[row] : 0.0f;
   float sum = 0.0f;
@@ -127,264 +194,434 @@ __device__ float teacher_entries(const DistillParams &p, uint32_t row, int lane,
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (p.teacher_lse) return sum;
-  if (sum == 0.0f) return 0.0f;
-  const float inv = 1.0f / sum, log_sum = logf(sum);
+  float inv = 1.0f, log_sum = 0.0f;
+  r.mass = sum;
+  if (!p.teacher_lse && sum != 0.0f) inv = 1.0f / sum, log_sum = logf(sum), r.mass = 1.0f;
   for (uint32_t k = lane; k < p.K; k += 32) {
-    e.p[k] *= inv;
-    e.logp[k] -= log_sum;
+    const int id = e.id[k];
+    if (!ours(id)) {
+      e.id[k] = -1;  // absent, or another block's
+      continue;
+    }
+    const float pk = e.p[k] * inv, x = e.x[k];
+    e.p[k] = pk;
+    if (pk != 0.0f)
+      r.part += pk * (x == kNegInf ? -kNegInf : fmaf(r.c - x, p.inv_temp, e.logp[k] - log_sum));
   }
-  return 1.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.part += __shfl_xor_sync(0xffffffffu, r.part, o);
+  return r;
+}
+
+// A slot of the dictionary of a slice's entries: an id and its first entry.
+struct Slot {
+  int id, first;
+};
+__device__ __forceinline__ uint32_t slot_of(int id, uint32_t slots) {
+  return ((uint32_t)id * 2654435761u >> 12) & (slots - 1);  // Knuth's multiplicative hash
+}
+
+// Of a slice's entries with the same id the first one is to write the gradient, of
+// the sum of their p (in the entries' order); the others' ids become -1.  `slots`
+// is a power of two, at least twice the entries.
+__device__ void join_repeated(uint32_t K, uint32_t slots, int lane, const Entries &e,
+                              Slot *dictionary) {
+  for (uint32_t i = lane; i < slots; i += 32) dictionary[i] = {-1, (int)K};
+  __syncwarp();
+  bool twice = false;
+  for (uint32_t k = lane; k < K; k += 32) {
+    const int id = e.id[k];
+    if (id < 0) continue;
+    for (uint32_t h = slot_of(id, slots), tries = 0; tries < slots; ++tries) {
+      const int was = atomicCAS(&dictionary[h].id, -1, id);
+      if (was == -1 || was == id) {
+        twice = twice || was == id;
+        atomicMin(&dictionary[h].first, (int)k);
+        break;
+      }
+      h = (h + 1) & (slots - 1);
+    }
+  }
+  if (!__any_sync(0xffffffffu, twice)) return;
+  for (uint32_t k = lane; k < K; k += 32) {
+    const int id = e.id[k];
+    if (id < 0) continue;
+    uint32_t h = slot_of(id, slots);
+    for (uint32_t tries = 0; tries < slots && dictionary[h].id != id; ++tries)
+      h = (h + 1) & (slots - 1);
+    float sum = -1.0f;  // no sum of probabilities: not the first
+    if (dictionary[h].first == (int)k) {
+      sum = 0.0f;
+      for (uint32_t i = k; i < K; ++i)
+        if (e.id[i] == id) sum += e.p[i];
+    }
+    e.logp[k] = sum;  // the loss is done with the logarithms
+  }
+  __syncwarp();
+  for (uint32_t k = lane; k < K; k += 32) {
+    if (e.logp[k] == -1.0f) e.id[k] = -1;
+    else e.p[k] = e.logp[k];
+  }
+}
+
+// Gradients whose chunks do not lie on 16-byte boundaries.
+template <class E>
+__device__ __noinline__ void store_apart(E *to, uint4 v) {
+  E x[16 / sizeof(E)];
+  *reinterpret_cast<uint4 *>(x) = v;
+#pragma unroll
+  for (int k = 0; k < (int)(16 / sizeof(E)); ++k) to[k] = x[k];
+}
+template <class E>
+__device__ __forceinline__ void store_chunk(E *to, bool wide, uint4 v) {
+  if (wide) *reinterpret_cast<uint4 *>(to) = v;
+  else store_apart<E>(to, v);
+}
+
+// The cluster's rows: its number, and every `stride`-th one from there.  `mask` is
+// read for 32 of them at once, a lane each.
+struct RowWalk {
+  uint32_t next, stride, bits, left;  // bits of the `left` rows from `next` on
+  __device__ __forceinline__ RowWalk(uint32_t first, uint32_t s) : next(first), stride(s) {
+    bits = left = 0;
+  }
+  // The next learned row (N: there is none); `skipped` is called with each row before.
+  template <class F>
+  __device__ __forceinline__ uint32_t learned(const DistillParams &p, int lane, F skipped) {
+    while (next < p.N) {
+      if (left == 0) {
+        const uint64_t r = next + (uint64_t)lane * stride;
+        bits = __ballot_sync(0xffffffffu, r < p.N && (!p.mask || p.mask[r] != 0));
+        left = 32;
+      }
+      const uint32_t row = next;
+      const bool is = bits & 1u;
+      bits >>= 1, --left;
+      next = stride < p.N - next ? next + stride : p.N;
+      if (is) return row;
+      skipped(row);
+    }
+    return p.N;
+  }
+};
+
+struct Shared {
+  float4 stats[2][kMaxCluster];  // every slice's maximum, sum and part, of two rows
+  uint64_t arrived[2];           // mbarriers: the stats have
+  float2 warp_stats[kMaxThreads / 32];  // the entry warp's last: the row's ends
+  EntrySums sums[2];
+};
+
+// The row's maximum and sum from every slice's, and the loss's parts added up.
+__device__ __forceinline__ MaxSum row_stats(const DistillParams &p, Shared &sh, uint32_t round,
+                                            uint32_t C, bool &lost, float &parts) {
+  if (!lost && !barrier_wait(&sh.arrived[round & 1], round >> 1 & 1)) lost = true;
+  const float4 *v = sh.stats[round & 1];
+  MaxSum r = {v[0].x, v[0].y};
+  parts = v[0].z;
+  for (uint32_t i = 1; i < C; ++i) {
+    r = join(r, {v[i].x, v[i].y}, p.scale);
+    parts += v[i].z;
+  }
+  if (lost) r.s = parts = __int_as_float(0x7fffffff);  // shows in the loss and the gradient
+  return r;
+}
+__device__ __forceinline__ MaxSum warp_join(MaxSum a, float scale) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)},
+             scale);
+  return a;
+}
+
+// The entry warp of a block.
+template <class E, bool kGrad>
+__device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, float *arrays,
+                                        uint32_t rank, uint32_t C, uint32_t stride, int lane) {
+  const E *logits = static_cast<const E *>(p.logits);
+  auto entries = [&](uint32_t i) {  // of even and odd rounds
+    Entries e;
+    e.p = arrays + (i & 1) * 4 * p.K;
+    e.logp = e.p + p.K;
+    e.x = e.logp + p.K;
+    e.id = reinterpret_cast<int *>(e.x + p.K);
+    return e;
+  };
+  Slot *dictionary = reinterpret_cast<Slot *>(arrays + 8 * p.K);
+  float end = kNegInf, next_end = kNegInf;  // this lane's logit at the row's ends
+  auto prepare = [&](uint32_t row, uint32_t i) {
+    const RowSlice<E> s(p, row, rank);
+    const E *src = logits + (int64_t)row * p.logits_row;
+    const int at = s.end_of(p, rank, lane);
+    next_end = at >= 0 ? to_f32(src[at]) : kNegInf;
+    const Entries e = entries(i);
+    const EntrySums r = teacher_entries<E>(p, row, src, s, rank, lane, e);
+    if (lane == 0) sh.sums[i & 1] = r;
+    if (kGrad) join_repeated(p.K, p.slots, lane, e, dictionary);
+    __syncwarp();
+  };
+  auto nothing = [](uint32_t) {};
+  bool lost = false;
+  RowWalk walk(blockIdx.x / C, stride);
+  uint32_t row = walk.learned(p, lane, nothing);
+  if (row < p.N) prepare(row, 0);
+  for (uint32_t i = 0; row < p.N; ++i) {
+    const uint32_t next = walk.learned(p, lane, nothing);
+    const float weight = p.weight ? p.weight[row] : 1.0f;
+    end = next_end;
+    const MaxSum ends = warp_join({end, end == kNegInf ? 0.0f : end == end ? 1.0f : end}, p.scale);
+    if (lane == 0) sh.warp_stats[blockDim.x / 32 - 1] = make_float2(ends.m, ends.s);
+    __syncthreads();  // (1) the row's slice is reduced, its entries are here
+    if (next < p.N) prepare(next, i + 1);
+    float parts;
+    const MaxSum all = row_stats(p, sh, i, C, lost, parts);
+    const EntrySums sums = sh.sums[i & 1];
+    if (rank == 0 && lane == 0) {
+      float loss = parts + sums.mass * fmaf(base_of(all.m) - sums.c, p.inv_temp, logf(all.s));
+      // a student without any logit above -inf gives the teacher's entries probability 0
+      if (all.s == 0.0f) loss = -kNegInf;
+      p.loss[row] = sums.mass == 0.0f ? 0.0f : loss * p.temp * p.temp;
+    }
+    if (kGrad) {
+      const float w = weight * p.temp;
+      const float f = all.s == 0.0f ? 0.0f : w * sums.mass / all.s;
+      E *dst = static_cast<E *>(p.dlogits) + (int64_t)row * p.dlogits_row;
+      const int at = RowSlice<E>(p, row, rank).end_of(p, rank, lane);
+      if (at >= 0)
+        dst[at] = from_f32<E>(
+            sums.mass == 0.0f ? 0.0f : f * exp2_sfu((end - base_of(all.m)) * p.scale));
+      const Entries e = entries(i);
+      // (2) the row's gradient is written
+      asm volatile("bar.sync 1, %0;" ::"r"(blockDim.x) : "memory");
+      if (sums.mass != 0.0f)
+        for (uint32_t k = lane; k < p.K; k += 32)
+          if (e.id[k] >= 0) {
+            const float g = f * exp2_sfu((e.x[k] - base_of(all.m)) * p.scale);
+            dst[e.id[k]] = from_f32<E>(fmaf(-w, e.p[k], g));
+          }
+      __syncwarp();
+    }
+    row = next;
+  }
+}
+
+// An unlearned row: no loss, no gradient.
+template <class E, bool kGrad>
+__device__ __noinline__ void unlearned(const DistillParams &p, uint32_t row, uint32_t rank,
+                                       uint32_t nthr) {
+  if (kGrad) {
+    const RowSlice<E> s(p, row, rank);
+    E *dst = static_cast<E *>(p.dlogits) + (int64_t)row * p.dlogits_row, *to = dst + s.from;
+    const bool wide = ((uintptr_t)to & 15) == 0;
+    for (uint32_t c = threadIdx.x; c < s.mine; c += nthr)
+      store_chunk<E>(to + c * RowSlice<E>::kN, wide, make_uint4(0, 0, 0, 0));
+    if (threadIdx.x < 32) {
+      const int at = s.end_of(p, rank, threadIdx.x);
+      if (at >= 0) dst[at] = from_f32<E>(0.0f);
+    }
+  }
+  if (rank == 0 && threadIdx.x == 0) p.loss[row] = 0.0f;
 }
 
 template <class E, bool kGrad>
 __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillParams p) {
-  constexpr int kN = 16 / sizeof(E);  // elements of a chunk
+  constexpr int kN = 16 / sizeof(E);
   extern __shared__ __align__(16) unsigned char smem[];
-  // every slice's maximum, sum, part_r and pm_r
-  __shared__ __align__(16) float4 stats[kMaxCluster];
-  __shared__ float2 warp_stats[kMaxThreads / 32];
-  __shared__ float mass_of_row;
+  __shared__ __align__(16) Shared sh;
   const uint32_t rank = cluster_rank(), C = cluster_size();
-  const uint32_t row = blockIdx.x / C;
-  const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
-
-  // The row in chunks of 16 bytes from the boundary at or below its start.
-  const E *src = static_cast<const E *>(p.logits) + (int64_t)row * p.logits_row;
-  const int mis = (int)(((uintptr_t)src & 15) / sizeof(E));
-  const uint32_t chunks = (uint32_t)(((uint64_t)mis + p.V + kN - 1) / kN);
-  const uint32_t first = min(rank * p.slice, chunks), mine = min(p.slice, chunks - first);
-  const int e0 = (int)(first * kN) - mis;  // index of this slice's first element
-  // chunks [whole, whole + wholes) lie inside the row, at most one on either side does not
-  const uint32_t whole = e0 < 0 ? 1 : 0;
-  const uint32_t wholes =
-      mine - whole - (mine > whole && e0 + (int)mine * kN > (int)p.V ? 1 : 0);
-  E *dst = kGrad ? static_cast<E *>(p.dlogits) + (int64_t)row * p.dlogits_row : nullptr;
-  // whole chunks of the gradient can be stored at once
-  const bool wide = kGrad && ((uintptr_t)(dst - mis) & 15) == 0;
-  auto store_chunk = [&](uint32_t c, uint4 v) {
-    E *to = dst + e0 + (int)(c * kN);
-    if (wide && c - whole < wholes) {
-      *reinterpret_cast<uint4 *>(to) = v;
-    } else {
-      E x[kN];
-      *reinterpret_cast<uint4 *>(x) = v;
-#pragma unroll
-      for (int k = 0; k < kN; ++k) {
-        const int i = e0 + (int)(c * kN) + k;
-        if (i >= 0 && i < (int)p.V) to[k] = x[k];
-      }
-    }
-  };
-
-  if (p.mask && p.mask[row] == 0) {  // the same for every block of the cluster
-    if (kGrad)
-      for (uint32_t c = tid; c < mine; c += nthr) store_chunk(c, make_uint4(0, 0, 0, 0));
-    if (rank == 0 && tid == 0) p.loss[row] = 0.0f;
+  const uint32_t stride = gridDim.x / C;  // rows between two of a cluster
+  // the last warp has the entries, the others the rows
+  const uint32_t tid = threadIdx.x, nthr = blockDim.x - 32;
+  const int lane = tid & 31, warp = tid >> 5;
+  uint4 *slice = reinterpret_cast<uint4 *>(smem);
+  if (tid == 0) {
+    barrier_init(&sh.arrived[0]);
+    barrier_init(&sh.arrived[1]);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_arrive();  // the others' barriers are there before anything is sent
+  cluster_wait();
+  if (tid >= nthr) {
+    entry_warp<E, kGrad>(p, sh, reinterpret_cast<float *>(smem + (size_t)p.slice * 16), rank, C,
+                         stride, lane);
     return;
   }
-  cluster_arrive_relaxed();  // waited for before the first write to another block
 
-  // Copies of this thread's chunks, in kGroups groups.
-  uint4 *slice = reinterpret_cast<uint4 *>(smem);
-  const uint32_t per = (mine + nthr - 1) / nthr;  // chunks of a thread
-  uint32_t c = tid;
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const uint32_t end = min((per * (g + 1) + kGroups - 1) / kGroups * nthr, mine);
-    for (; c < end; c += nthr) {
-      const E *from = src + e0 + (int)(c * kN);
-      if (c - whole < wholes) {
-        copy_async<16>(slice + c, from);
-      } else {  // the row's ends
-        E x[kN];
-#pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const int i = e0 + (int)(c * kN) + k;
-          x[k] = i >= 0 && i < (int)p.V ? from[k] : from_f32<E>(kNegInf);
-        }
-        slice[c] = *reinterpret_cast<const uint4 *>(x);
-      }
-    }
-    copy_commit();
-  }
-
-  Entries e;
-  e.p = reinterpret_cast<float *>(smem + (size_t)p.slice * 16);
-  e.logp = e.p + p.K;
-  e.x = e.logp + p.K;
-  e.id = reinterpret_cast<int *>(e.x + p.K);
-  if (warp == 0) {
-    const float m = teacher_entries(p, row, lane, e);
-    if (lane == 0) mass_of_row = m;
-  }
-
-  // Maximum and sum of this thread's chunks, as they arrive.
-  MaxSum acc = {kNegInf, 0.0f};
+  const E *logits = static_cast<const E *>(p.logits);
+  E *dlogits = static_cast<E *>(p.dlogits);
   const Ch<2> scale = splat<2>(p.scale);
-  c = tid;
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const uint32_t end = min((per * (g + 1) + kGroups - 1) / kGroups * nthr, mine);
-    copy_wait_left(kGroups - 1 - g);
+  bool lost = false;
+  const uint32_t quarter = (p.slice + kGroups * nthr - 1) / (kGroups * nthr) * nthr;
+  auto skip = [&](uint32_t row) { unlearned<E, kGrad>(p, row, rank, nthr); };
+  RowWalk walk(blockIdx.x / C, stride);
+  uint32_t row = walk.learned(p, lane, skip);
+  if (row < p.N) {
+    const RowSlice<E> s(p, row, rank);
+    const E *from = logits + (int64_t)row * p.logits_row + s.from;
+    uint32_t c = tid;
+#pragma unroll 1
+    for (uint32_t end = quarter; end <= kGroups * quarter; end += quarter) {
+      for (; c < min(end, s.mine); c += nthr) copy_async<16>(slice + c, from + c * kN);
+      copy_commit();
+    }
+  }
+  for (uint32_t i = 0; row < p.N; ++i) {
+    const uint32_t next = walk.learned(p, lane, skip);
+    const float weight = kGrad && p.weight ? p.weight[row] : 1.0f;
+    uint32_t mine, mine_next = 0;
+    int at, wide = 0;
+    {
+      const RowSlice<E> s(p, row, rank);
+      mine = s.mine, at = s.from;
+    }
+    const E *from = logits;
+    if (next < p.N) {
+      const RowSlice<E> s(p, next, rank);
+      mine_next = s.mine;
+      from += (int64_t)next * p.logits_row + s.from;
+    }
+    // Maximum and sum of this thread's chunks, as they arrive.
+    MaxSum acc = {kNegInf, 0.0f};
+    uint32_t c = tid;
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g) {
+      uint32_t next_c = c;
+      const uint32_t end = (g + 1) * quarter, stop = min(end, mine);
+      copy_wait_left(kGrad ? kGroups - 1 - g : kGroups - 1);
 #pragma unroll 2
-    for (; c < end; c += nthr) {
-      Ch<2> x[kN / 2];
-      widen_chunk<E>(slice[c], x);
-      float top = fmaxf(x[0].v[0], x[0].v[1]);
+      for (; c < stop; c += nthr) {
+        Ch<2> x[kN / 2];
+        widen_chunk<E>(slice[c], x);
+        float top = fmaxf(x[0].v[0], x[0].v[1]);
 #pragma unroll
-      for (int k = 1; k < kN / 2; ++k) top = fmaxf(top, fmaxf(x[k].v[0], x[k].v[1]));
-      if (top > acc.m) {
-        acc.s *= exp2_sfu((acc.m - top) * p.scale);
-        acc.m = top;
-      }
-      const Ch<2> base = splat<2>(-base_of(acc.m));
-      Ch<2> sum;
-#pragma unroll
-      for (int k = 0; k < kN / 2; ++k) {
-        const Ch<2> y = (x[k] + base) * scale;
-        const Ch<2> v = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
-        sum = k == 0 ? v : sum + v;
-      }
-      acc.s += sum.v[0] + sum.v[1];
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const MaxSum other = {__shfl_xor_sync(0xffffffffu, acc.m, o),
-                          __shfl_xor_sync(0xffffffffu, acc.s, o)};
-    acc = join(acc, other, p.scale);
-  }
-  if (lane == 0) warp_stats[warp] = make_float2(acc.m, acc.s);
-  __syncthreads();  // also: the slice is in shared memory
-  if (warp == 0) {
-    acc = {kNegInf, 0.0f};
-    if (lane < nthr / 32) acc = {warp_stats[lane].x, warp_stats[lane].y};
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      const MaxSum other = {__shfl_xor_sync(0xffffffffu, acc.m, o),
-                            __shfl_xor_sync(0xffffffffu, acc.s, o)};
-      acc = join(acc, other, p.scale);
-    }
-    // lanes 16 and up joined nothing: lane 0 has the slice's
-    acc = {__shfl_sync(0xffffffffu, acc.m, 0), __shfl_sync(0xffffffffu, acc.s, 0)};
-    const float base = base_of(acc.m);
-    float part = 0.0f, pm = 0.0f;
-    for (uint32_t k = lane; k < p.K; k += 32) {
-      const int at = e.id[k] - e0;
-      if (e.id[k] >= 0 && at >= 0 && at < (int)(mine * kN)) {
-        const float x = to_f32(reinterpret_cast<const E *>(slice)[at]), pk = e.p[k];
-        e.x[k] = x;
-        if (pk != 0.0f) {
-          part += pk * (x == kNegInf ? -kNegInf : fmaf(base - x, p.inv_temp, e.logp[k]));
-          pm += pk;
+        for (int k = 1; k < kN / 2; ++k) top = fmaxf(top, fmaxf(x[k].v[0], x[k].v[1]));
+        if (top > acc.m) {
+          acc.s *= exp2_sfu((acc.m - top) * p.scale);
+          acc.m = top;
         }
-      } else {
-        e.id[k] = -1;
+        const Ch<2> base = splat<2>(-base_of(acc.m));
+        Ch<2> sum;
+#pragma unroll
+        for (int k = 0; k < kN / 2; ++k) {
+          const Ch<2> y = (x[k] + base) * scale;
+          const Ch<2> v = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+          sum = k == 0 ? v : sum + v;
+        }
+        acc.s += sum.v[0] + sum.v[1];
+      }
+      if (!kGrad) {  // nothing else wants the chunks
+        for (; next_c < min(end, mine_next); next_c += nthr)
+          copy_async<16>(slice + next_c, from + next_c * kN);
+        copy_commit();
+        c = next_c > c ? next_c : c;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      part += __shfl_xor_sync(0xffffffffu, part, o);
-      pm += __shfl_xor_sync(0xffffffffu, pm, o);
+    acc = warp_join(acc, p.scale);
+    if (lane == 0) sh.warp_stats[warp] = make_float2(acc.m, acc.s);
+    __syncthreads();  // (1)
+    if (warp == 0) {
+      acc = {kNegInf, 0.0f};
+      if (lane <= (int)nthr / 32) acc = {sh.warp_stats[lane].x, sh.warp_stats[lane].y};
+      acc = warp_join(acc, p.scale);
+      if (lane == 0) barrier_expect(&sh.arrived[i & 1], C * sizeof(float4));
+      if (lane < (int)C)
+        send(remote_smem(&sh.stats[i & 1][rank], lane), remote_smem(&sh.arrived[i & 1], lane),
+             make_float4(acc.m, acc.s, sh.sums[i & 1].part, 0.0f));
     }
     if (kGrad) {
-      // Of entries with the same id, one writes the sum of their p: the one whose
-      // number is left in the slice at that id.  (What the gradient's loop makes of
-      // the numbers is written over.)
-      __syncwarp();
-      for (uint32_t k = lane; k < p.K; k += 32)
-        if (e.id[k] >= 0) reinterpret_cast<Tag<E> *>(slice)[e.id[k] - e0] = (Tag<E>)k;
-    }
-    cluster_wait();  // every block of the cluster has started
-    if (lane < (int)C)
-      remote_store(remote_smem(&stats[rank], lane), make_float4(acc.m, acc.s, part, pm));
-  } else {
-    cluster_wait();
-  }
-  cluster_arrive();
-  cluster_wait();
-  acc = {stats[0].x, stats[0].y};
-  for (uint32_t r = 1; r < C; ++r) acc = join(acc, {stats[r].x, stats[r].y}, p.scale);
-  const float mass = mass_of_row;
-  if (rank == 0 && tid == 0) {
-    const float log_s = logf(acc.s);
-    float loss = 0.0f;
-    for (uint32_t r = 0; r < C; ++r) {
-      const float4 v = stats[r];
-      if (v.w != 0.0f)
-        loss += v.z + v.w * fmaf(base_of(acc.m) - base_of(v.x), p.inv_temp, log_s);
-    }
-    // a student without any logit above -inf gives the teacher's entries probability 0
-    if (acc.s == 0.0f) loss = mass == 0.0f ? 0.0f : -kNegInf;
-    p.loss[row] = loss * p.temp * p.temp;
-  }
-  if (!kGrad) return;
-
-  const float w = (p.weight ? p.weight[row] : 1.0f) * p.temp;
-  const float f = acc.s == 0.0f ? 0.0f : w * mass / acc.s;  // of the exponentials
-  const Ch<2> base = splat<2>(-base_of(acc.m)), by = splat<2>(f);
-  if (mass == 0.0f) {  // no entry: nothing to learn, whatever the logits are
-    for (uint32_t i = tid; i < mine; i += nthr) store_chunk(i, make_uint4(0, 0, 0, 0));
-    return;
-  }
+      float parts;
+      acc = row_stats(p, sh, i, C, lost, parts);
+      const float mass = sh.sums[i & 1].mass;
+      // no entry: nothing to learn, whatever the logits are
+      const uint32_t keep = mass == 0.0f ? 0u : 0xffffffffu;
+      const float w = weight * p.temp;
+      const float f = acc.s == 0.0f ? 0.0f : w * mass / acc.s;  // of the exponentials
+      const Ch<2> base = splat<2>(-base_of(acc.m)), by = splat<2>(f);
+      E *to = dlogits + (int64_t)row * p.dlogits_row + at;
+      wide = ((uintptr_t)to & 15) == 0;
+      c = tid;
+#pragma unroll 1
+      for (uint32_t end = quarter; end <= kGroups * quarter; end += quarter) {
+        const uint32_t stop = min(end, max(mine, mine_next));
 #pragma unroll 2
-  for (uint32_t i = tid; i < mine; i += nthr) {
-    Ch<2> x[kN / 2];
-    widen_chunk<E>(slice[i], x);
+        for (; c < stop; c += nthr) {
+          if (c < mine) {
+            Ch<2> x[kN / 2];
+            widen_chunk<E>(slice[c], x);
 #pragma unroll
-    for (int k = 0; k < kN / 2; ++k) {
-      const Ch<2> y = (x[k] + base) * scale;
-      x[k] = by * Ch<2>{exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
-    }
-    store_chunk(i, narrow_chunk<E>(x));
-  }
-  __syncthreads();  // the gradient is written
-  if (warp == 0) {
-    const Tag<E> *tags = reinterpret_cast<const Tag<E> *>(slice);
-    bool twice = false;
-    for (uint32_t k = lane; k < p.K; k += 32)
-      if (e.id[k] >= 0 && tags[e.id[k] - e0] != (Tag<E>)k) twice = true;
-    twice = __any_sync(0xffffffffu, twice);
-    for (uint32_t k = lane; k < p.K; k += 32) {
-      if (e.id[k] < 0 || tags[e.id[k] - e0] != (Tag<E>)k) continue;
-      float pk = e.p[k];
-      if (twice) {  // in the entries' order
-        pk = 0.0f;
-        for (uint32_t i = 0; i < p.K; ++i)
-          if (e.id[i] == e.id[k]) pk += e.p[i];
+            for (int k = 0; k < kN / 2; ++k) {
+              const Ch<2> y = (x[k] + base) * scale;
+              x[k] = by * Ch<2>{exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+            }
+            uint4 v = narrow_chunk<E>(x);
+            v.x &= keep, v.y &= keep, v.z &= keep, v.w &= keep;
+            store_chunk<E>(to + c * kN, wide, v);
+          }
+          if (c < mine_next) copy_async<16>(slice + c, from + c * kN);
+        }
+        copy_commit();
       }
-      const float g = f * exp2_sfu((e.x[k] - base_of(acc.m)) * p.scale);
-      dst[e.id[k]] = from_f32<E>(fmaf(-w, pk, g));
+      asm volatile("bar.arrive 1, %0;" ::"r"(blockDim.x) : "memory");  // (2)
     }
+    row = next;
   }
+  copy_wait<0>();
 }
 
-// Bytes of shared memory of a block's slice that let three blocks share an SM.
+// Bytes of a block's slice: three blocks share an SM, so that one's stores and
+// copies run beside another's sums.
 constexpr uint64_t kSliceBytes = 66 * 1024;
+
+// Clusters that the GPU holds at a time (fewer than its room for their blocks,
+// which have to lie in one part of it), asked once for a layout and device.
+template <class... KArgs>
+cudaError_t clusters_resident(void (*k)(KArgs...), const cudaLaunchConfig_t &cfg, int *n) {
+  struct Known {
+    const void *k;
+    int device;
+    unsigned cluster, threads;
+    size_t smem;
+    int n;
+  };
+  thread_local Known known[16];
+  thread_local int count = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned cluster = cfg.attrs[0].val.clusterDim.x, threads = cfg.blockDim.x;
+  for (int i = 0; i < (count < 16 ? count : 16); ++i) {
+    const Known &c = known[i];
+    if (c.k == (const void *)k && c.device == device && c.cluster == cluster &&
+        c.threads == threads && c.smem == cfg.dynamicSmemBytes) {
+      *n = c.n;
+      return cudaSuccess;
+    }
+  }
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cfg.dynamicSmemBytes);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(n, k, &cfg);
+  if (e == cudaSuccess && *n < 1) e = cudaErrorLaunchOutOfResources;
+  if (e == cudaSuccess)
+    known[count++ % 16] = {(const void *)k, device, cluster, threads, cfg.dynamicSmemBytes, *n};
+  return e;
+}
 
 template <class E, bool kGrad>
 cudaError_t launch(DistillParams &p, cudaStream_t st) {
-  // chunks of a row at its least favourable alignment
-  const uint64_t bytes = ((uint64_t)p.V * sizeof(E) + 15 + 15) / 16 * 16;
+  const uint32_t chunks = (uint32_t)((uint64_t)p.V * sizeof(E) / 16);  // of a row at most
   uint32_t C = 1;
-  while (C < kMaxCluster && bytes > C * kSliceBytes) C *= 2;
-  p.slice = (uint32_t)((bytes / 16 + C - 1) / C);
-  const size_t smem = (size_t)p.slice * 16 + (size_t)p.K * 16;
-  const unsigned threads = p.slice >= 2048 ? 512 : p.slice >= 512 ? 256 : 128;
+  while (C < kMaxCluster && chunks > C * (kSliceBytes / 16)) C *= 2;
+  p.slice = chunks ? (chunks + C - 1) / C : 1;
+  p.slots = 2;
+  while (p.slots < 2 * p.K) p.slots *= 2;
+  const size_t smem =
+      (size_t)p.slice * 16 + (size_t)p.K * 32 + (kGrad ? p.slots * sizeof(Slot) : 0);
+  const unsigned threads = p.slice >= 1024 ? kMaxThreads : p.slice >= 256 ? 160 : 96;
   auto *k = distill_kernel<E, kGrad>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.N * C);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(C);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -393,8 +630,22 @@ cudaError_t launch(DistillParams &p, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  int resident = 0;
+  cudaError_t e = clusters_resident(k, cfg, &resident);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  if (smem > 48 * 1024) {  // another layout may have asked for less since
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+  }
+  cfg.gridDim = dim3(C * (p.N < (uint32_t)resident ? p.N : (uint32_t)resident));
   ++launch_counter();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, (const DistillParams)p);
+  e = cudaLaunchKernelEx(&cfg, k, (const DistillParams)p);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }

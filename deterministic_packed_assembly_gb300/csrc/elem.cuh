@@ -194,4 +194,42 @@ __device__ __forceinline__ void remote_store(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// ---- barriers that asynchronous stores count down --------------------------------
+__device__ __forceinline__ void barrier_init(uint64_t *bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(bar))
+               : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// Wait for the phase of this parity; false if it has not come after about a second.
+__device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(bar);
+  for (int i = 0; i < 100000; ++i) {  // each try suspends for some microseconds at most
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+// Asynchronous store of 16 bytes to `to`, which counts them down at `bar` (both
+// addresses of a block of the cluster).
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, float4 v) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(to),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+      : "memory");
+}
+
 }  // namespace nsk

@@ -330,33 +330,6 @@ struct Quads {
   uint64_t arrived;  // an mbarrier
 };
 
-__device__ __forceinline__ void barrier_init(uint64_t *bar) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(bar))
-               : "memory");
-}
-__device__ __forceinline__ void barrier_expect(uint64_t *bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(bar)),
-               "r"(bytes)
-               : "memory");
-}
-// Wait for the phase of this parity; false if it has not come after about a second.
-__device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity) {
-  const uint32_t at = (uint32_t)__cvta_generic_to_shared(bar);
-  for (int i = 0; i < 100000; ++i) {  // each try suspends for some microseconds at most
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 10000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
-}
 template <int CH>
 __device__ __forceinline__ void send_run(uint32_t to, uint32_t bar, Run<CH> r) {
   if constexpr (CH == 2) {
