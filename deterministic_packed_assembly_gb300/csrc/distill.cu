@@ -53,7 +53,6 @@ struct DistillParams {
   int32_t top_dtype, ids_64;
   float temp, inv_temp, scale;  // scale = log2 e / temp
   uint32_t slice;               // 16-byte chunks of a block's slice
-  uint32_t slots;               // of the dictionary of its entries
   float *loss;
   void *dlogits;
   int64_t dlogits_row;
@@ -213,52 +212,46 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
   return r;
 }
 
-// A slot of the dictionary of a slice's entries: an id and its first entry.
-struct Slot {
-  int id, first;
-};
-__device__ __forceinline__ uint32_t slot_of(int id, uint32_t slots) {
-  return ((uint32_t)id * 2654435761u >> 12) & (slots - 1);  // Knuth's multiplicative hash
-}
-
 // Of a slice's entries with the same id the first one is to write the gradient, of
-// the sum of their p (in the entries' order); the others' ids become -1.  `slots`
-// is a power of two, at least twice the entries.
-__device__ void join_repeated(uint32_t K, uint32_t slots, int lane, const Entries &e,
-                              Slot *dictionary) {
-  for (uint32_t i = lane; i < slots; i += 32) dictionary[i] = {-1, (int)K};
-  __syncwarp();
+// the sum of their p (in the entries' order); the others' ids become -1.  `seen`: a
+// bit for every id of the slice, [from, last); all 0 before and after.
+// (The ids at the row's ends, before and after the slice, are compared one by one.)
+__device__ void join_repeated(uint32_t K, int from, int last, int lane, const Entries &e,
+                              uint32_t *seen) {
   bool twice = false;
+#pragma unroll 1
   for (uint32_t k = lane; k < K; k += 32) {
     const int id = e.id[k];
     if (id < 0) continue;
-    for (uint32_t h = slot_of(id, slots), tries = 0; tries < slots; ++tries) {
-      const int was = atomicCAS(&dictionary[h].id, -1, id);
-      if (was == -1 || was == id) {
-        twice = twice || was == id;
-        atomicMin(&dictionary[h].first, (int)k);
-        break;
-      }
-      h = (h + 1) & (slots - 1);
+    if (id < from || id >= last) {
+      for (uint32_t i = 0; i < k; ++i) twice = twice || e.id[i] == id;
+    } else {
+      const uint32_t bit = 1u << ((id - from) & 31);
+      if (atomicOr(&seen[(id - from) >> 5], bit) & bit) twice = true;
     }
+  }
+  __syncwarp();
+  for (uint32_t k = lane; k < K; k += 32) {
+    const int id = e.id[k];
+    if (id >= from && id < last) seen[(id - from) >> 5] = 0;
   }
   if (!__any_sync(0xffffffffu, twice)) return;
   for (uint32_t k = lane; k < K; k += 32) {
     const int id = e.id[k];
     if (id < 0) continue;
-    uint32_t h = slot_of(id, slots);
-    for (uint32_t tries = 0; tries < slots && dictionary[h].id != id; ++tries)
-      h = (h + 1) & (slots - 1);
     float sum = -1.0f;  // no sum of probabilities: not the first
-    if (dictionary[h].first == (int)k) {
+    uint32_t i = 0;
+    while (e.id[i] != id) ++i;
+    if (i == k) {
       sum = 0.0f;
-      for (uint32_t i = k; i < K; ++i)
+      for (; i < K; ++i)
         if (e.id[i] == id) sum += e.p[i];
     }
     e.logp[k] = sum;  // the loss is done with the logarithms
   }
   __syncwarp();
   for (uint32_t k = lane; k < K; k += 32) {
+    if (e.id[k] < 0) continue;
     if (e.logp[k] == -1.0f) e.id[k] = -1;
     else e.p[k] = e.logp[k];
   }
@@ -306,24 +299,34 @@ struct RowWalk {
 };
 
 struct Shared {
-  float4 stats[2][kMaxCluster];  // every slice's maximum, sum and part, of two rows
+  float4 stats[2][kMaxCluster];  // every slice's maximum, sum and part, and the row's mass
   uint64_t arrived[2];           // mbarriers: the stats have
-  float2 warp_stats[kMaxThreads / 32];  // the entry warp's last: the row's ends
-  EntrySums sums[2];
+  float2 warp_stats[2][kMaxThreads / 32];
 };
 
-// The row's maximum and sum from every slice's, and the loss's parts added up.
-__device__ __forceinline__ MaxSum row_stats(const DistillParams &p, Shared &sh, uint32_t round,
-                                            uint32_t C, bool &lost, float &parts) {
+// Barrier 1: a row's gradient is written; 2 and 3: an even or odd round's
+// warp_stats are.  The rows' warps only arrive.
+__device__ __forceinline__ void named_arrive(int barrier) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "r"(blockDim.x) : "memory");
+}
+__device__ __forceinline__ void named_wait(int barrier) {
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(blockDim.x) : "memory");
+}
+
+struct RowStats {
+  MaxSum all;
+  float parts, mass;
+};
+__device__ __forceinline__ RowStats row_stats(const DistillParams &p, Shared &sh, uint32_t round,
+                                              uint32_t C, bool &lost) {
   if (!lost && !barrier_wait(&sh.arrived[round & 1], round >> 1 & 1)) lost = true;
   const float4 *v = sh.stats[round & 1];
-  MaxSum r = {v[0].x, v[0].y};
-  parts = v[0].z;
+  RowStats r = {{v[0].x, v[0].y}, v[0].z, v[0].w};
   for (uint32_t i = 1; i < C; ++i) {
-    r = join(r, {v[i].x, v[i].y}, p.scale);
-    parts += v[i].z;
+    r.all = join(r.all, {v[i].x, v[i].y}, p.scale);
+    r.parts += v[i].z;
   }
-  if (lost) r.s = parts = __int_as_float(0x7fffffff);  // shows in the loss and the gradient
+  if (lost) r.all.s = r.parts = __int_as_float(0x7fffffff);  // shows in loss and gradient
   return r;
 }
 __device__ __forceinline__ MaxSum warp_join(MaxSum a, float scale) {
@@ -338,26 +341,29 @@ __device__ __forceinline__ MaxSum warp_join(MaxSum a, float scale) {
 template <class E, bool kGrad>
 __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, float *arrays,
                                         uint32_t rank, uint32_t C, uint32_t stride, int lane) {
+  constexpr int kN = 16 / sizeof(E);
   const E *logits = static_cast<const E *>(p.logits);
   auto entries = [&](uint32_t i) {  // of even and odd rounds
     Entries e;
-    e.p = arrays + (i & 1) * 4 * p.K;
-    e.logp = e.p + p.K;
-    e.x = e.logp + p.K;
+    e.logp = arrays;  // of the row that is prepared
+    e.p = arrays + (1 + (i & 1) * 3) * p.K;
+    e.x = e.p + p.K;
     e.id = reinterpret_cast<int *>(e.x + p.K);
     return e;
   };
-  Slot *dictionary = reinterpret_cast<Slot *>(arrays + 8 * p.K);
-  float end = kNegInf, next_end = kNegInf;  // this lane's logit at the row's ends
+  uint32_t *seen = reinterpret_cast<uint32_t *>(arrays + 7 * p.K);
+  for (uint32_t w = lane; kGrad && w < (p.slice * kN + 31) / 32; w += 32) seen[w] = 0;
+  __syncwarp();
+  float next_end = kNegInf;  // this lane's logit at the row's ends
+  EntrySums next_sums = {};
   auto prepare = [&](uint32_t row, uint32_t i) {
     const RowSlice<E> s(p, row, rank);
     const E *src = logits + (int64_t)row * p.logits_row;
     const int at = s.end_of(p, rank, lane);
     next_end = at >= 0 ? to_f32(src[at]) : kNegInf;
     const Entries e = entries(i);
-    const EntrySums r = teacher_entries<E>(p, row, src, s, rank, lane, e);
-    if (lane == 0) sh.sums[i & 1] = r;
-    if (kGrad) join_repeated(p.K, p.slots, lane, e, dictionary);
+    next_sums = teacher_entries<E>(p, row, src, s, rank, lane, e);
+    if (kGrad) join_repeated(p.K, s.from, s.from + (int)s.mine * kN, lane, e, seen);
     __syncwarp();
   };
   auto nothing = [](uint32_t) {};
@@ -368,35 +374,40 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
   for (uint32_t i = 0; row < p.N; ++i) {
     const uint32_t next = walk.learned(p, lane, nothing);
     const float weight = p.weight ? p.weight[row] : 1.0f;
-    end = next_end;
-    const MaxSum ends = warp_join({end, end == kNegInf ? 0.0f : end == end ? 1.0f : end}, p.scale);
-    if (lane == 0) sh.warp_stats[blockDim.x / 32 - 1] = make_float2(ends.m, ends.s);
-    __syncthreads();  // (1) the row's slice is reduced, its entries are here
+    const float end = next_end;
+    const EntrySums sums = next_sums;
+    if (lane == 0) barrier_expect(&sh.arrived[i & 1], C * sizeof(float4));
+    MaxSum mine = {end, end == kNegInf ? 0.0f : end == end ? 1.0f : end};
+    named_wait(2 + (i & 1));
+    const int warps = (int)blockDim.x / 32 - 1;
+    if (lane < warps)
+      mine = join(mine, {sh.warp_stats[i & 1][lane].x, sh.warp_stats[i & 1][lane].y}, p.scale);
+    mine = warp_join(mine, p.scale);
+    if (lane < (int)C)
+      send(remote_smem(&sh.stats[i & 1][rank], lane), remote_smem(&sh.arrived[i & 1], lane),
+           make_float4(mine.m, mine.s, sums.part, sums.mass));
     if (next < p.N) prepare(next, i + 1);
-    float parts;
-    const MaxSum all = row_stats(p, sh, i, C, lost, parts);
-    const EntrySums sums = sh.sums[i & 1];
+    const RowStats r = row_stats(p, sh, i, C, lost);
     if (rank == 0 && lane == 0) {
-      float loss = parts + sums.mass * fmaf(base_of(all.m) - sums.c, p.inv_temp, logf(all.s));
+      float loss = r.parts + r.mass * fmaf(base_of(r.all.m) - sums.c, p.inv_temp, logf(r.all.s));
       // a student without any logit above -inf gives the teacher's entries probability 0
-      if (all.s == 0.0f) loss = -kNegInf;
-      p.loss[row] = sums.mass == 0.0f ? 0.0f : loss * p.temp * p.temp;
+      if (r.all.s == 0.0f) loss = -kNegInf;
+      p.loss[row] = r.mass == 0.0f ? 0.0f : loss * p.temp * p.temp;
     }
     if (kGrad) {
       const float w = weight * p.temp;
-      const float f = all.s == 0.0f ? 0.0f : w * sums.mass / all.s;
+      const float f = r.all.s == 0.0f ? 0.0f : w * r.mass / r.all.s;
       E *dst = static_cast<E *>(p.dlogits) + (int64_t)row * p.dlogits_row;
       const int at = RowSlice<E>(p, row, rank).end_of(p, rank, lane);
       if (at >= 0)
         dst[at] = from_f32<E>(
-            sums.mass == 0.0f ? 0.0f : f * exp2_sfu((end - base_of(all.m)) * p.scale));
+            r.mass == 0.0f ? 0.0f : f * exp2_sfu((end - base_of(r.all.m)) * p.scale));
       const Entries e = entries(i);
-      // (2) the row's gradient is written
-      asm volatile("bar.sync 1, %0;" ::"r"(blockDim.x) : "memory");
-      if (sums.mass != 0.0f)
+      named_wait(1);
+      if (r.mass != 0.0f)
         for (uint32_t k = lane; k < p.K; k += 32)
           if (e.id[k] >= 0) {
-            const float g = f * exp2_sfu((e.x[k] - base_of(all.m)) * p.scale);
+            const float g = f * exp2_sfu((e.x[k] - base_of(r.all.m)) * p.scale);
             dst[e.id[k]] = from_f32<E>(fmaf(-w, e.p[k], g));
           }
       __syncwarp();
@@ -517,21 +528,16 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
       }
     }
     acc = warp_join(acc, p.scale);
-    if (lane == 0) sh.warp_stats[warp] = make_float2(acc.m, acc.s);
-    __syncthreads();  // (1)
-    if (warp == 0) {
-      acc = {kNegInf, 0.0f};
-      if (lane <= (int)nthr / 32) acc = {sh.warp_stats[lane].x, sh.warp_stats[lane].y};
-      acc = warp_join(acc, p.scale);
-      if (lane == 0) barrier_expect(&sh.arrived[i & 1], C * sizeof(float4));
-      if (lane < (int)C)
-        send(remote_smem(&sh.stats[i & 1][rank], lane), remote_smem(&sh.arrived[i & 1], lane),
-             make_float4(acc.m, acc.s, sh.sums[i & 1].part, 0.0f));
-    }
+    // the place was read when the round before the last had its statistics
+    if (!kGrad && i >= 2 && !lost && !barrier_wait(&sh.arrived[i & 1], (i - 2) >> 1 & 1))
+      lost = true;
+    if (lane == 0) sh.warp_stats[i & 1][warp] = make_float2(acc.m, acc.s);
+    __syncwarp();
+    named_arrive(2 + (i & 1));
     if (kGrad) {
-      float parts;
-      acc = row_stats(p, sh, i, C, lost, parts);
-      const float mass = sh.sums[i & 1].mass;
+      const RowStats r = row_stats(p, sh, i, C, lost);
+      acc = r.all;
+      const float mass = r.mass;
       // no entry: nothing to learn, whatever the logits are
       const uint32_t keep = mass == 0.0f ? 0u : 0xffffffffu;
       const float w = weight * p.temp;
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
         }
         copy_commit();
       }
-      asm volatile("bar.arrive 1, %0;" ::"r"(blockDim.x) : "memory");  // (2)
+      named_arrive(1);
     }
     row = next;
   }
@@ -606,16 +612,20 @@ cudaError_t clusters_resident(void (*k)(KArgs...), const cudaLaunchConfig_t &cfg
   return e;
 }
 
+// Shared memory of a block: its slice, the entries, and for the gradient a bit for
+// each of the slice's elements.
+size_t distill_smem(uint32_t slice, uint32_t K, size_t element) {
+  return (size_t)slice * 16 + (size_t)K * 28 +
+         (element ? ((size_t)slice * 16 / element + 31) / 32 * 4 : 0);
+}
+
 template <class E, bool kGrad>
 cudaError_t launch(DistillParams &p, cudaStream_t st) {
   const uint32_t chunks = (uint32_t)((uint64_t)p.V * sizeof(E) / 16);  // of a row at most
   uint32_t C = 1;
   while (C < kMaxCluster && chunks > C * (kSliceBytes / 16)) C *= 2;
   p.slice = chunks ? (chunks + C - 1) / C : 1;
-  p.slots = 2;
-  while (p.slots < 2 * p.K) p.slots *= 2;
-  const size_t smem =
-      (size_t)p.slice * 16 + (size_t)p.K * 32 + (kGrad ? p.slots * sizeof(Slot) : 0);
+  const size_t smem = distill_smem(p.slice, p.K, kGrad ? sizeof(E) : 0);
   const unsigned threads = p.slice >= 1024 ? kMaxThreads : p.slice >= 256 ? 160 : 96;
   auto *k = distill_kernel<E, kGrad>;
   cudaLaunchConfig_t cfg = {};

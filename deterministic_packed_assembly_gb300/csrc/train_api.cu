@@ -86,7 +86,8 @@ int ns_distill(const ns_distill_inputs *in, float *loss, void *dlogits, int64_t 
   if (!in) return NS_ERR_INVALID_ARG;
   const uint64_t es = size_of(in->dtype), ts = size_of(in->top_dtype);
   if (!es || !ts || in->V == 0 || in->V * es > NS_DISTILL_MAX_ROW || in->K == 0 ||
-      in->K > NS_DISTILL_MAX_TOP || in->N >= (1u << 28))
+      in->K > NS_DISTILL_MAX_TOP || in->N >= (1u << 28) ||
+      (in->V * es > NS_DISTILL_WIDE_ROW && in->K > NS_DISTILL_WIDE_TOP))
     return NS_ERR_INVALID_ARG;
   if (!(in->temperature > 0.0f) || !std::isfinite(in->temperature) ||
       !std::isfinite(2.0f / in->temperature))

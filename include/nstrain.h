@@ -55,6 +55,8 @@ extern "C" {
 #define NS_SCAN_MAX_T (1u << 30) /* time steps of a row */
 #define NS_DISTILL_MAX_TOP 1024u /* teacher logits a row */
 #define NS_DISTILL_MAX_ROW (8u * 200u * 1024u) /* bytes of a row of logits */
+#define NS_DISTILL_WIDE_ROW (8u * 176u * 1024u) /* beyond these, at most ... */
+#define NS_DISTILL_WIDE_TOP 256u               /* ... so many teacher logits */
 #define NS_ROUTE_MAX_EXPERTS 1024u
 #define NS_ROUTE_MAX_K 32u       /* experts a token */
 
@@ -132,7 +134,8 @@ typedef struct {
   const float *teacher_lse; /* [N] or NULL */
   const uint8_t *mask;     /* [N] or NULL: every row is learned */
   const float *weight;     /* [N] or NULL */
-  uint32_t N, V, K;        /* V * element size <= NS_DISTILL_MAX_ROW, K <= NS_DISTILL_MAX_TOP */
+  uint32_t N, V, K;        /* N < 2^28, V * element size <= NS_DISTILL_MAX_ROW,
+                              K <= NS_DISTILL_MAX_TOP (see NS_DISTILL_WIDE_ROW) */
   int32_t dtype, top_dtype;
   int32_t ids_64;
   float temperature;       /* > 0, finite */

@@ -72,7 +72,7 @@ def distill(nsp, **kw):
 @pytest.mark.parametrize("kw", [
     dict(logits=None), dict(logits=AT + 1), dict(logits_row=63), dict(logits_row=-64),
     dict(top_logits=None), dict(top_logits=AT + 2), dict(top_ids=None), dict(top_ids=AT + 4, ids_64=1),
-    dict(V=0), dict(V=1 << 21), dict(K=0), dict(K=1025), dict(N=1 << 28), dict(dtype=9),
+    dict(V=0), dict(V=1 << 21), dict(K=0), dict(K=1025), dict(V=780_000, logits_row=780_000, K=257), dict(N=1 << 28), dict(dtype=9),
     dict(top_dtype=5), dict(teacher_lse=AT + 1), dict(weight=AT + 2), dict(loss=None),
     dict(loss=AT + 1), dict(dlogits=AT + 4097), dict(dlogits_row=10), dict(dlogits=AT + 64),
     dict(dlogits=AT, dlogits_row=65), dict(temperature=0.0), dict(temperature=-2.0),
