@@ -11,14 +11,15 @@
 // asynchronously, reduces them to a running maximum and sum as they arrive, and,
 // once the blocks have exchanged theirs, turns each into the gradient and starts
 // the copy of the cluster's next row into its place.  So the copies of a row run
-// beside the stores of the one before.  The teacher's K entries are few: a warp of
-// their own in each block has them, a row ahead.  With c the student's logit at the
+// beside the stores of the one before.  The teacher's K entries are few: two
+// warps of their own in each block have them, of even and of odd rows, ahead of the
+// rows' warps.  With c the student's logit at the
 // teacher's first choice, M and S the row's maximum and sum,
 //   sum_k p_k (log p_k - log q_k) = sum_k p_k (log p_k - (s_k - c) / temp)
 //                                   + m (log S + (M - c) / temp),
 // whose first sum each block takes over the ids in its slice, without the row's
 // statistics, so that one exchange is enough; its terms are small, as the
-// teacher's choices are near c.  After the gradient is written the warp writes the
+// teacher's choices are near c.  After the gradient is written their warp writes the
 // entries' own over it.
 //
 // Logits are kept as they came.  An exponential is 2^((s - max) log2 e / temp):
@@ -37,7 +38,8 @@
 namespace nsk {
 namespace {
 
-constexpr int kMaxThreads = 288;  // eight warps for the row, one for the entries
+constexpr int kEntryWarps = 2;  // one for even rows, one for odd ones
+constexpr int kMaxThreads = 256 + 32 * kEntryWarps;
 constexpr int kMaxCluster = 8;
 constexpr int kGroups = 4;  // of asynchronous copies, waited for in order
 
@@ -119,6 +121,19 @@ struct RowSlice {
   }
 };
 
+// A row's ids and teacher logits into the L2 cache: read from memory beside the rows'
+// copies they take microseconds.
+__device__ __forceinline__ void prefetch_entries(const DistillParams &p, uint32_t row, int lane) {
+  const uint64_t ids = (uint64_t)p.K * (p.ids_64 ? 8 : 4),
+                 top = (uint64_t)p.K * (p.top_dtype == NS_F32 ? 4 : 2);
+  const char *a = static_cast<const char *>(p.ids) + row * ids,
+             *b = static_cast<const char *>(p.top) + row * top;
+  for (uint64_t i = (uint64_t)lane * 128; i < ids; i += 32 * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a + i));
+  for (uint64_t i = (uint64_t)lane * 128; i < top; i += 32 * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
+}
+
 // The entries' warp: the teacher's probabilities and the student's logits at the
 // entries of this block's slice [from, to).
 struct EntrySums {
@@ -139,34 +154,15 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
   float m = kNegInf;
   uint32_t top = 0xffffffffu;  // the first entry of the largest logit, and its id
   int top_id = 0;
-  constexpr int kBatch = 4;  // loads in flight
-  for (uint32_t k0 = lane; k0 < p.K; k0 += 32 * kBatch) {
-    int id[kBatch];
-    float t[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint32_t k = k0 + 32 * i;
-      id[i] = -1;
-      if (k < p.K) {
-        const int64_t v = p.ids_64 ? static_cast<const int64_t *>(p.ids)[base + k]
-                                   : (int64_t)static_cast<const int32_t *>(p.ids)[base + k];
-        if (v >= 0 && v < (int64_t)p.V) id[i] = (int)v;
-        t[i] = load_top(p.top, p.top_dtype, base + k);
-      }
-    }
-    float x[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (ours(id[i])) x[i] = to_f32(logits[id[i]]);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint32_t k = k0 + 32 * i;
-      if (k >= p.K) continue;
-      e.id[k] = id[i];
-      e.logp[k] = id[i] >= 0 ? t[i] : kNegInf;
-      if (id[i] >= 0 && t[i] > m) m = t[i], top = k, top_id = id[i];
-      if (ours(id[i])) e.x[k] = x[i];
-    }
+#pragma unroll 4
+  for (uint32_t k = lane; k < p.K; k += 32) {
+    const int64_t v = p.ids_64 ? static_cast<const int64_t *>(p.ids)[base + k]
+                               : (int64_t)static_cast<const int32_t *>(p.ids)[base + k];
+    const float t = load_top(p.top, p.top_dtype, base + k);
+    const int id = v >= 0 && v < (int64_t)p.V ? (int)v : -1;
+    e.id[k] = id;
+    e.logp[k] = id >= 0 ? t : kNegInf;
+    if (id >= 0 && t > m) m = t, top = k, top_id = id;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -176,11 +172,28 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
     if (om > m || (om == m && ok < top)) m = om, top = ok, top_id = oi;
   }
   EntrySums r = {0.0f, 0.0f, 0.0f};
-  if (top != 0xffffffffu) r.c = to_f32(logits[top_id]);
+  E at_top = from_f32<E>(0.0f);
+  if (top != 0xffffffffu) at_top = logits[top_id];
+  constexpr int kBatch = 8;  // loads in flight
+  for (uint32_t k0 = lane; k0 < p.K; k0 += 32 * kBatch) {
+    E x[kBatch];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint32_t k = k0 + 32 * i;
+      const int id = k < p.K ? e.id[k] : -1;
+      if (ours(id)) x[i] = logits[id], mine |= 1u << i;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (mine >> i & 1) e.x[k0 + 32 * i] = to_f32(x[i]);
+  }
+  r.c = to_f32(at_top);
   if (r.c == kNegInf) r.c = 0.0f;
   const float base_m = base_of(m);
   const float lse = p.teacher_lse ? p.teacher_lse[row] : 0.0f;
   float sum = 0.0f;
+#pragma unroll 2
   for (uint32_t k = lane; k < p.K; k += 32) {
     const float t = e.logp[k];
     const float l = p.teacher_lse ? fmaf(t, p.inv_temp, -lse) : (t - base_m) * p.inv_temp;
@@ -196,6 +209,7 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
   float inv = 1.0f, log_sum = 0.0f;
   r.mass = sum;
   if (!p.teacher_lse && sum != 0.0f) inv = 1.0f / sum, log_sum = logf(sum), r.mass = 1.0f;
+#pragma unroll 2
   for (uint32_t k = lane; k < p.K; k += 32) {
     const int id = e.id[k];
     if (!ours(id)) {
@@ -213,29 +227,37 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
 }
 
 // Of a slice's entries with the same id the first one is to write the gradient, of
-// the sum of their p (in the entries' order); the others' ids become -1.  `seen`: a
-// bit for every id of the slice, [from, last); all 0 before and after.
-// (The ids at the row's ends, before and after the slice, are compared one by one.)
-__device__ void join_repeated(uint32_t K, int from, int last, int lane, const Entries &e,
-                              uint32_t *seen) {
-  bool twice = false;
-#pragma unroll 1
-  for (uint32_t k = lane; k < K; k += 32) {
+// the sum of their p (in the entries' order); the others' ids become -1.  `seen` has
+// kSeen bits, 0 before and after, that an id's hash picks from: an id that finds its
+// bit set is looked for among the others.
+constexpr uint32_t kSeen = 8192;
+__device__ __forceinline__ uint32_t bit_of(int id) {  // Knuth's multiplicative hash
+  return (uint32_t)id * 2654435761u >> 19;
+}
+static_assert(kSeen == 1u << (32 - 19), "a hash is a bit's number");
+static_assert(NS_DISTILL_MAX_TOP <= 32 * 32, "a lane's entries are a word's bits");
+__device__ void join_repeated(uint32_t K, int lane, const Entries &e, uint32_t *seen) {
+  uint32_t again = 0;  // this lane's entries (k / 32) that found their bit set
+  for (uint32_t k = lane, i = 0; k < K; k += 32, ++i) {
     const int id = e.id[k];
     if (id < 0) continue;
-    if (id < from || id >= last) {
-      for (uint32_t i = 0; i < k; ++i) twice = twice || e.id[i] == id;
-    } else {
-      const uint32_t bit = 1u << ((id - from) & 31);
-      if (atomicOr(&seen[(id - from) >> 5], bit) & bit) twice = true;
-    }
+    const uint32_t h = bit_of(id), bit = 1u << (h & 31);
+    if (atomicOr(&seen[h >> 5], bit) & bit) again |= 1u << i;
   }
   __syncwarp();
-  for (uint32_t k = lane; k < K; k += 32) {
-    const int id = e.id[k];
-    if (id >= from && id < last) seen[(id - from) >> 5] = 0;
+  for (uint32_t k = lane; k < K; k += 32)
+    if (e.id[k] >= 0) seen[bit_of(e.id[k]) >> 5] = 0;
+  bool twice = false;
+  for (uint32_t lanes; (lanes = __ballot_sync(0xffffffffu, again != 0)) != 0;) {
+    const int from = __ffs(lanes) - 1;  // the warp looks for one of this lane's
+    const int id = __shfl_sync(0xffffffffu, again ? e.id[lane + 32 * (__ffs(again) - 1)] : 0, from);
+    if (lane == from) again &= again - 1;
+    int found = 0;
+    for (uint32_t k = lane; k < K; k += 32) found += e.id[k] == id;
+    if (__reduce_add_sync(0xffffffffu, found) > 1) twice = true;
   }
-  if (!__any_sync(0xffffffffu, twice)) return;
+  __syncwarp();
+  if (!twice) return;
   for (uint32_t k = lane; k < K; k += 32) {
     const int id = e.id[k];
     if (id < 0) continue;
@@ -298,19 +320,28 @@ struct RowWalk {
   }
 };
 
+// Statistics of rows on their way between the blocks: a row's place is written again
+// four rows later.  By then every reader has read it: a block's statistics of row i
+// + 4 are sent when those of row i + 3, and so of row i + 2, are complete, which
+// every entry warp sends after it has read those of row i.
+constexpr int kPlaces = 4;
 struct Shared {
-  float4 stats[2][kMaxCluster];  // every slice's maximum, sum and part, and the row's mass
-  uint64_t arrived[2];           // mbarriers: the stats have
+  float4 stats[kPlaces][kMaxCluster];  // every slice's maximum, sum and part, the row's mass
+  uint64_t arrived[kPlaces];           // mbarriers: the stats have
   float2 warp_stats[2][kMaxThreads / 32];
 };
 
-// Barrier 1: a row's gradient is written; 2 and 3: an even or odd round's
-// warp_stats are.  The rows' warps only arrive.
+// Barriers 1 and 2: an even or odd row's gradient is written; 3 and 4: its
+// warp_stats are.  The rows' warps only arrive, one entry warp waits.
+__device__ __forceinline__ int row_threads() { return blockDim.x - 32 * kEntryWarps; }
 __device__ __forceinline__ void named_arrive(int barrier) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "r"(blockDim.x) : "memory");
+  asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "r"(row_threads() + 32) : "memory");
 }
 __device__ __forceinline__ void named_wait(int barrier) {
-  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(blockDim.x) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(row_threads() + 32) : "memory");
+}
+__device__ __forceinline__ bool stats_wait(Shared &sh, uint32_t round) {
+  return barrier_wait(&sh.arrived[round % kPlaces], round / kPlaces & 1);
 }
 
 struct RowStats {
@@ -319,8 +350,8 @@ struct RowStats {
 };
 __device__ __forceinline__ RowStats row_stats(const DistillParams &p, Shared &sh, uint32_t round,
                                               uint32_t C, bool &lost) {
-  if (!lost && !barrier_wait(&sh.arrived[round & 1], round >> 1 & 1)) lost = true;
-  const float4 *v = sh.stats[round & 1];
+  if (!lost && !stats_wait(sh, round)) lost = true;
+  const float4 *v = sh.stats[round % kPlaces];
   RowStats r = {{v[0].x, v[0].y}, v[0].z, v[0].w};
   for (uint32_t i = 1; i < C; ++i) {
     r.all = join(r.all, {v[i].x, v[i].y}, p.scale);
@@ -337,56 +368,46 @@ __device__ __forceinline__ MaxSum warp_join(MaxSum a, float scale) {
   return a;
 }
 
-// The entry warp of a block.
+// An entry warp of a block, for the even rows of its walk or the odd ones.
 template <class E, bool kGrad>
 __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, float *arrays,
-                                        uint32_t rank, uint32_t C, uint32_t stride, int lane) {
-  constexpr int kN = 16 / sizeof(E);
+                                           uint32_t *seen, uint32_t parity, uint32_t rank,
+                                           uint32_t C, uint32_t stride, int lane) {
   const E *logits = static_cast<const E *>(p.logits);
-  auto entries = [&](uint32_t i) {  // of even and odd rounds
-    Entries e;
-    e.logp = arrays;  // of the row that is prepared
-    e.p = arrays + (1 + (i & 1) * 3) * p.K;
-    e.x = e.p + p.K;
-    e.id = reinterpret_cast<int *>(e.x + p.K);
-    return e;
-  };
-  uint32_t *seen = reinterpret_cast<uint32_t *>(arrays + 7 * p.K);
-  for (uint32_t w = lane; kGrad && w < (p.slice * kN + 31) / 32; w += 32) seen[w] = 0;
+  Entries e;
+  e.logp = arrays;
+  e.p = e.logp + p.K;
+  e.x = e.p + p.K;
+  e.id = reinterpret_cast<int *>(e.x + p.K);
+  for (uint32_t w = lane; kGrad && w < kSeen / 32; w += 32) seen[w] = 0;
   __syncwarp();
-  float next_end = kNegInf;  // this lane's logit at the row's ends
-  EntrySums next_sums = {};
-  auto prepare = [&](uint32_t row, uint32_t i) {
-    const RowSlice<E> s(p, row, rank);
-    const E *src = logits + (int64_t)row * p.logits_row;
-    const int at = s.end_of(p, rank, lane);
-    next_end = at >= 0 ? to_f32(src[at]) : kNegInf;
-    const Entries e = entries(i);
-    next_sums = teacher_entries<E>(p, row, src, s, rank, lane, e);
-    if (kGrad) join_repeated(p.K, s.from, s.from + (int)s.mine * kN, lane, e, seen);
-    __syncwarp();
-  };
   auto nothing = [](uint32_t) {};
   bool lost = false;
   RowWalk walk(blockIdx.x / C, stride);
   uint32_t row = walk.learned(p, lane, nothing);
-  if (row < p.N) prepare(row, 0);
-  for (uint32_t i = 0; row < p.N; ++i) {
-    const uint32_t next = walk.learned(p, lane, nothing);
+  if (parity) row = walk.learned(p, lane, nothing);
+  for (uint32_t i = parity; row < p.N; i += 2) {
+    uint32_t next = walk.learned(p, lane, nothing);
+    next = walk.learned(p, lane, nothing);
+    if (next < p.N) prefetch_entries(p, next, lane);
+    const RowSlice<E> s(p, row, rank);
+    const E *src = logits + (int64_t)row * p.logits_row;
+    const int at = s.end_of(p, rank, lane);
+    const float end = at >= 0 ? to_f32(src[at]) : kNegInf;  // this lane's logit at the row's ends
     const float weight = p.weight ? p.weight[row] : 1.0f;
-    const float end = next_end;
-    const EntrySums sums = next_sums;
-    if (lane == 0) barrier_expect(&sh.arrived[i & 1], C * sizeof(float4));
+    const EntrySums sums = teacher_entries<E>(p, row, src, s, rank, lane, e);
+    if (kGrad) join_repeated(p.K, lane, e, seen);
+    __syncwarp();
+    if (lane == 0) barrier_expect(&sh.arrived[i % kPlaces], C * sizeof(float4));
     MaxSum mine = {end, end == kNegInf ? 0.0f : end == end ? 1.0f : end};
-    named_wait(2 + (i & 1));
-    const int warps = (int)blockDim.x / 32 - 1;
-    if (lane < warps)
-      mine = join(mine, {sh.warp_stats[i & 1][lane].x, sh.warp_stats[i & 1][lane].y}, p.scale);
+    named_wait(3 + parity);
+    if (lane < row_threads() / 32)
+      mine = join(mine, {sh.warp_stats[parity][lane].x, sh.warp_stats[parity][lane].y}, p.scale);
     mine = warp_join(mine, p.scale);
     if (lane < (int)C)
-      send(remote_smem(&sh.stats[i & 1][rank], lane), remote_smem(&sh.arrived[i & 1], lane),
+      send(remote_smem(&sh.stats[i % kPlaces][rank], lane),
+           remote_smem(&sh.arrived[i % kPlaces], lane),
            make_float4(mine.m, mine.s, sums.part, sums.mass));
-    if (next < p.N) prepare(next, i + 1);
     const RowStats r = row_stats(p, sh, i, C, lost);
     if (rank == 0 && lane == 0) {
       float loss = r.parts + r.mass * fmaf(base_of(r.all.m) - sums.c, p.inv_temp, logf(r.all.s));
@@ -398,12 +419,11 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
       const float w = weight * p.temp;
       const float f = r.all.s == 0.0f ? 0.0f : w * r.mass / r.all.s;
       E *dst = static_cast<E *>(p.dlogits) + (int64_t)row * p.dlogits_row;
-      const int at = RowSlice<E>(p, row, rank).end_of(p, rank, lane);
       if (at >= 0)
         dst[at] = from_f32<E>(
             r.mass == 0.0f ? 0.0f : f * exp2_sfu((end - base_of(r.all.m)) * p.scale));
-      const Entries e = entries(i);
-      named_wait(1);
+      __syncwarp();  // an entry there is another lane's
+      named_wait(1 + parity);
       if (r.mass != 0.0f)
         for (uint32_t k = lane; k < p.K; k += 32)
           if (e.id[k] >= 0) {
@@ -441,20 +461,22 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
   __shared__ __align__(16) Shared sh;
   const uint32_t rank = cluster_rank(), C = cluster_size();
   const uint32_t stride = gridDim.x / C;  // rows between two of a cluster
-  // the last warp has the entries, the others the rows
-  const uint32_t tid = threadIdx.x, nthr = blockDim.x - 32;
+  // the last two warps have the entries, the others the rows
+  const uint32_t tid = threadIdx.x, nthr = row_threads();
   const int lane = tid & 31, warp = tid >> 5;
   uint4 *slice = reinterpret_cast<uint4 *>(smem);
   if (tid == 0) {
-    barrier_init(&sh.arrived[0]);
-    barrier_init(&sh.arrived[1]);
+    for (int i = 0; i < kPlaces; ++i) barrier_init(&sh.arrived[i]);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   cluster_arrive();  // the others' barriers are there before anything is sent
   cluster_wait();
   if (tid >= nthr) {
-    entry_warp<E, kGrad>(p, sh, reinterpret_cast<float *>(smem + (size_t)p.slice * 16), rank, C,
-                         stride, lane);
+    const uint32_t parity = warp - nthr / 32;
+    float *arrays = reinterpret_cast<float *>(smem + (size_t)p.slice * 16);
+    uint32_t *seen = reinterpret_cast<uint32_t *>(arrays + kEntryWarps * 4 * p.K);
+    entry_warp<E, kGrad>(p, sh, arrays + parity * 4 * p.K, seen + parity * (kSeen / 32),
+                         parity, rank, C, stride, lane);
     return;
   }
 
@@ -529,11 +551,10 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
     }
     acc = warp_join(acc, p.scale);
     // the place was read when the round before the last had its statistics
-    if (!kGrad && i >= 2 && !lost && !barrier_wait(&sh.arrived[i & 1], (i - 2) >> 1 & 1))
-      lost = true;
+    if (!kGrad && i >= 2 && !lost && !stats_wait(sh, i - 2)) lost = true;
     if (lane == 0) sh.warp_stats[i & 1][warp] = make_float2(acc.m, acc.s);
     __syncwarp();
-    named_arrive(2 + (i & 1));
+    named_arrive(3 + (i & 1));
     if (kGrad) {
       const RowStats r = row_stats(p, sh, i, C, lost);
       acc = r.all;
@@ -567,7 +588,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
         }
         copy_commit();
       }
-      named_arrive(1);
+      named_arrive(1 + (i & 1));
     }
     row = next;
   }
@@ -612,11 +633,9 @@ cudaError_t clusters_resident(void (*k)(KArgs...), const cudaLaunchConfig_t &cfg
   return e;
 }
 
-// Shared memory of a block: its slice, the entries, and for the gradient a bit for
-// each of the slice's elements.
-size_t distill_smem(uint32_t slice, uint32_t K, size_t element) {
-  return (size_t)slice * 16 + (size_t)K * 28 +
-         (element ? ((size_t)slice * 16 / element + 31) / 32 * 4 : 0);
+// Shared memory of a block: its slice, and two rows' entries.
+size_t distill_smem(uint32_t slice, uint32_t K, bool grad) {
+  return (size_t)slice * 16 + kEntryWarps * ((size_t)K * 16 + (grad ? kSeen / 8 : 0));
 }
 
 template <class E, bool kGrad>
@@ -625,8 +644,9 @@ cudaError_t launch(DistillParams &p, cudaStream_t st) {
   uint32_t C = 1;
   while (C < kMaxCluster && chunks > C * (kSliceBytes / 16)) C *= 2;
   p.slice = chunks ? (chunks + C - 1) / C : 1;
-  const size_t smem = distill_smem(p.slice, p.K, kGrad ? sizeof(E) : 0);
-  const unsigned threads = p.slice >= 1024 ? kMaxThreads : p.slice >= 256 ? 160 : 96;
+  const size_t smem = distill_smem(p.slice, p.K, kGrad);
+  const unsigned threads =
+      (p.slice >= 1024 ? 256 : p.slice >= 256 ? 128 : 64) + 32 * kEntryWarps;
   auto *k = distill_kernel<E, kGrad>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
