@@ -386,35 +386,44 @@ __global__ void __launch_bounds__(kFinalThreads) __cluster_dims__(kFinalBlocks, 
 }
 
 // ---- backward -------------------------------------------------------------------
-// A lane's R experts of a token from `src`, in pairs; -inf where there is none.
+// A lane's R experts of a token as they lie in memory.
 template <class E, int R>
-__device__ __forceinline__ void load_logits(const E *src, uint32_t i0, uint32_t experts, bool wide,
-                                            Ch<2> (&x)[R / 2]) {
-  constexpr int kN = 16 / sizeof(E);
-  if (wide) {
+struct Piece {
+  static constexpr int kN = 16 / sizeof(E);
+  uint4 v[R / kN];
+  __device__ __forceinline__ void load(const E *src, uint32_t i0, uint32_t experts, bool wide) {
+    if (wide) {
 #pragma unroll
-    for (int r = 0; r < R; r += kN) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      const bool in = i0 + r < experts;
-      if (in) v = *reinterpret_cast<const uint4 *>(src + r);
-      if constexpr (sizeof(E) == 4) {
-        x[r / 2] = {__uint_as_float(v.x), __uint_as_float(v.y)};
-        x[r / 2 + 1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
-      } else {
-        x[r / 2] = widen_pair<E>(v.x), x[r / 2 + 1] = widen_pair<E>(v.y);
-        x[r / 2 + 2] = widen_pair<E>(v.z), x[r / 2 + 3] = widen_pair<E>(v.w);
-      }
-      if (!in) {
+      for (int r = 0; r < R; r += kN)
+        if (i0 + r < experts) v[r / kN] = *reinterpret_cast<const uint4 *>(src + r);
+    } else {
 #pragma unroll
-        for (int q = 0; q < kN; ++q) x[(r + q) / 2].v[(r + q) % 2] = kNegInf;
+      for (int r = 0; r < R; r += kN) {
+        E x[kN];
+#pragma unroll
+        for (int q = 0; q < kN; ++q)
+          x[q] = i0 + r + q < experts ? src[r + q] : from_f32<E>(0.0f);
+        v[r / kN] = *reinterpret_cast<const uint4 *>(x);
       }
     }
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      x[r / 2].v[r % 2] = i0 + r < experts ? to_f32(src[r]) : kNegInf;
   }
-}
+  // In pairs; -inf where there is no expert.
+  __device__ __forceinline__ void widen(uint32_t i0, uint32_t experts, bool wide,
+                                        Ch<2> (&x)[R / 2]) const {
+#pragma unroll
+    for (int r = 0; r < R; r += kN) {
+      Ch<2> y[kN / 2];
+      widen_chunk<E>(v[r / kN], y);
+#pragma unroll
+      for (int q = 0; q < kN / 2; ++q) x[r / 2 + q] = y[q];
+      if (i0 + r + kN > experts) {  // the last experts: none, or (not wide) some
+#pragma unroll
+        for (int q = 0; q < kN; ++q)
+          if (i0 + r + q >= experts) x[(r + q) / 2].v[(r + q) % 2] = kNegInf;
+      }
+    }
+  }
+};
 template <class E, int R>
 __device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t experts, bool wide,
                                              const Ch<2> (&d)[R / 2]) {
@@ -422,14 +431,10 @@ __device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t exper
   if (wide) {
 #pragma unroll
     for (int r = 0; r < R; r += kN) {
-      uint4 v;
-      if constexpr (sizeof(E) == 4)
-        v = make_uint4(__float_as_uint(d[r / 2].v[0]), __float_as_uint(d[r / 2].v[1]),
-                       __float_as_uint(d[r / 2 + 1].v[0]), __float_as_uint(d[r / 2 + 1].v[1]));
-      else
-        v = make_uint4(narrow_pair<E>(d[r / 2]), narrow_pair<E>(d[r / 2 + 1]),
-                       narrow_pair<E>(d[r / 2 + 2]), narrow_pair<E>(d[r / 2 + 3]));
-      if (i0 + r < experts) *reinterpret_cast<uint4 *>(dst + r) = v;
+      Ch<2> y[kN / 2];
+#pragma unroll
+      for (int q = 0; q < kN / 2; ++q) y[q] = d[r / 2 + q];
+      if (i0 + r < experts) *reinterpret_cast<uint4 *>(dst + r) = narrow_chunk<E>(y);
     }
   } else {
 #pragma unroll
@@ -439,7 +444,7 @@ __device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t exper
 }
 
 template <class E, int L, int R>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) route_backward_kernel(const RouteParams p) {
   constexpr int G = 32 / L, kExperts = L * R, kP = R / 2;
   // the weights' part of a token's gradient, 0 but where it has one; four floats
   // more a token keep the lanes' 16-byte reads off each other's banks
@@ -457,27 +462,47 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RoutePar
   }
   __syncwarp();
   const uint32_t step = gridDim.x * kWarps * G;
-  uint64_t n0 = ((uint64_t)blockIdx.x * kWarps + warp) * G;
-  const E *src = static_cast<const E *>(p.logits) + (int64_t)(n0 + group) * p.logits_row + i0;
-  E *dst = static_cast<E *>(p.dlogits) + (int64_t)(n0 + group) * p.E + i0;
-  for (; n0 < p.N; n0 += step, src += (int64_t)step * p.logits_row, dst += (int64_t)step * p.E) {
-    const bool in = n0 + group < p.N;
-    const uint32_t n = in ? (uint32_t)n0 + group : 0;
-    const bool real = in && !(p.doc && __ldg(p.doc + n) < 0);
+  const uint64_t n_first = ((uint64_t)blockIdx.x * kWarps + warp) * G + group;
+  const E *src = static_cast<const E *>(p.logits) + (int64_t)n_first * p.logits_row + i0;
+  E *dst = static_cast<E *>(p.dlogits) + (int64_t)n_first * p.E + i0;
+  auto counts = [&](uint64_t n) { return n < p.N && !(p.doc && __ldg(p.doc + n) < 0); };
+  bool next_real = counts(n_first);
+  Piece<E, R> next;
+  if (next_real) next.load(src, i0, p.E, p.wide);
+  // A lane has one of the token's choices at most, or goes through several.
+  const bool one = p.k <= (uint32_t)L;
+  int next_id = -1;  // -1: there is no such choice
+  float next_w = 0.0f, next_dw = 0.0f;
+  auto load_choice = [&](uint64_t n) {
+    next_id = -1;
+    if (next_real && p.d_weights && one && gl < (int)p.k) {
+      const uint32_t at = (uint32_t)n * p.k + gl;  // below 2^31
+      next_id = p.ids[at], next_w = p.weights[at], next_dw = p.d_weights[at];
+    }
+  };
+  load_choice(n_first);
+  for (uint64_t n0 = n_first - group; n0 < p.N;) {
+    const uint64_t n = n0 + group;
+    const bool in = n < p.N, real = next_real;
     Ch<2> x[kP];
-    if (real) {
-      load_logits<E, R>(src, i0, p.E, p.wide, x);
-    } else {
+    next.widen(i0, p.E, p.wide, x);
+    if (!real) {
 #pragma unroll
       for (int r = 0; r < kP; ++r) x[r] = splat<2>(kNegInf);
     }
-    const uint32_t at = n * p.k;  // below 2^31
     // w = p at the chosen ones: dl_j = w_j dw_j - p_j t at them, t = sum w dw;
-    // normalised, w is their own softmax: dl_j = w_j (dw_j - t)
-    float t = 0.0f;
-    if (p.d_weights) {
-      for (uint32_t j = gl; real && j < p.k; j += L)
-        if (p.ids[at + j] >= 0) t += p.weights[at + j] * p.d_weights[at + j];  // -1: no choice
+    // normalised, w is their own softmax: dl_j = w_j (dw_j - t).
+    const int id = next_id;
+    const float w = next_w, dw = next_dw;
+    n0 += step, src += (int64_t)step * p.logits_row;
+    next_real = counts(n0 + group);
+    if (next_real) next.load(src, i0, p.E, p.wide);
+    load_choice(n0 + group);
+    const uint32_t at = real ? (uint32_t)n * p.k : 0;
+    float t = id >= 0 ? w * dw : 0.0f;
+    if (p.d_weights && real && !one) {
+      for (uint32_t j = gl; j < p.k; j += L)
+        if (p.ids[at + j] >= 0) t += p.weights[at + j] * p.d_weights[at + j];
     }
     float m = kNegInf;
 #pragma unroll
@@ -497,35 +522,44 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RoutePar
     for (int o = L / 2; o > 0; o >>= 1) {
       s += __shfl_xor_sync(0xffffffffu, s, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (p.d_weights) t += __shfl_xor_sync(0xffffffffu, t, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
     }
+    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s), mean = p.normalize ? t : 0.0f;
     if (p.d_weights) {
-      for (uint32_t j = gl; real && j < p.k; j += L) {
-        const int id = p.ids[at + j];
-        if (id >= 0 && id < (int)p.E)
-          my_add[place(id)] = p.weights[at + j] * (p.d_weights[at + j] - (p.normalize ? t : 0.0f));
+      if (one) {
+        if (id >= 0 && id < (int)p.E) my_add[place(id)] = w * (dw - mean);
+      } else if (real) {
+        for (uint32_t j = gl; j < p.k; j += L) {
+          const int e = p.ids[at + j];
+          if (e >= 0 && e < (int)p.E)
+            my_add[place(e)] = p.weights[at + j] * (p.d_weights[at + j] - mean);
+        }
       }
       __syncwarp();
     }
-    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s);
     dot = fmaf(dot, inv, p.normalize ? 0.0f : t);
     const Ch<2> inv2 = splat<2>(inv), minus = splat<2>(-dot);
 #pragma unroll
     for (int r = 0; r < kP; r += 2) {
-      const float4 w = *reinterpret_cast<const float4 *>(my_add + place(i0) + 2 * r);
-      x[r] = fma(x[r] * inv2, g[r] + minus, Ch<2>{w.x, w.y});
-      x[r + 1] = fma(x[r + 1] * inv2, g[r + 1] + minus, Ch<2>{w.z, w.w});
+      const float4 v = *reinterpret_cast<const float4 *>(my_add + place(i0) + 2 * r);
+      x[r] = fma(x[r] * inv2, g[r] + minus, Ch<2>{v.x, v.y});
+      x[r + 1] = fma(x[r + 1] * inv2, g[r + 1] + minus, Ch<2>{v.z, v.w});
     }
     if (s == 0.0f) {  // the token counts for nothing
 #pragma unroll
       for (int r = 0; r < kP; ++r) x[r] = splat<2>(0.0f);
     }
     if (in) store_logits<E, R>(dst, i0, p.E, p.wide, x);
+    dst += (int64_t)step * p.E;
     if (p.d_weights) {
       __syncwarp();
-      for (uint32_t j = gl; real && j < p.k; j += L) {
-        const int id = p.ids[at + j];
+      if (one) {
         if (id >= 0 && id < (int)p.E) my_add[place(id)] = 0.0f;
+      } else if (real) {
+        for (uint32_t j = gl; j < p.k; j += L) {
+          const int e = p.ids[at + j];
+          if (e >= 0 && e < (int)p.E) my_add[place(e)] = 0.0f;
+        }
       }
       __syncwarp();
     }
