@@ -39,7 +39,8 @@ struct RouteParams {
   int64_t logits_row;
   const int32_t *doc;
   uint32_t N, E, k;
-  int32_t normalize, wide;  // wide: a lane's experts can be moved at once
+  int32_t normalize;
+  int32_t wide;  // bytes of a row that can be moved at once: 16, 8, 4, or 0 for two
   int32_t *ids;
   float *weights;
   // forward
@@ -73,37 +74,65 @@ __device__ __forceinline__ float balance(uint32_t E, uint32_t k, int32_t M) {
 }
 
 // ---- forward ------------------------------------------------------------------
-// A tile's logits into shared memory, as floats: token n0 + row's expert e at
-// row `row * lanes + e / SG`, place e % SG.  `tokens` of them are inside the call.
+// A thread's pieces of a tile of `per` pieces a row, kForwardThreads apart: the row
+// and the place move on without a division.
+template <class E>
+struct Walk {
+  uint32_t row, at, rows, rest, per;
+  const E *from;
+  int64_t step, wrap;
+  __device__ __forceinline__ Walk(const RouteParams &p, uint64_t n0, uint32_t pieces,
+                                  uint32_t size) {
+    per = pieces, rows = kForwardThreads / per, rest = kForwardThreads % per;
+    row = threadIdx.x / per, at = threadIdx.x % per;
+    from = static_cast<const E *>(p.logits) + (int64_t)(n0 + row) * p.logits_row + at * size;
+    step = (int64_t)rows * p.logits_row + rest * size;
+    wrap = p.logits_row - (int64_t)per * size;
+  }
+  __device__ __forceinline__ void next() {
+    row += rows, at += rest, from += step;
+    if (at >= per) at -= per, ++row, from += wrap;
+  }
+};
+
+// A tile's logits into shared memory as they are: token n0 + row's expert e at row
+// `row * lanes + e / SG`, place e % SG.  `tokens` of them are inside the call.  A
+// row of 16-bit logits takes the second half of its room of floats: its thread
+// widens it in place, from the front.
+template <class E, int kBytes, int SG, int kPitch>
+__device__ __forceinline__ void copy_pieces(const RouteParams &p, uint64_t n0, uint32_t tokens,
+                                            float *tile) {
+  constexpr int kN = kBytes / sizeof(E);
+  for (Walk<E> w(p, n0, p.E / kN, kN); w.row < tokens; w.next()) {
+    const uint32_t e = w.at * kN;
+    E *row = reinterpret_cast<E *>(tile + (w.row * p.lanes + e / SG) * kPitch +
+                                   (sizeof(E) == 2 ? SG / 2 : 0));
+    copy_async<kBytes>(row + e % SG, w.from);
+  }
+}
 template <class E, int SG, int kPitch>
 __device__ __forceinline__ void load_tile(const RouteParams &p, uint64_t n0, uint32_t tokens,
                                           float *tile) {
-  // A thread's pieces are kForwardThreads apart: the row and the place move on
-  // without a division.
-  constexpr int kN = 16 / sizeof(E);
-  const uint32_t per = p.wide ? p.E / kN : p.E, size = p.wide ? kN : 1;  // pieces a row
-  const uint32_t rows = kForwardThreads / per, rest = kForwardThreads % per;
-  uint32_t row = threadIdx.x / per, at = threadIdx.x % per;
-  const E *from =
-      static_cast<const E *>(p.logits) + (int64_t)(n0 + row) * p.logits_row + at * size;
-  const int64_t step = (int64_t)rows * p.logits_row + rest * size,
-                wrap = p.logits_row - (int64_t)per * size;
-  while (row < tokens) {
-    const uint32_t e = at * size;
-    float *to = tile + row * (p.lanes * kPitch) + e + e / SG * (kPitch - SG);
-    if (!p.wide) {
-      *to = to_f32(*from);
-    } else if constexpr (sizeof(E) == 4) {
-      copy_async<16>(to, from);
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4 *>(from);
-      const Ch<2> a = widen_pair<E>(v.x), b = widen_pair<E>(v.y), c = widen_pair<E>(v.z),
-                  d = widen_pair<E>(v.w);
-      reinterpret_cast<float4 *>(to)[0] = make_float4(a.v[0], a.v[1], b.v[0], b.v[1]);
-      reinterpret_cast<float4 *>(to)[1] = make_float4(c.v[0], c.v[1], d.v[0], d.v[1]);
+  if (p.wide == 16) {
+    copy_pieces<E, 16, SG, kPitch>(p, n0, tokens, tile);
+  } else if (p.wide == 8) {
+    copy_pieces<E, 8, SG, kPitch>(p, n0, tokens, tile);
+  } else if (p.wide == 4) {
+    copy_pieces<E, 4, SG, kPitch>(p, n0, tokens, tile);
+  } else if constexpr (sizeof(E) == 2) {  // no asynchronous copy takes two bytes
+    constexpr int kFlight = 8;
+    Walk<E> load(p, n0, p.E, 1), store = load;
+    while (load.row < tokens) {
+      E v[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i, load.next())
+        if (load.row < tokens) v[i] = *load.from;
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i, store.next())
+        if (store.row < tokens)
+          reinterpret_cast<E *>(tile + (store.row * p.lanes + store.at / SG) * kPitch +
+                                SG / 2)[store.at % SG] = v[i];
     }
-    row += rows, at += rest, from += step;
-    if (at >= per) at -= per, ++row, from += wrap;
   }
   copy_commit();
   copy_wait<0>();
@@ -115,6 +144,17 @@ __device__ __forceinline__ void load_group(const float *at, float (&v)[S]) {
   for (int q = 0; q < S; q += 4) {
     const float4 x = *reinterpret_cast<const float4 *>(at + q);
     v[q] = x.x, v[q + 1] = x.y, v[q + 2] = x.z, v[q + 3] = x.w;
+  }
+}
+
+template <class E, int S>
+__device__ __forceinline__ void load_narrow(const float *at, float (&v)[S]) {
+#pragma unroll
+  for (int q = 0; q < S; q += 8) {
+    Ch<2> x[4];
+    widen_chunk<E>(*reinterpret_cast<const uint4 *>(at + q / 2), x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[q + i] = x[i / 2].v[i % 2];
   }
 }
 
@@ -168,9 +208,8 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     else load_tile<__half, SG, kPitch>(p, n0, here, tile);
     const bool real = token < here && !(p.doc && __ldg(p.doc + n0 + token) < 0);
     __syncthreads();
-    // places beyond the last expert, and all of a token that does not count
+    // beyond are places beyond the last expert, and all of a token that does not count
     const int used = !real || p.E <= lp * SG ? 0 : (int)min(p.E - lp * SG, (uint32_t)SG);
-    for (int i = used; i < SG; ++i) mine[i] = kNegInf;
 
     // The k largest: by groups.  NaN is below everything (a maximum leaves it out).
     float top[G];
@@ -178,7 +217,23 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float v[S];
-      load_group<S>(mine + g * S, v);
+      if (p.dtype == NS_F32)
+        load_group<S>(mine + g * S, v);
+      else if (p.dtype == NS_BF16)
+        load_narrow<__nv_bfloat16, S>(mine + SG / 2 + g * S / 2, v);
+      else
+        load_narrow<__half, S>(mine + SG / 2 + g * S / 2, v);
+      if (used < SG) {
+#pragma unroll
+        for (int q = 0; q < S; ++q)
+          if (g * S + q >= used) v[q] = kNegInf;
+      }
+      if (used < SG || p.dtype != NS_F32) {
+#pragma unroll
+        for (int q = 0; q < S; q += 4)
+          *reinterpret_cast<float4 *>(mine + g * S + q) =
+              make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+      }
       top[g] = kNegInf;
 #pragma unroll
       for (int q = 0; q < S; ++q) top[g] = fmaxf(top[g], v[q]);
@@ -391,32 +446,39 @@ template <class E, int R>
 struct Piece {
   static constexpr int kN = 16 / sizeof(E);
   uint4 v[R / kN];
-  __device__ __forceinline__ void load(const E *src, uint32_t i0, uint32_t experts, bool wide) {
-    if (wide) {
+  __device__ __forceinline__ void load(const E *src, uint32_t i0, uint32_t experts, int wide) {
 #pragma unroll
-      for (int r = 0; r < R; r += kN)
-        if (i0 + r < experts) v[r / kN] = *reinterpret_cast<const uint4 *>(src + r);
-    } else {
-#pragma unroll
-      for (int r = 0; r < R; r += kN) {
+    for (int r = 0; r < R; r += kN) {
+      uint4 &to = v[r / kN];
+      if (wide == 16) {
+        if (i0 + r < experts) to = *reinterpret_cast<const uint4 *>(src + r);
+      } else if (wide == 8) {
+        if (i0 + r < experts) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(src + r);
+          to.x = x.x, to.y = x.y;
+        }
+        if (i0 + r + kN / 2 < experts) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(src + r + kN / 2);
+          to.z = x.x, to.w = x.y;
+        }
+      } else {
         E x[kN];
 #pragma unroll
         for (int q = 0; q < kN; ++q)
           x[q] = i0 + r + q < experts ? src[r + q] : from_f32<E>(0.0f);
-        v[r / kN] = *reinterpret_cast<const uint4 *>(x);
+        to = *reinterpret_cast<const uint4 *>(x);
       }
     }
   }
   // In pairs; -inf where there is no expert.
-  __device__ __forceinline__ void widen(uint32_t i0, uint32_t experts, bool wide,
-                                        Ch<2> (&x)[R / 2]) const {
+  __device__ __forceinline__ void widen(uint32_t i0, uint32_t experts, Ch<2> (&x)[R / 2]) const {
 #pragma unroll
     for (int r = 0; r < R; r += kN) {
       Ch<2> y[kN / 2];
       widen_chunk<E>(v[r / kN], y);
 #pragma unroll
       for (int q = 0; q < kN / 2; ++q) x[r / 2 + q] = y[q];
-      if (i0 + r + kN > experts) {  // the last experts: none, or (not wide) some
+      if (i0 + r + kN > experts) {  // the last experts: some, or none
 #pragma unroll
         for (int q = 0; q < kN; ++q)
           if (i0 + r + q >= experts) x[(r + q) / 2].v[(r + q) % 2] = kNegInf;
@@ -425,21 +487,28 @@ struct Piece {
   }
 };
 template <class E, int R>
-__device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t experts, bool wide,
+__device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t experts, int wide,
                                              const Ch<2> (&d)[R / 2]) {
   constexpr int kN = 16 / sizeof(E);
-  if (wide) {
 #pragma unroll
-    for (int r = 0; r < R; r += kN) {
-      Ch<2> y[kN / 2];
+  for (int r = 0; r < R; r += kN) {
+    Ch<2> y[kN / 2];
 #pragma unroll
-      for (int q = 0; q < kN / 2; ++q) y[q] = d[r / 2 + q];
-      if (i0 + r < experts) *reinterpret_cast<uint4 *>(dst + r) = narrow_chunk<E>(y);
+    for (int q = 0; q < kN / 2; ++q) y[q] = d[r / 2 + q];
+    const uint4 v = narrow_chunk<E>(y);
+    if (wide == 16) {
+      if (i0 + r < experts) *reinterpret_cast<uint4 *>(dst + r) = v;
+    } else if (wide == 8) {
+      if (i0 + r < experts) *reinterpret_cast<uint2 *>(dst + r) = make_uint2(v.x, v.y);
+      if (i0 + r + kN / 2 < experts)
+        *reinterpret_cast<uint2 *>(dst + r + kN / 2) = make_uint2(v.z, v.w);
+    } else {
+      E x[kN];
+      *reinterpret_cast<uint4 *>(x) = v;
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        if (i0 + r + q < experts) dst[r + q] = x[q];
     }
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i0 + r < experts) dst[r] = from_f32<E>(d[r / 2].v[r % 2]);
   }
 }
 
@@ -485,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
     const uint64_t n = n0 + group;
     const bool in = n < p.N, real = next_real;
     Ch<2> x[kP];
-    next.widen(i0, p.E, p.wide, x);
+    next.widen(i0, p.E, x);
     if (!real) {
 #pragma unroll
       for (int r = 0; r < kP; ++r) x[r] = splat<2>(kNegInf);
@@ -632,10 +701,13 @@ RouteParams params_of(const ns_route_inputs &in) {
   return p;
 }
 
-// Whether rows of `experts` can be moved 16 bytes at a time.
-bool whole_sixteens(const ns_route_inputs &in) {
-  const size_t es = in.dtype == NS_F32 ? 4 : 2;
-  return (uintptr_t)in.logits % 16 == 0 && (in.logits_row * es) % 16 == 0 && in.E * es % 16 == 0;
+// Bytes that rows can be moved by: 16, 8 or 4 where addresses, strides and widths
+// are multiples of them, else 0.
+int moved_at_once(const ns_route_inputs &in, const void *dlogits) {
+  const uint64_t es = in.dtype == NS_F32 ? 4 : 2;
+  const uint64_t all = (uint64_t)(uintptr_t)in.logits | (uint64_t)(uintptr_t)dlogits |
+                       (uint64_t)in.logits_row * es | in.E * es;
+  return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 0;
 }
 
 }  // namespace
@@ -652,7 +724,7 @@ cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float 
                                  cudaStream_t st) {
   RouteParams p = params_of(in);
   const Shape shape = shape_of(in.E);
-  p.wide = whole_sixteens(in), p.lanes = shape.lanes;
+  p.wide = moved_at_once(in, nullptr), p.lanes = shape.lanes;
   p.ids = ids, p.weights = weights, p.counts = counts, p.tokens = tokens, p.loss = loss;
   p.blocks = route_blocks(in.N, in.E);
   p.mass = static_cast<float *>(workspace);
@@ -677,8 +749,7 @@ cudaError_t launch_route_backward(const ns_route_inputs &in, const int32_t *ids,
   p.ids = const_cast<int32_t *>(ids), p.weights = const_cast<float *>(weights);
   p.counts = const_cast<int32_t *>(counts), p.tokens = const_cast<int32_t *>(tokens);
   p.d_weights = d_weights, p.d_loss = d_loss, p.dlogits = dlogits;
-  // a lane's experts are whole pieces of 16 bytes, or none
-  p.wide = whole_sixteens(in) && (uintptr_t)dlogits % 16 == 0;
+  p.wide = moved_at_once(in, dlogits);
   switch (in.dtype) {
     case NS_F32: return backward_of<float>(p, st);
     case NS_BF16: return backward_of<__nv_bfloat16>(p, st);
