@@ -624,8 +624,7 @@ cudaError_t clusters_resident(void (*k)(KArgs...), const cudaLaunchConfig_t &cfg
       return cudaSuccess;
     }
   }
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)cfg.dynamicSmemBytes);
+  e = allow_shared_memory((const void *)k);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(n, k, &cfg);
   if (e == cudaSuccess && *n < 1) e = cudaErrorLaunchOutOfResources;
   if (e == cudaSuccess)
@@ -665,13 +664,6 @@ cudaError_t launch(DistillParams &p, cudaStream_t st) {
   if (e != cudaSuccess) {
     cudaGetLastError();
     return e;
-  }
-  if (smem > 48 * 1024) {  // another layout may have asked for less since
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
   }
   cfg.gridDim = dim3(C * (p.N < (uint32_t)resident ? p.N : (uint32_t)resident));
   ++launch_counter();

@@ -33,6 +33,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kForwardThreads = 128;
 constexpr uint32_t kSMs = 152;
+constexpr int kTogether = 8;  // blocks of a cluster
 
 struct RouteParams {
   const void *logits;
@@ -52,6 +53,7 @@ struct RouteParams {
   int32_t *counts, *tokens;
   float *loss;
   uint32_t blocks;
+  bool together;    // the blocks are one cluster
   // backward
   const float *d_weights, *d_loss;
   void *dlogits;
@@ -147,6 +149,11 @@ __device__ __forceinline__ void load_group(const float *at, float (&v)[S]) {
   }
 }
 
+__device__ __forceinline__ void load_pairs(const float *at, Ch<2> (&x)[4]) {
+  const float4 a = reinterpret_cast<const float4 *>(at)[0],
+               b = reinterpret_cast<const float4 *>(at)[1];
+  x[0] = {a.x, a.y}, x[1] = {a.z, a.w}, x[2] = {b.x, b.y}, x[3] = {b.z, b.w};
+}
 template <class E, int S>
 __device__ __forceinline__ void load_narrow(const float *at, float (&v)[S]) {
 #pragma unroll
@@ -186,7 +193,10 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
   int *chosen = reinterpret_cast<int *>(inv + kForwardThreads);     // [columns]
   float *top_x = reinterpret_cast<float *>(chosen + columns);       // [tokens][k]: logit, weight
   int *top_id = reinterpret_cast<int *>(top_x + tokens * p.k);      // [tokens][k]
-  __shared__ int real_tokens;
+  // in a cluster, the first block's: the others' sums and counts, and tokens
+  float2 *gathered = reinterpret_cast<float2 *>(top_id + tokens * p.k);
+  __shared__ int real_tokens, real_of[kTogether];
+  if (p.together) cluster_arrive_relaxed();
   const uint32_t tid = threadIdx.x, lane = tid & 31, token = tid / LP, lp = tid % LP;
   float *mine = tile + tid * kPitch;
   for (uint32_t e = tid; e < columns; e += kForwardThreads) chosen[e] = 0;
@@ -292,19 +302,31 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     // Exponentials in the logits' place, and their sum.  The difference is taken
     // before the change of base, which overflows near the type's lowest value.
     const float base = m == kNegInf ? 0.0f : m;
-    Ch<2> s2 = splat<2>(0.0f);
-#pragma unroll 4
-    for (int i = 0; i < SG; i += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(mine + i);
-      Ch<2> a = (Ch<2>{x.x, x.y} + splat<2>(-base)) * splat<2>(kLog2e);
-      Ch<2> b = (Ch<2>{x.z, x.w} + splat<2>(-base)) * splat<2>(kLog2e);
-      a = {exp2_sfu(a.v[0]), exp2_sfu(a.v[1])};
-      b = {exp2_sfu(b.v[0]), exp2_sfu(b.v[1])};
-      s2 = s2 + (a + b);
-      *reinterpret_cast<float4 *>(mine + i) = make_float4(a.v[0], a.v[1], b.v[0], b.v[1]);
+    // The sum is that of every eight experts, and of those by pairs of neighbours: the
+    // same whatever the number of threads.
+    float part[SG / 8];
+#pragma unroll
+    for (int i = 0; i < SG; i += 8) {
+      Ch<2> x[4], sum;
+      load_pairs(mine + i, x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const Ch<2> y = (x[q] + splat<2>(-base)) * splat<2>(kLog2e);
+        x[q] = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+        sum = q == 0 ? x[q] : sum + x[q];
+      }
+      *reinterpret_cast<float4 *>(mine + i) =
+          make_float4(x[0].v[0], x[0].v[1], x[1].v[0], x[1].v[1]);
+      *reinterpret_cast<float4 *>(mine + i + 4) =
+          make_float4(x[2].v[0], x[2].v[1], x[3].v[0], x[3].v[1]);
+      part[i / 8] = sum.v[0] + sum.v[1];
     }
-    float s = s2.v[0] + s2.v[1];
-    for (uint32_t o = LP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+    for (int n = 1; n < SG / 8; n *= 2)
+#pragma unroll
+      for (int i = 0; i < SG / 8; i += 2 * n) part[i] += part[i + n];
+    float s = part[0];
+    for (uint32_t o = 1; o < LP; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float by_all = s == 0.0f ? 0.0f : 1.0f / s;
     if (lp == 0) {
       inv[token] = by_all;
@@ -312,9 +334,10 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     }
     __syncwarp();  // the token's threads have written their choices
     float total = 0.0f;
-    for (uint32_t j = lp; j < p.k; j += LP)
-      total += exp2_sfu((top_x[token * p.k + j] - base) * kLog2e);
-    for (uint32_t o = LP / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (p.normalize)  // every thread in the choices' order
+      for (uint32_t j = 0; j < p.k; ++j)
+        total += exp2_sfu((top_x[token * p.k + j] - base) * kLog2e);
+    __syncwarp();  // before the weights take the logits' places
     // a NaN logit is never chosen, but makes s and so the token's weights NaN
     const float by =
         p.normalize ? (total == 0.0f ? 0.0f : 1.0f / total) + (s - s) : by_all;
@@ -329,7 +352,7 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
       p.weights[n0 * p.k + i] = top_x[i];
     }
     const float *column = tile + (tid % side) / SG * kPitch + (tid % side) % SG;
-    if (SG < kForwardThreads || per_thread == 1)
+    if (per_thread == 1)
       add_columns<1, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
     else if (per_thread == 2)
       add_columns<2, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
@@ -346,29 +369,48 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
   for (int i = 0; i < kMaxColumns; ++i)
     if (i < (int)per_thread) tile[my_part * columns + tid % side + i * kForwardThreads] = sum[i];
   __syncthreads();
-  float part = 0.0f;
+  const uint32_t rank = p.together ? cluster_rank() : 0;
+  if (p.together) cluster_wait();  // the first block runs
   for (uint32_t e = tid; e < p.E; e += kForwardThreads) {
     float v = tile[e];
     for (uint32_t q = 1; q < parts; ++q) v += tile[q * columns + e];
-    if (p.blocks == 1) {
-      p.counts[e] = chosen[e];
-      part += v * (float)chosen[e];
+    if (p.together) {
+      remote_store(remote_smem(&gathered[rank * p.E + e], 0),
+                   make_float2(v, __int_as_float(chosen[e])));
     } else {
       p.mass[(uint64_t)blockIdx.x * p.E + e] = v;
       p.chosen[(uint64_t)blockIdx.x * p.E + e] = chosen[e];
     }
   }
-  if (p.blocks == 1) {  // few tokens: this block has all of them
-    part = group_sum<32>(part);
-    if (lane == 0) inv[tid / 32] = part;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kForwardThreads / 32; ++w) part += inv[w];
-      p.tokens[0] = real_tokens;
-      p.loss[0] = part * balance(p.E, p.k, real_tokens);
+  if (!p.together) {
+    if (tid == 0) p.real[blockIdx.x] = real_tokens;
+    return;
+  }
+  if (tid == 0) remote_store(remote_smem(&real_of[rank], 0), __int_as_float(real_tokens));
+  cluster_arrive();
+  cluster_wait();
+  if (rank != 0) return;
+  // few tokens: the first block of the cluster adds everything up
+  float part = 0.0f;
+  for (uint32_t e = tid; e < p.E; e += kForwardThreads) {
+    float v = 0.0f;
+    int n = 0;
+    for (uint32_t q = 0; q < gridDim.x; ++q) {
+      v += gathered[q * p.E + e].x;
+      n += __float_as_int(gathered[q * p.E + e].y);
     }
-  } else if (tid == 0) {
-    p.real[blockIdx.x] = real_tokens;
+    p.counts[e] = n;
+    part += v * (float)n;
+  }
+  part = group_sum<32>(part);
+  if (lane == 0) inv[tid / 32] = part;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kForwardThreads / 32; ++w) part += inv[w];
+    int real = 0;
+    for (uint32_t q = 0; q < gridDim.x; ++q) real += real_of[q];
+    p.tokens[0] = real;
+    p.loss[0] = part * balance(p.E, p.k, real);
   }
 }
 
@@ -635,41 +677,58 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
   }
 }
 
-// The forward kernel's groups and threads a token: 64 experts a thread, in groups
-// of eight, for up to 128 experts; 128 a thread, in groups of 16, beyond.  (262144
-// tokens in bfloat16: 128 experts 98 us with 64 a thread, 141 us with 128; 256
-// experts 176 us and 150 us.  Fewer a thread leave room for more threads an SM, but
-// each of a token's threads goes through every choice.)
+// The forward kernel's groups and threads a token.  With tokens enough to fill the
+// GPU: 64 experts a thread, in groups of eight, for up to 128 experts; 128 a thread,
+// in groups of 16, beyond.  (262144 tokens in bfloat16: 128 experts 98 us with 64 a
+// thread, 141 us with 128; 256 experts 176 us and 150 us.  Fewer a thread leave room
+// for more threads an SM, but each of a token's threads goes through every choice.)
+// With few tokens what counts is how long one takes: eight experts a thread.
 struct Shape {
   int S, G;
   uint32_t lanes;
+  uint64_t tiles;
 };
-Shape shape_of(uint32_t E) {
-  if (E <= 8) return {8, 1, 1};
-  if (E <= 16) return {8, 2, 1};
-  if (E <= 32) return {8, 4, 1};
-  if (E <= 64) return {8, 8, 1};
-  if (E <= 128) return {8, 8, 2};
-  uint32_t lanes = 2;
-  while (lanes * 128 < E) lanes *= 2;
-  return {16, 8, lanes};
+Shape shape_of(uint32_t N, uint32_t E) {
+  uint32_t eights = 1;  // groups of eight, a power of two
+  while (eights * 8 < E) eights *= 2;
+  Shape s = {8, (int)(eights < 8 ? eights : 8), eights <= 8 ? 1u : 2u, 0};
+  if (eights > 16) s = {16, 8, eights / 16, 0};
+  uint32_t tokens = kForwardThreads / s.lanes;
+  s.tiles = ((uint64_t)N + tokens - 1) / tokens;
+  if (s.tiles < kSMs) {
+    s = {8, eights <= 32 ? 1 : (int)(eights / 32), eights <= 32 ? eights : 32, 0};
+    tokens = kForwardThreads / s.lanes;
+    s.tiles = ((uint64_t)N + tokens - 1) / tokens;
+  }
+  return s;
 }
 
 template <int S, int G>
 cudaError_t launch_forward(RouteParams &p, cudaStream_t st) {
   const size_t tokens = kForwardThreads / p.lanes;
-  const size_t smem = 4 * (kForwardThreads * (size_t)(S * G + 4) + kForwardThreads +
-                           p.lanes * S * G + 2 * tokens * p.k);
+  size_t smem = 4 * (kForwardThreads * (size_t)(S * G + 4) + kForwardThreads +
+                     p.lanes * S * G + 2 * tokens * p.k);
+  smem = (smem + 15) / 16 * 16;  // the sums of a cluster's blocks start at a whole pair
+  if (p.together) smem += 8 * (size_t)p.blocks * p.E;
   auto *k = route_forward_kernel<S, G>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return e;
-  }
+  cudaError_t e = allow_shared_memory((const void *)k);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.blocks);
+  cfg.blockDim = dim3(kForwardThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = p.blocks;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.together ? 1 : 0;
   ++launch_counter();
-  k<<<p.blocks, kForwardThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  e = cudaLaunchKernelEx(&cfg, k, (const RouteParams)p);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
 }
 
 // A token's lanes backward, R experts each.
@@ -713,20 +772,23 @@ int moved_at_once(const ns_route_inputs &in, const void *dlogits) {
 }  // namespace
 
 uint32_t route_blocks(uint32_t N, uint32_t E) {
-  const uint32_t tokens = kForwardThreads / shape_of(E).lanes;
-  const uint64_t tiles = ((uint64_t)N + tokens - 1) / tokens;
-  // up to two tiles, one block does without the second kernel
-  return tiles <= 2 ? 1 : tiles < 3 * kSMs ? (uint32_t)tiles : 3 * kSMs;
+  const uint64_t tiles = shape_of(N, E).tiles;
+  // up to two tiles a block, one cluster does without the second kernel
+  if (tiles <= 2 * kTogether) return 0;
+  return tiles < 3 * kSMs ? (uint32_t)tiles : 3 * kSMs;
 }
 
 cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float *weights,
                                  int32_t *counts, int32_t *tokens, float *loss, void *workspace,
                                  cudaStream_t st) {
   RouteParams p = params_of(in);
-  const Shape shape = shape_of(in.E);
+  const Shape shape = shape_of(in.N, in.E);
   p.wide = moved_at_once(in, nullptr), p.lanes = shape.lanes;
   p.ids = ids, p.weights = weights, p.counts = counts, p.tokens = tokens, p.loss = loss;
   p.blocks = route_blocks(in.N, in.E);
+  p.together = p.blocks == 0;
+  if (p.together) p.blocks = shape.tiles < kTogether ? (uint32_t)shape.tiles : kTogether;
+  if (p.blocks == 0) p.blocks = 1;  // no token: the counts are still written
   p.mass = static_cast<float *>(workspace);
   p.chosen = reinterpret_cast<int32_t *>(p.mass + (uint64_t)p.blocks * in.E);
   p.real = p.chosen + (uint64_t)p.blocks * in.E;
@@ -735,7 +797,7 @@ cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float 
                         : shape.G == 4 ? launch_forward<8, 4>(p, st)
                         : shape.G == 2 ? launch_forward<8, 2>(p, st)
                                        : launch_forward<8, 1>(p, st);
-  if (e != cudaSuccess || p.blocks == 1) return e;
+  if (e != cudaSuccess || p.together) return e;
   ++launch_counter();
   pdl_launch(route_total_kernel, dim3(kFinalBlocks), dim3(kFinalThreads), 0, st, p);
   return cudaGetLastError();

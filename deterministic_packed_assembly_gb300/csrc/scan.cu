@@ -833,13 +833,9 @@ Layout layout_of(uint32_t B, uint32_t T, uint32_t D, uint64_t resident) {
 template <class... KArgs>
 cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint32_t cluster,
                    size_t smem, cudaStream_t st, const ScanParams &p) {
-  if (smem > 0) {  // with the static part it may be beyond what needs no leave
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
+  if (smem > 0) {
+    const cudaError_t e = allow_shared_memory((const void *)k);
+    if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);

@@ -10,6 +10,10 @@
 
 namespace nsk {
 
+// Lets a kernel take as much dynamic shared memory as a block can have; asked once
+// for a kernel and device by each thread that launches it.
+cudaError_t allow_shared_memory(const void *kernel);
+
 cudaError_t launch_scan_forward(const ns_scan_inputs &in, const float *h0, void *y, float *h_last,
                                 float *states, cudaStream_t st);
 // Rows of partial bias gradients that the backward pass writes ([rows][D]).
@@ -22,7 +26,7 @@ cudaError_t launch_scan_backward(const ns_scan_inputs &in, const float *states, 
 cudaError_t launch_distill(const ns_distill_inputs &in, float *loss, void *dlogits,
                            int64_t dlogits_row, cudaStream_t st);
 
-// Blocks of the forward kernel, each with a row of partial sums.
+// Rows of partial sums that the forward kernel's blocks write.
 uint32_t route_blocks(uint32_t N, uint32_t E);
 cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float *weights,
                                  int32_t *counts, int32_t *tokens, float *loss, void *workspace,

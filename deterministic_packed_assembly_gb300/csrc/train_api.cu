@@ -46,6 +46,37 @@ bool check_scan(const ns_scan_inputs *in) {
 
 }  // namespace
 
+namespace nsk {
+
+cudaError_t allow_shared_memory(const void *kernel) {
+  struct Known {
+    const void *kernel;
+    int device;
+  };
+  thread_local Known known[64];
+  thread_local unsigned count = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  for (unsigned i = 0; e == cudaSuccess && i < count && i < 64; ++i)
+    if (known[i].kernel == kernel && known[i].device == device) return cudaSuccess;
+  cudaFuncAttributes a;
+  int most = 0;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most - (int)a.sharedSizeBytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  known[count++ % 64] = {kernel, device};
+  return cudaSuccess;
+}
+
+}  // namespace nsk
+
 extern "C" {
 
 int ns_scan_forward(const ns_scan_inputs *in, const float *h0, void *y, float *h_last,
@@ -121,8 +152,7 @@ static bool check_route(const ns_route_inputs *in) {
 }
 
 uint64_t ns_route_workspace(uint32_t N, uint32_t E) {
-  const uint64_t blocks = nsk::route_blocks(N, E);
-  return blocks == 1 ? 0 : blocks * (8ull * E + 4);
+  return nsk::route_blocks(N, E) * (8ull * E + 4);
 }
 
 int ns_route_forward(const ns_route_inputs *in, int32_t *ids, float *weights, int32_t *counts,
