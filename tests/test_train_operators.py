@@ -925,3 +925,35 @@ def test_route_refusals(nsp):
             lambda: nsp.route_backward(x, None, dw), lambda: nsp.route_backward(x[:, :39], r, dw),
             lambda: nsp.route_backward(x, r, dw, torch.ones(2).cuda())):
         refused(nsp, call)
+
+
+def test_operators_on_a_packed_update(nsp):
+    """The packer's own arrays through every operator, forward and backward, by the
+    example: the loss falls, and padding chose no expert."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "packed_training_step.py")
+    spec = importlib.util.spec_from_file_location("packed_training_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses = example.train(steps=8)
+    assert all(math.isfinite(x) for x in losses) and losses[-1] < losses[0] - 0.1
+    from corpus import make_preset
+    c = make_preset("c1")
+    pk = nsp.Packer.from_corpus(c)
+    out = pk.step(0)
+    doc = out["doc"][0]
+    r = nsp.route(torch.randn(doc.numel(), 8, generator=gen(1)).cuda(), 2, doc=doc.reshape(-1))
+    assert int(r.tokens) == int((doc >= 0).sum())
+    assert ((r.ids == -1).all(1) == (doc.reshape(-1) < 0)).all()
+    # packed rows give what their documents give alone
+    z = torch.randn(*doc.shape, 32, generator=gen(2)).cuda()
+    f = torch.randn(*doc.shape, 32, generator=gen(3)).cuda()
+    y, _ = nsp.gated_scan(z, f, pos=out["pos"][0], doc=doc)
+    row, pos = doc[0].cpu(), out["pos"][0][0].cpu()
+    starts = [t for t in range(len(row)) if pos[t] == 0 and row[t] >= 0] + [int((row >= 0).sum())]
+    for a, b in zip(starts[:6], starts[1:7]):
+        alone, _ = nsp.gated_scan(z[:1, a:b], f[:1, a:b])
+        close(y[0, a:b], alone[0].double().cpu(), 2e-5, f"document at {a}")
+    pk.close()
