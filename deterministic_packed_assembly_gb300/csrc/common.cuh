@@ -48,6 +48,13 @@ __device__ __forceinline__ void pdl_wait_then_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Let the next kernel's blocks be scheduled as this one's leave room, without a
+// wait: for a next kernel that needs nothing of this one but to end after it (it
+// calls pdl_wait last).
+__device__ __forceinline__ void release_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Launch `k` on `st` with programmatic dependent launch allowed: its blocks
 // may be scheduled while the previous kernel in the stream drains, and wait
 // in pdl_wait_then_release (which every such kernel calls first) for it to

@@ -322,8 +322,9 @@ __device__ __forceinline__ Ch<CH> pass_block(const Exchange<CH, kWarps> &x, int 
 // is stored into every block, asynchronously: the stores themselves count down
 // the barrier that the receiving block's warps wait at.  (A cluster barrier in
 // its place has each warp wait for its earlier stores to global memory: a quarter
-// of the stalls.)  A block sends for round i + 2 when it has everything of round
-// i + 1, which the others sent after they had read round i: two buffers do.
+// of the stalls.)  A block sends round i + 1 when it has read round i, and has
+// everything of round i, which the others sent after they had read round i - 1:
+// two buffers do.
 template <int CH>
 struct Quads {
   Exchange<CH, kMaxCluster * kQuads> x;
@@ -354,9 +355,8 @@ __device__ __forceinline__ void send_word(uint32_t to, uint32_t bar, uint32_t v)
 }
 
 template <int CH>
-__device__ __forceinline__ Ch<CH> pass_cluster(const Exchange<CH, kWarps> &x, Quads<CH> &quads,
-                                               uint32_t parity, bool &lost, uint32_t rank,
-                                               uint32_t split, int lane, int warp, Ch<CH> &h) {
+__device__ __forceinline__ void send_quad(const Exchange<CH, kWarps> &x, Quads<CH> &quads,
+                                          uint32_t rank, uint32_t split, int lane, int warp) {
   const int quad = warp / kQuad;
   const uint32_t cuts = quad_cuts(x, quad);
   const Run<CH> all = quad_run(x, quad, lane, cuts);
@@ -367,7 +367,14 @@ __device__ __forceinline__ Ch<CH> pass_cluster(const Exchange<CH, kWarps> &x, Qu
     send_run<CH>(remote_smem(&quads.x.run[self][lane], to), bar, all);
     if (lane == 0) send_word(remote_smem(&quads.x.cut[self], to), bar, cuts);
   }
-  if (!lost && !barrier_wait(&quads.arrived, parity)) lost = true;
+}
+// The state before this warp's quad, and h moved on past the cluster's tiles.
+template <int CH>
+__device__ __forceinline__ Ch<CH> pass_cluster(const Quads<CH> &quads, uint64_t *arrived,
+                                               uint32_t parity, bool &lost, uint32_t rank,
+                                               uint32_t split, int lane, int warp, Ch<CH> &h) {
+  const uint32_t self = rank * kQuads + warp / kQuad, count = split * kQuads;
+  if (!lost && !barrier_wait(arrived, parity)) lost = true;
   const uint32_t any =
       __ballot_sync(0xffffffffu, (uint32_t)lane < count && quads.x.cut[lane] != 0);
   Ch<CH> mine = h;
@@ -385,7 +392,7 @@ __device__ __forceinline__ Ch<CH> pass_cluster(const Exchange<CH, kWarps> &x, Qu
     }
   }
   if (lost) mine = h = splat<CH>(__int_as_float(0x7fffffff));  // shows in every output
-  return inside_quad(x, lane, warp, cuts, mine);
+  return mine;
 }
 
 // Blocks of an SM: 24 warps forward (80 registers), 16 backward (128).
@@ -422,17 +429,145 @@ __device__ __forceinline__ void cluster_begin(Quads<CH> (&quads)[2]) {
   cluster_wait();
 }
 
-template <class E, int CH, bool kCluster>
+// ---- forward --------------------------------------------------------------------
+// A segment's gates a and inputs c z; a = 1, c z = 0 at skipped steps.
+template <class E, int CH>
+__device__ __forceinline__ void forward_gates(const Stage<E, CH, 2> &in, int lane, Ch<CH> nb,
+                                              uint32_t skip, Ch<CH> (&a)[kSteps],
+                                              Ch<CH> (&cz)[kSteps]) {
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    Ch<CH> r, c;
+    gate<CH>(widen<E, CH>(in.v[1][s][lane]), nb, r, c, a[s]);
+    cz[s] = c * widen<E, CH>(in.v[0][s][lane]);
+  }
+  if (skip) {  // the same for the warp
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const bool gone = (skip >> s) & 1u;
+      a[s] = pick(gone, splat<CH>(1.0f), a[s]);
+      cz[s] = pick(gone, splat<CH>(0.0f), cz[s]);
+    }
+  }
+}
+template <int CH>
+__device__ __forceinline__ Run<CH> forward_run(const Ch<CH> (&a)[kSteps],
+                                               const Ch<CH> (&cz)[kSteps], uint32_t start) {
+  Run<CH> run = {a[0], cz[0]};
+  if (start == 0) {
+#pragma unroll
+    for (int s = 1; s < kSteps; ++s) {
+      run.H = fma(a[s], run.H, cz[s]);
+      run.A = run.A * a[s];
+    }
+  } else {
+#pragma unroll
+    for (int s = 1; s < kSteps; ++s) {
+      run.H = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), run.H), cz[s]);
+      run.A = run.A * a[s];
+    }
+  }
+  return run;
+}
+// The segment's states from the one before it, into y.
+template <class E, int CH>
+__device__ __forceinline__ void forward_apply(const ScanParams &p, const Ch<CH> (&a)[kSteps],
+                                              const Ch<CH> (&cz)[kSteps], Ch<CH> h, bool live,
+                                              int left, uint32_t start, uint32_t skip, E *y) {
+  if ((start | skip) == 0) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s, y += p.D) {
+      h = fma(a[s], h, cz[s]);
+      if (live) *reinterpret_cast<Raw<E, CH> *>(y) = narrow<E, CH>(h);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s, y += p.D) {
+      h = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), h), cz[s]);
+      if (live && s < left)
+        *reinterpret_cast<Raw<E, CH> *>(y) =
+            narrow<E, CH>(pick((skip >> s) & 1u, splat<CH>(0.0f), h));
+    }
+  }
+}
+
+// Blocks that each take a unit's whole row.
+template <class E, int CH>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     scan_forward_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) Exchange<CH, kWarps> seg[2];
-  __shared__ __align__(16) unsigned char quads_mem[kCluster ? 2 * sizeof(Quads<CH>) : 16];
-  Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
-  const Place at = place_of<CH, kCluster>(p);
+  const Place at = place_of<CH, false>(p);
   const int lane = at.lane, warp = at.warp;
   Stage<E, CH, 2> *ring = reinterpret_cast<Stage<E, CH, 2> *>(smem) + warp * kRing;
-  if (kCluster) cluster_begin<CH>(quads);
+  release_dependents();
+  const int T = (int)p.T, rounds = (T + kTile - 1) / kTile;
+  int t = warp * kSteps;  // may lie past the row
+  Copier<E, CH> copier;
+  const E *z_from = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
+  const E *f_from = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
+  z_from += copier.set(p.z_time, p.D - at.cg, p.wide, lane);
+  f_from += copier.set(p.f_time, p.D - at.cg, p.wide, lane);
+  auto fetch = [&](int at_step, Stage<E, CH, 2> &to) {
+    const int n = steps_at(T, at_step);
+    copier.copy(z_from, p.z_time, n, p.wide, lane, to.v[0]);
+    copier.copy(f_from, p.f_time, n, p.wide, lane, to.v[1]);
+    z_from += p.z_step, f_from += p.f_step;
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kRing - 1; ++k) fetch(t + k * kTile, ring[k]);
+  Flags flags;
+  flags.set(p, at.b, t, kTile, lane);
+  const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
+  Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
+  E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
+  float *state = nullptr;  // the state before a quad is its first warp's to save
+  if (p.states && warp % kQuad == 0)
+    state = p.states + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
+                        t / NS_SCAN_TILE) * p.D + at.c0;
+  int slot = 0;
+  for (int i = 0; i < rounds; ++i, t += kTile) {
+    __syncwarp();  // the slot that is filled now was read in the last round
+    fetch(t + (kRing - 1) * kTile, ring[slot == 0 ? kRing - 1 : slot - 1]);
+    flags.next(p, kTile, i);
+    const uint32_t start = flags.start & 0xffu, skip = flags.skip & 0xffu;
+    copy_wait<kRing - 1>();
+    __syncwarp();
+    Ch<CH> a[kSteps], cz[kSteps];
+    forward_gates<E, CH>(ring[slot], lane, nb, skip, a, cz);
+    slot = slot == kRing - 1 ? 0 : slot + 1;
+    Exchange<CH, kWarps> &x = seg[i & 1];
+    x.run[warp][lane] = forward_run<CH>(a, cz, start);
+    if (lane == 0) x.cut[warp] = start;
+    __syncthreads();
+    const Ch<CH> in = pass_block<CH>(x, lane, warp, h);
+    if (state) {
+      store_channels<CH>(state, 0, at.live && t < T, in);
+      state += p.state_step;
+    }
+    forward_apply<E, CH>(p, a, cz, in, at.live, T - t, start, skip, y);
+    y += p.out_step;
+  }
+  copy_wait<0>();
+  if (warp == 0) store_channels<CH>(p.h_last, (int64_t)at.b * p.D + at.c0, at.live, h);
+}
+
+// Clusters of blocks, each with every split-th tile of a unit's row.  The runs of
+// round i + 1 are computed and sent before the steps of round i are written, so
+// that their way between the blocks lies beside this and the next round's runs;
+// the gates of a round are computed twice instead of kept.
+template <class E, int CH>
+__global__ void __launch_bounds__(kThreads, kForwardBlocks)
+    scan_forward_cluster_kernel(const ScanParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) Exchange<CH, kWarps> seg[3];
+  __shared__ __align__(16) unsigned char quads_mem[2 * sizeof(Quads<CH>)];
+  Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
+  const Place at = place_of<CH, true>(p);
+  const int lane = at.lane, warp = at.warp;
+  Stage<E, CH, 2> *ring = reinterpret_cast<Stage<E, CH, 2> *>(smem) + warp * kRing;
+  cluster_begin<CH>(quads);
   const int T = (int)p.T, rounds = (T + p.step - 1) / p.step;
   int t = (int)at.rank * kTile + warp * kSteps;  // may lie past the row
   Copier<E, CH> copier;
@@ -447,89 +582,59 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     z_from += p.z_step, f_from += p.f_step;
     copy_commit();
   };
-#pragma unroll
-  for (int k = 0; k < kRing - 1; ++k) fetch(t + k * p.step, ring[k]);
+  fetch(t, ring[0]);
   Flags flags;
   flags.set(p, at.b, t, p.step, lane);
   const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
   E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
-  float *state = nullptr;  // the state before a quad is its first warp's to save
+  float *state = nullptr;
   if (p.states && warp % kQuad == 0)
     state = p.states + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
                         t / NS_SCAN_TILE) * p.D + at.c0;
-  int slot = 0;
   bool lost = false;
-  for (int i = 0; i < rounds; ++i, t += p.step) {
-    __syncwarp();  // the slot that is filled now was read in the last round
-    fetch(t + (kRing - 1) * p.step, ring[slot == 0 ? kRing - 1 : slot - 1]);
-    flags.next(p, p.step, i);
-    const uint32_t start = flags.start & 0xffu, skip = flags.skip & 0xffu;
-    const bool plain = (start | skip) == 0;  // the same for the warp
-    copy_wait<kRing - 1>();
+  uint32_t start = 0, skip = 0;
+  Ch<CH> a[kSteps], cz[kSteps];
+  // Round i's runs, its tile at step t_i.
+  auto runs = [&](int i, int t_i) {
     __syncwarp();
-    const Stage<E, CH, 2> &in_smem = ring[slot];
-    slot = slot == kRing - 1 ? 0 : slot + 1;
-    Ch<CH> a[kSteps], cz[kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      Ch<CH> r, c;
-      gate<CH>(widen<E, CH>(in_smem.v[1][s][lane]), nb, r, c, a[s]);
-      cz[s] = c * widen<E, CH>(in_smem.v[0][s][lane]);
-    }
-    Run<CH> run;
-    if (plain) {
-      run.H = cz[0], run.A = a[0];
-#pragma unroll
-      for (int s = 1; s < kSteps; ++s) {
-        run.H = fma(a[s], run.H, cz[s]);
-        run.A = run.A * a[s];
-      }
-    } else {
-      run.H = splat<CH>(0.0f), run.A = splat<CH>(1.0f);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const bool out = (skip >> s) & 1u;
-        a[s] = pick(out, splat<CH>(1.0f), a[s]);
-        cz[s] = pick(out, splat<CH>(0.0f), cz[s]);
-        run.H = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), run.H), cz[s]);
-        run.A = run.A * a[s];
-      }
-    }
-    Exchange<CH, kWarps> &x = seg[i & 1];
-    x.run[warp][lane] = run;
+    fetch(t_i + p.step, ring[(i + 1) % kRing]);
+    flags.next(p, p.step, i);
+    start = flags.start & 0xffu, skip = flags.skip & 0xffu;
+    copy_wait<1>();
+    __syncwarp();
+    forward_gates<E, CH>(ring[i % kRing], lane, nb, skip, a, cz);
+    Exchange<CH, kWarps> &x = seg[i % 3];
+    x.run[warp][lane] = forward_run<CH>(a, cz, start);
     if (lane == 0) x.cut[warp] = start;
     __syncthreads();
-    Ch<CH> in;
-    if constexpr (kCluster)
-      in = pass_cluster<CH>(x, quads[i & 1], (i >> 1) & 1, lost, at.rank, p.split, lane, warp, h);
-    else
-      in = pass_block<CH>(x, lane, warp, h);
+  };
+  runs(0, t);
+  send_quad<CH>(seg[0], quads[0], at.rank, p.split, lane, warp);
+  for (int i = 0; i < rounds; ++i, t += p.step) {
+    const uint32_t start_i = start, skip_i = skip;
+    if (i + 1 < rounds) runs(i + 1, t + p.step);
+    Quads<CH> &q = quads[i & 1];
+    const Ch<CH> mine = pass_cluster<CH>(q, &q.arrived, (i >> 1) & 1, lost, at.rank, p.split, lane,
+                                         warp, h);
+    if (i + 1 < rounds) {
+      __syncthreads();  // every warp has read round i
+      send_quad<CH>(seg[(i + 1) % 3], quads[(i + 1) & 1], at.rank, p.split, lane, warp);
+    }
+    const Exchange<CH, kWarps> &x = seg[i % 3];
+    const Ch<CH> in = inside_quad<CH>(x, lane, warp, quad_cuts(x, warp / kQuad), mine);
     if (state) {
       store_channels<CH>(state, 0, at.live && t < T, in);
       state += p.state_step;
     }
-    E *to = y;
-    if (plain) {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s, to += p.D) {
-        in = fma(a[s], in, cz[s]);
-        if (at.live) *reinterpret_cast<Raw<E, CH> *>(to) = narrow<E, CH>(in);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s, to += p.D) {
-        in = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), in), cz[s]);
-        if (at.live && t + s < T)
-          *reinterpret_cast<Raw<E, CH> *>(to) =
-              narrow<E, CH>(pick((skip >> s) & 1u, splat<CH>(0.0f), in));
-      }
-    }
+    forward_gates<E, CH>(ring[i % kRing], lane, nb, skip_i, a, cz);
+    forward_apply<E, CH>(p, a, cz, in, at.live, T - t, start_i, skip_i, y);
     y += p.out_step;
   }
   copy_wait<0>();
   if (at.rank == 0 && warp == 0)
     store_channels<CH>(p.h_last, (int64_t)at.b * p.D + at.c0, at.live, h);
+  pdl_wait();  // what waits for this launch also waits for the one before
 }
 
 // Rows of at most kSteps steps: a thread takes a row's channels alone, one
@@ -562,24 +667,163 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
   store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, true, h);
 }
 
+// ---- backward -------------------------------------------------------------------
 // The backward pass walks the tiles from the last one, and a warp's segments
 // with them: warp w takes the segment that is w-th from the tile's end.
 //   d_t = dy_t + u_t,  u_{t-1} = a_t d_t  (0 where a sequence starts)
 // is a run in the other direction with the same A, exchanged as in the forward
 // pass.  The states inside a quad are run again from the saved one before it,
 // by the segments' forward runs, which are exchanged too.
+//
+// A segment's gates: a, c and q = a c from the unrounded gate; a = 1, c = q = 0 at
+// skipped steps.
+template <class E, int CH>
+__device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in, int lane, Ch<CH> nb,
+                                               uint32_t skip, Ch<CH> (&a)[kSteps],
+                                               Ch<CH> (&c)[kSteps], Ch<CH> (&q)[kSteps]) {
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    Ch<CH> r;
+    gate<CH>(widen<E, CH>(in.v[1][s][lane]), nb, r, c[s], a[s]);
+    q[s] = r * c[s];
+  }
+  if (skip) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const bool gone = (skip >> s) & 1u;
+      a[s] = pick(gone, splat<CH>(1.0f), a[s]);
+      c[s] = pick(gone, splat<CH>(0.0f), c[s]);
+      q[s] = pick(gone, splat<CH>(0.0f), q[s]);
+    }
+  }
+}
+// (A, U) of the segment, and H.
+template <class E, int CH>
+__device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in, int lane,
+                                                const Ch<CH> (&a)[kSteps],
+                                                const Ch<CH> (&c)[kSteps], uint32_t start,
+                                                uint32_t skip, Ch<CH> &H) {
+  const Ch<CH> zero = splat<CH>(0.0f);
+  Run<CH> run = {splat<CH>(1.0f), zero};
+  H = zero;
+  if ((start | skip) == 0) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      H = fma(a[s], H, c[s] * widen<E, CH>(in.v[0][s][lane]));
+      run.A = run.A * a[s];
+    }
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s)
+      run.H = a[s] * (widen<E, CH>(in.v[2][s][lane]) + run.H);
+  } else {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const Ch<CH> cz = pick((skip >> s) & 1u, zero, c[s] * widen<E, CH>(in.v[0][s][lane]));
+      H = fma(a[s], pick((start >> s) & 1u, zero, H), cz);
+      run.A = run.A * a[s];
+    }
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s) {
+      const Ch<CH> g = pick((skip >> s) & 1u, zero, widen<E, CH>(in.v[2][s][lane]));
+      run.H = pick((start >> s) & 1u, zero, a[s] * (g + run.H));
+    }
+  }
+  return run;
+}
+// The state before this warp's segment, from the saved one before its quad:
+// through the quad's earlier segments, which later warps hold.
+template <int CH>
+__device__ __forceinline__ Ch<CH> state_before(const Exchange<CH, kWarps> &x,
+                                               const Ch<CH> (&ahead)[kWarps][32], int lane,
+                                               int warp, Ch<CH> h) {
+#pragma unroll
+  for (int k = kQuad - 1; k > 0; --k) {
+    if ((kWarps - 1 - warp) % kQuad >= k) {
+      const Run<CH> r = {x.run[warp + k][lane].A, ahead[warp + k][lane]};
+      h = after(r, x.cut[warp + k] != 0, h);
+    }
+  }
+  return h;
+}
+// The segment's gradients, from the state before it and u after it.
+template <class E, int CH>
+__device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<E, CH, 3> &in,
+                                               int lane, const Ch<CH> (&a)[kSteps],
+                                               const Ch<CH> (&c)[kSteps], Ch<CH> (&q)[kSteps],
+                                               Ch<CH> h, Ch<CH> u, bool live, int left,
+                                               uint32_t start, uint32_t skip, E *dz, E *df,
+                                               Ch<CH> &sum) {
+  const Ch<CH> zero = splat<CH>(0.0f);
+  dz += (int64_t)(kSteps - 1) * p.D, df += (int64_t)(kSteps - 1) * p.D;
+  if ((start | skip) == 0) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {  // q takes p_t - z_t in
+      const Ch<CH> z = widen<E, CH>(in.v[0][s][lane]);
+      q[s] = q[s] * sub(h, z);
+      h = fma(a[s], h, c[s] * z);
+    }
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
+      const Ch<CH> d = widen<E, CH>(in.v[2][s][lane]) + u, vf = q[s] * d;
+      u = a[s] * d;
+      sum = sum + vf;
+      if (live) {
+        *reinterpret_cast<Raw<E, CH> *>(dz) = narrow<E, CH>(c[s] * d);
+        *reinterpret_cast<Raw<E, CH> *>(df) = narrow<E, CH>(vf);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const Ch<CH> z = pick((skip >> s) & 1u, zero, widen<E, CH>(in.v[0][s][lane]));
+      const Ch<CH> before = pick((start >> s) & 1u, zero, h);
+      q[s] = q[s] * sub(before, z);
+      h = fma(a[s], before, c[s] * z);
+    }
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
+      const bool gone = (skip >> s) & 1u;
+      const Ch<CH> d = pick(gone, zero, widen<E, CH>(in.v[2][s][lane])) + u;
+      const Ch<CH> vf = pick(gone, zero, q[s] * d);
+      u = pick((start >> s) & 1u, zero, a[s] * d);
+      sum = sum + vf;
+      if (live && s < left) {
+        *reinterpret_cast<Raw<E, CH> *>(dz) = narrow<E, CH>(pick(gone, zero, c[s] * d));
+        *reinterpret_cast<Raw<E, CH> *>(df) = narrow<E, CH>(vf);
+      }
+    }
+  }
+}
+// A block's part of the bias's gradient: `sum` over its warps.
+template <int CH>
+__device__ __forceinline__ void store_sums(const ScanParams &p, const Place &at,
+                                           Ch<CH> (&room)[kWarps][32], Ch<CH> sum) {
+  __syncthreads();
+  room[at.warp][at.lane] = sum;
+  __syncthreads();
+  if (at.warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) sum = sum + room[w][at.lane];
+  float *to = p.partial + (int64_t)at.b * p.sums * p.D + at.c0;
+  store_channels<CH>(to, (int64_t)at.rank * p.D, at.live, sum);
+  for (uint32_t r = p.split + at.rank; r < p.sums; r += p.split)
+    store_channels<CH>(to, (int64_t)r * p.D, at.live, splat<CH>(0.0f));
+}
+
 template <class E, int CH, bool kCluster>
 __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     scan_backward_kernel(const ScanParams p) {
+  constexpr int kSegs = kCluster ? 3 : 2;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) Exchange<CH, kWarps> seg[2];  // (A, U)
-  __shared__ Ch<CH> ahead[2][kWarps][32];                // H of the same segments
+  __shared__ __align__(16) Exchange<CH, kWarps> seg[kSegs];  // (A, U)
+  __shared__ Ch<CH> ahead[kSegs][kWarps][32];                // H of the same segments
   __shared__ __align__(16) unsigned char quads_mem[kCluster ? 2 * sizeof(Quads<CH>) : 16];
   Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
   const Place at = place_of<CH, kCluster>(p);
   const int lane = at.lane, warp = at.warp;
   Stage<E, CH, 3> *ring = reinterpret_cast<Stage<E, CH, 3> *>(smem) + warp * kRing;
   if (kCluster) cluster_begin<CH>(quads);
+  else release_dependents();
   const int T = (int)p.T, rounds = (T + p.step - 1) / p.step;
   const int back = kWarps - 1 - warp;  // this warp's segment of a tile
   // negative in a tile before the first one, past the end of the walk
@@ -599,144 +843,87 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     z_from -= p.z_step, f_from -= p.f_step, g_from -= p.dy_step;
     copy_commit();
   };
+  // Copies run two tiles ahead in a block alone, one in a cluster, whose blocks
+  // have two tiles in hand.
+  constexpr int kAhead = kCluster ? 1 : kRing - 1;
 #pragma unroll
-  for (int k = 0; k < kRing - 1; ++k) fetch(t - k * p.step, ring[k]);
+  for (int k = 0; k < kAhead; ++k) fetch(t - k * p.step, ring[k]);
   Flags flags;
   flags.set(p, at.b, t, -p.step, lane);
-  const Ch<CH> zero = splat<CH>(0.0f);
   // the saved state before the segment's quad
   const float *saved = p.saved + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
                                   t / (int)NS_SCAN_TILE) * p.D + at.c0;
   Ch<CH> next_h = load_channels<CH>(saved, 0, at.live && t >= 0 && t < T);
   const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
-  Ch<CH> u = load_channels<CH>(p.dh_last, (int64_t)at.b * p.D + at.c0, at.live), sum = zero;
+  Ch<CH> u = load_channels<CH>(p.dh_last, (int64_t)at.b * p.D + at.c0, at.live);
+  Ch<CH> sum = splat<CH>(0.0f);
   const int64_t out = ((int64_t)at.b * p.T + t) * p.D + at.c0;
   E *dz = static_cast<E *>(p.dz) + out, *df = static_cast<E *>(p.df) + out;
-  int slot = 0;
   bool lost = false;
-  for (int i = 0; i < rounds; ++i, t -= p.step) {
+  uint32_t start = 0, skip = 0;
+  Ch<CH> a[kSteps], c[kSteps], q[kSteps];
+  // Round i's runs, its tile at step t_i.
+  auto runs = [&](int i, int t_i, int slot, int s) {
     __syncwarp();
-    fetch(t - (kRing - 1) * p.step, ring[slot == 0 ? kRing - 1 : slot - 1]);
+    fetch(t_i - kAhead * p.step, ring[slot + kAhead >= kRing ? slot + kAhead - kRing : slot + kAhead]);
     flags.next(p, -p.step, i);
-    const uint32_t start = flags.start & 0xffu, skip = flags.skip & 0xffu;
-    const bool plain = (start | skip) == 0;
-    Ch<CH> h = next_h;
-    saved -= p.state_step;
-    next_h = load_channels<CH>(saved, 0, at.live && t - p.step >= 0 && t - p.step < T);
-    copy_wait<kRing - 1>();
+    start = flags.start & 0xffu, skip = flags.skip & 0xffu;
+    copy_wait<kAhead>();
     __syncwarp();
-    const Stage<E, CH, 3> &in = ring[slot];
-    slot = slot == kRing - 1 ? 0 : slot + 1;
-    Ch<CH> a[kSteps], c[kSteps], q[kSteps], H = zero;  // q = a c, from the unrounded gate
-    Run<CH> run = {splat<CH>(1.0f), zero};
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      Ch<CH> r;
-      gate<CH>(widen<E, CH>(in.v[1][s][lane]), nb, r, c[s], a[s]);
-      q[s] = r * c[s];
-    }
-    if (plain) {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        H = fma(a[s], H, c[s] * widen<E, CH>(in.v[0][s][lane]));
-        run.A = run.A * a[s];
-      }
-#pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s)
-        run.H = a[s] * (widen<E, CH>(in.v[2][s][lane]) + run.H);
-    } else {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const bool gone = (skip >> s) & 1u;
-        a[s] = pick(gone, splat<CH>(1.0f), a[s]);
-        c[s] = pick(gone, zero, c[s]);
-        const Ch<CH> cz = pick(gone, zero, c[s] * widen<E, CH>(in.v[0][s][lane]));
-        H = fma(a[s], pick((start >> s) & 1u, zero, H), cz);
-        run.A = run.A * a[s];
-      }
-#pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s) {
-        const Ch<CH> g = pick((skip >> s) & 1u, zero, widen<E, CH>(in.v[2][s][lane]));
-        run.H = pick((start >> s) & 1u, zero, a[s] * (g + run.H));
-      }
-    }
-    Exchange<CH, kWarps> &x = seg[i & 1];
-    x.run[warp][lane] = run;
-    ahead[i & 1][warp][lane] = H;
-    if (lane == 0) x.cut[warp] = start;
+    backward_gates<E, CH>(ring[slot], lane, nb, skip, a, c, q);
+    Ch<CH> H;
+    seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], lane, a, c, start, skip, H);
+    ahead[s][warp][lane] = H;
+    if (lane == 0) seg[s].cut[warp] = start;
     __syncthreads();
-    // the state before this segment: through the quad's earlier ones, which
-    // later warps hold
-#pragma unroll
-    for (int k = kQuad - 1; k > 0; --k) {
-      if (back % kQuad >= k) {
-        const Run<CH> r = {x.run[warp + k][lane].A, ahead[i & 1][warp + k][lane]};
-        h = after(r, x.cut[warp + k] != 0, h);
-      }
+  };
+  auto take_state = [&](int t_i) {
+    const Ch<CH> h = next_h;
+    saved -= p.state_step;
+    next_h = load_channels<CH>(saved, 0, at.live && t_i - p.step >= 0 && t_i - p.step < T);
+    return h;
+  };
+  if constexpr (!kCluster) {
+    int slot = 0;
+    for (int i = 0; i < rounds; ++i, t -= p.step) {
+      Ch<CH> h = take_state(t);
+      runs(i, t, slot, i & 1);
+      h = state_before<CH>(seg[i & 1], ahead[i & 1], lane, warp, h);
+      const Ch<CH> ui = pass_block<CH>(seg[i & 1], lane, warp, u);
+      backward_apply<E, CH>(p, ring[slot], lane, a, c, q, h, ui, at.live, t < 0 ? 0 : T - t, start,
+                            skip, dz, df, sum);
+      dz -= p.out_step, df -= p.out_step;
+      slot = slot == kRing - 1 ? 0 : slot + 1;
     }
-    Ch<CH> ui;
-    if constexpr (kCluster)
-      ui = pass_cluster<CH>(x, quads[i & 1], (i >> 1) & 1, lost, at.rank, p.split, lane, warp, u);
-    else
-      ui = pass_block<CH>(x, lane, warp, u);
-    E *to_z = dz + (int64_t)(kSteps - 1) * p.D, *to_f = df + (int64_t)(kSteps - 1) * p.D;
-    if (plain) {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {  // q takes p_t - z_t in
-        const Ch<CH> z = widen<E, CH>(in.v[0][s][lane]);
-        q[s] = q[s] * sub(h, z);
-        h = fma(a[s], h, c[s] * z);
+  } else {  // as the forward pass's clusters
+    int slot = 0, s = 0;
+    runs(0, t, 0, 0);
+    send_quad<CH>(seg[0], quads[0], at.rank, p.split, lane, warp);
+    for (int i = 0; i < rounds; ++i, t -= p.step) {
+      const uint32_t start_i = start, skip_i = skip;
+      const int next_slot = slot == kRing - 1 ? 0 : slot + 1, next_s = s == 2 ? 0 : s + 1;
+      if (i + 1 < rounds) runs(i + 1, t - p.step, next_slot, next_s);
+      Quads<CH> &from = quads[i & 1];
+      const Ch<CH> mine = pass_cluster<CH>(from, &from.arrived, (i >> 1) & 1, lost, at.rank,
+                                           p.split, lane, warp, u);
+      if (i + 1 < rounds) {
+        __syncthreads();  // every warp has read round i
+        send_quad<CH>(seg[next_s], quads[(i + 1) & 1], at.rank, p.split, lane, warp);
       }
-#pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s, to_z -= p.D, to_f -= p.D) {
-        const Ch<CH> d = widen<E, CH>(in.v[2][s][lane]) + ui, vf = q[s] * d;
-        ui = a[s] * d;
-        sum = sum + vf;
-        if (at.live) {
-          *reinterpret_cast<Raw<E, CH> *>(to_z) = narrow<E, CH>(c[s] * d);
-          *reinterpret_cast<Raw<E, CH> *>(to_f) = narrow<E, CH>(vf);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const bool gone = (skip >> s) & 1u;
-        const Ch<CH> z = pick(gone, zero, widen<E, CH>(in.v[0][s][lane]));
-        const Ch<CH> before = pick((start >> s) & 1u, zero, h);
-        q[s] = q[s] * sub(before, z);
-        h = fma(a[s], before, c[s] * z);
-      }
-#pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s, to_z -= p.D, to_f -= p.D) {
-        const bool gone = (skip >> s) & 1u;
-        const Ch<CH> d = pick(gone, zero, widen<E, CH>(in.v[2][s][lane])) + ui;
-        const Ch<CH> vf = pick(gone, zero, q[s] * d);
-        ui = pick((start >> s) & 1u, zero, a[s] * d);
-        sum = sum + vf;
-        if (at.live && t + s < T && t >= 0) {
-          *reinterpret_cast<Raw<E, CH> *>(to_z) = narrow<E, CH>(pick(gone, zero, c[s] * d));
-          *reinterpret_cast<Raw<E, CH> *>(to_f) = narrow<E, CH>(vf);
-        }
-      }
+      const Ch<CH> h = state_before<CH>(seg[s], ahead[s], lane, warp, take_state(t));
+      const Ch<CH> ui = inside_quad<CH>(seg[s], lane, warp, quad_cuts(seg[s], warp / kQuad), mine);
+      backward_gates<E, CH>(ring[slot], lane, nb, skip_i, a, c, q);
+      backward_apply<E, CH>(p, ring[slot], lane, a, c, q, h, ui, at.live, t < 0 ? 0 : T - t,
+                            start_i, skip_i, dz, df, sum);
+      dz -= p.out_step, df -= p.out_step;
+      slot = next_slot, s = next_s;
     }
-    dz -= p.out_step, df -= p.out_step;
   }
   copy_wait<0>();
   if (at.rank == 0 && warp == 0)
     store_channels<CH>(p.dh0, (int64_t)at.b * p.D + at.c0, at.live, u);
-  if (p.partial) {
-    __syncthreads();
-    ahead[0][warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) sum = sum + ahead[0][w][lane];
-      float *to = p.partial + (int64_t)at.b * p.sums * p.D + at.c0;
-      store_channels<CH>(to, (int64_t)at.rank * p.D, at.live, sum);
-      for (uint32_t r = p.split + at.rank; r < p.sums; r += p.split)
-        store_channels<CH>(to, (int64_t)r * p.D, at.live, zero);
-    }
-  }
+  if (p.partial) store_sums<CH>(p, at, ahead[0], sum);
+  if (kCluster) pdl_wait();  // what waits for this launch also waits for the one before
 }
 
 template <class E, int CH>
@@ -832,7 +1019,7 @@ Layout layout_of(uint32_t B, uint32_t T, uint32_t D, uint64_t resident) {
 
 template <class... KArgs>
 cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint32_t cluster,
-                   size_t smem, cudaStream_t st, const ScanParams &p) {
+                   size_t smem, cudaStream_t st, const ScanParams &p, bool beside = false) {
   if (smem > 0) {
     const cudaError_t e = allow_shared_memory((const void *)k);
     if (e != cudaSuccess) return e;
@@ -842,13 +1029,16 @@ cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint3
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cluster;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  // the rest of a pass, beside the last blocks of its first launch
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? beside ? 2 : 1 : 0;
   ++launch_counter();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k, p);
   const cudaError_t last = cudaGetLastError();
@@ -875,12 +1065,12 @@ cudaError_t run_as(ScanParams &p, cudaStream_t st) {
     p.z_step = p.step * p.z_time, p.f_step = p.step * p.f_time, p.dy_step = p.step * p.dy_time;
     p.out_step = (int64_t)p.step * p.D, p.state_step = (int64_t)(p.step / (int)NS_SCAN_TILE) * p.D;
     return kForward
-               ? launch(split == 1 ? scan_forward_kernel<E, CH, false>
-                                   : scan_forward_kernel<E, CH, true>,
+               ? launch(split == 1 ? scan_forward_kernel<E, CH>
+                                   : scan_forward_cluster_kernel<E, CH>,
                         count * split, kThreads, split, smem, st, p)
                : launch(split == 1 ? scan_backward_kernel<E, CH, false>
                                    : scan_backward_kernel<E, CH, true>,
-                        count * split, kThreads, split, smem, st, p);
+                        count * split, kThreads, split, smem, st, p, first > 0);
   };
   if (whole) {
     const cudaError_t e = part(0, whole, 1);
