@@ -555,10 +555,11 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
 
 // Clusters of blocks, each with every split-th tile of a unit's row.  The runs of
 // round i + 1 are computed and sent before the steps of round i are written, so
-// that their way between the blocks lies beside this and the next round's runs;
-// the gates of a round are computed twice instead of kept.
+// that their way between the blocks lies beside this and the next round's runs.
+// Two rounds' gates are in registers: two blocks an SM, which is what the grids of
+// clusters hold anyway.
 template <class E, int CH>
-__global__ void __launch_bounds__(kThreads, kForwardBlocks)
+__global__ void __launch_bounds__(kThreads, 2)
     scan_forward_cluster_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) Exchange<CH, kWarps> seg[3];
@@ -582,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     z_from += p.z_step, f_from += p.f_step;
     copy_commit();
   };
-  fetch(t, ring[0]);
+#pragma unroll
+  for (int k = 0; k < kRing - 1; ++k) fetch(t + k * p.step, ring[k]);
   Flags flags;
   flags.set(p, at.b, t, p.step, lane);
   const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
@@ -593,27 +595,29 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     state = p.states + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
                         t / NS_SCAN_TILE) * p.D + at.c0;
   bool lost = false;
-  uint32_t start = 0, skip = 0;
-  Ch<CH> a[kSteps], cz[kSteps];
+  // What is left to do of a round whose runs are sent.
+  struct Round {
+    Ch<CH> a[kSteps], cz[kSteps];
+    uint32_t start, skip;
+  } now, next;
   // Round i's runs, its tile at step t_i.
-  auto runs = [&](int i, int t_i) {
+  auto runs = [&](int i, int t_i, Round &r) {
     __syncwarp();
-    fetch(t_i + p.step, ring[(i + 1) % kRing]);
+    fetch(t_i + (kRing - 1) * p.step, ring[(i + kRing - 1) % kRing]);
     flags.next(p, p.step, i);
-    start = flags.start & 0xffu, skip = flags.skip & 0xffu;
-    copy_wait<1>();
+    r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
+    copy_wait<kRing - 1>();
     __syncwarp();
-    forward_gates<E, CH>(ring[i % kRing], lane, nb, skip, a, cz);
+    forward_gates<E, CH>(ring[i % kRing], lane, nb, r.skip, r.a, r.cz);
     Exchange<CH, kWarps> &x = seg[i % 3];
-    x.run[warp][lane] = forward_run<CH>(a, cz, start);
-    if (lane == 0) x.cut[warp] = start;
+    x.run[warp][lane] = forward_run<CH>(r.a, r.cz, r.start);
+    if (lane == 0) x.cut[warp] = r.start;
     __syncthreads();
   };
-  runs(0, t);
+  runs(0, t, now);
   send_quad<CH>(seg[0], quads[0], at.rank, p.split, lane, warp);
   for (int i = 0; i < rounds; ++i, t += p.step) {
-    const uint32_t start_i = start, skip_i = skip;
-    if (i + 1 < rounds) runs(i + 1, t + p.step);
+    if (i + 1 < rounds) runs(i + 1, t + p.step, next);
     Quads<CH> &q = quads[i & 1];
     const Ch<CH> mine = pass_cluster<CH>(q, &q.arrived, (i >> 1) & 1, lost, at.rank, p.split, lane,
                                          warp, h);
@@ -627,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
       store_channels<CH>(state, 0, at.live && t < T, in);
       state += p.state_step;
     }
-    forward_gates<E, CH>(ring[i % kRing], lane, nb, skip_i, a, cz);
-    forward_apply<E, CH>(p, a, cz, in, at.live, T - t, start_i, skip_i, y);
+    forward_apply<E, CH>(p, now.a, now.cz, in, at.live, T - t, now.start, now.skip, y);
+    now = next;
     y += p.out_step;
   }
   copy_wait<0>();
@@ -860,21 +864,23 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   const int64_t out = ((int64_t)at.b * p.T + t) * p.D + at.c0;
   E *dz = static_cast<E *>(p.dz) + out, *df = static_cast<E *>(p.df) + out;
   bool lost = false;
-  uint32_t start = 0, skip = 0;
-  Ch<CH> a[kSteps], c[kSteps], q[kSteps];
+  struct Round {
+    Ch<CH> a[kSteps], c[kSteps], q[kSteps];
+    uint32_t start, skip;
+  };
   // Round i's runs, its tile at step t_i.
-  auto runs = [&](int i, int t_i, int slot, int s) {
+  auto runs = [&](int i, int t_i, int slot, int s, Round &r) {
     __syncwarp();
     fetch(t_i - kAhead * p.step, ring[slot + kAhead >= kRing ? slot + kAhead - kRing : slot + kAhead]);
     flags.next(p, -p.step, i);
-    start = flags.start & 0xffu, skip = flags.skip & 0xffu;
+    r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
     copy_wait<kAhead>();
     __syncwarp();
-    backward_gates<E, CH>(ring[slot], lane, nb, skip, a, c, q);
+    backward_gates<E, CH>(ring[slot], lane, nb, r.skip, r.a, r.c, r.q);
     Ch<CH> H;
-    seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], lane, a, c, start, skip, H);
+    seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], lane, r.a, r.c, r.start, r.skip, H);
     ahead[s][warp][lane] = H;
-    if (lane == 0) seg[s].cut[warp] = start;
+    if (lane == 0) seg[s].cut[warp] = r.start;
     __syncthreads();
   };
   auto take_state = [&](int t_i) {
@@ -885,24 +891,25 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   };
   if constexpr (!kCluster) {
     int slot = 0;
+    Round r;
     for (int i = 0; i < rounds; ++i, t -= p.step) {
       Ch<CH> h = take_state(t);
-      runs(i, t, slot, i & 1);
+      runs(i, t, slot, i & 1, r);
       h = state_before<CH>(seg[i & 1], ahead[i & 1], lane, warp, h);
       const Ch<CH> ui = pass_block<CH>(seg[i & 1], lane, warp, u);
-      backward_apply<E, CH>(p, ring[slot], lane, a, c, q, h, ui, at.live, t < 0 ? 0 : T - t, start,
-                            skip, dz, df, sum);
+      backward_apply<E, CH>(p, ring[slot], lane, r.a, r.c, r.q, h, ui, at.live, t < 0 ? 0 : T - t,
+                            r.start, r.skip, dz, df, sum);
       dz -= p.out_step, df -= p.out_step;
       slot = slot == kRing - 1 ? 0 : slot + 1;
     }
   } else {  // as the forward pass's clusters
     int slot = 0, s = 0;
-    runs(0, t, 0, 0);
+    Round now, next;
+    runs(0, t, 0, 0, now);
     send_quad<CH>(seg[0], quads[0], at.rank, p.split, lane, warp);
     for (int i = 0; i < rounds; ++i, t -= p.step) {
-      const uint32_t start_i = start, skip_i = skip;
       const int next_slot = slot == kRing - 1 ? 0 : slot + 1, next_s = s == 2 ? 0 : s + 1;
-      if (i + 1 < rounds) runs(i + 1, t - p.step, next_slot, next_s);
+      if (i + 1 < rounds) runs(i + 1, t - p.step, next_slot, next_s, next);
       Quads<CH> &from = quads[i & 1];
       const Ch<CH> mine = pass_cluster<CH>(from, &from.arrived, (i >> 1) & 1, lost, at.rank,
                                            p.split, lane, warp, u);
@@ -912,9 +919,12 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
       }
       const Ch<CH> h = state_before<CH>(seg[s], ahead[s], lane, warp, take_state(t));
       const Ch<CH> ui = inside_quad<CH>(seg[s], lane, warp, quad_cuts(seg[s], warp / kQuad), mine);
-      backward_gates<E, CH>(ring[slot], lane, nb, skip_i, a, c, q);
-      backward_apply<E, CH>(p, ring[slot], lane, a, c, q, h, ui, at.live, t < 0 ? 0 : T - t,
-                            start_i, skip_i, dz, df, sum);
+      // two channels' gates of two rounds do not fit the registers: computed twice
+      if constexpr (CH == 2)
+        backward_gates<E, CH>(ring[slot], lane, nb, now.skip, now.a, now.c, now.q);
+      backward_apply<E, CH>(p, ring[slot], lane, now.a, now.c, now.q, h, ui, at.live,
+                            t < 0 ? 0 : T - t, now.start, now.skip, dz, df, sum);
+      now = next;
       dz -= p.out_step, df -= p.out_step;
       slot = next_slot, s = next_s;
     }
