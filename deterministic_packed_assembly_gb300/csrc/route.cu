@@ -576,8 +576,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
   const uint64_t n_first = ((uint64_t)blockIdx.x * kWarps + warp) * G + group;
   const E *src = static_cast<const E *>(p.logits) + (int64_t)n_first * p.logits_row + i0;
   E *dst = static_cast<E *>(p.dlogits) + (int64_t)n_first * p.E + i0;
-  auto counts = [&](uint64_t n) { return n < p.N && !(p.doc && __ldg(p.doc + n) < 0); };
-  bool next_real = counts(n_first);
+  // a token's document id is read two steps ahead: whether its logits are to be read
+  // is known when the step before begins
+  auto document = [&](uint64_t n) { return n < p.N ? (p.doc ? __ldg(p.doc + n) : 0) : -1; };
+  bool next_real = document(n_first) >= 0;
+  int ahead = document(n_first + step);
   Piece<E, R> next;
   if (next_real) next.load(src, i0, p.E, p.wide);
   // A lane has one of the token's choices at most, or goes through several.
@@ -606,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
     const int id = next_id;
     const float w = next_w, dw = next_dw;
     n0 += step, src += (int64_t)step * p.logits_row;
-    next_real = counts(n0 + group);
+    next_real = ahead >= 0;
+    ahead = document(n0 + group + step);
     if (next_real) next.load(src, i0, p.E, p.wide);
     load_choice(n0 + group);
     const uint32_t at = real ? (uint32_t)n * p.k : 0;
