@@ -213,10 +213,13 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     const uint64_t n0 = t * tokens;
     __syncthreads();  // the last tile is done with
     const uint32_t here = p.N - n0 < tokens ? (uint32_t)(p.N - n0) : tokens;
+    // on its way beside the copies
+    const int document =
+        token < here ? (p.doc ? __ldg(p.doc + n0 + token) : 0) : -1;
     if (p.dtype == NS_F32) load_tile<float, SG, kPitch>(p, n0, here, tile);
     else if (p.dtype == NS_BF16) load_tile<__nv_bfloat16, SG, kPitch>(p, n0, here, tile);
     else load_tile<__half, SG, kPitch>(p, n0, here, tile);
-    const bool real = token < here && !(p.doc && __ldg(p.doc + n0 + token) < 0);
+    const bool real = document >= 0;
     __syncthreads();
     // beyond are places beyond the last expert, and all of a token that does not count
     const int used = !real || p.E <= lp * SG ? 0 : (int)min(p.E - lp * SG, (uint32_t)SG);
