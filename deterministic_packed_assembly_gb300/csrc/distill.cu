@@ -8,7 +8,7 @@
 // written, and a row (256 KB for a vocabulary of 128K in 16 bits) is read from
 // memory once: a cluster of C blocks keeps the row in its shared memory, a slice
 // each.  A thread has its own 16-byte chunks of the slice: it copies them in
-// asynchronously, reduces them to a running maximum and sum as they arrive, and,
+// asynchronously, reduces them to a reference and a sum as they arrive, and,
 // once the blocks have exchanged theirs, turns each into the gradient and starts
 // the copy of the cluster's next row into its place.  So the copies of a row run
 // beside the stores of the one before.  The teacher's K entries are few: two
@@ -67,11 +67,16 @@ __device__ __forceinline__ void copy_wait_left(int left) {
   else copy_wait<0>();
 }
 
-// A running maximum (-inf at first) and the sum of exp((x - maximum) / temp).
+// A reference (-inf at first), and the sum of exp((x - reference) / temp).  The
+// reference is one of the logits and no more than a few powers of two below the
+// largest so far: it is raised only when a chunk's sum passes kFarAbove, so that the
+// maximum of every chunk need not be found; an exponent's rounding stays that of a
+// number of a few units.
+constexpr float kFarAbove = 256.0f;
 struct MaxSum {
   float m, s;
 };
-// What is taken from x: the maximum, where -inf leaves x = -inf alone.
+// What is taken from x: the reference, where -inf leaves x = -inf alone.
 __device__ __forceinline__ float base_of(float m) { return m == kNegInf ? 0.0f : m; }
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float scale) {
   MaxSum r;
@@ -79,6 +84,29 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float scale) {
   const float base = base_of(r.m);
   r.s = a.s * exp2_sfu((a.m - base) * scale) + b.s * exp2_sfu((b.m - base) * scale);
   return r;
+}
+
+template <class E>
+__device__ __forceinline__ float chunk_max(uint4 v) {
+  Ch<2> x[8 / sizeof(E)];
+  widen_chunk<E>(v, x);
+  float top = fmaxf(x[0].v[0], x[0].v[1]);
+#pragma unroll
+  for (int k = 1; k < (int)(8 / sizeof(E)); ++k) top = fmaxf(top, fmaxf(x[k].v[0], x[k].v[1]));
+  return top;
+}
+// Sum of 2^((x + minus) scale).
+template <class E>
+__device__ __forceinline__ float chunk_sum(uint4 v, float minus, Ch<2> scale) {
+  Ch<2> x[8 / sizeof(E)], sum;
+  widen_chunk<E>(v, x);
+#pragma unroll
+  for (int k = 0; k < (int)(8 / sizeof(E)); ++k) {
+    const Ch<2> y = (x[k] + splat<2>(minus)) * scale;
+    const Ch<2> e = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+    sum = k == 0 ? e : sum + e;
+  }
+  return sum.v[0] + sum.v[1];
 }
 
 __device__ __forceinline__ float load_top(const void *top, int dtype, int64_t i) {
@@ -513,7 +541,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
       mine_next = s.mine;
       from += (int64_t)next * p.logits_row + s.from;
     }
-    // Maximum and sum of this thread's chunks, as they arrive.
+    // The sum of this thread's chunks, as they arrive.
     MaxSum acc = {kNegInf, 0.0f};
     uint32_t c = tid;
 #pragma unroll 1
@@ -521,26 +549,26 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
       uint32_t next_c = c;
       const uint32_t end = (g + 1) * quarter, stop = min(end, mine);
       copy_wait_left(kGrad ? kGroups - 1 - g : kGroups - 1);
+      if (g == 0) {  // the warp's first chunks give its reference
+        float top = kNegInf;
+        if (c < stop) top = chunk_max<E>(slice[c]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        acc.m = top;
+      }
 #pragma unroll 2
       for (; c < stop; c += nthr) {
-        Ch<2> x[kN / 2];
-        widen_chunk<E>(slice[c], x);
-        float top = fmaxf(x[0].v[0], x[0].v[1]);
-#pragma unroll
-        for (int k = 1; k < kN / 2; ++k) top = fmaxf(top, fmaxf(x[k].v[0], x[k].v[1]));
-        if (top > acc.m) {
-          acc.s *= exp2_sfu((acc.m - top) * p.scale);
-          acc.m = top;
+        const uint4 v = slice[c];
+        float sum = chunk_sum<E>(v, -base_of(acc.m), scale);
+        if (acc.m == kNegInf || !(sum < kFarAbove)) {  // or a NaN
+          const float top = chunk_max<E>(v);
+          if (top > acc.m) {
+            acc.s *= exp2_sfu((acc.m - top) * p.scale);
+            acc.m = top;
+          }
+          sum = chunk_sum<E>(v, -base_of(acc.m), scale);
         }
-        const Ch<2> base = splat<2>(-base_of(acc.m));
-        Ch<2> sum;
-#pragma unroll
-        for (int k = 0; k < kN / 2; ++k) {
-          const Ch<2> y = (x[k] + base) * scale;
-          const Ch<2> v = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
-          sum = k == 0 ? v : sum + v;
-        }
-        acc.s += sum.v[0] + sum.v[1];
+        acc.s += sum;
       }
       if (!kGrad) {  // nothing else wants the chunks
         for (; next_c < min(end, mine_next); next_c += nthr)

@@ -58,35 +58,23 @@ template <>
 struct alignas(8) Ch<2> {
   float v[2];
 };
-__device__ __forceinline__ uint64_t bits(Ch<2> a) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.v[0]), "f"(a.v[1]));
-  return r;
-}
-__device__ __forceinline__ Ch<2> unbits(uint64_t r) {
-  Ch<2> a;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.v[0]), "=f"(a.v[1]) : "l"(r));
-  return a;
-}
+__device__ __forceinline__ float2 pair(Ch<2> a) { return make_float2(a.v[0], a.v[1]); }
 __device__ __forceinline__ Ch<1> fma(Ch<1> a, Ch<1> b, Ch<1> c) {
   return {fmaf(a.v[0], b.v[0], c.v[0])};
 }
 __device__ __forceinline__ Ch<2> fma(Ch<2> a, Ch<2> b, Ch<2> c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return unbits(r);
+  const float2 r = __ffma2_rn(pair(a), pair(b), pair(c));
+  return {r.x, r.y};
 }
 __device__ __forceinline__ Ch<1> operator*(Ch<1> a, Ch<1> b) { return {a.v[0] * b.v[0]}; }
 __device__ __forceinline__ Ch<2> operator*(Ch<2> a, Ch<2> b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return unbits(r);
+  const float2 r = __fmul2_rn(pair(a), pair(b));
+  return {r.x, r.y};
 }
 __device__ __forceinline__ Ch<1> operator+(Ch<1> a, Ch<1> b) { return {a.v[0] + b.v[0]}; }
 __device__ __forceinline__ Ch<2> operator+(Ch<2> a, Ch<2> b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return unbits(r);
+  const float2 r = __fadd2_rn(pair(a), pair(b));
+  return {r.x, r.y};
 }
 template <int CH>
 __device__ __forceinline__ Ch<CH> splat(float x) {
