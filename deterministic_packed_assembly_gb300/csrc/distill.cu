@@ -54,6 +54,7 @@ struct DistillParams {
   uint32_t N, V, K;
   int32_t top_dtype, ids_64;
   float temp, inv_temp, scale;  // scale = log2 e / temp
+  bool same;                    // every row starts at the same place of 16 bytes
   uint32_t slice;               // 16-byte chunks of a block's slice
   float *loss;
   void *dlogits;
@@ -380,20 +381,25 @@ __device__ __forceinline__ RowStats row_stats(const DistillParams &p, Shared &sh
                                               uint32_t C, bool &lost) {
   if (!lost && !stats_wait(sh, round)) lost = true;
   const float4 *v = sh.stats[round % kPlaces];
-  RowStats r = {{v[0].x, v[0].y}, v[0].z, v[0].w};
-  for (uint32_t i = 1; i < C; ++i) {
-    r.all = join(r.all, {v[i].x, v[i].y}, p.scale);
+  RowStats r = {{v[0].x, 0.0f}, 0.0f, v[0].w};
+  for (uint32_t i = 1; i < C; ++i) r.all.m = fmaxf(r.all.m, v[i].x);
+  const float base = base_of(r.all.m);
+  for (uint32_t i = 0; i < C; ++i) {
+    r.all.s += v[i].y * exp2_sfu((v[i].x - base) * p.scale);
     r.parts += v[i].z;
   }
   if (lost) r.all.s = r.parts = __int_as_float(0x7fffffff);  // shows in loss and gradient
   return r;
 }
+// The lanes' sums together: referred to the largest reference first.
 __device__ __forceinline__ MaxSum warp_join(MaxSum a, float scale) {
+  float m = a.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)},
-             scale);
-  return a;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = a.s * exp2_sfu((a.m - base_of(m)) * scale);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return {m, s};
 }
 
 // An entry warp of a block, for the even rows of its walk or the odd ones.
@@ -516,8 +522,9 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
   auto skip = [&](uint32_t row) { unlearned<E, kGrad>(p, row, rank, nthr); };
   RowWalk walk(blockIdx.x / C, stride);
   uint32_t row = walk.learned(p, lane, skip);
+  RowSlice<E> slice_of(p, row < p.N ? row : 0, rank);  // of the row in hand
   if (row < p.N) {
-    const RowSlice<E> s(p, row, rank);
+    const RowSlice<E> s = slice_of;
     const E *from = logits + (int64_t)row * p.logits_row + s.from;
     uint32_t c = tid;
 #pragma unroll 1
@@ -529,17 +536,14 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
   for (uint32_t i = 0; row < p.N; ++i) {
     const uint32_t next = walk.learned(p, lane, skip);
     const float weight = kGrad && p.weight ? p.weight[row] : 1.0f;
-    uint32_t mine, mine_next = 0;
-    int at, wide = 0;
-    {
-      const RowSlice<E> s(p, row, rank);
-      mine = s.mine, at = s.from;
-    }
+    const uint32_t mine = slice_of.mine;
+    const int at = slice_of.from;
+    uint32_t mine_next = 0;
     const E *from = logits;
     if (next < p.N) {
-      const RowSlice<E> s(p, next, rank);
-      mine_next = s.mine;
-      from += (int64_t)next * p.logits_row + s.from;
+      if (!p.same) slice_of = RowSlice<E>(p, next, rank);
+      mine_next = slice_of.mine;
+      from += (int64_t)next * p.logits_row + slice_of.from;
     }
     // The sum of this thread's chunks, as they arrive.
     MaxSum acc = {kNegInf, 0.0f};
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
       const float f = acc.s == 0.0f ? 0.0f : w * mass / acc.s;  // of the exponentials
       const Ch<2> base = splat<2>(-base_of(acc.m)), by = splat<2>(f);
       E *to = dlogits + (int64_t)row * p.dlogits_row + at;
-      wide = ((uintptr_t)to & 15) == 0;
+      const bool wide = ((uintptr_t)to & 15) == 0;
       c = tid;
 #pragma unroll 1
       for (uint32_t end = quarter; end <= kGroups * quarter; end += quarter) {
@@ -668,6 +672,7 @@ size_t distill_smem(uint32_t slice, uint32_t K, bool grad) {
 template <class E, bool kGrad>
 cudaError_t launch(DistillParams &p, cudaStream_t st) {
   const uint32_t chunks = (uint32_t)((uint64_t)p.V * sizeof(E) / 16);  // of a row at most
+  p.same = p.logits_row * sizeof(E) % 16 == 0;
   uint32_t C = 1;
   while (C < kMaxCluster && chunks > C * (kSliceBytes / 16)) C *= 2;
   p.slice = chunks ? (chunks + C - 1) / C : 1;
