@@ -627,9 +627,11 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
   copy_wait<0>();
 }
 
-// Bytes of a block's slice: three blocks share an SM, so that one's stores and
-// copies run beside another's sums.
-constexpr uint64_t kSliceBytes = 66 * 1024;
+// Bytes of a block's slice at most: three blocks share an SM below 72 KB, so that
+// one's stores and copies run beside another's sums, two above.  (Rows of 297 KB,
+// 151936 bfloat16: 722 us for 8192 rows with four slices of 74 KB, 818 us with
+// eight of 37 KB.)
+constexpr uint64_t kSliceBytes = 80 * 1024;
 
 // Clusters that the GPU holds at a time (fewer than its room for their blocks,
 // which have to lie in one part of it), asked once for a layout and device.
@@ -677,8 +679,11 @@ cudaError_t launch(DistillParams &p, cudaStream_t st) {
   while (C < kMaxCluster && chunks > C * (kSliceBytes / 16)) C *= 2;
   p.slice = chunks ? (chunks + C - 1) / C : 1;
   const size_t smem = distill_smem(p.slice, p.K, kGrad);
+  // A warp's work on a row beside its chunks is worth some 60 of them: eight warps
+  // for the largest slices (64 KB: 585 us a pass against 640 us with four), four for
+  // smaller ones (37 KB: 743 us with four, 818 us with eight), two for the smallest.
   const unsigned threads =
-      (p.slice >= 1024 ? 256 : p.slice >= 256 ? 128 : 64) + 32 * kEntryWarps;
+      (p.slice >= 3500 ? 256 : p.slice >= 1024 ? 128 : 64) + 32 * kEntryWarps;
   auto *k = distill_kernel<E, kGrad>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
