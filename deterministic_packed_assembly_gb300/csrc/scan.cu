@@ -51,7 +51,8 @@ struct ScanParams {
   uint32_t split;   // blocks of a cluster, along time
   uint32_t first;   // the launch's first (row, group)
   uint32_t sums;    // partial sums of the bias's gradient that a row has
-  bool wide;        // rows are copied 16 bytes at a time
+  int wide;         // bytes that rows are copied by: 16, 8, 4, or 2
+  const void *z_end, *f_end, *dy_end;
   int step;         // steps from a warp's segment to its next one
   // and what that is in z, f, dy, in a contiguous [T][D] and in the saved states
   int64_t z_step, f_step, dy_step, out_step, state_step;
@@ -155,46 +156,117 @@ __device__ __forceinline__ void gate(Ch<CH> f, Ch<CH> nb, Ch<CH> &r, Ch<CH> &c, 
 // (Prefetched into registers instead, the backward kernel spilled at 128 of them
 // and ran 16 warps an SM.)
 constexpr int kRing = 3;
+// Single 16-bit channels are copied as the 17 words that 32 of them may touch: their
+// rows have room for 34, and begin at either half of the first word.
+template <class E, int CH>
+constexpr bool kHalves = sizeof(E) == 2 && CH == 1;
+template <class E, int CH>
+constexpr int kRowRoom = kHalves<E, CH> ? 34 : 32;
 template <class E, int CH, int A>
 struct alignas(16) Stage {
-  Raw<E, CH> v[A][kSteps][32];
+  Raw<E, CH> v[A][kSteps][kRowRoom<E, CH>];
 };
 
-// Copies of a segment's rows.  `wide`: rows, strides and widths are multiples of 16
-// bytes, and a lane copies 16 bytes of every fourth row; else its own channels of
-// every row (a single 16-bit one, which no asynchronous copy takes, by way of a
-// register).
-template <class E, int CH>
+// An array that is copied: where it lies, and its strides.
+template <class E>
+struct Source {
+  const E *at;      // this lane's place in the segment that is copied next
+  int64_t time;     // elements to the next step
+  const E *begin, *end;  // of the array (kHalves)
+};
+
+// Copies of a segment's rows of 128 bytes by `p.wide` bytes a lane: 16 (kWide) where
+// rows, strides and widths are multiples of them, a lane copying from every fourth
+// row; 8; or 4.  Rows of 16-bit channels that begin at any 2 bytes are copied in the words
+// they touch.
+template <class E, int CH, bool kWide>
 struct Copier {
-  static constexpr int kN = 16 / sizeof(E), kPerRow = 32 * CH / kN, kRows = 32 / kPerRow;
-  int row;  // the first row that this lane copies from, far out where it has none
-  // This lane's place in a group, in elements from its first row's first channel.
-  __device__ __forceinline__ int64_t set(int64_t time, uint32_t width, bool wide, int lane) {
-    const int at = wide ? lane % kPerRow * kN : lane * CH;
-    row = wide ? lane / kPerRow : 0;
-    const int64_t off = row * time + at;
-    if ((uint32_t)at >= width) row = kSteps;
-    return off;
-  }
-  // Copy steps [0, n) of the segment whose place is `from`.
-  __device__ __forceinline__ void copy(const E *from, int64_t time, int n, bool wide, int lane,
-                                       Raw<E, CH> (&dst)[kSteps][32]) const {
-    if (wide) {
-      E *to = reinterpret_cast<E *>(dst) + lane * kN;
-#pragma unroll
-      for (int s = 0; s < kSteps; s += kRows)
-        if (s + row < n) copy_async<16>(to + s * 32 * CH, from + s * time);
+  int row;        // the first row that this lane copies from, far out where it has none
+  uint32_t into;  // byte of its row that it copies to
+
+  // Sets this lane's place in an array whose segment's group starts at `group`.
+  __device__ __forceinline__ Source<E> set(const ScanParams &p, const E *group, int64_t time,
+                                           uint32_t width, int lane, const void *begin,
+                                           const void *end) {
+    if constexpr (kHalves<E, CH>) {
+      row = lane <= 16 ? 0 : kSteps;
+      into = lane * 4;
+      return {group, time, static_cast<const E *>(begin), static_cast<const E *>(end)};
     } else {
+      const int bytes = kWide ? 16 : p.wide, per_row = 128 / bytes, first = lane / per_row;
+      into = lane % per_row * bytes;
+      const uint32_t at = into / sizeof(E);
+      row = at < width ? first : kSteps;
+      return {group + first * time + at, time, nullptr, nullptr};
+    }
+  }
+  template <int kBytes>
+  __device__ __forceinline__ void rows(const Source<E> &from, int n, unsigned char *to,
+                                       int lane) const {
+    constexpr int kRows = kBytes / 4;
+    to += lane / (32 / kRows) * 128 + into;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s + row < n) {
-          if constexpr (sizeof(E) * CH == 4)
-            copy_async<4>(&dst[s][lane], from + s * time);
-          else
-            dst[s][lane] = from[s * time];
+    for (int s = 0; s < kSteps; s += kRows)
+      if (s + row < n) copy_async<kBytes>(to + s * 128, from.at + s * from.time);
+  }
+  // Copy steps [0, n) of the segment.
+  __device__ __forceinline__ void copy(const ScanParams &p, const Source<E> &from, int n,
+                                       uint32_t width, int lane,
+                                       Raw<E, CH> (&dst)[kSteps][kRowRoom<E, CH>]) const {
+    unsigned char *to = reinterpret_cast<unsigned char *>(dst);
+    if constexpr (kHalves<E, CH>) {
+      // words of rows of even and of odd steps: with an odd stride the halves alternate,
+      // two steps on they are the same
+      const uintptr_t even = (uintptr_t)from.at, odd = (uintptr_t)(from.at + from.time);
+      const char *word[2] = {(const char *)(even & ~(uintptr_t)3) + into,
+                             (const char *)(odd & ~(uintptr_t)3) + into};
+      const int64_t two_steps = from.time * 4;
+      const int channels = (int)min(width, 32u);
+      const bool has[2] = {lane < ((int)(even & 2) / 2 + channels + 1) / 2,
+                           lane < ((int)(odd & 2) / 2 + channels + 1) / 2};
+      to += into;
+      if (word[0] >= (const char *)from.begin && from.at + kSteps * from.time + 34 <= from.end) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          if (s + row < n && has[s % 2])
+            copy_async<4>(to + s * sizeof(dst[0]), word[s % 2] + s / 2 * two_steps);
+      } else {  // near the array's ends, whose elements may share a word with nothing
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          if (s + row >= n || !has[s % 2]) continue;
+          const E *w = reinterpret_cast<const E *>(word[s % 2] + s / 2 * two_steps);
+          E *into_row = reinterpret_cast<E *>(to + s * sizeof(dst[0]));
+          if (w >= from.begin) into_row[0] = w[0];
+          if (w + 1 >= from.begin && w + 2 <= from.end) into_row[1] = w[1];
         }
       }
+    } else {
+      if (kWide) rows<16>(from, n, to, lane);
+      else if (p.wide == 8) rows<8>(from, n, to, lane);
+      else rows<4>(from, n, to, lane);
     }
+  }
+};
+
+// Where a lane's channels lie in a row of a stage: in kHalves one element on where the
+// row begins at a word's second half, which alternates with the step where the
+// step's stride is odd.
+template <class E, int CH, int A>
+struct Places {
+  int even[A], odd[A];
+  __device__ __forceinline__ void set(int k, const E *group, int64_t time, int lane) {
+    even[k] = odd[k] = lane;
+    if constexpr (kHalves<E, CH>) {
+      const int half = (int)((uintptr_t)group / 2 & 1);
+      even[k] += half;
+      odd[k] += (half + (int)time) & 1;
+    }
+  }
+  __device__ __forceinline__ Ch<CH> read(const Stage<E, CH, A> &in, int k, int s, int lane) const {
+    if constexpr (kHalves<E, CH>)
+      return widen<E, CH>(in.v[k][s][s % 2 ? odd[k] : even[k]]);
+    else
+      return widen<E, CH>(in.v[k][s][lane]);
   }
 };
 
@@ -432,14 +504,15 @@ __device__ __forceinline__ void cluster_begin(Quads<CH> (&quads)[2]) {
 // ---- forward --------------------------------------------------------------------
 // A segment's gates a and inputs c z; a = 1, c z = 0 at skipped steps.
 template <class E, int CH>
-__device__ __forceinline__ void forward_gates(const Stage<E, CH, 2> &in, int lane, Ch<CH> nb,
+__device__ __forceinline__ void forward_gates(const Stage<E, CH, 2> &in,
+                                              const Places<E, CH, 2> &at, int lane, Ch<CH> nb,
                                               uint32_t skip, Ch<CH> (&a)[kSteps],
                                               Ch<CH> (&cz)[kSteps]) {
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     Ch<CH> r, c;
-    gate<CH>(widen<E, CH>(in.v[1][s][lane]), nb, r, c, a[s]);
-    cz[s] = c * widen<E, CH>(in.v[0][s][lane]);
+    gate<CH>(at.read(in, 1, s, lane), nb, r, c, a[s]);
+    cz[s] = c * at.read(in, 0, s, lane);
   }
   if (skip) {  // the same for the warp
 #pragma unroll
@@ -492,7 +565,7 @@ __device__ __forceinline__ void forward_apply(const ScanParams &p, const Ch<CH> 
 }
 
 // Blocks that each take a unit's whole row.
-template <class E, int CH>
+template <class E, int CH, bool kWide>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     scan_forward_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -503,16 +576,20 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
   release_dependents();
   const int T = (int)p.T, rounds = (T + kTile - 1) / kTile;
   int t = warp * kSteps;  // may lie past the row
-  Copier<E, CH> copier;
-  const E *z_from = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
-  const E *f_from = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
-  z_from += copier.set(p.z_time, p.D - at.cg, p.wide, lane);
-  f_from += copier.set(p.f_time, p.D - at.cg, p.wide, lane);
+  Copier<E, CH, kWide> copier;
+  Places<E, CH, 2> places;
+  const uint32_t width = p.D - at.cg;
+  const E *group = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
+  Source<E> z_from = copier.set(p, group, p.z_time, width, lane, p.z, p.z_end);
+  places.set(0, group, p.z_time, lane);
+  group = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
+  Source<E> f_from = copier.set(p, group, p.f_time, width, lane, p.f, p.f_end);
+  places.set(1, group, p.f_time, lane);
   auto fetch = [&](int at_step, Stage<E, CH, 2> &to) {
     const int n = steps_at(T, at_step);
-    copier.copy(z_from, p.z_time, n, p.wide, lane, to.v[0]);
-    copier.copy(f_from, p.f_time, n, p.wide, lane, to.v[1]);
-    z_from += p.z_step, f_from += p.f_step;
+    copier.copy(p, z_from, n, width, lane, to.v[0]);
+    copier.copy(p, f_from, n, width, lane, to.v[1]);
+    z_from.at += p.z_step, f_from.at += p.f_step;
     copy_commit();
   };
 #pragma unroll
@@ -535,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     copy_wait<kRing - 1>();
     __syncwarp();
     Ch<CH> a[kSteps], cz[kSteps];
-    forward_gates<E, CH>(ring[slot], lane, nb, skip, a, cz);
+    forward_gates<E, CH>(ring[slot], places, lane, nb, skip, a, cz);
     slot = slot == kRing - 1 ? 0 : slot + 1;
     Exchange<CH, kWarps> &x = seg[i & 1];
     x.run[warp][lane] = forward_run<CH>(a, cz, start);
@@ -558,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
 // that their way between the blocks lies beside this and the next round's runs.
 // Two rounds' gates are in registers: two blocks an SM, which is what the grids of
 // clusters hold anyway.
-template <class E, int CH>
+template <class E, int CH, bool kWide>
 __global__ void __launch_bounds__(kThreads, 2)
     scan_forward_cluster_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -571,16 +648,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_begin<CH>(quads);
   const int T = (int)p.T, rounds = (T + p.step - 1) / p.step;
   int t = (int)at.rank * kTile + warp * kSteps;  // may lie past the row
-  Copier<E, CH> copier;
-  const E *z_from = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
-  const E *f_from = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
-  z_from += copier.set(p.z_time, p.D - at.cg, p.wide, lane);
-  f_from += copier.set(p.f_time, p.D - at.cg, p.wide, lane);
+  Copier<E, CH, kWide> copier;
+  Places<E, CH, 2> places;
+  const uint32_t width = p.D - at.cg;
+  const E *group = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
+  Source<E> z_from = copier.set(p, group, p.z_time, width, lane, p.z, p.z_end);
+  places.set(0, group, p.z_time, lane);
+  group = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
+  Source<E> f_from = copier.set(p, group, p.f_time, width, lane, p.f, p.f_end);
+  places.set(1, group, p.f_time, lane);
   auto fetch = [&](int at_step, Stage<E, CH, 2> &to) {
     const int n = steps_at(T, at_step);
-    copier.copy(z_from, p.z_time, n, p.wide, lane, to.v[0]);
-    copier.copy(f_from, p.f_time, n, p.wide, lane, to.v[1]);
-    z_from += p.z_step, f_from += p.f_step;
+    copier.copy(p, z_from, n, width, lane, to.v[0]);
+    copier.copy(p, f_from, n, width, lane, to.v[1]);
+    z_from.at += p.z_step, f_from.at += p.f_step;
     copy_commit();
   };
 #pragma unroll
@@ -608,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
     copy_wait<kRing - 1>();
     __syncwarp();
-    forward_gates<E, CH>(ring[i % kRing], lane, nb, r.skip, r.a, r.cz);
+    forward_gates<E, CH>(ring[i % kRing], places, lane, nb, r.skip, r.a, r.cz);
     Exchange<CH, kWarps> &x = seg[i % 3];
     x.run[warp][lane] = forward_run<CH>(r.a, r.cz, r.start);
     if (lane == 0) x.cut[warp] = r.start;
@@ -682,13 +763,14 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
 // A segment's gates: a, c and q = a c from the unrounded gate; a = 1, c = q = 0 at
 // skipped steps.
 template <class E, int CH>
-__device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in, int lane, Ch<CH> nb,
+__device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in,
+                                               const Places<E, CH, 3> &at, int lane, Ch<CH> nb,
                                                uint32_t skip, Ch<CH> (&a)[kSteps],
                                                Ch<CH> (&c)[kSteps], Ch<CH> (&q)[kSteps]) {
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     Ch<CH> r;
-    gate<CH>(widen<E, CH>(in.v[1][s][lane]), nb, r, c[s], a[s]);
+    gate<CH>(at.read(in, 1, s, lane), nb, r, c[s], a[s]);
     q[s] = r * c[s];
   }
   if (skip) {
@@ -703,7 +785,8 @@ __device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in, int la
 }
 // (A, U) of the segment, and H.
 template <class E, int CH>
-__device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in, int lane,
+__device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
+                                                const Places<E, CH, 3> &at, int lane,
                                                 const Ch<CH> (&a)[kSteps],
                                                 const Ch<CH> (&c)[kSteps], uint32_t start,
                                                 uint32_t skip, Ch<CH> &H) {
@@ -713,22 +796,22 @@ __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in, int l
   if ((start | skip) == 0) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      H = fma(a[s], H, c[s] * widen<E, CH>(in.v[0][s][lane]));
+      H = fma(a[s], H, c[s] * at.read(in, 0, s, lane));
       run.A = run.A * a[s];
     }
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s)
-      run.H = a[s] * (widen<E, CH>(in.v[2][s][lane]) + run.H);
+      run.H = a[s] * (at.read(in, 2, s, lane) + run.H);
   } else {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const Ch<CH> cz = pick((skip >> s) & 1u, zero, c[s] * widen<E, CH>(in.v[0][s][lane]));
+      const Ch<CH> cz = pick((skip >> s) & 1u, zero, c[s] * at.read(in, 0, s, lane));
       H = fma(a[s], pick((start >> s) & 1u, zero, H), cz);
       run.A = run.A * a[s];
     }
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
-      const Ch<CH> g = pick((skip >> s) & 1u, zero, widen<E, CH>(in.v[2][s][lane]));
+      const Ch<CH> g = pick((skip >> s) & 1u, zero, at.read(in, 2, s, lane));
       run.H = pick((start >> s) & 1u, zero, a[s] * (g + run.H));
     }
   }
@@ -752,7 +835,7 @@ __device__ __forceinline__ Ch<CH> state_before(const Exchange<CH, kWarps> &x,
 // The segment's gradients, from the state before it and u after it.
 template <class E, int CH>
 __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<E, CH, 3> &in,
-                                               int lane, const Ch<CH> (&a)[kSteps],
+                                               const Places<E, CH, 3> &at, int lane, const Ch<CH> (&a)[kSteps],
                                                const Ch<CH> (&c)[kSteps], Ch<CH> (&q)[kSteps],
                                                Ch<CH> h, Ch<CH> u, bool live, int left,
                                                uint32_t start, uint32_t skip, E *dz, E *df,
@@ -762,13 +845,13 @@ __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<
   if ((start | skip) == 0) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {  // q takes p_t - z_t in
-      const Ch<CH> z = widen<E, CH>(in.v[0][s][lane]);
+      const Ch<CH> z = at.read(in, 0, s, lane);
       q[s] = q[s] * sub(h, z);
       h = fma(a[s], h, c[s] * z);
     }
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
-      const Ch<CH> d = widen<E, CH>(in.v[2][s][lane]) + u, vf = q[s] * d;
+      const Ch<CH> d = at.read(in, 2, s, lane) + u, vf = q[s] * d;
       u = a[s] * d;
       sum = sum + vf;
       if (live) {
@@ -779,7 +862,7 @@ __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<
   } else {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const Ch<CH> z = pick((skip >> s) & 1u, zero, widen<E, CH>(in.v[0][s][lane]));
+      const Ch<CH> z = pick((skip >> s) & 1u, zero, at.read(in, 0, s, lane));
       const Ch<CH> before = pick((start >> s) & 1u, zero, h);
       q[s] = q[s] * sub(before, z);
       h = fma(a[s], before, c[s] * z);
@@ -787,7 +870,7 @@ __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
       const bool gone = (skip >> s) & 1u;
-      const Ch<CH> d = pick(gone, zero, widen<E, CH>(in.v[2][s][lane])) + u;
+      const Ch<CH> d = pick(gone, zero, at.read(in, 2, s, lane)) + u;
       const Ch<CH> vf = pick(gone, zero, q[s] * d);
       u = pick((start >> s) & 1u, zero, a[s] * d);
       sum = sum + vf;
@@ -814,7 +897,7 @@ __device__ __forceinline__ void store_sums(const ScanParams &p, const Place &at,
     store_channels<CH>(to, (int64_t)r * p.D, at.live, splat<CH>(0.0f));
 }
 
-template <class E, int CH, bool kCluster>
+template <class E, int CH, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     scan_backward_kernel(const ScanParams p) {
   constexpr int kSegs = kCluster ? 3 : 2;
@@ -832,19 +915,24 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   const int back = kWarps - 1 - warp;  // this warp's segment of a tile
   // negative in a tile before the first one, past the end of the walk
   int t = ((T + kTile - 1) / kTile - 1 - (int)at.rank) * kTile + back * kSteps;
-  Copier<E, CH> copier;
-  const E *z_from = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
-  const E *f_from = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
-  const E *g_from = static_cast<const E *>(p.dy) + (int64_t)at.b * p.dy_row + t * p.dy_time + at.cg;
-  z_from += copier.set(p.z_time, p.D - at.cg, p.wide, lane);
-  f_from += copier.set(p.f_time, p.D - at.cg, p.wide, lane);
-  g_from += copier.set(p.dy_time, p.D - at.cg, p.wide, lane);
+  Copier<E, CH, kWide> copier;
+  Places<E, CH, 3> places;
+  const uint32_t width = p.D - at.cg;
+  const E *group = static_cast<const E *>(p.z) + (int64_t)at.b * p.z_row + t * p.z_time + at.cg;
+  Source<E> z_from = copier.set(p, group, p.z_time, width, lane, p.z, p.z_end);
+  places.set(0, group, p.z_time, lane);
+  group = static_cast<const E *>(p.f) + (int64_t)at.b * p.f_row + t * p.f_time + at.cg;
+  Source<E> f_from = copier.set(p, group, p.f_time, width, lane, p.f, p.f_end);
+  places.set(1, group, p.f_time, lane);
+  group = static_cast<const E *>(p.dy) + (int64_t)at.b * p.dy_row + t * p.dy_time + at.cg;
+  Source<E> g_from = copier.set(p, group, p.dy_time, width, lane, p.dy, p.dy_end);
+  places.set(2, group, p.dy_time, lane);
   auto fetch = [&](int at_step, Stage<E, CH, 3> &to) {
     const int n = steps_at(T, at_step);
-    copier.copy(z_from, p.z_time, n, p.wide, lane, to.v[0]);
-    copier.copy(f_from, p.f_time, n, p.wide, lane, to.v[1]);
-    copier.copy(g_from, p.dy_time, n, p.wide, lane, to.v[2]);
-    z_from -= p.z_step, f_from -= p.f_step, g_from -= p.dy_step;
+    copier.copy(p, z_from, n, width, lane, to.v[0]);
+    copier.copy(p, f_from, n, width, lane, to.v[1]);
+    copier.copy(p, g_from, n, width, lane, to.v[2]);
+    z_from.at -= p.z_step, f_from.at -= p.f_step, g_from.at -= p.dy_step;
     copy_commit();
   };
   // Copies run two tiles ahead in a block alone, one in a cluster, whose blocks
@@ -876,9 +964,9 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
     copy_wait<kAhead>();
     __syncwarp();
-    backward_gates<E, CH>(ring[slot], lane, nb, r.skip, r.a, r.c, r.q);
+    backward_gates<E, CH>(ring[slot], places, lane, nb, r.skip, r.a, r.c, r.q);
     Ch<CH> H;
-    seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], lane, r.a, r.c, r.start, r.skip, H);
+    seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], places, lane, r.a, r.c, r.start, r.skip, H);
     ahead[s][warp][lane] = H;
     if (lane == 0) seg[s].cut[warp] = r.start;
     __syncthreads();
@@ -897,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
       runs(i, t, slot, i & 1, r);
       h = state_before<CH>(seg[i & 1], ahead[i & 1], lane, warp, h);
       const Ch<CH> ui = pass_block<CH>(seg[i & 1], lane, warp, u);
-      backward_apply<E, CH>(p, ring[slot], lane, r.a, r.c, r.q, h, ui, at.live, t < 0 ? 0 : T - t,
+      backward_apply<E, CH>(p, ring[slot], places, lane, r.a, r.c, r.q, h, ui, at.live, t < 0 ? 0 : T - t,
                             r.start, r.skip, dz, df, sum);
       dz -= p.out_step, df -= p.out_step;
       slot = slot == kRing - 1 ? 0 : slot + 1;
@@ -921,8 +1009,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
       const Ch<CH> ui = inside_quad<CH>(seg[s], lane, warp, quad_cuts(seg[s], warp / kQuad), mine);
       // two channels' gates of two rounds do not fit the registers: computed twice
       if constexpr (CH == 2)
-        backward_gates<E, CH>(ring[slot], lane, nb, now.skip, now.a, now.c, now.q);
-      backward_apply<E, CH>(p, ring[slot], lane, now.a, now.c, now.q, h, ui, at.live,
+        backward_gates<E, CH>(ring[slot], places, lane, nb, now.skip, now.a, now.c, now.q);
+      backward_apply<E, CH>(p, ring[slot], places, lane, now.a, now.c, now.q, h, ui, at.live,
                             t < 0 ? 0 : T - t, now.start, now.skip, dz, df, sum);
       now = next;
       dz -= p.out_step, df -= p.out_step;
@@ -1055,7 +1143,7 @@ cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint3
   return e != cudaSuccess ? e : last;
 }
 
-template <class E, int CH, bool kForward>
+template <class E, int CH, bool kWide, bool kForward>
 cudaError_t run_as(ScanParams &p, cudaStream_t st) {
   if (p.T <= (uint32_t)kSteps) {
     const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
@@ -1075,11 +1163,11 @@ cudaError_t run_as(ScanParams &p, cudaStream_t st) {
     p.z_step = p.step * p.z_time, p.f_step = p.step * p.f_time, p.dy_step = p.step * p.dy_time;
     p.out_step = (int64_t)p.step * p.D, p.state_step = (int64_t)(p.step / (int)NS_SCAN_TILE) * p.D;
     return kForward
-               ? launch(split == 1 ? scan_forward_kernel<E, CH>
-                                   : scan_forward_cluster_kernel<E, CH>,
+               ? launch(split == 1 ? scan_forward_kernel<E, CH, kWide>
+                                   : scan_forward_cluster_kernel<E, CH, kWide>,
                         count * split, kThreads, split, smem, st, p)
-               : launch(split == 1 ? scan_backward_kernel<E, CH, false>
-                                   : scan_backward_kernel<E, CH, true>,
+               : launch(split == 1 ? scan_backward_kernel<E, CH, kWide, false>
+                                   : scan_backward_kernel<E, CH, kWide, true>,
                         count * split, kThreads, split, smem, st, p, first > 0);
   };
   if (whole) {
@@ -1100,11 +1188,18 @@ bool pairs(const ScanParams &p, size_t es) {
   return e % (2 * es) == 0 && s % 8 == 0 && st % 2 == 0;
 }
 
-// 16 bytes at a time need addresses, strides and widths of whole 16 bytes.
-bool sixteens(const ScanParams &p, size_t es) {
-  const uintptr_t e = (uintptr_t)p.z | (uintptr_t)p.f | (uintptr_t)p.dy;
+// Bytes that rows can be copied by: 16, 8 or 4 where addresses, strides and widths
+// are multiples of them, else 2.
+int copied_by(const ScanParams &p, size_t es) {
   const int64_t st = p.z_row | p.z_time | p.f_row | p.f_time | p.dy_row | p.dy_time | p.D;
-  return e % 16 == 0 && st % (int64_t)(16 / es) == 0;
+  const uint64_t all = (uint64_t)((uintptr_t)p.z | (uintptr_t)p.f | (uintptr_t)p.dy) |
+                       (uint64_t)st * es;
+  return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
+}
+const void *end_of(const void *array, int64_t row, int64_t time, const ScanParams &p, size_t es) {
+  if (!array || !p.B || !p.T) return array;
+  return static_cast<const char *>(array) +
+         ((int64_t)(p.B - 1) * row + (int64_t)(p.T - 1) * time + p.D) * (int64_t)es;
 }
 
 ScanParams params_of(const ns_scan_inputs &in) {
@@ -1120,15 +1215,23 @@ template <bool kForward>
 cudaError_t run(ScanParams &p, int dtype, cudaStream_t st) {
   const size_t es = dtype == NS_F32 ? 4 : 2;
   const bool two = pairs(p, es);
-  p.wide = (two || es == 4) && sixteens(p, es);
+  p.wide = copied_by(p, es);
+  p.z_end = end_of(p.z, p.z_row, p.z_time, p, es);
+  p.f_end = end_of(p.f, p.f_row, p.f_time, p, es);
+  p.dy_end = end_of(p.dy, p.dy_row, p.dy_time, p, es);
+  const bool wide = p.wide == 16;
+#define NSK_PAIRS(E)                                       \
+  (!two  ? run_as<E, 1, false, kForward>(p, st)            \
+   : wide ? run_as<E, 2, true, kForward>(p, st)            \
+          : run_as<E, 2, false, kForward>(p, st))
   switch (dtype) {
-    case NS_F32: return run_as<float, 1, kForward>(p, st);
-    case NS_BF16:
-      return two ? run_as<__nv_bfloat16, 2, kForward>(p, st)
-                 : run_as<__nv_bfloat16, 1, kForward>(p, st);
-    default:
-      return two ? run_as<__half, 2, kForward>(p, st) : run_as<__half, 1, kForward>(p, st);
+    case NS_F32:
+      return wide ? run_as<float, 1, true, kForward>(p, st)
+                  : run_as<float, 1, false, kForward>(p, st);
+    case NS_BF16: return NSK_PAIRS(__nv_bfloat16);
+    default: return NSK_PAIRS(__half);
   }
+#undef NSK_PAIRS
 }
 
 }  // namespace
