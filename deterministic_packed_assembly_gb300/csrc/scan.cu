@@ -36,7 +36,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = kSteps * kWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kShortThreads = 256;
+constexpr int kShortSteps = NS_SCAN_TILE;  // rows up to this long are a thread's alone
+constexpr int kShortThreads = 128;
 constexpr int kBiasWarps = 8;
 static_assert(NS_SCAN_TILE % kSteps == 0, "states are saved at the start of a segment");
 constexpr int kSaveEvery = NS_SCAN_TILE / kSteps;  // segments between two saved states
@@ -722,8 +723,31 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_wait();  // what waits for this launch also waits for the one before
 }
 
-// Rows of at most kSteps steps: a thread takes a row's channels alone, one
-// segment, no exchange.
+// Rows of at most kShortSteps steps: a thread takes a row's channels alone, with no
+// exchange, eight steps' loads in flight.
+template <class E, int CH>
+struct ShortRow {
+  Raw<E, CH> z[kSteps], f[kSteps];
+  uint32_t start, skip;
+  int n;
+  // Steps [t0, t0 + kSteps) of the row, as many as it has.
+  __device__ __forceinline__ void load(const ScanParams &p, uint32_t b, uint32_t c0, int t0) {
+    n = min((int)p.T - t0, kSteps);
+    const E *zp = static_cast<const E *>(p.z) + (int64_t)b * p.z_row + t0 * p.z_time + c0;
+    const E *fp = static_cast<const E *>(p.f) + (int64_t)b * p.f_row + t0 * p.f_time + c0;
+    const int64_t at = (int64_t)b * p.T + t0;
+    start = skip = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      if (s < n) {
+        z[s] = *reinterpret_cast<const Raw<E, CH> *>(zp + s * p.z_time);
+        f[s] = *reinterpret_cast<const Raw<E, CH> *>(fp + s * p.f_time);
+        if (p.pos && __ldg(p.pos + at + s) == 0) start |= 1u << s;
+        if (p.doc && __ldg(p.doc + at + s) < 0) skip |= 1u << s;
+      }
+    }
+  }
+};
 template <class E, int CH>
 __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const ScanParams p) {
   const uint32_t per_row = (p.D + CH - 1) / CH;
@@ -733,21 +757,21 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
   const Ch<CH> nb = load_channels<CH>(p.bias, c0, true) * splat<CH>(-kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)b * p.D + c0, true);
   store_channels<CH>(p.states, (int64_t)b * p.D + c0, p.T > 0, h);
-  const E *z = static_cast<const E *>(p.z) + (int64_t)b * p.z_row + c0;
-  const E *f = static_cast<const E *>(p.f) + (int64_t)b * p.f_row + c0;
   E *y = static_cast<E *>(p.y) + (int64_t)b * p.T * p.D + c0;
-#pragma unroll 2
-  for (uint32_t t = 0; t < p.T; ++t) {
-    const int64_t at = (int64_t)b * p.T + t;
-    const bool start = p.pos && __ldg(p.pos + at) == 0, skip = p.doc && __ldg(p.doc + at) < 0;
-    const Raw<E, CH> zv = *reinterpret_cast<const Raw<E, CH> *>(z + t * p.z_time);
-    const Raw<E, CH> fv = *reinterpret_cast<const Raw<E, CH> *>(f + t * p.f_time);
-    Ch<CH> r, c, a;
-    gate<CH>(widen<E, CH>(fv), nb, r, c, a);
-    const Ch<CH> to = fma(a, pick(start, splat<CH>(0.0f), h), c * widen<E, CH>(zv));
-    h = pick(skip, h, to);
-    *reinterpret_cast<Raw<E, CH> *>(y + (int64_t)t * p.D) =
-        narrow<E, CH>(pick(skip, splat<CH>(0.0f), to));
+  ShortRow<E, CH> row;
+  for (int t0 = 0; t0 < (int)p.T; t0 += kSteps) {
+    row.load(p, b, c0, t0);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s, y += p.D) {
+      if (s >= row.n) break;
+      const bool gone = (row.skip >> s) & 1u;
+      Ch<CH> r, c, a;
+      gate<CH>(widen<E, CH>(row.f[s]), nb, r, c, a);
+      const Ch<CH> before = pick((row.start >> s) & 1u, splat<CH>(0.0f), h);
+      const Ch<CH> to = fma(a, before, c * widen<E, CH>(row.z[s]));
+      h = pick(gone, h, to);
+      *reinterpret_cast<Raw<E, CH> *>(y) = narrow<E, CH>(pick(gone, splat<CH>(0.0f), to));
+    }
   }
   store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, true, h);
 }
@@ -1024,6 +1048,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   if (kCluster) pdl_wait();  // what waits for this launch also waits for the one before
 }
 
+// Backward, the states before every eight steps are kept, and those steps run again.
 template <class E, int CH>
 __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(const ScanParams p) {
   const uint32_t per_row = (p.D + CH - 1) / CH;
@@ -1033,41 +1058,58 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
   const int64_t bc = (int64_t)b * p.D + c0;
   const Ch<CH> zero = splat<CH>(0.0f);
   const Ch<CH> nb = load_channels<CH>(p.bias, c0, true) * splat<CH>(-kLog2e);
-  Ch<CH> h = load_channels<CH>(p.saved, bc, p.T > 0);
   Ch<CH> u = load_channels<CH>(p.dh_last, bc, true), sum = zero;
-  const E *z = static_cast<const E *>(p.z) + (int64_t)b * p.z_row + c0;
-  const E *f = static_cast<const E *>(p.f) + (int64_t)b * p.f_row + c0;
-  const E *dy = static_cast<const E *>(p.dy) + (int64_t)b * p.dy_row + c0;
-  Ch<CH> a[kSteps], c[kSteps], q[kSteps], e[kSteps];  // e: p_t - z_t
-  uint32_t start = 0, skip = 0;
+  Ch<CH> kept[kShortSteps / kSteps];
+  kept[0] = load_channels<CH>(p.saved, bc, p.T > 0);
+  ShortRow<E, CH> row;
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    if (s < (int)p.T) {
-      const int64_t at = (int64_t)b * p.T + s;
-      if (p.pos && __ldg(p.pos + at) == 0) start |= 1u << s;
-      if (p.doc && __ldg(p.doc + at) < 0) skip |= 1u << s;
-      const Raw<E, CH> zv = *reinterpret_cast<const Raw<E, CH> *>(z + s * p.z_time);
-      const Raw<E, CH> fv = *reinterpret_cast<const Raw<E, CH> *>(f + s * p.f_time);
-      Ch<CH> r;
-      gate<CH>(widen<E, CH>(fv), nb, r, c[s], a[s]);
-      q[s] = r * c[s];
-      const Ch<CH> before = pick((start >> s) & 1u, zero, h);
-      e[s] = sub(before, widen<E, CH>(zv));
-      h = pick((skip >> s) & 1u, h, fma(a[s], before, c[s] * widen<E, CH>(zv)));
+  for (int k = 0; k + 1 < kShortSteps / kSteps; ++k) {
+    kept[k + 1] = kept[k];
+    if ((k + 1) * kSteps >= (int)p.T) continue;
+    row.load(p, b, c0, k * kSteps);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      Ch<CH> r, c, a;
+      gate<CH>(widen<E, CH>(row.f[s]), nb, r, c, a);
+      const Ch<CH> before = pick((row.start >> s) & 1u, zero, kept[k + 1]);
+      kept[k + 1] = pick((row.skip >> s) & 1u, kept[k + 1],
+                         fma(a, before, c * widen<E, CH>(row.z[s])));
     }
   }
 #pragma unroll
-  for (int s = kSteps - 1; s >= 0; --s) {
-    if (s < (int)p.T) {
-      const bool out = (skip >> s) & 1u;
-      const Ch<CH> d = widen<E, CH>(*reinterpret_cast<const Raw<E, CH> *>(dy + s * p.dy_time)) + u;
-      const Ch<CH> vf = pick(out, zero, q[s] * d * e[s]);
-      u = pick(out, u, pick((start >> s) & 1u, zero, a[s] * d));
-      sum = sum + vf;
-      const int64_t at = ((int64_t)b * p.T + s) * p.D + c0;
-      *reinterpret_cast<Raw<E, CH> *>(static_cast<E *>(p.dz) + at) =
-          narrow<E, CH>(pick(out, zero, c[s] * d));
-      *reinterpret_cast<Raw<E, CH> *>(static_cast<E *>(p.df) + at) = narrow<E, CH>(vf);
+  for (int k = kShortSteps / kSteps - 1; k >= 0; --k) {
+    const int t0 = k * kSteps;
+    if (t0 >= (int)p.T) continue;
+    row.load(p, b, c0, t0);
+    const E *gp = static_cast<const E *>(p.dy) + (int64_t)b * p.dy_row + t0 * p.dy_time + c0;
+    Raw<E, CH> g[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      if (s < row.n) g[s] = *reinterpret_cast<const Raw<E, CH> *>(gp + s * p.dy_time);
+    Ch<CH> a[kSteps], c[kSteps], q[kSteps], h = kept[k];  // q: a c (p_t - z_t)
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      if (s < row.n) {
+        Ch<CH> r;
+        gate<CH>(widen<E, CH>(row.f[s]), nb, r, c[s], a[s]);
+        const Ch<CH> before = pick((row.start >> s) & 1u, zero, h), z = widen<E, CH>(row.z[s]);
+        q[s] = r * c[s] * sub(before, z);
+        h = pick((row.skip >> s) & 1u, h, fma(a[s], before, c[s] * z));
+      }
+    }
+    const int64_t at = ((int64_t)b * p.T + t0) * p.D + c0;
+    E *dz = static_cast<E *>(p.dz) + at, *df = static_cast<E *>(p.df) + at;
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s) {
+      if (s < row.n) {
+        const bool gone = (row.skip >> s) & 1u;
+        const Ch<CH> d = widen<E, CH>(g[s]) + u, vf = pick(gone, zero, q[s] * d);
+        u = pick(gone, u, pick((row.start >> s) & 1u, zero, a[s] * d));
+        sum = sum + vf;
+        *reinterpret_cast<Raw<E, CH> *>(dz + (int64_t)s * p.D) =
+            narrow<E, CH>(pick(gone, zero, c[s] * d));
+        *reinterpret_cast<Raw<E, CH> *>(df + (int64_t)s * p.D) = narrow<E, CH>(vf);
+      }
     }
   }
   store_channels<CH>(p.dh0, bc, true, u);
@@ -1145,7 +1187,7 @@ cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint3
 
 template <class E, int CH, bool kWide, bool kForward>
 cudaError_t run_as(ScanParams &p, cudaStream_t st) {
-  if (p.T <= (uint32_t)kSteps) {
+  if (p.T <= (uint32_t)kShortSteps) {
     const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
     return launch(kForward ? scan_forward_short_kernel<E, CH> : scan_backward_short_kernel<E, CH>,
                   (n + kShortThreads - 1) / kShortThreads, kShortThreads, 1, 0, st, p);
@@ -1244,7 +1286,7 @@ cudaError_t launch_scan_forward(const ns_scan_inputs &in, const float *h0, void 
 }
 
 uint64_t scan_partial_rows(uint32_t B, uint32_t T, uint32_t D) {
-  return (uint64_t)B * (T <= (uint32_t)kSteps ? 1 : layout_of(B, T, D, kBackwardResident).split);
+  return (uint64_t)B * (T <= (uint32_t)kShortSteps ? 1 : layout_of(B, T, D, kBackwardResident).split);
 }
 
 cudaError_t launch_scan_backward(const ns_scan_inputs &in, const float *states, const void *dy,
