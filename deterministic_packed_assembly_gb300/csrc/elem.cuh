@@ -47,7 +47,8 @@ __device__ __forceinline__ float rcp_sfu(float x) {
 
 // ---- pairs of floats ----------------------------------------------------------
 // A lane's one or two channels, or values; two are computed by the packed
-// instructions.
+// instructions.  Each is rounded as written, never fused with another, so that the same
+// formula has the same bits in every kernel.
 template <int CH>
 struct Ch;
 template <>
@@ -66,12 +67,12 @@ __device__ __forceinline__ Ch<2> fma(Ch<2> a, Ch<2> b, Ch<2> c) {
   const float2 r = __ffma2_rn(pair(a), pair(b), pair(c));
   return {r.x, r.y};
 }
-__device__ __forceinline__ Ch<1> operator*(Ch<1> a, Ch<1> b) { return {a.v[0] * b.v[0]}; }
+__device__ __forceinline__ Ch<1> operator*(Ch<1> a, Ch<1> b) { return {__fmul_rn(a.v[0], b.v[0])}; }
 __device__ __forceinline__ Ch<2> operator*(Ch<2> a, Ch<2> b) {
   const float2 r = __fmul2_rn(pair(a), pair(b));
   return {r.x, r.y};
 }
-__device__ __forceinline__ Ch<1> operator+(Ch<1> a, Ch<1> b) { return {a.v[0] + b.v[0]}; }
+__device__ __forceinline__ Ch<1> operator+(Ch<1> a, Ch<1> b) { return {__fadd_rn(a.v[0], b.v[0])}; }
 __device__ __forceinline__ Ch<2> operator+(Ch<2> a, Ch<2> b) {
   const float2 r = __fadd2_rn(pair(a), pair(b));
   return {r.x, r.y};

@@ -36,7 +36,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = kSteps * kWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kShortSteps = NS_SCAN_TILE;  // rows up to this long are a thread's alone
+constexpr int kShortSteps = NS_SCAN_TILE;  // rows up to this long can be a thread's alone
 constexpr int kShortThreads = 128;
 constexpr int kBiasWarps = 8;
 static_assert(NS_SCAN_TILE % kSteps == 0, "states are saved at the start of a segment");
@@ -723,8 +723,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_wait();  // what waits for this launch also waits for the one before
 }
 
-// Rows of at most kShortSteps steps: a thread takes a row's channels alone, with no
-// exchange, eight steps' loads in flight.
+// Rows of at most kShortSteps steps, which are one quad: a thread takes a row's
+// channels alone, segment by segment, eight steps' loads in flight.  States at the
+// segments' starts and the quad's end come from the segments' runs, as between warps:
+// the results are the same bits as the blocks'.
 template <class E, int CH>
 struct ShortRow {
   Raw<E, CH> z[kSteps], f[kSteps];
@@ -746,6 +748,7 @@ struct ShortRow {
         if (p.doc && __ldg(p.doc + at + s) < 0) skip |= 1u << s;
       }
     }
+    start &= ~skip;  // padding starts nothing
   }
 };
 template <class E, int CH>
@@ -759,21 +762,32 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
   store_channels<CH>(p.states, (int64_t)b * p.D + c0, p.T > 0, h);
   E *y = static_cast<E *>(p.y) + (int64_t)b * p.T * p.D + c0;
   ShortRow<E, CH> row;
+  Run<CH> all = {splat<CH>(1.0f), splat<CH>(0.0f)};
+  bool cut = false;  // a sequence started
+  const Ch<CH> first = h;
   for (int t0 = 0; t0 < (int)p.T; t0 += kSteps) {
     row.load(p, b, c0, t0);
+    Run<CH> run = {splat<CH>(1.0f), splat<CH>(0.0f)};
+    Ch<CH> in = h;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s, y += p.D) {
       if (s >= row.n) break;
-      const bool gone = (row.skip >> s) & 1u;
+      const bool gone = (row.skip >> s) & 1u, start = (row.start >> s) & 1u;
       Ch<CH> r, c, a;
       gate<CH>(widen<E, CH>(row.f[s]), nb, r, c, a);
-      const Ch<CH> before = pick((row.start >> s) & 1u, splat<CH>(0.0f), h);
-      const Ch<CH> to = fma(a, before, c * widen<E, CH>(row.z[s]));
-      h = pick(gone, h, to);
-      *reinterpret_cast<Raw<E, CH> *>(y) = narrow<E, CH>(pick(gone, splat<CH>(0.0f), to));
+      a = pick(gone, splat<CH>(1.0f), a);
+      const Ch<CH> cz = pick(gone, splat<CH>(0.0f), c * widen<E, CH>(row.z[s]));
+      in = fma(a, pick(start, splat<CH>(0.0f), in), cz);
+      run.H = fma(a, pick(start, splat<CH>(0.0f), run.H), cz);
+      run.A = run.A * a;
+      *reinterpret_cast<Raw<E, CH> *>(y) = narrow<E, CH>(pick(gone, splat<CH>(0.0f), in));
     }
+    h = after(run, row.start != 0, h);
+    all.H = after(run, row.start != 0, all.H);
+    all.A = all.A * run.A;
+    cut = cut || row.start != 0;
   }
-  store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, true, h);
+  store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, true, after(all, cut, first));
 }
 
 // ---- backward -------------------------------------------------------------------
@@ -823,9 +837,10 @@ __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
       H = fma(a[s], H, c[s] * at.read(in, 0, s, lane));
       run.A = run.A * a[s];
     }
+    Ch<CH> d = at.read(in, 2, kSteps - 1, lane);
 #pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s)
-      run.H = a[s] * (at.read(in, 2, s, lane) + run.H);
+    for (int s = kSteps - 2; s >= 0; --s) d = fma(a[s + 1], d, at.read(in, 2, s, lane));
+    run.H = a[0] * d;
   } else {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -833,11 +848,13 @@ __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
       H = fma(a[s], pick((start >> s) & 1u, zero, H), cz);
       run.A = run.A * a[s];
     }
+    Ch<CH> d = zero;
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
       const Ch<CH> g = pick((skip >> s) & 1u, zero, at.read(in, 2, s, lane));
-      run.H = pick((start >> s) & 1u, zero, a[s] * (g + run.H));
+      d = pick((start >> s) & 1u, zero, s == kSteps - 1 ? g : fma(a[s + 1], d, g));
     }
+    run.H = a[0] * d;
   }
   return run;
 }
@@ -875,8 +892,9 @@ __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<
     }
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
-      const Ch<CH> d = at.read(in, 2, s, lane) + u, vf = q[s] * d;
-      u = a[s] * d;
+      const Ch<CH> g = at.read(in, 2, s, lane);
+      u = s == kSteps - 1 ? g + u : fma(a[s + 1], u, g);  // d_s
+      const Ch<CH> d = u, vf = q[s] * d;
       sum = sum + vf;
       if (live) {
         *reinterpret_cast<Raw<E, CH> *>(dz) = narrow<E, CH>(c[s] * d);
@@ -894,9 +912,10 @@ __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
       const bool gone = (skip >> s) & 1u;
-      const Ch<CH> d = pick(gone, zero, at.read(in, 2, s, lane)) + u;
+      const Ch<CH> g = pick(gone, zero, at.read(in, 2, s, lane));
+      const Ch<CH> d = s == kSteps - 1 ? g + u : fma(a[s + 1], u, g);
       const Ch<CH> vf = pick(gone, zero, q[s] * d);
-      u = pick((start >> s) & 1u, zero, a[s] * d);
+      u = pick((start >> s) & 1u, zero, d);
       sum = sum + vf;
       if (live && s < left) {
         *reinterpret_cast<Raw<E, CH> *>(dz) = narrow<E, CH>(pick(gone, zero, c[s] * d));
@@ -1066,16 +1085,23 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
   for (int k = 0; k + 1 < kShortSteps / kSteps; ++k) {
     kept[k + 1] = kept[k];
     if ((k + 1) * kSteps >= (int)p.T) continue;
-    row.load(p, b, c0, k * kSteps);
+    row.load(p, b, c0, k * kSteps);  // eight steps: more follow
+    Run<CH> run = {splat<CH>(1.0f), zero};
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
+      const bool gone = (row.skip >> s) & 1u;
       Ch<CH> r, c, a;
       gate<CH>(widen<E, CH>(row.f[s]), nb, r, c, a);
-      const Ch<CH> before = pick((row.start >> s) & 1u, zero, kept[k + 1]);
-      kept[k + 1] = pick((row.skip >> s) & 1u, kept[k + 1],
-                         fma(a, before, c * widen<E, CH>(row.z[s])));
+      a = pick(gone, splat<CH>(1.0f), a);
+      const Ch<CH> cz = pick(gone, zero, c * widen<E, CH>(row.z[s]));
+      run.H = fma(a, pick((row.start >> s) & 1u, zero, run.H), cz);
+      run.A = run.A * a;
     }
+    kept[k + 1] = after(run, row.start != 0, kept[k]);
   }
+  Run<CH> all = {splat<CH>(1.0f), zero};
+  bool cut = false;
+  const Ch<CH> last = u;
 #pragma unroll
   for (int k = kShortSteps / kSteps - 1; k >= 0; --k) {
     const int t0 = k * kSteps;
@@ -1089,30 +1115,46 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
     Ch<CH> a[kSteps], c[kSteps], q[kSteps], h = kept[k];  // q: a c (p_t - z_t)
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      if (s < row.n) {
+      a[s] = splat<CH>(1.0f);
+      c[s] = q[s] = zero;
+      if (s < row.n && !((row.skip >> s) & 1u)) {
         Ch<CH> r;
         gate<CH>(widen<E, CH>(row.f[s]), nb, r, c[s], a[s]);
-        const Ch<CH> before = pick((row.start >> s) & 1u, zero, h), z = widen<E, CH>(row.z[s]);
-        q[s] = r * c[s] * sub(before, z);
-        h = pick((row.skip >> s) & 1u, h, fma(a[s], before, c[s] * z));
+        const Ch<CH> before = pick((row.start >> s) & 1u, zero, h);
+        const Ch<CH> z = widen<E, CH>(row.z[s]);
+        q[s] = (r * c[s]) * sub(before, z);
+        h = fma(a[s], before, c[s] * z);
       }
     }
     const int64_t at = ((int64_t)b * p.T + t0) * p.D + c0;
     E *dz = static_cast<E *>(p.dz) + at, *df = static_cast<E *>(p.df) + at;
+    Run<CH> run = {splat<CH>(1.0f), zero};
+    Ch<CH> ui = u;
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
-      if (s < row.n) {
-        const bool gone = (row.skip >> s) & 1u;
-        const Ch<CH> d = widen<E, CH>(g[s]) + u, vf = pick(gone, zero, q[s] * d);
-        u = pick(gone, u, pick((row.start >> s) & 1u, zero, a[s] * d));
-        sum = sum + vf;
+      const bool have = s < row.n, start = (row.start >> s) & 1u;
+      const bool gone = !have || ((row.skip >> s) & 1u);
+      const Ch<CH> gs = gone ? zero : widen<E, CH>(g[s]);
+      const Ch<CH> d = s == kSteps - 1 ? gs + ui : fma(a[s + 1], ui, gs);
+      const Ch<CH> vf = pick(gone, zero, q[s] * d);
+      ui = pick(start, zero, d);
+      run.H = pick(start, zero, s == kSteps - 1 ? gs : fma(a[s + 1], run.H, gs));
+      sum = sum + vf;
+      if (have) {
         *reinterpret_cast<Raw<E, CH> *>(dz + (int64_t)s * p.D) =
             narrow<E, CH>(pick(gone, zero, c[s] * d));
         *reinterpret_cast<Raw<E, CH> *>(df + (int64_t)s * p.D) = narrow<E, CH>(vf);
       }
     }
+    run.H = a[0] * run.H;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) run.A = run.A * a[s];
+    u = after(run, row.start != 0, u);
+    all.H = after(run, row.start != 0, all.H);
+    all.A = all.A * run.A;
+    cut = cut || row.start != 0;
   }
-  store_channels<CH>(p.dh0, bc, true, u);
+  store_channels<CH>(p.dh0, bc, true, after(all, cut, last));
   store_channels<CH>(p.partial, bc, true, sum);
 }
 
@@ -1185,9 +1227,18 @@ cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint3
   return e != cudaSuccess ? e : last;
 }
 
+// Whether a thread takes a row's channels alone: up to eight steps always, up to 32
+// where there are threads for every SM (forward and backward of T = 32 in bfloat16:
+// 64 rows of 2048 channels 25 us, 41 us by blocks; 8 rows of 512 17 us, 9 us by
+// blocks).
+bool short_rows(uint32_t B, uint32_t T, uint32_t D) {
+  return T <= (uint32_t)kSteps ||
+         (T <= (uint32_t)kShortSteps && (uint64_t)B * D >= 2 * kShortThreads * kSMs);
+}
+
 template <class E, int CH, bool kWide, bool kForward>
 cudaError_t run_as(ScanParams &p, cudaStream_t st) {
-  if (p.T <= (uint32_t)kShortSteps) {
+  if (short_rows(p.B, p.T, p.D)) {
     const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
     return launch(kForward ? scan_forward_short_kernel<E, CH> : scan_backward_short_kernel<E, CH>,
                   (n + kShortThreads - 1) / kShortThreads, kShortThreads, 1, 0, st, p);
@@ -1286,7 +1337,7 @@ cudaError_t launch_scan_forward(const ns_scan_inputs &in, const float *h0, void 
 }
 
 uint64_t scan_partial_rows(uint32_t B, uint32_t T, uint32_t D) {
-  return (uint64_t)B * (T <= (uint32_t)kShortSteps ? 1 : layout_of(B, T, D, kBackwardResident).split);
+  return (uint64_t)B * (short_rows(B, T, D) ? 1 : layout_of(B, T, D, kBackwardResident).split);
 }
 
 cudaError_t launch_scan_backward(const ns_scan_inputs &in, const float *states, const void *dy,

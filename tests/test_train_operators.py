@@ -295,6 +295,36 @@ def test_scan_token_by_token_equals_the_whole_row(nsp):
         assert torch.equal(out, want[0]) and torch.equal(h, want[1])
 
 
+@pytest.mark.parametrize("T", [1, 7, 8, 9, 24, 31, 32, 33, 70, 700])
+def test_scan_rows_do_not_depend_on_the_other_rows(nsp, T):
+    # few rows and many take other kernels and other clusters: the same bits
+    host, cuda, dy, dh = scan_inputs(60, T, 1300, "bf16", T)
+    kw = dict(pos=dev(host["pos"]), doc=dev(host["doc"]))
+    bias, h0, dhc = dev(host["bias"]), dev(host["h0"]), dev(dh)
+    y, h, st = nsp.gated_scan_forward(cuda["z"], cuda["f"], bias, h0=h0, **kw)
+    back = nsp.gated_scan_backward(cuda["dy"], dhc, cuda["z"], cuda["f"], bias, st, **kw)
+    for rows in (slice(3, 4), slice(17, 22)):
+        kw = dict(pos=dev(host["pos"])[rows], doc=dev(host["doc"])[rows])
+        part = dict(z=cuda["z"][rows], f=cuda["f"][rows])
+        y1, h1, s1 = nsp.gated_scan_forward(part["z"], part["f"], bias, h0=h0[rows], **kw)
+        one = nsp.gated_scan_backward(cuda["dy"][rows], dhc[rows], part["z"], part["f"], bias, s1, **kw)
+        assert torch.equal(y1, y[rows]) and torch.equal(h1, h[rows]) and torch.equal(s1, st[rows])
+        for a, b, name in zip(one, back, ("dz", "df", "dbias", "dh0")):
+            assert name == "dbias" or torch.equal(a, b[rows]), name
+
+
+def test_route_tokens_do_not_depend_on_the_other_tokens(nsp):
+    for E, k in ((64, 8), (100, 4), (250, 3), (1000, 8)):
+        x = torch.randn(30_000, E, generator=gen(E)).cuda()
+        dw = torch.randn(30_000, k, generator=gen(k)).cuda()
+        many = nsp.route(x, k)
+        for n in (1, 77, 2000):
+            few = nsp.route(x[:n], k)
+            assert torch.equal(few.ids, many.ids[:n]) and torch.equal(few.weights, many.weights[:n])
+            assert torch.equal(nsp.route_backward(x[:n], few, dw[:n]),
+                               nsp.route_backward(x, many, dw)[:n])
+
+
 def test_scan_offsets_past_32_bits(nsp):
     B, T, D = 3, 360_001, 2048  # 2.2e9 elements
     g = torch.Generator(device="cuda")
