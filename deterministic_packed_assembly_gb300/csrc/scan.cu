@@ -20,6 +20,7 @@
 // document does not reach the next.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -130,26 +131,27 @@ __device__ __forceinline__ void store_channels(float *dst, int64_t off, bool liv
   if (dst && live) *reinterpret_cast<Ch<CH> *>(dst + off) = v;
 }
 
-// With x = f + bias and e = exp(-x): r = 1 / (1 + e) = sigmoid(x), c = e r =
-// sigmoid(-x), both to 2 ulp whatever x is, and a = 1 - c, so that a and c add
-// up to 1 to the last bit: an error of r near 1 would build up over 1 / c steps.
-// nb = -bias log2 e.  e is kept finite (at most 2^120) where it would not be;
-// a NaN stays one.
+// With x = f + bias and u = exp(x): c = 1 / (1 + u) = sigmoid(-x), to 2 ulp whatever x
+// is (0 where that is below 2^-126), and a = 1 - c, so that a and c add up to 1 to the
+// last bit: an error of a near 1 would build up over 1 / c steps.  pb = bias log2 e.
 template <int CH>
-__device__ __forceinline__ void gate(Ch<CH> f, Ch<CH> nb, Ch<CH> &r, Ch<CH> &c, Ch<CH> &a) {
-  const Ch<CH> t = fma(f, splat<CH>(-kLog2e), nb);
-  Ch<CH> e;
+__device__ __forceinline__ void gate(Ch<CH> f, Ch<CH> pb, Ch<CH> &u, Ch<CH> &c, Ch<CH> &a) {
+  const Ch<CH> t = fma(f, splat<CH>(kLog2e), pb);
 #pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    float m;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(t.v[k]), "f"(120.0f));
-    e.v[k] = exp2_sfu(m);
-  }
-  const Ch<CH> d = e + splat<CH>(1.0f);
+  for (int k = 0; k < CH; ++k) u.v[k] = exp2_sfu(t.v[k]);
+  const Ch<CH> d = u + splat<CH>(1.0f);
 #pragma unroll
-  for (int k = 0; k < CH; ++k) r.v[k] = rcp_sfu(d.v[k]);
-  c = e * r;
+  for (int k = 0; k < CH; ++k) c.v[k] = rcp_sfu(d.v[k]);
   a = sub(splat<CH>(1.0f), c);
+}
+// da / dx = u c^2, u c = sigmoid(x) to 2 ulp; where u is infinite, or c a NaN, u c counts
+// as 1.
+template <int CH>
+__device__ __forceinline__ Ch<CH> slope(Ch<CH> u, Ch<CH> c) {
+  Ch<CH> r = u * c;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) r.v[k] = fminf(r.v[k], 1.0f);
+  return r * c;
 }
 
 // A warp's ring of segments in shared memory, filled by asynchronous copies that
@@ -470,8 +472,7 @@ __device__ __forceinline__ Ch<CH> pass_cluster(const Quads<CH> &quads, uint64_t 
 
 // Blocks of an SM: 24 warps forward (80 registers), 16 backward (128).
 constexpr int kForwardBlocks = 24 / kWarps, kBackwardBlocks = 16 / kWarps;
-constexpr uint64_t kSMs = 152, kForwardResident = kForwardBlocks * kSMs,
-                   kBackwardResident = kBackwardBlocks * kSMs;
+constexpr uint64_t kSMs = 152;
 
 // Where a block works: a group of 32 lanes' channels of a row, and with others of
 // its cluster every split-th tile.
@@ -506,13 +507,13 @@ __device__ __forceinline__ void cluster_begin(Quads<CH> (&quads)[2]) {
 // A segment's gates a and inputs c z; a = 1, c z = 0 at skipped steps.
 template <class E, int CH>
 __device__ __forceinline__ void forward_gates(const Stage<E, CH, 2> &in,
-                                              const Places<E, CH, 2> &at, int lane, Ch<CH> nb,
+                                              const Places<E, CH, 2> &at, int lane, Ch<CH> pb,
                                               uint32_t skip, Ch<CH> (&a)[kSteps],
                                               Ch<CH> (&cz)[kSteps]) {
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    Ch<CH> r, c;
-    gate<CH>(at.read(in, 1, s, lane), nb, r, c, a[s]);
+    Ch<CH> u, c;
+    gate<CH>(at.read(in, 1, s, lane), pb, u, c, a[s]);
     cz[s] = c * at.read(in, 0, s, lane);
   }
   if (skip) {  // the same for the warp
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
   for (int k = 0; k < kRing - 1; ++k) fetch(t + k * kTile, ring[k]);
   Flags flags;
   flags.set(p, at.b, t, kTile, lane);
-  const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
+  const Ch<CH> pb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
   E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
   float *state = nullptr;  // the state before a quad is its first warp's to save
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     copy_wait<kRing - 1>();
     __syncwarp();
     Ch<CH> a[kSteps], cz[kSteps];
-    forward_gates<E, CH>(ring[slot], places, lane, nb, skip, a, cz);
+    forward_gates<E, CH>(ring[slot], places, lane, pb, skip, a, cz);
     slot = slot == kRing - 1 ? 0 : slot + 1;
     Exchange<CH, kWarps> &x = seg[i & 1];
     x.run[warp][lane] = forward_run<CH>(a, cz, start);
@@ -634,10 +635,11 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
 // Clusters of blocks, each with every split-th tile of a unit's row.  The runs of
 // round i + 1 are computed and sent before the steps of round i are written, so
 // that their way between the blocks lies beside this and the next round's runs.
-// Two rounds' gates are in registers: two blocks an SM, which is what the grids of
-// clusters hold anyway.
-template <class E, int CH, bool kWide>
-__global__ void __launch_bounds__(kThreads, 2)
+// kAlone: two rounds' gates are in registers, for two blocks an SM, which is what grids
+// of clusters alone hold anyway; else, beside blocks with whole rows, they are computed
+// twice.
+template <class E, int CH, bool kWide, bool kAlone>
+__global__ void __launch_bounds__(kThreads, kAlone ? 2 : kForwardBlocks)
     scan_forward_cluster_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) Exchange<CH, kWarps> seg[3];
@@ -665,11 +667,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     z_from.at += p.z_step, f_from.at += p.f_step;
     copy_commit();
   };
+  constexpr int kAhead = kAlone ? kRing - 1 : 1;  // tiles: a slot is read again where not alone
 #pragma unroll
-  for (int k = 0; k < kRing - 1; ++k) fetch(t + k * p.step, ring[k]);
+  for (int k = 0; k < kAhead; ++k) fetch(t + k * p.step, ring[k]);
   Flags flags;
   flags.set(p, at.b, t, p.step, lane);
-  const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
+  const Ch<CH> pb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
   E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
   float *state = nullptr;
@@ -685,12 +688,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   // Round i's runs, its tile at step t_i.
   auto runs = [&](int i, int t_i, Round &r) {
     __syncwarp();
-    fetch(t_i + (kRing - 1) * p.step, ring[(i + kRing - 1) % kRing]);
+    fetch(t_i + kAhead * p.step, ring[(i + kAhead) % kRing]);
     flags.next(p, p.step, i);
     r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
-    copy_wait<kRing - 1>();
+    copy_wait<kAhead>();
     __syncwarp();
-    forward_gates<E, CH>(ring[i % kRing], places, lane, nb, r.skip, r.a, r.cz);
+    forward_gates<E, CH>(ring[i % kRing], places, lane, pb, r.skip, r.a, r.cz);
     Exchange<CH, kWarps> &x = seg[i % 3];
     x.run[warp][lane] = forward_run<CH>(r.a, r.cz, r.start);
     if (lane == 0) x.cut[warp] = r.start;
@@ -713,6 +716,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       store_channels<CH>(state, 0, at.live && t < T, in);
       state += p.state_step;
     }
+    if constexpr (!kAlone)
+      forward_gates<E, CH>(ring[i % kRing], places, lane, pb, now.skip, now.a, now.cz);
     forward_apply<E, CH>(p, now.a, now.cz, in, at.live, T - t, now.start, now.skip, y);
     now = next;
     y += p.out_step;
@@ -757,7 +762,7 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
   const uint64_t i = (uint64_t)blockIdx.x * kShortThreads + threadIdx.x;
   if (i >= (uint64_t)p.B * per_row) return;
   const uint32_t b = (uint32_t)(i / per_row), c0 = (uint32_t)(i % per_row) * CH;
-  const Ch<CH> nb = load_channels<CH>(p.bias, c0, true) * splat<CH>(-kLog2e);
+  const Ch<CH> pb = load_channels<CH>(p.bias, c0, true) * splat<CH>(kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)b * p.D + c0, true);
   store_channels<CH>(p.states, (int64_t)b * p.D + c0, p.T > 0, h);
   E *y = static_cast<E *>(p.y) + (int64_t)b * p.T * p.D + c0;
@@ -773,8 +778,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
     for (int s = 0; s < kSteps; ++s, y += p.D) {
       if (s >= row.n) break;
       const bool gone = (row.skip >> s) & 1u, start = (row.start >> s) & 1u;
-      Ch<CH> r, c, a;
-      gate<CH>(widen<E, CH>(row.f[s]), nb, r, c, a);
+      Ch<CH> e, c, a;
+      gate<CH>(widen<E, CH>(row.f[s]), pb, e, c, a);
       a = pick(gone, splat<CH>(1.0f), a);
       const Ch<CH> cz = pick(gone, splat<CH>(0.0f), c * widen<E, CH>(row.z[s]));
       in = fma(a, pick(start, splat<CH>(0.0f), in), cz);
@@ -798,18 +803,18 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
 // pass.  The states inside a quad are run again from the saved one before it,
 // by the segments' forward runs, which are exchanged too.
 //
-// A segment's gates: a, c and q = a c from the unrounded gate; a = 1, c = q = 0 at
+// A segment's gates: a, c and q = da / dx; a = 1, c = q = 0 at
 // skipped steps.
 template <class E, int CH>
 __device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in,
-                                               const Places<E, CH, 3> &at, int lane, Ch<CH> nb,
+                                               const Places<E, CH, 3> &at, int lane, Ch<CH> pb,
                                                uint32_t skip, Ch<CH> (&a)[kSteps],
                                                Ch<CH> (&c)[kSteps], Ch<CH> (&q)[kSteps]) {
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    Ch<CH> r;
-    gate<CH>(at.read(in, 1, s, lane), nb, r, c[s], a[s]);
-    q[s] = r * c[s];
+    Ch<CH> u;
+    gate<CH>(at.read(in, 1, s, lane), pb, u, c[s], a[s]);
+    q[s] = slope(u, c[s]);
   }
   if (skip) {
 #pragma unroll
@@ -989,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   const float *saved = p.saved + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
                                   t / (int)NS_SCAN_TILE) * p.D + at.c0;
   Ch<CH> next_h = load_channels<CH>(saved, 0, at.live && t >= 0 && t < T);
-  const Ch<CH> nb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(-kLog2e);
+  const Ch<CH> pb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(kLog2e);
   Ch<CH> u = load_channels<CH>(p.dh_last, (int64_t)at.b * p.D + at.c0, at.live);
   Ch<CH> sum = splat<CH>(0.0f);
   const int64_t out = ((int64_t)at.b * p.T + t) * p.D + at.c0;
@@ -1007,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
     copy_wait<kAhead>();
     __syncwarp();
-    backward_gates<E, CH>(ring[slot], places, lane, nb, r.skip, r.a, r.c, r.q);
+    backward_gates<E, CH>(ring[slot], places, lane, pb, r.skip, r.a, r.c, r.q);
     Ch<CH> H;
     seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], places, lane, r.a, r.c, r.start, r.skip, H);
     ahead[s][warp][lane] = H;
@@ -1052,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
       const Ch<CH> ui = inside_quad<CH>(seg[s], lane, warp, quad_cuts(seg[s], warp / kQuad), mine);
       // two channels' gates of two rounds do not fit the registers: computed twice
       if constexpr (CH == 2)
-        backward_gates<E, CH>(ring[slot], places, lane, nb, now.skip, now.a, now.c, now.q);
+        backward_gates<E, CH>(ring[slot], places, lane, pb, now.skip, now.a, now.c, now.q);
       backward_apply<E, CH>(p, ring[slot], places, lane, now.a, now.c, now.q, h, ui, at.live,
                             t < 0 ? 0 : T - t, now.start, now.skip, dz, df, sum);
       now = next;
@@ -1076,7 +1081,7 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
   const uint32_t b = (uint32_t)(i / per_row), c0 = (uint32_t)(i % per_row) * CH;
   const int64_t bc = (int64_t)b * p.D + c0;
   const Ch<CH> zero = splat<CH>(0.0f);
-  const Ch<CH> nb = load_channels<CH>(p.bias, c0, true) * splat<CH>(-kLog2e);
+  const Ch<CH> pb = load_channels<CH>(p.bias, c0, true) * splat<CH>(kLog2e);
   Ch<CH> u = load_channels<CH>(p.dh_last, bc, true), sum = zero;
   Ch<CH> kept[kShortSteps / kSteps];
   kept[0] = load_channels<CH>(p.saved, bc, p.T > 0);
@@ -1090,8 +1095,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const bool gone = (row.skip >> s) & 1u;
-      Ch<CH> r, c, a;
-      gate<CH>(widen<E, CH>(row.f[s]), nb, r, c, a);
+      Ch<CH> e, c, a;
+      gate<CH>(widen<E, CH>(row.f[s]), pb, e, c, a);
       a = pick(gone, splat<CH>(1.0f), a);
       const Ch<CH> cz = pick(gone, zero, c * widen<E, CH>(row.z[s]));
       run.H = fma(a, pick((row.start >> s) & 1u, zero, run.H), cz);
@@ -1118,11 +1123,11 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
       a[s] = splat<CH>(1.0f);
       c[s] = q[s] = zero;
       if (s < row.n && !((row.skip >> s) & 1u)) {
-        Ch<CH> r;
-        gate<CH>(widen<E, CH>(row.f[s]), nb, r, c[s], a[s]);
+        Ch<CH> e;
+        gate<CH>(widen<E, CH>(row.f[s]), pb, e, c[s], a[s]);
         const Ch<CH> before = pick((row.start >> s) & 1u, zero, h);
         const Ch<CH> z = widen<E, CH>(row.z[s]);
-        q[s] = (r * c[s]) * sub(before, z);
+        q[s] = slope(e, c[s]) * sub(before, z);
         h = fma(a[s], before, c[s] * z);
       }
     }
@@ -1180,24 +1185,42 @@ __global__ void __launch_bounds__(32 * kBiasWarps)
   }
 }
 
-// How a call's units (a row's group of 64 channels) are laid out: as many as fill
-// the SMs' room of `resident` blocks a whole number of times by a block each, the
-// rest by clusters of blocks along time, doubled while they leave SMs with fewer
-// than two blocks and every block still has a tile.  Measured on 320 units of T =
-// 4096 in bfloat16: backward, where 304 blocks are resident, 231 us in one launch
-// and 178 us with the last 16 units in clusters; forward, where all are, 135 us in
-// one launch and 145 us in two, 156 us in clusters of two.
+// How a call's units (a row's group of 64 channels, of 32 where a lane has single ones)
+// are laid out: as many as give every SM the same number by a block each, the rest by
+// clusters of blocks along time.
+//
+// Forward an SM has room for three blocks, and the clusters run in the room beside the
+// others (8 rows of T = 4096, bfloat16: 320 units 98 us with the last 16 in clusters of
+// four, 114 us by a block each, 110 us in clusters of eight; 160 units 76 us and 98 us;
+// 376 units 116 us in clusters of two, 130 us by a block each), but a lane's single
+// channels are slower there than in clusters alone (5 rows of T = 32749, 1001 floats:
+// 786 us and 583 us).  Backward two blocks fill an SM, and the rest comes after them
+// (320 units 170 us, 231 us by a block each), unless it is more than a unit an SM (252
+// units 141 us by a block each, 181 us in clusters).  Without others, and after them,
+// clusters of four may be three blocks an SM (104 units backward 88 us, 96 us in
+// clusters of two), those of eight two (44 units of T = 16384 forward 149 us, 136 us in
+// clusters of four).
 struct Layout {
   uint64_t whole;  // units taken by one block each
   uint32_t split;  // blocks for each of the others
 };
-Layout layout_of(uint32_t B, uint32_t T, uint32_t D, uint64_t resident) {
-  const uint64_t units = (uint64_t)B * ((D + 63) / 64), tiles = (T + (uint64_t)kTile - 1) / kTile;
-  const uint64_t whole = units / resident * resident, rest = units - whole;
-  uint32_t split = 1;
-  while (rest && split < kMaxCluster && rest * split < 2 * kSMs && tiles >= 2 * split) split *= 2;
+Layout layout_of(uint64_t units, uint32_t T, bool forward, bool single = false) {
+  const uint64_t tiles = (T + (uint64_t)kTile - 1) / kTile;
+  const uint64_t fill = forward ? kSMs : kBackwardBlocks * kSMs, whole = units / fill * fill;
+  const uint64_t rest = units - whole;
+  const bool beside = forward && whole / kSMs % kForwardBlocks != 0;
+  uint32_t split = 1, most = beside ? kMaxCluster / 2 : kMaxCluster;
+  auto fits = [&](uint32_t n) {
+    const uint64_t blocks = beside ? 1 : n <= 4 ? 3 : 2;  // an SM
+    return n <= most && rest * n <= blocks * kSMs && tiles >= n;
+  };
+  if (rest && rest <= kSMs)
+    while (fits(2 * split)) split *= 2;
+  if (single && beside && whole == kSMs && split > 1) return {0, split};
   return {split == 1 ? units : whole, split};
 }
+
+uint64_t backward_units(uint32_t B, uint32_t D) { return (uint64_t)B * ((D + 63) / 64); }
 
 template <class... KArgs>
 cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint32_t cluster,
@@ -1243,12 +1266,14 @@ cudaError_t run_as(ScanParams &p, cudaStream_t st) {
     return launch(kForward ? scan_forward_short_kernel<E, CH> : scan_backward_short_kernel<E, CH>,
                   (n + kShortThreads - 1) / kShortThreads, kShortThreads, 1, 0, st, p);
   }
-  const Layout l = layout_of(p.B, p.T, p.D, kForward ? kForwardResident : kBackwardResident);
+  // Backward, where a lane has single channels, two groups count as a unit: the
+  // workspace's size depends on the sizes alone.
   p.groups = (p.D + 32 * CH - 1) / (32 * CH);
-  p.sums = l.split;
   const uint64_t units = (uint64_t)p.B * p.groups;
-  // in a lane's single channels a unit is two groups, but for a row's odd end
-  const uint64_t whole = l.split == 1 ? units : l.whole * (2 / CH) < units ? l.whole * (2 / CH) : units;
+  Layout l = layout_of(kForward ? units : backward_units(p.B, p.D), p.T, kForward, CH == 1);
+  if (!kForward && CH == 1) l.whole = l.split == 1 ? units : std::min(l.whole * 2, units);
+  p.sums = l.split;
+  const uint64_t whole = l.whole;
   const size_t smem = sizeof(Stage<E, CH, kForward ? 2 : 3>) * kRing * kWarps;
   auto part = [&](uint64_t first, uint64_t count, uint32_t split) {
     p.first = (uint32_t)first, p.split = split;
@@ -1257,8 +1282,9 @@ cudaError_t run_as(ScanParams &p, cudaStream_t st) {
     p.out_step = (int64_t)p.step * p.D, p.state_step = (int64_t)(p.step / (int)NS_SCAN_TILE) * p.D;
     return kForward
                ? launch(split == 1 ? scan_forward_kernel<E, CH, kWide>
-                                   : scan_forward_cluster_kernel<E, CH, kWide>,
-                        count * split, kThreads, split, smem, st, p)
+                          : first > 0  ? scan_forward_cluster_kernel<E, CH, kWide, false>
+                                       : scan_forward_cluster_kernel<E, CH, kWide, true>,
+                        count * split, kThreads, split, smem, st, p, first > 0)
                : launch(split == 1 ? scan_backward_kernel<E, CH, kWide, false>
                                    : scan_backward_kernel<E, CH, kWide, true>,
                         count * split, kThreads, split, smem, st, p, first > 0);
@@ -1337,7 +1363,7 @@ cudaError_t launch_scan_forward(const ns_scan_inputs &in, const float *h0, void 
 }
 
 uint64_t scan_partial_rows(uint32_t B, uint32_t T, uint32_t D) {
-  return (uint64_t)B * (short_rows(B, T, D) ? 1 : layout_of(B, T, D, kBackwardResident).split);
+  return (uint64_t)B * (short_rows(B, T, D) ? 1 : layout_of(backward_units(B, D), T, false).split);
 }
 
 cudaError_t launch_scan_backward(const ns_scan_inputs &in, const float *states, const void *dy,
