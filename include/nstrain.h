@@ -27,9 +27,11 @@
  *  - Element types: NS_F32, NS_BF16, NS_F16.  States, sums, softmax
  *    statistics and losses are 32-bit floats; an output of 16 bits is rounded
  *    once, from 32 bits.
- *  - Every sum is taken in an order fixed by the sizes alone: the same
- *    arguments give the same bits, on every call and every stream.  What a row
- *    (of a scan, of logits) gets does not depend on the other rows of the call.
+ *  - Every sum is taken in a fixed order: the same arguments give the same
+ *    bits, on every call and every stream.  What a row (of a scan, of logits)
+ *    gets does not depend on the other rows of the call; the order of a sum
+ *    over rows (dbias, the balance loss) depends on the sizes and on the
+ *    alignment of the arrays.
  *  - Values at padded or unlearned positions are never used, whatever they
  *    are (NaN and infinities among them); the outputs there are 0 (-1 for
  *    expert ids).
