@@ -216,6 +216,14 @@ struct Copier {
                                        int lane) const {
     constexpr int kRows = kBytes / 4;
     to += lane / (32 / kRows) * 128 + into;
+    if (kBytes == 4 && n == kSteps) {  // one branch in place of one a row
+      if (row == kSteps) return;
+      const E *at = from.at;
+#pragma unroll
+      for (int s = 0; s < kSteps; s += kRows, at += kRows * from.time)
+        copy_async<kBytes>(to + s * 128, at);
+      return;
+    }
 #pragma unroll
     for (int s = 0; s < kSteps; s += kRows)
       if (s + row < n) copy_async<kBytes>(to + s * 128, from.at + s * from.time);
