@@ -168,6 +168,30 @@ __device__ __forceinline__ void prefetch_entries(const DistillParams &p, uint32_
     asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
 }
 
+// A row's ids and teacher logits into `e`, by lanes; its largest teacher logit, the
+// first of them and its id.
+struct Teacher {
+  float m, lse;
+  uint32_t top;  // 0xffffffff: no entry
+  int top_id;
+};
+__device__ __forceinline__ Teacher load_teacher(const DistillParams &p, uint32_t row, int lane,
+                                                int *ids, float *logits) {
+  const int64_t base = (int64_t)row * p.K;
+  Teacher r = {kNegInf, p.teacher_lse ? p.teacher_lse[row] : 0.0f, 0xffffffffu, 0};
+#pragma unroll 4
+  for (uint32_t k = lane; k < p.K; k += 32) {
+    const int64_t v = p.ids_64 ? static_cast<const int64_t *>(p.ids)[base + k]
+                               : (int64_t)static_cast<const int32_t *>(p.ids)[base + k];
+    const float t = load_top(p.top, p.top_dtype, base + k);
+    const int id = v >= 0 && v < (int64_t)p.V ? (int)v : -1;
+    ids[k] = id;
+    logits[k] = id >= 0 ? t : kNegInf;
+    if (id >= 0 && t > r.m) r.m = t, r.top = k, r.top_id = id;
+  }
+  return r;
+}
+
 // The entries' warp: the teacher's probabilities and the student's logits at the
 // entries of this block's slice [from, to).
 struct EntrySums {
@@ -176,28 +200,18 @@ struct EntrySums {
   float part;  // sum of p (log p - (s - c) / temp) over the slice
 };
 template <class E>
-__device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uint32_t row,
+__device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p,
                                                      const E *logits, const RowSlice<E> &s,
-                                                     uint32_t rank, int lane, const Entries &e) {
+                                                     uint32_t rank, int lane, const Entries &e,
+                                                     const Teacher &teacher) {
   // an id is this block's: in its chunks, or at the row's ends for the first block
   const int last = s.from + (int)s.mine * (16 / (int)sizeof(E));
   auto ours = [&](int id) {
     return (id >= s.from && id < last) || (rank == 0 && id >= 0 && (id < s.head || id >= s.tail));
   };
-  const int64_t base = (int64_t)row * p.K;
-  float m = kNegInf;
-  uint32_t top = 0xffffffffu;  // the first entry of the largest logit, and its id
-  int top_id = 0;
-#pragma unroll 4
-  for (uint32_t k = lane; k < p.K; k += 32) {
-    const int64_t v = p.ids_64 ? static_cast<const int64_t *>(p.ids)[base + k]
-                               : (int64_t)static_cast<const int32_t *>(p.ids)[base + k];
-    const float t = load_top(p.top, p.top_dtype, base + k);
-    const int id = v >= 0 && v < (int64_t)p.V ? (int)v : -1;
-    e.id[k] = id;
-    e.logp[k] = id >= 0 ? t : kNegInf;
-    if (id >= 0 && t > m) m = t, top = k, top_id = id;
-  }
+  float m = teacher.m;
+  uint32_t top = teacher.top;
+  int top_id = teacher.top_id;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float om = __shfl_xor_sync(0xffffffffu, m, o);
@@ -225,12 +239,11 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
   r.c = to_f32(at_top);
   if (r.c == kNegInf) r.c = 0.0f;
   const float base_m = base_of(m);
-  const float lse = p.teacher_lse ? p.teacher_lse[row] : 0.0f;
   float sum = 0.0f;
 #pragma unroll 2
   for (uint32_t k = lane; k < p.K; k += 32) {
     const float t = e.logp[k];
-    const float l = p.teacher_lse ? fmaf(t, p.inv_temp, -lse) : (t - base_m) * p.inv_temp;
+    const float l = p.teacher_lse ? fmaf(t, p.inv_temp, -teacher.lse) : (t - base_m) * p.inv_temp;
     // an absent entry stays at -inf whatever lse is
     const float keep = e.id[k] < 0 ? kNegInf : l;
     const float v = expf(keep);
@@ -264,11 +277,11 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p, uin
 // the sum of their p (in the entries' order); the others' ids become -1.  `seen` has
 // kSeen bits, 0 before and after, that an id's hash picks from: an id that finds its
 // bit set is looked for among the others.
-constexpr uint32_t kSeen = 8192;
+constexpr uint32_t kSeen = 4096;
 __device__ __forceinline__ uint32_t bit_of(int id) {  // Knuth's multiplicative hash
-  return (uint32_t)id * 2654435761u >> 19;
+  return (uint32_t)id * 2654435761u >> 20;
 }
-static_assert(kSeen == 1u << (32 - 19), "a hash is a bit's number");
+static_assert(kSeen == 1u << (32 - 20), "a hash is a bit's number");
 static_assert(NS_DISTILL_MAX_TOP <= 32 * 32, "a lane's entries are a word's bits");
 __device__ void join_repeated(uint32_t K, int lane, const Entries &e, uint32_t *seen) {
   uint32_t again = 0;  // this lane's entries (k / 32) that found their bit set
@@ -418,6 +431,7 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
   e.p = e.logp + p.K;
   e.x = e.p + p.K;
   e.id = reinterpret_cast<int *>(e.x + p.K);
+  int *next_id = e.id + p.K;
   for (uint32_t w = lane; kGrad && w < kSeen / 32; w += 32) seen[w] = 0;
   __syncwarp();
   auto nothing = [](uint32_t) {};
@@ -425,6 +439,8 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
   RowWalk walk(blockIdx.x / C, stride);
   uint32_t row = walk.learned(p, lane, nothing);
   if (parity) row = walk.learned(p, lane, nothing);
+  Teacher teacher = {};
+  if (row < p.N) teacher = load_teacher(p, row, lane, e.id, e.logp);
   for (uint32_t i = parity; row < p.N; i += 2) {
     uint32_t next = walk.learned(p, lane, nothing);
     next = walk.learned(p, lane, nothing);
@@ -434,9 +450,7 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
     const int at = s.end_of(p, rank, lane);
     const float end = at >= 0 ? to_f32(src[at]) : kNegInf;  // this lane's logit at the row's ends
     const float weight = p.weight ? p.weight[row] : 1.0f;
-    const EntrySums sums = teacher_entries<E>(p, row, src, s, rank, lane, e);
-    if (kGrad) join_repeated(p.K, lane, e, seen);
-    __syncwarp();
+    const EntrySums sums = teacher_entries<E>(p, src, s, rank, lane, e, teacher);
     if (lane == 0) barrier_expect(&sh.arrived[i % kPlaces], C * sizeof(float4));
     MaxSum mine = {end, end == kNegInf ? 0.0f : end == end ? 1.0f : end};
     named_wait(3 + parity);
@@ -447,6 +461,10 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
       send(remote_smem(&sh.stats[i % kPlaces][rank], lane),
            remote_smem(&sh.arrived[i % kPlaces], lane),
            make_float4(mine.m, mine.s, sums.part, sums.mass));
+    // what the exchange does not wait for: on its way meanwhile
+    __syncwarp();
+    if (kGrad) join_repeated(p.K, lane, e, seen);
+    if (next < p.N) teacher = load_teacher(p, next, lane, next_id, e.logp);
     const RowStats r = row_stats(p, sh, i, C, lost);
     if (rank == 0 && lane == 0) {
       float loss = r.parts + r.mass * fmaf(base_of(r.all.m) - sums.c, p.inv_temp, logf(r.all.s));
@@ -472,6 +490,8 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
       __syncwarp();
     }
     row = next;
+    int *const ids = e.id;
+    e.id = next_id, next_id = ids;
   }
 }
 
@@ -513,8 +533,8 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
   if (tid >= nthr) {
     const uint32_t parity = warp - nthr / 32;
     float *arrays = reinterpret_cast<float *>(smem + (size_t)p.slice * 16);
-    uint32_t *seen = reinterpret_cast<uint32_t *>(arrays + kEntryWarps * 4 * p.K);
-    entry_warp<E, kGrad>(p, sh, arrays + parity * 4 * p.K, seen + parity * (kSeen / 32),
+    uint32_t *seen = reinterpret_cast<uint32_t *>(arrays + kEntryWarps * 5 * p.K);
+    entry_warp<E, kGrad>(p, sh, arrays + parity * 5 * p.K, seen + parity * (kSeen / 32),
                          parity, rank, C, stride, lane);
     return;
   }
@@ -673,7 +693,7 @@ cudaError_t clusters_resident(void (*k)(KArgs...), const cudaLaunchConfig_t &cfg
 
 // Shared memory of a block: its slice, and two rows' entries.
 size_t distill_smem(uint32_t slice, uint32_t K, bool grad) {
-  return (size_t)slice * 16 + kEntryWarps * ((size_t)K * 16 + (grad ? kSeen / 8 : 0));
+  return (size_t)slice * 16 + kEntryWarps * ((size_t)K * 20 + (grad ? kSeen / 8 : 0));
 }
 
 template <class E, bool kGrad>
