@@ -109,7 +109,19 @@ template <class E, int kBytes, int SG, int kPitch>
 __device__ __forceinline__ void copy_pieces(const RouteParams &p, uint64_t n0, uint32_t tokens,
                                             float *tile) {
   constexpr int kN = kBytes / sizeof(E);
-  for (Walk<E> w(p, n0, p.E / kN, kN); w.row < tokens; w.next()) {
+  Walk<E> w(p, n0, p.E / kN, kN);
+  if (w.rest == 0) {  // whole rows at a time: a thread stays in its column
+    const uint32_t e = w.at * kN;
+    float *row = tile + (w.row * p.lanes + e / SG) * kPitch;
+    unsigned char *to = reinterpret_cast<unsigned char *>(
+        reinterpret_cast<E *>(row + (sizeof(E) == 2 ? SG / 2 : 0)) + e % SG);
+    const uint32_t step = w.rows * p.lanes * kPitch * 4;
+#pragma unroll 4
+    for (uint32_t r = w.row; r < tokens; r += w.rows, to += step, w.from += w.step)
+      copy_async<kBytes>(to, w.from);
+    return;
+  }
+  for (; w.row < tokens; w.next()) {
     const uint32_t e = w.at * kN;
     E *row = reinterpret_cast<E *>(tile + (w.row * p.lanes + e / SG) * kPitch +
                                    (sizeof(E) == 2 ? SG / 2 : 0));
@@ -169,19 +181,22 @@ __device__ __forceinline__ void load_narrow(const float *at, float (&v)[S]) {
   }
 }
 
-// Add the probabilities of a thread's n experts, kForwardThreads (a row or more of
-// SG) apart, up over every `parts`-th token.
+// Add the probabilities of a thread's n times four experts, kForwardThreads times four
+// (whole rows of SG) apart, up over every `parts`-th token.
 template <int n, int SG, int kPitch, int kMax>
 __device__ __forceinline__ void add_columns(const float *column, const float *inv, uint32_t first,
                                             uint32_t tokens, uint32_t parts, uint32_t lanes,
-                                            float (&sum)[kMax]) {
+                                            Ch<2> (&sum)[kMax][2]) {
   const float *at = column + first * lanes * kPitch;
 #pragma unroll 4
   for (uint32_t r = first; r < tokens; r += parts, at += parts * lanes * kPitch) {
-    const float by = inv[r];
+    const Ch<2> by = splat<2>(inv[r]);
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      sum[i] = fmaf(at[i * (kForwardThreads / SG) * kPitch], by, sum[i]);
+    for (int i = 0; i < n; ++i) {
+      const float4 x = *reinterpret_cast<const float4 *>(at + i * (4 * kForwardThreads / SG) * kPitch);
+      sum[i][0] = fma(Ch<2>{x.x, x.y}, by, sum[i][0]);
+      sum[i][1] = fma(Ch<2>{x.z, x.w}, by, sum[i][1]);
+    }
   }
 }
 
@@ -190,7 +205,7 @@ __device__ __forceinline__ void add_columns(const float *column, const float *in
 // all banks.
 template <int S, int G>
 __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forward_kernel(const RouteParams p) {
-  constexpr int SG = S * G, kPitch = SG + 4, kMaxColumns = NS_ROUTE_MAX_EXPERTS / kForwardThreads;
+  constexpr int SG = S * G, kPitch = SG + 4, kMaxColumns = NS_ROUTE_MAX_EXPERTS / (4 * kForwardThreads);
   extern __shared__ __align__(16) float tile[];
   const uint32_t LP = p.lanes, tokens = kForwardThreads / LP, columns = LP * SG;
   float *inv = tile + kForwardThreads * kPitch;                     // [tokens]
@@ -201,16 +216,17 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
   float2 *gathered = reinterpret_cast<float2 *>(top_id + tokens * p.k);
   __shared__ int real_tokens, real_of[kTogether];
   if (p.together) cluster_arrive_relaxed();
+  else release_dependents();  // the second kernel is there when this one ends
   const uint32_t tid = threadIdx.x, lane = tid & 31, token = tid / LP, lp = tid % LP;
   float *mine = tile + tid * kPitch;
   for (uint32_t e = tid; e < columns; e += kForwardThreads) chosen[e] = 0;
   if (tid == 0) real_tokens = 0;
-  // an expert's (or several's, 128 apart) sum over every `parts`-th token
-  const uint32_t side = columns < kForwardThreads ? columns : kForwardThreads;
-  const uint32_t parts = kForwardThreads / side, my_part = tid / side, per_thread = columns / side;
-  float sum[kMaxColumns];
+  // four experts' (or more, 512 apart) sums over every `parts`-th token
+  const uint32_t side = columns / 4 < kForwardThreads ? columns / 4 : kForwardThreads;
+  const uint32_t parts = kForwardThreads / side, my_part = tid / side;
+  Ch<2> sum[kMaxColumns][2];
 #pragma unroll
-  for (int i = 0; i < kMaxColumns; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < kMaxColumns; ++i) sum[i][0] = sum[i][1] = splat<2>(0.0f);
   int counted = 0;
   const uint64_t tiles = ((uint64_t)p.N + tokens - 1) / tokens;
   for (uint64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -358,15 +374,12 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
       p.ids[n0 * p.k + i] = top_id[i];
       p.weights[n0 * p.k + i] = top_x[i];
     }
-    const float *column = tile + (tid % side) / SG * kPitch + (tid % side) % SG;
-    if (per_thread == 1)
+    const uint32_t e = tid % side * 4;
+    const float *column = tile + e / SG * kPitch + e % SG;
+    if (columns <= 4 * kForwardThreads)
       add_columns<1, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
-    else if (per_thread == 2)
-      add_columns<2, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
-    else if (per_thread == 4)
-      add_columns<4, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
     else
-      add_columns<8, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
+      add_columns<2, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
   }
   counted = warp_sum_i32(counted);
   if (lane == 0) atomicAdd(&real_tokens, counted);
@@ -374,7 +387,9 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
   // the parts of an expert's sum, in order
 #pragma unroll
   for (int i = 0; i < kMaxColumns; ++i)
-    if (i < (int)per_thread) tile[my_part * columns + tid % side + i * kForwardThreads] = sum[i];
+    if (4 * (tid % side + i * kForwardThreads) < columns)
+      *reinterpret_cast<float4 *>(tile + my_part * columns + 4 * (tid % side + i * kForwardThreads)) =
+          make_float4(sum[i][0].v[0], sum[i][0].v[1], sum[i][1].v[0], sum[i][1].v[1]);
   __syncthreads();
   const uint32_t rank = p.together ? cluster_rank() : 0;
   if (p.together) cluster_wait();  // the first block runs
