@@ -24,8 +24,8 @@
 // every SM full it is bound by their issue (8 x 4096 x 2432 bfloat16: 92 us, 5.2 TB/s,
 // 54 % of the slots, the rest waiting for a tile's exchange), backward by memory (142
 // us, 5.6 TB/s: 10 bytes and 40 instructions).  Few units are bound by the latency of a
-// tile, 1.2 us in a block alone, 2 to 4 us in a cluster (1 x 32749 x 1001 floats: 130
-// and 198 us, 3.0 and 3.3 TB/s).
+// tile, 1.2 us in a block alone, 2 to 4 us in a cluster (1 x 32749 x 1001 floats: 129
+// and 195 us, 3.1 and 3.4 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
