@@ -10,19 +10,19 @@
 // registers.  A choice is the largest group's, found again among that group's S
 // logits alone; of equal ones the first group and the first place win.  Then the
 // logits are replaced by their exponentials, and the threads turn round: each
-// takes an expert and adds its probabilities up over the tile's tokens.  Blocks
+// takes four experts and adds their probabilities up over the tile's tokens.  Blocks
 // write rows of partial sums and counts, and a second kernel adds them in a fixed
 // order (no floating-point atomics: the loss has the same bits every time).
 //
 // Backward, L lanes take a token, R consecutive experts each, in registers; the
 // softmax is computed again, which costs less than keeping it.
 //
-// Forward latency bounds it (262144 x 256 bfloat16, k = 8: 97 us, 1.5 TB/s, 46 % of the
-// issue slots): a token's logits take 1 KB of shared memory, which holds twelve warps
-// an SM; a choice costs 4 us of it.  Backward 69 us, 4.2 TB/s, 62 % of the issue slots.
+// Forward latency bounds it, of 20 warps an SM (262144 x 256 bfloat16, k = 8: 86 us, 1.7
+// TB/s); a choice costs 4 us of it.  Backward 69 us, 4.2 TB/s, 62 % of the issue slots.
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -104,9 +104,9 @@ struct Walk {
 
 // A tile's logits into shared memory as they are: token n0 + row's expert e at row
 // `row * lanes + e / SG`, place e % SG.  `tokens` of them are inside the call.  A
-// row of 16-bit logits takes the second half of its room of floats: its thread
-// widens it in place, from the front.
-template <class E, int kBytes, int SG, int kPitch>
+// row of 16-bit logits takes the second half of its room of floats, if it has that: its
+// thread widens it in place, from the front.
+template <class E, int kBytes, int SG, int kPitch, int kAt>
 __device__ __forceinline__ void copy_pieces(const RouteParams &p, uint64_t n0, uint32_t tokens,
                                             float *tile) {
   constexpr int kN = kBytes / sizeof(E);
@@ -115,7 +115,7 @@ __device__ __forceinline__ void copy_pieces(const RouteParams &p, uint64_t n0, u
     const uint32_t e = w.at * kN;
     float *row = tile + (w.row * p.lanes + e / SG) * kPitch;
     unsigned char *to = reinterpret_cast<unsigned char *>(
-        reinterpret_cast<E *>(row + (sizeof(E) == 2 ? SG / 2 : 0)) + e % SG);
+        reinterpret_cast<E *>(row + kAt) + e % SG);
     const uint32_t step = w.rows * p.lanes * kPitch * 4;
 #pragma unroll 4
     for (uint32_t r = w.row; r < tokens; r += w.rows, to += step, w.from += w.step)
@@ -124,20 +124,20 @@ __device__ __forceinline__ void copy_pieces(const RouteParams &p, uint64_t n0, u
   }
   for (; w.row < tokens; w.next()) {
     const uint32_t e = w.at * kN;
-    E *row = reinterpret_cast<E *>(tile + (w.row * p.lanes + e / SG) * kPitch +
-                                   (sizeof(E) == 2 ? SG / 2 : 0));
+    E *row = reinterpret_cast<E *>(tile + (w.row * p.lanes + e / SG) * kPitch + kAt);
     copy_async<kBytes>(row + e % SG, w.from);
   }
 }
 template <class E, int SG, int kPitch>
 __device__ __forceinline__ void load_tile(const RouteParams &p, uint64_t n0, uint32_t tokens,
                                           float *tile) {
+  constexpr int kAt = sizeof(E) == 2 && kPitch > SG ? SG / 2 : 0;
   if (p.wide == 16) {
-    copy_pieces<E, 16, SG, kPitch>(p, n0, tokens, tile);
+    copy_pieces<E, 16, SG, kPitch, kAt>(p, n0, tokens, tile);
   } else if (p.wide == 8) {
-    copy_pieces<E, 8, SG, kPitch>(p, n0, tokens, tile);
+    copy_pieces<E, 8, SG, kPitch, kAt>(p, n0, tokens, tile);
   } else if (p.wide == 4) {
-    copy_pieces<E, 4, SG, kPitch>(p, n0, tokens, tile);
+    copy_pieces<E, 4, SG, kPitch, kAt>(p, n0, tokens, tile);
   } else if constexpr (sizeof(E) == 2) {  // no asynchronous copy takes two bytes
     constexpr int kFlight = 8;
     Walk<E> load(p, n0, p.E, 1), store = load;
@@ -150,7 +150,7 @@ __device__ __forceinline__ void load_tile(const RouteParams &p, uint64_t n0, uin
       for (int i = 0; i < kFlight; ++i, store.next())
         if (store.row < tokens)
           reinterpret_cast<E *>(tile + (store.row * p.lanes + store.at / SG) * kPitch +
-                                SG / 2)[store.at % SG] = v[i];
+                                kAt)[store.at % SG] = v[i];
     }
   }
   copy_commit();
@@ -201,16 +201,41 @@ __device__ __forceinline__ void add_columns(const float *column, const float *in
   }
 }
 
+// The same of logits that are kept: their exponentials are computed again.  of[r]: minus
+// a token's maximum, and what its exponentials are scaled by.
+template <class E, int SG, int kPitch>
+__device__ __forceinline__ void add_kept(const float *column, const float2 *of, uint32_t first,
+                                         uint32_t tokens, uint32_t parts, uint32_t lanes,
+                                         Ch<2> (&sum)[2]) {
+  const float *at = column + first * lanes * kPitch;
+#pragma unroll 4
+  for (uint32_t r = first; r < tokens; r += parts, at += parts * lanes * kPitch) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(at);
+    const float2 f = of[r];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Ch<2> y = (widen_pair<E>(i ? x.y : x.x) + splat<2>(f.x)) * splat<2>(kLog2e);
+      sum[i] = fma(Ch<2>{exp2_sfu(y.v[0]), exp2_sfu(y.v[1])}, splat<2>(f.y), sum[i]);
+    }
+  }
+}
+
 // G groups of S experts a thread.  Its row of shared memory is S * G floats and
 // four more, an odd number of 16 bytes: eight threads' 16-byte accesses then use
-// all banks.
-template <int S, int G>
-__global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forward_kernel(const RouteParams p) {
-  constexpr int SG = S * G, kPitch = SG + 4, kMaxColumns = NS_ROUTE_MAX_EXPERTS / (4 * kForwardThreads);
+// all banks.  With a 16-bit type for T the logits (of that type) are kept as they are, in
+// half the room: 20 warps share an SM in place of 12, and exponentials are computed twice
+// (262144 x 256: 86 us, 97 us with floats in shared memory).
+template <int S, int G, class T>
+__global__ void __launch_bounds__(kForwardThreads, S != 16 ? 5 : sizeof(T) == 2 ? 5 : 3)
+    route_forward_kernel(const RouteParams p) {
+  constexpr bool kKept = sizeof(T) == 2;
+  constexpr int SG = S * G, kPitch = (kKept ? SG / 2 : SG) + 4, kMaxColumns = NS_ROUTE_MAX_EXPERTS / (4 * kForwardThreads);
   extern __shared__ __align__(16) float tile[];
   const uint32_t LP = p.lanes, tokens = kForwardThreads / LP, columns = LP * SG;
   float *inv = tile + kForwardThreads * kPitch;                     // [tokens]
-  int *chosen = reinterpret_cast<int *>(inv + kForwardThreads);     // [columns]
+  float2 *of = reinterpret_cast<float2 *>(inv);                     // or this [tokens]
+  int *chosen =                                                     // [columns]
+      reinterpret_cast<int *>(inv + (kKept ? 2 : 1) * kForwardThreads);
   float *top_x = reinterpret_cast<float *>(chosen + columns);       // [tokens][k]: logit, weight
   int *top_id = reinterpret_cast<int *>(top_x + tokens * p.k);      // [tokens][k]
   // in a cluster, the first block's: the others' sums and counts, and tokens
@@ -237,7 +262,8 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     // on its way beside the copies
     const int document =
         token < here ? (p.doc ? __ldg(p.doc + n0 + token) : 0) : -1;
-    if (p.dtype == NS_F32) load_tile<float, SG, kPitch>(p, n0, here, tile);
+    if constexpr (kKept) load_tile<T, SG, kPitch>(p, n0, here, tile);
+    else if (p.dtype == NS_F32) load_tile<float, SG, kPitch>(p, n0, here, tile);
     else if (p.dtype == NS_BF16) load_tile<__nv_bfloat16, SG, kPitch>(p, n0, here, tile);
     else load_tile<__half, SG, kPitch>(p, n0, here, tile);
     const bool real = document >= 0;
@@ -251,7 +277,9 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float v[S];
-      if (p.dtype == NS_F32)
+      if constexpr (kKept)
+        load_narrow<T, S>(mine + g * S / 2, v);
+      else if (p.dtype == NS_F32)
         load_group<S>(mine + g * S, v);
       else if (p.dtype == NS_BF16)
         load_narrow<__nv_bfloat16, S>(mine + SG / 2 + g * S / 2, v);
@@ -262,7 +290,16 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
         for (int q = 0; q < S; ++q)
           if (g * S + q >= used) v[q] = kNegInf;
       }
-      if (used < SG || p.dtype != NS_F32) {
+      if constexpr (kKept) {
+        if (used < SG) {
+#pragma unroll
+          for (int q = 0; q < S; q += 8) {
+            const Ch<2> x[4] = {{v[q], v[q + 1]}, {v[q + 2], v[q + 3]}, {v[q + 4], v[q + 5]},
+                                {v[q + 6], v[q + 7]}};
+            *reinterpret_cast<uint4 *>(mine + (g * S + q) / 2) = narrow_chunk<T>(x);
+          }
+        }
+      } else if (used < SG || p.dtype != NS_F32) {
 #pragma unroll
         for (int q = 0; q < S; q += 4)
           *reinterpret_cast<float4 *>(mine + g * S + q) =
@@ -301,7 +338,8 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
         if (top[i] == best) g = i;
       if (top[0] == best) g = 0;
       float v[S];
-      load_group<S>(mine + g * S, v);
+      if constexpr (kKept) load_narrow<T, S>(mine + g * S / 2, v);
+      else load_group<S>(mine + g * S, v);
       uint32_t equal = 0;
       float less = kNegInf;
 #pragma unroll
@@ -328,32 +366,43 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
     const float base = m == kNegInf ? 0.0f : m;
     // The sum is that of every eight experts, and of those by pairs of neighbours: the
     // same whatever the number of threads.
-    float part[SG / 8];
+    constexpr int kRun = SG < 64 ? SG : 64;  // not all unrolled: registers
+    float s = 0.0f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < SG; i0 += kRun) {
+      float part[kRun / 8];
 #pragma unroll
-    for (int i = 0; i < SG; i += 8) {
-      Ch<2> x[4], sum;
-      load_pairs(mine + i, x);
+      for (int i = 0; i < kRun; i += 8) {
+        Ch<2> x[4], sum;
+        float *at = mine + (kKept ? (i0 + i) / 2 : i0 + i);
+        if constexpr (kKept) widen_chunk<T>(*reinterpret_cast<const uint4 *>(at), x);
+        else load_pairs(at, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const Ch<2> y = (x[q] + splat<2>(-base)) * splat<2>(kLog2e);
-        x[q] = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
-        sum = q == 0 ? x[q] : sum + x[q];
+        for (int q = 0; q < 4; ++q) {
+          const Ch<2> y = (x[q] + splat<2>(-base)) * splat<2>(kLog2e);
+          x[q] = {exp2_sfu(y.v[0]), exp2_sfu(y.v[1])};
+          sum = q == 0 ? x[q] : sum + x[q];
+        }
+        if constexpr (!kKept) {
+          reinterpret_cast<float4 *>(at)[0] =
+              make_float4(x[0].v[0], x[0].v[1], x[1].v[0], x[1].v[1]);
+          reinterpret_cast<float4 *>(at)[1] =
+              make_float4(x[2].v[0], x[2].v[1], x[3].v[0], x[3].v[1]);
+        }
+        part[i / 8] = sum.v[0] + sum.v[1];
       }
-      *reinterpret_cast<float4 *>(mine + i) =
-          make_float4(x[0].v[0], x[0].v[1], x[1].v[0], x[1].v[1]);
-      *reinterpret_cast<float4 *>(mine + i + 4) =
-          make_float4(x[2].v[0], x[2].v[1], x[3].v[0], x[3].v[1]);
-      part[i / 8] = sum.v[0] + sum.v[1];
+#pragma unroll
+      for (int n = 1; n < kRun / 8; n *= 2)
+#pragma unroll
+        for (int i = 0; i < kRun / 8; i += 2 * n) part[i] += part[i + n];
+      s = i0 == 0 ? part[0] : s + part[0];
     }
-#pragma unroll
-    for (int n = 1; n < SG / 8; n *= 2)
-#pragma unroll
-      for (int i = 0; i < SG / 8; i += 2 * n) part[i] += part[i + n];
-    float s = part[0];
+    static_assert(SG <= 2 * kRun, "the sum of two runs is that of neighbours");
     for (uint32_t o = 1; o < LP; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float by_all = s == 0.0f ? 0.0f : 1.0f / s;
     if (lp == 0) {
-      inv[token] = by_all;
+      if constexpr (kKept) of[token] = make_float2(-base, by_all);
+      else inv[token] = by_all;
       counted += s != 0.0f;
     }
     __syncwarp();  // the token's threads have written their choices
@@ -376,8 +425,15 @@ __global__ void __launch_bounds__(kForwardThreads, S == 16 ? 3 : 5) route_forwar
       p.weights[n0 * p.k + i] = top_x[i];
     }
     const uint32_t e = tid % side * 4;
-    const float *column = tile + e / SG * kPitch + e % SG;
-    if (columns <= 4 * kForwardThreads)
+    const float *column = tile + e / SG * kPitch + (kKept ? e % SG / 2 : e % SG);
+    if constexpr (kKept)
+#pragma unroll
+      for (int i = 0; i < kMaxColumns; ++i) {
+        if (4 * kForwardThreads * i < columns)
+          add_kept<T, SG, kPitch>(column + i * (4 * kForwardThreads / SG) * kPitch, of, my_part,
+                                  tokens, parts, LP, sum[i]);
+      }
+    else if (columns <= 4 * kForwardThreads)
       add_columns<1, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
     else
       add_columns<2, SG, kPitch>(column, inv, my_part, tokens, parts, LP, sum);
@@ -730,14 +786,14 @@ Shape shape_of(uint32_t N, uint32_t E) {
   return s;
 }
 
-template <int S, int G>
+template <int S, int G, class T = float>
 cudaError_t launch_forward(RouteParams &p, cudaStream_t st) {
-  const size_t tokens = kForwardThreads / p.lanes;
-  size_t smem = 4 * (kForwardThreads * (size_t)(S * G + 4) + kForwardThreads +
+  const size_t tokens = kForwardThreads / p.lanes, es = sizeof(T);
+  size_t smem = 4 * (kForwardThreads * (size_t)(S * G * es / 4 + 4) + kForwardThreads * 4 / es +
                      p.lanes * S * G + 2 * tokens * p.k);
   smem = (smem + 15) / 16 * 16;  // the sums of a cluster's blocks start at a whole pair
   if (p.together) smem += 8 * (size_t)p.blocks * p.E;
-  auto *k = route_forward_kernel<S, G>;
+  auto *k = route_forward_kernel<S, G, T>;
   cudaError_t e = allow_shared_memory((const void *)k);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -802,7 +858,8 @@ uint32_t route_blocks(uint32_t N, uint32_t E) {
   const uint64_t tiles = shape_of(N, E).tiles;
   // up to two tiles a block, one cluster does without the second kernel
   if (tiles <= 2 * kTogether) return 0;
-  return tiles < 3 * kSMs ? (uint32_t)tiles : 3 * kSMs;
+  const uint32_t most = (E > 128 ? 5 : 3) * kSMs;
+  return tiles < most ? (uint32_t)tiles : most;
 }
 
 cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float *weights,
@@ -819,7 +876,11 @@ cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float 
   p.mass = static_cast<float *>(workspace);
   p.chosen = reinterpret_cast<int32_t *>(p.mass + (uint64_t)p.blocks * in.E);
   p.real = p.chosen + (uint64_t)p.blocks * in.E;
-  const cudaError_t e = shape.S == 16  ? launch_forward<16, 8>(p, st)
+  const bool kept = shape.S == 16 && in.dtype != NS_F32;
+  if (shape.S == 16 && !kept) p.blocks = std::min(p.blocks, 3 * kSMs);
+  const cudaError_t e = kept ? in.dtype == NS_BF16 ? launch_forward<16, 8, __nv_bfloat16>(p, st)
+                                                   : launch_forward<16, 8, __half>(p, st)
+                        : shape.S == 16 ? launch_forward<16, 8>(p, st)
                         : shape.G == 8 ? launch_forward<8, 8>(p, st)
                         : shape.G == 4 ? launch_forward<8, 4>(p, st)
                         : shape.G == 2 ? launch_forward<8, 2>(p, st)
