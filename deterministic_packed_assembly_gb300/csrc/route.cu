@@ -14,11 +14,11 @@
 // write rows of partial sums and counts, and a second kernel adds them in a fixed
 // order (no floating-point atomics: the loss has the same bits every time).
 //
-// Backward, L lanes take a token, R consecutive experts each, in registers; the
-// softmax is computed again, which costs less than keeping it.
+// Backward, L lanes take a token, R experts each, in registers; the softmax is computed
+// again, which costs less than keeping it.
 //
 // Forward latency bounds it, of 20 warps an SM (262144 x 256 bfloat16, k = 8: 86 us, 1.7
-// TB/s); a choice costs 4 us of it.  Backward 69 us, 4.2 TB/s, 62 % of the issue slots.
+// TB/s); a choice costs 4 us of it.  Backward issue and memory (62 us, 4.7 TB/s).
 
 #include <cuda_runtime.h>
 
@@ -562,93 +562,92 @@ __global__ void __launch_bounds__(kFinalThreads) __cluster_dims__(kFinalBlocks, 
 }
 
 // ---- backward -------------------------------------------------------------------
-// A lane's R experts of a token as they lie in memory.
-template <class E, int R>
+// A lane's R experts of a token: every L-th one, or (kPairs) pair of 16-bit ones where
+// rows can be moved by 4 bytes, so that lanes side by side move what lies side by side,
+// whatever the rows' alignment.  (R consecutive ones, by 16 bytes a lane where aligned:
+// 262144 x 256 floats 110 us, 97 us so; bfloat16 69 us and 62 us; 250 experts, by 2
+// bytes, 310 us and 61 us.)
+template <int L, bool kPairs>
+struct Places {
+  uint32_t first;
+  __device__ __forceinline__ explicit Places(uint32_t lane) : first(lane * (kPairs ? 2 : 1)) {}
+  static __device__ __forceinline__ uint32_t after(int r) {  // expert r: first + after(r)
+    return r / 2 * 2 * L + r % 2 * (kPairs ? 1 : L);
+  }
+};
+
+// They as they lie in memory, in pairs: one register of 16-bit ones, or two.
+template <class E, int L, int R, bool kPairs>
 struct Piece {
-  static constexpr int kN = 16 / sizeof(E);
-  uint4 v[R / kN];
-  __device__ __forceinline__ void load(const E *src, uint32_t i0, uint32_t experts, int wide) {
+  using Pair = std::conditional_t<sizeof(E) == 2, uint32_t, float2>;
+  Pair x[R / 2];
+  // -inf where there is no expert.
+  __device__ __forceinline__ void load(const E *src, const Places<L, kPairs> &at, uint32_t experts) {
 #pragma unroll
-    for (int r = 0; r < R; r += kN) {
-      uint4 &to = v[r / kN];
-      if (wide == 16) {
-        if (i0 + r < experts) to = *reinterpret_cast<const uint4 *>(src + r);
-      } else if (wide == 8) {
-        if (i0 + r < experts) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(src + r);
-          to.x = x.x, to.y = x.y;
-        }
-        if (i0 + r + kN / 2 < experts) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(src + r + kN / 2);
-          to.z = x.x, to.w = x.y;
-        }
+    for (int r = 0; r < R; r += 2) {
+      const uint32_t e = at.after(r), i = at.first + e;
+      if constexpr (sizeof(E) == 4) {
+        x[r / 2] = {i < experts ? src[e] : kNegInf, i + L < experts ? src[e + L] : kNegInf};
       } else {
-        E x[kN];
-#pragma unroll
-        for (int q = 0; q < kN; ++q)
-          x[q] = i0 + r + q < experts ? src[r + q] : from_f32<E>(0.0f);
-        to = *reinterpret_cast<const uint4 *>(x);
+        const uint32_t none = narrow_pair<E>(splat<2>(kNegInf));
+        if constexpr (kPairs) {
+          x[r / 2] = i < experts ? *reinterpret_cast<const uint32_t *>(src + e) : none;
+        } else {
+          const uint16_t *bits = reinterpret_cast<const uint16_t *>(src);
+          const uint32_t lo = i < experts ? bits[e] : none & 0xffffu;
+          x[r / 2] = lo | (i + L < experts ? (uint32_t)bits[e + L] << 16 : none & 0xffff0000u);
+        }
       }
     }
   }
-  // In pairs; -inf where there is no expert.
-  __device__ __forceinline__ void widen(uint32_t i0, uint32_t experts, Ch<2> (&x)[R / 2]) const {
+  __device__ __forceinline__ void widen(Ch<2> (&y)[R / 2]) const {
 #pragma unroll
-    for (int r = 0; r < R; r += kN) {
-      Ch<2> y[kN / 2];
-      widen_chunk<E>(v[r / kN], y);
-#pragma unroll
-      for (int q = 0; q < kN / 2; ++q) x[r / 2 + q] = y[q];
-      if (i0 + r + kN > experts) {  // the last experts: some, or none
-#pragma unroll
-        for (int q = 0; q < kN; ++q)
-          if (i0 + r + q >= experts) x[(r + q) / 2].v[(r + q) % 2] = kNegInf;
-      }
+    for (int r = 0; r < R / 2; ++r) {
+      if constexpr (sizeof(E) == 4) y[r] = {x[r].x, x[r].y};
+      else y[r] = widen_pair<E>(x[r]);
     }
   }
 };
-template <class E, int R>
-__device__ __forceinline__ void store_logits(E *dst, uint32_t i0, uint32_t experts, int wide,
+template <class E, int L, int R, bool kPairs>
+__device__ __forceinline__ void store_logits(E *dst, const Places<L, kPairs> &at, uint32_t experts,
                                              const Ch<2> (&d)[R / 2]) {
-  constexpr int kN = 16 / sizeof(E);
 #pragma unroll
-  for (int r = 0; r < R; r += kN) {
-    Ch<2> y[kN / 2];
-#pragma unroll
-    for (int q = 0; q < kN / 2; ++q) y[q] = d[r / 2 + q];
-    const uint4 v = narrow_chunk<E>(y);
-    if (wide == 16) {
-      if (i0 + r < experts) *reinterpret_cast<uint4 *>(dst + r) = v;
-    } else if (wide == 8) {
-      if (i0 + r < experts) *reinterpret_cast<uint2 *>(dst + r) = make_uint2(v.x, v.y);
-      if (i0 + r + kN / 2 < experts)
-        *reinterpret_cast<uint2 *>(dst + r + kN / 2) = make_uint2(v.z, v.w);
+  for (int r = 0; r < R; r += 2) {
+    const uint32_t e = at.after(r), i = at.first + e;
+    const Ch<2> &y = d[r / 2];
+    if constexpr (sizeof(E) == 4) {
+      if (i < experts) dst[e] = y.v[0];
+      if (i + L < experts) dst[e + L] = y.v[1];
     } else {
-      E x[kN];
-      *reinterpret_cast<uint4 *>(x) = v;
-#pragma unroll
-      for (int q = 0; q < kN; ++q)
-        if (i0 + r + q < experts) dst[r + q] = x[q];
+      const uint32_t v = narrow_pair<E>(y);
+      uint16_t *bits = reinterpret_cast<uint16_t *>(dst);
+      if constexpr (kPairs) {
+        if (i < experts) *reinterpret_cast<uint32_t *>(dst + e) = v;
+      } else {
+        if (i < experts) bits[e] = (uint16_t)v;
+        if (i + L < experts) bits[e + L] = (uint16_t)(v >> 16);
+      }
     }
   }
 }
 
-template <class E, int L, int R>
-__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) route_backward_kernel(const RouteParams p) {
+template <class E, int L, int R, bool kPairs>
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2)
+    route_backward_kernel(const RouteParams p) {
   constexpr int G = 32 / L, kExperts = L * R, kP = R / 2;
-  // the weights' part of a token's gradient, 0 but where it has one; four floats
-  // more a token keep the lanes' 16-byte reads off each other's banks
-  __shared__ __align__(16) float add[kWarps][G][kExperts + 4 * L];
+  // the weights' part of a token's gradient, 0 but where it has one
+  __shared__ __align__(16) float add[kWarps][G][kExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / L, gl = lane % L;
-  const uint32_t i0 = gl * R;
+  const Places<L, kPairs> mine(gl);
+  const uint32_t i0 = mine.first;
   float *my_add = add[warp][group];
-  auto place = [](uint32_t e) { return e + e / R * 4; };
   Ch<2> g[kP];
   const float coef = p.d_loss ? p.d_loss[0] * balance(p.E, p.k, p.tokens[0]) : 0.0f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    g[r / 2].v[r % 2] = p.d_loss && i0 + r < p.E ? coef * (float)p.counts[i0 + r] : 0.0f;
-    my_add[place(i0 + r)] = 0.0f;
+    const uint32_t e = i0 + mine.after(r);
+    g[r / 2].v[r % 2] = p.d_loss && e < p.E ? coef * (float)p.counts[e] : 0.0f;
+    my_add[e] = 0.0f;
   }
   __syncwarp();
   const uint32_t step = gridDim.x * kWarps * G;
@@ -660,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
   auto document = [&](uint64_t n) { return n < p.N ? (p.doc ? __ldg(p.doc + n) : 0) : -1; };
   bool next_real = document(n_first) >= 0;
   int ahead = document(n_first + step);
-  Piece<E, R> next;
-  if (next_real) next.load(src, i0, p.E, p.wide);
+  Piece<E, L, R, kPairs> next;
+  if (next_real) next.load(src, mine, p.E);
   // A lane has one of the token's choices at most, or goes through several.
   const bool one = p.k <= (uint32_t)L;
   int next_id = -1;  // -1: there is no such choice
@@ -678,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
     const uint64_t n = n0 + group;
     const bool in = n < p.N, real = next_real;
     Ch<2> x[kP];
-    next.widen(i0, p.E, x);
+    next.widen(x);
     if (!real) {
 #pragma unroll
       for (int r = 0; r < kP; ++r) x[r] = splat<2>(kNegInf);
@@ -690,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
     n0 += step, src += (int64_t)step * p.logits_row;
     next_real = ahead >= 0;
     ahead = document(n0 + group + step);
-    if (next_real) next.load(src, i0, p.E, p.wide);
+    if (next_real) next.load(src, mine, p.E);
     load_choice(n0 + group);
     const uint32_t at = real ? (uint32_t)n * p.k : 0;
     float t = id >= 0 ? w * dw : 0.0f;
@@ -721,12 +720,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
     const float inv = s == 0.0f ? 0.0f : rcp_sfu(s), mean = p.normalize ? t : 0.0f;
     if (p.d_weights) {
       if (one) {
-        if (id >= 0 && id < (int)p.E) my_add[place(id)] = w * (dw - mean);
+        if (id >= 0 && id < (int)p.E) my_add[id] = w * (dw - mean);
       } else if (real) {
         for (uint32_t j = gl; j < p.k; j += L) {
           const int e = p.ids[at + j];
           if (e >= 0 && e < (int)p.E)
-            my_add[place(e)] = p.weights[at + j] * (p.d_weights[at + j] - mean);
+            my_add[e] = p.weights[at + j] * (p.d_weights[at + j] - mean);
         }
       }
       __syncwarp();
@@ -734,25 +733,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2) r
     dot = fmaf(dot, inv, p.normalize ? 0.0f : t);
     const Ch<2> inv2 = splat<2>(inv), minus = splat<2>(-dot);
 #pragma unroll
-    for (int r = 0; r < kP; r += 2) {
-      const float4 v = *reinterpret_cast<const float4 *>(my_add + place(i0) + 2 * r);
-      x[r] = fma(x[r] * inv2, g[r] + minus, Ch<2>{v.x, v.y});
-      x[r + 1] = fma(x[r + 1] * inv2, g[r + 1] + minus, Ch<2>{v.z, v.w});
+    for (int r = 0; r < kP; ++r) {
+      const float *a = my_add + i0 + mine.after(2 * r);
+      const Ch<2> v = kPairs ? *reinterpret_cast<const Ch<2> *>(a) : Ch<2>{a[0], a[L]};
+      x[r] = fma(x[r] * inv2, g[r] + minus, v);
     }
     if (s == 0.0f) {  // the token counts for nothing
 #pragma unroll
       for (int r = 0; r < kP; ++r) x[r] = splat<2>(0.0f);
     }
-    if (in) store_logits<E, R>(dst, i0, p.E, p.wide, x);
+    if (in) store_logits<E, L, R, kPairs>(dst, mine, p.E, x);
     dst += (int64_t)step * p.E;
     if (p.d_weights) {
       __syncwarp();
       if (one) {
-        if (id >= 0 && id < (int)p.E) my_add[place(id)] = 0.0f;
+        if (id >= 0 && id < (int)p.E) my_add[id] = 0.0f;
       } else if (real) {
         for (uint32_t j = gl; j < p.k; j += L) {
           const int e = p.ids[at + j];
-          if (e >= 0 && e < (int)p.E) my_add[place(e)] = 0.0f;
+          if (e >= 0 && e < (int)p.E) my_add[e] = 0.0f;
         }
       }
       __syncwarp();
@@ -820,8 +819,10 @@ cudaError_t launch_backward(RouteParams &p, cudaStream_t st) {
   constexpr uint32_t kTokens = kWarps * (32 / L);  // a block takes at once
   const uint32_t blocks = (uint32_t)(((uint64_t)p.N + kTokens - 1) / kTokens);
   ++launch_counter();
-  route_backward_kernel<E, L, R>
-      <<<blocks < 8 * kSMs ? blocks : 8 * kSMs, kThreads, 0, st>>>(p);
+  constexpr bool kNarrow = sizeof(E) == 2;
+  auto *k = kNarrow && p.wide ? route_backward_kernel<E, L, R, kNarrow>
+                              : route_backward_kernel<E, L, R, false>;
+  k<<<blocks < 8 * kSMs ? blocks : 8 * kSMs, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
