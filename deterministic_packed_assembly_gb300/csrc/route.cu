@@ -631,7 +631,7 @@ __device__ __forceinline__ void store_logits(E *dst, const Places<L, kPairs> &at
   }
 }
 
-template <class E, int L, int R, bool kPairs>
+template <class E, int L, int R, bool kPairs, bool kNormalize>
 __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2)
     route_backward_kernel(const RouteParams p) {
   constexpr int G = 32 / L, kExperts = L * R, kP = R / 2;
@@ -692,11 +692,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2)
     if (next_real) next.load(src, mine, p.E);
     load_choice(n0 + group);
     const uint32_t at = real ? (uint32_t)n * p.k : 0;
-    float t = id >= 0 ? w * dw : 0.0f;
-    if (p.d_weights && real && !one) {
-      for (uint32_t j = gl; j < p.k; j += L)
-        if (p.ids[at + j] >= 0) t += p.weights[at + j] * p.d_weights[at + j];
-    }
     float m = kNegInf;
 #pragma unroll
     for (int r = 0; r < kP; ++r) m = fmaxf(m, fmaxf(x[r].v[0], x[r].v[1]));
@@ -710,6 +705,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2)
       s2 = s2 + x[r];
       dot2 = fma(x[r], g[r], dot2);
     }
+    // Normalised weights' gradient is the same for dw plus a constant: taken from the
+    // first choice's, of the largest weight, dw_j - t loses nothing where they are alike.
+    float from = 0.0f;
+    if constexpr (kNormalize) from = __shfl_sync(0xffffffffu, dw, group * L);
+    float t = id >= 0 ? w * (dw - from) : 0.0f;
+    if (p.d_weights && real && !one) {
+      if (kNormalize) from = p.d_weights[at];
+      for (uint32_t j = gl; j < p.k; j += L)
+        if (p.ids[at + j] >= 0) t += p.weights[at + j] * (p.d_weights[at + j] - from);
+    }
     float s = s2.v[0] + s2.v[1], dot = dot2.v[0] + dot2.v[1];
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) {
@@ -717,20 +722,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2)
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
       t += __shfl_xor_sync(0xffffffffu, t, o);
     }
-    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s), mean = p.normalize ? t : 0.0f;
+    const float inv = s == 0.0f ? 0.0f : rcp_sfu(s), mean = kNormalize ? t : 0.0f;
     if (p.d_weights) {
       if (one) {
-        if (id >= 0 && id < (int)p.E) my_add[id] = w * (dw - mean);
+        if (id >= 0 && id < (int)p.E) my_add[id] = w * ((dw - from) - mean);
       } else if (real) {
         for (uint32_t j = gl; j < p.k; j += L) {
           const int e = p.ids[at + j];
           if (e >= 0 && e < (int)p.E)
-            my_add[e] = p.weights[at + j] * (p.d_weights[at + j] - mean);
+            my_add[e] = p.weights[at + j] * ((p.d_weights[at + j] - from) - mean);
         }
       }
       __syncwarp();
     }
-    dot = fmaf(dot, inv, p.normalize ? 0.0f : t);
+    dot = fmaf(dot, inv, kNormalize ? 0.0f : t);
     const Ch<2> inv2 = splat<2>(inv), minus = splat<2>(-dot);
 #pragma unroll
     for (int r = 0; r < kP; ++r) {
@@ -820,8 +825,11 @@ cudaError_t launch_backward(RouteParams &p, cudaStream_t st) {
   const uint32_t blocks = (uint32_t)(((uint64_t)p.N + kTokens - 1) / kTokens);
   ++launch_counter();
   constexpr bool kNarrow = sizeof(E) == 2;
-  auto *k = kNarrow && p.wide ? route_backward_kernel<E, L, R, kNarrow>
-                              : route_backward_kernel<E, L, R, false>;
+  const bool pairs = kNarrow && p.wide;
+  auto *k = p.normalize ? pairs ? route_backward_kernel<E, L, R, kNarrow, true>
+                                : route_backward_kernel<E, L, R, false, true>
+            : pairs     ? route_backward_kernel<E, L, R, kNarrow, false>
+                        : route_backward_kernel<E, L, R, false, false>;
   k<<<blocks < 8 * kSMs ? blocks : 8 * kSMs, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }

@@ -325,6 +325,19 @@ def test_route_tokens_do_not_depend_on_the_other_tokens(nsp):
                                nsp.route_backward(x, many, dw)[:n])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_route_16_bit_tokens_do_not_depend_on_the_other_tokens(nsp, dtype):
+    for E, k in ((61, 2), (250, 3), (1000, 8)):
+        x = torch.randn(30_000, E, generator=gen(E)).to(DTYPES[dtype]).cuda()
+        dw = torch.randn(30_000, k, generator=gen(k)).cuda()
+        many = nsp.route(x, k)
+        for n in (1, 77, 2000):
+            few = nsp.route(x[:n], k)
+            assert torch.equal(few.ids, many.ids[:n]) and torch.equal(few.weights, many.weights[:n])
+            assert torch.equal(nsp.route_backward(x[:n], few, dw[:n]),
+                               nsp.route_backward(x, many, dw)[:n])
+
+
 def test_scan_offsets_past_32_bits(nsp):
     B, T, D = 3, 360_001, 2048  # 2.2e9 elements
     g = torch.Generator(device="cuda")
@@ -706,6 +719,24 @@ def test_route_many_tokens(nsp, N, E, dtype):
     logits = (torch.randn(N, E, generator=g) + torch.randn(1, E, generator=g)).to(DTYPES[dtype])
     doc = (torch.rand(N, generator=g) < 0.9).int() - 1
     check_route(nsp, logits, min(E, 4), doc, True, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,E,k", [(11_003, 251, 8), (11_003, 250, 2), (10_001, 256, 8), (5_001, 514, 3)])
+def test_route_many_tokens_of_many_experts(nsp, N, E, k, dtype):
+    # masked experts, rows without any, rows of the lowest value, padding that holds anything
+    g = gen(E + k)
+    logits = torch.randn(N, E, generator=g).to(DTYPES[dtype])
+    logits[torch.rand(N, E, generator=g) < 0.2] = -INF
+    logits[::97] = -INF
+    logits[5::97] = torch.finfo(DTYPES[dtype]).min
+    doc = (torch.rand(N, generator=g) < 0.9).int() - 1
+    check_route(nsp, logits, k, doc, True, dtype)
+    bad = logits.clone()
+    bad[doc < 0] = NAN
+    a, b = nsp.route(logits.cuda(), k, doc=doc.cuda()), nsp.route(bad.cuda(), k, doc=doc.cuda())
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
