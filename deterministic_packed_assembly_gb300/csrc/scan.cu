@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
 // ---- backward -------------------------------------------------------------------
 // The backward pass walks the tiles from the last one, and a warp's segments
 // with them: warp w takes the segment that is w-th from the tile's end.
-//   d_t = dy_t + u_t,  u_{t-1} = a_t d_t  (0 where a sequence starts)
+//   d_t = dy_t + u_t,  u_{t-1} = a_t d_t  (0 where a sequence starts: in the product's
+//   place, which is a NaN where the gate is one)
 // is a run in the other direction with the same A, exchanged as in the forward
 // pass.  The states inside a quad are run again from the saved one before it,
 // by the segments' forward runs, which are exchanged too.
@@ -873,9 +874,9 @@ __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
       const Ch<CH> g = pick((skip >> s) & 1u, zero, at.read(in, 2, s, lane));
-      d = pick((start >> s) & 1u, zero, s == kSteps - 1 ? g : fma(a[s + 1], d, g));
+      d = s == kSteps - 1 ? g : pick((start >> (s + 1)) & 1u, g, fma(a[s + 1], d, g));
     }
-    run.H = a[0] * d;
+    run.H = pick(start & 1u, zero, a[0] * d);
   }
   return run;
 }
@@ -934,9 +935,8 @@ __device__ __forceinline__ void backward_apply(const ScanParams &p, const Stage<
     for (int s = kSteps - 1; s >= 0; --s, dz -= p.D, df -= p.D) {
       const bool gone = (skip >> s) & 1u;
       const Ch<CH> g = pick(gone, zero, at.read(in, 2, s, lane));
-      const Ch<CH> d = s == kSteps - 1 ? g + u : fma(a[s + 1], u, g);
-      const Ch<CH> vf = pick(gone, zero, q[s] * d);
-      u = pick((start >> s) & 1u, zero, d);
+      u = s == kSteps - 1 ? g + u : pick((start >> (s + 1)) & 1u, g, fma(a[s + 1], u, g));
+      const Ch<CH> d = u, vf = pick(gone, zero, q[s] * d);
       sum = sum + vf;
       if (live && s < left) {
         *reinterpret_cast<Raw<E, CH> *>(dz) = narrow<E, CH>(pick(gone, zero, c[s] * d));
@@ -1153,13 +1153,12 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
     Ch<CH> ui = u;
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
-      const bool have = s < row.n, start = (row.start >> s) & 1u;
+      const bool have = s < row.n, after_start = s < kSteps - 1 && (row.start >> (s + 1)) & 1u;
       const bool gone = !have || ((row.skip >> s) & 1u);
       const Ch<CH> gs = gone ? zero : widen<E, CH>(g[s]);
-      const Ch<CH> d = s == kSteps - 1 ? gs + ui : fma(a[s + 1], ui, gs);
-      const Ch<CH> vf = pick(gone, zero, q[s] * d);
-      ui = pick(start, zero, d);
-      run.H = pick(start, zero, s == kSteps - 1 ? gs : fma(a[s + 1], run.H, gs));
+      ui = s == kSteps - 1 ? gs + ui : pick(after_start, gs, fma(a[s + 1], ui, gs));
+      const Ch<CH> d = ui, vf = pick(gone, zero, q[s] * d);
+      run.H = s == kSteps - 1 ? gs : pick(after_start, gs, fma(a[s + 1], run.H, gs));
       sum = sum + vf;
       if (have) {
         *reinterpret_cast<Raw<E, CH> *>(dz + (int64_t)s * p.D) =
@@ -1167,7 +1166,7 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
         *reinterpret_cast<Raw<E, CH> *>(df + (int64_t)s * p.D) = narrow<E, CH>(vf);
       }
     }
-    run.H = a[0] * run.H;
+    run.H = pick(row.start & 1u, zero, a[0] * run.H);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) run.A = run.A * a[s];
     u = after(run, row.start != 0, u);

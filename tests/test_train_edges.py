@@ -1,0 +1,67 @@
+"""The training operators at the edges of their definitions: a NaN gate where a
+document starts, gates near 0 and near 1, logits of a type's lowest value, a NaN
+teacher, forward-mode derivatives, states written over their input, sums of many
+rows.  The references are those of test_train_operators, in 64 bits on the host.
+
+Tolerances, with u = 2**-24, are derived at each test.
+"""
+import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
+
+from test_train_operators import (  # noqa: F401
+    DTYPES, INF, NAN, ROUND, close, dev, distill_inputs, distill_reference, gen, nsp, refused,
+    run_distill, scan_inputs, scan_reference)
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0**-24
+
+
+# ---- a document's NaN gate stays in the document --------------------------------
+def starts_of(B, T):
+    """Steps at which each row's second document starts: the first one, the middle, a
+    segment of eight's edge, its last step, a tile of 64's edge, the last step."""
+    at = [0, T // 2, T // 16 * 8, T // 16 * 8 + 7, T // 128 * 64, T - 1]
+    return [min(at[b % len(at)], T - 1) for b in range(B)]
+
+
+def check_nan_gates(nsp, B, T, D, dtype, shift=0):
+    host, cuda, dy, dh = scan_inputs(B, T, D, dtype, B + T + D, packed=False, shift=shift)
+    pos = torch.arange(1, T + 1).expand(B, T).clone().int()
+    channels = [0, D // 2, D - 1]
+    for b, s in enumerate(starts_of(B, T)):
+        pos[b, s] = 0
+        for k, c in enumerate(channels):
+            host["f"][b, s, c] = (NAN, INF, NAN)[k]
+    doc = torch.zeros(B, T, dtype=torch.int32)
+    doc[:, T // 3] = -1  # padding between (where it is the start, the row has one document)
+    host.update(pos=pos, doc=doc)
+    cuda["f"].copy_(host["f"])
+    want = scan_reference(**host, dy=dy, dh=dh)
+    kw = dict(pos=pos.cuda(), doc=doc.cuda())
+    bias, h0 = dev(host["bias"]), dev(host["h0"])
+    y, h, states = nsp.gated_scan_forward(cuda["z"], cuda["f"], bias, h0=h0, **kw)
+    got = nsp.gated_scan_backward(cuda["dy"], dev(dh), cuda["z"], cuda["f"], bias, states, **kw)
+    for g, name in zip((y, h, *got), ("y", "h_last", "dz", "df", "dbias", "dh0")):
+        floor = float(dy.double().abs().max()) if name in ("dbias", "dh0") else 0.0
+        close(g, want[name], 2e-5, name, 0.0 if name in ("h_last", "dbias", "dh0") else ROUND[dtype],
+              floor)
+    # the documents before are what they are without the NaN
+    assert not torch.isnan(want["dh0"]).any()
+    for b, s in enumerate(starts_of(B, T)):
+        assert not torch.isnan(got[0][b, :s]).any() and not torch.isnan(got[1][b, :s]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [2, 7, 8, 9, 16, 31, 32, 33, 63, 64, 65, 130, 517, 1200])
+def test_scan_nan_gate_where_a_document_starts(nsp, T, dtype):
+    """With test_train_operators' tolerances: beside the NaN these are its inputs."""
+    check_nan_gates(nsp, 6, T, 34, dtype)
+    check_nan_gates(nsp, 6, T, 33, dtype, shift=1)
+
+
+@pytest.mark.parametrize("T", [32, 100])
+def test_scan_nan_gate_in_many_rows(nsp, T):
+    # rows of a thread alone, and rows of a block alone
+    check_nan_gates(nsp, 306, T, 130, "bf16")
