@@ -152,6 +152,7 @@ static bool check_route(const ns_route_inputs *in) {
 }
 
 uint64_t ns_route_workspace(uint32_t N, uint32_t E) {
+  if (E > NS_ROUTE_MAX_EXPERTS) return 0;  // the layout is not made for them
   return nsk::route_blocks(N, E) * (8ull * E + 4);
 }
 

@@ -169,7 +169,8 @@ typedef struct {
   int32_t normalize;
 } ns_route_inputs;
 
-/* Bytes of the workspace of ns_route_forward for these sizes (0: none). */
+/* Bytes of the workspace of ns_route_forward for these sizes (0: none, or sizes that it
+ * refuses). */
 uint64_t ns_route_workspace(uint32_t N, uint32_t E);
 
 /* workspace: ns_route_workspace bytes, 4-byte aligned, or NULL for none.  Errors: INVALID_ARG (a
