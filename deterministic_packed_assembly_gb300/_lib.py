@@ -105,7 +105,27 @@ class ns_pack_info_t(C.Structure):
     ]
 
 
-class ns_scan_inputs(C.Structure):
+def _fits(name: str, v: int) -> None:
+    """Refuse a size that is not one of 32 bits: ctypes would pass what is left of it."""
+    if v >> 32:
+        raise NsPackError(NS_ERR_INVALID_ARG, f"{name}: {v}, expected 0 to 2**32 - 1")
+
+
+class _Sized(C.Structure):
+    """A structure with sizes of 32 bits, checked where all its fields are given in order."""
+
+    def __init_subclass__(cls):
+        super().__init_subclass__()
+        cls._sizes = [(i, f[0]) for i, f in enumerate(cls._fields_) if f[1] is C.c_uint32]
+
+    def __init__(self, *args):
+        if args:
+            for i, name in self._sizes:
+                _fits(name, args[i])
+        super().__init__(*args)
+
+
+class ns_scan_inputs(_Sized):
     _fields_ = [
         ("z", C.c_void_p),
         ("f", C.c_void_p),
@@ -123,7 +143,7 @@ class ns_scan_inputs(C.Structure):
     ]
 
 
-class ns_distill_inputs(C.Structure):
+class ns_distill_inputs(_Sized):
     _fields_ = [
         ("logits", C.c_void_p),
         ("logits_row", C.c_int64),
@@ -142,7 +162,7 @@ class ns_distill_inputs(C.Structure):
     ]
 
 
-class ns_route_inputs(C.Structure):
+class ns_route_inputs(_Sized):
     _fields_ = [
         ("logits", C.c_void_p),
         ("logits_row", C.c_int64),
@@ -325,6 +345,7 @@ def ns_scan_forward(inputs: ns_scan_inputs, h0, y, h_last, states, stream) -> No
 
 
 def ns_scan_workspace(B: int, T: int, D: int) -> int:
+    _fits("B", B), _fits("T", T), _fits("D", D)
     return lib.ns_scan_workspace(B, T, D)
 
 
@@ -339,6 +360,7 @@ def ns_distill(inputs: ns_distill_inputs, loss, dlogits, dlogits_row: int, strea
 
 
 def ns_route_workspace(N: int, E: int) -> int:
+    _fits("N", N), _fits("E", E)
     return lib.ns_route_workspace(N, E)
 
 

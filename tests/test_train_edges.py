@@ -65,3 +65,16 @@ def test_scan_nan_gate_where_a_document_starts(nsp, T, dtype):
 def test_scan_nan_gate_in_many_rows(nsp, T):
     # rows of a thread alone, and rows of a block alone
     check_nan_gates(nsp, 306, T, 130, "bf16")
+
+
+# ---- sizes past 32 bits -----------------------------------------------------------------------
+def test_sizes_past_32_bits_are_refused(nsp):
+    """Four more than 2**32: not four."""
+    n = 2**32 + 4
+    z = torch.zeros(1, 1, 1, dtype=torch.bfloat16, device="cuda").expand(1, n, 1)
+    refused(nsp, lambda: nsp.gated_scan(z, z))
+    x = torch.empty(n, 1, dtype=torch.bfloat16, device="cuda")
+    refused(nsp, lambda: nsp.route(x, 1))
+    top = torch.empty(n, 1, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    refused(nsp, lambda: nsp.distill_loss(x, top, ids))

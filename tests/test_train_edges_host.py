@@ -17,3 +17,30 @@ def test_route_workspace_up_to_the_most_experts(nsp):
     for E in (1, 8, 100, 512, 513, 1024):
         assert nsp.ns_route_workspace(1 << 20, E) % (8 * E + 4) == 0
         assert nsp.ns_route_workspace(1 << 20, E) > 0
+
+
+# ---- sizes that 32 bits do not hold ---------------------------------------------------
+@pytest.mark.parametrize("size", [2**32, 2**32 + 4, 2**40, 2**63, -1])
+def test_sizes_past_32_bits_are_refused(nsp, size):
+    """What is left of them in 32 bits is another size, 4 for 2**32 + 4."""
+    L = nsp._lib
+    scan = [None, None, 0, 0, 0, 0, None, None, None, 1, 1, 1, 0]
+    distill = [None, 1, None, None, None, None, None, 1, 1, 1, 0, 0, 0, 1.0]
+    route = [None, 1, None, 1, 1, 1, 0, 0]
+    calls = [lambda: nsp.ns_scan_workspace(size, 1, 1), lambda: nsp.ns_scan_workspace(1, size, 1),
+             lambda: nsp.ns_scan_workspace(1, 1, size), lambda: nsp.ns_route_workspace(size, 1),
+             lambda: nsp.ns_route_workspace(1, size)]
+    for make, good, first in ((L.ns_scan_inputs, scan, 9), (L.ns_distill_inputs, distill, 7),
+                              (L.ns_route_inputs, route, 3)):
+        made = make(*good)
+        for i in range(first, first + 3):
+            assert getattr(made, make._fields_[i][0]) == 1
+            bad = list(good)
+            bad[i] = size
+            calls.append(lambda make=make, bad=bad: make(*bad))
+            last = make(*good[:i], 2**32 - 1, *good[i + 1:])
+            assert getattr(last, make._fields_[i][0]) == 2**32 - 1
+    for call in calls:
+        with pytest.raises(nsp.NsPackError) as e:
+            call()
+        assert e.value.code == nsp.NS_ERR_INVALID_ARG
