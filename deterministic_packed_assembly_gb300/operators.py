@@ -5,7 +5,7 @@
 ``distill_loss`` compares the model's logits with a teacher's.  They take the
 packed batch's position ids (0 starts a document), document ids (below 0 is
 padding) and loss mask as ``Packer.step`` writes them.  Each has a form that
-PyTorch differentiates and the explicit passes behind it.  The work is queued on
+PyTorch differentiates, in reverse mode, and the explicit passes behind it.  The work is queued on
 the current stream of the inputs' device; outputs and workspaces come from
 PyTorch's caching allocator there.  All sums run in a fixed order: the same
 inputs give the same bits.
@@ -15,6 +15,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib as L
@@ -71,6 +72,16 @@ def _wants_grad(*tensors) -> bool:
             if isinstance(t, torch.Tensor) and t.requires_grad:
                 return True
     return False
+
+
+def _reverse_only(*tensors) -> None:
+    """Forward-mode derivatives are not there: an error, where outputs without a tangent
+    would be a derivative of 0."""
+    if forward_ad._current_level < 0:  # no dual level: 1 us a call saved
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("the operators have no forward-mode derivative")
 
 
 # ---- gated linear recurrence ---------------------------------------------------
@@ -167,6 +178,7 @@ class _GatedScan(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh_last):
+        _reverse_only(dy, dh_last)
         z, f, bias, pos, doc, states = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros(z.shape, dtype=z.dtype, device=z.device)
@@ -196,6 +208,7 @@ def gated_scan(z: torch.Tensor, f: torch.Tensor, bias: Optional[torch.Tensor] = 
     [D], ``h0`` and ``h_last`` [B, D] are float32, ``pos`` and ``doc`` [B, T]
     int32.  PyTorch differentiates it with respect to z, f, bias and h0.
     """
+    _reverse_only(z, f, bias, h0)
     if _wants_grad(z, f, bias, h0):
         return _GatedScan.apply(z, f, bias, h0, pos, doc)
     return _scan(z, f, bias, pos, doc, h0, False)[:2]
@@ -271,6 +284,7 @@ class _DistillLoss(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, d_loss):
+        _reverse_only(d_loss)
         logits, top_logits, top_ids, mask, teacher_lse = ctx.saved_tensors
         _, dlogits = _distill(logits, top_logits, top_ids, mask, ctx.temperature, teacher_lse,
                               d_loss.contiguous(), None, True)
@@ -293,6 +307,7 @@ def distill_loss(logits: torch.Tensor, top_logits: torch.Tensor, top_ids: torch.
     ``top_ids`` int32 or int64.  PyTorch differentiates it with respect to
     ``logits`` (reading them a second time; ``distill_grad`` needs only one pass).
     """
+    _reverse_only(logits, top_logits, teacher_lse)
     if _wants_grad(logits):
         return _DistillLoss.apply(logits, top_logits, top_ids, mask, temperature, teacher_lse)
     return _distill(logits, top_logits, top_ids, mask, temperature, teacher_lse, None, None,
@@ -391,6 +406,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, _ids, d_weights, _counts, _tokens, d_loss):
+        _reverse_only(d_weights, d_loss)
         logits, doc, *r = ctx.saved_tensors
         if d_weights is not None:
             d_weights = d_weights.contiguous()
@@ -413,6 +429,7 @@ def route(logits: torch.Tensor, k: int, *, doc: Optional[torch.Tensor] = None,
 
     PyTorch differentiates ``weights`` and ``loss`` with respect to ``logits``.
     """
+    _reverse_only(logits)
     if _wants_grad(logits):
         return Routing(*_Route.apply(logits, k, doc, normalize))
     return _route(logits, k, doc, normalize)

@@ -67,6 +67,35 @@ def test_scan_nan_gate_in_many_rows(nsp, T):
     check_nan_gates(nsp, 306, T, 130, "bf16")
 
 
+# ---- forward-mode derivatives --------------------------------------------------------------
+def test_forward_mode_derivatives_are_refused(nsp):
+    """They are not there: an error, not outputs without a tangent."""
+    z = torch.randn(2, 5, 8).cuda()
+    x = torch.randn(6, 40).cuda()
+    top, ids = x.topk(3, 1)
+    h0, bias, lse = torch.zeros(2, 8).cuda(), torch.zeros(8).cuda(), torch.zeros(6).cuda() + 9
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+        for call in (
+                lambda: nsp.gated_scan(dual(z), z), lambda: nsp.gated_scan(z, dual(z)),
+                lambda: nsp.gated_scan(z, z, dual(bias)), lambda: nsp.gated_scan(z, z, h0=dual(h0)),
+                lambda: nsp.distill_loss(dual(x), top, ids),
+                lambda: nsp.distill_loss(x, dual(top), ids),
+                lambda: nsp.distill_loss(x, top, ids, teacher_lse=dual(lse)),
+                lambda: nsp.route(dual(x), 4)):
+            for grad in (True, False):
+                with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError):
+                    call()
+        assert nsp.gated_scan(z, z)[0].shape == z.shape  # others of the level go on
+        # the gradients of an output that are duals themselves
+        zr, xr = z.clone().requires_grad_(), x.clone().requires_grad_()
+        for y, at in ((nsp.gated_scan(zr, z)[0], zr), (nsp.distill_loss(xr, top, ids), xr),
+                      (nsp.route(xr, 4).weights, xr)):
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(y, at, dual(torch.ones_like(y)))
+
+
 # ---- sizes past 32 bits -----------------------------------------------------------------------
 def test_sizes_past_32_bits_are_refused(nsp):
     """Four more than 2**32: not four."""

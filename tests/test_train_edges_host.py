@@ -44,3 +44,23 @@ def test_sizes_past_32_bits_are_refused(nsp, size):
         with pytest.raises(nsp.NsPackError) as e:
             call()
         assert e.value.code == nsp.NS_ERR_INVALID_ARG
+
+
+# ---- forward-mode derivatives -----------------------------------------------------------
+def test_forward_mode_derivatives_are_refused(nsp):
+    """They are refused before anything else is looked at (host tensors here)."""
+    import torch
+    import torch.autograd.forward_ad as forward_ad
+    z, x = torch.randn(2, 5, 8), torch.randn(6, 40)
+    top, ids = x.topk(3, 1)
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+        for call in (lambda: nsp.gated_scan(dual(z), z), lambda: nsp.gated_scan(z, dual(z)),
+                     lambda: nsp.gated_scan(z, z, h0=dual(z[:, 0])),
+                     lambda: nsp.distill_loss(dual(x), top, ids),
+                     lambda: nsp.distill_loss(x, dual(top), ids), lambda: nsp.route(dual(x), 4)):
+            with pytest.raises(NotImplementedError):
+                call()
+        with pytest.raises(nsp.NsPackError):  # no tangent: the device is what is wrong
+            nsp.gated_scan(z, z)
