@@ -237,7 +237,10 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p,
     for (int i = 0; i < kBatch; ++i)
       if (mine >> i & 1) e.x[k0 + 32 * i] = to_f32(x[i]);
   }
-  r.c = to_f32(at_top);
+  // The exchange waits for the value itself: its logit may be in another block's slice,
+  // which writes the gradient there, perhaps over the logits, as soon as this block has
+  // sent its sums, and no store waits for a load whose value nothing has used.
+  r.c = __shfl_sync(0xffffffffu, to_f32(at_top), 0);
   if (r.c == kNegInf) r.c = 0.0f;
   const float base_m = base_of(m);
   float sum = 0.0f;
