@@ -739,6 +739,10 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 2 : kForwardBlocks)
     y += p.out_step;
   }
   copy_wait<0>();
+  if (p.h_last == p.h0) {  // the other blocks have taken their h0 into the states by here
+    cluster_arrive();
+    cluster_wait();
+  }
   if (at.rank == 0 && warp == 0)
     store_channels<CH>(p.h_last, (int64_t)at.b * p.D + at.c0, at.live, h);
   pdl_wait();  // what waits for this launch also waits for the one before

@@ -107,3 +107,20 @@ def test_sizes_past_32_bits_are_refused(nsp):
     top = torch.empty(n, 1, dtype=torch.bfloat16, device="cuda")
     ids = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
     refused(nsp, lambda: nsp.distill_loss(x, top, ids))
+
+
+# ---- states over their input --------------------------------------------------------------------
+@pytest.mark.parametrize("T", [60, 100, 129, 200, 300, 400, 500, 512, 513, 2000])
+def test_scan_last_states_over_the_first(nsp, T):
+    # h_last may be h0: in clusters of every size, of one round and of several
+    host, cuda, _, _ = scan_inputs(2, T, 96, "f32", T, packed=False)
+    h0, bias = dev(host["h0"]), dev(host["bias"])
+    want = nsp.gated_scan(cuda["z"], cuda["f"], bias, h0=h0)
+    for _ in range(5):
+        h, y = h0.clone(), torch.empty_like(want[0])
+        inputs = nsp._lib.ns_scan_inputs(
+            cuda["z"].data_ptr(), cuda["f"].data_ptr(), T * 96, 96, T * 96, 96, bias.data_ptr(), None,
+            None, 2, T, 96, nsp.NS_F32)
+        nsp.ns_scan_forward(inputs, h.data_ptr(), y.data_ptr(), h.data_ptr(), None,
+                            torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1])
