@@ -14,14 +14,16 @@
 // beside the stores of the one before.  The teacher's K entries are few: two
 // warps of their own in each block have them, of even and of odd rows, ahead of the
 // rows' warps: what they do for a row is a chain of loads that takes as long as one or
-// two rows, so that each loads its next row's entries while statistics are exchanged.  With c the student's logit at the
-// teacher's first choice, M and S the row's maximum and sum,
-//   sum_k p_k (log p_k - log q_k) = sum_k p_k (log p_k - (s_k - c) / temp)
-//                                   + m (log S + (M - c) / temp),
-// whose first sum each block takes over the ids in its slice, without the row's
-// statistics, so that one exchange is enough; its terms are small, as the
-// teacher's choices are near c.  After the gradient is written their warp writes the
-// entries' own over it.
+// two rows, so that each loads its next row's entries while statistics are exchanged.
+// With c the student's logit at the teacher's first choice, M and S the row's maximum
+// and sum,
+//   temp sum_k p_k (log p_k - log q_k) = sum_k p_k (temp log p_k - (s_k - c))
+//                                        + m (temp log S + (M - c)),
+// (not divided by temp: a choice whose logit is near the type's lowest value has a large
+// loss, not an infinity less another).  The first sum each block takes over the ids in
+// its slice, without the row's statistics, so that one exchange is enough; its terms are
+// small, as the teacher's choices are near c.  After the gradient is written their warp
+// writes the entries' own over it.
 //
 // Logits are kept as they came.  An exponential is 2^((s - max) log2 e / temp):
 // the difference is taken first, so that it is exact where it matters, near the
@@ -198,7 +200,7 @@ __device__ __forceinline__ Teacher load_teacher(const DistillParams &p, uint32_t
 struct EntrySums {
   float mass;  // sum of p over the row: 1 unless the teacher's own normaliser is given
   float c;     // the student's logit at the teacher's first choice
-  float part;  // sum of p (log p - (s - c) / temp) over the slice
+  float part;  // sum of p (temp log p - (s - c)) over the slice
 };
 template <class E>
 __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p,
@@ -270,7 +272,7 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p,
     const float pk = e.p[k] * inv, x = e.x[k];
     e.p[k] = pk;
     if (pk != 0.0f)
-      r.part += pk * (x == kNegInf ? -kNegInf : fmaf(r.c - x, p.inv_temp, e.logp[k] - log_sum));
+      r.part += pk * (x == kNegInf ? -kNegInf : fmaf(p.temp, e.logp[k] - log_sum, r.c - x));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r.part += __shfl_xor_sync(0xffffffffu, r.part, o);
@@ -471,10 +473,10 @@ __device__ __forceinline__ void entry_warp(const DistillParams &p, Shared &sh, f
     if (next < p.N) teacher = load_teacher(p, next, lane, next_id, e.logp);
     const RowStats r = row_stats(p, sh, i, C, lost);
     if (rank == 0 && lane == 0) {
-      float loss = r.parts + r.mass * fmaf(base_of(r.all.m) - sums.c, p.inv_temp, logf(r.all.s));
+      float loss = r.parts + r.mass * fmaf(p.temp, logf(r.all.s), base_of(r.all.m) - sums.c);
       // a student without any logit above -inf gives the teacher's entries probability 0
       if (r.all.s == 0.0f) loss = -kNegInf;
-      p.loss[row] = r.mass == 0.0f ? 0.0f : loss * p.temp * p.temp;
+      p.loss[row] = r.mass == 0.0f ? 0.0f : loss * p.temp;
     }
     if (kGrad) {
       const float w = weight * p.temp;

@@ -67,6 +67,29 @@ def test_scan_nan_gate_in_many_rows(nsp, T):
     check_nan_gates(nsp, 306, T, 130, "bf16")
 
 
+# ---- distillation ----------------------------------------------------------------------
+@pytest.mark.parametrize("temp", [0.25, 0.5, 1.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [300, 90_000])
+def test_distill_teacher_chooses_a_masked_token(nsp, V, dtype, temp):
+    """Logits of the type's lowest value at the teacher's choices: the loss is large, not a
+    NaN.  It is a sum of terms of that size, of which each is rounded a few times: 2e-5 as
+    elsewhere."""
+    c = distill_inputs(4, V, 6, dtype, 5, temp=temp)
+    low = torch.finfo(DTYPES[dtype]).min
+    c["logits"][0, c["ids"][0, 0].long()] = low
+    c["logits"][1, c["ids"][1, 3].long()] = low
+    c["logits"][2, c["ids"][2].long()] = low
+    c["top"][0, 0] += 1.0  # the first choice has most of the probability
+    want_loss, want_g = distill_reference(**c)
+    assert torch.isfinite(want_loss).all() and (want_loss[[0, 2]] > 1e35).all()
+    loss, g = run_distill(nsp, c)
+    assert ((loss.double().cpu() - want_loss).abs() <= 2e-5 * (1 + want_loss.abs())).all()
+    assert torch.isfinite(g).all()
+    scale = temp * c["weight"].double().abs()[:, None]
+    assert ((g.double().cpu() - want_g).abs() <= 4e-5 * scale + ROUND[dtype] * 1.01 * want_g.abs()).all()
+
+
 # ---- forward-mode derivatives --------------------------------------------------------------
 def test_forward_mode_derivatives_are_refused(nsp):
     """They are not there: an error, not outputs without a tangent."""
