@@ -261,7 +261,8 @@ __device__ __forceinline__ EntrySums teacher_entries(const DistillParams &p,
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   float inv = 1.0f, log_sum = 0.0f;
   r.mass = sum;
-  if (!p.teacher_lse && sum != 0.0f) inv = 1.0f / sum, log_sum = logf(sum), r.mass = 1.0f;
+  if (!p.teacher_lse && sum != 0.0f)
+    inv = 1.0f / sum, log_sum = logf(sum), r.mass = sum == sum ? 1.0f : sum;  // or a NaN
 #pragma unroll 2
   for (uint32_t k = lane; k < p.K; k += 32) {
     const int id = e.id[k];

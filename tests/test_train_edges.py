@@ -90,6 +90,22 @@ def test_distill_teacher_chooses_a_masked_token(nsp, V, dtype, temp):
     assert ((g.double().cpu() - want_g).abs() <= 4e-5 * scale + ROUND[dtype] * 1.01 * want_g.abs()).all()
 
 
+# ---- a NaN teacher
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V", [300, 90_000])
+def test_distill_nan_teacher_makes_its_row_nan(nsp, V, tail):
+    # m = sum p is a NaN, and m q with it at every place of the row
+    c = distill_inputs(4, V, 6, "f32", 6, tail)
+    want = run_distill(nsp, c)
+    for at in (0, 4):
+        d = dict(c, top=c["top"].clone())
+        d["top"][2, at] = NAN
+        loss, g = run_distill(nsp, d)
+        assert torch.isnan(loss[2]) and torch.isnan(g[2]).all()
+        for r in (0, 1, 3):
+            assert torch.equal(loss[r], want[0][r]) and torch.equal(g[r], want[1][r])
+
+
 # ---- forward-mode derivatives --------------------------------------------------------------
 def test_forward_mode_derivatives_are_refused(nsp):
     """They are not there: an error, not outputs without a tangent."""
