@@ -139,27 +139,24 @@ __device__ __forceinline__ void store_channels(float *dst, int64_t off, bool liv
   if (dst && live) *reinterpret_cast<Ch<CH> *>(dst + off) = v;
 }
 
-// With x = f + bias and u = exp(x): c = 1 / (1 + u) = sigmoid(-x), to 2 ulp whatever x
-// is (0 where that is below 2^-126), and a = 1 - c, so that a and c add up to 1 to the
-// last bit: an error of a near 1 would build up over 1 / c steps.  pb = bias log2 e.
+// With x = f + bias and u = exp(x): c = 1 / (1 + u) = sigmoid(-x), and a = sigmoid(x) as u c
+// where u < 1, else as 1 - c, each the form that keeps its digits there: a gate near 0
+// is what is left of h0 and dh0 beside nothing else, and one near 1 is rounded once.
+// Relative errors, with 2^-24 for 1: the exponent t is rounded, |x| + |bias| (log2 e itself
+// is off by a quarter of |x|); 4 by 2^t and 2 by 1 / d (special function unit); 1 by
+// the sum and 1 by the product.  (0 where c is below 2^-126.)  pb = bias log2 e.
 template <int CH>
-__device__ __forceinline__ void gate(Ch<CH> f, Ch<CH> pb, Ch<CH> &u, Ch<CH> &c, Ch<CH> &a) {
+__device__ __forceinline__ void gate(Ch<CH> f, Ch<CH> pb, Ch<CH> &c, Ch<CH> &a) {
   const Ch<CH> t = fma(f, splat<CH>(kLog2e), pb);
+  Ch<CH> u;
 #pragma unroll
   for (int k = 0; k < CH; ++k) u.v[k] = exp2_sfu(t.v[k]);
   const Ch<CH> d = u + splat<CH>(1.0f);
 #pragma unroll
   for (int k = 0; k < CH; ++k) c.v[k] = rcp_sfu(d.v[k]);
-  a = sub(splat<CH>(1.0f), c);
-}
-// da / dx = u c^2, u c = sigmoid(x) to 2 ulp; where u is infinite, or c a NaN, u c counts
-// as 1.
-template <int CH>
-__device__ __forceinline__ Ch<CH> slope(Ch<CH> u, Ch<CH> c) {
-  Ch<CH> r = u * c;
+  const Ch<CH> low = u * c, high = sub(splat<CH>(1.0f), c);
 #pragma unroll
-  for (int k = 0; k < CH; ++k) r.v[k] = fminf(r.v[k], 1.0f);
-  return r * c;
+  for (int k = 0; k < CH; ++k) a.v[k] = u.v[k] < 1.0f ? low.v[k] : high.v[k];
 }
 
 // A warp's ring of segments in shared memory, filled by asynchronous copies that
@@ -528,8 +525,8 @@ __device__ __forceinline__ void forward_gates(const Stage<E, CH, 2> &in,
                                               Ch<CH> (&cz)[kSteps]) {
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    Ch<CH> u, c;
-    gate<CH>(at.read(in, 1, s, lane), pb, u, c, a[s]);
+    Ch<CH> c;
+    gate<CH>(at.read(in, 1, s, lane), pb, c, a[s]);
     cz[s] = c * at.read(in, 0, s, lane);
   }
   if (skip) {  // the same for the warp
@@ -798,8 +795,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
     for (int s = 0; s < kSteps; ++s, y += p.D) {
       if (s >= row.n) break;
       const bool gone = (row.skip >> s) & 1u, start = (row.start >> s) & 1u;
-      Ch<CH> e, c, a;
-      gate<CH>(widen<E, CH>(row.f[s]), pb, e, c, a);
+      Ch<CH> c, a;
+      gate<CH>(widen<E, CH>(row.f[s]), pb, c, a);
       a = pick(gone, splat<CH>(1.0f), a);
       const Ch<CH> cz = pick(gone, splat<CH>(0.0f), c * widen<E, CH>(row.z[s]));
       in = fma(a, pick(start, splat<CH>(0.0f), in), cz);
@@ -833,9 +830,8 @@ __device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in,
                                                Ch<CH> (&c)[kSteps], Ch<CH> (&q)[kSteps]) {
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    Ch<CH> u;
-    gate<CH>(at.read(in, 1, s, lane), pb, u, c[s], a[s]);
-    q[s] = slope(u, c[s]);
+    gate<CH>(at.read(in, 1, s, lane), pb, c[s], a[s]);
+    q[s] = a[s] * c[s];
   }
   if (skip) {
 #pragma unroll
@@ -1115,8 +1111,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const bool gone = (row.skip >> s) & 1u;
-      Ch<CH> e, c, a;
-      gate<CH>(widen<E, CH>(row.f[s]), pb, e, c, a);
+      Ch<CH> c, a;
+      gate<CH>(widen<E, CH>(row.f[s]), pb, c, a);
       a = pick(gone, splat<CH>(1.0f), a);
       const Ch<CH> cz = pick(gone, zero, c * widen<E, CH>(row.z[s]));
       run.H = fma(a, pick((row.start >> s) & 1u, zero, run.H), cz);
@@ -1143,11 +1139,10 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
       a[s] = splat<CH>(1.0f);
       c[s] = q[s] = zero;
       if (s < row.n && !((row.skip >> s) & 1u)) {
-        Ch<CH> e;
-        gate<CH>(widen<E, CH>(row.f[s]), pb, e, c[s], a[s]);
+        gate<CH>(widen<E, CH>(row.f[s]), pb, c[s], a[s]);
         const Ch<CH> before = pick((row.start >> s) & 1u, zero, h);
         const Ch<CH> z = widen<E, CH>(row.z[s]);
-        q[s] = slope(e, c[s]) * sub(before, z);
+        q[s] = a[s] * c[s] * sub(before, z);
         h = fma(a[s], before, c[s] * z);
       }
     }

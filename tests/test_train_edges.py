@@ -67,6 +67,41 @@ def test_scan_nan_gate_in_many_rows(nsp, T):
     check_nan_gates(nsp, 306, T, 130, "bf16")
 
 
+# ---- gates near 0 -----------------------------------------------------------------
+def gate_error(x, bias):
+    """Bound of the relative error of both gates at x = f + bias: the exponent t = x log2 e is
+    rounded by half a unit of |t|, and so is bias log2 e (ln 2 log2 e = 1), log2 e itself
+    is off by 2**-26 of it; 2 units of 2**-23 from 2^t, 1 from 1/d, half a unit each from 1 + u and
+    the product: 8 u."""
+    return U * (1.25 * abs(x) + abs(bias) + 8)
+
+
+@pytest.mark.parametrize("bias", [0.0, 3.0])
+@pytest.mark.parametrize("T", [1, 5, 8, 9, 40, 300])
+@pytest.mark.parametrize("B,D", [(2, 17), (2, 18), (400, 130)])
+def test_scan_closed_gates_keep_their_digits(nsp, B, D, T, bias):
+    """A row that starts with a closed gate: dh0 = a_0 d_0 and the part a_0 h0 of the states
+    (z = 0 there is nothing else) to the gate's own relative error, and 3 u for each product
+    of the some 50 steps that are remembered."""
+    x0 = torch.linspace(-20.0, -2.0, D)
+    f = torch.full((B, T, D), 2.0) - bias
+    f[:, 0] = x0 - bias
+    z = torch.zeros(B, T, D)
+    h0 = torch.rand(B, D, generator=gen(1)) + 0.5
+    dy = torch.rand(B, T, D, generator=gen(2)) + 0.5
+    b = torch.full((D,), bias)
+    want = scan_reference(z, f, b, None, None, h0, dy=dy)
+    y, h, st = nsp.gated_scan_forward(z.cuda(), f.cuda(), b.cuda(), h0=h0.cuda())
+    _, _, _, dh0 = nsp.gated_scan_backward(dy.cuda(), None, z.cuda(), f.cuda(), b.cuda(), st)
+    # the later steps' gates, at x = 2, add theirs as long as they are remembered
+    bound = gate_error(20 + abs(bias), bias) + 3 * U * min(T, 50) + min(T, 50) * 0.14 * gate_error(2, bias)
+    assert ((dh0.double().cpu() - want["dh0"]).abs() <= bound * want["dh0"]).all()
+    first = (y[:, 0].double().cpu() - want["y"][:, 0]).abs()
+    assert (first <= bound * want["y"][:, 0]).all()
+    some = min(T, 30) - 1
+    assert ((y[:, some].double().cpu() - want["y"][:, some]).abs() <= bound * want["y"][:, some]).all()
+
+
 # ---- distillation ----------------------------------------------------------------------
 @pytest.mark.parametrize("temp", [0.25, 0.5, 1.0])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
