@@ -337,11 +337,27 @@ template <int CH>
 __device__ __forceinline__ Ch<CH> after(const Run<CH> &r, bool cut, Ch<CH> h) {
   return cut ? r.H : fma(r.A, h, r.H);
 }
+// A is a product of gates; K = 1 - A = c_0 a_1 a_2 ... + c_1 a_2 ... + ... is a sum of
+// positive terms.  Near 1 each factor and product is rounded to a multiple of 2^-24 or
+// 2^-25, the same way where the gates are alike, step after step, while K keeps the digits
+// of the c.  So K is summed beside A over a quad, and what A is off by, e = (1 - A) - K, is
+// added: A + A e is 1 - K, rounded once, but for e K, where A is near 1, and A, to its own
+// digits, where it is near 0.  (A constant gate of f + bias = 10 is then off by 2^-24 each 32
+// steps, not by 2^-25 each step and product.)
+template <int CH>
+__device__ __forceinline__ Ch<CH> factor(Ch<CH> A, Ch<CH> K) {
+  return fma(A, sub(sub(splat<CH>(1.0f), A), K), A);
+}
 // Runs that warps or blocks exchange, N of them for every lane's channels.
 template <int CH, int N>
 struct Exchange {
   Run<CH> run[N][32];
   uint32_t cut[N];
+};
+// A tile's segments', with their K.
+template <int CH>
+struct Segments : Exchange<CH, kWarps> {
+  Ch<CH> K[kWarps][32];
 };
 
 // A quad is four consecutive segments: NS_SCAN_TILE steps from a multiple of
@@ -353,16 +369,19 @@ constexpr int kQuad = kSaveEvery;
 constexpr int kQuads = kWarps / kQuad;  // of a tile
 
 template <int CH>
-__device__ __forceinline__ Run<CH> quad_run(const Exchange<CH, kWarps> &x, int quad, int lane,
+__device__ __forceinline__ Run<CH> quad_run(const Segments<CH> &x, int quad, int lane,
                                             uint32_t cuts) {
   Run<CH> all = x.run[quad * kQuad][lane];
   if (cuts == 0) {
+    Ch<CH> K = x.K[quad * kQuad][lane];
 #pragma unroll
     for (int k = 1; k < kQuad; ++k) {
       const Run<CH> r = x.run[quad * kQuad + k][lane];
       all.H = fma(r.A, all.H, r.H);
       all.A = all.A * r.A;
+      K = fma(r.A, K, x.K[quad * kQuad + k][lane]);
     }
+    all.A = factor(all.A, K);
   } else {
 #pragma unroll
     for (int k = 1; k < kQuad; ++k) {
@@ -374,13 +393,13 @@ __device__ __forceinline__ Run<CH> quad_run(const Exchange<CH, kWarps> &x, int q
 }
 // Nonzero where a sequence starts in the quad.
 template <int CH>
-__device__ __forceinline__ uint32_t quad_cuts(const Exchange<CH, kWarps> &x, int quad) {
+__device__ __forceinline__ uint32_t quad_cuts(const Segments<CH> &x, int quad) {
   const uint4 c = *reinterpret_cast<const uint4 *>(&x.cut[quad * kQuad]);
   return c.x | c.y | c.z | c.w;
 }
 // The state before this warp's segment, from the one before its quad.
 template <int CH>
-__device__ __forceinline__ Ch<CH> inside_quad(const Exchange<CH, kWarps> &x, int lane, int warp,
+__device__ __forceinline__ Ch<CH> inside_quad(const Segments<CH> &x, int lane, int warp,
                                               uint32_t cuts, Ch<CH> h) {
   const int first = warp / kQuad * kQuad;
 #pragma unroll
@@ -390,23 +409,28 @@ __device__ __forceinline__ Ch<CH> inside_quad(const Exchange<CH, kWarps> &x, int
   return h;
 }
 
-// The state before this warp's segment, and h moved on past the tile: in a
-// block alone ...
+// In a block alone: the state before this warp's segment, from h before the tile, and after
+// the segment's steps, which need nothing of it, h past the tile.  `mid` is the state before
+// the tile's second quad for its warps, for the first one's still h.
+static_assert(kQuads == 2, "the quads of a tile are written out");
 template <int CH>
-__device__ __forceinline__ Ch<CH> pass_block(const Exchange<CH, kWarps> &x, int lane, int warp,
-                                             Ch<CH> &h) {
-  Ch<CH> mine = h;
-  uint32_t my_cuts = 0;
-#pragma unroll
-  for (int q = 0; q < kQuads; ++q) {
-    const uint32_t cuts = quad_cuts(x, q);
-    if (q == warp / kQuad) mine = h, my_cuts = cuts;
-    h = after(quad_run(x, q, lane, cuts), cuts != 0, h);
-  }
-  return inside_quad(x, lane, warp, my_cuts, mine);
+__device__ __forceinline__ Ch<CH> past_quad(const Segments<CH> &x, int quad, int lane, Ch<CH> h) {
+  const uint32_t cuts = quad_cuts(x, quad);
+  return after(quad_run(x, quad, lane, cuts), cuts != 0, h);
+}
+template <int CH>
+__device__ __forceinline__ Ch<CH> pass_block(const Segments<CH> &x, int lane, int warp, Ch<CH> h,
+                                             Ch<CH> &mid) {
+  mid = warp < kQuad ? h : past_quad(x, 0, lane, h);  // the same for the warp
+  return inside_quad(x, lane, warp, quad_cuts(x, warp / kQuad), mid);
+}
+template <int CH>
+__device__ __forceinline__ Ch<CH> past_tile(const Segments<CH> &x, int lane, int warp, Ch<CH> mid) {
+  if (warp < kQuad) mid = past_quad(x, 0, lane, mid);
+  return past_quad(x, 1, lane, mid);
 }
 
-// ... and in a cluster whose blocks took consecutive tiles, where every quad's run
+// In a cluster the blocks take consecutive tiles, and every quad's run
 // is stored into every block, asynchronously: the stores themselves count down
 // the barrier that the receiving block's warps wait at.  (A cluster barrier in
 // its place has each warp wait for its earlier stores to global memory: a quarter
@@ -443,7 +467,7 @@ __device__ __forceinline__ void send_word(uint32_t to, uint32_t bar, uint32_t v)
 }
 
 template <int CH>
-__device__ __forceinline__ void send_quad(const Exchange<CH, kWarps> &x, Quads<CH> &quads,
+__device__ __forceinline__ void send_quad(const Segments<CH> &x, Quads<CH> &quads,
                                           uint32_t rank, uint32_t split, int lane, int warp) {
   const int quad = warp / kQuad;
   const uint32_t cuts = quad_cuts(x, quad);
@@ -517,30 +541,38 @@ __device__ __forceinline__ void cluster_begin(Quads<CH> (&quads)[2]) {
 }
 
 // ---- forward --------------------------------------------------------------------
-// A segment's gates a and inputs c z; a = 1, c z = 0 at skipped steps.
+// A segment's gates a and inputs c z, and K of its run; a = 1, c = 0 at skipped steps.
 template <class E, int CH>
 __device__ __forceinline__ void forward_gates(const Stage<E, CH, 2> &in,
                                               const Places<E, CH, 2> &at, int lane, Ch<CH> pb,
                                               uint32_t skip, Ch<CH> (&a)[kSteps],
-                                              Ch<CH> (&cz)[kSteps]) {
+                                              Ch<CH> (&cz)[kSteps], Ch<CH> &K) {
+  const Ch<CH> zero = splat<CH>(0.0f);
+  K = zero;
+  if (skip == 0) {  // the same for the warp
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    Ch<CH> c;
-    gate<CH>(at.read(in, 1, s, lane), pb, c, a[s]);
-    cz[s] = c * at.read(in, 0, s, lane);
-  }
-  if (skip) {  // the same for the warp
+    for (int s = 0; s < kSteps; ++s) {
+      Ch<CH> c;
+      gate<CH>(at.read(in, 1, s, lane), pb, c, a[s]);
+      cz[s] = c * at.read(in, 0, s, lane);
+      K = fma(a[s], K, c);
+    }
+  } else {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const bool gone = (skip >> s) & 1u;
+      Ch<CH> c;
+      gate<CH>(at.read(in, 1, s, lane), pb, c, a[s]);
       a[s] = pick(gone, splat<CH>(1.0f), a[s]);
-      cz[s] = pick(gone, splat<CH>(0.0f), cz[s]);
+      cz[s] = pick(gone, zero, c * at.read(in, 0, s, lane));
+      K = fma(a[s], K, pick(gone, zero, c));
     }
   }
 }
 template <int CH>
 __device__ __forceinline__ Run<CH> forward_run(const Ch<CH> (&a)[kSteps],
-                                               const Ch<CH> (&cz)[kSteps], uint32_t start) {
+                                               const Ch<CH> (&cz)[kSteps], Ch<CH> K,
+                                               uint32_t start) {
   Run<CH> run = {a[0], cz[0]};
   if (start == 0) {
 #pragma unroll
@@ -548,12 +580,11 @@ __device__ __forceinline__ Run<CH> forward_run(const Ch<CH> (&a)[kSteps],
       run.H = fma(a[s], run.H, cz[s]);
       run.A = run.A * a[s];
     }
-  } else {
+    run.A = factor(run.A, K);
+  } else {  // A is not used
 #pragma unroll
-    for (int s = 1; s < kSteps; ++s) {
+    for (int s = 1; s < kSteps; ++s)
       run.H = fma(a[s], pick((start >> s) & 1u, splat<CH>(0.0f), run.H), cz[s]);
-      run.A = run.A * a[s];
-    }
   }
   return run;
 }
@@ -584,7 +615,7 @@ template <class E, int CH, bool kWide>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     scan_forward_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) Exchange<CH, kWarps> seg[2];
+  __shared__ __align__(16) Segments<CH> seg[2];
   const Place at = place_of<CH, false>(p);
   const int lane = at.lane, warp = at.warp;
   Stage<E, CH, 2> *ring = reinterpret_cast<Stage<E, CH, 2> *>(smem) + warp * kRing;
@@ -614,10 +645,6 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
   const Ch<CH> pb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
   E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
-  float *state = nullptr;  // the state before a quad is its first warp's to save
-  if (p.states && warp % kQuad == 0)
-    state = p.states + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
-                        t / NS_SCAN_TILE) * p.D + at.c0;
   int slot = 0;
   for (int i = 0; i < rounds; ++i, t += kTile) {
     __syncwarp();  // the slot that is filled now was read in the last round
@@ -626,19 +653,22 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     const uint32_t start = flags.start & 0xffu, skip = flags.skip & 0xffu;
     copy_wait<kRing - 1>();
     __syncwarp();
-    Ch<CH> a[kSteps], cz[kSteps];
-    forward_gates<E, CH>(ring[slot], places, lane, pb, skip, a, cz);
+    Ch<CH> a[kSteps], cz[kSteps], K;
+    forward_gates<E, CH>(ring[slot], places, lane, pb, skip, a, cz, K);
     slot = slot == kRing - 1 ? 0 : slot + 1;
-    Exchange<CH, kWarps> &x = seg[i & 1];
-    x.run[warp][lane] = forward_run<CH>(a, cz, start);
+    Segments<CH> &x = seg[i & 1];
+    x.run[warp][lane] = forward_run<CH>(a, cz, K, start);
+    x.K[warp][lane] = K;
     if (lane == 0) x.cut[warp] = start;
     __syncthreads();
-    const Ch<CH> in = pass_block<CH>(x, lane, warp, h);
-    if (state) {
-      store_channels<CH>(state, 0, at.live && t < T, in);
-      state += p.state_step;
-    }
+    Ch<CH> mid;
+    const Ch<CH> in = pass_block<CH>(x, lane, warp, h, mid);
+    // the state before a quad is its first warp's to save
+    if (p.states && warp % kQuad == 0)
+      store_channels<CH>(p.states, ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
+                                    t / NS_SCAN_TILE) * p.D + at.c0, at.live && t < T, in);
     forward_apply<E, CH>(p, a, cz, in, at.live, T - t, start, skip, y);
+    h = past_tile<CH>(x, lane, warp, mid);
     y += p.out_step;
   }
   copy_wait<0>();
@@ -655,7 +685,7 @@ template <class E, int CH, bool kWide, bool kAlone>
 __global__ void __launch_bounds__(kThreads, kAlone ? 2 : kForwardBlocks)
     scan_forward_cluster_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) Exchange<CH, kWarps> seg[3];
+  __shared__ __align__(16) Segments<CH> seg[3];
   __shared__ __align__(16) unsigned char quads_mem[2 * sizeof(Quads<CH>)];
   Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
   const Place at = place_of<CH, true>(p);
@@ -688,10 +718,6 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 2 : kForwardBlocks)
   const Ch<CH> pb = load_channels<CH>(p.bias, at.c0, at.live) * splat<CH>(kLog2e);
   Ch<CH> h = load_channels<CH>(p.h0, (int64_t)at.b * p.D + at.c0, at.live);
   E *y = static_cast<E *>(p.y) + ((int64_t)at.b * p.T + t) * p.D + at.c0;
-  float *state = nullptr;
-  if (p.states && warp % kQuad == 0)
-    state = p.states + ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
-                        t / NS_SCAN_TILE) * p.D + at.c0;
   bool lost = false;
   // What is left to do of a round whose runs are sent.
   struct Round {
@@ -706,9 +732,11 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 2 : kForwardBlocks)
     r.start = flags.start & 0xffu, r.skip = flags.skip & 0xffu;
     copy_wait<kAhead>();
     __syncwarp();
-    forward_gates<E, CH>(ring[i % kRing], places, lane, pb, r.skip, r.a, r.cz);
-    Exchange<CH, kWarps> &x = seg[i % 3];
-    x.run[warp][lane] = forward_run<CH>(r.a, r.cz, r.start);
+    Ch<CH> K;
+    forward_gates<E, CH>(ring[i % kRing], places, lane, pb, r.skip, r.a, r.cz, K);
+    Segments<CH> &x = seg[i % 3];
+    x.run[warp][lane] = forward_run<CH>(r.a, r.cz, K, r.start);
+    x.K[warp][lane] = K;
     if (lane == 0) x.cut[warp] = r.start;
     __syncthreads();
   };
@@ -723,14 +751,15 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 2 : kForwardBlocks)
       __syncthreads();  // every warp has read round i
       send_quad<CH>(seg[(i + 1) % 3], quads[(i + 1) & 1], at.rank, p.split, lane, warp);
     }
-    const Exchange<CH, kWarps> &x = seg[i % 3];
+    const Segments<CH> &x = seg[i % 3];
     const Ch<CH> in = inside_quad<CH>(x, lane, warp, quad_cuts(x, warp / kQuad), mine);
-    if (state) {
-      store_channels<CH>(state, 0, at.live && t < T, in);
-      state += p.state_step;
+    if (p.states && warp % kQuad == 0)
+      store_channels<CH>(p.states, ((int64_t)at.b * ((T + NS_SCAN_TILE - 1) / NS_SCAN_TILE) +
+                                    t / NS_SCAN_TILE) * p.D + at.c0, at.live && t < T, in);
+    if constexpr (!kAlone) {
+      Ch<CH> K;
+      forward_gates<E, CH>(ring[i % kRing], places, lane, pb, now.skip, now.a, now.cz, K);
     }
-    if constexpr (!kAlone)
-      forward_gates<E, CH>(ring[i % kRing], places, lane, pb, now.skip, now.a, now.cz);
     forward_apply<E, CH>(p, now.a, now.cz, in, at.live, T - t, now.start, now.skip, y);
     now = next;
     y += p.out_step;
@@ -785,12 +814,13 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
   E *y = static_cast<E *>(p.y) + (int64_t)b * p.T * p.D + c0;
   ShortRow<E, CH> row;
   Run<CH> all = {splat<CH>(1.0f), splat<CH>(0.0f)};
+  Ch<CH> all_K = splat<CH>(0.0f);
   bool cut = false;  // a sequence started
   const Ch<CH> first = h;
   for (int t0 = 0; t0 < (int)p.T; t0 += kSteps) {
     row.load(p, b, c0, t0);
     Run<CH> run = {splat<CH>(1.0f), splat<CH>(0.0f)};
-    Ch<CH> in = h;
+    Ch<CH> in = h, K = splat<CH>(0.0f);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s, y += p.D) {
       if (s >= row.n) break;
@@ -802,13 +832,17 @@ __global__ void __launch_bounds__(kShortThreads) scan_forward_short_kernel(const
       in = fma(a, pick(start, splat<CH>(0.0f), in), cz);
       run.H = fma(a, pick(start, splat<CH>(0.0f), run.H), cz);
       run.A = run.A * a;
+      K = fma(a, K, pick(gone, splat<CH>(0.0f), c));
       *reinterpret_cast<Raw<E, CH> *>(y) = narrow<E, CH>(pick(gone, splat<CH>(0.0f), in));
     }
+    run.A = factor(run.A, K);
     h = after(run, row.start != 0, h);
     all.H = after(run, row.start != 0, all.H);
     all.A = all.A * run.A;
+    all_K = fma(run.A, all_K, K);
     cut = cut || row.start != 0;
   }
+  all.A = factor(all.A, all_K);
   store_channels<CH>(p.h_last, (int64_t)b * p.D + c0, true, after(all, cut, first));
 }
 
@@ -843,22 +877,25 @@ __device__ __forceinline__ void backward_gates(const Stage<E, CH, 3> &in,
     }
   }
 }
-// (A, U) of the segment, and H.
+// (A, U) of the segment, and H and K.
 template <class E, int CH>
 __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
                                                 const Places<E, CH, 3> &at, int lane,
                                                 const Ch<CH> (&a)[kSteps],
                                                 const Ch<CH> (&c)[kSteps], uint32_t start,
-                                                uint32_t skip, Ch<CH> &H) {
+                                                uint32_t skip, Ch<CH> &H, Ch<CH> &K) {
   const Ch<CH> zero = splat<CH>(0.0f);
   Run<CH> run = {splat<CH>(1.0f), zero};
-  H = zero;
+  H = K = zero;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    run.A = run.A * a[s];
+    K = fma(a[s], K, c[s]);
+  }
+  run.A = factor(run.A, K);
   if ((start | skip) == 0) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      H = fma(a[s], H, c[s] * at.read(in, 0, s, lane));
-      run.A = run.A * a[s];
-    }
+    for (int s = 0; s < kSteps; ++s) H = fma(a[s], H, c[s] * at.read(in, 0, s, lane));
     Ch<CH> d = at.read(in, 2, kSteps - 1, lane);
 #pragma unroll
     for (int s = kSteps - 2; s >= 0; --s) d = fma(a[s + 1], d, at.read(in, 2, s, lane));
@@ -868,7 +905,6 @@ __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
     for (int s = 0; s < kSteps; ++s) {
       const Ch<CH> cz = pick((skip >> s) & 1u, zero, c[s] * at.read(in, 0, s, lane));
       H = fma(a[s], pick((start >> s) & 1u, zero, H), cz);
-      run.A = run.A * a[s];
     }
     Ch<CH> d = zero;
 #pragma unroll
@@ -883,7 +919,7 @@ __device__ __forceinline__ Run<CH> backward_run(const Stage<E, CH, 3> &in,
 // The state before this warp's segment, from the saved one before its quad:
 // through the quad's earlier segments, which later warps hold.
 template <int CH>
-__device__ __forceinline__ Ch<CH> state_before(const Exchange<CH, kWarps> &x,
+__device__ __forceinline__ Ch<CH> state_before(const Segments<CH> &x,
                                                const Ch<CH> (&ahead)[kWarps][32], int lane,
                                                int warp, Ch<CH> h) {
 #pragma unroll
@@ -966,8 +1002,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     scan_backward_kernel(const ScanParams p) {
   constexpr int kSegs = kCluster ? 3 : 2;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) Exchange<CH, kWarps> seg[kSegs];  // (A, U)
-  __shared__ Ch<CH> ahead[kSegs][kWarps][32];                // H of the same segments
+  __shared__ __align__(16) Segments<CH> seg[kSegs];  // (A, U)
+  __shared__ Ch<CH> ahead[kSegs][kWarps][32];        // H of the same segments
   __shared__ __align__(16) unsigned char quads_mem[kCluster ? 2 * sizeof(Quads<CH>) : 16];
   Quads<CH>(&quads)[2] = *reinterpret_cast<Quads<CH>(*)[2]>(quads_mem);
   const Place at = place_of<CH, kCluster>(p);
@@ -1029,8 +1065,10 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     copy_wait<kAhead>();
     __syncwarp();
     backward_gates<E, CH>(ring[slot], places, lane, pb, r.skip, r.a, r.c, r.q);
-    Ch<CH> H;
-    seg[s].run[warp][lane] = backward_run<E, CH>(ring[slot], places, lane, r.a, r.c, r.start, r.skip, H);
+    Ch<CH> H, K;
+    seg[s].run[warp][lane] =
+        backward_run<E, CH>(ring[slot], places, lane, r.a, r.c, r.start, r.skip, H, K);
+    seg[s].K[warp][lane] = K;
     ahead[s][warp][lane] = H;
     if (lane == 0) seg[s].cut[warp] = r.start;
     __syncthreads();
@@ -1048,9 +1086,11 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
       Ch<CH> h = take_state(t);
       runs(i, t, slot, i & 1, r);
       h = state_before<CH>(seg[i & 1], ahead[i & 1], lane, warp, h);
-      const Ch<CH> ui = pass_block<CH>(seg[i & 1], lane, warp, u);
+      Ch<CH> mid;
+      const Ch<CH> ui = pass_block<CH>(seg[i & 1], lane, warp, u, mid);
       backward_apply<E, CH>(p, ring[slot], places, lane, r.a, r.c, r.q, h, ui, at.live, t < 0 ? 0 : T - t,
                             r.start, r.skip, dz, df, sum);
+      u = past_tile<CH>(seg[i & 1], lane, warp, mid);
       dz -= p.out_step, df -= p.out_step;
       slot = slot == kRing - 1 ? 0 : slot + 1;
     }
@@ -1108,6 +1148,7 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
     if ((k + 1) * kSteps >= (int)p.T) continue;
     row.load(p, b, c0, k * kSteps);  // eight steps: more follow
     Run<CH> run = {splat<CH>(1.0f), zero};
+    Ch<CH> K = zero;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const bool gone = (row.skip >> s) & 1u;
@@ -1117,10 +1158,13 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
       const Ch<CH> cz = pick(gone, zero, c * widen<E, CH>(row.z[s]));
       run.H = fma(a, pick((row.start >> s) & 1u, zero, run.H), cz);
       run.A = run.A * a;
+      K = fma(a, K, pick(gone, zero, c));
     }
+    run.A = factor(run.A, K);
     kept[k + 1] = after(run, row.start != 0, kept[k]);
   }
   Run<CH> all = {splat<CH>(1.0f), zero};
+  Ch<CH> all_K = zero;
   bool cut = false;
   const Ch<CH> last = u;
 #pragma unroll
@@ -1166,13 +1210,20 @@ __global__ void __launch_bounds__(kShortThreads) scan_backward_short_kernel(cons
       }
     }
     run.H = pick(row.start & 1u, zero, a[0] * run.H);
+    Ch<CH> K = zero;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) run.A = run.A * a[s];
+    for (int s = 0; s < kSteps; ++s) {
+      run.A = run.A * a[s];
+      K = fma(a[s], K, c[s]);
+    }
+    run.A = factor(run.A, K);
     u = after(run, row.start != 0, u);
     all.H = after(run, row.start != 0, all.H);
     all.A = all.A * run.A;
+    all_K = fma(run.A, all_K, K);
     cut = cut || row.start != 0;
   }
+  all.A = factor(all.A, all_K);
   store_channels<CH>(p.dh0, bc, true, after(all, cut, last));
   store_channels<CH>(p.partial, bc, true, sum);
 }
@@ -1238,9 +1289,10 @@ uint64_t backward_units(uint32_t B, uint32_t D) { return (uint64_t)B * ((D + 63)
 
 template <class... KArgs>
 cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint32_t cluster,
-                   size_t smem, cudaStream_t st, const ScanParams &p, bool beside = false) {
+                   size_t smem, cudaStream_t st, const ScanParams &p, bool beside = false,
+                   bool all = false) {
   if (smem > 0) {
-    const cudaError_t e = allow_shared_memory((const void *)k);
+    const cudaError_t e = allow_shared_memory((const void *)k, all);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -1298,10 +1350,10 @@ cudaError_t run_as(ScanParams &p, cudaStream_t st) {
                ? launch(split == 1 ? scan_forward_kernel<E, CH, kWide>
                           : first > 0  ? scan_forward_cluster_kernel<E, CH, kWide, false>
                                        : scan_forward_cluster_kernel<E, CH, kWide, true>,
-                        count * split, kThreads, split, smem, st, p, first > 0)
+                        count * split, kThreads, split, smem, st, p, first > 0, kWide)
                : launch(split == 1 ? scan_backward_kernel<E, CH, kWide, false>
                                    : scan_backward_kernel<E, CH, kWide, true>,
-                        count * split, kThreads, split, smem, st, p, first > 0);
+                        count * split, kThreads, split, smem, st, p, first > 0, kWide);
   };
   if (whole) {
     const cudaError_t e = part(0, whole, 1);

@@ -11,8 +11,10 @@
 namespace nsk {
 
 // Lets a kernel take as much dynamic shared memory as a block can have; asked once
-// for a kernel and device by each thread that launches it.
-cudaError_t allow_shared_memory(const void *kernel);
+// for a kernel and device by each thread that launches it.  `all`: an SM that runs it gives
+// all that it has for shared memory, so that another kernel's blocks find room beside its own
+// (what is set for one kernel's blocks alone stays until they have left).
+cudaError_t allow_shared_memory(const void *kernel, bool all = false);
 
 cudaError_t launch_scan_forward(const ns_scan_inputs &in, const float *h0, void *y, float *h_last,
                                 float *states, cudaStream_t st);

@@ -48,7 +48,7 @@ bool check_scan(const ns_scan_inputs *in) {
 
 namespace nsk {
 
-cudaError_t allow_shared_memory(const void *kernel) {
+cudaError_t allow_shared_memory(const void *kernel, bool all) {
   struct Known {
     const void *kernel;
     int device;
@@ -67,6 +67,9 @@ cudaError_t allow_shared_memory(const void *kernel) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              most - (int)a.sharedSizeBytes);
+  if (e == cudaSuccess && all)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return e;

@@ -102,6 +102,45 @@ def test_scan_closed_gates_keep_their_digits(nsp, B, D, T, bias):
     assert ((y[:, some].double().cpu() - want["y"][:, some]).abs() <= bound * want["y"][:, some]).all()
 
 
+# ---- gates near 1 -------------------------------------------------------------------
+@pytest.mark.parametrize("T,B,D", [(4096, 1, 8), (20_000, 1, 8), (20_000, 2, 33), (1000, 310, 4)])
+def test_scan_long_memories(nsp, T, B, D):
+    """Constant gates of x = 8 to 14, which are the same step after step, so that what each
+    rounds the same way adds up.  Values are positive, so that a bound is relative.  From a
+    state to the one 32 steps on the run's factor, just below 1, is rounded once (u / 2) and the
+    state once (u): 1.5 u each 32 steps.  What the run adds, and how far its factor is from 1, is
+    sums of 32 positive terms, off by 64 u and the gates' own error of themselves: such an error
+    of c changes what is remembered by (1 + T c) times it."""
+    g = gen(T + D)
+    bias = torch.linspace(8.0, 14.0, D)
+    f = torch.zeros(B, T, D)
+    z = torch.rand(B, T, D, generator=g) + 0.5
+    dy = torch.rand(B, T, D, generator=g) + 0.5
+    h0 = torch.rand(B, D, generator=g) * 2 + 0.5
+    dh = torch.rand(B, D, generator=g) + 0.5
+    rows = slice(0, min(B, 2))  # the reference is slow
+    want = scan_reference(z[rows], f[rows], bias, None, None, h0[rows], dy=dy[rows], dh=dh[rows])
+    zc, fc, bc = z.cuda(), f.cuda(), bias.cuda()
+    y, h, st = nsp.gated_scan_forward(zc, fc, bc, h0=h0.cuda())
+    dz, df, _, dh0 = nsp.gated_scan_backward(dy.cuda(), dh.cuda(), zc, fc, bc, st)
+    c = torch.sigmoid(-bias.double())
+    gates = torch.tensor([gate_error(float(x), float(x)) for x in bias], dtype=torch.float64)
+    bound = U * (1.5 * T / 32 + 64) + (1 + T * c) * (gates + 64 * U)
+
+    def near(got, w, name, size=None):
+        got = got.double().cpu()[rows]
+        off = ((got - w).abs() / (bound * (w.abs() if size is None else size))).max()
+        assert off <= 1, (name, float(off))
+
+    near(y, want["y"], "y")
+    near(h, want["h_last"], "h_last")
+    near(dz, want["dz"], "dz")
+    near(dh0, want["dh0"], "dh0")
+    # df takes the difference of two values, of which each is as near as that
+    before = torch.cat([h0[rows].double()[:, None], want["y"][:, :-1]], 1)
+    near(df, want["df"], "df", (1 - c) * want["dz"] * (before + z[rows].double()))
+
+
 # ---- distillation ----------------------------------------------------------------------
 @pytest.mark.parametrize("temp", [0.25, 0.5, 1.0])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
