@@ -237,3 +237,52 @@ def test_scan_last_states_over_the_first(nsp, T):
         nsp.ns_scan_forward(inputs, h.data_ptr(), y.data_ptr(), h.data_ptr(), None,
                             torch.cuda.current_stream().cuda_stream)
         assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+
+
+# ---- the bias's gradient ---------------------------------------------------------------------------
+def dirty_memory():
+    """What PyTorch hands out next holds NaN."""
+    junk = [torch.full((n,), NAN, device="cuda") for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22, 1 << 24)]
+    del junk
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(60, 700, 355), (64, 200, 320), (2, 300, 64), (310, 70, 33), (60, 24, 1300)])
+def test_scan_bias_gradient_of_many_rows(nsp, B, T, D, dtype):
+    """Blocks with whole rows and clusters beside them share a workspace, some rows of which
+    are zeros.  dbias against the sum, in 64 bits, of the df that came with it: in 16 bits
+    each of those is off by its own rounding.  A term goes through at most T / 8 additions in
+    its warp, 8 between warps and B + 8 between rows, each off by u of at most the sizes' sum."""
+    host, cuda, dy, dh = scan_inputs(B, T, D, dtype, B + T)
+    kw = dict(pos=dev(host["pos"]), doc=dev(host["doc"]))
+    bias, h0 = dev(host["bias"]), dev(host["h0"])
+    _, _, st = nsp.gated_scan_forward(cuda["z"], cuda["f"], bias, h0=h0, **kw)
+    dirty_memory()
+    _, df, dbias, _ = nsp.gated_scan_backward(cuda["dy"], dev(dh), cuda["z"], cuda["f"], bias, st, **kw)
+    size = df.double().abs().sum((0, 1))
+    bound = ((T / 8 + B + 16) * U + ROUND[dtype]) * size + 1e-30
+    assert ((dbias.double() - df.double().sum((0, 1))).abs() <= bound).all()
+
+
+def test_scan_with_a_bias_is_captured_in_a_graph(nsp):
+    # the sums of the bias's gradient are a launch that may begin before the one it waits for ends
+    z, dy = torch.randn(330, 70, 64).cuda(), torch.randn(330, 70, 64).cuda()
+    bias = torch.rand(64).cuda()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        for _ in range(2):
+            _, _, s = nsp.gated_scan_forward(z, z, bias)
+            nsp.gated_scan_backward(dy, None, z, z, bias, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h, states = nsp.gated_scan_forward(z, z, bias)
+        back = nsp.gated_scan_backward(dy, None, z, z, bias, states)
+    z.normal_(), dy.normal_(), bias.uniform_()
+    graph.replay()
+    torch.cuda.synchronize()
+    want = nsp.gated_scan_forward(z, z, bias)
+    for a, b in zip((y, h, states), want):
+        assert torch.equal(a, b)
+    for a, b in zip(back, nsp.gated_scan_backward(dy, None, z, z, bias, want[2])):
+        assert torch.equal(a, b)
