@@ -764,22 +764,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 && R == 16 ? 3 : 2)
   }
 }
 
-// The forward kernel's groups and threads a token.  With tokens enough to fill the
-// GPU: 64 experts a thread, in groups of eight, for up to 128 experts; 128 a thread,
-// in groups of 16, beyond.  (262144 tokens in bfloat16: 128 experts 98 us with 64 a
-// thread, 141 us with 128; 256 experts 176 us and 150 us.  Fewer a thread leave room
-// for more threads an SM, but each of a token's threads goes through every choice.)
-// With few tokens what counts is how long one takes: eight experts a thread.
+// The forward kernel's groups and threads a token.  With tokens enough to fill the GPU: up
+// to 64 experts a thread, in groups of eight; 128, in groups of 16, where there are more
+// than 128, and from 65 on where logits have 16 bits and are kept so.  (262144 tokens, k =
+// 8: 128 experts in bfloat16 59 us with 64 a thread, 53 with 128, 127 experts, read by 2
+// bytes, 99 and 102; 128 in floats 62 and 81; 256 in bfloat16 111 and 87, in floats 113 and
+// 102.  Fewer a thread leave room for more threads an SM, but each of a token's threads
+// goes through every choice.)  With few tokens what counts is how long one takes: eight
+// experts a thread.
 struct Shape {
   int S, G;
   uint32_t lanes;
   uint64_t tiles;
 };
-Shape shape_of(uint32_t N, uint32_t E) {
+Shape shape_of(uint32_t N, uint32_t E, bool narrow) {
   uint32_t eights = 1;  // groups of eight, a power of two
   while (eights * 8 < E) eights *= 2;
   Shape s = {8, (int)(eights < 8 ? eights : 8), eights <= 8 ? 1u : 2u, 0};
-  if (eights > 16) s = {16, 8, eights / 16, 0};
+  const bool filled = N >= kForwardThreads * kSMs;  // a tile an SM, with a thread a token
+  if (eights > 16 || (eights == 16 && narrow && filled)) s = {16, 8, eights / 16, 0};
   uint32_t tokens = kForwardThreads / s.lanes;
   s.tiles = ((uint64_t)N + tokens - 1) / tokens;
   if (s.tiles < kSMs) {
@@ -863,8 +866,7 @@ int moved_at_once(const ns_route_inputs &in, const void *dlogits) {
 
 }  // namespace
 
-uint32_t route_blocks(uint32_t N, uint32_t E) {
-  const uint64_t tiles = shape_of(N, E).tiles;
+static uint32_t blocks_of(uint64_t tiles) {
   // up to two tiles a block, one cluster does without the second kernel
   if (tiles <= 2 * kTogether) return 0;
   // as many blocks as an SM has room for: five (262144 tokens in bfloat16, k = 8: 64
@@ -874,14 +876,18 @@ uint32_t route_blocks(uint32_t N, uint32_t E) {
   return tiles < most ? (uint32_t)tiles : most;
 }
 
+uint32_t route_blocks(uint32_t N, uint32_t E) {  // of logits of either size
+  return std::max(blocks_of(shape_of(N, E, false).tiles), blocks_of(shape_of(N, E, true).tiles));
+}
+
 cudaError_t launch_route_forward(const ns_route_inputs &in, int32_t *ids, float *weights,
                                  int32_t *counts, int32_t *tokens, float *loss, void *workspace,
                                  cudaStream_t st) {
   RouteParams p = params_of(in);
-  const Shape shape = shape_of(in.N, in.E);
+  const Shape shape = shape_of(in.N, in.E, in.dtype != NS_F32);
   p.wide = moved_at_once(in, nullptr), p.lanes = shape.lanes;
   p.ids = ids, p.weights = weights, p.counts = counts, p.tokens = tokens, p.loss = loss;
-  p.blocks = route_blocks(in.N, in.E);
+  p.blocks = blocks_of(shape.tiles);
   p.together = p.blocks == 0;
   if (p.together) p.blocks = shape.tiles < kTogether ? (uint32_t)shape.tiles : kTogether;
   if (p.blocks == 0) p.blocks = 1;  // no token: the counts are still written

@@ -10,7 +10,7 @@ import torch
 import torch.autograd.forward_ad as forward_ad
 
 from test_train_operators import (  # noqa: F401
-    DTYPES, INF, NAN, ROUND, close, dev, distill_inputs, distill_reference, gen, nsp, refused,
+    DTYPES, INF, NAN, ROUND, check_route, close, dev, distill_inputs, distill_reference, gen, nsp, refused,
     run_distill, scan_inputs, scan_reference)
 
 pytestmark = pytest.mark.gpu
@@ -286,3 +286,26 @@ def test_scan_with_a_bias_is_captured_in_a_graph(nsp):
         assert torch.equal(a, b)
     for a, b in zip(back, nsp.gated_scan_backward(dy, None, z, z, bias, want[2])):
         assert torch.equal(a, b)
+
+
+# ---- logits of 65 to 128 experts in 16 bits ----------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("E,k", [(65, 3), (100, 8), (127, 2), (128, 32)])
+def test_route_16_bit_logits_of_a_thread_alone(nsp, E, k, dtype):
+    """On both sides of as many tokens as fill the GPU with a thread each, to the bounds and
+    with the bits of test_train_operators."""
+    g = gen(E + k)
+    x = torch.randn(21_011, E, generator=g).to(DTYPES[dtype])
+    x[torch.rand(21_011, E, generator=g) < 0.1] = -INF
+    x[7::113] = -INF
+    x[9::113] = torch.finfo(DTYPES[dtype]).min
+    doc = (torch.rand(21_011, generator=g) < 0.9).int() - 1
+    check_route(nsp, x, k, doc, True, dtype)
+    check_route(nsp, x[:19_456], k, None, False, dtype)
+    xc, dw = x.cuda(), torch.randn(21_011, k, generator=g).cuda()
+    many = nsp.route(xc, k)
+    for n in (1, 77, 3000, 19_455):
+        few = nsp.route(xc[:n], k)
+        assert torch.equal(few.ids, many.ids[:n]) and torch.equal(few.weights, many.weights[:n])
+        assert torch.equal(nsp.route_backward(xc[:n], few, dw[:n]),
+                           nsp.route_backward(xc, many, dw)[:n])
