@@ -301,7 +301,8 @@ def distill_loss(logits: torch.Tensor, top_logits: torch.Tensor, top_ids: torch.
     the teacher's own probabilities) and q the softmax of ``logits / temperature``
     over V, loss = temperature**2 * sum_k p_k (log p_k - log q_{top_ids_k}).  Rows
     whose ``mask`` (uint8 or bool [N]) is 0 are not read and have loss 0; entries
-    whose id is outside [0, V) are absent.
+    whose id is outside [0, V) are absent.  (Where a row's loss is that of the next
+    token, its mask is the next position's, 0 where that starts a document.)
 
     ``logits`` [N, V] and ``top_logits`` [N, K] are float32, bfloat16 or float16,
     ``top_ids`` int32 or int64.  PyTorch differentiates it with respect to

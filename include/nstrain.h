@@ -6,7 +6,8 @@
  * ns_pack_step writes them:
  *  - pos == 0 starts a new sequence within a row (ns_pack_out.pos);
  *  - doc < 0 is padding (ns_pack_out.doc);
- *  - mask == 0 is a position that is not learned (ns_pack_out.mask).
+ *  - mask == 0 is a position that is not learned (ns_pack_out.mask; for the
+ *    loss of a position's next token, the mask of the next position).
  *
  *  - ns_scan_forward / ns_scan_backward: a gated linear recurrence over time
  *    that starts again at every sequence and passes over padding;

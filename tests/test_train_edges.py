@@ -309,3 +309,33 @@ def test_route_16_bit_logits_of_a_thread_alone(nsp, E, k, dtype):
         assert torch.equal(few.ids, many.ids[:n]) and torch.equal(few.weights, many.weights[:n])
         assert torch.equal(nsp.route_backward(xc[:n], few, dw[:n]),
                            nsp.route_backward(xc, many, dw)[:n])
+
+
+# ---- the README's lines ---------------------------------------------------------------------------
+def test_readme_lines_run_on_an_update(nsp):
+    """On the arrays that the packer writes, and with the learned positions of the example."""
+    import os
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    lines = text.split("### Training on the packed rows")[1].split("```python\n")[1].split("```")[0]
+    from corpus import make_preset
+    pk = nsp.Packer.from_corpus(make_preset("c1"))
+    out = pk.step(0)
+    v = {n: out[n][0] for n in ("pos", "doc", "mask")}
+    B, T = v["pos"].shape
+    v.update(z=torch.randn(B, T, 32).cuda(), f=torch.randn(B, T, 32).cuda(), bias=torch.zeros(32).cuda(),
+             z1=torch.randn(B, 1, 32).cuda(), f1=torch.randn(B, 1, 32).cuda(),
+             logits=torch.randn(B * T, 16).cuda(), student=torch.randn(B * T, 50).cuda(),
+             w=torch.ones(B * T).cuda())
+    v["top_logits"], v["top_ids"] = v["student"].topk(4, 1)
+    exec(lines, v)
+    sys.path.insert(0, os.path.join(root, "examples"))
+    try:
+        from packed_training_step import targets
+    finally:
+        sys.path.pop(0)
+    _, learned = targets(out["tokens"][0], out["pos"][0], out["mask"][0])
+    assert torch.equal(v["learned"], learned) and 0 < int(learned.sum()) < learned.numel()
+    assert v["loss"].shape == (B * T,) and ((v["loss"] != 0) == (learned != 0)).all()
+    pk.close()
