@@ -75,7 +75,8 @@ extern "C" {
  * elements) over rows and time; the halves of one projection are given as
  * they lie.  y, dz and df are contiguous [B][T][D]; bias is [D], h0 and
  * h_last [B][D], pos and doc contiguous [B][T] (either may be NULL: no
- * sequence starts, no padding).  h_last may be h0.
+ * sequence starts, no padding).  h_last may be h0; no other output may overlap
+ * an input.
  *
  * states ([B][ceil(T / NS_SCAN_TILE)][D] floats, NULL if no gradient is
  * wanted) receives the state before every tile of NS_SCAN_TILE steps; the
@@ -105,8 +106,8 @@ uint64_t ns_scan_workspace(uint32_t B, uint32_t T, uint32_t D);
  *   d_t = dy_t + u_t, u_{t-1} = a_t d_t (0 where pos_t == 0), u_{T-1} = dh_last
  *   dz_t = (1 - a_t) d_t,  df_t = a_t (1 - a_t) d_t (p_t - z_t)
  *   dbias = the sum of df over rows and time, dh0 = u_{-1}
- * dbias ([D]) and dh0 ([B][D]) may be NULL.  dz and df may not overlap the
- * inputs.  workspace: ns_scan_workspace bytes, 4-byte aligned; it may be NULL
+ * dbias ([D]) and dh0 ([B][D]) may be NULL.  No output may overlap an
+ * input.  workspace: ns_scan_workspace bytes, 4-byte aligned; it may be NULL
  * where dbias is.  Errors: as ns_scan_forward. */
 int ns_scan_backward(const ns_scan_inputs *in, const float *states, const void *dy,
                      int64_t dy_row, int64_t dy_time, const float *dh_last, void *dz, void *df,
