@@ -660,9 +660,9 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillPa
 }
 
 // Bytes of a block's slice at most: three blocks share an SM below 72 KB, so that
-// one's stores and copies run beside another's sums, two above.  (Rows of 297 KB,
-// 151936 bfloat16: 722 us for 8192 rows with four slices of 74 KB, 818 us with
-// eight of 37 KB.)
+// one's stores and copies run beside another's sums, two above.  (8192 rows of 297 KB,
+// 151936 bfloat16: 707 us with four slices of 74 KB, 728 with eight of 37 KB.  Rows of 250
+// KB: 566 us with four slices, 645 with eight, 790 with two of 125 KB.)
 constexpr uint64_t kSliceBytes = 80 * 1024;
 
 // Clusters that the GPU holds at a time (fewer than its room for their blocks,
@@ -712,10 +712,12 @@ cudaError_t launch(DistillParams &p, cudaStream_t st) {
   p.slice = chunks ? (chunks + C - 1) / C : 1;
   const size_t smem = distill_smem(p.slice, p.K, kGrad);
   // A warp's work on a row beside its chunks is worth some 60 of them: eight warps
-  // for the largest slices (64 KB: 585 us a pass against 640 us with four), four for
-  // smaller ones (37 KB: 743 us with four, 818 us with eight), two for the smallest.
+  // for the largest slices (64 KB, 8192 x 128256 bfloat16: 567 us, 637 with four), four for
+  // smaller ones (37 KB, 8192 x 151936: 727 us with four, 815 with eight; 8 KB, 16384 x 4000
+  // without and with the gradient: 56 and 92 us, 60 and 103 with two), two for the
+  // smallest (2 KB, 16384 x 1000: 46 and 74 us, 48 and 76 with four).
   const unsigned threads =
-      (p.slice >= 3500 ? 256 : p.slice >= 1024 ? 128 : 64) + 32 * kEntryWarps;
+      (p.slice >= 3500 ? 256 : p.slice >= 384 ? 128 : 64) + 32 * kEntryWarps;
   auto *k = distill_kernel<E, kGrad>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
