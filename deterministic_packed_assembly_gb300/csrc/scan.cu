@@ -49,6 +49,7 @@ constexpr int kShortSteps = NS_SCAN_TILE;  // rows up to this long can be a thre
 constexpr int kShortThreads = 128;
 constexpr int kBiasWarps = 8;
 static_assert(NS_SCAN_TILE % kSteps == 0, "states are saved at the start of a segment");
+static_assert(kShortSteps <= kTile, "short rows are a tile, which is not split");
 constexpr int kSaveEvery = NS_SCAN_TILE / kSteps;  // segments between two saved states
 
 struct ScanParams {
@@ -1316,19 +1317,22 @@ cudaError_t launch(void (*k)(KArgs...), uint64_t blocks, unsigned threads, uint3
   return e != cudaSuccess ? e : last;
 }
 
-// Whether a thread takes a row's channels alone: up to eight steps always, up to 32
-// where there are threads for every SM (forward and backward of T = 32 in bfloat16:
-// 64 rows of 2048 channels 25 us, 41 us by blocks; 8 rows of 512 17 us, 9 us by
-// blocks).
-bool short_rows(uint32_t B, uint32_t T, uint32_t D) {
+// Whether a thread takes a row's channels alone: up to eight steps always.  Up to 32, where
+// there are threads enough: they take T steps one after the other, the more at a time the
+// more of them there are, blocks the same time for any T.  (Forward and backward in
+// bfloat16, two channels a thread, us by threads and by blocks: T = 32, 49152 threads 36 and
+// 37, 32768 32 and 26; T = 16, 12288 13.3 and 13.5, 8192 12.6 and 10.2; floats: T = 32, 65536
+// 29 and 38, 32768 26 and 24.)  Single 16-bit channels always: by blocks they are copied in
+// words with the half of another (T = 32, 8 x 1001: 18.5 and 19.3 us, 96 x 1001: 35 and 94).
+bool short_rows(uint64_t threads, uint32_t T, bool halves) {
   return T <= (uint32_t)kSteps ||
-         (T <= (uint32_t)kShortSteps && (uint64_t)B * D >= 2 * kShortThreads * kSMs);
+         (T <= (uint32_t)kShortSteps && (halves || threads >= 48ull * T * T));
 }
 
 template <class E, int CH, bool kWide, bool kForward>
 cudaError_t run_as(ScanParams &p, cudaStream_t st) {
-  if (short_rows(p.B, p.T, p.D)) {
-    const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
+  const uint64_t n = (uint64_t)p.B * ((p.D + CH - 1) / CH);
+  if (short_rows(n, p.T, kHalves<E, CH>)) {
     return launch(kForward ? scan_forward_short_kernel<E, CH> : scan_backward_short_kernel<E, CH>,
                   (n + kShortThreads - 1) / kShortThreads, kShortThreads, 1, 0, st, p);
   }
@@ -1429,7 +1433,7 @@ cudaError_t launch_scan_forward(const ns_scan_inputs &in, const float *h0, void 
 }
 
 uint64_t scan_partial_rows(uint32_t B, uint32_t T, uint32_t D) {
-  return (uint64_t)B * (short_rows(B, T, D) ? 1 : layout_of(backward_units(B, D), T, false).split);
+  return (uint64_t)B * layout_of(backward_units(B, D), T, false).split;  // 1 for short rows
 }
 
 cudaError_t launch_scan_backward(const ns_scan_inputs &in, const float *states, const void *dy,
