@@ -1256,21 +1256,22 @@ __global__ void __launch_bounds__(32 * kBiasWarps)
 // clusters of blocks along time.
 //
 // Forward an SM has room for three blocks, and the clusters run in the room beside the
-// others (8 rows of T = 4096, bfloat16: 320 units 98 us with the last 16 in clusters of
-// four, 114 us by a block each, 110 us in clusters of eight; 160 units 76 us and 98 us;
-// 376 units 116 us in clusters of two, 130 us by a block each), but a lane's single
-// channels are slower there than in clusters alone (5 rows of T = 32749, 1001 floats:
-// 786 us and 583 us).  Backward two blocks fill an SM, and the rest comes after them
-// (320 units 170 us, 231 us by a block each), unless it is more than a unit an SM (252
-// units 141 us by a block each, 181 us in clusters).  Without others, and after them,
-// clusters of four may be three blocks an SM (104 units backward 88 us, 96 us in
-// clusters of two), those of eight two (44 units of T = 16384 forward 149 us, 136 us in
+// others (8 rows of T = 4096, bfloat16: 320 units 107 us with the last 16 in clusters of
+// four, 131 us by a block each, 112 us in clusters of eight; 160 units 78 us and 95 us;
+// 376 units 117 us in clusters of two, 131 us by a block each; floats, 5 rows of T = 32749,
+// 1024 channels: 442 us with the last 8 in clusters of four, 508 us all in clusters), but
+// rows copied by 8 bytes or fewer a lane are slower there than in clusters alone (1001
+// channels: 906 us and 602 us).  Backward two blocks fill an SM, and the rest comes after
+// them (320 units 173 us, 230 us by a block each), unless it is more than a unit an SM (252
+// units 147 us by a block each, 191 us in clusters).  Without others, and after them,
+// clusters of four may be three blocks an SM (104 units backward 90 us, 100 us in
+// clusters of two), those of eight two (44 units of T = 16384 forward 152 us, 134 us in
 // clusters of four).
 struct Layout {
   uint64_t whole;  // units taken by one block each
   uint32_t split;  // blocks for each of the others
 };
-Layout layout_of(uint64_t units, uint32_t T, bool forward, bool single = false) {
+Layout layout_of(uint64_t units, uint32_t T, bool forward, bool slow = false) {
   const uint64_t tiles = (T + (uint64_t)kTile - 1) / kTile;
   const uint64_t fill = forward ? kSMs : kBackwardBlocks * kSMs, whole = units / fill * fill;
   const uint64_t rest = units - whole;
@@ -1282,7 +1283,7 @@ Layout layout_of(uint64_t units, uint32_t T, bool forward, bool single = false) 
   };
   if (rest && rest <= kSMs)
     while (fits(2 * split)) split *= 2;
-  if (single && beside && whole == kSMs && split > 1) return {0, split};
+  if (slow && beside && whole == kSMs && split > 1) return {0, split};
   return {split == 1 ? units : whole, split};
 }
 
@@ -1340,7 +1341,8 @@ cudaError_t run_as(ScanParams &p, cudaStream_t st) {
   // workspace's size depends on the sizes alone.
   p.groups = (p.D + 32 * CH - 1) / (32 * CH);
   const uint64_t units = (uint64_t)p.B * p.groups;
-  Layout l = layout_of(kForward ? units : backward_units(p.B, p.D), p.T, kForward, CH == 1);
+  Layout l = layout_of(kForward ? units : backward_units(p.B, p.D), p.T, kForward,
+                       CH == 1 && !kWide);
   if (!kForward && CH == 1) l.whole = l.split == 1 ? units : std::min(l.whole * 2, units);
   p.sums = l.split;
   const uint64_t whole = l.whole;
