@@ -30,9 +30,9 @@
 // maximum, and a row at the type's lowest value does not overflow.
 //
 // Bound by memory where the gradient is wanted (8192 x 128256 bfloat16, 65 % of the rows
-// learned: 562 us, 6.18 TB/s, 0.91 of a copy's bandwidth), by the SMs' instructions where
+// learned: 565 us, 6.15 TB/s, 0.90 of a copy's bandwidth), by the SMs' instructions where
 // it is not (4093 x 50257: 76 us, 63 % of the issue slots, 5.1 TB/s), by the entries'
-// chain where K is large (1021 x 50257 float: 94 us with K = 200, 76 us with 16).
+// chain where K is large (1021 x 50257 float: 93 us with K = 200, 75 us with 16).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -19,13 +19,12 @@
 // that state is then not used at all (not even times 0), so that a NaN of one
 // document does not reach the next.
 //
-// Forward 6 bytes an element move (16 bits) and some 21 warp instructions a step of 32
-// pairs of channels run, half of them the gate's and the two passes' arithmetic.  With
-// every SM full it is bound by their issue (8 x 4096 x 2432 bfloat16: 92 us, 5.2 TB/s,
-// 54 % of the slots, the rest waiting for a tile's exchange), backward by memory (142
-// us, 5.6 TB/s: 10 bytes and 40 instructions).  Few units are bound by the latency of a
-// tile, 1.2 us in a block alone, 2 to 4 us in a cluster (1 x 32749 x 1001 floats: 129
-// and 195 us, 3.1 and 3.4 TB/s).
+// Forward 6 bytes an element move (16 bits), backward 10.  With two units on every SM
+// nothing is used up: warps wait for arithmetic, shared memory and a tile's exchange (8 x
+// 4096 x 2432 bfloat16: forward 95 us, 5.1 TB/s, DRAM 61 % and 58 % of the issue slots;
+// backward 146 us, 5.5 TB/s, DRAM 66 % and 62 %).  Few units are bound by the latency of a
+// round, 1.5 us in a block alone, 2 and 3 us in a cluster (1 x 32749 x 1001 floats: 130 and
+// 196 us, 3.0 and 3.4 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
