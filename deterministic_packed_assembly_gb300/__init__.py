@@ -5,10 +5,11 @@ Pre-tokenized documents from a weighted mixture of sources become fixed
 a 64-bit fingerprint and a learned-position count per row -- that depend only
 on the recipe, the seed and the update index.  The work runs in the CUDA
 kernels of ``libnspack.so`` (C ABI in ``include/nspack.h``); this package is
-the Python binding.  ``gated_scan``, ``route`` and ``distill_loss`` are operators
-of a model trained on such batches (C ABI in ``include/nstrain.h``): they take
-the position ids, document ids and loss masks as the packer writes them.  Importing it fails if the library is not built: there is
-no CPU path.
+the Python binding.  ``embed``, ``layer_norm``, ``gated_scan``, ``route``,
+``dispatch``, ``combine`` and ``distill_loss`` are operators of a model trained on
+such batches (C ABI in ``include/nstrain.h``): they take the tokens, position ids,
+document ids and loss masks as the packer writes them.  Importing it fails if the
+library is not built: there is no CPU path.
 """
 from ._lib import (  # noqa: F401
     NS_BF16,
@@ -32,7 +33,17 @@ from ._lib import (  # noqa: F401
     LIB_PATH,
     SYMBOLS,
     NsPackError,
+    ns_combine,
+    ns_combine_backward,
+    ns_dispatch,
+    ns_dispatch_workspace,
     ns_distill,
+    ns_embed_backward,
+    ns_embed_forward,
+    ns_embed_workspace,
+    ns_norm_backward,
+    ns_norm_forward,
+    ns_norm_workspace,
     ns_pack_batch_fp,
     ns_pack_check,
     ns_pack_fingerprint,
@@ -51,6 +62,18 @@ from ._lib import (  # noqa: F401
     ns_scan_backward,
     ns_scan_forward,
     ns_scan_workspace,
+)
+from .layers import (  # noqa: F401
+    ExpertOrder,
+    combine,
+    combine_backward,
+    dispatch,
+    dispatch_backward,
+    embed,
+    embed_backward,
+    layer_norm,
+    layer_norm_backward,
+    layer_norm_forward,
 )
 from .operators import (  # noqa: F401
     Routing,

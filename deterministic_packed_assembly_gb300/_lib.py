@@ -175,13 +175,55 @@ class ns_route_inputs(_Sized):
     ]
 
 
+class ns_embed_inputs(_Sized):
+    _fields_ = [
+        ("tokens", C.c_void_p),
+        ("doc", C.c_void_p),
+        ("N", C.c_uint32),
+        ("V", C.c_uint32),
+        ("D", C.c_uint32),
+        ("table_dtype", C.c_int32),
+        ("dtype", C.c_int32),
+        ("ids_64", C.c_int32),
+        ("scale", C.c_float),
+    ]
+
+
+class ns_norm_inputs(_Sized):
+    _fields_ = [
+        ("x", C.c_void_p),
+        ("x_row", C.c_int64),
+        ("weight", C.c_void_p),
+        ("bias", C.c_void_p),
+        ("doc", C.c_void_p),
+        ("N", C.c_uint32),
+        ("D", C.c_uint32),
+        ("dtype", C.c_int32),
+        ("weight_dtype", C.c_int32),
+        ("eps", C.c_float),
+    ]
+
+
+class ns_expert_sizes(_Sized):
+    _fields_ = [
+        ("N", C.c_uint32),
+        ("k", C.c_uint32),
+        ("E", C.c_uint32),
+        ("D", C.c_uint32),
+        ("dtype", C.c_int32),
+    ]
+
+
 # Every symbol the headers declare, for the load check.
 SYMBOLS = ("ns_pack_init", "ns_pack_step", "ns_pack_fingerprint", "ns_pack_batch_fp",
            "ns_pack_step_learned", "ns_pack_info", "ns_pack_stream_windows",
            "ns_pack_quota_table", "ns_pack_check", "ns_pack_free", "ns_pack_strerror",
            "ns_pack_quota_noalloc", "ns_pack_probe_hash_terms",
            "ns_scan_forward", "ns_scan_workspace", "ns_scan_backward", "ns_distill",
-           "ns_route_workspace", "ns_route_forward", "ns_route_backward")
+           "ns_route_workspace", "ns_route_forward", "ns_route_backward",
+           "ns_embed_forward", "ns_embed_workspace", "ns_embed_backward",
+           "ns_norm_forward", "ns_norm_workspace", "ns_norm_backward",
+           "ns_dispatch_workspace", "ns_dispatch", "ns_combine", "ns_combine_backward")
 
 
 def _load() -> C.CDLL:
@@ -234,6 +276,28 @@ def _load() -> C.CDLL:
     L.ns_route_forward.argtypes = [route, vp, vp, vp, vp, vp, vp, vp]
     L.ns_route_backward.restype = i32
     L.ns_route_backward.argtypes = [route, vp, vp, vp, vp, vp, vp, vp, vp]
+    embed, norm, experts = (C.POINTER(t) for t in
+                            (ns_embed_inputs, ns_norm_inputs, ns_expert_sizes))
+    L.ns_embed_forward.restype = i32
+    L.ns_embed_forward.argtypes = [embed, vp, i64, vp, vp]
+    L.ns_embed_workspace.restype = u64
+    L.ns_embed_workspace.argtypes = [u32, u32, u32]
+    L.ns_embed_backward.restype = i32
+    L.ns_embed_backward.argtypes = [embed, vp, i64, vp, vp, vp]
+    L.ns_norm_forward.restype = i32
+    L.ns_norm_forward.argtypes = [norm, vp, vp, vp, vp]
+    L.ns_norm_workspace.restype = u64
+    L.ns_norm_workspace.argtypes = [u32, u32]
+    L.ns_norm_backward.restype = i32
+    L.ns_norm_backward.argtypes = [norm, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.ns_dispatch_workspace.restype = u64
+    L.ns_dispatch_workspace.argtypes = [u32, u32, u32]
+    L.ns_dispatch.restype = i32
+    L.ns_dispatch.argtypes = [experts, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    L.ns_combine.restype = i32
+    L.ns_combine.argtypes = [experts, vp, vp, vp, vp, i64, vp, vp]
+    L.ns_combine_backward.restype = i32
+    L.ns_combine_backward.argtypes = [experts, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp]
     return L
 
 
@@ -374,3 +438,55 @@ def ns_route_backward(inputs: ns_route_inputs, ids, weights, counts, tokens, d_w
                       dlogits, stream) -> None:
     check(lib.ns_route_backward(C.byref(inputs), ids, weights, counts, tokens, d_weights, d_loss,
                                 dlogits, stream), "ns_route_backward")
+
+
+def ns_embed_forward(inputs: ns_embed_inputs, table, table_row: int, y, stream) -> None:
+    check(lib.ns_embed_forward(C.byref(inputs), table, table_row, y, stream), "ns_embed_forward")
+
+
+def ns_embed_workspace(N: int, V: int, D: int) -> int:
+    _fits("N", N), _fits("V", V), _fits("D", D)
+    return lib.ns_embed_workspace(N, V, D)
+
+
+def ns_embed_backward(inputs: ns_embed_inputs, dy, dy_row: int, dtable, workspace, stream) -> None:
+    check(lib.ns_embed_backward(C.byref(inputs), dy, dy_row, dtable, workspace, stream),
+          "ns_embed_backward")
+
+
+def ns_norm_forward(inputs: ns_norm_inputs, y, mean, rstd, stream) -> None:
+    check(lib.ns_norm_forward(C.byref(inputs), y, mean, rstd, stream), "ns_norm_forward")
+
+
+def ns_norm_workspace(N: int, D: int) -> int:
+    _fits("N", N), _fits("D", D)
+    return lib.ns_norm_workspace(N, D)
+
+
+def ns_norm_backward(inputs: ns_norm_inputs, mean, rstd, dy, dy_row: int, dx, dweight, dbias,
+                     workspace, stream) -> None:
+    check(lib.ns_norm_backward(C.byref(inputs), mean, rstd, dy, dy_row, dx, dweight, dbias,
+                               workspace, stream), "ns_norm_backward")
+
+
+def ns_dispatch_workspace(N: int, k: int, E: int) -> int:
+    _fits("N", N), _fits("k", k), _fits("E", E)
+    return lib.ns_dispatch_workspace(N, k, E)
+
+
+def ns_dispatch(sizes: ns_expert_sizes, ids, x, x_row: int, place, slots, offsets, rows, workspace,
+                stream) -> None:
+    check(lib.ns_dispatch(C.byref(sizes), ids, x, x_row, place, slots, offsets, rows, workspace,
+                          stream), "ns_dispatch")
+
+
+def ns_combine(sizes: ns_expert_sizes, place, offsets, weights, rows, rows_row: int, out,
+               stream) -> None:
+    check(lib.ns_combine(C.byref(sizes), place, offsets, weights, rows, rows_row, out, stream),
+          "ns_combine")
+
+
+def ns_combine_backward(sizes: ns_expert_sizes, place, offsets, weights, rows, rows_row: int, d_out,
+                        d_out_row: int, d_rows, d_weights, stream) -> None:
+    check(lib.ns_combine_backward(C.byref(sizes), place, offsets, weights, rows, rows_row, d_out,
+                                  d_out_row, d_rows, d_weights, stream), "ns_combine_backward")

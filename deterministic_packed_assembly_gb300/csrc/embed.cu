@@ -1,0 +1,391 @@
+// Rows of a table at a batch's tokens, and the table's gradient.
+//
+//   y[n] = scale table[t_n],  dtable[v] = scale sum of dy[n] over the n with t_n = v
+//
+// where a position with doc < 0 or a token outside [0, V) has y = 0 and no gradient.
+//
+// Memory bounds both.  The gradient has V rows, of which a batch touches few, while a
+// few tokens make up much of a batch: the positions are sorted by token (order.cu, so
+// that sums have a fixed order and every row is written once), and the order is cut into
+// tiles of 32 positions whatever the tokens.  A warp takes a tile's 256 columns; it writes
+// the rows of the tokens that begin in its tile, and reads up to 31 positions on for the
+// last one.  A token of more positions than that, across tiles, leaves 32-bit sums of each
+// tile, which the last kernel adds up, in the tiles' order.  The rows of tokens that are
+// not there are filled with 0 by the same launch.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "elem.cuh"
+#include "kernels.h"
+#include "order.h"
+#include "rows.cuh"
+#include "train.h"
+
+namespace nsk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;
+constexpr uint32_t kTile = 32;                 // positions of a tile
+constexpr uint32_t kSlice = 32 * kChunk;       // columns of a warp
+constexpr uint32_t kBefore = 0xffffffffu, kBehind = 0xfffffffeu;
+
+struct EmbedParams {
+  const void *tokens;
+  const int32_t *doc;
+  uint32_t N, V, D;
+  int32_t wide;
+  float scale;
+  // forward
+  const void *table;
+  int64_t table_row;
+  void *y;
+  uint32_t lanes, slices;
+  // backward
+  const void *dy;
+  int64_t dy_row;
+  void *dtable;
+  const Sorted *sorted;
+  const uint8_t *used;
+  uint32_t *counter;      // tiles in `open`
+  uint32_t *open;         // tiles whose last token goes on beyond the next tile's reach
+  float *head, *tail;     // [tiles][slices * kSlice]: a tile's sums of the token before it, of
+                          // the one that goes on
+  uint32_t tiles, sum_blocks;
+};
+
+// ---- forward ------------------------------------------------------------------------
+template <class W, class E, bool kWhole>
+__global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
+  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
+  const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
+  if (n >= p.N) return;
+  const int64_t t = p.wide ? static_cast<const int64_t *>(p.tokens)[n]
+                           : static_cast<const int32_t *>(p.tokens)[n];
+  const bool there = t >= 0 && t < (int64_t)p.V && !(p.doc && p.doc[n] < 0);
+  const W *row = static_cast<const W *>(p.table) + (there ? t : 0) * p.table_row;
+  E *y = static_cast<E *>(p.y) + (int64_t)n * p.D;
+  const int lead = lead_of<E, kWhole>(y);
+  const uint32_t first = slice * p.lanes * kUnroll + threadIdx.x % p.lanes;
+  Words<W> v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t c = (int64_t)(first + u * p.lanes) * kChunk - lead;
+    if (there && c < p.D) v[u] = load_columns<W, kWhole>(row, c, p.D);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t c = (int64_t)(first + u * p.lanes) * kChunk - lead;
+    float x[kChunk] = {};
+    if (there) {
+      widen<W>(v[u], x);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) x[i] *= p.scale;
+    }
+    if (c < p.D) store_columns<E, kWhole>(y, c, p.D, narrow<E>(x));
+  }
+}
+
+// ---- backward --------------------------------------------------------------------------
+// 0 to the elements at [a, b), by a block.
+template <class W>
+__device__ __forceinline__ void fill_zero(uintptr_t a, uintptr_t b) {
+  uintptr_t lo = (a + 15) / 16 * 16, hi = b / 16 * 16;
+  if (lo > hi) lo = hi = b;
+  for (uintptr_t i = a + threadIdx.x * sizeof(W); i < lo; i += kThreads * sizeof(W))
+    *reinterpret_cast<W *>(i) = from_f32<W>(0.0f);
+  for (uintptr_t i = lo + threadIdx.x * 16; i < hi; i += kThreads * 16)
+    *reinterpret_cast<uint4 *>(i) = make_uint4(0, 0, 0, 0);
+  for (uintptr_t i = hi + threadIdx.x * sizeof(W); i < b; i += kThreads * sizeof(W))
+    *reinterpret_cast<W *>(i) = from_f32<W>(0.0f);
+}
+
+// Rows of tokens that are not there, of 32 tokens: runs of them are one stretch of bytes.
+template <class W>
+__device__ __forceinline__ void zero_rows(const EmbedParams &p, uint32_t part) {
+  const uint32_t lane = threadIdx.x % 32;
+  const uint32_t v0 = part * 32, rows = min(32u, p.V - v0);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.dtable);
+  const uint64_t bytes = (uint64_t)p.D * sizeof(W);
+  uint32_t left = __ballot_sync(0xffffffffu, lane < rows && !p.used[v0 + lane]);
+  while (left) {
+    const int a = __ffs(left) - 1;
+    const uint32_t ones = ~(left >> a);
+    const int n = ones ? __ffs(ones) - 1 : 32;  // of the run at a
+    fill_zero<W>(at + (v0 + a) * bytes, at + (v0 + a + n) * bytes);
+    left &= a + n >= 32 ? 0u : ~0u << (a + n);
+  }
+}
+
+template <class W, class E, bool kWhole>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p) {
+  pdl_wait();
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (blockIdx.x >= p.sum_blocks) {
+    zero_rows<W>(p, blockIdx.x - p.sum_blocks);
+    return;
+  }
+  const uint64_t unit = (uint64_t)blockIdx.x * kWarps + warp;
+  const uint32_t tile = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
+  if (tile >= p.tiles) return;
+  // three tiles' keys: the one before, this one, the next
+  const uint32_t i0 = tile * kTile, i = i0 + lane;
+  uint32_t before = kBefore;
+  Sorted cur = {kBehind, 0}, next = {kBehind, 0};
+  if (tile) before = p.sorted[i - kTile].key;
+  if (i < p.N) cur = p.sorted[i];
+  if (i + kTile < p.N) next = p.sorted[i + kTile];
+  if (cur.key >= p.V) cur.key = kBehind;
+  if (next.key >= p.V) next.key = kBehind;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const uint32_t k0 = __shfl_sync(kAll, cur.key, 0), k31 = __shfl_sync(kAll, cur.key, 31);
+  const uint32_t n0 = __popc(__ballot_sync(kAll, cur.key == k0));
+  const uint32_t n31 = __popc(__ballot_sync(kAll, cur.key == k31));
+  const uint32_t back = __popc(__ballot_sync(kAll, before == k0));  // positions in the tile before
+  const uint32_t on = __popc(__ballot_sync(kAll, next.key == k31));  // and in the next one
+  if (k0 == kBehind) return;  // padding comes last
+  uint32_t e = 0, end = __popc(__ballot_sync(kAll, cur.key != kBehind));
+  uint32_t first_end = 0;     // the positions before it go to `head`
+  if (back) {
+    if (back + n0 > kTile)
+      first_end = n0;
+    else
+      e = n0;                 // the tile before has them
+  }
+  bool open = false;          // the last token's sum goes to `tail`
+  if (k31 != kBehind && on && !(back && n0 == kTile)) {
+    if (n31 + on > kTile)
+      open = true;
+    else
+      end += on;
+  }
+  const uint64_t partial = ((uint64_t)tile * p.slices + slice) * kSlice + lane * kChunk;
+  const E *dy = static_cast<const E *>(p.dy);
+  W *dtable = static_cast<W *>(p.dtable);
+  float acc[kChunk] = {};
+  constexpr int kAhead = kWhole && sizeof(E) == 2 ? 8 : 4;
+  while (e < end) {
+    Words<E> v[kAhead];
+    uint32_t key[kAhead + 1];
+    int64_t col[kAhead];
+#pragma unroll
+    for (int a = 0; a <= kAhead; ++a) {
+      const uint32_t x = __shfl_sync(kAll, cur.key, (e + a) & 31);
+      const uint32_t y = __shfl_sync(kAll, next.key, (e + a) & 31);
+      key[a] = e + a >= end ? kBehind : e + a < kTile ? x : y;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const uint32_t x = __shfl_sync(kAll, cur.at, (e + a) & 31);
+      const uint32_t y = __shfl_sync(kAll, next.at, (e + a) & 31);
+      if (key[a] == kBehind) continue;
+      const int lead = lead_of<W, kWhole>(dtable + (int64_t)key[a] * p.D);
+      col[a] = (int64_t)(slice * 32 + lane) * kChunk - lead;
+      const uint32_t at = e + a < kTile ? x : y;
+      if (col[a] < p.D) v[a] = load_columns<E, kWhole>(dy + (int64_t)at * p.dy_row, col[a], p.D);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (key[a] == kBehind) continue;
+      if (col[a] < p.D) {
+        float x[kChunk];
+        widen<E>(v[a], x);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) acc[j] += x[j];
+      }
+      if (key[a + 1] == key[a]) continue;
+      // the token's last position here
+      const bool to_head = e + a < first_end;
+      const bool to_tail = open && e + a + 1 == end && !to_head;
+      if (col[a] < p.D) {
+        if (to_head || to_tail) {
+          float4 *to = reinterpret_cast<float4 *>((to_head ? p.head : p.tail) + partial);
+          to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) acc[j] *= p.scale;
+          store_columns<W, kWhole>(dtable + (int64_t)key[a] * p.D, col[a], p.D, narrow<W>(acc));
+        }
+      }
+      if (to_tail && slice == 0 && lane == 0) p.open[atomicAdd(p.counter, 1u)] = tile;
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) acc[j] = 0.0f;
+    }
+    e += kAhead;
+  }
+}
+
+// The tokens across tiles: the tail where one begins and the heads behind it.  A
+// block takes one's 256 columns, each warp a run of its tiles; the runs are added in order.
+template <class W, bool kWhole>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams p) {
+  pdl_wait();
+  __shared__ float sums[kWarps][kSlice];
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint64_t units = (uint64_t)*p.counter * p.slices;
+  for (uint64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const uint32_t tile = p.open[unit / p.slices], slice = (uint32_t)(unit % p.slices);
+    const uint32_t key = p.sorted[tile * kTile + kTile - 1].key;
+    uint32_t more = 0;  // tiles that begin with the token
+    for (;;) {
+      const uint64_t at = (uint64_t)(tile + 1 + more + threadIdx.x) * kTile;
+      const int n = __syncthreads_count(at < p.N && p.sorted[at].key == key);
+      more += n;
+      if (n < kThreads) break;
+    }
+    const uint32_t run = (more + kWarps - 1) / kWarps;
+    const uint32_t a = min(more, warp * run), b = min(more, a + run);
+    const uint64_t step = (uint64_t)p.slices * kSlice, at = (uint64_t)slice * kSlice + lane * kChunk;
+    float acc[kChunk] = {};
+    if (warp == 0) {
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) acc[j] = p.tail[tile * step + at + j];
+    }
+#pragma unroll 4
+    for (uint32_t t = a; t < b; ++t) {
+      const float4 *from = reinterpret_cast<const float4 *>(p.head + (tile + 1 + t) * step + at);
+      const float4 x = from[0], y = from[1];
+      acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+      acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+    }
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) sums[warp][lane * kChunk + j] = acc[j];
+    __syncthreads();
+    if (warp == 0) {
+      W *row = static_cast<W *>(p.dtable) + (int64_t)key * p.D;
+      const int64_t c = (int64_t)(slice * 32 + lane) * kChunk - lead_of<W, kWhole>(row);
+      for (int w = 1; w < kWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) acc[j] += sums[w][lane * kChunk + j];
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) acc[j] *= p.scale;
+      if (c < p.D) store_columns<W, kWhole>(row, c, p.D, narrow<W>(acc));
+    }
+    __syncthreads();
+  }
+}
+
+// ---- launches ------------------------------------------------------------------------
+uint64_t rounded(uint64_t bytes) { return (bytes + 255) / 256 * 256; }
+uint32_t tiles_of(uint32_t N) { return (uint32_t)(((uint64_t)N + kTile - 1) / kTile); }
+
+struct Layout {
+  uint64_t sorted, used, counter, open, partial, keys, bytes;
+};
+Layout layout_of(uint32_t N, uint32_t V, uint32_t D) {
+  const uint64_t tiles = tiles_of(N);
+  const uint64_t columns = ((uint64_t)chunks_of(D, false) + 31) / 32 * kSlice;
+  Layout l = {};
+  l.sorted = 0;
+  l.used = l.sorted + rounded((uint64_t)N * sizeof(Sorted));
+  l.counter = l.used + rounded((uint64_t)V + 16);
+  l.open = l.counter + 256;
+  l.partial = l.open + rounded(tiles * 4);
+  l.keys = l.partial + 2 * tiles * columns * sizeof(float);
+  l.bytes = l.keys + rounded(order_tokens_workspace(N, V));
+  return l;
+}
+
+template <class W, class E>
+cudaError_t forward_of(EmbedParams &p, cudaStream_t st) {
+  const bool whole = whole_rows(p.table, p.table_row, p.D, sizeof(W)) &&
+                     whole_rows(p.y, p.D, p.D, sizeof(E));
+  const uint32_t chunks = chunks_of(p.D, whole);
+  p.lanes = 1;
+  while (p.lanes < 32 && p.lanes < chunks) p.lanes *= 2;
+  p.slices = (chunks + p.lanes * kUnroll - 1) / (p.lanes * kUnroll);
+  const uint32_t each = kThreads / p.lanes;
+  ++launch_counter();
+  auto *k = whole ? embed_kernel<W, E, true> : embed_kernel<W, E, false>;
+  k<<<(uint32_t)(((uint64_t)p.N * p.slices + each - 1) / each), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <class W, class E>
+cudaError_t backward_of(EmbedParams &p, void *workspace, cudaStream_t st) {
+  const bool whole = whole_rows(p.dy, p.dy_row, p.D, sizeof(E)) &&
+                     whole_rows(p.dtable, p.D, p.D, sizeof(W));
+  char *ws = static_cast<char *>(workspace);
+  const Layout l = layout_of(p.N, p.V, p.D);
+  Sorted *sorted = reinterpret_cast<Sorted *>(ws + l.sorted);
+  uint8_t *used = reinterpret_cast<uint8_t *>(ws + l.used);
+  p.sorted = sorted, p.used = used;
+  p.counter = reinterpret_cast<uint32_t *>(ws + l.counter);
+  p.open = reinterpret_cast<uint32_t *>(ws + l.open);
+  p.slices = (chunks_of(p.D, whole) + 31) / 32;
+  p.tiles = tiles_of(p.N);
+  p.head = reinterpret_cast<float *>(ws + l.partial);
+  p.tail = p.head + (uint64_t)p.tiles * p.slices * kSlice;
+  cudaError_t e = launch_order_tokens({p.tokens, p.doc, p.N, p.V, p.wide != 0}, sorted, used,
+                                      p.counter, ws + l.keys, st);
+  if (e != cudaSuccess) return e;
+  p.sum_blocks = (uint32_t)(((uint64_t)p.tiles * p.slices + kWarps - 1) / kWarps);
+  const uint32_t zero = (p.V + 31) / 32;
+  launch_counter() += 2;
+  pdl_launch(whole ? embed_sum_kernel<W, E, true> : embed_sum_kernel<W, E, false>,
+             dim3(p.sum_blocks + zero), dim3(kThreads), 0, st, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const uint64_t most = (uint64_t)p.tiles * p.slices;
+  pdl_launch(whole ? embed_join_kernel<W, true> : embed_join_kernel<W, false>,
+             dim3((uint32_t)std::min<uint64_t>(most ? most : 1, 4 * 152)), dim3(kThreads), 0, st, p);
+  return cudaGetLastError();
+}
+
+template <class W>
+cudaError_t forward_by(EmbedParams &p, int32_t dtype, cudaStream_t st) {
+  switch (dtype) {
+    case NS_F32: return forward_of<W, float>(p, st);
+    case NS_BF16: return forward_of<W, __nv_bfloat16>(p, st);
+    default: return forward_of<W, __half>(p, st);
+  }
+}
+template <class W>
+cudaError_t backward_by(EmbedParams &p, int32_t dtype, void *ws, cudaStream_t st) {
+  switch (dtype) {
+    case NS_F32: return backward_of<W, float>(p, ws, st);
+    case NS_BF16: return backward_of<W, __nv_bfloat16>(p, ws, st);
+    default: return backward_of<W, __half>(p, ws, st);
+  }
+}
+
+EmbedParams params_of(const ns_embed_inputs &in) {
+  EmbedParams p = {};
+  p.tokens = in.tokens, p.doc = in.doc, p.N = in.N, p.V = in.V, p.D = in.D;
+  p.wide = in.ids_64 != 0, p.scale = in.scale;
+  return p;
+}
+
+}  // namespace
+
+uint64_t embed_workspace(uint32_t N, uint32_t V, uint32_t D) { return layout_of(N, V, D).bytes; }
+
+cudaError_t launch_embed_forward(const ns_embed_inputs &in, const void *table, int64_t table_row,
+                                 void *y, cudaStream_t st) {
+  EmbedParams p = params_of(in);
+  p.table = table, p.table_row = table_row, p.y = y;
+  switch (in.table_dtype) {
+    case NS_F32: return forward_by<float>(p, in.dtype, st);
+    case NS_BF16: return forward_by<__nv_bfloat16>(p, in.dtype, st);
+    default: return forward_by<__half>(p, in.dtype, st);
+  }
+}
+
+cudaError_t launch_embed_backward(const ns_embed_inputs &in, const void *dy, int64_t dy_row,
+                                  void *dtable, void *workspace, cudaStream_t st) {
+  EmbedParams p = params_of(in);
+  p.dy = dy, p.dy_row = dy_row, p.dtable = dtable;
+  switch (in.table_dtype) {
+    case NS_F32: return backward_by<float>(p, in.dtype, workspace, st);
+    case NS_BF16: return backward_by<__nv_bfloat16>(p, in.dtype, workspace, st);
+    default: return backward_by<__half>(p, in.dtype, workspace, st);
+  }
+}
+
+}  // namespace nsk

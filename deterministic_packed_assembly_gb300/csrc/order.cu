@@ -1,0 +1,240 @@
+// A stable sort of small whole numbers by counting: one pass a digit, the lowest first.
+//
+// Two kernels a pass.  The first counts the digits of each block's stretch of keys
+// (R counters a block).  In the second every block adds up the counters of all
+// blocks itself (at most 152 x R words, from the L2 cache: a kernel between the two would
+// cost its launch), so that it knows where its own keys of each digit go; a warp
+// takes a contiguous part of the stretch, 32 keys at a time, and its lanes with the same
+// digit rank themselves by a match.  Counts are whole numbers: atomics in shared memory do
+// not change them, and equal keys keep their order.
+//
+// What bounds it is latency: two launches and some trips to the L2 cache a pass.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "order.h"
+#include "train.h"
+
+namespace nsk {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr uint32_t kMostBlocks = 152;
+constexpr uint32_t kNone = 0xffffffffu;
+
+struct Pass {
+  Keys keys;
+  const Sorted *from;  // the pass before's, or null: the keys themselves
+  Sorted *to;          // or null: place and slots
+  int32_t *place, *slots, *offsets;
+  uint8_t *used;       // first pass
+  uint32_t *counter;
+  uint32_t *table;     // [blocks][R]
+  uint32_t R, shift, mask, stretch;
+};
+
+__device__ __forceinline__ Sorted key_at(const Pass &p, uint32_t i) {
+  if (p.from) return p.from[i];
+  const int64_t id = p.keys.wide ? static_cast<const int64_t *>(p.keys.ids)[i]
+                                 : static_cast<const int32_t *>(p.keys.ids)[i];
+  const bool there =
+      id >= 0 && id < (int64_t)p.keys.limit && !(p.keys.doc && p.keys.doc[i] < 0);
+  return {there ? (uint32_t)id : p.keys.limit, i};
+}
+
+__global__ void __launch_bounds__(kThreads) count_kernel(const Pass p) {
+  extern __shared__ uint32_t count[];
+  for (uint32_t d = threadIdx.x; d < p.R; d += kThreads) count[d] = 0;
+  pdl_wait_then_release();
+  if (p.used) {
+    const uint32_t pieces = p.keys.limit / 16 + 1;
+    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < pieces; i += gridDim.x * kThreads)
+      reinterpret_cast<uint4 *>(p.used)[i] = make_uint4(0, 0, 0, 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
+  }
+  __syncthreads();
+  const uint32_t begin = blockIdx.x * p.stretch;
+  const uint32_t end = min(p.keys.N, begin + p.stretch);
+  for (uint32_t i = begin + threadIdx.x; i < end; i += kThreads)
+    atomicAdd(&count[(key_at(p, i).key >> p.shift) & p.mask], 1u);
+  __syncthreads();
+  for (uint32_t d = threadIdx.x; d < p.R; d += kThreads)
+    p.table[(uint64_t)blockIdx.x * p.R + d] = count[d];
+}
+
+__global__ void __launch_bounds__(kThreads) place_kernel(const Pass p) {
+  extern __shared__ uint32_t shared[];
+  uint32_t *total = shared;              // [R]: of all blocks, then the digits before
+  uint32_t *before = total + p.R;        // [R]: of the blocks before this one
+  uint32_t *start = before + p.R;        // [kWarps][R]
+  __shared__ uint32_t sums[kWarps];
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (uint32_t d = threadIdx.x; d < (2 + kWarps) * p.R; d += kThreads) shared[d] = 0;
+  __syncthreads();
+  pdl_wait_then_release();
+
+  // this warp's own digits
+  const uint32_t part = p.stretch / kWarps;
+  const uint32_t begin = min(p.keys.N, blockIdx.x * p.stretch + warp * part);
+  const uint32_t end = min(p.keys.N, begin + part);
+  uint32_t *mine = start + warp * p.R;
+  for (uint32_t i = begin + lane; i < end; i += 32) {
+    const uint32_t key = key_at(p, i).key;
+    atomicAdd(&mine[(key >> p.shift) & p.mask], 1u);
+    if (p.used && key < p.keys.limit) p.used[key] = 1;
+  }
+  // all blocks' counters: neighbouring threads take neighbouring digits, groups of them
+  // share the blocks
+  const uint32_t wide = p.R < kThreads ? p.R : kThreads, groups = kThreads / wide;
+  const uint32_t group = threadIdx.x / wide;
+  if (group < groups) {
+    for (uint32_t d = threadIdx.x % wide; d < p.R; d += wide) {
+      uint32_t all = 0, ahead = 0;
+#pragma unroll 8
+      for (uint32_t b = group; b < gridDim.x; b += groups) {
+        const uint32_t c = p.table[(uint64_t)b * p.R + d];
+        all += c;
+        ahead += b < blockIdx.x ? c : 0;
+      }
+      atomicAdd(&total[d], all);
+      atomicAdd(&before[d], ahead);
+    }
+  }
+  __syncthreads();
+  // digits before: each thread has a run of them
+  const uint32_t run = (p.R + kThreads - 1) / kThreads;
+  const uint32_t d0 = min(p.R, threadIdx.x * run), d1 = min(p.R, d0 + run);
+  uint32_t sum = 0;
+  for (uint32_t d = d0; d < d1; ++d) sum += total[d];
+  uint32_t scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= (uint32_t)o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  uint32_t base = scan - sum;
+  for (uint32_t w = 0; w < warp; ++w) base += sums[w];
+  for (uint32_t d = d0; d < d1; ++d) {
+    const uint32_t n = total[d];
+    if (p.offsets && blockIdx.x == 0) p.offsets[d] = (int32_t)base;
+    uint32_t at = base + before[d];
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t c = start[w * p.R + d];
+      start[w * p.R + d] = at;
+      at += c;
+    }
+    base += n;
+  }
+  __syncthreads();
+
+  for (uint32_t i0 = begin; i0 < end; i0 += 32) {
+    const uint32_t i = i0 + lane;
+    Sorted s = {kNone, 0};
+    if (i < end) s = key_at(p, i);
+    const uint32_t d = i < end ? (s.key >> p.shift) & p.mask : kNone;
+    const uint32_t same = __match_any_sync(0xffffffffu, d);
+    const uint32_t rank = __popc(same & ((1u << lane) - 1));
+    uint32_t at = 0;
+    if (i < end) at = mine[d] + rank;
+    __syncwarp();
+    if (i < end && rank == 0) mine[d] += __popc(same);
+    __syncwarp();
+    if (i < end) {
+      if (p.to) {
+        p.to[at] = s;
+      } else {
+        p.place[i] = (int32_t)at;
+        p.slots[at] = (int32_t)i;
+      }
+    }
+  }
+}
+
+// Keys of a block's stretch: as few blocks as fill the SMs, a multiple of 32 a warp.
+uint32_t stretch_of(uint32_t N) {
+  const uint32_t each = (N + kMostBlocks - 1) / kMostBlocks;
+  return std::max<uint32_t>(1, (each + kThreads - 1) / kThreads) * kThreads;
+}
+uint32_t blocks_of(uint32_t N) {
+  const uint32_t s = stretch_of(N);
+  return std::max<uint32_t>(1, (N + s - 1) / s);
+}
+
+cudaError_t launch_pass(const Pass &p, bool first, cudaStream_t st) {
+  const uint32_t blocks = blocks_of(p.keys.N);
+  const size_t shared = (2 + kWarps) * (size_t)p.R * sizeof(uint32_t);
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void *>(place_kernel));
+  if (e != cudaSuccess) return e;
+  launch_counter() += 2;
+  if (first)
+    count_kernel<<<blocks, kThreads, p.R * sizeof(uint32_t), st>>>(p);
+  else
+    pdl_launch(count_kernel, dim3(blocks), dim3(kThreads), p.R * sizeof(uint32_t), st, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  pdl_launch(place_kernel, dim3(blocks), dim3(kThreads), shared, st, p);
+  return cudaGetLastError();
+}
+
+// Digits of the keys 0 to limit: passes of at most nine bits.
+struct Digits {
+  uint32_t passes, bits;
+};
+Digits digits_of(uint32_t limit) {
+  uint32_t bits = 1;
+  while (bits < 32 && (limit >> bits)) ++bits;
+  const uint32_t passes = (bits + 8) / 9;
+  return {passes, (bits + passes - 1) / passes};
+}
+uint64_t rounded(uint64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+}  // namespace
+
+uint64_t order_choices_workspace(uint32_t N, uint32_t limit) {
+  return (uint64_t)blocks_of(N) * (limit + 1) * sizeof(uint32_t);
+}
+
+cudaError_t launch_order_choices(const Keys &keys, int32_t *place, int32_t *slots,
+                                 int32_t *offsets, void *workspace, cudaStream_t st) {
+  Pass p = {};
+  p.keys = keys, p.place = place, p.slots = slots, p.offsets = offsets;
+  p.table = static_cast<uint32_t *>(workspace);
+  p.R = keys.limit + 1, p.shift = 0, p.mask = kNone, p.stretch = stretch_of(keys.N);
+  return launch_pass(p, true, st);
+}
+
+uint64_t order_tokens_workspace(uint32_t N, uint32_t limit) {
+  const Digits d = digits_of(limit);
+  return rounded((uint64_t)blocks_of(N) * (1u << d.bits) * sizeof(uint32_t)) +
+         (d.passes > 1 ? (uint64_t)N * sizeof(Sorted) : 0);
+}
+
+cudaError_t launch_order_tokens(const Keys &keys, Sorted *sorted, uint8_t *used,
+                                uint32_t *counter, void *workspace, cudaStream_t st) {
+  const Digits d = digits_of(keys.limit);
+  Sorted *other = reinterpret_cast<Sorted *>(
+      static_cast<char *>(workspace) +
+      rounded((uint64_t)blocks_of(keys.N) * (1u << d.bits) * sizeof(uint32_t)));
+  Pass p = {};
+  p.keys = keys, p.table = static_cast<uint32_t *>(workspace);
+  p.R = 1u << d.bits, p.mask = p.R - 1, p.stretch = stretch_of(keys.N);
+  for (uint32_t i = 0; i < d.passes; ++i) {
+    p.shift = i * d.bits;
+    p.from = i == 0 ? nullptr : p.to;
+    p.to = (d.passes - i) % 2 ? sorted : other;  // the last pass writes `sorted`
+    p.used = i == 0 ? used : nullptr, p.counter = counter;
+    const cudaError_t e = launch_pass(p, i == 0, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace nsk

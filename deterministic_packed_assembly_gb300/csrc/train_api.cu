@@ -183,4 +183,148 @@ int ns_route_backward(const ns_route_inputs *in, const int32_t *ids, const float
                                          dlogits, static_cast<cudaStream_t>(cuda_stream)));
 }
 
+// ---- rows of a table -------------------------------------------------------------
+// Strides of rows of D elements, where there is more than one row.
+static bool fits_row(int64_t row, uint32_t D, uint32_t N) {
+  return N <= 1 || (row >= (int64_t)D && row <= ((int64_t)1 << 44));
+}
+
+static bool check_embed(const ns_embed_inputs *in) {
+  if (!in || !size_of(in->table_dtype) || !size_of(in->dtype)) return false;
+  if (in->N >= (1u << 31) || in->V >= (1u << 31) || in->D >= (1u << 31)) return false;
+  // blocks of a launch, and bytes of a workspace: past any memory long before
+  if ((uint64_t)in->N * in->D >= (1ull << 42) || (uint64_t)in->V * in->D >= (1ull << 42))
+    return false;
+  if (!std::isfinite(in->scale)) return false;
+  return usable(in->tokens, in->ids_64 ? 8 : 4, in->N == 0) && usable(in->doc, 4, true);
+}
+
+int ns_embed_forward(const ns_embed_inputs *in, const void *table, int64_t table_row, void *y,
+                     void *cuda_stream) {
+  if (!check_embed(in) || !fits_row(table_row, in->D, in->V)) return NS_ERR_INVALID_ARG;
+  if (in->N == 0 || in->D == 0) return NS_OK;
+  if (!usable(table, size_of(in->table_dtype), in->V == 0) || !usable(y, size_of(in->dtype)))
+    return NS_ERR_INVALID_ARG;
+  return done(nsk::launch_embed_forward(*in, table, table_row, y,
+                                        static_cast<cudaStream_t>(cuda_stream)));
+}
+
+uint64_t ns_embed_workspace(uint32_t N, uint32_t V, uint32_t D) {
+  if (N >= (1u << 31) || V >= (1u << 31) || D >= (1u << 31) || (uint64_t)N * D >= (1ull << 42))
+    return 0;
+  return nsk::embed_workspace(N, V, D);
+}
+
+int ns_embed_backward(const ns_embed_inputs *in, const void *dy, int64_t dy_row, void *dtable,
+                      void *workspace, void *cuda_stream) {
+  if (!check_embed(in) || !fits_row(dy_row, in->D, in->N)) return NS_ERR_INVALID_ARG;
+  if (in->V == 0 || in->D == 0) return NS_OK;
+  if (!usable(dy, size_of(in->dtype), in->N == 0) || !usable(dtable, size_of(in->table_dtype)) ||
+      !usable(workspace, 16))
+    return NS_ERR_INVALID_ARG;
+  return done(nsk::launch_embed_backward(*in, dy, dy_row, dtable, workspace,
+                                         static_cast<cudaStream_t>(cuda_stream)));
+}
+
+// ---- layer norm ------------------------------------------------------------------
+static bool check_norm(const ns_norm_inputs *in) {
+  if (!in || !size_of(in->dtype) ||
+      (in->weight_dtype != NS_F32 && in->weight_dtype != in->dtype))
+    return false;
+  if (in->N >= (1u << 31) || in->D == 0 || in->D >= (1u << 30)) return false;
+  if (!(in->eps >= 0.0f) || !std::isfinite(in->eps)) return false;
+  if (!fits_row(in->x_row, in->D, in->N)) return false;
+  const uint64_t es = size_of(in->dtype), ws = size_of(in->weight_dtype);
+  return usable(in->x, es, in->N == 0) && usable(in->weight, ws, true) &&
+         usable(in->bias, ws, true) && usable(in->doc, 4, true);
+}
+
+int ns_norm_forward(const ns_norm_inputs *in, void *y, float *mean, float *rstd,
+                    void *cuda_stream) {
+  if (!check_norm(in)) return NS_ERR_INVALID_ARG;
+  if (in->N == 0) return NS_OK;
+  if (!usable(y, size_of(in->dtype)) || !usable(mean, 4, true) || !usable(rstd, 4, true))
+    return NS_ERR_INVALID_ARG;
+  return done(
+      nsk::launch_norm_forward(*in, y, mean, rstd, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+uint64_t ns_norm_workspace(uint32_t N, uint32_t D) {
+  return N < (1u << 31) && D < (1u << 30) ? nsk::norm_workspace(N, D) : 0;
+}
+
+int ns_norm_backward(const ns_norm_inputs *in, const float *mean, const float *rstd,
+                     const void *dy, int64_t dy_row, void *dx, void *dweight, void *dbias,
+                     void *workspace, void *cuda_stream) {
+  if (!check_norm(in) || !fits_row(dy_row, in->D, in->N)) return NS_ERR_INVALID_ARG;
+  const uint64_t es = size_of(in->dtype), ws = size_of(in->weight_dtype);
+  const bool none = in->N == 0;
+  if (!usable(mean, 4, none) || !usable(rstd, 4, none) || !usable(dy, es, none) ||
+      !usable(dx, es, none) || !usable(dweight, ws, true) || !usable(dbias, ws, true) ||
+      !usable(workspace, 4, none || (!dweight && !dbias)))
+    return NS_ERR_INVALID_ARG;
+  return done(nsk::launch_norm_backward(*in, mean, rstd, dy, dy_row, dx, dweight, dbias,
+                                        static_cast<float *>(workspace),
+                                        static_cast<cudaStream_t>(cuda_stream)));
+}
+
+// ---- tokens by expert, and back ----------------------------------------------------
+static bool check_experts(const ns_expert_sizes *s) {
+  return s && size_of(s->dtype) && s->k >= 1 && s->E >= 1 && s->E <= NS_DISPATCH_MAX_EXPERTS &&
+         (uint64_t)s->N * s->k < (1ull << 31) && s->D < (1u << 30) &&
+         (uint64_t)s->N * s->k * s->D < (1ull << 42);
+}
+
+uint64_t ns_dispatch_workspace(uint32_t N, uint32_t k, uint32_t E) {
+  if (k == 0 || E == 0 || E > NS_DISPATCH_MAX_EXPERTS || (uint64_t)N * k >= (1ull << 31)) return 0;
+  return nsk::dispatch_workspace(N, k, E);
+}
+
+int ns_dispatch(const ns_expert_sizes *sizes, const int32_t *ids, const void *x, int64_t x_row,
+                int32_t *place, int32_t *slots, int32_t *offsets, void *rows, void *workspace,
+                void *cuda_stream) {
+  if (!check_experts(sizes) || !fits_row(x_row, sizes->D, sizes->N)) return NS_ERR_INVALID_ARG;
+  const uint64_t es = size_of(sizes->dtype);
+  const bool none = sizes->N == 0, nothing = none || sizes->D == 0;
+  if (!usable(ids, 4, none) || !usable(x, es, nothing) || !usable(place, 4, none) ||
+      !usable(slots, 4, none) || !usable(offsets, 4) || !usable(rows, es, nothing) ||
+      !usable(workspace, 4, ns_dispatch_workspace(sizes->N, sizes->k, sizes->E) == 0))
+    return NS_ERR_INVALID_ARG;
+  return done(nsk::launch_dispatch(*sizes, ids, x, x_row, place, slots, offsets, rows, workspace,
+                                   static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int ns_combine(const ns_expert_sizes *sizes, const int32_t *place, const int32_t *offsets,
+               const float *weights, const void *rows, int64_t rows_row, void *out,
+               void *cuda_stream) {
+  if (!check_experts(sizes) || !fits_row(rows_row, sizes->D, sizes->N * sizes->k))
+    return NS_ERR_INVALID_ARG;
+  if (sizes->N == 0 || sizes->D == 0) return NS_OK;
+  const uint64_t es = size_of(sizes->dtype);
+  if (!usable(place, 4) || !usable(offsets, 4) || !usable(weights, 4, true) ||
+      !usable(rows, es) || !usable(out, es))
+    return NS_ERR_INVALID_ARG;
+  return done(nsk::launch_combine(*sizes, place, offsets, weights, rows, rows_row, out,
+                                  static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int ns_combine_backward(const ns_expert_sizes *sizes, const int32_t *place,
+                        const int32_t *offsets, const float *weights, const void *rows,
+                        int64_t rows_row, const void *d_out, int64_t d_out_row, void *d_rows,
+                        float *d_weights, void *cuda_stream) {
+  if (!check_experts(sizes) || !fits_row(d_out_row, sizes->D, sizes->N) ||
+      (d_weights && !fits_row(rows_row, sizes->D, sizes->N * sizes->k)))
+    return NS_ERR_INVALID_ARG;
+  if (sizes->N == 0) return NS_OK;
+  const uint64_t es = size_of(sizes->dtype);
+  const bool nothing = sizes->D == 0;
+  if (!usable(place, 4) || !usable(offsets, 4) || !usable(weights, 4, true) ||
+      !usable(rows, es, nothing || !d_weights) || !usable(d_out, es, nothing) ||
+      !usable(d_rows, es, nothing) || !usable(d_weights, 4, true))
+    return NS_ERR_INVALID_ARG;
+  return done(nsk::launch_combine_backward(*sizes, place, offsets, weights, rows, rows_row, d_out,
+                                           d_out_row, d_rows, d_weights,
+                                           static_cast<cudaStream_t>(cuda_stream)));
+}
+
 }  // extern "C"

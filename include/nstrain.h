@@ -15,7 +15,14 @@
  *    positions, and its gradient in the same pass;
  *  - ns_route_forward / ns_route_backward: a router's choice of experts, the
  *    experts' counts and the balance loss over the real positions, and the
- *    logits' gradient.
+ *    logits' gradient;
+ *  - ns_embed_forward / ns_embed_backward: rows of a table at the tokens, and
+ *    the table's gradient over the real positions;
+ *  - ns_norm_forward / ns_norm_backward: the layer norm of the real positions,
+ *    and its gradients;
+ *  - ns_dispatch, ns_combine / ns_combine_backward: tokens sorted by the
+ *    experts that a router chose, and the experts' rows brought back with the
+ *    router's weights.
  *
  * Conventions:
  *  - Every argument is checked on the host before anything is enqueued; a
@@ -31,8 +38,8 @@
  *  - Every sum is taken in a fixed order: the same arguments give the same
  *    bits, on every call and every stream.  What a row (of a scan, of logits)
  *    gets does not depend on the other rows of the call; the order of a sum
- *    over rows (dbias, the balance loss) depends on the sizes and on the
- *    alignment of the arrays.
+ *    over rows (dbias, the balance loss, a table's gradient) depends on the
+ *    sizes, on the alignment of the arrays and, for the table, on the tokens.
  *  - Values at padded or unlearned positions are never used, whatever they
  *    are (NaN and infinities among them); the outputs there are 0 (-1 for
  *    expert ids).
@@ -187,6 +194,123 @@ int ns_route_forward(const ns_route_inputs *in, int32_t *ids, float *weights, in
 int ns_route_backward(const ns_route_inputs *in, const int32_t *ids, const float *weights,
                       const int32_t *counts, const int32_t *tokens, const float *d_weights,
                       const float *d_loss, void *dlogits, void *cuda_stream);
+
+/* ---- rows of a table ------------------------------------------------------------
+ * Position n has the token t_n and the row
+ *   y[n] = scale table[t_n];   dtable[v] = scale sum_{n: t_n = v} dy[n]
+ * A position with doc[n] < 0, or whose token is outside [0, V), has y[n] = 0
+ * and no part in the gradient.  The table's rows are strided (in elements), its
+ * gradient and y are contiguous, [V][D] and [N][D].  Each sum is taken in 32
+ * bits over the positions in ascending order, in runs of up to 32 positions
+ * that the sorted order of all tokens fixes, and rounded once; rows of tokens
+ * that are not there are 0. */
+typedef struct {
+  const void *tokens;  /* [N] int32, or int64 where ids_64 != 0 */
+  const int32_t *doc;  /* [N] or NULL */
+  uint32_t N, V, D;    /* each < 2^31 */
+  int32_t table_dtype; /* of the table and of its gradient */
+  int32_t dtype;       /* of y and dy */
+  int32_t ids_64;
+  float scale;         /* finite */
+} ns_embed_inputs;
+
+/* Errors: INVALID_ARG (a needed pointer NULL or misaligned, an unknown type, a
+ * stride below D, sizes or scale out of range), CUDA. */
+int ns_embed_forward(const ns_embed_inputs *in, const void *table, int64_t table_row, void *y,
+                     void *cuda_stream);
+
+/* Bytes of the workspace of ns_embed_backward for these sizes. */
+uint64_t ns_embed_workspace(uint32_t N, uint32_t V, uint32_t D);
+
+/* dtable from dy (rows of D, strided).  It may not overlap dy.  workspace:
+ * ns_embed_workspace bytes, 16-byte aligned.  Errors: as ns_embed_forward. */
+int ns_embed_backward(const ns_embed_inputs *in, const void *dy, int64_t dy_row, void *dtable,
+                      void *workspace, void *cuda_stream);
+
+/* ---- layer norm -------------------------------------------------------------------
+ *   mean = the mean of x over D,  rstd = 1 / sqrt(the mean of (x - mean)^2 + eps)
+ *   y = (x - mean) rstd weight + bias
+ * for every row x of D channels.  Where doc[n] < 0, y, mean and rstd are 0, and
+ * so is the row's gradient; it has no part in those of weight and bias.  x is
+ * [N][D], its rows strided (in elements); y, dx are contiguous.  weight and bias
+ * ([D], either may be NULL: 1 and 0) are of weight_dtype, which is NS_F32 or
+ * dtype. */
+typedef struct {
+  const void *x;
+  int64_t x_row;
+  const void *weight;  /* [D] or NULL */
+  const void *bias;    /* [D] or NULL */
+  const int32_t *doc;  /* [N] or NULL */
+  uint32_t N, D;       /* N < 2^31, 1 <= D < 2^30 */
+  int32_t dtype;       /* of x, y and their gradients */
+  int32_t weight_dtype;
+  float eps;           /* >= 0, finite */
+} ns_norm_inputs;
+
+/* mean and rstd ([N], for the backward pass) may be NULL.  No output may overlap
+ * an input.  Errors: INVALID_ARG (a needed pointer NULL or misaligned, unknown
+ * types, a stride below D, sizes or eps out of range), CUDA. */
+int ns_norm_forward(const ns_norm_inputs *in, void *y, float *mean, float *rstd,
+                    void *cuda_stream);
+
+/* Bytes of the workspace of ns_norm_backward for these sizes. */
+uint64_t ns_norm_workspace(uint32_t N, uint32_t D);
+
+/* The gradients from dy (rows strided), with what the forward pass wrote:
+ *   g = dy weight, h = (x - mean) rstd
+ *   dx = rstd (g - mean of g - h mean of (g h)),  dweight = sum dy h,  dbias = sum dy
+ * dweight and dbias ([D], of weight_dtype) may be NULL.  No output may overlap an
+ * input.  workspace: ns_norm_workspace bytes, 4-byte aligned, or NULL where
+ * dweight and dbias are.  in->bias is not used.  Errors: as ns_norm_forward. */
+int ns_norm_backward(const ns_norm_inputs *in, const float *mean, const float *rstd,
+                     const void *dy, int64_t dy_row, void *dx, void *dweight, void *dbias,
+                     void *workspace, void *cuda_stream);
+
+/* ---- tokens by expert, and back ------------------------------------------------------
+ * Token n has chosen the experts ids[n][0..k) (as ns_route_forward writes them;
+ * outside [0, E): none).  Its choice j is number n k + j, and the choices are
+ * sorted by expert, in the order of their numbers, those without one last:
+ *   place[n][j]  the choice's place among all N k;  slots[place] its number
+ *   offsets[e]   the choices before expert e's;  M = offsets[E] choices in all
+ *   rows[place[n][j]] = x[n];  rows from M on are 0
+ * so that expert e's rows are [offsets[e], offsets[e + 1]).  x is [N][D], its
+ * rows strided (in elements); rows is contiguous [N k][D]. */
+#define NS_DISPATCH_MAX_EXPERTS 1024u
+typedef struct {
+  uint32_t N, k, E, D; /* N k < 2^31, k >= 1, 1 <= E <= NS_DISPATCH_MAX_EXPERTS, D < 2^30 */
+  int32_t dtype;       /* of the rows */
+} ns_expert_sizes;
+
+/* Bytes of the workspace of ns_dispatch for these sizes (0: none, or sizes that it
+ * refuses). */
+uint64_t ns_dispatch_workspace(uint32_t N, uint32_t k, uint32_t E);
+
+/* place, slots: [N k]; offsets: [E + 1].  workspace: 4-byte aligned, or NULL for
+ * none.  No output may overlap an input.  Errors: INVALID_ARG (a needed pointer
+ * NULL or misaligned, an unknown type, a stride below D, sizes out of range),
+ * CUDA. */
+int ns_dispatch(const ns_expert_sizes *sizes, const int32_t *ids, const void *x, int64_t x_row,
+                int32_t *place, int32_t *slots, int32_t *offsets, void *rows, void *workspace,
+                void *cuda_stream);
+
+/* out[n] = sum_j weights[n][j] rows[place[n][j]] over the choices that have an
+ * expert (place < M), in 32 bits, in the order of j, rounded once.  weights [N][k]
+ * or NULL (1).  rows is [N k][D], its rows strided; those from M on are not read;
+ * out is contiguous.  Without weights this is the gradient of ns_dispatch's x from
+ * that of its rows.  Errors: as ns_dispatch. */
+int ns_combine(const ns_expert_sizes *sizes, const int32_t *place, const int32_t *offsets,
+               const float *weights, const void *rows, int64_t rows_row, void *out,
+               void *cuda_stream);
+
+/* The gradients of ns_combine from d_out ([N][D], rows strided):
+ *   d_rows[place[n][j]] = weights[n][j] d_out[n], 0 from M on  (contiguous [N k][D])
+ *   d_weights[n][j] = the dot product of d_out[n] and rows[place[n][j]], 0 without an expert
+ * d_weights may be NULL; rows may be then.  No output may overlap an input.
+ * Errors: as ns_dispatch. */
+int ns_combine_backward(const ns_expert_sizes *sizes, const int32_t *place,
+                        const int32_t *offsets, const float *weights, const void *rows,
+                        int64_t rows_row, const void *d_out, int64_t d_out_row, void *d_rows,
+                        float *d_weights, void *cuda_stream);
 
 #ifdef __cplusplus
 }
