@@ -3,7 +3,8 @@
 One process, one GPU: ``Packer.step`` assembles an update's rows, and the model's
 operators take its arrays as they are:
 
-    tokens -> embedding -> gated_scan (pos, doc) -> route (doc) -> experts
+    tokens -> embed (doc) -> layer_norm (doc) -> gated_scan (pos, doc)
+           -> layer_norm (doc) -> route (doc) -> dispatch -> experts -> combine
            -> logits -> distill_loss (mask) -> gradients
 
 The corpus is the synthetic two-source one, the weights are random, and the
@@ -31,7 +32,8 @@ class Model(torch.nn.Module):
     def __init__(self, vocab: int, width: int = 256, experts: int = 8, chosen: int = 2):
         super().__init__()
         self.chosen = chosen
-        self.embed = torch.nn.Embedding(vocab, width)
+        self.embed = torch.nn.Parameter(torch.randn(vocab, width))
+        self.norms = torch.nn.ParameterList(torch.full((width,), float(i % 2 == 0)) for i in range(4))
         self.mix = torch.nn.Linear(width, 2 * width)
         self.forget = torch.nn.Parameter(torch.linspace(0.0, 5.0, width))  # short memories to long
         self.router = torch.nn.Linear(width, experts, bias=False)
@@ -40,15 +42,20 @@ class Model(torch.nn.Module):
 
     def forward(self, tokens, pos, doc):
         B, T = tokens.shape
-        x = self.embed(tokens)
-        z, f = self.mix(x).chunk(2, dim=-1)  # halves of one projection, taken as they lie
+        w1, b1, w2, b2 = self.norms
+        x = nsp.embed(self.embed, tokens, doc=doc)
+        z, f = self.mix(nsp.layer_norm(x, w1, b1, doc=doc)).chunk(2, dim=-1)  # as they lie
         y, _ = nsp.gated_scan(z, f, self.forget, pos=pos, doc=doc)
         x = (x + y).reshape(B * T, -1)
-        r = nsp.route(self.router(x), self.chosen, doc=doc.reshape(-1))
-        # the few small experts are all computed; a large model would gather by r.ids
-        share = torch.zeros(B * T, self.experts.shape[0], device=x.device)
-        share = share.scatter_add(1, r.ids.clamp(min=0).long(), r.weights)
-        x = x + torch.einsum("ne,nd,edk->nk", share, x, self.experts).tanh()
+        doc = doc.reshape(-1)
+        n = nsp.layer_norm(x, w2, b2, doc=doc)
+        r = nsp.route(self.router(n), self.chosen, doc=doc)
+        rows, order = nsp.dispatch(n, r.ids, len(self.experts))
+        # each expert's rows; the counts go to the host once a step, rows without an expert last
+        counts = r.counts.tolist()
+        parts = rows.split([*counts, len(rows) - sum(counts)])
+        done = [part @ expert for part, expert in zip(parts, self.experts)]
+        x = x + nsp.combine(torch.cat([*done, parts[-1]]).tanh(), order, r.weights)
         return self.head(x), r
 
 
