@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -30,9 +31,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
+constexpr int kCopied = 4;                     // spans of a unit (rows.cuh)
 constexpr uint32_t kTile = 32;                 // positions of a tile
-constexpr uint32_t kSlice = 32 * kChunk;       // columns of a warp
+constexpr uint32_t kSlice = 32 * kOct;         // columns of a warp
 constexpr uint32_t kBefore = 0xffffffffu, kBehind = 0xfffffffeu;
 
 struct EmbedParams {
@@ -60,7 +61,7 @@ struct EmbedParams {
 };
 
 // ---- forward ------------------------------------------------------------------------
-template <class W, class E, bool kWhole>
+template <class W, class E, int V>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
   const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
@@ -70,24 +71,21 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
   const bool there = t >= 0 && t < (int64_t)p.V && !(p.doc && p.doc[n] < 0);
   const W *row = static_cast<const W *>(p.table) + (there ? t : 0) * p.table_row;
   E *y = static_cast<E *>(p.y) + (int64_t)n * p.D;
-  const int lead = lead_of<E, kWhole>(y);
-  const uint32_t first = slice * p.lanes * kUnroll + threadIdx.x % p.lanes;
-  Words<W> v[kUnroll];
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint32_t first = slice * kCopied * span + threadIdx.x % p.lanes * V;
+  Oct<W, V> v[kCopied];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t c = (int64_t)(first + u * p.lanes) * kChunk - lead;
-    if (there && c < p.D) v[u] = load_columns<W, kWhole>(row, c, p.D);
+  for (int u = 0; u < kCopied; ++u) {
+    clear(v[u]);
+    if (there) load_oct(v[u], row, first + u * span, step, p.D);
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t c = (int64_t)(first + u * p.lanes) * kChunk - lead;
-    float x[kChunk] = {};
-    if (there) {
-      widen<W>(v[u], x);
+  for (int u = 0; u < kCopied; ++u) {
+    Ch<2> x[kOct / 2];
+    widen(v[u], x);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) x[i] *= p.scale;
-    }
-    if (c < p.D) store_columns<E, kWhole>(y, c, p.D, narrow<E>(x));
+    for (int i = 0; i < kOct / 2; ++i) x[i] = x[i] * splat<2>(there ? p.scale : 0.0f);
+    store_oct(y, first + u * span, step, p.D, narrow<E, V>(x));
   }
 }
 
@@ -122,7 +120,7 @@ __device__ __forceinline__ void zero_rows(const EmbedParams &p, uint32_t part) {
   }
 }
 
-template <class W, class E, bool kWhole>
+template <class W, class E, int V>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p) {
   pdl_wait();
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -164,15 +162,18 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p
     else
       end += on;
   }
-  const uint64_t partial = ((uint64_t)tile * p.slices + slice) * kSlice + lane * kChunk;
+  // partial sums lie by lanes: a lane's eight columns beside one another
+  const uint64_t partial = ((uint64_t)tile * p.slices + slice) * kSlice + lane * kOct;
+  const uint32_t col = slice * kSlice + lane * V;
   const E *dy = static_cast<const E *>(p.dy);
   W *dtable = static_cast<W *>(p.dtable);
-  float acc[kChunk] = {};
-  constexpr int kAhead = kWhole && sizeof(E) == 2 ? 8 : 4;
+  Ch<2> acc[kOct / 2];
+#pragma unroll
+  for (int j = 0; j < kOct / 2; ++j) acc[j] = {0.0f, 0.0f};
+  constexpr int kAhead = Oct<E, V>::kPieces * Oct<E, V>::kWords == 4 ? 8 : 4;
   while (e < end) {
-    Words<E> v[kAhead];
+    Oct<E, V> v[kAhead];
     uint32_t key[kAhead + 1];
-    int64_t col[kAhead];
 #pragma unroll
     for (int a = 0; a <= kAhead; ++a) {
       const uint32_t x = __shfl_sync(kAll, cur.key, (e + a) & 31);
@@ -183,39 +184,32 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p
     for (int a = 0; a < kAhead; ++a) {
       const uint32_t x = __shfl_sync(kAll, cur.at, (e + a) & 31);
       const uint32_t y = __shfl_sync(kAll, next.at, (e + a) & 31);
-      if (key[a] == kBehind) continue;
-      const int lead = lead_of<W, kWhole>(dtable + (int64_t)key[a] * p.D);
-      col[a] = (int64_t)(slice * 32 + lane) * kChunk - lead;
       const uint32_t at = e + a < kTile ? x : y;
-      if (col[a] < p.D) v[a] = load_columns<E, kWhole>(dy + (int64_t)at * p.dy_row, col[a], p.D);
+      if (key[a] != kBehind) load_oct(v[a], dy + (int64_t)at * p.dy_row, col, 32 * V, p.D);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       if (key[a] == kBehind) continue;
-      if (col[a] < p.D) {
-        float x[kChunk];
-        widen<E>(v[a], x);
+      Ch<2> x[kOct / 2];
+      widen(v[a], x);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) acc[j] += x[j];
-      }
+      for (int j = 0; j < kOct / 2; ++j) acc[j] = acc[j] + x[j];
       if (key[a + 1] == key[a]) continue;
       // the token's last position here
       const bool to_head = e + a < first_end;
       const bool to_tail = open && e + a + 1 == end && !to_head;
-      if (col[a] < p.D) {
-        if (to_head || to_tail) {
-          float4 *to = reinterpret_cast<float4 *>((to_head ? p.head : p.tail) + partial);
-          to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        } else {
+      if (to_head || to_tail) {
+        float4 *to = reinterpret_cast<float4 *>((to_head ? p.head : p.tail) + partial);
+        to[0] = make_float4(acc[0].v[0], acc[0].v[1], acc[1].v[0], acc[1].v[1]);
+        to[1] = make_float4(acc[2].v[0], acc[2].v[1], acc[3].v[0], acc[3].v[1]);
+        if (to_tail && slice == 0 && lane == 0) p.open[atomicAdd(p.counter, 1u)] = tile;
+      } else {
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) acc[j] *= p.scale;
-          store_columns<W, kWhole>(dtable + (int64_t)key[a] * p.D, col[a], p.D, narrow<W>(acc));
-        }
+        for (int j = 0; j < kOct / 2; ++j) acc[j] = acc[j] * splat<2>(p.scale);
+        store_oct(dtable + (int64_t)key[a] * p.D, col, 32 * V, p.D, narrow<W, V>(acc));
       }
-      if (to_tail && slice == 0 && lane == 0) p.open[atomicAdd(p.counter, 1u)] = tile;
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) acc[j] = 0.0f;
+      for (int j = 0; j < kOct / 2; ++j) acc[j] = {0.0f, 0.0f};
     }
     e += kAhead;
   }
@@ -223,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p
 
 // The tokens across tiles: the tail where one begins and the heads behind it.  A
 // block takes one's 256 columns, each warp a run of its tiles; the runs are added in order.
-template <class W, bool kWhole>
+template <class W, int V>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams p) {
   pdl_wait();
   __shared__ float sums[kWarps][kSlice];
@@ -241,11 +235,11 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams 
     }
     const uint32_t run = (more + kWarps - 1) / kWarps;
     const uint32_t a = min(more, warp * run), b = min(more, a + run);
-    const uint64_t step = (uint64_t)p.slices * kSlice, at = (uint64_t)slice * kSlice + lane * kChunk;
-    float acc[kChunk] = {};
+    const uint64_t step = (uint64_t)p.slices * kSlice, at = (uint64_t)slice * kSlice + lane * kOct;
+    float acc[kOct] = {};
     if (warp == 0) {
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) acc[j] = p.tail[tile * step + at + j];
+      for (int j = 0; j < kOct; ++j) acc[j] = p.tail[tile * step + at + j];
     }
 #pragma unroll 4
     for (uint32_t t = a; t < b; ++t) {
@@ -255,17 +249,17 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams 
       acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
     }
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) sums[warp][lane * kChunk + j] = acc[j];
+    for (int j = 0; j < kOct; ++j) sums[warp][lane + 32 * j] = acc[j];
     __syncthreads();
     if (warp == 0) {
-      W *row = static_cast<W *>(p.dtable) + (int64_t)key * p.D;
-      const int64_t c = (int64_t)(slice * 32 + lane) * kChunk - lead_of<W, kWhole>(row);
       for (int w = 1; w < kWarps; ++w)
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) acc[j] += sums[w][lane * kChunk + j];
+        for (int j = 0; j < kOct; ++j) acc[j] += sums[w][lane + 32 * j];
+      Ch<2> x[kOct / 2];
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) acc[j] *= p.scale;
-      if (c < p.D) store_columns<W, kWhole>(row, c, p.D, narrow<W>(acc));
+      for (int j = 0; j < kOct; ++j) x[j / 2].v[j & 1] = acc[j] * p.scale;
+      store_oct(static_cast<W *>(p.dtable) + (int64_t)key * p.D, slice * kSlice + lane * V, 32 * V,
+                p.D, narrow<W, V>(x));
     }
     __syncthreads();
   }
@@ -280,7 +274,7 @@ struct Layout {
 };
 Layout layout_of(uint32_t N, uint32_t V, uint32_t D) {
   const uint64_t tiles = tiles_of(N);
-  const uint64_t columns = ((uint64_t)chunks_of(D, false) + 31) / 32 * kSlice;
+  const uint64_t columns = ((uint64_t)D + kSlice - 1) / kSlice * kSlice;
   Layout l = {};
   l.sorted = 0;
   l.used = l.sorted + rounded((uint64_t)N * sizeof(Sorted));
@@ -292,25 +286,19 @@ Layout layout_of(uint32_t N, uint32_t V, uint32_t D) {
   return l;
 }
 
-template <class W, class E>
+template <class W, class E, int V>
 cudaError_t forward_of(EmbedParams &p, cudaStream_t st) {
-  const bool whole = whole_rows(p.table, p.table_row, p.D, sizeof(W)) &&
-                     whole_rows(p.y, p.D, p.D, sizeof(E));
-  const uint32_t chunks = chunks_of(p.D, whole);
-  p.lanes = 1;
-  while (p.lanes < 32 && p.lanes < chunks) p.lanes *= 2;
-  p.slices = (chunks + p.lanes * kUnroll - 1) / (p.lanes * kUnroll);
+  p.lanes = lanes_for(p.D);
+  p.slices = (uint32_t)((spans_for(p.D, p.lanes) + kCopied - 1) / kCopied);
   const uint32_t each = kThreads / p.lanes;
   ++launch_counter();
-  auto *k = whole ? embed_kernel<W, E, true> : embed_kernel<W, E, false>;
-  k<<<(uint32_t)(((uint64_t)p.N * p.slices + each - 1) / each), kThreads, 0, st>>>(p);
+  embed_kernel<W, E, V>
+      <<<(uint32_t)(((uint64_t)p.N * p.slices + each - 1) / each), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-template <class W, class E>
+template <class W, class E, int V>
 cudaError_t backward_of(EmbedParams &p, void *workspace, cudaStream_t st) {
-  const bool whole = whole_rows(p.dy, p.dy_row, p.D, sizeof(E)) &&
-                     whole_rows(p.dtable, p.D, p.D, sizeof(W));
   char *ws = static_cast<char *>(workspace);
   const Layout l = layout_of(p.N, p.V, p.D);
   Sorted *sorted = reinterpret_cast<Sorted *>(ws + l.sorted);
@@ -318,7 +306,7 @@ cudaError_t backward_of(EmbedParams &p, void *workspace, cudaStream_t st) {
   p.sorted = sorted, p.used = used;
   p.counter = reinterpret_cast<uint32_t *>(ws + l.counter);
   p.open = reinterpret_cast<uint32_t *>(ws + l.open);
-  p.slices = (chunks_of(p.D, whole) + 31) / 32;
+  p.slices = (p.D + kSlice - 1) / kSlice;
   p.tiles = tiles_of(p.N);
   p.head = reinterpret_cast<float *>(ws + l.partial);
   p.tail = p.head + (uint64_t)p.tiles * p.slices * kSlice;
@@ -328,32 +316,33 @@ cudaError_t backward_of(EmbedParams &p, void *workspace, cudaStream_t st) {
   p.sum_blocks = (uint32_t)(((uint64_t)p.tiles * p.slices + kWarps - 1) / kWarps);
   const uint32_t zero = (p.V + 31) / 32;
   launch_counter() += 2;
-  pdl_launch(whole ? embed_sum_kernel<W, E, true> : embed_sum_kernel<W, E, false>,
-             dim3(p.sum_blocks + zero), dim3(kThreads), 0, st, p);
+  pdl_launch(embed_sum_kernel<W, E, V>, dim3(p.sum_blocks + zero), dim3(kThreads), 0, st, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const uint64_t most = (uint64_t)p.tiles * p.slices;
-  pdl_launch(whole ? embed_join_kernel<W, true> : embed_join_kernel<W, false>,
-             dim3((uint32_t)std::min<uint64_t>(most ? most : 1, 4 * 152)), dim3(kThreads), 0, st, p);
+  pdl_launch(embed_join_kernel<W, V>, dim3((uint32_t)std::min<uint64_t>(most ? most : 1, 4 * 152)),
+             dim3(kThreads), 0, st, p);
   return cudaGetLastError();
 }
 
-template <class W>
-cudaError_t forward_by(EmbedParams &p, int32_t dtype, cudaStream_t st) {
-  switch (dtype) {
-    case NS_F32: return forward_of<W, float>(p, st);
-    case NS_BF16: return forward_of<W, __nv_bfloat16>(p, st);
-    default: return forward_of<W, __half>(p, st);
-  }
+// By the types of the table and of the rows, and the pieces that both can be moved by.
+template <class F>
+cudaError_t by_types(const ns_embed_inputs &in, int piece, F &&call) {
+  const auto with_rows = [&](auto w, auto e) {
+    if (piece == 8) return call(w, e, std::integral_constant<int, 8>{});
+    if (piece == 2) return call(w, e, std::integral_constant<int, 2>{});
+    return call(w, e, std::integral_constant<int, 1>{});
+  };
+  const auto with_table = [&](auto w) {
+    if (in.dtype == NS_F32) return with_rows(w, float{});
+    if (in.dtype == NS_BF16) return with_rows(w, __nv_bfloat16{});
+    return with_rows(w, __half{});
+  };
+  if (in.table_dtype == NS_F32) return with_table(float{});
+  if (in.table_dtype == NS_BF16) return with_table(__nv_bfloat16{});
+  return with_table(__half{});
 }
-template <class W>
-cudaError_t backward_by(EmbedParams &p, int32_t dtype, void *ws, cudaStream_t st) {
-  switch (dtype) {
-    case NS_F32: return backward_of<W, float>(p, ws, st);
-    case NS_BF16: return backward_of<W, __nv_bfloat16>(p, ws, st);
-    default: return backward_of<W, __half>(p, ws, st);
-  }
-}
+uint64_t size_of(int32_t dtype) { return dtype == NS_F32 ? 4 : 2; }
 
 EmbedParams params_of(const ns_embed_inputs &in) {
   EmbedParams p = {};
@@ -370,22 +359,22 @@ cudaError_t launch_embed_forward(const ns_embed_inputs &in, const void *table, i
                                  void *y, cudaStream_t st) {
   EmbedParams p = params_of(in);
   p.table = table, p.table_row = table_row, p.y = y;
-  switch (in.table_dtype) {
-    case NS_F32: return forward_by<float>(p, in.dtype, st);
-    case NS_BF16: return forward_by<__nv_bfloat16>(p, in.dtype, st);
-    default: return forward_by<__half>(p, in.dtype, st);
-  }
+  const int piece = std::min(piece_of(table, table_row, in.D, size_of(in.table_dtype)),
+                             piece_of(y, in.D, in.D, size_of(in.dtype)));
+  return by_types(in, piece, [&](auto w, auto e, auto v) {
+    return forward_of<decltype(w), decltype(e), decltype(v)::value>(p, st);
+  });
 }
 
 cudaError_t launch_embed_backward(const ns_embed_inputs &in, const void *dy, int64_t dy_row,
                                   void *dtable, void *workspace, cudaStream_t st) {
   EmbedParams p = params_of(in);
   p.dy = dy, p.dy_row = dy_row, p.dtable = dtable;
-  switch (in.table_dtype) {
-    case NS_F32: return backward_by<float>(p, in.dtype, workspace, st);
-    case NS_BF16: return backward_by<__nv_bfloat16>(p, in.dtype, workspace, st);
-    default: return backward_by<__half>(p, in.dtype, workspace, st);
-  }
+  const int piece = std::min(piece_of(dy, dy_row, in.D, size_of(in.dtype)),
+                             piece_of(dtable, in.D, in.D, size_of(in.table_dtype)));
+  return by_types(in, piece, [&](auto w, auto e, auto v) {
+    return backward_of<decltype(w), decltype(e), decltype(v)::value>(p, workspace, st);
+  });
 }
 
 }  // namespace nsk

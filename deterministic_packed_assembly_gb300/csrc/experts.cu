@@ -14,12 +14,14 @@
 // once too, without a pass of their own.
 //
 // L lanes take a token and a slice of its columns, eight elements each at a time
-// (rows.cuh); a dot product takes a whole row, so that its order depends on nothing but D.
+// (rows.cuh); a dot product takes a whole row, so that its order depends on nothing but D
+// and the rows' alignment.
 
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -32,11 +34,10 @@ namespace nsk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // chunks a lane has under way
 
 struct ExpertParams {
   uint32_t N, k, E, D;
-  uint32_t lanes, slices, chunks;  // lanes of a unit, units of a row, chunks of a row
+  uint32_t lanes, spans, slices;  // lanes of a unit, spans of a row (rows.cuh), units of a row
   const int32_t *ids;
   int32_t *place, *slots, *offsets;
   const void *x;       // or d_out
@@ -48,57 +49,49 @@ struct ExpertParams {
   float *d_weights;
 };
 
+// Registers of rows that a lane has under way: 32 of 16-bit rows, eight of which fit in
+// four each.
+template <class E, int V>
+constexpr int kUnderWay = Oct<E, V>::kPieces * Oct<E, V>::kWords == 4 ? 8 : 4;
+
 // ---- dispatch --------------------------------------------------------------------
+constexpr int kCopied = 4;  // spans of a unit
+
 // One slice of token n's row into the places of its choices.
-template <class E, bool kWhole>
+template <class E, int V>
 __device__ __forceinline__ void copy_slice(const ExpertParams &p, uint32_t n, uint32_t slice,
                                            uint32_t lane, const int32_t *place, uint32_t M) {
   const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
   E *to = static_cast<E *>(p.to);
-  const uint32_t first = slice * p.lanes * kUnroll + lane;
-  Words<E> v[kUnroll];
-  if constexpr (kWhole) {
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint32_t first = slice * kCopied * span + lane * V;
+  Oct<E, V> v[kCopied], zero;
+  clear(zero);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (first + u * p.lanes < p.chunks)
-        v[u] = load_words<E, true>(x + (int64_t)(first + u * p.lanes) * kChunk);
-  }
-  Words<E> zero;
-#pragma unroll
-  for (int i = 0; i < Words<E>::kN; ++i) zero.w[i] = 0;
+  for (int u = 0; u < kCopied; ++u) load_oct(v[u], x, first + u * span, step, p.D);
   for (uint32_t j = 0; j < p.k; ++j) {
     const uint32_t at = (uint32_t)place[j];
     E *row = to + (int64_t)at * p.D;
-    const int lead = lead_of<E, kWhole>(row);
-    if constexpr (!kWhole) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int64_t c = (int64_t)(first + u * p.lanes) * kChunk - lead;
-        if (at < M && c < p.D) v[u] = load_columns<E, false>(x, c, p.D);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t c = (int64_t)(first + u * p.lanes) * kChunk - lead;
-      if (c < p.D) store_columns<E, kWhole>(row, c, p.D, at < M ? v[u] : zero);
-    }
+    for (int u = 0; u < kCopied; ++u)
+      store_oct(row, first + u * span, step, p.D, at < M ? v[u] : zero);
   }
 }
 
 // Blocks of kThreads / lanes units: a slice of a token each.
-template <class E, bool kWhole>
+template <class E, int V>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const ExpertParams p) {
   pdl_wait();
   const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
   if (n >= p.N) return;
-  copy_slice<E, kWhole>(p, n, slice, threadIdx.x % p.lanes, p.place + (uint64_t)n * p.k,
-                        (uint32_t)p.offsets[p.E]);
+  copy_slice<E, V>(p, n, slice, threadIdx.x % p.lanes, p.place + (uint64_t)n * p.k,
+                   (uint32_t)p.offsets[p.E]);
 }
 
 // Few choices: a block a token finds its places by counting the keys below and before
 // them, and no sort is needed.  The last block has the offsets.
-template <class E, bool kWhole>
+template <class E, int V>
 __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const ExpertParams p) {
   extern __shared__ uint32_t key[];  // [S], then what the block counts
   const uint32_t S = p.N * p.k;
@@ -152,59 +145,66 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const ExpertPara
   }
   const uint32_t M = count[p.k];
   for (uint32_t unit = threadIdx.x / p.lanes; unit < p.slices; unit += kThreads / p.lanes)
-    copy_slice<E, kWhole>(p, n, unit, threadIdx.x % p.lanes,
+    copy_slice<E, V>(p, n, unit, threadIdx.x % p.lanes,
                           reinterpret_cast<const int32_t *>(count), M);
 }
 
 // ---- combine ------------------------------------------------------------------------
-template <class E, bool kWhole>
+// R choices' rows and U spans of them under way: what hides memory's latency is R U.
+template <class E, int V, int R, int U>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const ExpertParams p) {
   const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
   if (n >= p.N) return;
-  const uint32_t lane = threadIdx.x % p.lanes;
   const uint32_t M = min((uint32_t)p.offsets[p.E], p.N * p.k);
   const int32_t *place = p.place + (uint64_t)n * p.k;
   const float *weights = p.weights ? p.weights + (uint64_t)n * p.k : nullptr;
   const E *from = static_cast<const E *>(p.from);
   E *out = static_cast<E *>(p.to) + (int64_t)n * p.D;
-  const int lead = lead_of<E, kWhole>(out);
-  constexpr int kRows = 4;  // rows under way
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t c = (int64_t)(slice * p.lanes * kUnroll + u * p.lanes + lane) * kChunk - lead;
-    if (c >= p.D) return;
-    float acc[kChunk] = {};
-    for (uint32_t j0 = 0; j0 < p.k; j0 += kRows) {
-      Words<E> v[kRows];
-      float w[kRows];
-      bool there[kRows];
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint32_t first = slice * U * span + threadIdx.x % p.lanes * V;
+  Ch<2> acc[U][kOct / 2];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        there[r] = j0 + r < p.k;
-        const uint32_t at = there[r] ? (uint32_t)place[j0 + r] : M;
-        there[r] = at < M;
-        if (there[r]) {
-          v[r] = load_columns<E, kWhole>(from + (int64_t)at * p.from_row, c, p.D);
-          w[r] = weights ? weights[j0 + r] : 1.0f;
-        }
-      }
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (!there[r]) continue;
-        float x[kChunk];
-        widen<E>(v[r], x);
+    for (int i = 0; i < kOct / 2; ++i) acc[u][i] = {0.0f, 0.0f};
+  for (uint32_t j0 = 0; j0 < p.k; j0 += R) {
+    Oct<E, V> v[R][U];
+    float w[R];
+    bool there[R];
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) acc[i] = fmaf(w[r], x[i], acc[i]);
+    for (int r = 0; r < R; ++r) {
+      const uint32_t at = j0 + r < p.k ? (uint32_t)place[j0 + r] : M;
+      there[r] = at < M;
+      if (there[r]) {
+        w[r] = weights ? weights[j0 + r] : 1.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          load_oct(v[r][u], from + (int64_t)at * p.from_row, first + u * span, step, p.D);
       }
     }
-    store_columns<E, kWhole>(out, c, p.D, narrow<E>(acc));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!there[r]) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Ch<2> x[kOct / 2];
+        widen(v[r][u], x);
+#pragma unroll
+        for (int i = 0; i < kOct / 2; ++i) acc[u][i] = fma(splat<2>(w[r]), x[i], acc[u][i]);
+      }
+    }
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    store_oct(out, first + u * span, step, p.D, narrow<E, V>(acc[u]));
 }
 
 // ---- combine's backward pass -----------------------------------------------------------
 // L lanes a choice: neighbouring units are a token's, whose row stays in the L1 cache.
-template <class E, bool kWhole>
+template <class E, int V>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const ExpertParams p) {
+  constexpr int U = kUnderWay<E, V> / 2;  // spans under way, of two rows
   const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
   const uint32_t S = p.N * p.k;
   const bool real = unit < S;  // all lanes stay: they add up together
@@ -216,65 +216,47 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Expert
   const E *y = static_cast<const E *>(p.from) + (int64_t)at * p.from_row;
   E *to = static_cast<E *>(p.to) + (int64_t)at * p.D;
   const bool there = real && at < M;
-  const float w = there && p.weights ? p.weights[s] : there ? 1.0f : 0.0f;
-  float dot = 0.0f;
-  if (there && (p.d_weights || kWhole)) {
-    const uint32_t pieces = (uint32_t)(((uint64_t)p.D + kChunk - 1) / kChunk);
-    for (uint32_t q0 = lane; q0 < pieces; q0 += p.lanes * kUnroll) {
-      Words<E> a[kUnroll], b[kUnroll];
+  const Ch<2> w = splat<2>(there && p.weights ? p.weights[s] : 1.0f);
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  Ch<2> dot = {0.0f, 0.0f};
+  if (real && at < S) {
+    for (uint32_t c = lane * V; c < p.D; c += U * span) {
+      Oct<E, V> a[U], b[U];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int64_t c = (int64_t)(q0 + u * p.lanes) * kChunk;
-        if (c < p.D) {
-          a[u] = load_columns<E, kWhole>(d_out, c, p.D);
-          if (p.d_weights) b[u] = load_columns<E, kWhole>(y, c, p.D);
+      for (int u = 0; u < U; ++u) {
+        clear(a[u]), clear(b[u]);
+        if (there) {
+          load_oct(a[u], d_out, c + u * span, step, p.D);
+          if (p.d_weights) load_oct(b[u], y, c + u * span, step, p.D);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int64_t c = (int64_t)(q0 + u * p.lanes) * kChunk;
-        if (c >= p.D) break;
-        float d[kChunk], x[kChunk];
-        widen<E>(a[u], d);
-        if (p.d_weights) {
-          widen<E>(b[u], x);
+      for (int u = 0; u < U; ++u) {
+        Ch<2> d[kOct / 2], x[kOct / 2];
+        widen(a[u], d);
+        widen(b[u], x);
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) dot = fmaf(d[i], x[i], dot);
+        for (int i = 0; i < kOct / 2; ++i) {
+          dot = fma(d[i], x[i], dot);
+          d[i] = d[i] * w;
         }
-        if constexpr (kWhole) {
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) d[i] *= w;
-          store_columns<E, true>(to, c, p.D, narrow<E>(d));
-        }
+        store_oct(to, c + u * span, step, p.D, narrow<E, V>(d));
       }
     }
   }
   if (p.d_weights) {
-    for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (real && lane == 0) p.d_weights[s] = dot;
-  }
-  if (!real || at >= S || (kWhole && there)) return;
-  const int lead = lead_of<E, kWhole>(to);
-  for (uint32_t q = lane; q < p.chunks; q += p.lanes) {
-    const int64_t c = (int64_t)q * kChunk - lead;
-    if (c >= p.D) break;
-    float d[kChunk] = {};
-    if (there) {
-      widen<E>(load_columns<E, kWhole>(d_out, c, p.D), d);
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) d[i] *= w;
-    }
-    store_columns<E, kWhole>(to, c, p.D, narrow<E>(d));
+    float sum = dot.v[0] + dot.v[1];
+    for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (real && lane == 0) p.d_weights[s] = sum;
   }
 }
 
 // ---- launches ------------------------------------------------------------------------
-// Lanes of a unit: as few as hold a row, at most a warp.
-void set_shape(ExpertParams &p, bool whole, bool sliced) {
-  p.chunks = chunks_of(p.D, whole);
-  p.lanes = 1;
-  while (p.lanes < 32 && p.lanes < p.chunks) p.lanes *= 2;
-  p.slices = sliced ? (p.chunks + p.lanes * kUnroll - 1) / (p.lanes * kUnroll) : 1;
+// The lanes of a unit, which has `spans` of the row's, or all of them.
+void set_shape(ExpertParams &p, uint32_t spans) {
+  p.lanes = lanes_for(p.D);
+  p.spans = (uint32_t)spans_for(p.D, p.lanes);
+  p.slices = spans ? (p.spans + spans - 1) / spans : 1;
 }
 uint32_t blocks_of(uint64_t units, uint32_t lanes) {
   const uint32_t each = kThreads / lanes;
@@ -285,48 +267,61 @@ uint32_t blocks_of(uint64_t units, uint32_t lanes) {
 // shared memory: up to so many comparisons a thread, the sort's two launches cost more.
 bool few(uint64_t N, uint64_t k) { return N * k <= 2048 && N * k * k <= (1 << 14); }
 
-template <class E>
+template <class E, int V>
 cudaError_t dispatch_of(ExpertParams &p, void *workspace, cudaStream_t st) {
-  const bool whole =
-      whole_rows(p.x, p.x_row, p.D, sizeof(E)) && whole_rows(p.to, p.D, p.D, sizeof(E));
-  set_shape(p, whole, true);
+  set_shape(p, kCopied);
   if (few(p.N, p.k)) {
-    auto *k = whole ? dispatch_few_kernel<E, true> : dispatch_few_kernel<E, false>;
     const size_t shared = (p.N * p.k + std::max(p.k, p.E) + 1) * sizeof(uint32_t);
     ++launch_counter();
-    k<<<p.N + 1, kThreads, shared, st>>>(p);
+    dispatch_few_kernel<E, V><<<p.N + 1, kThreads, shared, st>>>(p);
     return cudaGetLastError();
   }
   const cudaError_t e = launch_order_choices({p.ids, nullptr, p.N * p.k, p.E, false}, p.place,
                                              p.slots, p.offsets, workspace, st);
   if (e != cudaSuccess || p.D == 0) return e;
   ++launch_counter();
-  pdl_launch(whole ? dispatch_kernel<E, true> : dispatch_kernel<E, false>,
-             dim3(blocks_of((uint64_t)p.N * p.slices, p.lanes)), dim3(kThreads), 0, st, p);
+  pdl_launch(dispatch_kernel<E, V>, dim3(blocks_of((uint64_t)p.N * p.slices, p.lanes)),
+             dim3(kThreads), 0, st, p);
   return cudaGetLastError();
 }
 
-template <class E>
+template <class E, int V, int R>
+cudaError_t combine_by(ExpertParams &p, cudaStream_t st) {
+  constexpr int U = kUnderWay<E, V> > R ? kUnderWay<E, V> / R : 1;
+  set_shape(p, U);
+  ++launch_counter();
+  combine_kernel<E, V, R, U>
+      <<<blocks_of((uint64_t)p.N * p.slices, p.lanes), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+template <class E, int V>
 cudaError_t combine_of(ExpertParams &p, cudaStream_t st) {
-  const bool whole =
-      whole_rows(p.from, p.from_row, p.D, sizeof(E)) && whole_rows(p.to, p.D, p.D, sizeof(E));
-  set_shape(p, whole, true);
-  auto *k = whole ? combine_kernel<E, true> : combine_kernel<E, false>;
+  if (p.k == 1) return combine_by<E, V, 1>(p, st);
+  if (p.k == 2) return combine_by<E, V, 2>(p, st);
+  if (p.k <= 4 || kUnderWay<E, V> == 4) return combine_by<E, V, 4>(p, st);
+  return combine_by<E, V, kUnderWay<E, V>>(p, st);
+}
+
+template <class E, int V>
+cudaError_t combine_backward_of(ExpertParams &p, cudaStream_t st) {
+  set_shape(p, 0);
   ++launch_counter();
-  k<<<blocks_of((uint64_t)p.N * p.slices, p.lanes), kThreads, 0, st>>>(p);
+  combine_backward_kernel<E, V>
+      <<<blocks_of((uint64_t)p.N * p.k, p.lanes), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-template <class E>
-cudaError_t combine_backward_of(ExpertParams &p, cudaStream_t st) {
-  const bool whole = whole_rows(p.x, p.x_row, p.D, sizeof(E)) &&
-                     whole_rows(p.from, p.from_row, p.D, sizeof(E)) &&
-                     whole_rows(p.to, p.D, p.D, sizeof(E));
-  set_shape(p, whole, false);
-  auto *k = whole ? combine_backward_kernel<E, true> : combine_backward_kernel<E, false>;
-  ++launch_counter();
-  k<<<blocks_of((uint64_t)p.N * p.k, p.lanes), kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+// By the rows' type and the pieces that all of them can be moved by.
+template <class F>
+cudaError_t by_pieces(int32_t dtype, int piece, F &&call) {
+  const auto with = [&](auto e) {
+    if (piece == 8) return call(e, std::integral_constant<int, 8>{});
+    if (piece == 2) return call(e, std::integral_constant<int, 2>{});
+    return call(e, std::integral_constant<int, 1>{});
+  };
+  if (dtype == NS_F32) return with(float{});
+  if (dtype == NS_BF16) return with(__nv_bfloat16{});
+  return with(__half{});
 }
 
 ExpertParams params_of(const ns_expert_sizes &s) {
@@ -334,6 +329,7 @@ ExpertParams params_of(const ns_expert_sizes &s) {
   p.N = s.N, p.k = s.k, p.E = s.E, p.D = s.D;
   return p;
 }
+uint64_t size_of(const ns_expert_sizes &s) { return s.dtype == NS_F32 ? 4 : 2; }
 
 }  // namespace
 
@@ -347,11 +343,11 @@ cudaError_t launch_dispatch(const ns_expert_sizes &s, const int32_t *ids, const 
   ExpertParams p = params_of(s);
   p.ids = ids, p.x = x, p.x_row = x_row;
   p.place = place, p.slots = slots, p.offsets = offsets, p.to = rows;
-  switch (s.dtype) {
-    case NS_F32: return dispatch_of<float>(p, workspace, st);
-    case NS_BF16: return dispatch_of<__nv_bfloat16>(p, workspace, st);
-    default: return dispatch_of<__half>(p, workspace, st);
-  }
+  const uint64_t es = size_of(s);
+  const int piece = std::min(piece_of(x, x_row, s.D, es), piece_of(rows, s.D, s.D, es));
+  return by_pieces(s.dtype, piece, [&](auto e, auto v) {
+    return dispatch_of<decltype(e), decltype(v)::value>(p, workspace, st);
+  });
 }
 
 cudaError_t launch_combine(const ns_expert_sizes &s, const int32_t *place, const int32_t *offsets,
@@ -360,11 +356,11 @@ cudaError_t launch_combine(const ns_expert_sizes &s, const int32_t *place, const
   ExpertParams p = params_of(s);
   p.place = const_cast<int32_t *>(place), p.offsets = const_cast<int32_t *>(offsets);
   p.weights = weights, p.from = rows, p.from_row = rows_row, p.to = out;
-  switch (s.dtype) {
-    case NS_F32: return combine_of<float>(p, st);
-    case NS_BF16: return combine_of<__nv_bfloat16>(p, st);
-    default: return combine_of<__half>(p, st);
-  }
+  const uint64_t es = size_of(s);
+  const int piece = std::min(piece_of(rows, rows_row, s.D, es), piece_of(out, s.D, s.D, es));
+  return by_pieces(s.dtype, piece, [&](auto e, auto v) {
+    return combine_of<decltype(e), decltype(v)::value>(p, st);
+  });
 }
 
 cudaError_t launch_combine_backward(const ns_expert_sizes &s, const int32_t *place,
@@ -376,11 +372,12 @@ cudaError_t launch_combine_backward(const ns_expert_sizes &s, const int32_t *pla
   p.place = const_cast<int32_t *>(place), p.offsets = const_cast<int32_t *>(offsets);
   p.weights = weights, p.from = rows, p.from_row = rows_row;
   p.x = d_out, p.x_row = d_out_row, p.to = d_rows, p.d_weights = d_weights;
-  switch (s.dtype) {
-    case NS_F32: return combine_backward_of<float>(p, st);
-    case NS_BF16: return combine_backward_of<__nv_bfloat16>(p, st);
-    default: return combine_backward_of<__half>(p, st);
-  }
+  const uint64_t es = size_of(s);
+  int piece = std::min(piece_of(d_out, d_out_row, s.D, es), piece_of(d_rows, s.D, s.D, es));
+  if (d_weights) piece = std::min(piece, piece_of(rows, rows_row, s.D, es));
+  return by_pieces(s.dtype, piece, [&](auto e, auto v) {
+    return combine_backward_of<decltype(e), decltype(v)::value>(p, st);
+  });
 }
 
 }  // namespace nsk

@@ -27,6 +27,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kMostBlocks = 152;
 constexpr uint32_t kNone = 0xffffffffu;
+constexpr int kAhead = 8;  // keys a thread has under way
 
 struct Pass {
   Keys keys;
@@ -35,9 +36,11 @@ struct Pass {
   int32_t *place, *slots, *offsets;
   uint8_t *used;       // first pass
   uint32_t *counter;
-  uint32_t *table;     // [blocks][R]
+  uint32_t *table;     // [blocks][rounded_digits(R)]
   uint32_t R, shift, mask, stretch;
 };
+
+__host__ __device__ __forceinline__ uint32_t rounded_digits(uint32_t R) { return (R + 3) / 4 * 4; }
 
 __device__ __forceinline__ Sorted key_at(const Pass &p, uint32_t i) {
   if (p.from) return p.from[i];
@@ -61,21 +64,30 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const Pass p) {
   __syncthreads();
   const uint32_t begin = blockIdx.x * p.stretch;
   const uint32_t end = min(p.keys.N, begin + p.stretch);
-  for (uint32_t i = begin + threadIdx.x; i < end; i += kThreads)
-    atomicAdd(&count[(key_at(p, i).key >> p.shift) & p.mask], 1u);
+  for (uint32_t i0 = begin + threadIdx.x; i0 < end; i0 += kThreads * kAhead) {
+    uint32_t key[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i0 + a * kThreads < end) key[a] = key_at(p, i0 + a * kThreads).key;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i0 + a * kThreads < end) atomicAdd(&count[(key[a] >> p.shift) & p.mask], 1u);
+  }
   __syncthreads();
-  for (uint32_t d = threadIdx.x; d < p.R; d += kThreads)
-    p.table[(uint64_t)blockIdx.x * p.R + d] = count[d];
+  const uint32_t Rp = rounded_digits(p.R);
+  for (uint32_t d = threadIdx.x; d < Rp; d += kThreads)
+    p.table[(uint64_t)blockIdx.x * Rp + d] = d < p.R ? count[d] : 0;
 }
 
 __global__ void __launch_bounds__(kThreads) place_kernel(const Pass p) {
   extern __shared__ uint32_t shared[];
   uint32_t *total = shared;              // [R]: of all blocks, then the digits before
-  uint32_t *before = total + p.R;        // [R]: of the blocks before this one
-  uint32_t *start = before + p.R;        // [kWarps][R]
+  const uint32_t Rp = rounded_digits(p.R);
+  uint32_t *before = total + Rp;         // [R]: of the blocks before this one
+  uint32_t *start = before + Rp;         // [kWarps][R]
   __shared__ uint32_t sums[kWarps];
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (uint32_t d = threadIdx.x; d < (2 + kWarps) * p.R; d += kThreads) shared[d] = 0;
+  for (uint32_t d = threadIdx.x; d < 2 * Rp + kWarps * p.R; d += kThreads) shared[d] = 0;
   __syncthreads();
   pdl_wait_then_release();
 
@@ -84,27 +96,36 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const Pass p) {
   const uint32_t begin = min(p.keys.N, blockIdx.x * p.stretch + warp * part);
   const uint32_t end = min(p.keys.N, begin + part);
   uint32_t *mine = start + warp * p.R;
-  for (uint32_t i = begin + lane; i < end; i += 32) {
-    const uint32_t key = key_at(p, i).key;
-    atomicAdd(&mine[(key >> p.shift) & p.mask], 1u);
-    if (p.used && key < p.keys.limit) p.used[key] = 1;
-  }
-  // all blocks' counters: neighbouring threads take neighbouring digits, groups of them
-  // share the blocks
-  const uint32_t wide = p.R < kThreads ? p.R : kThreads, groups = kThreads / wide;
-  const uint32_t group = threadIdx.x / wide;
-  if (group < groups) {
-    for (uint32_t d = threadIdx.x % wide; d < p.R; d += wide) {
-      uint32_t all = 0, ahead = 0;
-#pragma unroll 8
-      for (uint32_t b = group; b < gridDim.x; b += groups) {
-        const uint32_t c = p.table[(uint64_t)b * p.R + d];
-        all += c;
-        ahead += b < blockIdx.x ? c : 0;
-      }
-      atomicAdd(&total[d], all);
-      atomicAdd(&before[d], ahead);
+  for (uint32_t i0 = begin + lane; i0 < end; i0 += 32 * kAhead) {
+    uint32_t key[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i0 + 32 * a < end) key[a] = key_at(p, i0 + 32 * a).key;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (i0 + 32 * a >= end) break;
+      atomicAdd(&mine[(key[a] >> p.shift) & p.mask], 1u);
+      if (p.used && key[a] < p.keys.limit) p.used[key[a]] = 1;
     }
+  }
+  // all blocks' counters: neighbouring threads take four neighbouring digits each, groups of
+  // them share the blocks
+  const uint32_t quads = Rp / 4, groups = kThreads / min(quads, (uint32_t)kThreads);
+  const uint32_t group = threadIdx.x / quads;
+  if (group < groups) {
+    const uint4 *table = reinterpret_cast<const uint4 *>(p.table);
+    const uint32_t d = threadIdx.x % quads;
+    uint4 all = make_uint4(0, 0, 0, 0), ahead = all;
+#pragma unroll 8
+    for (uint32_t b = group; b < gridDim.x; b += groups) {
+      const uint4 c = table[(uint64_t)b * quads + d];
+      all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+      if (b < blockIdx.x) ahead.x += c.x, ahead.y += c.y, ahead.z += c.z, ahead.w += c.w;
+    }
+    atomicAdd(&total[4 * d], all.x), atomicAdd(&before[4 * d], ahead.x);
+    atomicAdd(&total[4 * d + 1], all.y), atomicAdd(&before[4 * d + 1], ahead.y);
+    atomicAdd(&total[4 * d + 2], all.z), atomicAdd(&before[4 * d + 2], ahead.z);
+    atomicAdd(&total[4 * d + 3], all.w), atomicAdd(&before[4 * d + 3], ahead.w);
   }
   __syncthreads();
   // digits before: each thread has a run of them
@@ -135,21 +156,26 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const Pass p) {
   }
   __syncthreads();
 
-  for (uint32_t i0 = begin; i0 < end; i0 += 32) {
-    const uint32_t i = i0 + lane;
-    Sorted s = {kNone, 0};
-    if (i < end) s = key_at(p, i);
-    const uint32_t d = i < end ? (s.key >> p.shift) & p.mask : kNone;
-    const uint32_t same = __match_any_sync(0xffffffffu, d);
-    const uint32_t rank = __popc(same & ((1u << lane) - 1));
-    uint32_t at = 0;
-    if (i < end) at = mine[d] + rank;
-    __syncwarp();
-    if (i < end && rank == 0) mine[d] += __popc(same);
-    __syncwarp();
-    if (i < end) {
+  for (uint32_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
+    Sorted key[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i0 + 32 * a + lane < end) key[a] = key_at(p, i0 + 32 * a + lane);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (i0 + 32 * a >= end) break;
+      const uint32_t i = i0 + 32 * a + lane;
+      const uint32_t d = i < end ? (key[a].key >> p.shift) & p.mask : kNone;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      const uint32_t rank = __popc(same & ((1u << lane) - 1));
+      uint32_t at = 0;
+      if (i < end) at = mine[d] + rank;
+      __syncwarp();
+      if (i < end && rank == 0) mine[d] += __popc(same);
+      __syncwarp();
+      if (i >= end) continue;
       if (p.to) {
-        p.to[at] = s;
+        p.to[at] = key[a];
       } else {
         p.place[i] = (int32_t)at;
         p.slots[at] = (int32_t)i;
@@ -170,7 +196,7 @@ uint32_t blocks_of(uint32_t N) {
 
 cudaError_t launch_pass(const Pass &p, bool first, cudaStream_t st) {
   const uint32_t blocks = blocks_of(p.keys.N);
-  const size_t shared = (2 + kWarps) * (size_t)p.R * sizeof(uint32_t);
+  const size_t shared = (2 * rounded_digits(p.R) + kWarps * (size_t)p.R) * sizeof(uint32_t);
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void *>(place_kernel));
   if (e != cudaSuccess) return e;
   launch_counter() += 2;
@@ -199,7 +225,7 @@ uint64_t rounded(uint64_t bytes) { return (bytes + 255) / 256 * 256; }
 }  // namespace
 
 uint64_t order_choices_workspace(uint32_t N, uint32_t limit) {
-  return (uint64_t)blocks_of(N) * (limit + 1) * sizeof(uint32_t);
+  return (uint64_t)blocks_of(N) * rounded_digits(limit + 1) * sizeof(uint32_t);
 }
 
 cudaError_t launch_order_choices(const Keys &keys, int32_t *place, int32_t *slots,
@@ -213,7 +239,7 @@ cudaError_t launch_order_choices(const Keys &keys, int32_t *place, int32_t *slot
 
 uint64_t order_tokens_workspace(uint32_t N, uint32_t limit) {
   const Digits d = digits_of(limit);
-  return rounded((uint64_t)blocks_of(N) * (1u << d.bits) * sizeof(uint32_t)) +
+  return rounded((uint64_t)blocks_of(N) * rounded_digits(1u << d.bits) * sizeof(uint32_t)) +
          (d.passes > 1 ? (uint64_t)N * sizeof(Sorted) : 0);
 }
 
@@ -222,7 +248,7 @@ cudaError_t launch_order_tokens(const Keys &keys, Sorted *sorted, uint8_t *used,
   const Digits d = digits_of(keys.limit);
   Sorted *other = reinterpret_cast<Sorted *>(
       static_cast<char *>(workspace) +
-      rounded((uint64_t)blocks_of(keys.N) * (1u << d.bits) * sizeof(uint32_t)));
+      rounded((uint64_t)blocks_of(keys.N) * rounded_digits(1u << d.bits) * sizeof(uint32_t)));
   Pass p = {};
   p.keys = keys, p.table = static_cast<uint32_t *>(workspace);
   p.R = 1u << d.bits, p.mask = p.R - 1, p.stretch = stretch_of(keys.N);

@@ -191,7 +191,7 @@ static bool fits_row(int64_t row, uint32_t D, uint32_t N) {
 
 static bool check_embed(const ns_embed_inputs *in) {
   if (!in || !size_of(in->table_dtype) || !size_of(in->dtype)) return false;
-  if (in->N >= (1u << 31) || in->V >= (1u << 31) || in->D >= (1u << 31)) return false;
+  if (in->N >= (1u << 31) || in->V >= (1u << 31) || in->D >= (1u << 30)) return false;
   // blocks of a launch, and bytes of a workspace: past any memory long before
   if ((uint64_t)in->N * in->D >= (1ull << 42) || (uint64_t)in->V * in->D >= (1ull << 42))
     return false;
@@ -210,7 +210,7 @@ int ns_embed_forward(const ns_embed_inputs *in, const void *table, int64_t table
 }
 
 uint64_t ns_embed_workspace(uint32_t N, uint32_t V, uint32_t D) {
-  if (N >= (1u << 31) || V >= (1u << 31) || D >= (1u << 31) || (uint64_t)N * D >= (1ull << 42))
+  if (N >= (1u << 31) || V >= (1u << 31) || D >= (1u << 30) || (uint64_t)N * D >= (1ull << 42))
     return 0;
   return nsk::embed_workspace(N, V, D);
 }
@@ -288,7 +288,7 @@ int ns_dispatch(const ns_expert_sizes *sizes, const int32_t *ids, const void *x,
   const bool none = sizes->N == 0, nothing = none || sizes->D == 0;
   if (!usable(ids, 4, none) || !usable(x, es, nothing) || !usable(place, 4, none) ||
       !usable(slots, 4, none) || !usable(offsets, 4) || !usable(rows, es, nothing) ||
-      !usable(workspace, 4, ns_dispatch_workspace(sizes->N, sizes->k, sizes->E) == 0))
+      !usable(workspace, 16, ns_dispatch_workspace(sizes->N, sizes->k, sizes->E) == 0))
     return NS_ERR_INVALID_ARG;
   return done(nsk::launch_dispatch(*sizes, ids, x, x_row, place, slots, offsets, rows, workspace,
                                    static_cast<cudaStream_t>(cuda_stream)));

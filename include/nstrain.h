@@ -207,7 +207,7 @@ int ns_route_backward(const ns_route_inputs *in, const int32_t *ids, const float
 typedef struct {
   const void *tokens;  /* [N] int32, or int64 where ids_64 != 0 */
   const int32_t *doc;  /* [N] or NULL */
-  uint32_t N, V, D;    /* each < 2^31 */
+  uint32_t N, V, D;    /* N, V < 2^31, D < 2^30 */
   int32_t table_dtype; /* of the table and of its gradient */
   int32_t dtype;       /* of y and dy */
   int32_t ids_64;
@@ -285,7 +285,7 @@ typedef struct {
  * refuses). */
 uint64_t ns_dispatch_workspace(uint32_t N, uint32_t k, uint32_t E);
 
-/* place, slots: [N k]; offsets: [E + 1].  workspace: 4-byte aligned, or NULL for
+/* place, slots: [N k]; offsets: [E + 1].  workspace: 16-byte aligned, or NULL for
  * none.  No output may overlap an input.  Errors: INVALID_ARG (a needed pointer
  * NULL or misaligned, an unknown type, a stride below D, sizes out of range),
  * CUDA. */
