@@ -1,0 +1,252 @@
+// What the layer norm's kernels share (norm.cu has the choice among them).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "common.cuh"
+#include "elem.cuh"
+#include "kernels.h"
+#include "ring.cuh"
+#include "rows.cuh"
+#include "train.h"
+
+namespace nsk {
+
+constexpr uint32_t kNormSMs = 152;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kNormNarrow = 512;   // columns up to which rows go without the ring
+constexpr uint32_t kNormWarps = 15;     // of a row, at most: with the one that copies 512 threads
+constexpr uint32_t kNormKept = 5 * 32 * kOct * kNormWarps;  // columns that they have registers for
+constexpr int kNormFew = 10;            // warps of a block of which an SM has two at least
+constexpr int kWideThreads = 512;       // of a row of more columns
+
+struct NormParams {
+  const void *x, *dy, *weight, *bias;
+  bool floats;  // weight and bias are, whatever the rows
+  int64_t x_row, dy_row;
+  const int32_t *doc;
+  void *y;  // or dx
+  float *mean, *rstd;
+  float eps;
+  uint32_t N, D;
+  uint32_t lanes, warps;  // of a row: lanes of one warp, or warps
+  uint32_t stages;        // of the ring
+  float *partial;         // [blocks][2][D]
+  void *dweight, *dbias;
+  uint32_t blocks;
+};
+
+// How a row lies on threads, by its columns alone: what a row gets does not depend on
+// the kernel that takes it.
+struct NormShape {
+  uint32_t lanes, nb, warps;  // nb spans a warp
+};
+inline NormShape norm_shape(uint32_t D) {
+  NormShape s;
+  s.lanes = lanes_for(D);
+  const uint64_t spans = spans_for(D, s.lanes);
+  s.nb = spans <= kNormWarps ? 1 : spans <= 2 * kNormWarps ? 2 : spans <= 4 * kNormWarps ? 4 : 5;
+  s.warps = (uint32_t)((spans + s.nb - 1) / s.nb);
+  return s;
+}
+
+// The ring's stages and batches of a pass with `arrays` rows a position, or no stages where
+// two rows do not fit.
+struct NormRing {
+  uint32_t stages, rows, blocks;  // blocks an SM
+  size_t shared;
+};
+inline NormRing norm_ring(uint32_t D, uint32_t es, uint32_t arrays,
+                          uint32_t most_blocks, uint32_t most_rows) {
+  constexpr uint32_t kShared = 224 * 1024, kHead = 2 * 1024;  // of an SM; of a block besides
+  const uint32_t slot = ring_slot(D, es) * arrays;
+  for (uint32_t blocks = most_blocks; blocks > 0; --blocks)
+    for (uint32_t rows = most_rows; rows > 0; rows /= 4) {
+      const uint32_t room = kShared / blocks - 1024 - kHead;
+      uint32_t stages = room / (slot * rows);
+      if (stages > kRingStages) stages = kRingStages;
+      // two stages of four rows, or of one where a block is alone
+      if (stages >= 2 && (rows == 4 || blocks == 1))
+        return {stages, rows, blocks, kHead + (size_t)stages * rows * slot};
+    }
+  return {0, 0, 0, 0};
+}
+
+// Blocks an SM that the ring's kernels may have.
+inline uint32_t ring_blocks(const NormShape &s) {
+  return s.nb > 1 || s.warps > kNormFew ? 1 : std::min<uint32_t>(6, 2 * kNormFew / s.warps);
+}
+
+// ---- sums over a row's lanes ------------------------------------------------------------
+__device__ __forceinline__ float lanes_sum(float v, uint32_t lanes) {
+  for (uint32_t o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+// Barrier of a group of warps.
+__device__ __forceinline__ void group_sync(uint32_t group, uint32_t warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+}
+// K sums over `warps` warps at once, the same in every thread: lanes halve the values
+// they add up as they halve their distance, in the order of lanes_sum.  part: [warps][K].
+template <int K>
+__device__ __forceinline__ void batch_sums(float (&v)[K], float *part, uint32_t warps,
+                                           uint32_t warp, uint32_t lane) {
+#pragma unroll
+  for (int o = 16, n = K; o > 0; o >>= 1) {
+    if (n > 1) {
+      n /= 2;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = lane & o ? v[i] : v[i + n], keep = lane & o ? v[i + n] : v[i];
+        v[i] = keep + __shfl_xor_sync(kFull, give, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(kFull, v[0], o);
+    }
+  }
+  // the value that is left is number (lane / (32 / K)) of them
+  if (lane % (32 / K) == 0) part[warp * K + lane / (32 / K)] = v[0];
+  group_sync(0, warps);
+  float sum = 0.0f;
+  for (uint32_t w = 0; w < warps; ++w) sum += part[w * K + lane % K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = __shfl_sync(kFull, sum, i);
+}
+
+// Eight columns of a weight vector, `otherwise` where there is none.
+template <class E, int V>
+__device__ __forceinline__ void load_vector(const void *p, bool floats, uint32_t c, uint32_t step,
+                                            uint32_t D, float otherwise, Ch<2> (&v)[kOct / 2]) {
+  if (p && floats) {
+    Oct<float, V> x;
+    clear(x);
+    load_oct(x, static_cast<const float *>(p), c, step, D);
+    widen(x, v);
+  } else if (p) {
+    Oct<E, V> x;
+    clear(x);
+    load_oct(x, static_cast<const E *>(p), c, step, D);
+    widen(x, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) v[j] = splat<2>(otherwise);
+  }
+}
+
+// Whether column j of a lane's eight is in the row.
+template <int V>
+__device__ __forceinline__ bool inside(uint32_t c, uint32_t step, uint32_t D, int j) {
+  return c + j / V * step + j % V < D;
+}
+
+// The sum of v over a block, the same in every thread.
+__device__ __forceinline__ float block_sum(float v, float *sums) {
+  v = lanes_sum(v, 32);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int w = 0; w < kWideThreads / 32; ++w) v += sums[w];
+  return v;
+}
+
+// ---- the ring's two sides -----------------------------------------------------------------
+// A row's statistics, and whether it is one that counts, beside it in the ring.
+struct alignas(16) NormHead {
+  float mean, rstd;
+  uint32_t there, unused;
+};
+// Shared memory: barriers, heads, partial sums, and the rows.
+struct NormShared {
+  uint64_t full[kRingStages], empty[kRingStages];
+  NormHead head[kRingStages][4];
+  float part[2][kNormWarps * 8];
+};
+static_assert(sizeof(NormShared) <= 2 * 1024, "what norm_ring leaves for it");
+constexpr uint32_t kNormRows = 2 * 1024;  // where the rows begin
+
+__device__ __forceinline__ char *ring_row(char *shared, uint32_t stage, uint32_t array,
+                                          uint32_t arrays, uint32_t R, uint32_t r, uint32_t slot) {
+  return shared + kNormRows + ((stage * arrays + array) * R + r) * slot;
+}
+
+// The warp that copies: lane r has row r of each batch.  Documents and statistics are read a
+// batch ahead, so that their way does not hold up the copies.
+template <class E, int R, bool kBack>
+__device__ __forceinline__ void produce_rows(const NormParams &p, char *shared) {
+  NormShared &sh = *reinterpret_cast<NormShared *>(shared);
+  const uint32_t lane = threadIdx.x % 32, slot = ring_slot(p.D, sizeof(E));
+  constexpr uint32_t kArrays = kBack ? 2 : 1;
+  if (lane >= R) return;
+  const uint64_t every = (uint64_t)gridDim.x * R;
+  uint64_t n = (uint64_t)blockIdx.x * R + lane;
+  const auto look = [&](uint64_t i) {
+    NormHead h = {0.0f, 0.0f, 0, 0};
+    h.there = i < p.N && !(p.doc && p.doc[i] < 0);
+    if (kBack && i < p.N) h.mean = p.mean[i], h.rstd = p.rstd[i];
+    return h;
+  };
+  NormHead head = look(n);
+  bool lost = false;
+  uint32_t stage = 0, turn = 0;
+  for (; n - lane < p.N; n += every) {
+    const NormHead next = look(n + every);
+    if (turn && !lost && !barrier_wait(&sh.empty[stage], (turn - 1) & 1)) lost = true;
+    sh.head[stage][lane] = head;
+    RingSpan x = {0, 0, 0}, dy = x;
+    char *xs = ring_row(shared, stage, 0, kArrays, R, lane, slot);
+    char *ds = ring_row(shared, stage, kArrays - 1, kArrays, R, lane, slot);
+    if (head.there) {
+      x = ring_span(xs, static_cast<const E *>(p.x) + (int64_t)n * p.x_row, p.D, n == 0,
+                    n + 1 == p.N);
+      if (kBack)
+        dy = ring_span(ds, static_cast<const E *>(p.dy) + (int64_t)n * p.dy_row, p.D, n == 0,
+                       n + 1 == p.N);
+    }
+    barrier_expect(&sh.full[stage], x.bytes() + dy.bytes());  // arrives
+    x.copy(xs, &sh.full[stage]);
+    dy.copy(ds, &sh.full[stage]);
+    head = next;
+    if (++stage == p.stages) stage = 0, ++turn;
+  }
+}
+
+// Barriers, by the first thread; `warps` leave a stage.
+template <int R>
+__device__ __forceinline__ void start_ring(char *shared, uint32_t stages, uint32_t warps) {
+  NormShared &sh = *reinterpret_cast<NormShared *>(shared);
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < stages; ++i) {
+      barrier_init_count(&sh.full[i], R);
+      barrier_init_count(&sh.empty[i], warps);
+    }
+    barrier_fence_init();
+  }
+  __syncthreads();
+}
+
+// ---- launches -----------------------------------------------------------------------
+cudaError_t norm_forward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st);
+cudaError_t norm_backward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st);
+// Rows of partial sums that the backward pass may write.
+uint32_t norm_partials(uint32_t N, uint32_t D);
+
+// By the rows' type and the pieces that all arrays can be moved by.
+template <class F>
+cudaError_t norm_by_type(const ns_norm_inputs &in, int piece, F &&call) {
+  const auto with = [&](auto e) {
+    constexpr int kMost = sizeof(e) == 4 ? 4 : 8;
+    if (piece >= kMost) return call(e, std::integral_constant<int, kMost>{});
+    if (piece >= 2) return call(e, std::integral_constant<int, 2>{});
+    return call(e, std::integral_constant<int, 1>{});
+  };
+  if (in.dtype == NS_F32) return with(float{});
+  if (in.dtype == NS_BF16) return with(__nv_bfloat16{});
+  return with(__half{});
+}
+
+}  // namespace nsk

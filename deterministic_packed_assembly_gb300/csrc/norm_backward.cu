@@ -1,0 +1,435 @@
+// Layer norm, backward: see norm.cu.
+#include "norm.cuh"
+
+namespace nsk {
+namespace {
+
+constexpr int kDirectThreads = 320;  // of rows straight from memory
+constexpr int kColumnWarps = 8;      // of 256 columns' sums
+
+// ---- rows straight from memory -----------------------------------------------------------
+// Groups of `warps` warps (or of `lanes` lanes) walk rows, the next one's loads under way.
+// A row's values as they lie, its statistics, and whether it is one.
+template <class E, int NC, int V>
+struct NormRow {
+  Oct<E, V> x[NC], g[NC];
+  float mean, rstd;
+  bool real, there;
+};
+template <class E, int NC, int V>
+__device__ __forceinline__ void load_row(NormRow<E, NC, V> &r, const NormParams &p, uint64_t n,
+                                         uint32_t first, uint32_t span, uint32_t step) {
+  r.real = n < p.N;
+  r.there = r.real && !(p.doc && p.doc[n] < 0);
+  r.mean = r.rstd = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) clear(r.x[i]), clear(r.g[i]);
+  if (!r.there) return;
+  r.mean = p.mean[n], r.rstd = p.rstd[n];
+  const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
+  const E *dy = static_cast<const E *>(p.dy) + (int64_t)n * p.dy_row;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    load_oct(r.x[i], x, first + i * span, step, p.D);
+    load_oct(r.g[i], dy, first + i * span, step, p.D);
+  }
+}
+
+template <class E, int V>
+__global__ void __launch_bounds__(kDirectThreads, 2) norm_backward_direct_kernel(const NormParams p) {
+  constexpr int NC = 1;
+  __shared__ float2 sums[2][kDirectThreads / 32];
+  extern __shared__ float joined[];  // [2][columns]: the groups' sums
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t group = warp / p.warps, part = warp % p.warps;
+  const uint32_t groups = blockDim.x / 32 / p.warps, per = 32 / p.lanes;
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint32_t first = part * NC * span + lane % p.lanes * V;
+  const float share = 1.0f / (float)p.D;
+  Ch<2> w[NC][kOct / 2], dw[NC][kOct / 2], db[NC][kOct / 2];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) dw[i][j] = db[i][j] = {0.0f, 0.0f};
+    load_vector<E, V>(p.weight, p.floats, first + i * span, step, p.D, 1.0f, w[i]);
+  }
+  const uint64_t every = (uint64_t)gridDim.x * groups * per;
+  uint32_t turn = 0;
+  // a group's lanes stay together: rows from the first lane's on
+  uint64_t n0 = ((uint64_t)blockIdx.x * groups + group) * per;
+  NormRow<E, NC, V> row;
+  load_row(row, p, n0 + lane / p.lanes, first, span, step);
+  for (; n0 < p.N; n0 += every) {
+    NormRow<E, NC, V> next;
+    load_row(next, p, n0 + every + lane / p.lanes, first, span, step);
+    const Ch<2> minus = splat<2>(-row.mean), scale = splat<2>(row.rstd);
+    Ch<2> s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      Ch<2> f[kOct / 2], g[kOct / 2];
+      widen(row.x[i], f);
+      widen(row.g[i], g);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) {
+        const Ch<2> xh = (f[j] + minus) * scale, gw = g[j] * w[i][j];
+        s1 = s1 + gw;
+        s2 = fma(gw, xh, s2);
+        dw[i][j] = fma(g[j], xh, dw[i][j]);
+        db[i][j] = db[i][j] + g[j];
+      }
+    }
+    float a = lanes_sum(s1.v[0] + s1.v[1], p.lanes), b = lanes_sum(s2.v[0] + s2.v[1], p.lanes);
+    if (p.warps > 1) {  // two buffers: one barrier a row
+      if (lane == 0) sums[turn][warp] = make_float2(a, b);
+      group_sync(group, p.warps);
+      a = b = 0.0f;
+      for (uint32_t k = 0; k < p.warps; ++k) {
+        const float2 v = sums[turn][group * p.warps + k];
+        a += v.x, b += v.y;
+      }
+      turn ^= 1;
+    }
+    const Ch<2> m1 = splat<2>(-a * share), m2 = splat<2>(-b * share);
+    if (row.real) {
+      E *dx = static_cast<E *>(p.y) + (int64_t)(n0 + lane / p.lanes) * p.D;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        Ch<2> f[kOct / 2], g[kOct / 2];
+        forget(row.x[i]), forget(row.g[i]);
+        widen(row.x[i], f);
+        widen(row.g[i], g);
+#pragma unroll
+        for (int j = 0; j < kOct / 2; ++j) {
+          const Ch<2> xh = (f[j] + minus) * scale;
+          f[j] = scale * fma(xh, m2, fma(g[j], w[i][j], m1));
+          if (!row.there) f[j] = {0.0f, 0.0f};
+        }
+        store_oct(dx, first + i * span, step, p.D, narrow<E, V>(f));
+      }
+    }
+    row = next;
+  }
+  if (!p.partial) return;
+  // lanes that share columns, then groups that do, in order
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j)
+      for (uint32_t o = p.lanes; o < 32; o <<= 1)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          dw[i][j].v[h] += __shfl_xor_sync(kFull, dw[i][j].v[h], o);
+          db[i][j].v[h] += __shfl_xor_sync(kFull, db[i][j].v[h], o);
+        }
+  const uint32_t columns = p.warps * NC * span;
+  for (uint32_t g = 0; g < groups; ++g) {
+    if (g == group && lane < p.lanes) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < kOct; ++j) {
+          float *a = joined + first + i * span + j / V * step + j % V, *b = a + columns;
+          const float u = dw[i][j / 2].v[j & 1], v = db[i][j / 2].v[j & 1];
+          *a = g ? *a + u : u;
+          *b = g ? *b + v : v;
+        }
+    }
+    __syncthreads();
+  }
+  float *to = p.partial + (uint64_t)blockIdx.x * 2 * p.D;
+  for (uint32_t c = threadIdx.x; c < p.D; c += blockDim.x) {
+    to[c] = joined[c];
+    to[p.D + c] = joined[columns + c];
+  }
+}
+
+// ---- rows through the ring -----------------------------------------------------------------
+// All warps but the last take a batch of R rows together, NB spans each, and keep the sums of
+// their columns' dw and db.  The batch is read from shared memory twice: for the rows' two
+// sums, exchanged for all R at once, and for dx.
+template <class E, int NB, int V, int R, int kWarps>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
+    norm_backward_ring_kernel(const NormParams p) {
+  extern __shared__ __align__(128) char shared[];
+  NormShared &sh = *reinterpret_cast<NormShared *>(shared);
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  start_ring<R>(shared, p.stages, p.warps);
+  if (warp == p.warps) {
+    produce_rows<E, R, true>(p, shared);
+    return;
+  }
+  constexpr uint32_t kSpan = 32 * kOct, kStep = 32 * V;
+  const uint32_t first = warp * NB * kSpan + lane * V, slot = ring_slot(p.D, sizeof(E));
+  const float share = 1.0f / (float)p.D;
+  // the weights of up to two spans stay in registers, more are read where they are used
+  constexpr int kHeld = NB <= 2 ? NB : 1;
+  Ch<2> w[kHeld][kOct / 2], dw[NB][kOct / 2], db[NB][kOct / 2];
+  const auto weights = [&](int i) {
+    load_vector<E, V>(p.weight, p.floats, first + i * kSpan, kStep, p.D, 1.0f, w[i % kHeld]);
+  };
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) dw[i][j] = db[i][j] = {0.0f, 0.0f};
+    if constexpr (kHeld == NB) weights(i);
+  }
+  bool lost = false;
+  uint32_t stage = 0, turn = 0, buffer = 0;
+  for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
+    if (!lost && !barrier_wait(&sh.full[stage], turn & 1)) lost = true;
+    const char *xr[R], *gr[R];
+    float v[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      uint32_t xo = 0, go = 0;
+      if constexpr (Oct<E, V>::kBytes < 16) {
+        xo = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
+                                                   (int64_t)(n0 + r) * p.x_row) & 15u;
+        go = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.dy) +
+                                                   (int64_t)(n0 + r) * p.dy_row) & 15u;
+      }
+      xr[r] = ring_row(shared, stage, 0, 2, R, r, slot) + xo;
+      gr[r] = ring_row(shared, stage, 1, 2, R, r, slot) + go;
+      const NormHead head = sh.head[stage][r];
+      Ch<2> s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
+      if (head.there) {
+        const Ch<2> minus = splat<2>(-head.mean), scale = splat<2>(head.rstd);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          Oct<E, V> x, y;
+          Ch<2> f[kOct / 2], g[kOct / 2];
+          ring_oct(x, xr[r], first + i * kSpan, kStep, p.D);
+          ring_oct(y, gr[r], first + i * kSpan, kStep, p.D);
+          if constexpr (kHeld < NB) weights(i);
+          widen(x, f);
+          widen(y, g);
+#pragma unroll
+          for (int j = 0; j < kOct / 2; ++j) {
+            const Ch<2> xh = (f[j] + minus) * scale, gw = g[j] * w[i % kHeld][j];
+            s1 = s1 + gw;
+            s2 = fma(gw, xh, s2);
+            dw[i][j] = fma(g[j], xh, dw[i][j]);
+            db[i][j] = db[i][j] + g[j];
+          }
+        }
+      }
+      v[2 * r] = s1.v[0] + s1.v[1], v[2 * r + 1] = s2.v[0] + s2.v[1];
+    }
+    batch_sums<2 * R>(v, sh.part[buffer], p.warps, warp, lane);
+    buffer ^= 1;  // two buffers: one barrier a batch
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t n = n0 + r;
+      if (n >= p.N) break;
+      const NormHead head = sh.head[stage][r];
+      const Ch<2> minus = splat<2>(-head.mean), scale = splat<2>(head.rstd);
+      const Ch<2> m1 = splat<2>(-v[2 * r] * share), m2 = splat<2>(-v[2 * r + 1] * share);
+      E *dx = static_cast<E *>(p.y) + (int64_t)n * p.D;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        Oct<E, V> x, y;
+        Ch<2> f[kOct / 2], g[kOct / 2];
+        ring_oct(x, xr[r], first + i * kSpan, kStep, p.D);
+        ring_oct(y, gr[r], first + i * kSpan, kStep, p.D);
+        if constexpr (kHeld < NB) weights(i);
+        widen(x, f);
+        widen(y, g);
+#pragma unroll
+        for (int j = 0; j < kOct / 2; ++j) {
+          const Ch<2> xh = (f[j] + minus) * scale;
+          f[j] = scale * fma(xh, m2, fma(g[j], w[i % kHeld][j], m1));
+          if (!head.there) f[j] = {0.0f, 0.0f};
+        }
+        store_oct(dx, first + i * kSpan, kStep, p.D, narrow<E, V>(f));
+      }
+    }
+    __syncwarp();
+    if (lane == 0) barrier_arrive(&sh.empty[stage]);
+    if (++stage == p.stages) stage = 0, ++turn;
+  }
+  if (!p.partial) return;
+  float *to = p.partial + (uint64_t)blockIdx.x * 2 * p.D;
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < kOct; ++j) {
+      const uint32_t c = first + i * kSpan + j / V * kStep + j % V;
+      if (c < p.D) to[c] = dw[i][j / 2].v[j & 1], to[p.D + c] = db[i][j / 2].v[j & 1];
+    }
+}
+
+// ---- rows of any width -----------------------------------------------------------------------
+// A block a row of any width, read twice.
+template <class E, int V>
+__global__ void __launch_bounds__(kWideThreads) norm_backward_wide_kernel(const NormParams p) {
+  __shared__ float sums[kWideThreads / 32];
+  const uint32_t n = blockIdx.x, lane = threadIdx.x % 32, D = p.D;
+  const bool there = !(p.doc && p.doc[n] < 0);
+  const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
+  const E *dy = static_cast<const E *>(p.dy) + (int64_t)n * p.dy_row;
+  E *dx = static_cast<E *>(p.y) + (int64_t)n * D;
+  constexpr uint32_t kStep = 32 * V, kAll = kWideThreads * kOct;
+  const uint32_t c0 = threadIdx.x / 32 * 32 * kOct + lane * V;
+  Ch<2> s1 = {0.0f, 0.0f}, s2 = s1, minus = s1, scale = s1, m1 = s1, m2 = s1;
+  Ch<2> f[kOct / 2], g[kOct / 2], w[kOct / 2];
+  Oct<E, V> xv, gv;
+  clear(xv), clear(gv);
+  if (there) {
+    minus = splat<2>(-p.mean[n]), scale = splat<2>(p.rstd[n]);
+    for (uint32_t c = c0; c < D; c += kAll) {
+      clear(gv);
+      load_oct(xv, x, c, kStep, D);
+      load_oct(gv, dy, c, kStep, D);
+      load_vector<E, V>(p.weight, p.floats, c, kStep, D, 1.0f, w);
+      widen(xv, f);
+      widen(gv, g);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) {
+        const Ch<2> gw = g[j] * w[j];
+        s1 = s1 + gw;
+        s2 = fma(gw, (f[j] + minus) * scale, s2);
+      }
+    }
+    m1 = splat<2>(-block_sum(s1.v[0] + s1.v[1], sums) / (float)D);
+    m2 = splat<2>(-block_sum(s2.v[0] + s2.v[1], sums) / (float)D);
+  }
+  for (uint32_t c = c0; c < D; c += kAll) {
+    if (there) {
+      load_oct(xv, x, c, kStep, D);
+      load_oct(gv, dy, c, kStep, D);
+    }
+    load_vector<E, V>(p.weight, p.floats, c, kStep, D, 1.0f, w);
+    widen(xv, f);
+    widen(gv, g);
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) {
+      f[j] = scale * fma((f[j] + minus) * scale, m2, fma(g[j], w[j], m1));
+      if (!there) f[j] = {0.0f, 0.0f};
+    }
+    store_oct(dx, c, kStep, D, narrow<E, V>(f));
+  }
+}
+
+// Rows y, y + blocks, ... of 256 columns.
+template <class E, int V>
+__global__ void __launch_bounds__(32 * kColumnWarps) norm_columns_kernel(const NormParams p) {
+  __shared__ float sums[kColumnWarps][2][32 * kOct];
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t c = blockIdx.x * 32 * kOct + lane * V;
+  Ch<2> dw[kOct / 2], db[kOct / 2];
+#pragma unroll
+  for (int j = 0; j < kOct / 2; ++j) dw[j] = db[j] = {0.0f, 0.0f};
+#pragma unroll 2
+  for (uint64_t n = (uint64_t)blockIdx.y * kColumnWarps + warp; n < p.N;
+       n += (uint64_t)gridDim.y * kColumnWarps) {
+    if (p.doc && p.doc[n] < 0) continue;
+    Oct<E, V> xv, gv;
+    clear(xv), clear(gv);
+    load_oct(xv, static_cast<const E *>(p.x) + (int64_t)n * p.x_row, c, 32 * V, p.D);
+    load_oct(gv, static_cast<const E *>(p.dy) + (int64_t)n * p.dy_row, c, 32 * V, p.D);
+    const Ch<2> minus = splat<2>(-p.mean[n]), scale = splat<2>(p.rstd[n]);
+    Ch<2> f[kOct / 2], g[kOct / 2];
+    widen(xv, f);
+    widen(gv, g);
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) {
+      dw[j] = fma(g[j], (f[j] + minus) * scale, dw[j]);
+      db[j] = db[j] + g[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kOct; ++j) {
+    sums[warp][0][j / V * 32 * V + lane * V + j % V] = dw[j / 2].v[j & 1];
+    sums[warp][1][j / V * 32 * V + lane * V + j % V] = db[j / 2].v[j & 1];
+  }
+  __syncthreads();
+  const uint64_t col = (uint64_t)blockIdx.x * 32 * kOct + threadIdx.x;
+  if (col < p.D) {
+    float a = 0.0f, b = 0.0f;
+    for (int k = 0; k < kColumnWarps; ++k) a += sums[k][0][threadIdx.x], b += sums[k][1][threadIdx.x];
+    float *to = p.partial + (uint64_t)blockIdx.y * 2 * p.D;
+    to[col] = a, to[p.D + col] = b;
+  }
+}
+
+// ---- launches -----------------------------------------------------------------------
+template <class E, int NB, int V, int R, int kWarps>
+cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
+  auto *k = norm_backward_ring_kernel<E, NB, V, R, kWarps>;
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void *>(k), true);
+  if (e != cudaSuccess) return e;
+  p.stages = ring.stages;
+  const uint64_t batches = ((uint64_t)p.N + R - 1) / R;
+  p.blocks = (uint32_t)std::min<uint64_t>(batches, ring.blocks * kNormSMs);
+  ++launch_counter();
+  k<<<p.blocks, 32 * (p.warps + 1), ring.shared, st>>>(p);
+  return cudaGetLastError();
+}
+template <class E, int NB, int V, int kWarps>
+cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
+  if constexpr (NB <= 2)
+    if (ring.rows == 4) return launch_ring<E, NB, V, 4, kWarps>(p, ring, st);
+  return launch_ring<E, NB, V, 1, kWarps>(p, ring, st);
+}
+// A block's warps decide how many registers a thread may have, and how many blocks an SM.
+template <class E, int V>
+cudaError_t launch_ring(NormParams &p, const NormShape &s, const NormRing &ring, cudaStream_t st) {
+  if (s.nb == 1 && s.warps <= kNormFew) return launch_ring<E, 1, V, 4, kNormFew>(p, ring, st);
+  if (s.nb == 1) return launch_ring<E, 1, V, kNormWarps>(p, ring, st);
+  if (s.nb == 2) return launch_ring<E, 2, V, kNormWarps>(p, ring, st);
+  if (s.nb == 4) return launch_ring<E, 4, V, kNormWarps>(p, ring, st);
+  return launch_ring<E, 5, V, kNormWarps>(p, ring, st);
+}
+
+template <class E, int V>
+cudaError_t wide_of(NormParams &p, cudaStream_t st) {
+  ++launch_counter();
+  norm_backward_wide_kernel<E, V><<<p.N, kWideThreads, 0, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.partial) return e;
+  // blocks of 256 columns: enough to fill the SMs, each with rows for its warps
+  const uint32_t spans = (p.D + 32 * kOct - 1) / (32 * kOct);
+  const uint64_t most = ((uint64_t)p.N + 4 * kColumnWarps - 1) / (4 * kColumnWarps);
+  p.blocks = (uint32_t)std::min<uint64_t>(most, (8 * kNormSMs + spans - 1) / spans);
+  ++launch_counter();
+  norm_columns_kernel<E, V><<<dim3(spans, p.blocks), 32 * kColumnWarps, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <class E, int V>
+cudaError_t direct_of(NormParams &p, cudaStream_t st) {
+  const uint32_t groups = kDirectThreads / 32 / p.warps, rows = groups * (32 / p.lanes);
+  p.blocks = (uint32_t)std::min<uint64_t>(((uint64_t)p.N + rows - 1) / rows, 2 * kNormSMs);
+  const size_t shared = 2 * sizeof(float) * p.warps * p.lanes * kOct;
+  ++launch_counter();
+  norm_backward_direct_kernel<E, V><<<p.blocks, groups * p.warps * 32, shared, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <class E, int V>
+cudaError_t backward_of(NormParams &p, cudaStream_t st) {
+  const NormShape s = norm_shape(p.D);
+  p.lanes = s.lanes, p.warps = s.warps;
+  if (p.D <= kNormNarrow) return direct_of<E, V>(p, st);
+  const NormRing ring = norm_ring(p.D, sizeof(E), 2, ring_blocks(s), s.nb <= 2 ? 4 : 1);
+  if (p.D > kNormKept || !ring.stages) return wide_of<E, V>(p, st);
+  return launch_ring<E, V>(p, s, ring, st);
+}
+
+}  // namespace
+
+uint32_t norm_partials(uint32_t N, uint32_t D) {
+  // as many blocks as any of the kernels has, of which each has a row at least
+  if (D <= kNormNarrow) return std::min(N, 2 * kNormSMs);
+  const uint32_t spans = (D + 32 * kOct - 1) / (32 * kOct);
+  const uint32_t ring = ring_blocks(norm_shape(D)) * kNormSMs;
+  return std::min(N, std::max(ring, (8 * kNormSMs + spans - 1) / spans));
+}
+
+cudaError_t norm_backward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st) {
+  return norm_by_type(in, piece, [&](auto e, auto v) {
+    return backward_of<decltype(e), decltype(v)::value>(p, st);
+  });
+}
+
+}  // namespace nsk

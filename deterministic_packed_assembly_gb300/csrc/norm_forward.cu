@@ -1,0 +1,336 @@
+// Layer norm, forward: see norm.cu.
+#include "norm.cuh"
+
+namespace nsk {
+namespace {
+
+constexpr int kDirectWarps = 8;  // of a block of rows of up to as many warps
+
+// ---- rows straight from memory -----------------------------------------------------------
+// Rows of `lanes` lanes of a warp, or of `warps` warps; a lane has NB spans of each.
+template <class E, int NB, int V>
+__global__ void __launch_bounds__(32 * kNormWarps) norm_direct_kernel(const NormParams p) {
+  __shared__ float sums[2][kNormWarps];
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t group = warp / p.warps, part = warp % p.warps;
+  const uint32_t groups = blockDim.x / 32 / p.warps, per = 32 / p.lanes;
+  const uint64_t n = ((uint64_t)blockIdx.x * groups + group) * per + lane / p.lanes;
+  const bool real = n < p.N, there = real && !(p.doc && p.doc[n] < 0);
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint32_t first = part * NB * span + lane % p.lanes * V;
+  const E *x = static_cast<const E *>(p.x) + (int64_t)(real ? n : 0) * p.x_row;
+  E *y = static_cast<E *>(p.y) + (int64_t)(real ? n : 0) * p.D;
+  const float share = 1.0f / (float)p.D;
+  Oct<E, V> v[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    clear(v[i]);
+    if (there) load_oct(v[i], x, first + i * span, step, p.D);
+  }
+  Ch<2> two = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    Ch<2> f[kOct / 2];
+    widen(v[i], f);
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
+  }
+  float sum = lanes_sum(two.v[0] + two.v[1], p.lanes);
+  if (p.warps > 1) {
+    if (lane == 0) sums[0][warp] = sum;
+    group_sync(group, p.warps);
+    sum = 0.0f;
+    for (uint32_t w = 0; w < p.warps; ++w) sum += sums[0][group * p.warps + w];
+  }
+  const float mean = sum * share;
+  const Ch<2> minus = splat<2>(-mean);
+  two = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const uint32_t c = first + i * span;
+    Ch<2> f[kOct / 2];
+    forget(v[i]);
+    widen(v[i], f);
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) {
+      Ch<2> d = f[j] + minus;
+      if (!inside<V>(c, step, p.D, 2 * j)) d.v[0] = 0.0f;
+      if (!inside<V>(c, step, p.D, 2 * j + 1)) d.v[1] = 0.0f;
+      two = fma(d, d, two);
+    }
+  }
+  float square = lanes_sum(two.v[0] + two.v[1], p.lanes);
+  if (p.warps > 1) {
+    if (lane == 0) sums[1][warp] = square;
+    group_sync(group, p.warps);
+    square = 0.0f;
+    for (uint32_t w = 0; w < p.warps; ++w) square += sums[1][group * p.warps + w];
+  }
+  const float rstd = __frsqrt_rn(fmaf(square, share, p.eps));
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const uint32_t c = first + i * span;
+    if (c >= p.D) break;
+    Ch<2> f[kOct / 2], w[kOct / 2], b[kOct / 2];
+    load_vector<E, V>(p.weight, p.floats, c, step, p.D, 1.0f, w);
+    load_vector<E, V>(p.bias, p.floats, c, step, p.D, 0.0f, b);
+    forget(v[i]);
+    widen(v[i], f);
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) {
+      f[j] = fma((f[j] + minus) * splat<2>(rstd), w[j], b[j]);
+      if (!there) f[j] = {0.0f, 0.0f};
+    }
+    if (real) store_oct(y, c, step, p.D, narrow<E, V>(f));
+  }
+  if (real && part == 0 && lane % p.lanes == 0) {
+    if (p.mean) p.mean[n] = there ? mean : 0.0f;
+    if (p.rstd) p.rstd[n] = there ? rstd : 0.0f;
+  }
+}
+
+// ---- rows through the ring -----------------------------------------------------------------
+// All warps but the last take a batch of R rows together, NB spans each: sums, squares and
+// outputs read the batch from shared memory anew, and a batch's sums are exchanged at once.
+template <class E, int NB, int V, int R, int kWarps>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
+    norm_ring_kernel(const NormParams p) {
+  extern __shared__ __align__(128) char shared[];
+  NormShared &sh = *reinterpret_cast<NormShared *>(shared);
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  start_ring<R>(shared, p.stages, p.warps);
+  if (warp == p.warps) {
+    produce_rows<E, R, false>(p, shared);
+    return;
+  }
+  constexpr uint32_t kSpan = 32 * kOct, kStep = 32 * V;
+  const uint32_t first = warp * NB * kSpan + lane * V, slot = ring_slot(p.D, sizeof(E));
+  const float share = 1.0f / (float)p.D;
+  // the weights of up to two spans stay in registers, more are read where they are used
+  constexpr int kHeld = NB <= 2 ? NB : 1;
+  Ch<2> w[kHeld][kOct / 2], b[kHeld][kOct / 2];
+  const auto weights = [&](int i) {
+    const uint32_t c = first + i * kSpan;
+    load_vector<E, V>(p.weight, p.floats, c, kStep, p.D, 1.0f, w[i % kHeld]);
+    load_vector<E, V>(p.bias, p.floats, c, kStep, p.D, 0.0f, b[i % kHeld]);
+  };
+  if constexpr (kHeld == NB) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) weights(i);
+  }
+  const bool all = warp * NB * kSpan + NB * kSpan <= p.D;  // no lane beyond the row
+  bool lost = false;
+  uint32_t stage = 0, turn = 0;
+  for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
+    if (!lost && !barrier_wait(&sh.full[stage], turn & 1)) lost = true;
+    const char *row[R];
+    bool there[R];
+    float v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t off =
+          Oct<E, V>::kBytes >= 16
+              ? 0
+              : (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
+                                                      (int64_t)(n0 + r) * p.x_row) & 15u;
+      row[r] = ring_row(shared, stage, 0, 1, R, r, slot) + off;
+      there[r] = sh.head[stage][r].there;
+      Ch<2> two = {0.0f, 0.0f};
+      if (there[r]) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          Oct<E, V> x;
+          Ch<2> f[kOct / 2];
+          ring_oct(x, row[r], first + i * kSpan, kStep, p.D);
+          widen(x, f);
+#pragma unroll
+          for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
+        }
+      }
+      v[r] = two.v[0] + two.v[1];
+    }
+    batch_sums<R>(v, sh.part[0], p.warps, warp, lane);
+    float mean[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = v[r] * share;
+      const Ch<2> minus = splat<2>(-mean[r]);
+      Ch<2> two = {0.0f, 0.0f};
+      if (there[r]) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const uint32_t c = first + i * kSpan;
+          Oct<E, V> x;
+          Ch<2> f[kOct / 2];
+          ring_oct(x, row[r], c, kStep, p.D);
+          widen(x, f);
+#pragma unroll
+          for (int j = 0; j < kOct / 2; ++j) {
+            Ch<2> d = f[j] + minus;
+            if (!all) {
+              if (!inside<V>(c, kStep, p.D, 2 * j)) d.v[0] = 0.0f;
+              if (!inside<V>(c, kStep, p.D, 2 * j + 1)) d.v[1] = 0.0f;
+            }
+            two = fma(d, d, two);
+          }
+        }
+      }
+      v[r] = two.v[0] + two.v[1];
+    }
+    batch_sums<R>(v, sh.part[1], p.warps, warp, lane);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t n = n0 + r;
+      if (n >= p.N) break;
+      const float rstd = __frsqrt_rn(fmaf(v[r], share, p.eps));
+      const Ch<2> minus = splat<2>(-mean[r]), scale = splat<2>(rstd);
+      E *y = static_cast<E *>(p.y) + (int64_t)n * p.D;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t c = first + i * kSpan;
+        Oct<E, V> x;
+        Ch<2> f[kOct / 2];
+        if constexpr (kHeld < NB) weights(i);
+        ring_oct(x, row[r], c, kStep, p.D);
+        widen(x, f);
+#pragma unroll
+        for (int j = 0; j < kOct / 2; ++j) {
+          f[j] = fma((f[j] + minus) * scale, w[i % kHeld][j], b[i % kHeld][j]);
+          if (!there[r]) f[j] = {0.0f, 0.0f};
+        }
+        store_oct(y, c, kStep, p.D, narrow<E, V>(f));
+      }
+      if (threadIdx.x == 0) {
+        if (p.mean) p.mean[n] = there[r] ? mean[r] : 0.0f;
+        if (p.rstd) p.rstd[n] = there[r] ? rstd : 0.0f;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) barrier_arrive(&sh.empty[stage]);
+    if (++stage == p.stages) stage = 0, ++turn;
+  }
+}
+
+// ---- rows of any width -----------------------------------------------------------------------
+// A block a row, read three times.
+template <class E, int V>
+__global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParams p) {
+  __shared__ float sums[kWideThreads / 32];
+  const uint32_t n = blockIdx.x, lane = threadIdx.x % 32, D = p.D;
+  const bool there = !(p.doc && p.doc[n] < 0);
+  const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
+  E *y = static_cast<E *>(p.y) + (int64_t)n * D;
+  constexpr uint32_t kStep = 32 * V, kAll = kWideThreads * kOct;
+  const uint32_t c0 = threadIdx.x / 32 * 32 * kOct + lane * V;
+  const float share = 1.0f / (float)D;
+  float mean = 0.0f, rstd = 0.0f;
+  Ch<2> f[kOct / 2], two = {0.0f, 0.0f};
+  Oct<E, V> v;
+  clear(v);
+  if (there) {
+    for (uint32_t c = c0; c < D; c += kAll) {
+      clear(v);
+      load_oct(v, x, c, kStep, D);
+      widen(v, f);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
+    }
+    mean = block_sum(two.v[0] + two.v[1], sums) * share;
+    two = {0.0f, 0.0f};
+    for (uint32_t c = c0; c < D; c += kAll) {
+      load_oct(v, x, c, kStep, D);
+      widen(v, f);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) {
+        Ch<2> d = f[j] + splat<2>(-mean);
+        if (!inside<V>(c, kStep, D, 2 * j)) d.v[0] = 0.0f;
+        if (!inside<V>(c, kStep, D, 2 * j + 1)) d.v[1] = 0.0f;
+        two = fma(d, d, two);
+      }
+    }
+    rstd = __frsqrt_rn(fmaf(block_sum(two.v[0] + two.v[1], sums), share, p.eps));
+  }
+  for (uint32_t c = c0; c < D; c += kAll) {
+    Ch<2> w[kOct / 2], b[kOct / 2];
+    load_vector<E, V>(p.weight, p.floats, c, kStep, D, 1.0f, w);
+    load_vector<E, V>(p.bias, p.floats, c, kStep, D, 0.0f, b);
+    if (there) load_oct(v, x, c, kStep, D);
+    widen(v, f);
+#pragma unroll
+    for (int j = 0; j < kOct / 2; ++j) {
+      f[j] = fma((f[j] + splat<2>(-mean)) * splat<2>(rstd), w[j], b[j]);
+      if (!there) f[j] = {0.0f, 0.0f};
+    }
+    store_oct(y, c, kStep, D, narrow<E, V>(f));
+  }
+  if (threadIdx.x == 0) {
+    if (p.mean) p.mean[n] = mean;
+    if (p.rstd) p.rstd[n] = rstd;
+  }
+}
+
+// ---- launches -----------------------------------------------------------------------
+template <class E, int NB, int V, int R, int kWarps>
+cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
+  auto *k = norm_ring_kernel<E, NB, V, R, kWarps>;
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void *>(k), true);
+  if (e != cudaSuccess) return e;
+  p.stages = ring.stages;
+  const uint64_t batches = ((uint64_t)p.N + R - 1) / R;
+  const uint32_t blocks = (uint32_t)std::min<uint64_t>(batches, ring.blocks * kNormSMs);
+  ++launch_counter();
+  k<<<blocks, 32 * (p.warps + 1), ring.shared, st>>>(p);
+  return cudaGetLastError();
+}
+template <class E, int NB, int V, int kWarps>
+cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
+  if constexpr (NB <= 2)
+    if (ring.rows == 4) return launch_ring<E, NB, V, 4, kWarps>(p, ring, st);
+  return launch_ring<E, NB, V, 1, kWarps>(p, ring, st);
+}
+// A block's warps decide how many registers a thread may have, and how many blocks an SM.
+template <class E, int V>
+cudaError_t launch_ring(NormParams &p, const NormShape &s, const NormRing &ring, cudaStream_t st) {
+  if (s.nb == 1 && s.warps <= kNormFew) return launch_ring<E, 1, V, 4, kNormFew>(p, ring, st);
+  if (s.nb == 1) return launch_ring<E, 1, V, kNormWarps>(p, ring, st);
+  if (s.nb == 2) return launch_ring<E, 2, V, kNormWarps>(p, ring, st);
+  if (s.nb == 4) return launch_ring<E, 4, V, kNormWarps>(p, ring, st);
+  return launch_ring<E, 5, V, kNormWarps>(p, ring, st);
+}
+
+template <class E, int V>
+cudaError_t forward_of(NormParams &p, cudaStream_t st) {
+  if (p.D > kNormKept) {
+    ++launch_counter();
+    norm_wide_kernel<E, V><<<p.N, kWideThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  const NormShape s = norm_shape(p.D);
+  p.lanes = s.lanes, p.warps = s.warps;
+  // rows that fill the SMs' rings, else straight from memory: a call of 64 rows waits for
+  // nothing but its own loads
+  if (p.D > kNormNarrow && p.N > 4 * kNormSMs) {
+    const NormRing ring = norm_ring(p.D, sizeof(E), 1, ring_blocks(s), s.nb <= 2 ? 4 : 1);
+    if (ring.stages) return launch_ring<E, V>(p, s, ring, st);
+  }
+  const uint32_t groups = std::max<uint32_t>(1, kDirectWarps / p.warps);
+  const uint32_t threads = groups * p.warps * 32, rows = groups * (32 / p.lanes);
+  const uint32_t blocks = (uint32_t)(((uint64_t)p.N + rows - 1) / rows);
+  ++launch_counter();
+  auto *k = s.nb == 1   ? norm_direct_kernel<E, 1, V>
+            : s.nb == 2 ? norm_direct_kernel<E, 2, V>
+            : s.nb == 4 ? norm_direct_kernel<E, 4, V>
+                        : norm_direct_kernel<E, 5, V>;
+  k<<<blocks, threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t norm_forward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st) {
+  return norm_by_type(in, piece, [&](auto e, auto v) {
+    return forward_of<decltype(e), decltype(v)::value>(p, st);
+  });
+}
+
+}  // namespace nsk
