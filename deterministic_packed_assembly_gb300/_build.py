@@ -17,7 +17,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnspack.so")
 SOURCES = ("api.cu", "init_kernels.cu", "gather.cu", "learned.cu", "noalloc.cu", "probe.cu",
            "scan.cu", "distill.cu", "route.cu", "train_api.cu", "order.cu", "embed.cu", "norm.cu",
-           "norm_forward.cu", "norm_backward.cu", "experts.cu")
+           "norm_f32.cu", "norm_bf16.cu", "norm_f16.cu", "experts.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -6,7 +6,7 @@
 //
 // Memory bounds both passes, and next to it instructions: they go by pairs of values
 // (elem.cuh).  A row's columns lie on threads in one way, whatever kernel takes it: eight a
-// lane (rows.cuh), up to 15 warps and five spans a warp.  The variance is taken from the
+// lane (rows.cuh), up to 15 warps and five spans a warp (norm.cuh).  The variance is taken from the
 // values less their mean, so that a mean far from 0 costs no digits.
 //
 // Rows come through a ring in shared memory (ring.cuh), filled by the bulk copy engine, so
@@ -53,6 +53,12 @@ NormParams params_of(const ns_norm_inputs &in) {
   p.N = in.N, p.D = in.D, p.eps = in.eps, p.floats = in.weight_dtype == NS_F32;
   return p;
 }
+// By the rows' type.
+template <class F>
+cudaError_t by_type(const ns_norm_inputs &in, F &&call) {
+  if (in.dtype == NS_F32) return call(float{});
+  return in.dtype == NS_BF16 ? call(__nv_bfloat16{}) : call(__half{});
+}
 int piece_of_inputs(const ns_norm_inputs &in, const void *y) {
   const uint64_t es = in.dtype == NS_F32 ? 4 : 2, ws = in.weight_dtype == NS_F32 ? 4 : 2;
   return std::min(std::min(piece_of(in.x, in.x_row, in.D, es), piece_of(y, in.D, in.D, es)),
@@ -62,14 +68,18 @@ int piece_of_inputs(const ns_norm_inputs &in, const void *y) {
 }  // namespace
 
 uint64_t norm_workspace(uint32_t N, uint32_t D) {
-  return (uint64_t)norm_partials(N, D) * 2 * D * sizeof(float);
+  // rows of partial sums: as many as any kernel has blocks, of which each has a row at least
+  uint32_t rows = 4 * kNormSMs;
+  if (D > kNormNarrow) rows = std::max<uint32_t>(rows, 8 * kNormSMs * 256 / D + 1);
+  return (uint64_t)std::min(N, rows) * 2 * D * sizeof(float);
 }
 
 cudaError_t launch_norm_forward(const ns_norm_inputs &in, void *y, float *mean, float *rstd,
                                 cudaStream_t st) {
   NormParams p = params_of(in);
   p.y = y, p.mean = mean, p.rstd = rstd;
-  return norm_forward(p, in, piece_of_inputs(in, y), st);
+  const int piece = piece_of_inputs(in, y);
+  return by_type(in, [&](auto e) { return norm_forward<decltype(e)>(p, piece, st); });
 }
 
 cudaError_t launch_norm_backward(const ns_norm_inputs &in, const float *mean, const float *rstd,
@@ -81,7 +91,9 @@ cudaError_t launch_norm_backward(const ns_norm_inputs &in, const float *mean, co
   p.partial = dweight || dbias ? partial : nullptr;
   const int piece =
       std::min(piece_of_inputs(in, dx), piece_of(dy, dy_row, in.D, in.dtype == NS_F32 ? 4 : 2));
-  const cudaError_t e = in.N ? norm_backward(p, in, piece, st) : cudaSuccess;
+  const cudaError_t e =
+      in.N ? by_type(in, [&](auto e) { return norm_backward<decltype(e)>(p, piece, st); })
+           : cudaSuccess;
   if (e != cudaSuccess || (!dweight && !dbias)) return e;
   const dim3 grid((in.D + 31) / 32, 2);
   ++launch_counter();

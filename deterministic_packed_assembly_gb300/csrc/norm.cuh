@@ -21,7 +21,6 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNormNarrow = 512;   // columns up to which rows go without the ring
 constexpr uint32_t kNormWarps = 15;     // of a row, at most: with the one that copies 512 threads
 constexpr uint32_t kNormKept = 5 * 32 * kOct * kNormWarps;  // columns that they have registers for
-constexpr int kNormFew = 10;            // warps of a block of which an SM has two at least
 constexpr int kWideThreads = 512;       // of a row of more columns
 
 struct NormParams {
@@ -41,44 +40,39 @@ struct NormParams {
 };
 
 // How a row lies on threads, by its columns alone: what a row gets does not depend on
-// the kernel that takes it.
+// the kernel that takes it.  nb spans a warp: forward as many as leave five warps (a row's
+// exchange of sums costs each of its warps the same; 32768 x 2560 bf16: ten warps 90 us, five FIVE),
+// backward as few as leave fifteen, whose sums take registers.
 struct NormShape {
-  uint32_t lanes, nb, warps;  // nb spans a warp
+  uint32_t lanes, nb, warps;
 };
-inline NormShape norm_shape(uint32_t D) {
+inline NormShape norm_shape(uint32_t D, bool back) {
   NormShape s;
   s.lanes = lanes_for(D);
   const uint64_t spans = spans_for(D, s.lanes);
-  s.nb = spans <= kNormWarps ? 1 : spans <= 2 * kNormWarps ? 2 : spans <= 4 * kNormWarps ? 4 : 5;
+  const uint32_t few = back ? kNormWarps : 5;
+  s.nb = spans <= few ? 1 : spans <= 2 * few ? 2 : spans <= 3 * few ? 3 : 5;
   s.warps = (uint32_t)((spans + s.nb - 1) / s.nb);
   return s;
 }
 
-// The ring's stages and batches of a pass with `arrays` rows a position, or no stages where
-// two rows do not fit.
+// The ring of a pass with `arrays` rows a position: as many blocks an SM as may be, batches
+// as large as leave two stages; or no stages where two rows do not fit.
 struct NormRing {
   uint32_t stages, rows, blocks;  // blocks an SM
   size_t shared;
 };
-inline NormRing norm_ring(uint32_t D, uint32_t es, uint32_t arrays,
-                          uint32_t most_blocks, uint32_t most_rows) {
+inline NormRing norm_ring(uint32_t D, uint32_t es, uint32_t arrays, uint32_t most_blocks,
+                          uint32_t most_rows, uint32_t least_rows, uint32_t besides) {
   constexpr uint32_t kShared = 224 * 1024, kHead = 2 * 1024;  // of an SM; of a block besides
   const uint32_t slot = ring_slot(D, es) * arrays;
   for (uint32_t blocks = most_blocks; blocks > 0; --blocks)
-    for (uint32_t rows = most_rows; rows > 0; rows /= 4) {
-      const uint32_t room = kShared / blocks - 1024 - kHead;
-      uint32_t stages = room / (slot * rows);
-      if (stages > kRingStages) stages = kRingStages;
-      // two stages of four rows, or of one where a block is alone
-      if (stages >= 2 && (rows == 4 || blocks == 1))
-        return {stages, rows, blocks, kHead + (size_t)stages * rows * slot};
+    for (uint32_t rows = most_rows; rows >= least_rows; rows /= 2) {
+      const uint32_t room = kShared / blocks - 1024 - kHead - besides;
+      const uint32_t stages = std::min(kRingStages, room / (slot * rows));
+      if (stages >= 2) return {stages, rows, blocks, kHead + besides + (size_t)stages * rows * slot};
     }
   return {0, 0, 0, 0};
-}
-
-// Blocks an SM that the ring's kernels may have.
-inline uint32_t ring_blocks(const NormShape &s) {
-  return s.nb > 1 || s.warps > kNormFew ? 1 : std::min<uint32_t>(6, 2 * kNormFew / s.warps);
 }
 
 // ---- sums over a row's lanes ------------------------------------------------------------
@@ -169,15 +163,15 @@ struct NormShared {
 static_assert(sizeof(NormShared) <= 2 * 1024, "what norm_ring leaves for it");
 constexpr uint32_t kNormRows = 2 * 1024;  // where the rows begin
 
-__device__ __forceinline__ char *ring_row(char *shared, uint32_t stage, uint32_t array,
+__device__ __forceinline__ char *ring_row(char *rows, uint32_t stage, uint32_t array,
                                           uint32_t arrays, uint32_t R, uint32_t r, uint32_t slot) {
-  return shared + kNormRows + ((stage * arrays + array) * R + r) * slot;
+  return rows + ((stage * arrays + array) * R + r) * slot;
 }
 
 // The warp that copies: lane r has row r of each batch.  Documents and statistics are read a
 // batch ahead, so that their way does not hold up the copies.
 template <class E, int R, bool kBack>
-__device__ __forceinline__ void produce_rows(const NormParams &p, char *shared) {
+__device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, char *rows) {
   NormShared &sh = *reinterpret_cast<NormShared *>(shared);
   const uint32_t lane = threadIdx.x % 32, slot = ring_slot(p.D, sizeof(E));
   constexpr uint32_t kArrays = kBack ? 2 : 1;
@@ -198,8 +192,8 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared) 
     if (turn && !lost && !barrier_wait(&sh.empty[stage], (turn - 1) & 1)) lost = true;
     sh.head[stage][lane] = head;
     RingSpan x = {0, 0, 0}, dy = x;
-    char *xs = ring_row(shared, stage, 0, kArrays, R, lane, slot);
-    char *ds = ring_row(shared, stage, kArrays - 1, kArrays, R, lane, slot);
+    char *xs = ring_row(rows, stage, 0, kArrays, R, lane, slot);
+    char *ds = ring_row(rows, stage, kArrays - 1, kArrays, R, lane, slot);
     if (head.there) {
       x = ring_span(xs, static_cast<const E *>(p.x) + (int64_t)n * p.x_row, p.D, n == 0,
                     n + 1 == p.N);
@@ -230,23 +224,19 @@ __device__ __forceinline__ void start_ring(char *shared, uint32_t stages, uint32
 }
 
 // ---- launches -----------------------------------------------------------------------
-cudaError_t norm_forward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st);
-cudaError_t norm_backward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st);
-// Rows of partial sums that the backward pass may write.
-uint32_t norm_partials(uint32_t N, uint32_t D);
+template <class E>
+cudaError_t norm_forward(NormParams &p, int piece, cudaStream_t st);
+template <class E>
+cudaError_t norm_backward(NormParams &p, int piece, cudaStream_t st);
 
-// By the rows' type and the pieces that all arrays can be moved by.
-template <class F>
-cudaError_t norm_by_type(const ns_norm_inputs &in, int piece, F &&call) {
-  const auto with = [&](auto e) {
-    constexpr int kMost = sizeof(e) == 4 ? 4 : 8;
-    if (piece >= kMost) return call(e, std::integral_constant<int, kMost>{});
-    if (piece >= 2) return call(e, std::integral_constant<int, 2>{});
-    return call(e, std::integral_constant<int, 1>{});
-  };
-  if (in.dtype == NS_F32) return with(float{});
-  if (in.dtype == NS_BF16) return with(__nv_bfloat16{});
-  return with(__half{});
+// By the pieces that all arrays can be moved by: for floats four elements at most, 16 bytes,
+// which shared memory has in one access.
+template <class E, class F>
+cudaError_t norm_by_piece(int piece, F &&call) {
+  constexpr int kMost = sizeof(E) == 4 ? 4 : 8;
+  if (piece >= kMost) return call(std::integral_constant<int, kMost>{});
+  if (piece >= 2) return call(std::integral_constant<int, 2>{});
+  return call(std::integral_constant<int, 1>{});
 }
 
 }  // namespace nsk

@@ -1,4 +1,6 @@
 // Layer norm, backward: see norm.cu.
+#pragma once
+
 #include "norm.cuh"
 
 namespace nsk {
@@ -147,32 +149,44 @@ __global__ void __launch_bounds__(kDirectThreads, 2) norm_backward_direct_kernel
 // All warps but the last take a batch of R rows together, NB spans each, and keep the sums of
 // their columns' dw and db.  The batch is read from shared memory twice: for the rows' two
 // sums, exchanged for all R at once, and for dx.
-template <class E, int NB, int V, int R, int kWarps>
-__global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
+// kWarps warps at most, kBlocks blocks an SM.
+template <class E, int NB, int V, int R, int kWarps, int kBlocks>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
     norm_backward_ring_kernel(const NormParams p) {
   extern __shared__ __align__(128) char shared[];
   NormShared &sh = *reinterpret_cast<NormShared *>(shared);
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  // the weights of up to three spans stay in registers, those of more in shared memory, a
+  // lane's columns beside one another
+  constexpr bool kHeld = NB <= 3;
+  Ch<2> *kept = reinterpret_cast<Ch<2> *>(shared + kNormRows);
+  char *rows = shared + kNormRows + (kHeld ? 0 : p.warps * NB * 32 * kOct * sizeof(float));
   start_ring<R>(shared, p.stages, p.warps);
   if (warp == p.warps) {
-    produce_rows<E, R, true>(p, shared);
+    produce_rows<E, R, true>(p, shared, rows);
     return;
   }
   constexpr uint32_t kSpan = 32 * kOct, kStep = 32 * V;
   const uint32_t first = warp * NB * kSpan + lane * V, slot = ring_slot(p.D, sizeof(E));
   const float share = 1.0f / (float)p.D;
-  // the weights of up to two spans stay in registers, more are read where they are used
-  constexpr int kHeld = NB <= 2 ? NB : 1;
-  Ch<2> w[kHeld][kOct / 2], dw[NB][kOct / 2], db[NB][kOct / 2];
-  const auto weights = [&](int i) {
-    load_vector<E, V>(p.weight, p.floats, first + i * kSpan, kStep, p.D, 1.0f, w[i % kHeld]);
-  };
+  Ch<2> w[kHeld ? NB : 1][kOct / 2], dw[NB][kOct / 2], db[NB][kOct / 2];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
 #pragma unroll
     for (int j = 0; j < kOct / 2; ++j) dw[i][j] = db[i][j] = {0.0f, 0.0f};
-    if constexpr (kHeld == NB) weights(i);
+    Ch<2>(&v)[kOct / 2] = w[kHeld ? i : 0];
+    load_vector<E, V>(p.weight, p.floats, first + i * kSpan, kStep, p.D, 1.0f, v);
+    if constexpr (!kHeld) {
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) kept[((warp * NB + i) * (kOct / 2) + j) * 32 + lane] = v[j];
+    }
   }
+  const auto weights = [&](int i) {  // each lane its own
+    if constexpr (!kHeld) {
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) w[0][j] = kept[((warp * NB + i) * (kOct / 2) + j) * 32 + lane];
+    }
+  };
   bool lost = false;
   uint32_t stage = 0, turn = 0, buffer = 0;
   for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
@@ -188,8 +202,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
         go = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.dy) +
                                                    (int64_t)(n0 + r) * p.dy_row) & 15u;
       }
-      xr[r] = ring_row(shared, stage, 0, 2, R, r, slot) + xo;
-      gr[r] = ring_row(shared, stage, 1, 2, R, r, slot) + go;
+      xr[r] = ring_row(rows, stage, 0, 2, R, r, slot) + xo;
+      gr[r] = ring_row(rows, stage, 1, 2, R, r, slot) + go;
       const NormHead head = sh.head[stage][r];
       Ch<2> s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
       if (head.there) {
@@ -200,12 +214,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
           Ch<2> f[kOct / 2], g[kOct / 2];
           ring_oct(x, xr[r], first + i * kSpan, kStep, p.D);
           ring_oct(y, gr[r], first + i * kSpan, kStep, p.D);
-          if constexpr (kHeld < NB) weights(i);
+          weights(i);
           widen(x, f);
           widen(y, g);
 #pragma unroll
           for (int j = 0; j < kOct / 2; ++j) {
-            const Ch<2> xh = (f[j] + minus) * scale, gw = g[j] * w[i % kHeld][j];
+            const Ch<2> xh = (f[j] + minus) * scale, gw = g[j] * w[kHeld ? i : 0][j];
             s1 = s1 + gw;
             s2 = fma(gw, xh, s2);
             dw[i][j] = fma(g[j], xh, dw[i][j]);
@@ -231,13 +245,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
         Ch<2> f[kOct / 2], g[kOct / 2];
         ring_oct(x, xr[r], first + i * kSpan, kStep, p.D);
         ring_oct(y, gr[r], first + i * kSpan, kStep, p.D);
-        if constexpr (kHeld < NB) weights(i);
+        weights(i);
         widen(x, f);
         widen(y, g);
 #pragma unroll
         for (int j = 0; j < kOct / 2; ++j) {
           const Ch<2> xh = (f[j] + minus) * scale;
-          f[j] = scale * fma(xh, m2, fma(g[j], w[i % kHeld][j], m1));
+          f[j] = scale * fma(xh, m2, fma(g[j], w[kHeld ? i : 0][j], m1));
           if (!head.there) f[j] = {0.0f, 0.0f};
         }
         store_oct(dx, first + i * kSpan, kStep, p.D, narrow<E, V>(f));
@@ -353,9 +367,9 @@ __global__ void __launch_bounds__(32 * kColumnWarps) norm_columns_kernel(const N
 }
 
 // ---- launches -----------------------------------------------------------------------
-template <class E, int NB, int V, int R, int kWarps>
-cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
-  auto *k = norm_backward_ring_kernel<E, NB, V, R, kWarps>;
+template <class E, int NB, int V, int R, int kWarps, int kBlocks>
+cudaError_t launch_back_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
+  auto *k = norm_backward_ring_kernel<E, NB, V, R, kWarps, kBlocks>;
   const cudaError_t e = allow_shared_memory(reinterpret_cast<const void *>(k), true);
   if (e != cudaSuccess) return e;
   p.stages = ring.stages;
@@ -365,20 +379,19 @@ cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
   k<<<p.blocks, 32 * (p.warps + 1), ring.shared, st>>>(p);
   return cudaGetLastError();
 }
-template <class E, int NB, int V, int kWarps>
-cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
-  if constexpr (NB <= 2)
-    if (ring.rows == 4) return launch_ring<E, NB, V, 4, kWarps>(p, ring, st);
-  return launch_ring<E, NB, V, 1, kWarps>(p, ring, st);
-}
-// A block's warps decide how many registers a thread may have, and how many blocks an SM.
-template <class E, int V>
-cudaError_t launch_ring(NormParams &p, const NormShape &s, const NormRing &ring, cudaStream_t st) {
-  if (s.nb == 1 && s.warps <= kNormFew) return launch_ring<E, 1, V, 4, kNormFew>(p, ring, st);
-  if (s.nb == 1) return launch_ring<E, 1, V, kNormWarps>(p, ring, st);
-  if (s.nb == 2) return launch_ring<E, 2, V, kNormWarps>(p, ring, st);
-  if (s.nb == 4) return launch_ring<E, 4, V, kNormWarps>(p, ring, st);
-  return launch_ring<E, 5, V, kNormWarps>(p, ring, st);
+// Batches of kMost rows down to kLeast; false in `done` where the ring has no room.
+template <class E, int NB, int V, int kWarps, int kBlocks, uint32_t kMost, uint32_t kLeast>
+cudaError_t back_ring_of(NormParams &p, bool &done, cudaStream_t st) {
+  const uint32_t besides = NB > 3 ? p.warps * NB * 32 * kOct * (uint32_t)sizeof(float) : 0;
+  const NormRing ring = norm_ring(p.D, sizeof(E), 2, kBlocks, kMost, kLeast, besides);
+  done = ring.stages > 0;
+  if constexpr (kMost == 4)
+    if (ring.rows == 4) return launch_back_ring<E, NB, V, 4, kWarps, kBlocks>(p, ring, st);
+  if constexpr (kMost >= 2 && kLeast <= 2)
+    if (ring.rows == 2) return launch_back_ring<E, NB, V, 2, kWarps, kBlocks>(p, ring, st);
+  if constexpr (kLeast == 1)
+    if (ring.rows == 1) return launch_back_ring<E, NB, V, 1, kWarps, kBlocks>(p, ring, st);
+  return cudaSuccess;
 }
 
 template <class E, int V>
@@ -408,28 +421,27 @@ cudaError_t direct_of(NormParams &p, cudaStream_t st) {
 
 template <class E, int V>
 cudaError_t backward_of(NormParams &p, cudaStream_t st) {
-  const NormShape s = norm_shape(p.D);
+  const NormShape s = norm_shape(p.D, true);
   p.lanes = s.lanes, p.warps = s.warps;
   if (p.D <= kNormNarrow) return direct_of<E, V>(p, st);
-  const NormRing ring = norm_ring(p.D, sizeof(E), 2, ring_blocks(s), s.nb <= 2 ? 4 : 1);
-  if (p.D > kNormKept || !ring.stages) return wide_of<E, V>(p, st);
-  return launch_ring<E, V>(p, s, ring, st);
+  if (p.D > kNormKept) return wide_of<E, V>(p, st);
+  bool done = false;
+  const cudaError_t e =
+      s.nb == 1 && s.warps <= 5    ? back_ring_of<E, 1, V, 5, 4, 4, 2>(p, done, st)
+      : s.nb == 1 && s.warps <= 10 ? back_ring_of<E, 1, V, 10, 2, 4, 2>(p, done, st)
+      : s.nb == 1                  ? back_ring_of<E, 1, V, kNormWarps, 1, 4, 2>(p, done, st)
+      : s.nb == 2                  ? back_ring_of<E, 2, V, kNormWarps, 1, 4, 1>(p, done, st)
+      : s.nb == 3                  ? back_ring_of<E, 3, V, kNormWarps, 1, 2, 1>(p, done, st)
+                                   : back_ring_of<E, 5, V, kNormWarps, 1, 1, 1>(p, done, st);
+  return done ? e : wide_of<E, V>(p, st);
 }
 
 }  // namespace
 
-uint32_t norm_partials(uint32_t N, uint32_t D) {
-  // as many blocks as any of the kernels has, of which each has a row at least
-  if (D <= kNormNarrow) return std::min(N, 2 * kNormSMs);
-  const uint32_t spans = (D + 32 * kOct - 1) / (32 * kOct);
-  const uint32_t ring = ring_blocks(norm_shape(D)) * kNormSMs;
-  return std::min(N, std::max(ring, (8 * kNormSMs + spans - 1) / spans));
-}
-
-cudaError_t norm_backward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st) {
-  return norm_by_type(in, piece, [&](auto e, auto v) {
-    return backward_of<decltype(e), decltype(v)::value>(p, st);
-  });
+template <class E>
+cudaError_t norm_backward(NormParams &p, int piece, cudaStream_t st) {
+  return norm_by_piece<E>(
+      piece, [&](auto v) { return backward_of<E, decltype(v)::value>(p, st); });
 }
 
 }  // namespace nsk

@@ -1,4 +1,6 @@
 // Layer norm, forward: see norm.cu.
+#pragma once
+
 #include "norm.cuh"
 
 namespace nsk {
@@ -92,31 +94,25 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_direct_kernel(const Norm
 // ---- rows through the ring -----------------------------------------------------------------
 // All warps but the last take a batch of R rows together, NB spans each: sums, squares and
 // outputs read the batch from shared memory anew, and a batch's sums are exchanged at once.
-template <class E, int NB, int V, int R, int kWarps>
-__global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
-    norm_ring_kernel(const NormParams p) {
+// kWarps warps at most, kBlocks blocks an SM.
+template <class E, int NB, int V, int R, int kWarps, int kBlocks>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(const NormParams p) {
   extern __shared__ __align__(128) char shared[];
   NormShared &sh = *reinterpret_cast<NormShared *>(shared);
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   start_ring<R>(shared, p.stages, p.warps);
   if (warp == p.warps) {
-    produce_rows<E, R, false>(p, shared);
+    produce_rows<E, R, false>(p, shared, shared + kNormRows);
     return;
   }
   constexpr uint32_t kSpan = 32 * kOct, kStep = 32 * V;
   const uint32_t first = warp * NB * kSpan + lane * V, slot = ring_slot(p.D, sizeof(E));
   const float share = 1.0f / (float)p.D;
-  // the weights of up to two spans stay in registers, more are read where they are used
-  constexpr int kHeld = NB <= 2 ? NB : 1;
-  Ch<2> w[kHeld][kOct / 2], b[kHeld][kOct / 2];
-  const auto weights = [&](int i) {
-    const uint32_t c = first + i * kSpan;
-    load_vector<E, V>(p.weight, p.floats, c, kStep, p.D, 1.0f, w[i % kHeld]);
-    load_vector<E, V>(p.bias, p.floats, c, kStep, p.D, 0.0f, b[i % kHeld]);
-  };
-  if constexpr (kHeld == NB) {
+  Ch<2> w[NB][kOct / 2], b[NB][kOct / 2];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) weights(i);
+  for (int i = 0; i < NB; ++i) {
+    load_vector<E, V>(p.weight, p.floats, first + i * kSpan, kStep, p.D, 1.0f, w[i]);
+    load_vector<E, V>(p.bias, p.floats, first + i * kSpan, kStep, p.D, 0.0f, b[i]);
   }
   const bool all = warp * NB * kSpan + NB * kSpan <= p.D;  // no lane beyond the row
   bool lost = false;
@@ -133,7 +129,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
               ? 0
               : (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
                                                       (int64_t)(n0 + r) * p.x_row) & 15u;
-      row[r] = ring_row(shared, stage, 0, 1, R, r, slot) + off;
+      row[r] = ring_row(shared + kNormRows, stage, 0, 1, R, r, slot) + off;
       there[r] = sh.head[stage][r].there;
       Ch<2> two = {0.0f, 0.0f};
       if (there[r]) {
@@ -190,12 +186,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kWarps > kNormFew ? 1 : 2)
         const uint32_t c = first + i * kSpan;
         Oct<E, V> x;
         Ch<2> f[kOct / 2];
-        if constexpr (kHeld < NB) weights(i);
         ring_oct(x, row[r], c, kStep, p.D);
         widen(x, f);
 #pragma unroll
         for (int j = 0; j < kOct / 2; ++j) {
-          f[j] = fma((f[j] + minus) * scale, w[i % kHeld][j], b[i % kHeld][j]);
+          f[j] = fma((f[j] + minus) * scale, w[i][j], b[i][j]);
           if (!there[r]) f[j] = {0.0f, 0.0f};
         }
         store_oct(y, c, kStep, p.D, narrow<E, V>(f));
@@ -270,9 +265,9 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParam
 }
 
 // ---- launches -----------------------------------------------------------------------
-template <class E, int NB, int V, int R, int kWarps>
+template <class E, int NB, int V, int R, int kWarps, int kBlocks>
 cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
-  auto *k = norm_ring_kernel<E, NB, V, R, kWarps>;
+  auto *k = norm_ring_kernel<E, NB, V, R, kWarps, kBlocks>;
   const cudaError_t e = allow_shared_memory(reinterpret_cast<const void *>(k), true);
   if (e != cudaSuccess) return e;
   p.stages = ring.stages;
@@ -282,20 +277,15 @@ cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
   k<<<blocks, 32 * (p.warps + 1), ring.shared, st>>>(p);
   return cudaGetLastError();
 }
-template <class E, int NB, int V, int kWarps>
-cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
-  if constexpr (NB <= 2)
-    if (ring.rows == 4) return launch_ring<E, NB, V, 4, kWarps>(p, ring, st);
-  return launch_ring<E, NB, V, 1, kWarps>(p, ring, st);
-}
-// A block's warps decide how many registers a thread may have, and how many blocks an SM.
-template <class E, int V>
-cudaError_t launch_ring(NormParams &p, const NormShape &s, const NormRing &ring, cudaStream_t st) {
-  if (s.nb == 1 && s.warps <= kNormFew) return launch_ring<E, 1, V, 4, kNormFew>(p, ring, st);
-  if (s.nb == 1) return launch_ring<E, 1, V, kNormWarps>(p, ring, st);
-  if (s.nb == 2) return launch_ring<E, 2, V, kNormWarps>(p, ring, st);
-  if (s.nb == 4) return launch_ring<E, 4, V, kNormWarps>(p, ring, st);
-  return launch_ring<E, 5, V, kNormWarps>(p, ring, st);
+// Batches of four, two or one row, of which the widest rows have the last two.
+template <class E, int NB, int V, int kWarps, int kBlocks>
+cudaError_t ring_of(NormParams &p, bool &done, cudaStream_t st) {
+  constexpr uint32_t kMost = NB > 3 ? 2 : 4;
+  const NormRing ring = norm_ring(p.D, sizeof(E), 1, kBlocks, kMost, kMost / 2, 0);
+  done = ring.stages > 0;
+  if (!done) return cudaSuccess;
+  if (ring.rows == kMost) return launch_ring<E, NB, V, kMost, kWarps, kBlocks>(p, ring, st);
+  return launch_ring<E, NB, V, kMost / 2, kWarps, kBlocks>(p, ring, st);
 }
 
 template <class E, int V>
@@ -305,13 +295,18 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
     norm_wide_kernel<E, V><<<p.N, kWideThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
-  const NormShape s = norm_shape(p.D);
+  const NormShape s = norm_shape(p.D, false);
   p.lanes = s.lanes, p.warps = s.warps;
   // rows that fill the SMs' rings, else straight from memory: a call of 64 rows waits for
   // nothing but its own loads
   if (p.D > kNormNarrow && p.N > 4 * kNormSMs) {
-    const NormRing ring = norm_ring(p.D, sizeof(E), 1, ring_blocks(s), s.nb <= 2 ? 4 : 1);
-    if (ring.stages) return launch_ring<E, V>(p, s, ring, st);
+    bool done = false;
+    const cudaError_t e = s.nb == 1       ? ring_of<E, 1, V, 5, 5>(p, done, st)
+                          : s.nb == 2     ? ring_of<E, 2, V, 5, 4>(p, done, st)
+                          : s.nb == 3     ? ring_of<E, 3, V, 5, 3>(p, done, st)
+                          : s.warps <= 7  ? ring_of<E, 5, V, 7, 2>(p, done, st)
+                                          : ring_of<E, 5, V, kNormWarps, 1>(p, done, st);
+    if (done) return e;
   }
   const uint32_t groups = std::max<uint32_t>(1, kDirectWarps / p.warps);
   const uint32_t threads = groups * p.warps * 32, rows = groups * (32 / p.lanes);
@@ -319,7 +314,7 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
   ++launch_counter();
   auto *k = s.nb == 1   ? norm_direct_kernel<E, 1, V>
             : s.nb == 2 ? norm_direct_kernel<E, 2, V>
-            : s.nb == 4 ? norm_direct_kernel<E, 4, V>
+            : s.nb == 3 ? norm_direct_kernel<E, 3, V>
                         : norm_direct_kernel<E, 5, V>;
   k<<<blocks, threads, 0, st>>>(p);
   return cudaGetLastError();
@@ -327,10 +322,10 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t norm_forward(NormParams &p, const ns_norm_inputs &in, int piece, cudaStream_t st) {
-  return norm_by_type(in, piece, [&](auto e, auto v) {
-    return forward_of<decltype(e), decltype(v)::value>(p, st);
-  });
+template <class E>
+cudaError_t norm_forward(NormParams &p, int piece, cudaStream_t st) {
+  return norm_by_piece<E>(
+      piece, [&](auto v) { return forward_of<E, decltype(v)::value>(p, st); });
 }
 
 }  // namespace nsk
