@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCopied = 4;                     // spans of a unit (rows.cuh)
 constexpr uint32_t kTile = 32;                 // positions of a tile
 constexpr uint32_t kSlice = 32 * kOct;         // columns of a warp
 constexpr uint32_t kBefore = 0xffffffffu, kBehind = 0xfffffffeu;
@@ -61,7 +60,9 @@ struct EmbedParams {
 };
 
 // ---- forward ------------------------------------------------------------------------
-template <class W, class E, int V>
+// U spans of a position's row a unit: short blocks, whose stores drain while others begin
+// (blocks that stay, with the next token under way: 32768 x 2560 bf16 47 us in place of 40).
+template <class W, class E, int V, int U>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
   const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
@@ -69,18 +70,18 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
   const int64_t t = p.wide ? static_cast<const int64_t *>(p.tokens)[n]
                            : static_cast<const int32_t *>(p.tokens)[n];
   const bool there = t >= 0 && t < (int64_t)p.V && !(p.doc && p.doc[n] < 0);
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint32_t first = slice * U * span + threadIdx.x % p.lanes * V;
   const W *row = static_cast<const W *>(p.table) + (there ? t : 0) * p.table_row;
   E *y = static_cast<E *>(p.y) + (int64_t)n * p.D;
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint32_t first = slice * kCopied * span + threadIdx.x % p.lanes * V;
-  Oct<W, V> v[kCopied];
+  Oct<W, V> v[U];
 #pragma unroll
-  for (int u = 0; u < kCopied; ++u) {
+  for (int u = 0; u < U; ++u) {
     clear(v[u]);
     if (there) load_oct(v[u], row, first + u * span, step, p.D);
   }
 #pragma unroll
-  for (int u = 0; u < kCopied; ++u) {
+  for (int u = 0; u < U; ++u) {
     Ch<2> x[kOct / 2];
     widen(v[u], x);
 #pragma unroll
@@ -286,15 +287,22 @@ Layout layout_of(uint32_t N, uint32_t V, uint32_t D) {
   return l;
 }
 
+template <class W, class E, int V, int U>
+cudaError_t forward_by(EmbedParams &p, cudaStream_t st) {
+  p.slices = (uint32_t)((spans_for(p.D, p.lanes) + U - 1) / U);
+  const uint64_t each = kThreads / p.lanes, blocks = ((uint64_t)p.N * p.slices + each - 1) / each;
+  ++launch_counter();
+  embed_kernel<W, E, V, U>
+      <<<(uint32_t)blocks, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
 template <class W, class E, int V>
 cudaError_t forward_of(EmbedParams &p, cudaStream_t st) {
   p.lanes = lanes_for(p.D);
-  p.slices = (uint32_t)((spans_for(p.D, p.lanes) + kCopied - 1) / kCopied);
-  const uint32_t each = kThreads / p.lanes;
-  ++launch_counter();
-  embed_kernel<W, E, V>
-      <<<(uint32_t)(((uint64_t)p.N * p.slices + each - 1) / each), kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const uint64_t spans = spans_for(p.D, p.lanes);
+  if (spans <= 1) return forward_by<W, E, V, 1>(p, st);
+  if (spans == 2) return forward_by<W, E, V, 2>(p, st);
+  return forward_by<W, E, V, 4>(p, st);
 }
 
 template <class W, class E, int V>

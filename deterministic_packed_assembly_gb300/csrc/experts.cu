@@ -37,7 +37,8 @@ constexpr int kThreads = 256;
 
 struct ExpertParams {
   uint32_t N, k, E, D;
-  uint32_t lanes, spans, slices;  // lanes of a unit, spans of a row (rows.cuh), units of a row
+  // lanes of a unit, spans of a row (rows.cuh) and of a unit, units of a row
+  uint32_t lanes, spans, each, slices;
   const int32_t *ids;
   int32_t *place, *slots, *offsets;
   const void *x;       // or d_out
@@ -54,44 +55,56 @@ struct ExpertParams {
 template <class E, int V>
 constexpr int kUnderWay = Oct<E, V>::kPieces * Oct<E, V>::kWords == 4 ? 8 : 4;
 
-// ---- dispatch --------------------------------------------------------------------
-constexpr int kCopied = 4;  // spans of a unit
-
-// One slice of token n's row into the places of its choices.
+// Blocks an SM: as many as have the registers for it.
 template <class E, int V>
-__device__ __forceinline__ void copy_slice(const ExpertParams &p, uint32_t n, uint32_t slice,
-                                           uint32_t lane, const int32_t *place, uint32_t M) {
-  const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
-  E *to = static_cast<E *>(p.to);
+constexpr int kBackBlocks = kUnderWay<E, V> == 8 ? 3 : 2;
+constexpr int kCombineBlocks = 2;
+
+// ---- dispatch --------------------------------------------------------------------
+// U spans of token n's row, from `first` on, into the places of its choices.
+template <class E, int V, int U>
+__device__ __forceinline__ void copy_slice(const ExpertParams &p, const Oct<E, V> (&v)[U],
+                                           uint32_t first, const int32_t *place, uint32_t M) {
   const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint32_t first = slice * kCopied * span + lane * V;
-  Oct<E, V> v[kCopied], zero;
+  E *to = static_cast<E *>(p.to);
+  Oct<E, V> zero;
   clear(zero);
-#pragma unroll
-  for (int u = 0; u < kCopied; ++u) load_oct(v[u], x, first + u * span, step, p.D);
+#pragma unroll 2
   for (uint32_t j = 0; j < p.k; ++j) {
     const uint32_t at = (uint32_t)place[j];
     E *row = to + (int64_t)at * p.D;
 #pragma unroll
-    for (int u = 0; u < kCopied; ++u)
+    for (int u = 0; u < U; ++u)
       store_oct(row, first + u * span, step, p.D, at < M ? v[u] : zero);
   }
 }
+template <class E, int V, int U>
+__device__ __forceinline__ void load_slice(const ExpertParams &p, Oct<E, V> (&v)[U], uint32_t n,
+                                           uint32_t first) {
+  const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    load_oct(v[u], x, first + u * p.lanes * kOct, p.lanes * V, p.D);
+}
 
-// Blocks of kThreads / lanes units: a slice of a token each.
-template <class E, int V>
+// A slice of a token a unit: short blocks, whose stores drain while others begin (blocks that
+// stay, with the next row under way: 32768 x 2560 bf16, k = 8: 279 us in place of 236).  Its row
+// is read before the sort has ended: x was there when the sort's first kernel began.
+template <class E, int V, int U>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const ExpertParams p) {
-  pdl_wait();
   const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
-  if (n >= p.N) return;
-  copy_slice<E, V>(p, n, slice, threadIdx.x % p.lanes, p.place + (uint64_t)n * p.k,
-                   (uint32_t)p.offsets[p.E]);
+  const uint32_t first = slice * U * p.lanes * kOct + threadIdx.x % p.lanes * V;
+  Oct<E, V> v[U];
+  if (n < p.N) load_slice<E, V, U>(p, v, n, first);
+  pdl_wait();
+  if (n < p.N)
+    copy_slice<E, V, U>(p, v, first, p.place + (uint64_t)n * p.k, (uint32_t)p.offsets[p.E]);
 }
 
 // Few choices: a block a token finds its places by counting the keys below and before
 // them, and no sort is needed.  The last block has the offsets.
-template <class E, int V>
+template <class E, int V, int U>
 __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const ExpertParams p) {
   extern __shared__ uint32_t key[];  // [S], then what the block counts
   const uint32_t S = p.N * p.k;
@@ -144,154 +157,206 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const ExpertPara
     p.slots[count[j]] = (int32_t)(n * p.k + j);
   }
   const uint32_t M = count[p.k];
-  for (uint32_t unit = threadIdx.x / p.lanes; unit < p.slices; unit += kThreads / p.lanes)
-    copy_slice<E, V>(p, n, unit, threadIdx.x % p.lanes,
-                          reinterpret_cast<const int32_t *>(count), M);
+  for (uint32_t unit = threadIdx.x / p.lanes; unit < p.slices; unit += kThreads / p.lanes) {
+    const uint32_t first = unit * U * p.lanes * kOct + threadIdx.x % p.lanes * V;
+    Oct<E, V> v[U];
+    load_slice<E, V, U>(p, v, n, first);
+    copy_slice<E, V, U>(p, v, first, reinterpret_cast<const int32_t *>(count), M);
+  }
 }
 
 // ---- combine ------------------------------------------------------------------------
-// R choices' rows and U spans of them under way: what hides memory's latency is R U.
-template <class E, int V, int R, int U>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const ExpertParams p) {
-  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
-  const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
-  if (n >= p.N) return;
-  const uint32_t M = min((uint32_t)p.offsets[p.E], p.N * p.k);
-  const int32_t *place = p.place + (uint64_t)n * p.k;
-  const float *weights = p.weights ? p.weights + (uint64_t)n * p.k : nullptr;
-  const E *from = static_cast<const E *>(p.from);
-  E *out = static_cast<E *>(p.to) + (int64_t)n * p.D;
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint32_t first = slice * U * span + threadIdx.x % p.lanes * V;
-  Ch<2> acc[U][kOct / 2];
+// R choices' places and weights; M where there is none.
+template <int R>
+struct Chosen {
+  uint32_t at[R];
+  float w[R];
+};
+template <int R>
+__device__ __forceinline__ void load_chosen(Chosen<R> &c, const ExpertParams &p, uint32_t n,
+                                            uint32_t j0, uint32_t M) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < kOct / 2; ++i) acc[u][i] = {0.0f, 0.0f};
-  for (uint32_t j0 = 0; j0 < p.k; j0 += R) {
-    Oct<E, V> v[R][U];
-    float w[R];
-    bool there[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t at = j0 + r < p.k ? (uint32_t)place[j0 + r] : M;
-      there[r] = at < M;
-      if (there[r]) {
-        w[r] = weights ? weights[j0 + r] : 1.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          load_oct(v[r][u], from + (int64_t)at * p.from_row, first + u * span, step, p.D);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (!there[r]) continue;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        Ch<2> x[kOct / 2];
-        widen(v[r][u], x);
-#pragma unroll
-        for (int i = 0; i < kOct / 2; ++i) acc[u][i] = fma(splat<2>(w[r]), x[i], acc[u][i]);
-      }
-    }
+  for (int r = 0; r < R; ++r) {
+    const uint64_t s = (uint64_t)n * p.k + j0 + r;
+    c.at[r] = j0 + r < p.k ? (uint32_t)p.place[s] : M;
+    c.w[r] = p.weights && j0 + r < p.k ? p.weights[s] : 1.0f;
   }
+}
+
+// Units of a slice of a token each, one after the other; R choices' rows and U spans of them are
+// under way (what hides memory's latency is R U), and the next unit's choices.
+template <class E, int V, int R, int U>
+__global__ void __launch_bounds__(kThreads, kCombineBlocks) combine_kernel(const ExpertParams p) {
+  const uint32_t M = min((uint32_t)p.offsets[p.E], p.N * p.k);
+  const E *from = static_cast<const E *>(p.from);
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+  const uint64_t every = (uint64_t)gridDim.x * kThreads / p.lanes;
+  const uint64_t units = (uint64_t)p.N * p.slices;
+  uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
+  Chosen<R> now, next;
+  if (unit < units) load_chosen(now, p, (uint32_t)(unit / p.slices), 0, M);
+  for (; unit < units; unit += every) {
+    const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
+    if (unit + every < units)
+      load_chosen(next, p, (uint32_t)((unit + every) / p.slices), 0, M);
+    E *out = static_cast<E *>(p.to) + (int64_t)n * p.D;
+    const uint32_t end = min(p.spans, (slice + 1) * p.each);
+    for (uint32_t s = slice * p.each; s < end; s += U) {
+      const uint32_t first = s * span + threadIdx.x % p.lanes * V;
+      Ch<2> acc[U][kOct / 2];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    store_oct(out, first + u * span, step, p.D, narrow<E, V>(acc[u]));
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < kOct / 2; ++i) acc[u][i] = {0.0f, 0.0f};
+      for (uint32_t j0 = 0; j0 < p.k; j0 += R) {
+        if (p.k > R) load_chosen(now, p, n, j0, M);
+        Oct<E, V> v[R][U];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (now.at[r] < M)
+              load_oct(v[r][u], from + (int64_t)now.at[r] * p.from_row, first + u * span, step,
+                       p.D);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (now.at[r] >= M) continue;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            Ch<2> x[kOct / 2];
+            widen(v[r][u], x);
+#pragma unroll
+            for (int i = 0; i < kOct / 2; ++i)
+              acc[u][i] = fma(splat<2>(now.w[r]), x[i], acc[u][i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s + u < end) store_oct(out, first + u * span, step, p.D, narrow<E, V>(acc[u]));
+    }
+    now = next;
+  }
 }
 
 // ---- combine's backward pass -----------------------------------------------------------
-// L lanes a choice: neighbouring units are a token's, whose row stays in the L1 cache.
-template <class E, int V>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const ExpertParams p) {
-  constexpr int U = kUnderWay<E, V> / 2;  // spans under way, of two rows
-  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
-  const uint32_t S = p.N * p.k;
-  const bool real = unit < S;  // all lanes stay: they add up together
-  const uint32_t s = real ? (uint32_t)unit : S - 1, n = s / p.k;
-  const uint32_t lane = threadIdx.x % p.lanes;
+// L lanes a choice, one after the other: neighbouring units are a token's, whose row stays in
+// the L1 cache.  U spans of both rows are under way, and the next choice's place.
+template <class E, int V, int U>
+__global__ void __launch_bounds__(kThreads, (kBackBlocks<E, V>))
+    combine_backward_kernel(const ExpertParams p) {
+  const uint32_t S = p.N * p.k, lane = threadIdx.x % p.lanes;
   const uint32_t M = min((uint32_t)p.offsets[p.E], S);
-  const uint32_t at = (uint32_t)p.place[s];
-  const E *d_out = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
-  const E *y = static_cast<const E *>(p.from) + (int64_t)at * p.from_row;
-  E *to = static_cast<E *>(p.to) + (int64_t)at * p.D;
-  const bool there = real && at < M;
-  const Ch<2> w = splat<2>(there && p.weights ? p.weights[s] : 1.0f);
   const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  Ch<2> dot = {0.0f, 0.0f};
-  if (real && at < S) {
-    for (uint32_t c = lane * V; c < p.D; c += U * span) {
-      Oct<E, V> a[U], b[U];
+  const uint64_t every = (uint64_t)gridDim.x * kThreads / p.lanes;
+  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
+  const uint64_t base = (uint64_t)blockIdx.x * (kThreads / p.lanes);  // of the block
+  Chosen<1> now, next;
+  const auto look = [&](Chosen<1> &c, uint64_t s) {
+    c.at[0] = s < S ? (uint32_t)p.place[s] : S;
+    c.w[0] = s < S && p.weights ? p.weights[s] : 1.0f;
+  };
+  look(now, unit);
+  // all lanes stay: they add up together
+  for (uint64_t b = base, s = unit; b < S; b += every, s += every) {
+    look(next, s + every);
+    const uint32_t at = now.at[0], n = (uint32_t)(s < S ? s : S - 1) / p.k;
+    const E *d_out = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
+    const E *y = static_cast<const E *>(p.from) + (int64_t)at * p.from_row;
+    E *to = static_cast<E *>(p.to) + (int64_t)at * p.D;
+    const bool there = at < M;
+    const Ch<2> w = splat<2>(there ? now.w[0] : 1.0f);
+    Ch<2> dot = {0.0f, 0.0f};
+    if (at < S) {
+      for (uint32_t c = lane * V; c < p.D; c += U * span) {
+        Oct<E, V> a[U], y8[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        clear(a[u]), clear(b[u]);
-        if (there) {
-          load_oct(a[u], d_out, c + u * span, step, p.D);
-          if (p.d_weights) load_oct(b[u], y, c + u * span, step, p.D);
+        for (int u = 0; u < U; ++u) {
+          clear(a[u]), clear(y8[u]);
+          if (there) {
+            load_oct(a[u], d_out, c + u * span, step, p.D);
+            if (p.d_weights) load_oct(y8[u], y, c + u * span, step, p.D);
+          }
         }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        Ch<2> d[kOct / 2], x[kOct / 2];
-        widen(a[u], d);
-        widen(b[u], x);
+        for (int u = 0; u < U; ++u) {
+          Ch<2> d[kOct / 2], x[kOct / 2];
+          widen(a[u], d);
+          widen(y8[u], x);
 #pragma unroll
-        for (int i = 0; i < kOct / 2; ++i) {
-          dot = fma(d[i], x[i], dot);
-          d[i] = d[i] * w;
+          for (int i = 0; i < kOct / 2; ++i) {
+            dot = fma(d[i], x[i], dot);
+            d[i] = d[i] * w;
+          }
+          store_oct(to, c + u * span, step, p.D, narrow<E, V>(d));
         }
-        store_oct(to, c + u * span, step, p.D, narrow<E, V>(d));
       }
     }
-  }
-  if (p.d_weights) {
-    float sum = dot.v[0] + dot.v[1];
-    for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (real && lane == 0) p.d_weights[s] = sum;
+    if (p.d_weights) {
+      float sum = dot.v[0] + dot.v[1];
+      for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (s < S && lane == 0) p.d_weights[s] = sum;
+    }
+    now = next;
   }
 }
 
 // ---- launches ------------------------------------------------------------------------
-// The lanes of a unit, which has `spans` of the row's, or all of them.
-void set_shape(ExpertParams &p, uint32_t spans) {
+constexpr uint32_t kSMs = 152;
+
+// Units of `each` spans of a row.
+void set_shape(ExpertParams &p, uint32_t each) {
   p.lanes = lanes_for(p.D);
   p.spans = (uint32_t)spans_for(p.D, p.lanes);
-  p.slices = spans ? (p.spans + spans - 1) / spans : 1;
+  p.each = std::max<uint32_t>(1, each);
+  p.slices = (p.spans + p.each - 1) / p.each;
 }
-uint32_t blocks_of(uint64_t units, uint32_t lanes) {
-  const uint32_t each = kThreads / lanes;
-  return (uint32_t)((units + each - 1) / each);
+// The blocks that all SMs have at once, or as many as there are units for.
+uint32_t blocks_for(uint64_t units, uint32_t lanes, uint32_t each_sm) {
+  const uint64_t each = kThreads / lanes;
+  return (uint32_t)std::min<uint64_t>((units + each - 1) / each, (uint64_t)each_sm * kSMs);
 }
 
 // Few choices that each block counts by itself.  A block reads all of the ids, k times from
 // shared memory: up to so many comparisons a thread, the sort's two launches cost more.
 bool few(uint64_t N, uint64_t k) { return N * k <= 2048 && N * k * k <= (1 << 14); }
 
-template <class E, int V>
-cudaError_t dispatch_of(ExpertParams &p, void *workspace, cudaStream_t st) {
-  set_shape(p, kCopied);
+template <class E, int V, int U>
+cudaError_t dispatch_by(ExpertParams &p, void *workspace, cudaStream_t st) {
+  set_shape(p, U);
   if (few(p.N, p.k)) {
     const size_t shared = (p.N * p.k + std::max(p.k, p.E) + 1) * sizeof(uint32_t);
     ++launch_counter();
-    dispatch_few_kernel<E, V><<<p.N + 1, kThreads, shared, st>>>(p);
+    dispatch_few_kernel<E, V, U><<<p.N + 1, kThreads, shared, st>>>(p);
     return cudaGetLastError();
   }
-  const cudaError_t e = launch_order_choices({p.ids, nullptr, p.N * p.k, p.E, false}, p.place,
-                                             p.slots, p.offsets, workspace, st);
+  const cudaError_t e = launch_order_choices({p.ids, nullptr, p.N * p.k, p.E, false}, p.place, p.slots,
+                                       p.offsets, workspace, st);
   if (e != cudaSuccess || p.D == 0) return e;
+  const uint64_t each = kThreads / p.lanes, blocks = ((uint64_t)p.N * p.slices + each - 1) / each;
   ++launch_counter();
-  pdl_launch(dispatch_kernel<E, V>, dim3(blocks_of((uint64_t)p.N * p.slices, p.lanes)),
-             dim3(kThreads), 0, st, p);
+  pdl_launch(dispatch_kernel<E, V, U>, dim3((uint32_t)blocks), dim3(kThreads), 0, st, p);
   return cudaGetLastError();
+}
+template <class E, int V>
+cudaError_t dispatch_of(ExpertParams &p, void *workspace, cudaStream_t st) {
+  const uint64_t spans = spans_for(p.D, lanes_for(p.D));
+  if (spans <= 1) return dispatch_by<E, V, 1>(p, workspace, st);
+  if (spans == 2 || kUnderWay<E, V> == 4) return dispatch_by<E, V, 2>(p, workspace, st);
+  return dispatch_by<E, V, 4>(p, workspace, st);
 }
 
 template <class E, int V, int R>
 cudaError_t combine_by(ExpertParams &p, cudaStream_t st) {
   constexpr int U = kUnderWay<E, V> > R ? kUnderWay<E, V> / R : 1;
-  set_shape(p, U);
+  // whole rows, or as many units of one as a call of few tokens needs to fill the SMs
+  set_shape(p, 1);
+  const uint64_t wanted = 32ull * kSMs;
+  const uint32_t parts = (uint32_t)std::min<uint64_t>((wanted + p.N - 1) / p.N, (p.spans + U - 1) / U);
+  set_shape(p, ((p.spans + parts - 1) / parts + U - 1) / U * U);
+  const uint32_t blocks = blocks_for((uint64_t)p.N * p.slices, p.lanes, kCombineBlocks);
   ++launch_counter();
-  combine_kernel<E, V, R, U>
-      <<<blocks_of((uint64_t)p.N * p.slices, p.lanes), kThreads, 0, st>>>(p);
+  combine_kernel<E, V, R, U><<<blocks, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 template <class E, int V>
@@ -302,13 +367,19 @@ cudaError_t combine_of(ExpertParams &p, cudaStream_t st) {
   return combine_by<E, V, kUnderWay<E, V>>(p, st);
 }
 
+template <class E, int V, int U>
+cudaError_t combine_backward_by(ExpertParams &p, cudaStream_t st) {
+  const uint32_t blocks = blocks_for((uint64_t)p.N * p.k, p.lanes, kBackBlocks<E, V>);
+  ++launch_counter();
+  combine_backward_kernel<E, V, U><<<blocks, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
 template <class E, int V>
 cudaError_t combine_backward_of(ExpertParams &p, cudaStream_t st) {
-  set_shape(p, 0);
-  ++launch_counter();
-  combine_backward_kernel<E, V>
-      <<<blocks_of((uint64_t)p.N * p.k, p.lanes), kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  set_shape(p, 1);
+  if (p.spans <= 1) return combine_backward_by<E, V, 1>(p, st);
+  if (p.spans == 2 || kUnderWay<E, V> == 4) return combine_backward_by<E, V, 2>(p, st);
+  return combine_backward_by<E, V, 4>(p, st);
 }
 
 // By the rows' type and the pieces that all of them can be moved by.
