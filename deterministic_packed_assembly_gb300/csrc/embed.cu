@@ -122,7 +122,7 @@ __device__ __forceinline__ void zero_rows(const EmbedParams &p, uint32_t part) {
 }
 
 template <class W, class E, int V>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p) {
+__global__ void __launch_bounds__(kThreads, 3) embed_sum_kernel(const EmbedParams p) {
   pdl_wait();
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (blockIdx.x >= p.sum_blocks) {
@@ -218,10 +218,11 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p
 
 // The tokens across tiles: the tail where one begins and the heads behind it.  A
 // block takes one's 256 columns, each warp a run of its tiles; the runs are added in order.
+constexpr int kJoinWarps = 16;
 template <class W, int V>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const EmbedParams p) {
   pdl_wait();
-  __shared__ float sums[kWarps][kSlice];
+  __shared__ float sums[kJoinWarps][kSlice];
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint64_t units = (uint64_t)*p.counter * p.slices;
   for (uint64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -232,9 +233,9 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams 
       const uint64_t at = (uint64_t)(tile + 1 + more + threadIdx.x) * kTile;
       const int n = __syncthreads_count(at < p.N && p.sorted[at].key == key);
       more += n;
-      if (n < kThreads) break;
+      if (n < 32 * kJoinWarps) break;
     }
-    const uint32_t run = (more + kWarps - 1) / kWarps;
+    const uint32_t run = (more + kJoinWarps - 1) / kJoinWarps;
     const uint32_t a = min(more, warp * run), b = min(more, a + run);
     const uint64_t step = (uint64_t)p.slices * kSlice, at = (uint64_t)slice * kSlice + lane * kOct;
     float acc[kOct] = {};
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams 
 #pragma unroll
       for (int j = 0; j < kOct; ++j) acc[j] = p.tail[tile * step + at + j];
     }
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t t = a; t < b; ++t) {
       const float4 *from = reinterpret_cast<const float4 *>(p.head + (tile + 1 + t) * step + at);
       const float4 x = from[0], y = from[1];
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams 
     for (int j = 0; j < kOct; ++j) sums[warp][lane + 32 * j] = acc[j];
     __syncthreads();
     if (warp == 0) {
-      for (int w = 1; w < kWarps; ++w)
+      for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
         for (int j = 0; j < kOct; ++j) acc[j] += sums[w][lane + 32 * j];
       Ch<2> x[kOct / 2];
@@ -328,8 +329,8 @@ cudaError_t backward_of(EmbedParams &p, void *workspace, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const uint64_t most = (uint64_t)p.tiles * p.slices;
-  pdl_launch(embed_join_kernel<W, V>, dim3((uint32_t)std::min<uint64_t>(most ? most : 1, 4 * 152)),
-             dim3(kThreads), 0, st, p);
+  pdl_launch(embed_join_kernel<W, V>, dim3((uint32_t)std::min<uint64_t>(most ? most : 1, 3 * 152)),
+             dim3(32 * kJoinWarps), 0, st, p);
   return cudaGetLastError();
 }
 

@@ -240,52 +240,62 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks) combine_kernel(const
 }
 
 // ---- combine's backward pass -----------------------------------------------------------
-// L lanes a choice, one after the other: neighbouring units are a token's, whose row stays in
-// the L1 cache.  U spans of both rows are under way, and the next choice's place.
-template <class E, int V, int U>
+// L lanes a choice, T choices at once: neighbouring units are a token's, whose row stays in
+// the L1 cache.  T U spans of both rows are under way, and the next choices' places.
+template <class E, int V, int T, int U>
 __global__ void __launch_bounds__(kThreads, (kBackBlocks<E, V>))
     combine_backward_kernel(const ExpertParams p) {
-  const uint32_t S = p.N * p.k, lane = threadIdx.x % p.lanes;
+  const uint32_t S = p.N * p.k, lane = threadIdx.x % p.lanes, groups = kThreads / p.lanes;
   const uint32_t M = min((uint32_t)p.offsets[p.E], S);
   const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint64_t every = (uint64_t)gridDim.x * kThreads / p.lanes;
-  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
-  const uint64_t base = (uint64_t)blockIdx.x * (kThreads / p.lanes);  // of the block
-  Chosen<1> now, next;
-  const auto look = [&](Chosen<1> &c, uint64_t s) {
-    c.at[0] = s < S ? (uint32_t)p.place[s] : S;
-    c.w[0] = s < S && p.weights ? p.weights[s] : 1.0f;
+  const uint64_t every = (uint64_t)gridDim.x * groups * T;
+  const uint64_t base = (uint64_t)blockIdx.x * groups * T;  // of the block
+  Chosen<T> now, next;
+  const auto look = [&](Chosen<T> &c, uint64_t b) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const uint64_t s = b + t * groups + threadIdx.x / p.lanes;
+      c.at[t] = s < S ? (uint32_t)p.place[s] : S;
+      c.w[t] = s < S && p.weights ? p.weights[s] : 1.0f;
+    }
   };
-  look(now, unit);
+  look(now, base);
   // all lanes stay: they add up together
-  for (uint64_t b = base, s = unit; b < S; b += every, s += every) {
-    look(next, s + every);
-    const uint32_t at = now.at[0], n = (uint32_t)(s < S ? s : S - 1) / p.k;
-    const E *d_out = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
-    const E *y = static_cast<const E *>(p.from) + (int64_t)at * p.from_row;
-    E *to = static_cast<E *>(p.to) + (int64_t)at * p.D;
-    const bool there = at < M;
-    const Ch<2> w = splat<2>(there ? now.w[0] : 1.0f);
-    Ch<2> dot = {0.0f, 0.0f};
-    if (at < S) {
-      for (uint32_t c = lane * V; c < p.D; c += U * span) {
-        Oct<E, V> a[U], y8[U];
+  for (uint64_t b = base; b < S; b += every) {
+    look(next, b + every);
+    Ch<2> dot[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) dot[t] = {0.0f, 0.0f};
+    for (uint32_t c = lane * V; c < p.D; c += U * span) {
+      Oct<E, V> a[T][U], y[T][U];
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const uint64_t s = b + t * groups + threadIdx.x / p.lanes;
+        const uint32_t n = (uint32_t)(s < S ? s : 0) / p.k;
+        const E *d_out = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
+        const E *from = static_cast<const E *>(p.from) + (int64_t)now.at[t] * p.from_row;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          clear(a[u]), clear(y8[u]);
-          if (there) {
-            load_oct(a[u], d_out, c + u * span, step, p.D);
-            if (p.d_weights) load_oct(y8[u], y, c + u * span, step, p.D);
+          clear(a[t][u]), clear(y[t][u]);
+          if (now.at[t] < M) {
+            load_oct(a[t][u], d_out, c + u * span, step, p.D);
+            if (p.d_weights) load_oct(y[t][u], from, c + u * span, step, p.D);
           }
         }
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        if (now.at[t] >= S) continue;
+        E *to = static_cast<E *>(p.to) + (int64_t)now.at[t] * p.D;
+        const Ch<2> w = splat<2>(now.at[t] < M ? now.w[t] : 1.0f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           Ch<2> d[kOct / 2], x[kOct / 2];
-          widen(a[u], d);
-          widen(y8[u], x);
+          widen(a[t][u], d);
+          widen(y[t][u], x);
 #pragma unroll
           for (int i = 0; i < kOct / 2; ++i) {
-            dot = fma(d[i], x[i], dot);
+            dot[t] = fma(d[i], x[i], dot[t]);
             d[i] = d[i] * w;
           }
           store_oct(to, c + u * span, step, p.D, narrow<E, V>(d));
@@ -293,9 +303,13 @@ __global__ void __launch_bounds__(kThreads, (kBackBlocks<E, V>))
       }
     }
     if (p.d_weights) {
-      float sum = dot.v[0] + dot.v[1];
-      for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (s < S && lane == 0) p.d_weights[s] = sum;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const uint64_t s = b + t * groups + threadIdx.x / p.lanes;
+        float sum = dot[t].v[0] + dot[t].v[1];
+        for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (s < S && lane == 0) p.d_weights[s] = sum;
+      }
     }
     now = next;
   }
@@ -367,19 +381,21 @@ cudaError_t combine_of(ExpertParams &p, cudaStream_t st) {
   return combine_by<E, V, kUnderWay<E, V>>(p, st);
 }
 
-template <class E, int V, int U>
+template <class E, int V, int T, int U>
 cudaError_t combine_backward_by(ExpertParams &p, cudaStream_t st) {
-  const uint32_t blocks = blocks_for((uint64_t)p.N * p.k, p.lanes, kBackBlocks<E, V>);
+  const uint64_t units = ((uint64_t)p.N * p.k + T - 1) / T;
   ++launch_counter();
-  combine_backward_kernel<E, V, U><<<blocks, kThreads, 0, st>>>(p);
+  combine_backward_kernel<E, V, T, U>
+      <<<blocks_for(units, p.lanes, kBackBlocks<E, V>), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 template <class E, int V>
 cudaError_t combine_backward_of(ExpertParams &p, cudaStream_t st) {
+  constexpr int K = kUnderWay<E, V> / 2;
   set_shape(p, 1);
-  if (p.spans <= 1) return combine_backward_by<E, V, 1>(p, st);
-  if (p.spans == 2 || kUnderWay<E, V> == 4) return combine_backward_by<E, V, 2>(p, st);
-  return combine_backward_by<E, V, 4>(p, st);
+  if (p.spans <= 1) return combine_backward_by<E, V, K, 1>(p, st);
+  if (p.spans == 2) return combine_backward_by<E, V, K / 2, 2>(p, st);
+  return combine_backward_by<E, V, 1, K>(p, st);
 }
 
 // By the rows' type and the pieces that all of them can be moved by.

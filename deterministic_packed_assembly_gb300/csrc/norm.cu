@@ -11,8 +11,8 @@
 //
 // Rows come through a ring in shared memory (ring.cuh), filled by the bulk copy engine, so
 // that memory is kept busy while sums are exchanged, and rows that begin anywhere cost no
-// more than others; a batch of four rows shares the barriers.  Rows of up to 512 columns (a
-// warp or two) and calls of few rows are read straight from memory.  Backward each thread
+// more than others; a batch of four rows shares the barriers.  Rows of up to 512 columns, which a
+// warp or a part of one has, and forward calls of few rows are read straight from memory.  Backward each thread
 // keeps the sums of its columns' dw and db over all its block's rows; blocks write them out
 // once, and the last kernel adds the blocks' rows in order.  Rows of more than 19200 columns
 // (or that do not fit the ring twice) are read again instead of kept.

@@ -50,8 +50,16 @@ inline NormShape norm_shape(uint32_t D, bool back) {
   NormShape s;
   s.lanes = lanes_for(D);
   const uint64_t spans = spans_for(D, s.lanes);
+  if (D <= kNormNarrow) {
+    s.nb = (uint32_t)spans, s.warps = 1;
+    return s;
+  }
   const uint32_t few = back ? kNormWarps : 5;
-  s.nb = spans <= few ? 1 : spans <= 2 * few ? 2 : spans <= 3 * few ? 3 : 5;
+  s.nb = spans <= few                ? 1
+         : spans <= 2 * few          ? 2
+         : spans <= 3 * few          ? 3
+         : !back && spans <= 4 * few ? 4
+                                     : 5;
   s.warps = (uint32_t)((spans + s.nb - 1) / s.nb);
   return s;
 }
@@ -74,6 +82,12 @@ inline NormRing norm_ring(uint32_t D, uint32_t es, uint32_t arrays, uint32_t mos
     }
   return {0, 0, 0, 0};
 }
+
+// Rows that a lane takes at once where a warp, or a part of one, has whole rows: 16
+// registers of each array's.
+template <class E, int NB, int V>
+constexpr int kNormAtOnce =
+    NB * Oct<E, V>::kPieces * Oct<E, V>::kWords > 8 ? 1 : 16 / (NB * Oct<E, V>::kPieces * Oct<E, V>::kWords);
 
 // ---- sums over a row's lanes ------------------------------------------------------------
 __device__ __forceinline__ float lanes_sum(float v, uint32_t lanes) {

@@ -6,115 +6,97 @@
 namespace nsk {
 namespace {
 
-constexpr int kDirectThreads = 320;  // of rows straight from memory
-constexpr int kColumnWarps = 8;      // of 256 columns' sums
+constexpr int kNarrowWarps = 8;   // of a block of narrow rows
+constexpr int kColumnWarps = 8;    // of 256 columns' sums
 
-// ---- rows straight from memory -----------------------------------------------------------
-// Groups of `warps` warps (or of `lanes` lanes) walk rows, the next one's loads under way.
-// A row's values as they lie, its statistics, and whether it is one.
-template <class E, int NC, int V>
-struct NormRow {
-  Oct<E, V> x[NC], g[NC];
-  float mean, rstd;
-  bool real, there;
-};
-template <class E, int NC, int V>
-__device__ __forceinline__ void load_row(NormRow<E, NC, V> &r, const NormParams &p, uint64_t n,
-                                         uint32_t first, uint32_t span, uint32_t step) {
-  r.real = n < p.N;
-  r.there = r.real && !(p.doc && p.doc[n] < 0);
-  r.mean = r.rstd = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) clear(r.x[i]), clear(r.g[i]);
-  if (!r.there) return;
-  r.mean = p.mean[n], r.rstd = p.rstd[n];
-  const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
-  const E *dy = static_cast<const E *>(p.dy) + (int64_t)n * p.dy_row;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    load_oct(r.x[i], x, first + i * span, step, p.D);
-    load_oct(r.g[i], dy, first + i * span, step, p.D);
-  }
-}
-
-template <class E, int V>
-__global__ void __launch_bounds__(kDirectThreads, 2) norm_backward_direct_kernel(const NormParams p) {
-  constexpr int NC = 1;
-  __shared__ float2 sums[2][kDirectThreads / 32];
-  extern __shared__ float joined[];  // [2][columns]: the groups' sums
-  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const uint32_t group = warp / p.warps, part = warp % p.warps;
-  const uint32_t groups = blockDim.x / 32 / p.warps, per = 32 / p.lanes;
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint32_t first = part * NC * span + lane % p.lanes * V;
+// ---- narrow rows ---------------------------------------------------------------------------
+// Rows of up to two spans: `lanes` lanes of a warp walk rows, M at once.
+template <class E, int NB, int V>
+__global__ void __launch_bounds__(32 * kNarrowWarps, 2)
+    norm_backward_narrow_kernel(const NormParams p) {
+  constexpr int M = kNormAtOnce<E, NB, V>;
+  __shared__ float joined[2][NB * 32 * kOct];  // the warps' sums
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = 32 / p.lanes;
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V, first = lane % p.lanes * V;
   const float share = 1.0f / (float)p.D;
-  Ch<2> w[NC][kOct / 2], dw[NC][kOct / 2], db[NC][kOct / 2];
+  Ch<2> w[NB][kOct / 2], dw[NB][kOct / 2], db[NB][kOct / 2];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
+  for (int i = 0; i < NB; ++i) {
 #pragma unroll
     for (int j = 0; j < kOct / 2; ++j) dw[i][j] = db[i][j] = {0.0f, 0.0f};
     load_vector<E, V>(p.weight, p.floats, first + i * span, step, p.D, 1.0f, w[i]);
   }
-  const uint64_t every = (uint64_t)gridDim.x * groups * per;
-  uint32_t turn = 0;
-  // a group's lanes stay together: rows from the first lane's on
-  uint64_t n0 = ((uint64_t)blockIdx.x * groups + group) * per;
-  NormRow<E, NC, V> row;
-  load_row(row, p, n0 + lane / p.lanes, first, span, step);
-  for (; n0 < p.N; n0 += every) {
-    NormRow<E, NC, V> next;
-    load_row(next, p, n0 + every + lane / p.lanes, first, span, step);
-    const Ch<2> minus = splat<2>(-row.mean), scale = splat<2>(row.rstd);
-    Ch<2> s1 = {0.0f, 0.0f}, s2 = {0.0f, 0.0f};
+  // a warp's lanes stay together: rows from its first lane's on
+  const uint64_t every = (uint64_t)gridDim.x * kNarrowWarps * M * per;
+  for (uint64_t n1 = ((uint64_t)blockIdx.x * kNarrowWarps + warp) * M * per; n1 < p.N; n1 += every) {
+    const uint64_t n0 = n1 + lane / p.lanes;
+    Oct<E, V> x[M][NB], y[M][NB];
+    float mean[M], rstd[M], s1[M], s2[M];
+    bool there[M];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      Ch<2> f[kOct / 2], g[kOct / 2];
-      widen(row.x[i], f);
-      widen(row.g[i], g);
-#pragma unroll
-      for (int j = 0; j < kOct / 2; ++j) {
-        const Ch<2> xh = (f[j] + minus) * scale, gw = g[j] * w[i][j];
-        s1 = s1 + gw;
-        s2 = fma(gw, xh, s2);
-        dw[i][j] = fma(g[j], xh, dw[i][j]);
-        db[i][j] = db[i][j] + g[j];
-      }
+    for (int m = 0; m < M; ++m) {
+      const uint64_t n = n0 + m * per;
+      there[m] = n < p.N && !(p.doc && p.doc[n] < 0);
+      mean[m] = there[m] ? p.mean[n] : 0.0f, rstd[m] = there[m] ? p.rstd[n] : 0.0f;
     }
-    float a = lanes_sum(s1.v[0] + s1.v[1], p.lanes), b = lanes_sum(s2.v[0] + s2.v[1], p.lanes);
-    if (p.warps > 1) {  // two buffers: one barrier a row
-      if (lane == 0) sums[turn][warp] = make_float2(a, b);
-      group_sync(group, p.warps);
-      a = b = 0.0f;
-      for (uint32_t k = 0; k < p.warps; ++k) {
-        const float2 v = sums[turn][group * p.warps + k];
-        a += v.x, b += v.y;
-      }
-      turn ^= 1;
-    }
-    const Ch<2> m1 = splat<2>(-a * share), m2 = splat<2>(-b * share);
-    if (row.real) {
-      E *dx = static_cast<E *>(p.y) + (int64_t)(n0 + lane / p.lanes) * p.D;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        clear(x[m][i]), clear(y[m][i]);
+        if (!there[m]) continue;
+        load_oct(x[m][i], static_cast<const E *>(p.x) + (int64_t)(n0 + m * per) * p.x_row,
+                 first + i * span, step, p.D);
+        load_oct(y[m][i], static_cast<const E *>(p.dy) + (int64_t)(n0 + m * per) * p.dy_row,
+                 first + i * span, step, p.D);
+      }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      Ch<2> a = {0.0f, 0.0f}, b = a;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
         Ch<2> f[kOct / 2], g[kOct / 2];
-        forget(row.x[i]), forget(row.g[i]);
-        widen(row.x[i], f);
-        widen(row.g[i], g);
+        widen(x[m][i], f);
+        widen(y[m][i], g);
 #pragma unroll
         for (int j = 0; j < kOct / 2; ++j) {
-          const Ch<2> xh = (f[j] + minus) * scale;
-          f[j] = scale * fma(xh, m2, fma(g[j], w[i][j], m1));
-          if (!row.there) f[j] = {0.0f, 0.0f};
+          const Ch<2> xh = (f[j] + splat<2>(-mean[m])) * splat<2>(rstd[m]), gw = g[j] * w[i][j];
+          a = a + gw;
+          b = fma(gw, xh, b);
+          dw[i][j] = fma(g[j], xh, dw[i][j]);
+          db[i][j] = db[i][j] + g[j];
+        }
+      }
+      s1[m] = a.v[0] + a.v[1], s2[m] = b.v[0] + b.v[1];
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      s1[m] = lanes_sum(s1[m], p.lanes) * -share, s2[m] = lanes_sum(s2[m], p.lanes) * -share;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const uint64_t n = n0 + m * per;
+      if (n >= p.N) break;
+      E *dx = static_cast<E *>(p.y) + (int64_t)n * p.D;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        Ch<2> f[kOct / 2], g[kOct / 2];
+        forget(x[m][i]), forget(y[m][i]);
+        widen(x[m][i], f);
+        widen(y[m][i], g);
+#pragma unroll
+        for (int j = 0; j < kOct / 2; ++j) {
+          const Ch<2> scale = splat<2>(rstd[m]), xh = (f[j] + splat<2>(-mean[m])) * scale;
+          f[j] = scale * fma(xh, splat<2>(s2[m]), fma(g[j], w[i][j], splat<2>(s1[m])));
+          if (!there[m]) f[j] = {0.0f, 0.0f};
         }
         store_oct(dx, first + i * span, step, p.D, narrow<E, V>(f));
       }
     }
-    row = next;
   }
   if (!p.partial) return;
-  // lanes that share columns, then groups that do, in order
+  // lanes that share columns, then warps, in order
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < kOct / 2; ++j)
       for (uint32_t o = p.lanes; o < 32; o <<= 1)
@@ -123,26 +105,23 @@ __global__ void __launch_bounds__(kDirectThreads, 2) norm_backward_direct_kernel
           dw[i][j].v[h] += __shfl_xor_sync(kFull, dw[i][j].v[h], o);
           db[i][j].v[h] += __shfl_xor_sync(kFull, db[i][j].v[h], o);
         }
-  const uint32_t columns = p.warps * NC * span;
-  for (uint32_t g = 0; g < groups; ++g) {
-    if (g == group && lane < p.lanes) {
+  for (uint32_t g = 0; g < kNarrowWarps; ++g) {
+    if (g == warp && lane < p.lanes) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int j = 0; j < kOct; ++j) {
-          float *a = joined + first + i * span + j / V * step + j % V, *b = a + columns;
+          const uint32_t c = first + i * span + j / V * step + j % V;
           const float u = dw[i][j / 2].v[j & 1], v = db[i][j / 2].v[j & 1];
-          *a = g ? *a + u : u;
-          *b = g ? *b + v : v;
+          joined[0][c] = g ? joined[0][c] + u : u;
+          joined[1][c] = g ? joined[1][c] + v : v;
         }
     }
     __syncthreads();
   }
   float *to = p.partial + (uint64_t)blockIdx.x * 2 * p.D;
-  for (uint32_t c = threadIdx.x; c < p.D; c += blockDim.x) {
-    to[c] = joined[c];
-    to[p.D + c] = joined[columns + c];
-  }
+  for (uint32_t c = threadIdx.x; c < p.D; c += blockDim.x)
+    to[c] = joined[0][c], to[p.D + c] = joined[1][c];
 }
 
 // ---- rows through the ring -----------------------------------------------------------------
@@ -409,13 +388,12 @@ cudaError_t wide_of(NormParams &p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <class E, int V>
-cudaError_t direct_of(NormParams &p, cudaStream_t st) {
-  const uint32_t groups = kDirectThreads / 32 / p.warps, rows = groups * (32 / p.lanes);
-  p.blocks = (uint32_t)std::min<uint64_t>(((uint64_t)p.N + rows - 1) / rows, 2 * kNormSMs);
-  const size_t shared = 2 * sizeof(float) * p.warps * p.lanes * kOct;
+template <class E, int NB, int V>
+cudaError_t narrow_of(NormParams &p, cudaStream_t st) {
+  const uint64_t rows = kNarrowWarps * (32 / p.lanes) * kNormAtOnce<E, NB, V>;
+  p.blocks = (uint32_t)std::min<uint64_t>((p.N + rows - 1) / rows, 2 * kNormSMs);
   ++launch_counter();
-  norm_backward_direct_kernel<E, V><<<p.blocks, groups * p.warps * 32, shared, st>>>(p);
+  norm_backward_narrow_kernel<E, NB, V><<<p.blocks, 32 * kNarrowWarps, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -423,7 +401,8 @@ template <class E, int V>
 cudaError_t backward_of(NormParams &p, cudaStream_t st) {
   const NormShape s = norm_shape(p.D, true);
   p.lanes = s.lanes, p.warps = s.warps;
-  if (p.D <= kNormNarrow) return direct_of<E, V>(p, st);
+  if (p.D <= kNormNarrow)
+    return s.nb == 1 ? narrow_of<E, 1, V>(p, st) : narrow_of<E, 2, V>(p, st);
   if (p.D > kNormKept) return wide_of<E, V>(p, st);
   bool done = false;
   const cudaError_t e =

@@ -9,17 +9,16 @@ namespace {
 constexpr int kDirectWarps = 8;  // of a block of rows of up to as many warps
 
 // ---- rows straight from memory -----------------------------------------------------------
-// Rows of `lanes` lanes of a warp, or of `warps` warps; a lane has NB spans of each.
+// A group of `warps` warps a row; a lane has NB spans of it.
 template <class E, int NB, int V>
 __global__ void __launch_bounds__(32 * kNormWarps) norm_direct_kernel(const NormParams p) {
   __shared__ float sums[2][kNormWarps];
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint32_t group = warp / p.warps, part = warp % p.warps;
-  const uint32_t groups = blockDim.x / 32 / p.warps, per = 32 / p.lanes;
-  const uint64_t n = ((uint64_t)blockIdx.x * groups + group) * per + lane / p.lanes;
+  const uint64_t n = (uint64_t)blockIdx.x * (blockDim.x / 32 / p.warps) + group;
   const bool real = n < p.N, there = real && !(p.doc && p.doc[n] < 0);
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint32_t first = part * NB * span + lane % p.lanes * V;
+  constexpr uint32_t span = 32 * kOct, step = 32 * V;
+  const uint32_t first = part * NB * span + lane * V;
   const E *x = static_cast<const E *>(p.x) + (int64_t)(real ? n : 0) * p.x_row;
   E *y = static_cast<E *>(p.y) + (int64_t)(real ? n : 0) * p.D;
   const float share = 1.0f / (float)p.D;
@@ -37,7 +36,7 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_direct_kernel(const Norm
 #pragma unroll
     for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
   }
-  float sum = lanes_sum(two.v[0] + two.v[1], p.lanes);
+  float sum = lanes_sum(two.v[0] + two.v[1], 32);
   if (p.warps > 1) {
     if (lane == 0) sums[0][warp] = sum;
     group_sync(group, p.warps);
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_direct_kernel(const Norm
       two = fma(d, d, two);
     }
   }
-  float square = lanes_sum(two.v[0] + two.v[1], p.lanes);
+  float square = lanes_sum(two.v[0] + two.v[1], 32);
   if (p.warps > 1) {
     if (lane == 0) sums[1][warp] = square;
     group_sync(group, p.warps);
@@ -85,9 +84,100 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_direct_kernel(const Norm
     }
     if (real) store_oct(y, c, step, p.D, narrow<E, V>(f));
   }
-  if (real && part == 0 && lane % p.lanes == 0) {
+  if (real && part == 0 && lane == 0) {
     if (p.mean) p.mean[n] = there ? mean : 0.0f;
     if (p.rstd) p.rstd[n] = there ? rstd : 0.0f;
+  }
+}
+
+// ---- narrow rows ---------------------------------------------------------------------------
+// Rows of up to two spans: `lanes` lanes of a warp take M rows at once.
+template <class E, int NB, int V>
+__global__ void __launch_bounds__(32 * kDirectWarps) norm_narrow_kernel(const NormParams p) {
+  constexpr int M = kNormAtOnce<E, NB, V>;
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = 32 / p.lanes;
+  const uint32_t span = p.lanes * kOct, step = p.lanes * V, first = lane % p.lanes * V;
+  const uint64_t n0 = ((uint64_t)blockIdx.x * kDirectWarps + warp) * M * per + lane / p.lanes;
+  const float share = 1.0f / (float)p.D;
+  Oct<E, V> v[M][NB];
+  bool there[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const uint64_t n = n0 + m * per;
+    there[m] = n < p.N && !(p.doc && p.doc[n] < 0);
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const E *x = static_cast<const E *>(p.x) + (int64_t)(n0 + m * per) * p.x_row;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      clear(v[m][i]);
+      if (there[m]) load_oct(v[m][i], x, first + i * span, step, p.D);
+    }
+  }
+  Ch<2> w[NB][kOct / 2], b[NB][kOct / 2];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    load_vector<E, V>(p.weight, p.floats, first + i * span, step, p.D, 1.0f, w[i]);
+    load_vector<E, V>(p.bias, p.floats, first + i * span, step, p.D, 0.0f, b[i]);
+  }
+  float mean[M], rstd[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    Ch<2> two = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      Ch<2> f[kOct / 2];
+      widen(v[m][i], f);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
+    }
+    mean[m] = two.v[0] + two.v[1];
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) mean[m] = lanes_sum(mean[m], p.lanes) * share;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    Ch<2> two = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      Ch<2> f[kOct / 2];
+      forget(v[m][i]);
+      widen(v[m][i], f);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) {
+        Ch<2> d = f[j] + splat<2>(-mean[m]);
+        if (!inside<V>(first + i * span, step, p.D, 2 * j)) d.v[0] = 0.0f;
+        if (!inside<V>(first + i * span, step, p.D, 2 * j + 1)) d.v[1] = 0.0f;
+        two = fma(d, d, two);
+      }
+    }
+    rstd[m] = two.v[0] + two.v[1];
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+    rstd[m] = __frsqrt_rn(fmaf(lanes_sum(rstd[m], p.lanes), share, p.eps));
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const uint64_t n = n0 + m * per;
+    if (n >= p.N) break;
+    E *y = static_cast<E *>(p.y) + (int64_t)n * p.D;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      Ch<2> f[kOct / 2];
+      forget(v[m][i]);
+      widen(v[m][i], f);
+#pragma unroll
+      for (int j = 0; j < kOct / 2; ++j) {
+        f[j] = fma((f[j] + splat<2>(-mean[m])) * splat<2>(rstd[m]), w[i][j], b[i][j]);
+        if (!there[m]) f[j] = {0.0f, 0.0f};
+      }
+      store_oct(y, first + i * span, step, p.D, narrow<E, V>(f));
+    }
+    if (lane % p.lanes == 0) {
+      if (p.mean) p.mean[n] = there[m] ? mean[m] : 0.0f;
+      if (p.rstd) p.rstd[n] = there[m] ? rstd[m] : 0.0f;
+    }
   }
 }
 
@@ -280,7 +370,7 @@ cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
 // Batches of four, two or one row, of which the widest rows have the last two.
 template <class E, int NB, int V, int kWarps, int kBlocks>
 cudaError_t ring_of(NormParams &p, bool &done, cudaStream_t st) {
-  constexpr uint32_t kMost = NB > 3 ? 2 : 4;
+  constexpr uint32_t kMost = NB > 4 ? 2 : 4;
   const NormRing ring = norm_ring(p.D, sizeof(E), 1, kBlocks, kMost, kMost / 2, 0);
   done = ring.stages > 0;
   if (!done) return cudaSuccess;
@@ -297,24 +387,37 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
   }
   const NormShape s = norm_shape(p.D, false);
   p.lanes = s.lanes, p.warps = s.warps;
+  if (p.D <= kNormNarrow) {
+    ++launch_counter();
+    if (s.nb == 1) {
+      const uint32_t rows = kDirectWarps * (32 / p.lanes) * kNormAtOnce<E, 1, V>;
+      norm_narrow_kernel<E, 1, V><<<(p.N + rows - 1) / rows, 32 * kDirectWarps, 0, st>>>(p);
+    } else {
+      const uint32_t rows = kDirectWarps * (32 / p.lanes) * kNormAtOnce<E, 2, V>;
+      norm_narrow_kernel<E, 2, V><<<(p.N + rows - 1) / rows, 32 * kDirectWarps, 0, st>>>(p);
+    }
+    return cudaGetLastError();
+  }
   // rows that fill the SMs' rings, else straight from memory: a call of 64 rows waits for
   // nothing but its own loads
-  if (p.D > kNormNarrow && p.N > 4 * kNormSMs) {
+  if (p.N > 4 * kNormSMs) {
     bool done = false;
     const cudaError_t e = s.nb == 1       ? ring_of<E, 1, V, 5, 5>(p, done, st)
                           : s.nb == 2     ? ring_of<E, 2, V, 5, 4>(p, done, st)
                           : s.nb == 3     ? ring_of<E, 3, V, 5, 3>(p, done, st)
+                          : s.nb == 4     ? ring_of<E, 4, V, 5, 3>(p, done, st)
                           : s.warps <= 7  ? ring_of<E, 5, V, 7, 2>(p, done, st)
                                           : ring_of<E, 5, V, kNormWarps, 1>(p, done, st);
     if (done) return e;
   }
   const uint32_t groups = std::max<uint32_t>(1, kDirectWarps / p.warps);
-  const uint32_t threads = groups * p.warps * 32, rows = groups * (32 / p.lanes);
-  const uint32_t blocks = (uint32_t)(((uint64_t)p.N + rows - 1) / rows);
+  const uint32_t threads = groups * p.warps * 32;
+  const uint32_t blocks = (uint32_t)(((uint64_t)p.N + groups - 1) / groups);
   ++launch_counter();
   auto *k = s.nb == 1   ? norm_direct_kernel<E, 1, V>
             : s.nb == 2 ? norm_direct_kernel<E, 2, V>
             : s.nb == 3 ? norm_direct_kernel<E, 3, V>
+            : s.nb == 4 ? norm_direct_kernel<E, 4, V>
                         : norm_direct_kernel<E, 5, V>;
   k<<<blocks, threads, 0, st>>>(p);
   return cudaGetLastError();
