@@ -64,16 +64,22 @@ inline NormShape norm_shape(uint32_t D, bool back) {
   return s;
 }
 
+// Columns that a row's threads have.
+__host__ __device__ __forceinline__ uint32_t norm_columns(uint32_t nb, uint32_t warps) {
+  return nb * warps * 32 * kOct;
+}
+inline uint32_t norm_columns(const NormShape &s) { return norm_columns(s.nb, s.warps); }
+
 // The ring of a pass with `arrays` rows a position: as many blocks an SM as may be, batches
 // as large as leave two stages; or no stages where two rows do not fit.
 struct NormRing {
   uint32_t stages, rows, blocks;  // blocks an SM
   size_t shared;
 };
-inline NormRing norm_ring(uint32_t D, uint32_t es, uint32_t arrays, uint32_t most_blocks,
+inline NormRing norm_ring(const NormShape &shape, uint32_t es, uint32_t arrays, uint32_t most_blocks,
                           uint32_t most_rows, uint32_t least_rows, uint32_t besides) {
   constexpr uint32_t kShared = 224 * 1024, kHead = 2 * 1024;  // of an SM; of a block besides
-  const uint32_t slot = ring_slot(D, es) * arrays;
+  const uint32_t slot = ring_slot(norm_columns(shape), es) * arrays;
   for (uint32_t blocks = most_blocks; blocks > 0; --blocks)
     for (uint32_t rows = most_rows; rows >= least_rows; rows /= 2) {
       const uint32_t room = kShared / blocks - 1024 - kHead - besides;
@@ -98,9 +104,9 @@ __device__ __forceinline__ float lanes_sum(float v, uint32_t lanes) {
 __device__ __forceinline__ void group_sync(uint32_t group, uint32_t warps) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
 }
-// K sums over `warps` warps at once, the same in every thread: lanes halve the values
+// K sums over `warps` warps (at most kWarps) at once, the same in every thread: lanes halve the values
 // they add up as they halve their distance, in the order of lanes_sum.  part: [warps][K].
-template <int K>
+template <int K, int kWarps>
 __device__ __forceinline__ void batch_sums(float (&v)[K], float *part, uint32_t warps,
                                            uint32_t warp, uint32_t lane) {
 #pragma unroll
@@ -120,7 +126,9 @@ __device__ __forceinline__ void batch_sums(float (&v)[K], float *part, uint32_t 
   if (lane % (32 / K) == 0) part[warp * K + lane / (32 / K)] = v[0];
   group_sync(0, warps);
   float sum = 0.0f;
-  for (uint32_t w = 0; w < warps; ++w) sum += part[w * K + lane % K];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < (int)warps) sum += part[w * K + lane % K];
 #pragma unroll
   for (int i = 0; i < K; ++i) v[i] = __shfl_sync(kFull, sum, i);
 }
@@ -185,9 +193,10 @@ __device__ __forceinline__ char *ring_row(char *rows, uint32_t stage, uint32_t a
 // The warp that copies: lane r has row r of each batch.  Documents and statistics are read a
 // batch ahead, so that their way does not hold up the copies.
 template <class E, int R, bool kBack>
-__device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, char *rows) {
+__device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, char *rows,
+                                             uint32_t slot) {
   NormShared &sh = *reinterpret_cast<NormShared *>(shared);
-  const uint32_t lane = threadIdx.x % 32, slot = ring_slot(p.D, sizeof(E));
+  const uint32_t lane = threadIdx.x % 32;
   constexpr uint32_t kArrays = kBack ? 2 : 1;
   if (lane >= R) return;
   const uint64_t every = (uint64_t)gridDim.x * R;

@@ -140,13 +140,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
   constexpr bool kHeld = NB <= 3;
   Ch<2> *kept = reinterpret_cast<Ch<2> *>(shared + kNormRows);
   char *rows = shared + kNormRows + (kHeld ? 0 : p.warps * NB * 32 * kOct * sizeof(float));
+  const uint32_t slot = ring_slot(norm_columns(NB, p.warps), sizeof(E));
   start_ring<R>(shared, p.stages, p.warps);
   if (warp == p.warps) {
-    produce_rows<E, R, true>(p, shared, rows);
+    produce_rows<E, R, true>(p, shared, rows, slot);
     return;
   }
   constexpr uint32_t kSpan = 32 * kOct, kStep = 32 * V;
-  const uint32_t first = warp * NB * kSpan + lane * V, slot = ring_slot(p.D, sizeof(E));
+  const uint32_t first = warp * NB * kSpan + lane * V;
   const float share = 1.0f / (float)p.D;
   Ch<2> w[kHeld ? NB : 1][kOct / 2], dw[NB][kOct / 2], db[NB][kOct / 2];
 #pragma unroll
@@ -166,20 +167,21 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
       for (int j = 0; j < kOct / 2; ++j) w[0][j] = kept[((warp * NB + i) * (kOct / 2) + j) * 32 + lane];
     }
   };
+  const bool all = (warp + 1) * NB * kSpan <= p.D;  // none of the warp's columns beyond the row
   bool lost = false;
   uint32_t stage = 0, turn = 0, buffer = 0;
   for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
     if (!lost && !barrier_wait(&sh.full[stage], turn & 1)) lost = true;
-    const char *xr[R], *gr[R];
+    const char *xr[R], *gr[R];  // this lane's first columns
     float v[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      uint32_t xo = 0, go = 0;
+      uint32_t xo = first * sizeof(E), go = xo;
       if constexpr (Oct<E, V>::kBytes < 16) {
-        xo = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
-                                                   (int64_t)(n0 + r) * p.x_row) & 15u;
-        go = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.dy) +
-                                                   (int64_t)(n0 + r) * p.dy_row) & 15u;
+        xo += (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
+                                                    (int64_t)(n0 + r) * p.x_row) & 15u;
+        go += (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.dy) +
+                                                    (int64_t)(n0 + r) * p.dy_row) & 15u;
       }
       xr[r] = ring_row(rows, stage, 0, 2, R, r, slot) + xo;
       gr[r] = ring_row(rows, stage, 1, 2, R, r, slot) + go;
@@ -191,8 +193,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
         for (int i = 0; i < NB; ++i) {
           Oct<E, V> x, y;
           Ch<2> f[kOct / 2], g[kOct / 2];
-          ring_oct(x, xr[r], first + i * kSpan, kStep, p.D);
-          ring_oct(y, gr[r], first + i * kSpan, kStep, p.D);
+          ring_oct(x, xr[r] + i * kSpan * sizeof(E));
+          ring_oct(y, gr[r] + i * kSpan * sizeof(E));
+          if (!all) only(x, first + i * kSpan, p.D), only(y, first + i * kSpan, p.D);
           weights(i);
           widen(x, f);
           widen(y, g);
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
       }
       v[2 * r] = s1.v[0] + s1.v[1], v[2 * r + 1] = s2.v[0] + s2.v[1];
     }
-    batch_sums<2 * R>(v, sh.part[buffer], p.warps, warp, lane);
+    batch_sums<2 * R, kWarps>(v, sh.part[buffer], p.warps, warp, lane);
     buffer ^= 1;  // two buffers: one barrier a batch
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -220,20 +223,27 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
       E *dx = static_cast<E *>(p.y) + (int64_t)n * p.D;
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
+        const uint32_t c = first + i * kSpan;
         Oct<E, V> x, y;
-        Ch<2> f[kOct / 2], g[kOct / 2];
-        ring_oct(x, xr[r], first + i * kSpan, kStep, p.D);
-        ring_oct(y, gr[r], first + i * kSpan, kStep, p.D);
-        weights(i);
-        widen(x, f);
-        widen(y, g);
+        clear(x);
+        if (head.there) {
+          Ch<2> f[kOct / 2], g[kOct / 2];
+          ring_oct(x, xr[r] + i * kSpan * sizeof(E));
+          ring_oct(y, gr[r] + i * kSpan * sizeof(E));
+          weights(i);
+          widen(x, f);
+          widen(y, g);
 #pragma unroll
-        for (int j = 0; j < kOct / 2; ++j) {
-          const Ch<2> xh = (f[j] + minus) * scale;
-          f[j] = scale * fma(xh, m2, fma(g[j], w[kHeld ? i : 0][j], m1));
-          if (!head.there) f[j] = {0.0f, 0.0f};
+          for (int j = 0; j < kOct / 2; ++j) {
+            const Ch<2> xh = (f[j] + minus) * scale;
+            f[j] = scale * fma(xh, m2, fma(g[j], w[kHeld ? i : 0][j], m1));
+          }
+          x = narrow<E, V>(f);
         }
-        store_oct(dx, first + i * kSpan, kStep, p.D, narrow<E, V>(f));
+        if (all)
+          store_all(dx + c, x);
+        else
+          store_oct(dx, c, kStep, p.D, x);
       }
     }
     __syncwarp();
@@ -362,7 +372,7 @@ cudaError_t launch_back_ring(NormParams &p, const NormRing &ring, cudaStream_t s
 template <class E, int NB, int V, int kWarps, int kBlocks, uint32_t kMost, uint32_t kLeast>
 cudaError_t back_ring_of(NormParams &p, bool &done, cudaStream_t st) {
   const uint32_t besides = NB > 3 ? p.warps * NB * 32 * kOct * (uint32_t)sizeof(float) : 0;
-  const NormRing ring = norm_ring(p.D, sizeof(E), 2, kBlocks, kMost, kLeast, besides);
+  const NormRing ring = norm_ring(norm_shape(p.D, true), sizeof(E), 2, kBlocks, kMost, kLeast, besides);
   done = ring.stages > 0;
   if constexpr (kMost == 4)
     if (ring.rows == 4) return launch_back_ring<E, NB, V, 4, kWarps, kBlocks>(p, ring, st);

@@ -190,13 +190,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
   extern __shared__ __align__(128) char shared[];
   NormShared &sh = *reinterpret_cast<NormShared *>(shared);
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t slot = ring_slot(norm_columns(NB, p.warps), sizeof(E));
   start_ring<R>(shared, p.stages, p.warps);
   if (warp == p.warps) {
-    produce_rows<E, R, false>(p, shared, shared + kNormRows);
+    produce_rows<E, R, false>(p, shared, shared + kNormRows, slot);
     return;
   }
   constexpr uint32_t kSpan = 32 * kOct, kStep = 32 * V;
-  const uint32_t first = warp * NB * kSpan + lane * V, slot = ring_slot(p.D, sizeof(E));
+  const uint32_t first = warp * NB * kSpan + lane * V;
   const float share = 1.0f / (float)p.D;
   Ch<2> w[NB][kOct / 2], b[NB][kOct / 2];
 #pragma unroll
@@ -204,21 +205,20 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
     load_vector<E, V>(p.weight, p.floats, first + i * kSpan, kStep, p.D, 1.0f, w[i]);
     load_vector<E, V>(p.bias, p.floats, first + i * kSpan, kStep, p.D, 0.0f, b[i]);
   }
-  const bool all = warp * NB * kSpan + NB * kSpan <= p.D;  // no lane beyond the row
+  const bool all = (warp + 1) * NB * kSpan <= p.D;  // none of the warp's columns beyond the row
   bool lost = false;
   uint32_t stage = 0, turn = 0;
   for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
     if (!lost && !barrier_wait(&sh.full[stage], turn & 1)) lost = true;
-    const char *row[R];
+    const char *row[R];  // this lane's first columns
     bool there[R];
     float v[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t off =
-          Oct<E, V>::kBytes >= 16
-              ? 0
-              : (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
-                                                      (int64_t)(n0 + r) * p.x_row) & 15u;
+      uint32_t off = first * sizeof(E);
+      if constexpr (Oct<E, V>::kBytes < 16)
+        off += (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
+                                                     (int64_t)(n0 + r) * p.x_row) & 15u;
       row[r] = ring_row(shared + kNormRows, stage, 0, 1, R, r, slot) + off;
       there[r] = sh.head[stage][r].there;
       Ch<2> two = {0.0f, 0.0f};
@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
         for (int i = 0; i < NB; ++i) {
           Oct<E, V> x;
           Ch<2> f[kOct / 2];
-          ring_oct(x, row[r], first + i * kSpan, kStep, p.D);
+          ring_oct(x, row[r] + i * kSpan * sizeof(E));
+          if (!all) only(x, first + i * kSpan, p.D);
           widen(x, f);
 #pragma unroll
           for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
       }
       v[r] = two.v[0] + two.v[1];
     }
-    batch_sums<R>(v, sh.part[0], p.warps, warp, lane);
+    batch_sums<R, kWarps>(v, sh.part[0], p.warps, warp, lane);
     float mean[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -248,22 +249,22 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
           const uint32_t c = first + i * kSpan;
           Oct<E, V> x;
           Ch<2> f[kOct / 2];
-          ring_oct(x, row[r], c, kStep, p.D);
+          ring_oct(x, row[r] + i * kSpan * sizeof(E));
           widen(x, f);
 #pragma unroll
-          for (int j = 0; j < kOct / 2; ++j) {
-            Ch<2> d = f[j] + minus;
-            if (!all) {
-              if (!inside<V>(c, kStep, p.D, 2 * j)) d.v[0] = 0.0f;
-              if (!inside<V>(c, kStep, p.D, 2 * j + 1)) d.v[1] = 0.0f;
-            }
-            two = fma(d, d, two);
+          for (int j = 0; j < kOct / 2; ++j) f[j] = f[j] + minus;
+          if (!all) {
+#pragma unroll
+            for (int j = 0; j < kOct; ++j)
+              if (!inside<V>(c, kStep, p.D, j)) f[j / 2].v[j & 1] = 0.0f;
           }
+#pragma unroll
+          for (int j = 0; j < kOct / 2; ++j) two = fma(f[j], f[j], two);
         }
       }
       v[r] = two.v[0] + two.v[1];
     }
-    batch_sums<R>(v, sh.part[1], p.warps, warp, lane);
+    batch_sums<R, kWarps>(v, sh.part[1], p.warps, warp, lane);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint64_t n = n0 + r;
@@ -275,15 +276,19 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
       for (int i = 0; i < NB; ++i) {
         const uint32_t c = first + i * kSpan;
         Oct<E, V> x;
-        Ch<2> f[kOct / 2];
-        ring_oct(x, row[r], c, kStep, p.D);
-        widen(x, f);
+        clear(x);
+        if (there[r]) {
+          Ch<2> f[kOct / 2];
+          ring_oct(x, row[r] + i * kSpan * sizeof(E));
+          widen(x, f);
 #pragma unroll
-        for (int j = 0; j < kOct / 2; ++j) {
-          f[j] = fma((f[j] + minus) * scale, w[i][j], b[i][j]);
-          if (!there[r]) f[j] = {0.0f, 0.0f};
+          for (int j = 0; j < kOct / 2; ++j) f[j] = fma((f[j] + minus) * scale, w[i][j], b[i][j]);
+          x = narrow<E, V>(f);
         }
-        store_oct(y, c, kStep, p.D, narrow<E, V>(f));
+        if (all)
+          store_all(y + c, x);
+        else
+          store_oct(y, c, kStep, p.D, x);
       }
       if (threadIdx.x == 0) {
         if (p.mean) p.mean[n] = there[r] ? mean[r] : 0.0f;
@@ -371,7 +376,7 @@ cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
 template <class E, int NB, int V, int kWarps, int kBlocks>
 cudaError_t ring_of(NormParams &p, bool &done, cudaStream_t st) {
   constexpr uint32_t kMost = NB > 4 ? 2 : 4;
-  const NormRing ring = norm_ring(p.D, sizeof(E), 1, kBlocks, kMost, kMost / 2, 0);
+  const NormRing ring = norm_ring(norm_shape(p.D, false), sizeof(E), 1, kBlocks, kMost, kMost / 2, 0);
   done = ring.stages > 0;
   if (!done) return cudaSuccess;
   if (ring.rows == kMost) return launch_ring<E, NB, V, kMost, kWarps, kBlocks>(p, ring, st);

@@ -45,9 +45,9 @@ __device__ __forceinline__ void bulk_copy(void *smem, const void *gmem, uint32_t
       : "memory");
 }
 
-// Bytes of a row's place in the ring.
-__host__ __device__ __forceinline__ uint32_t ring_slot(uint32_t D, uint32_t es) {
-  return (D * es + 30) / 16 * 16;
+// Bytes of a row's place in the ring, for as many columns as its threads read.
+__host__ __device__ __forceinline__ uint32_t ring_slot(uint32_t columns, uint32_t es) {
+  return (columns * es + 30) / 16 * 16;
 }
 
 // The part of a row that the engine copies, from `lo` to `hi`.
@@ -76,18 +76,15 @@ __device__ __forceinline__ RingSpan ring_span(char *slot, const E *row, uint32_t
   return s;
 }
 
-// A lane's eight columns of a row in the ring (as load_oct).
+// A lane's eight columns of a row in the ring, pieces 32 V columns apart; what lies behind the
+// row is read too, and comes to nothing by `only`.
 template <class E, int V>
-__device__ __forceinline__ void ring_oct(Oct<E, V> &x, const char *row, uint32_t c, uint32_t step,
-                                         uint32_t D) {
+__device__ __forceinline__ void ring_oct(Oct<E, V> &x, const char *at) {
   using O = Oct<E, V>;
 #pragma unroll
   for (int i = 0; i < O::kPieces; ++i) {
     uint32_t *w = x.w + i * O::kWords;
-#pragma unroll
-    for (int j = 0; j < O::kWords; ++j) w[j] = 0;
-    if (c + i * step >= D) continue;
-    const char *p = row + (c + i * step) * sizeof(E);
+    const char *p = at + i * 32 * V * (int)sizeof(E);
     if constexpr (O::kBytes >= 16) {
 #pragma unroll
       for (int j = 0; j < O::kWords / 4; ++j) {
@@ -103,6 +100,25 @@ __device__ __forceinline__ void ring_oct(Oct<E, V> &x, const char *row, uint32_t
       w[0] = *reinterpret_cast<const uint16_t *>(p);
     }
   }
+}
+// Columns c, c + 32 V, ... of V each; those beyond D become 0.
+template <class E, int V>
+__device__ __forceinline__ void only(Oct<E, V> &x, uint32_t c, uint32_t D) {
+  using O = Oct<E, V>;
+#pragma unroll
+  for (int i = 0; i < O::kPieces; ++i)
+    if (c + i * 32 * V >= D) {
+#pragma unroll
+      for (int j = 0; j < O::kWords; ++j) x.w[i * O::kWords + j] = 0;
+    }
+}
+// The eight columns to a row of which all lanes' are there.
+template <class E, int V>
+__device__ __forceinline__ void store_all(E *at, const Oct<E, V> &x) {
+  using O = Oct<E, V>;
+#pragma unroll
+  for (int i = 0; i < O::kPieces; ++i)
+    store_piece<O::kBytes>(at + i * 32 * V, x.w + i * O::kWords);
 }
 
 }  // namespace nsk
