@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libnspack.so")
@@ -214,6 +215,31 @@ class ns_expert_sizes(_Sized):
     ]
 
 
+def _packer(layout: str, of):
+    """The bytes of a structure from its fields in order: as good an argument as the structure,
+    and made in a tenth of the time.  Sizes that 32 bits do not hold are refused."""
+    pack = struct.Struct(layout).pack
+    assert struct.calcsize(layout) == C.sizeof(of)
+
+    def packed(*fields) -> bytes:
+        try:
+            return pack(*fields)
+        except (struct.error, OverflowError) as e:
+            raise NsPackError(NS_ERR_INVALID_ARG, f"{of.__name__}{fields}: {e}") from None
+
+    return packed
+
+
+pack_embed = _packer("@PPIIIiiif4x", ns_embed_inputs)
+pack_norm = _packer("@PqPPPIIiif4x", ns_norm_inputs)
+pack_experts = _packer("@IIIIi", ns_expert_sizes)
+
+
+def _argument(inputs):
+    """A structure, or the bytes of one, as an argument."""
+    return inputs if type(inputs) is bytes else C.byref(inputs)
+
+
 # Every symbol the headers declare, for the load check.
 SYMBOLS = ("ns_pack_init", "ns_pack_step", "ns_pack_fingerprint", "ns_pack_batch_fp",
            "ns_pack_step_learned", "ns_pack_info", "ns_pack_stream_windows",
@@ -276,8 +302,7 @@ def _load() -> C.CDLL:
     L.ns_route_forward.argtypes = [route, vp, vp, vp, vp, vp, vp, vp]
     L.ns_route_backward.restype = i32
     L.ns_route_backward.argtypes = [route, vp, vp, vp, vp, vp, vp, vp, vp]
-    embed, norm, experts = (C.POINTER(t) for t in
-                            (ns_embed_inputs, ns_norm_inputs, ns_expert_sizes))
+    embed = norm = experts = vp  # structures or their bytes
     L.ns_embed_forward.restype = i32
     L.ns_embed_forward.argtypes = [embed, vp, i64, vp, vp]
     L.ns_embed_workspace.restype = u64
@@ -440,8 +465,8 @@ def ns_route_backward(inputs: ns_route_inputs, ids, weights, counts, tokens, d_w
                                 dlogits, stream), "ns_route_backward")
 
 
-def ns_embed_forward(inputs: ns_embed_inputs, table, table_row: int, y, stream) -> None:
-    check(lib.ns_embed_forward(C.byref(inputs), table, table_row, y, stream), "ns_embed_forward")
+def ns_embed_forward(inputs, table, table_row: int, y, stream) -> None:
+    check(lib.ns_embed_forward(_argument(inputs), table, table_row, y, stream), "ns_embed_forward")
 
 
 def ns_embed_workspace(N: int, V: int, D: int) -> int:
@@ -449,13 +474,13 @@ def ns_embed_workspace(N: int, V: int, D: int) -> int:
     return lib.ns_embed_workspace(N, V, D)
 
 
-def ns_embed_backward(inputs: ns_embed_inputs, dy, dy_row: int, dtable, workspace, stream) -> None:
-    check(lib.ns_embed_backward(C.byref(inputs), dy, dy_row, dtable, workspace, stream),
+def ns_embed_backward(inputs, dy, dy_row: int, dtable, workspace, stream) -> None:
+    check(lib.ns_embed_backward(_argument(inputs), dy, dy_row, dtable, workspace, stream),
           "ns_embed_backward")
 
 
-def ns_norm_forward(inputs: ns_norm_inputs, y, mean, rstd, stream) -> None:
-    check(lib.ns_norm_forward(C.byref(inputs), y, mean, rstd, stream), "ns_norm_forward")
+def ns_norm_forward(inputs, y, mean, rstd, stream) -> None:
+    check(lib.ns_norm_forward(_argument(inputs), y, mean, rstd, stream), "ns_norm_forward")
 
 
 def ns_norm_workspace(N: int, D: int) -> int:
@@ -463,9 +488,9 @@ def ns_norm_workspace(N: int, D: int) -> int:
     return lib.ns_norm_workspace(N, D)
 
 
-def ns_norm_backward(inputs: ns_norm_inputs, mean, rstd, dy, dy_row: int, dx, dweight, dbias,
+def ns_norm_backward(inputs, mean, rstd, dy, dy_row: int, dx, dweight, dbias,
                      workspace, stream) -> None:
-    check(lib.ns_norm_backward(C.byref(inputs), mean, rstd, dy, dy_row, dx, dweight, dbias,
+    check(lib.ns_norm_backward(_argument(inputs), mean, rstd, dy, dy_row, dx, dweight, dbias,
                                workspace, stream), "ns_norm_backward")
 
 
@@ -474,19 +499,19 @@ def ns_dispatch_workspace(N: int, k: int, E: int) -> int:
     return lib.ns_dispatch_workspace(N, k, E)
 
 
-def ns_dispatch(sizes: ns_expert_sizes, ids, x, x_row: int, place, slots, offsets, rows, workspace,
+def ns_dispatch(sizes, ids, x, x_row: int, place, slots, offsets, rows, workspace,
                 stream) -> None:
-    check(lib.ns_dispatch(C.byref(sizes), ids, x, x_row, place, slots, offsets, rows, workspace,
+    check(lib.ns_dispatch(_argument(sizes), ids, x, x_row, place, slots, offsets, rows, workspace,
                           stream), "ns_dispatch")
 
 
-def ns_combine(sizes: ns_expert_sizes, place, offsets, weights, rows, rows_row: int, out,
+def ns_combine(sizes, place, offsets, weights, rows, rows_row: int, out,
                stream) -> None:
-    check(lib.ns_combine(C.byref(sizes), place, offsets, weights, rows, rows_row, out, stream),
+    check(lib.ns_combine(_argument(sizes), place, offsets, weights, rows, rows_row, out, stream),
           "ns_combine")
 
 
-def ns_combine_backward(sizes: ns_expert_sizes, place, offsets, weights, rows, rows_row: int, d_out,
+def ns_combine_backward(sizes, place, offsets, weights, rows, rows_row: int, d_out,
                         d_out_row: int, d_rows, d_weights, stream) -> None:
-    check(lib.ns_combine_backward(C.byref(sizes), place, offsets, weights, rows, rows_row, d_out,
+    check(lib.ns_combine_backward(_argument(sizes), place, offsets, weights, rows, rows_row, d_out,
                                   d_out_row, d_rows, d_weights, stream), "ns_combine_backward")

@@ -18,16 +18,17 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib as L
-from .operators import (_DTYPES, _elsewhere, _floats, _optional, _reverse_only, _shape, _stream,
+from .operators import (_DTYPES, _floats, _optional, _reverse_only, _shape, _stream,
                         _wants_grad)
 from .packer import _refuse
 
 
 def _row_step(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a [..., D] tensor, taken as rows in their order."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if t.is_contiguous():
         return shape[-1]
+    stride = t.stride()
     if shape[-1] > 1 and stride[-1] != 1:
         _refuse(f"{name}: strides {stride}, the last dimension has to be contiguous")
     step = None  # of the rows, from the last dimension with more than one on
@@ -54,16 +55,22 @@ def _even(t: torch.Tensor) -> torch.Tensor:
 
 
 # ---- rows of a table -----------------------------------------------------------------
-def _embed_inputs(tokens, V, D, table_code, code, scale, doc) -> L.ns_embed_inputs:
-    if not isinstance(tokens, torch.Tensor) or tokens.dtype not in (torch.int32, torch.int64):
-        _refuse("tokens: expected a tensor of int32 or int64")
-    scale = float(scale)
+def _embed_inputs(tokens, V, D, table_code, code, scale, doc) -> bytes:
+    dtype = tokens.dtype
+    if dtype != torch.int32 and dtype != torch.int64:
+        _refuse(f"tokens: dtype {dtype}, expected int32 or int64")
+    if not tokens.is_contiguous():
+        _refuse("tokens: not contiguous")
     if not math.isfinite(scale):
         _refuse(f"scale: {scale}, expected a finite number")
-    return L.ns_embed_inputs(
-        _optional(tokens, "tokens", tokens.dtype, tokens.shape, tokens.device),
-        _optional(doc, "doc", torch.int32, tokens.shape, tokens.device), tokens.numel(), V, D,
-        table_code, code, 1 if tokens.dtype == torch.int64 else 0, scale)
+    if doc is not None:
+        doc = _optional(doc, "doc", torch.int32, tokens.shape, tokens.device)
+    return L.pack_embed(tokens.data_ptr(), doc or 0, tokens.numel(), V, D, table_code, code,
+                        dtype == torch.int64, scale)
+
+
+# Its number; torch.cuda.current_device takes twice as long.
+_current_device = torch._C._cuda_getDevice
 
 
 def _code(dtype, name: str) -> int:
@@ -74,22 +81,25 @@ def _code(dtype, name: str) -> int:
 
 def _embed(weight, tokens, scale, doc, dtype):
     code = _floats(weight, "weight")
-    if weight.dim() != 2:
-        _refuse(f"weight: shape {tuple(weight.shape)}, expected [V, D]")
-    if not isinstance(tokens, torch.Tensor) or tokens.device != weight.device:
+    shape = weight.shape
+    if len(shape) != 2:
+        _refuse(f"weight: shape {tuple(shape)}, expected [V, D]")
+    device = weight.device
+    if not isinstance(tokens, torch.Tensor) or tokens.device != device:
         _refuse("tokens: expected a tensor on the weight's device")
-    if _elsewhere(weight):
-        with torch.cuda.device(weight.device):
+    index = device.index
+    if index != _current_device():
+        with torch.cuda.device(device):
             return _embed(weight, tokens, scale, doc, dtype)
-    V, D = weight.shape
+    V, D = shape
     if dtype is None:
         dtype, out_code = weight.dtype, code
     else:
         out_code = _code(dtype, "dtype")
     inputs = _embed_inputs(tokens, V, D, code, out_code, scale, doc)
-    step = _row_step(weight, "weight")
-    y = torch.empty((*tokens.shape, D), dtype=dtype, device=weight.device)
-    L.ns_embed_forward(inputs, weight.data_ptr(), step, y.data_ptr(), _stream(weight.device.index))
+    y = torch.empty((*tokens.shape, D), dtype=dtype, device=device)
+    L.ns_embed_forward(inputs, weight.data_ptr(), _row_step(weight, "weight"), y.data_ptr(),
+                       _stream(index))
     return y
 
 
@@ -101,10 +111,11 @@ def embed_backward(dy: torch.Tensor, tokens: torch.Tensor, vocab: int, *, scale:
     code = _floats(dy, "dy")
     if not isinstance(vocab, int) or vocab < 0 or vocab >= 1 << 31:
         _refuse(f"vocab: {vocab!r}, expected a number of tokens below 2**31")
-    if not isinstance(tokens, torch.Tensor) or tokens.device != dy.device:
+    device = dy.device
+    if not isinstance(tokens, torch.Tensor) or tokens.device != device:
         _refuse("tokens: expected a tensor on dy's device")
-    if _elsewhere(dy):
-        with torch.cuda.device(dy.device):
+    if device.index != _current_device():
+        with torch.cuda.device(device):
             return embed_backward(dy, tokens, vocab, scale=scale, doc=doc, dtype=dtype)
     if dy.dim() < 1 or dy.shape[:-1] != tokens.shape:
         _refuse(f"dy: shape {tuple(dy.shape)}, expected {(*tokens.shape, 'D')}")
@@ -115,9 +126,9 @@ def embed_backward(dy: torch.Tensor, tokens: torch.Tensor, vocab: int, *, scale:
         out_code = _code(dtype, "dtype")
     inputs = _embed_inputs(tokens, vocab, D, out_code, code, scale, doc)
     step = _row_step(dy, "dy")
-    device = dy.device
     dweight = torch.empty((vocab, D), dtype=dtype, device=device)
-    work = torch.empty(L.ns_embed_workspace(inputs.N, vocab, D), dtype=torch.uint8, device=device)
+    work = torch.empty(L.ns_embed_workspace(tokens.numel(), vocab, D), dtype=torch.uint8,
+                       device=device)
     L.ns_embed_backward(inputs, dy.data_ptr(), step, dweight.data_ptr(), work.data_ptr(),
                         _stream(device.index))
     return dweight
@@ -161,42 +172,45 @@ def embed(weight: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
 
 
 # ---- layer norm ------------------------------------------------------------------------
-def _norm_inputs(x, weight, bias, eps, doc) -> L.ns_norm_inputs:
+def _norm_inputs(x, weight, bias, eps, doc) -> bytes:
     code = _floats(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        _refuse(f"x: shape {tuple(x.shape)}, expected [..., D]")
     shape, device = x.shape, x.device
-    D = shape[-1]
+    D = shape[-1] if shape else 0
+    if D < 1:
+        _refuse(f"x: shape {tuple(shape)}, expected [..., D]")
     given = weight if weight is not None else bias
-    weight_code = code
+    weight_code, weight_ptr, bias_ptr, doc_ptr = code, 0, 0, 0
     if given is not None:
         weight_code = _floats(given, "weight" if weight is not None else "bias")
         if weight_code != L.NS_F32 and weight_code != code:
             _refuse(f"weight, bias: dtype {given.dtype}, expected float32 or {x.dtype}")
-    eps = float(eps)
+        if weight is not None:
+            weight_ptr = _optional(weight, "weight", given.dtype, (D,), device)
+        if bias is not None:
+            bias_ptr = _optional(bias, "bias", given.dtype, (D,), device)
+    if doc is not None:
+        doc_ptr = _optional(doc, "doc", torch.int32, shape[:-1], device)
     if not (eps >= 0.0 and math.isfinite(eps)):
         _refuse(f"eps: {eps}, expected 0 or a positive number")
-    return L.ns_norm_inputs(
-        x.data_ptr(), _row_step(x, "x"),
-        _optional(weight, "weight", None if given is None else given.dtype, (D,), device),
-        _optional(bias, "bias", None if given is None else given.dtype, (D,), device),
-        _optional(doc, "doc", torch.int32, shape[:-1], device),
-        x.numel() // D, D, code, weight_code, eps)
+    return L.pack_norm(x.data_ptr(), _row_step(x, "x"), weight_ptr, bias_ptr, doc_ptr,
+                       x.numel() // D, D, code, weight_code, eps)
 
 
 def _norm(x, weight, bias, eps, doc, keep: bool):
     inputs = _norm_inputs(x, weight, bias, eps, doc)
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
+    device = x.device
+    index = device.index
+    if index != _current_device():
+        with torch.cuda.device(device):
             return _norm(x, weight, bias, eps, doc, keep)
-    shape, device = x.shape, x.device
+    shape = x.shape
     y = torch.empty(shape, dtype=x.dtype, device=device)
-    mean = rstd = None
-    if keep:
-        mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-    L.ns_norm_forward(inputs, y.data_ptr(), mean.data_ptr() if keep else None,
-                      rstd.data_ptr() if keep else None, _stream(device.index))
+    if not keep:
+        L.ns_norm_forward(inputs, y.data_ptr(), None, None, _stream(index))
+        return y, None, None
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    L.ns_norm_forward(inputs, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream(index))
     return y, mean, rstd
 
 
@@ -215,10 +229,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     distances), with the forward pass's inputs and what it returned; dweight and dbias
     are None where ``weight`` and ``bias`` are."""
     inputs = _norm_inputs(x, weight, bias, 0.0, doc)
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
-            return layer_norm_backward(dy, x, weight, bias, mean, rstd, doc=doc)
     shape, device = x.shape, x.device
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return layer_norm_backward(dy, x, weight, bias, mean, rstd, doc=doc)
     if not isinstance(dy, torch.Tensor) or dy.dtype != x.dtype or dy.device != device:
         _refuse("dy: expected a tensor of x's dtype on x's device")
     _shape(dy, "dy", shape)
@@ -233,7 +247,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     if bias is not None:
         dbias = torch.empty(shape[-1], dtype=bias.dtype, device=device)
     if dweight is not None or dbias is not None:
-        work = torch.empty(L.ns_norm_workspace(inputs.N, inputs.D) // 4, dtype=torch.float32,
+        D = shape[-1]
+        work = torch.empty(L.ns_norm_workspace(x.numel() // D, D) // 4, dtype=torch.float32,
                            device=device)
     L.ns_norm_backward(inputs, mean_ptr, rstd_ptr, dy.data_ptr(), _row_step(dy, "dy"),
                        dx.data_ptr(), None if dweight is None else dweight.data_ptr(),
@@ -287,19 +302,21 @@ class ExpertOrder(NamedTuple):
 
 def _dispatch(x, ids, experts):
     code = _floats(x, "x")
-    if x.dim() != 2:
-        _refuse(f"x: shape {tuple(x.shape)}, expected [N, D]")
+    shape = x.shape
+    if len(shape) != 2:
+        _refuse(f"x: shape {tuple(shape)}, expected [N, D]")
     if not isinstance(experts, int) or experts < 1:
         _refuse(f"experts: {experts!r}, expected a positive integer")
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
-            return _dispatch(x, ids, experts)
-    N, D = x.shape
     device = x.device
+    index = device.index
+    if index != _current_device():
+        with torch.cuda.device(device):
+            return _dispatch(x, ids, experts)
+    N, D = shape
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         _refuse("ids: expected a tensor [N, k]")
     k = ids.shape[1]
-    sizes = L.ns_expert_sizes(N, k, experts, D, code)
+    sizes = L.pack_experts(N, k, experts, D, code)
     ids_ptr = _optional(ids, "ids", torch.int32, (N, k), device)
     step = _row_step(x, "x")
     place = torch.empty((N, k), dtype=torch.int32, device=device)
@@ -310,7 +327,7 @@ def _dispatch(x, ids, experts):
     work = torch.empty(size // 4, dtype=torch.int32, device=device) if size else None
     L.ns_dispatch(sizes, ids_ptr, x.data_ptr(), step, place.data_ptr(), slots.data_ptr(),
                   offsets.data_ptr(), rows.data_ptr(), work.data_ptr() if size else None,
-                  _stream(device.index))
+                  _stream(index))
     return rows, ExpertOrder(place, slots, offsets)
 
 
@@ -326,23 +343,25 @@ def _order(order, rows, name: str):
         _refuse("order.offsets: expected [E + 1]")
     N, k = place.shape
     E = offsets.shape[0] - 1
-    if rows.dim() != 2 or rows.shape[0] != N * k:
-        _refuse(f"{name}: shape {tuple(rows.shape)}, expected [{N * k}, D]")
-    return (code, N, k, E, _optional(place, "order.place", torch.int32, (N, k), rows.device),
-            _optional(offsets, "order.offsets", torch.int32, (E + 1,), rows.device))
+    shape, device = rows.shape, rows.device
+    if len(shape) != 2 or shape[0] != N * k:
+        _refuse(f"{name}: shape {tuple(shape)}, expected [{N * k}, D]")
+    return (code, N, k, E, _optional(place, "order.place", torch.int32, (N, k), device),
+            _optional(offsets, "order.offsets", torch.int32, (E + 1,), device))
 
 
 def _combine(rows, order, weights):
     code, N, k, E, place, offsets = _order(order, rows, "rows")
-    if _elsewhere(rows):
-        with torch.cuda.device(rows.device):
-            return _combine(rows, order, weights)
     D, device = rows.shape[1], rows.device
-    sizes = L.ns_expert_sizes(N, k, E, D, code)
+    index = device.index
+    if index != _current_device():
+        with torch.cuda.device(device):
+            return _combine(rows, order, weights)
+    if weights is not None:
+        weights = _optional(weights, "weights", torch.float32, (N, k), device)
     out = torch.empty((N, D), dtype=rows.dtype, device=device)
-    L.ns_combine(sizes, place, offsets,
-                 _optional(weights, "weights", torch.float32, (N, k), device), rows.data_ptr(),
-                 _row_step(rows, "rows"), out.data_ptr(), _stream(device.index))
+    L.ns_combine(L.pack_experts(N, k, E, D, code), place, offsets, weights, rows.data_ptr(),
+                 _row_step(rows, "rows"), out.data_ptr(), _stream(index))
     return out
 
 
@@ -357,14 +376,14 @@ def combine_backward(d_out: torch.Tensor, rows: torch.Tensor, order: ExpertOrder
     """Gradients (d_rows, d_weights) of ``combine`` from that of its output [N, D], with
     its inputs; d_weights is None where ``weights`` is."""
     code, N, k, E, place, offsets = _order(order, rows, "rows")
-    if _elsewhere(rows):
-        with torch.cuda.device(rows.device):
-            return combine_backward(d_out, rows, order, weights)
     D, device = rows.shape[1], rows.device
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return combine_backward(d_out, rows, order, weights)
     if not isinstance(d_out, torch.Tensor) or d_out.dtype != rows.dtype or d_out.device != device:
         _refuse("d_out: expected a tensor of the rows' dtype on their device")
     _shape(d_out, "d_out", (N, D))
-    sizes = L.ns_expert_sizes(N, k, E, D, code)
+    sizes = L.pack_experts(N, k, E, D, code)
     weights_ptr = _optional(weights, "weights", torch.float32, (N, k), device)
     d_rows = torch.empty((N * k, D), dtype=rows.dtype, device=device)
     d_weights = None
