@@ -62,32 +62,35 @@ struct EmbedParams {
 // ---- forward ------------------------------------------------------------------------
 // U spans of a position's row a unit: short blocks, whose stores drain while others begin
 // (blocks that stay, with the next token under way: 32768 x 2560 bf16 47 us in place of 40).
-template <class W, class E, int V, int U>
+template <class W, class E, int V, int U, bool kWarp>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
-  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
+  const uint32_t lanes = kWarp ? 32 : p.lanes, span = lanes * kOct, step = lanes * V;
+  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
   if (n >= p.N) return;
   const int64_t t = p.wide ? static_cast<const int64_t *>(p.tokens)[n]
                            : static_cast<const int32_t *>(p.tokens)[n];
   const bool there = t >= 0 && t < (int64_t)p.V && !(p.doc && p.doc[n] < 0);
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint32_t first = slice * U * span + threadIdx.x % p.lanes * V;
+  const uint32_t from = slice * U * span, first = from + threadIdx.x % lanes * V;
   const W *row = static_cast<const W *>(p.table) + (there ? t : 0) * p.table_row;
   E *y = static_cast<E *>(p.y) + (int64_t)n * p.D;
-  Oct<W, V> v[U];
+  by_all<V, kWarp>(from + U * span, p.D, [&](auto all) {
+    constexpr bool kAll = decltype(all)::value;
+    Oct<W, V> v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    clear(v[u]);
-    if (there) load_oct(v[u], row, first + u * span, step, p.D);
-  }
+    for (int u = 0; u < U; ++u) {
+      if (!kAll || !there) clear(v[u]);
+      if (there) load_oct<kAll>(v[u], row, first + u * span, step, p.D);
+    }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    Ch<2> x[kOct / 2];
-    widen(v[u], x);
+    for (int u = 0; u < U; ++u) {
+      Ch<2> x[kOct / 2];
+      widen(v[u], x);
 #pragma unroll
-    for (int i = 0; i < kOct / 2; ++i) x[i] = x[i] * splat<2>(there ? p.scale : 0.0f);
-    store_oct(y, first + u * span, step, p.D, narrow<E, V>(x));
-  }
+      for (int i = 0; i < kOct / 2; ++i) x[i] = x[i] * splat<2>(there ? p.scale : 0.0f);
+      store_oct<kAll>(y, first + u * span, step, p.D, narrow<E, V>(x));
+    }
+  });
 }
 
 // ---- backward --------------------------------------------------------------------------
@@ -293,8 +296,8 @@ cudaError_t forward_by(EmbedParams &p, cudaStream_t st) {
   p.slices = (uint32_t)((spans_for(p.D, p.lanes) + U - 1) / U);
   const uint64_t each = kThreads / p.lanes, blocks = ((uint64_t)p.N * p.slices + each - 1) / each;
   ++launch_counter();
-  embed_kernel<W, E, V, U>
-      <<<(uint32_t)blocks, kThreads, 0, st>>>(p);
+  auto *k = p.lanes == 32 ? embed_kernel<W, E, V, U, true> : embed_kernel<W, E, V, U, false>;
+  k<<<(uint32_t)blocks, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 template <class W, class E, int V>

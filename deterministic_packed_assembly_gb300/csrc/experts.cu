@@ -55,17 +55,18 @@ struct ExpertParams {
 template <class E, int V>
 constexpr int kUnderWay = Oct<E, V>::kPieces * Oct<E, V>::kWords == 4 ? 8 : 4;
 
-// Blocks an SM: as many as have the registers for it.
+// Blocks an SM: as many as have the registers for it (32768 x 2560 bf16, k = 8, backward: two
+// 487 us, three 414).
 template <class E, int V>
-constexpr int kBackBlocks = kUnderWay<E, V> == 8 ? 3 : 2;
+constexpr int kBackBlocks = V == kOct && kUnderWay<E, V> == 8 ? 3 : 2;
 constexpr int kCombineBlocks = 2;
 
 // ---- dispatch --------------------------------------------------------------------
-// U spans of token n's row, from `first` on, into the places of its choices.
-template <class E, int V, int U>
+// U spans of token n's row, from column `first` on, into the places of its choices.
+template <bool kAll, class E, int V, int U>
 __device__ __forceinline__ void copy_slice(const ExpertParams &p, const Oct<E, V> (&v)[U],
-                                           uint32_t first, const int32_t *place, uint32_t M) {
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
+                                           uint32_t first, uint32_t lanes, const int32_t *place,
+                                           uint32_t M) {
   E *to = static_cast<E *>(p.to);
   Oct<E, V> zero;
   clear(zero);
@@ -75,31 +76,35 @@ __device__ __forceinline__ void copy_slice(const ExpertParams &p, const Oct<E, V
     E *row = to + (int64_t)at * p.D;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      store_oct(row, first + u * span, step, p.D, at < M ? v[u] : zero);
+      store_oct<kAll>(row, first + u * lanes * kOct, lanes * V, p.D, at < M ? v[u] : zero);
   }
 }
-template <class E, int V, int U>
+template <bool kAll, class E, int V, int U>
 __device__ __forceinline__ void load_slice(const ExpertParams &p, Oct<E, V> (&v)[U], uint32_t n,
-                                           uint32_t first) {
+                                           uint32_t first, uint32_t lanes) {
   const E *x = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    load_oct(v[u], x, first + u * p.lanes * kOct, p.lanes * V, p.D);
+    load_oct<kAll>(v[u], x, first + u * lanes * kOct, lanes * V, p.D);
 }
 
 // A slice of a token a unit: short blocks, whose stores drain while others begin (blocks that
 // stay, with the next row under way: 32768 x 2560 bf16, k = 8: 279 us in place of 236).  Its row
 // is read before the sort has ended: x was there when the sort's first kernel began.
-template <class E, int V, int U>
+template <class E, int V, int U, bool kWarp>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const ExpertParams p) {
-  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
+  const uint32_t lanes = kWarp ? 32 : p.lanes;
+  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
   const uint32_t n = (uint32_t)(unit / p.slices), slice = (uint32_t)(unit % p.slices);
-  const uint32_t first = slice * U * p.lanes * kOct + threadIdx.x % p.lanes * V;
-  Oct<E, V> v[U];
-  if (n < p.N) load_slice<E, V, U>(p, v, n, first);
-  pdl_wait();
-  if (n < p.N)
-    copy_slice<E, V, U>(p, v, first, p.place + (uint64_t)n * p.k, (uint32_t)p.offsets[p.E]);
+  const uint32_t from = slice * U * lanes * kOct, first = from + threadIdx.x % lanes * V;
+  by_all<V, kWarp>(from + U * lanes * kOct, p.D, [&](auto all) {
+    constexpr bool kAll = decltype(all)::value;
+    Oct<E, V> v[U];
+    if (n < p.N) load_slice<kAll>(p, v, n, first, lanes);
+    pdl_wait();
+    if (n < p.N)
+      copy_slice<kAll>(p, v, first, lanes, p.place + (uint64_t)n * p.k, (uint32_t)p.offsets[p.E]);
+  });
 }
 
 // Few choices: a block a token finds its places by counting the keys below and before
@@ -160,8 +165,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const ExpertPara
   for (uint32_t unit = threadIdx.x / p.lanes; unit < p.slices; unit += kThreads / p.lanes) {
     const uint32_t first = unit * U * p.lanes * kOct + threadIdx.x % p.lanes * V;
     Oct<E, V> v[U];
-    load_slice<E, V, U>(p, v, n, first);
-    copy_slice<E, V, U>(p, v, first, reinterpret_cast<const int32_t *>(count), M);
+    load_slice<false>(p, v, n, first, p.lanes);
+    copy_slice<false>(p, v, first, p.lanes, reinterpret_cast<const int32_t *>(count), M);
   }
 }
 
@@ -185,14 +190,14 @@ __device__ __forceinline__ void load_chosen(Chosen<R> &c, const ExpertParams &p,
 
 // Units of a slice of a token each, one after the other; R choices' rows and U spans of them are
 // under way (what hides memory's latency is R U), and the next unit's choices.
-template <class E, int V, int R, int U>
+template <class E, int V, int R, int U, bool kWarp>
 __global__ void __launch_bounds__(kThreads, kCombineBlocks) combine_kernel(const ExpertParams p) {
   const uint32_t M = min((uint32_t)p.offsets[p.E], p.N * p.k);
   const E *from = static_cast<const E *>(p.from);
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint64_t every = (uint64_t)gridDim.x * kThreads / p.lanes;
+  const uint32_t lanes = kWarp ? 32 : p.lanes, span = lanes * kOct, step = lanes * V;
+  const uint64_t every = (uint64_t)gridDim.x * kThreads / lanes;
   const uint64_t units = (uint64_t)p.N * p.slices;
-  uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / p.lanes;
+  uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
   Chosen<R> now, next;
   if (unit < units) load_chosen(now, p, (uint32_t)(unit / p.slices), 0, M);
   for (; unit < units; unit += every) {
@@ -202,38 +207,42 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks) combine_kernel(const
     E *out = static_cast<E *>(p.to) + (int64_t)n * p.D;
     const uint32_t end = min(p.spans, (slice + 1) * p.each);
     for (uint32_t s = slice * p.each; s < end; s += U) {
-      const uint32_t first = s * span + threadIdx.x % p.lanes * V;
-      Ch<2> acc[U][kOct / 2];
+      const uint32_t first = s * span + threadIdx.x % lanes * V;
+      by_all<V, kWarp>((s + U) * span, p.D, [&](auto all) {
+        constexpr bool kAll = decltype(all)::value;
+        Ch<2> acc[U][kOct / 2];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < kOct / 2; ++i) acc[u][i] = {0.0f, 0.0f};
-      for (uint32_t j0 = 0; j0 < p.k; j0 += R) {
-        if (p.k > R) load_chosen(now, p, n, j0, M);
-        Oct<E, V> v[R][U];
+          for (int i = 0; i < kOct / 2; ++i) acc[u][i] = {0.0f, 0.0f};
+        for (uint32_t j0 = 0; j0 < p.k; j0 += R) {
+          if (p.k > R) load_chosen(now, p, n, j0, M);
+          Oct<E, V> v[R][U];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+          for (int r = 0; r < R; ++r)
+            if (now.at[r] < M) {
+              const E *row = from + (int64_t)now.at[r] * p.from_row;
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (now.at[r] < M)
-              load_oct(v[r][u], from + (int64_t)now.at[r] * p.from_row, first + u * span, step,
-                       p.D);
+              for (int u = 0; u < U; ++u) load_oct<kAll>(v[r][u], row, first + u * span, step, p.D);
+            }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (now.at[r] >= M) continue;
+          for (int r = 0; r < R; ++r) {
+            if (now.at[r] >= M) continue;
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            Ch<2> x[kOct / 2];
-            widen(v[r][u], x);
+            for (int u = 0; u < U; ++u) {
+              Ch<2> x[kOct / 2];
+              widen(v[r][u], x);
 #pragma unroll
-            for (int i = 0; i < kOct / 2; ++i)
-              acc[u][i] = fma(splat<2>(now.w[r]), x[i], acc[u][i]);
+              for (int i = 0; i < kOct / 2; ++i)
+                acc[u][i] = fma(splat<2>(now.w[r]), x[i], acc[u][i]);
+            }
           }
         }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u < end) store_oct(out, first + u * span, step, p.D, narrow<E, V>(acc[u]));
+        for (int u = 0; u < U; ++u)
+          if (kAll || s + u < end)
+            store_oct<kAll>(out, first + u * span, step, p.D, narrow<E, V>(acc[u]));
+      });
     }
     now = next;
   }
@@ -242,72 +251,79 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks) combine_kernel(const
 // ---- combine's backward pass -----------------------------------------------------------
 // L lanes a choice, T choices at once: neighbouring units are a token's, whose row stays in
 // the L1 cache.  T U spans of both rows are under way, and the next choices' places.
-template <class E, int V, int T, int U>
+template <class E, int V, int T, int U, bool kWarp>
 __global__ void __launch_bounds__(kThreads, (kBackBlocks<E, V>))
     combine_backward_kernel(const ExpertParams p) {
-  const uint32_t S = p.N * p.k, lane = threadIdx.x % p.lanes, groups = kThreads / p.lanes;
+  const uint32_t lanes = kWarp ? 32 : p.lanes, span = lanes * kOct, step = lanes * V;
+  const uint32_t S = p.N * p.k, lane = threadIdx.x % lanes, groups = kThreads / lanes;
   const uint32_t M = min((uint32_t)p.offsets[p.E], S);
-  const uint32_t span = p.lanes * kOct, step = p.lanes * V;
-  const uint64_t every = (uint64_t)gridDim.x * groups * T;
-  const uint64_t base = (uint64_t)blockIdx.x * groups * T;  // of the block
+  const uint32_t every = gridDim.x * groups * T;
   Chosen<T> now, next;
   const auto look = [&](Chosen<T> &c, uint64_t b) {
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      const uint64_t s = b + t * groups + threadIdx.x / p.lanes;
+      const uint64_t s = b + t * groups + threadIdx.x / lanes;
       c.at[t] = s < S ? (uint32_t)p.place[s] : S;
       c.w[t] = s < S && p.weights ? p.weights[s] : 1.0f;
     }
   };
+  const uint64_t base = (uint64_t)blockIdx.x * groups * T;  // of the block
   look(now, base);
   // all lanes stay: they add up together
   for (uint64_t b = base; b < S; b += every) {
     look(next, b + every);
+    const E *d_out[T];
     Ch<2> dot[T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) dot[t] = {0.0f, 0.0f};
-    for (uint32_t c = lane * V; c < p.D; c += U * span) {
-      Oct<E, V> a[T][U], y[T][U];
+    for (int t = 0; t < T; ++t) {
+      const uint64_t s = b + t * groups + threadIdx.x / lanes;
+      d_out[t] = static_cast<const E *>(p.x) + (int64_t)((uint32_t)(s < S ? s : 0) / p.k) * p.x_row;
+      dot[t] = {0.0f, 0.0f};
+    }
+    for (uint32_t c0 = 0; c0 < p.D; c0 += U * span) {
+      const uint32_t c = c0 + lane * V;
+      by_all<V, kWarp>(c0 + U * span, p.D, [&](auto all) {
+        constexpr bool kAll = decltype(all)::value;
+        Oct<E, V> a[T][U], y[T][U];
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const uint64_t s = b + t * groups + threadIdx.x / p.lanes;
-        const uint32_t n = (uint32_t)(s < S ? s : 0) / p.k;
-        const E *d_out = static_cast<const E *>(p.x) + (int64_t)n * p.x_row;
-        const E *from = static_cast<const E *>(p.from) + (int64_t)now.at[t] * p.from_row;
+        for (int t = 0; t < T; ++t) {
+          const E *from = static_cast<const E *>(p.from) + (int64_t)now.at[t] * p.from_row;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          clear(a[t][u]), clear(y[t][u]);
-          if (now.at[t] < M) {
-            load_oct(a[t][u], d_out, c + u * span, step, p.D);
-            if (p.d_weights) load_oct(y[t][u], from, c + u * span, step, p.D);
+          for (int u = 0; u < U; ++u) {
+            if (!kAll || now.at[t] >= M) clear(a[t][u]);
+            if (!kAll || now.at[t] >= M || !p.d_weights) clear(y[t][u]);
+            if (now.at[t] < M) {
+              load_oct<kAll>(a[t][u], d_out[t], c + u * span, step, p.D);
+              if (p.d_weights) load_oct<kAll>(y[t][u], from, c + u * span, step, p.D);
+            }
           }
         }
-      }
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        if (now.at[t] >= S) continue;
-        E *to = static_cast<E *>(p.to) + (int64_t)now.at[t] * p.D;
-        const Ch<2> w = splat<2>(now.at[t] < M ? now.w[t] : 1.0f);
+        for (int t = 0; t < T; ++t) {
+          if (now.at[t] >= S) continue;
+          E *to = static_cast<E *>(p.to) + (int64_t)now.at[t] * p.D;
+          const Ch<2> w = splat<2>(now.at[t] < M ? now.w[t] : 1.0f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          Ch<2> d[kOct / 2], x[kOct / 2];
-          widen(a[t][u], d);
-          widen(y[t][u], x);
+          for (int u = 0; u < U; ++u) {
+            Ch<2> d[kOct / 2], x[kOct / 2];
+            widen(a[t][u], d);
+            widen(y[t][u], x);
 #pragma unroll
-          for (int i = 0; i < kOct / 2; ++i) {
-            dot[t] = fma(d[i], x[i], dot[t]);
-            d[i] = d[i] * w;
+            for (int i = 0; i < kOct / 2; ++i) {
+              dot[t] = fma(d[i], x[i], dot[t]);
+              d[i] = d[i] * w;
+            }
+            store_oct<kAll>(to, c + u * span, step, p.D, narrow<E, V>(d));
           }
-          store_oct(to, c + u * span, step, p.D, narrow<E, V>(d));
         }
-      }
+      });
     }
     if (p.d_weights) {
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const uint64_t s = b + t * groups + threadIdx.x / p.lanes;
+        const uint64_t s = b + t * groups + threadIdx.x / lanes;
         float sum = dot[t].v[0] + dot[t].v[1];
-        for (uint32_t o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (uint32_t o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (s < S && lane == 0) p.d_weights[s] = sum;
       }
     }
@@ -349,7 +365,8 @@ cudaError_t dispatch_by(ExpertParams &p, void *workspace, cudaStream_t st) {
   if (e != cudaSuccess || p.D == 0) return e;
   const uint64_t each = kThreads / p.lanes, blocks = ((uint64_t)p.N * p.slices + each - 1) / each;
   ++launch_counter();
-  pdl_launch(dispatch_kernel<E, V, U>, dim3((uint32_t)blocks), dim3(kThreads), 0, st, p);
+  pdl_launch(p.lanes == 32 ? dispatch_kernel<E, V, U, true> : dispatch_kernel<E, V, U, false>,
+             dim3((uint32_t)blocks), dim3(kThreads), 0, st, p);
   return cudaGetLastError();
 }
 template <class E, int V>
@@ -370,7 +387,8 @@ cudaError_t combine_by(ExpertParams &p, cudaStream_t st) {
   set_shape(p, ((p.spans + parts - 1) / parts + U - 1) / U * U);
   const uint32_t blocks = blocks_for((uint64_t)p.N * p.slices, p.lanes, kCombineBlocks);
   ++launch_counter();
-  combine_kernel<E, V, R, U><<<blocks, kThreads, 0, st>>>(p);
+  auto *k = p.lanes == 32 ? combine_kernel<E, V, R, U, true> : combine_kernel<E, V, R, U, false>;
+  k<<<blocks, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 template <class E, int V>
@@ -385,8 +403,9 @@ template <class E, int V, int T, int U>
 cudaError_t combine_backward_by(ExpertParams &p, cudaStream_t st) {
   const uint64_t units = ((uint64_t)p.N * p.k + T - 1) / T;
   ++launch_counter();
-  combine_backward_kernel<E, V, T, U>
-      <<<blocks_for(units, p.lanes, kBackBlocks<E, V>), kThreads, 0, st>>>(p);
+  auto *k = p.lanes == 32 ? combine_backward_kernel<E, V, T, U, true>
+                          : combine_backward_kernel<E, V, T, U, false>;
+  k<<<blocks_for(units, p.lanes, kBackBlocks<E, V>), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 template <class E, int V>

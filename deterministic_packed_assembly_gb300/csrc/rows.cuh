@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "elem.cuh"
 
@@ -80,22 +81,36 @@ __device__ __forceinline__ void store_piece(void *p, const uint32_t *w) {
 }
 
 // Columns c, c + step, ... of a row of D, V of them each; what is beyond the row is left
-// as it is (loads) or out (stores).
-template <class E, int V>
+// as it is (loads) or out (stores).  kAll: nothing is.  Bounds and distances that are not
+// known cost more instructions than the moves themselves (20000 x 1001 bf16, 4 experts: combine
+// 69 us, its gradient 125), so that whole spans of a warp go without.
+template <bool kAll = false, class E, int V>
 __device__ __forceinline__ void load_oct(Oct<E, V> &x, const E *row, uint32_t c, uint32_t step,
                                          uint32_t D) {
   using O = Oct<E, V>;
+  const E *at = row + c;
 #pragma unroll
   for (int i = 0; i < O::kPieces; ++i)
-    if (c + i * step < D) load_piece<O::kBytes>(row + c + i * step, x.w + i * O::kWords);
+    if (kAll || c + i * step < D) load_piece<O::kBytes>(at + i * step, x.w + i * O::kWords);
 }
-template <class E, int V>
+template <bool kAll = false, class E, int V>
 __device__ __forceinline__ void store_oct(E *row, uint32_t c, uint32_t step, uint32_t D,
                                           const Oct<E, V> &x) {
   using O = Oct<E, V>;
+  E *at = row + c;
 #pragma unroll
   for (int i = 0; i < O::kPieces; ++i)
-    if (c + i * step < D) store_piece<O::kBytes>(row + c + i * step, x.w + i * O::kWords);
+    if (kAll || c + i * step < D) store_piece<O::kBytes>(at + i * step, x.w + i * O::kWords);
+}
+// Calls `body` with whether all of the columns up to `end` are in the row, known when it is
+// compiled: for narrow pieces of a warp, whose bounds would take a test each (where a lane
+// has one piece of a span, a second copy of the code costs more than its test).
+template <int V, bool kWarp, class F>
+__device__ __forceinline__ void by_all(uint32_t end, uint32_t D, F &&body) {
+  if (V < kOct && kWarp && end <= D)
+    body(std::integral_constant<bool, V < kOct && kWarp>{});
+  else
+    body(std::false_type{});
 }
 
 // The eight columns as pairs of floats, and back (each rounded once).
