@@ -40,9 +40,10 @@ struct NormParams {
 };
 
 // How a row lies on threads, by its columns alone: what a row gets does not depend on
-// the kernel that takes it.  nb spans a warp: forward as many as leave five warps (a row's
-// exchange of sums costs each of its warps the same; 32768 x 2560 bf16: ten warps 90 us, five FIVE),
-// backward as few as leave fifteen, whose sums take registers.
+// the kernel that takes it.  nb spans a warp.  Forward a row's exchange of sums costs each of
+// its warps the same, so that few are better while blocks are enough (32768 x 2560 bf16: ten
+// warps 90 us, five 71), but weights take registers; backward the sums of the weights'
+// gradients do.
 struct NormShape {
   uint32_t lanes, nb, warps;
 };
@@ -54,12 +55,10 @@ inline NormShape norm_shape(uint32_t D, bool back) {
     s.nb = (uint32_t)spans, s.warps = 1;
     return s;
   }
-  const uint32_t few = back ? kNormWarps : 5;
-  s.nb = spans <= few                ? 1
-         : spans <= 2 * few          ? 2
-         : spans <= 3 * few          ? 3
-         : !back && spans <= 4 * few ? 4
-                                     : 5;
+  if (back)
+    s.nb = spans <= kNormWarps ? 1 : spans <= 2 * kNormWarps ? 2 : spans <= 3 * kNormWarps ? 3 : 5;
+  else
+    s.nb = spans <= 5 ? 1 : spans <= 20 ? 2 : 5;
   s.warps = (uint32_t)((spans + s.nb - 1) / s.nb);
   return s;
 }

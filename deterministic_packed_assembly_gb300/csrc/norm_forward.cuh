@@ -221,18 +221,18 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
                                                      (int64_t)(n0 + r) * p.x_row) & 15u;
       row[r] = ring_row(shared + kNormRows, stage, 0, 1, R, r, slot) + off;
       there[r] = sh.head[stage][r].there;
+      // without a branch, so that the batch's rows are computed side by side: what an absent
+      // row's place holds comes to nothing
       Ch<2> two = {0.0f, 0.0f};
-      if (there[r]) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          Oct<E, V> x;
-          Ch<2> f[kOct / 2];
-          ring_oct(x, row[r] + i * kSpan * sizeof(E));
-          if (!all) only(x, first + i * kSpan, p.D);
-          widen(x, f);
+      for (int i = 0; i < NB; ++i) {
+        Oct<E, V> x;
+        Ch<2> f[kOct / 2];
+        ring_oct(x, row[r] + i * kSpan * sizeof(E));
+        if (!all) only(x, first + i * kSpan, p.D);
+        widen(x, f);
 #pragma unroll
-          for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
-        }
+        for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
       }
       v[r] = two.v[0] + two.v[1];
     }
@@ -243,24 +243,22 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
       mean[r] = v[r] * share;
       const Ch<2> minus = splat<2>(-mean[r]);
       Ch<2> two = {0.0f, 0.0f};
-      if (there[r]) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const uint32_t c = first + i * kSpan;
-          Oct<E, V> x;
-          Ch<2> f[kOct / 2];
-          ring_oct(x, row[r] + i * kSpan * sizeof(E));
-          widen(x, f);
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t c = first + i * kSpan;
+        Oct<E, V> x;
+        Ch<2> f[kOct / 2];
+        ring_oct(x, row[r] + i * kSpan * sizeof(E));
+        widen(x, f);
 #pragma unroll
-          for (int j = 0; j < kOct / 2; ++j) f[j] = f[j] + minus;
-          if (!all) {
+        for (int j = 0; j < kOct / 2; ++j) f[j] = f[j] + minus;
+        if (!all) {
 #pragma unroll
-            for (int j = 0; j < kOct; ++j)
-              if (!inside<V>(c, kStep, p.D, j)) f[j / 2].v[j & 1] = 0.0f;
-          }
-#pragma unroll
-          for (int j = 0; j < kOct / 2; ++j) two = fma(f[j], f[j], two);
+          for (int j = 0; j < kOct; ++j)
+            if (!inside<V>(c, kStep, p.D, j)) f[j / 2].v[j & 1] = 0.0f;
         }
+#pragma unroll
+        for (int j = 0; j < kOct / 2; ++j) two = fma(f[j], f[j], two);
       }
       v[r] = two.v[0] + two.v[1];
     }
@@ -275,16 +273,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         const uint32_t c = first + i * kSpan;
-        Oct<E, V> x;
-        clear(x);
-        if (there[r]) {
-          Ch<2> f[kOct / 2];
-          ring_oct(x, row[r] + i * kSpan * sizeof(E));
-          widen(x, f);
+        Oct<E, V> x, zero;
+        Ch<2> f[kOct / 2];
+        clear(zero);
+        ring_oct(x, row[r] + i * kSpan * sizeof(E));
+        widen(x, f);
 #pragma unroll
-          for (int j = 0; j < kOct / 2; ++j) f[j] = fma((f[j] + minus) * scale, w[i][j], b[i][j]);
-          x = narrow<E, V>(f);
-        }
+        for (int j = 0; j < kOct / 2; ++j) f[j] = fma((f[j] + minus) * scale, w[i][j], b[i][j]);
+        x = there[r] ? narrow<E, V>(f) : zero;
         if (all)
           store_all(y + c, x);
         else
@@ -375,7 +371,7 @@ cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
 // Batches of four, two or one row, of which the widest rows have the last two.
 template <class E, int NB, int V, int kWarps, int kBlocks>
 cudaError_t ring_of(NormParams &p, bool &done, cudaStream_t st) {
-  constexpr uint32_t kMost = NB > 4 ? 2 : 4;
+  constexpr uint32_t kMost = NB > 2 ? 2 : 4;
   const NormRing ring = norm_ring(norm_shape(p.D, false), sizeof(E), 1, kBlocks, kMost, kMost / 2, 0);
   done = ring.stages > 0;
   if (!done) return cudaSuccess;
@@ -407,12 +403,11 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
   // nothing but its own loads
   if (p.N > 4 * kNormSMs) {
     bool done = false;
-    const cudaError_t e = s.nb == 1       ? ring_of<E, 1, V, 5, 5>(p, done, st)
-                          : s.nb == 2     ? ring_of<E, 2, V, 5, 4>(p, done, st)
-                          : s.nb == 3     ? ring_of<E, 3, V, 5, 3>(p, done, st)
-                          : s.nb == 4     ? ring_of<E, 4, V, 5, 3>(p, done, st)
-                          : s.warps <= 7  ? ring_of<E, 5, V, 7, 2>(p, done, st)
-                                          : ring_of<E, 5, V, kNormWarps, 1>(p, done, st);
+    const cudaError_t e = s.nb == 1                   ? ring_of<E, 1, V, 5, 5>(p, done, st)
+                          : s.nb == 2 && s.warps <= 5 ? ring_of<E, 2, V, 5, 4>(p, done, st)
+                          : s.nb == 2                 ? ring_of<E, 2, V, 10, 2>(p, done, st)
+                          : s.warps <= 7              ? ring_of<E, 5, V, 7, 2>(p, done, st)
+                                         : ring_of<E, 5, V, kNormWarps, 1>(p, done, st);
     if (done) return e;
   }
   const uint32_t groups = std::max<uint32_t>(1, kDirectWarps / p.warps);
@@ -421,8 +416,6 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
   ++launch_counter();
   auto *k = s.nb == 1   ? norm_direct_kernel<E, 1, V>
             : s.nb == 2 ? norm_direct_kernel<E, 2, V>
-            : s.nb == 3 ? norm_direct_kernel<E, 3, V>
-            : s.nb == 4 ? norm_direct_kernel<E, 4, V>
                         : norm_direct_kernel<E, 5, V>;
   k<<<blocks, threads, 0, st>>>(p);
   return cudaGetLastError();

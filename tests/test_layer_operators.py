@@ -318,6 +318,22 @@ def test_layer_norm_many_rows(nsp, N, D, dtype):
     check_norm(nsp, x, w, b, doc, dy)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,D", [(2500, 514), (1300, 1281), (1001, 2560), (701, 2571), (650, 3841),
+                                 (640, 5003), (630, 7682), (620, 8200), (613, 11521), (611, 16384),
+                                 (610, 19200)])
+def test_layer_norm_rows_through_the_ring(nsp, N, D, dtype):
+    """Enough rows for every width of row, and of pieces, to come through shared memory, in
+    batches of which the last is not whole; padding of whole batches; the rows' places an odd
+    distance apart, and off a boundary."""
+    x, w, b, doc, dy = norm_inputs(N, D, dtype, "f32", N + D)
+    doc[40:80] = -1
+    doc[-1] = 0
+    check_norm(nsp, x, w, b, doc, dy)
+    if dtype != "f16":
+        check_norm(nsp, x, w, b, None, dy, xc=laid(x, 3, 5), dyc=laid(dy, 1, 7))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("pad,shift", [(0, 1), (3, 0), (8, 8), (16, 4), (1, 2), (5, 7)])
 def test_layer_norm_strides_and_alignment(nsp, pad, shift, dtype):
@@ -386,7 +402,9 @@ def test_layer_norm_of_nothing(nsp):
     assert not nsp.layer_norm_backward(x, x, w, w, m, r)[1].any()
 
 
-@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (520, "f32"), (1001, "bf16"), (2560, "bf16")])
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (300, "f16"), (520, "f32"), (1001, "bf16"),
+                                     (2560, "bf16"), (4096, "f32"), (5003, "bf16"), (8192, "f16"),
+                                     (16384, "bf16")])
 def test_layer_norm_rows_do_not_depend_on_the_other_rows(nsp, D, dtype):
     x, w, b, doc, dy = (t.cuda() for t in norm_inputs(700, D, dtype, "f32", D))
     y, m, r = nsp.layer_norm_forward(x, w, b, doc=doc)
