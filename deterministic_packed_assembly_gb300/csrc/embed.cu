@@ -93,6 +93,54 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p) {
   });
 }
 
+// Narrow rows: T positions at once (131072 x 512 bf16: 35 us one at a time, 29 two).
+template <class W, class E, int V, int T, int U, bool kWarp>
+__global__ void __launch_bounds__(kThreads) embed_narrow_kernel(const EmbedParams p) {
+  const uint32_t lanes = kWarp ? 32 : p.lanes, span = lanes * kOct, step = lanes * V;
+  const uint64_t unit = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
+  const uint64_t n0 = unit / p.slices * T;
+  const uint32_t slice = (uint32_t)(unit % p.slices);
+  if (n0 >= p.N) return;
+  int64_t id[T];
+  bool there[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const uint64_t n = n0 + t;
+    id[t] = -1;
+    if (n < p.N)
+      id[t] = p.wide ? static_cast<const int64_t *>(p.tokens)[n]
+                     : static_cast<const int32_t *>(p.tokens)[n];
+    there[t] = id[t] >= 0 && id[t] < (int64_t)p.V && !(p.doc && n < p.N && p.doc[n] < 0);
+  }
+  const uint32_t from = slice * U * span, first = from + threadIdx.x % lanes * V;
+  by_all<V, kWarp>(from + U * span, p.D, [&](auto all) {
+    constexpr bool kAll = decltype(all)::value;
+    Oct<W, V> v[T][U];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const W *row = static_cast<const W *>(p.table) + (there[t] ? id[t] : 0) * p.table_row;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!kAll || !there[t]) clear(v[t][u]);
+        if (there[t]) load_oct<kAll>(v[t][u], row, first + u * span, step, p.D);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      if (n0 + t >= p.N) break;
+      E *y = static_cast<E *>(p.y) + (int64_t)(n0 + t) * p.D;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Ch<2> x[kOct / 2];
+        widen(v[t][u], x);
+#pragma unroll
+        for (int i = 0; i < kOct / 2; ++i) x[i] = x[i] * splat<2>(there[t] ? p.scale : 0.0f);
+        store_oct<kAll>(y, first + u * span, step, p.D, narrow<E, V>(x));
+      }
+    }
+  });
+}
+
 // ---- backward --------------------------------------------------------------------------
 // 0 to the elements at [a, b), by a block.
 template <class W>
@@ -291,22 +339,31 @@ Layout layout_of(uint32_t N, uint32_t V, uint32_t D) {
   return l;
 }
 
-template <class W, class E, int V, int U>
+template <class W, class E, int V, int T, int U>
 cudaError_t forward_by(EmbedParams &p, cudaStream_t st) {
   p.slices = (uint32_t)((spans_for(p.D, p.lanes) + U - 1) / U);
-  const uint64_t each = kThreads / p.lanes, blocks = ((uint64_t)p.N * p.slices + each - 1) / each;
+  const uint64_t each = kThreads / p.lanes, units = ((uint64_t)p.N + T - 1) / T * p.slices;
+  const uint32_t blocks = (uint32_t)((units + each - 1) / each);
   ++launch_counter();
-  auto *k = p.lanes == 32 ? embed_kernel<W, E, V, U, true> : embed_kernel<W, E, V, U, false>;
-  k<<<(uint32_t)blocks, kThreads, 0, st>>>(p);
+  if constexpr (T == 1) {
+    auto *k = p.lanes == 32 ? embed_kernel<W, E, V, U, true> : embed_kernel<W, E, V, U, false>;
+    k<<<blocks, kThreads, 0, st>>>(p);
+  } else {
+    auto *k = p.lanes == 32 ? embed_narrow_kernel<W, E, V, T, U, true>
+                            : embed_narrow_kernel<W, E, V, T, U, false>;
+    k<<<blocks, kThreads, 0, st>>>(p);
+  }
   return cudaGetLastError();
 }
 template <class W, class E, int V>
 cudaError_t forward_of(EmbedParams &p, cudaStream_t st) {
   p.lanes = lanes_for(p.D);
   const uint64_t spans = spans_for(p.D, p.lanes);
-  if (spans <= 1) return forward_by<W, E, V, 1>(p, st);
-  if (spans == 2) return forward_by<W, E, V, 2>(p, st);
-  return forward_by<W, E, V, 4>(p, st);
+  if (spans > 2) return forward_by<W, E, V, 1, 4>(p, st);
+  // several positions at once only where there are enough to fill the SMs
+  if ((uint64_t)p.N * p.lanes < 32ull * 32 * 152)
+    return spans == 2 ? forward_by<W, E, V, 1, 2>(p, st) : forward_by<W, E, V, 1, 1>(p, st);
+  return spans == 2 ? forward_by<W, E, V, 2, 2>(p, st) : forward_by<W, E, V, 4, 1>(p, st);
 }
 
 template <class W, class E, int V>
