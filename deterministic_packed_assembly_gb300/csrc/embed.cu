@@ -12,6 +12,10 @@
 // last one.  A token of more positions than that, across tiles, leaves 32-bit sums of each
 // tile, which the last kernel adds up, in the tiles' order.  The rows of tokens that are
 // not there are filled with 0 by the same launch.
+//
+// 8 x 4096 tokens of 128256 x 2560 bf16: lookup 40 us (86 % of the copy's bandwidth),
+// gradient 140 (87 %), of which the sort 17 and the join 6.  (Rows of 0 filled beside the
+// sort's kernels slowed those by as much: 143.)
 
 #include <cuda_runtime.h>
 

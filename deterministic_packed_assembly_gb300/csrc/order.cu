@@ -10,7 +10,9 @@
 // and equal keys keep their order.
 //
 // What bounds it is latency: a launch and some trips to the L2 cache a pass.  The first pass
-// reads its keys while the counters are still being made.
+// reads its keys while the counters are still being made.  32768 tokens of 128256: 17 us;
+// 262144 choices of 64 experts 9, 1048576 of 256 21.  (One block for few keys, all passes in
+// shared memory, was slower from 1000 keys on: 8192 in 38 us in place of 15.)
 
 #include <cuda_runtime.h>
 
