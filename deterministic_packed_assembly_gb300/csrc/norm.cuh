@@ -190,7 +190,8 @@ __device__ __forceinline__ char *ring_row(char *rows, uint32_t stage, uint32_t a
 }
 
 // The warp that copies: lane r has row r of each batch.  Documents and statistics are read a
-// batch ahead, so that their way does not hold up the copies.
+// batch ahead, so that their way does not hold up the copies.  If a wait runs out it copies no
+// more, and the others' waits run out too.
 template <class E, int R, bool kBack>
 __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, char *rows,
                                              uint32_t slot) {
@@ -207,11 +208,10 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, 
     return h;
   };
   NormHead head = look(n);
-  bool lost = false;
   uint32_t stage = 0, turn = 0;
   for (; n - lane < p.N; n += every) {
     const NormHead next = look(n + every);
-    if (turn && !lost && !barrier_wait(&sh.empty[stage], (turn - 1) & 1)) lost = true;
+    if (turn && !barrier_wait(&sh.empty[stage], (turn - 1) & 1)) return;
     sh.head[stage][lane] = head;
     RingSpan x = {0, 0, 0}, dy = x;
     char *xs = ring_row(rows, stage, 0, kArrays, R, lane, slot);
@@ -230,6 +230,9 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, 
     if (++stage == p.stages) stage = 0, ++turn;
   }
 }
+
+// What every output of a batch comes to where a wait for it ran out.
+__device__ __forceinline__ float norm_lost() { return __int_as_float(0x7fffffff); }
 
 // Barriers, by the first thread; `warps` leave a stage.
 template <int R>

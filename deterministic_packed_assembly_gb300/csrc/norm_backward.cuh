@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
           }
         }
       }
-      v[2 * r] = s1.v[0] + s1.v[1], v[2 * r + 1] = s2.v[0] + s2.v[1];
+      v[2 * r] = lost ? norm_lost() : s1.v[0] + s1.v[1], v[2 * r + 1] = s2.v[0] + s2.v[1];
     }
     batch_sums<2 * R, kWarps>(v, sh.part[buffer], p.warps, warp, lane);
     buffer ^= 1;  // two buffers: one barrier a batch
@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
 #pragma unroll
     for (int j = 0; j < kOct; ++j) {
       const uint32_t c = first + i * kSpan + j / V * kStep + j % V;
-      if (c < p.D) to[c] = dw[i][j / 2].v[j & 1], to[p.D + c] = db[i][j / 2].v[j & 1];
+      if (c < p.D)
+        to[c] = lost ? norm_lost() : dw[i][j / 2].v[j & 1],
+        to[p.D + c] = lost ? norm_lost() : db[i][j / 2].v[j & 1];
     }
 }
 

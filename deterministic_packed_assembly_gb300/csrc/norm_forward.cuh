@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
 #pragma unroll
         for (int j = 0; j < kOct / 2; ++j) two = two + f[j];
       }
-      v[r] = two.v[0] + two.v[1];
+      v[r] = lost ? norm_lost() : two.v[0] + two.v[1];
     }
     batch_sums<R, kWarps>(v, sh.part[0], p.warps, warp, lane);
     float mean[R];

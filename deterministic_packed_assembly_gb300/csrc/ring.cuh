@@ -73,6 +73,8 @@ __device__ __forceinline__ RingSpan ring_span(char *slot, const E *row, uint32_t
     *reinterpret_cast<E *>(slot + (i - s.base)) = *reinterpret_cast<const E *>(i);
   for (uintptr_t i = s.hi; i < b; i += sizeof(E))
     *reinterpret_cast<E *>(slot + (i - s.base)) = *reinterpret_cast<const E *>(i);
+  // later copies of the engine to the same place come after these
+  if (a < s.lo || s.hi < b) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   return s;
 }
 
