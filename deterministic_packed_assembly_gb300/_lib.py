@@ -28,6 +28,7 @@ NS_PACK_SHUFFLE_ROWS = 4
 NS_PACK_WRAP = 8
 NS_PACK_HOST_CORPUS = 16
 NS_PACK_ORDERED_FREE = 32
+NS_DISPATCH_MAX_EXPERTS = 1024
 NS_F32 = 0
 NS_BF16 = 1
 NS_F16 = 2

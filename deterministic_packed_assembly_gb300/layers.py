@@ -70,7 +70,7 @@ def _embed_inputs(tokens, V, D, table_code, code, scale, doc) -> bytes:
 
 
 # Its number; torch.cuda.current_device takes twice as long.
-_current_device = torch._C._cuda_getDevice
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _code(dtype, name: str) -> int:
@@ -228,11 +228,16 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     """Gradients (dx, dweight, dbias) from that of ``y`` ([..., D], rows at even
     distances), with the forward pass's inputs and what it returned; dweight and dbias
     are None where ``weight`` and ``bias`` are."""
+    return _norm_backward(dy, x, weight, bias, mean, rstd, doc, weight is not None,
+                          bias is not None)
+
+
+def _norm_backward(dy, x, weight, bias, mean, rstd, doc, to_weight: bool, to_bias: bool):
     inputs = _norm_inputs(x, weight, bias, 0.0, doc)
     shape, device = x.shape, x.device
     if device.index != _current_device():
         with torch.cuda.device(device):
-            return layer_norm_backward(dy, x, weight, bias, mean, rstd, doc=doc)
+            return _norm_backward(dy, x, weight, bias, mean, rstd, doc, to_weight, to_bias)
     if not isinstance(dy, torch.Tensor) or dy.dtype != x.dtype or dy.device != device:
         _refuse("dy: expected a tensor of x's dtype on x's device")
     _shape(dy, "dy", shape)
@@ -242,9 +247,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     rstd_ptr = _optional(rstd, "rstd", torch.float32, shape[:-1], device)
     dx = torch.empty(shape, dtype=x.dtype, device=device)
     dweight = dbias = work = None
-    if weight is not None:
+    if to_weight:
         dweight = torch.empty(shape[-1], dtype=weight.dtype, device=device)
-    if bias is not None:
+    if to_bias:
         dbias = torch.empty(shape[-1], dtype=bias.dtype, device=device)
     if dweight is not None or dbias is not None:
         D = shape[-1]
@@ -270,9 +275,9 @@ class _LayerNorm(torch.autograd.Function):
         _reverse_only(dy)
         x, weight, bias, doc, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dweight, dbias = layer_norm_backward(_even(dy), x, weight, bias, mean, rstd, doc=doc)
-        return (dx if need[0] else None, dweight if need[1] else None, dbias if need[2] else None,
-                None, None)
+        dx, dweight, dbias = _norm_backward(_even(dy), x, weight, bias, mean, rstd, doc,
+                                            need[1], need[2])
+        return dx if need[0] else None, dweight, dbias, None, None
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -305,8 +310,8 @@ def _dispatch(x, ids, experts):
     shape = x.shape
     if len(shape) != 2:
         _refuse(f"x: shape {tuple(shape)}, expected [N, D]")
-    if not isinstance(experts, int) or experts < 1:
-        _refuse(f"experts: {experts!r}, expected a positive integer")
+    if not isinstance(experts, int) or not 1 <= experts <= L.NS_DISPATCH_MAX_EXPERTS:
+        _refuse(f"experts: {experts!r}, expected 1 to {L.NS_DISPATCH_MAX_EXPERTS}")
     device = x.device
     index = device.index
     if index != _current_device():
@@ -375,11 +380,15 @@ def combine_backward(d_out: torch.Tensor, rows: torch.Tensor, order: ExpertOrder
                      weights: Optional[torch.Tensor] = None):
     """Gradients (d_rows, d_weights) of ``combine`` from that of its output [N, D], with
     its inputs; d_weights is None where ``weights`` is."""
+    return _combine_backward(d_out, rows, order, weights, weights is not None)
+
+
+def _combine_backward(d_out, rows, order, weights, to_weights: bool):
     code, N, k, E, place, offsets = _order(order, rows, "rows")
     D, device = rows.shape[1], rows.device
     if device.index != _current_device():
         with torch.cuda.device(device):
-            return combine_backward(d_out, rows, order, weights)
+            return _combine_backward(d_out, rows, order, weights, to_weights)
     if not isinstance(d_out, torch.Tensor) or d_out.dtype != rows.dtype or d_out.device != device:
         _refuse("d_out: expected a tensor of the rows' dtype on their device")
     _shape(d_out, "d_out", (N, D))
@@ -387,7 +396,7 @@ def combine_backward(d_out: torch.Tensor, rows: torch.Tensor, order: ExpertOrder
     weights_ptr = _optional(weights, "weights", torch.float32, (N, k), device)
     d_rows = torch.empty((N * k, D), dtype=rows.dtype, device=device)
     d_weights = None
-    if weights is not None:
+    if to_weights:
         d_weights = torch.empty((N, k), dtype=torch.float32, device=device)
     L.ns_combine_backward(sizes, place, offsets, weights_ptr, rows.data_ptr(),
                           _row_step(rows, "rows"), d_out.data_ptr(), _row_step(d_out, "d_out"),
@@ -445,8 +454,9 @@ class _Combine(torch.autograd.Function):
         _reverse_only(d_out)
         rows, weights, *order = ctx.saved_tensors
         need = ctx.needs_input_grad
-        d_rows, d_weights = combine_backward(_even(d_out), rows, ExpertOrder(*order), weights)
-        return d_rows if need[0] else None, d_weights if need[1] else None, None, None, None
+        d_rows, d_weights = _combine_backward(_even(d_out), rows, ExpertOrder(*order), weights,
+                                             need[1])
+        return d_rows if need[0] else None, d_weights, None, None, None
 
 
 def combine(rows: torch.Tensor, order: ExpertOrder,

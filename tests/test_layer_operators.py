@@ -677,6 +677,46 @@ def test_experts_gradients_and_autograd(nsp):
     assert same(dx, nsp.dispatch_backward(dr, order))
 
 
+def test_gradients_of_frozen_weights_are_not_computed(nsp, monkeypatch):
+    made = {}
+
+    def watch(name, *which):
+        call = getattr(nsp._lib, name)
+
+        def watched(*args):
+            made[name] = [args[i] for i in which]
+            return call(*args)
+
+        monkeypatch.setattr(nsp._lib, name, watched)
+
+    watch("ns_norm_backward", 6, 7)
+    watch("ns_combine_backward", 9)
+    x, w, b, doc, dy = (t.cuda() for t in norm_inputs(700, 520, "bf16", "f32", 4))
+    full = nsp.layer_norm_backward(dy, x, w, b, *nsp.layer_norm_forward(x, w, b, doc=doc)[1:],
+                                   doc=doc)
+    for leaves in ((x,), (x, w), (x, b), (w,)):
+        for t in (x, w, b):
+            t.requires_grad_(any(t is leaf for leaf in leaves))
+        y = nsp.layer_norm(x, w, b, doc=doc)
+        grads = torch.autograd.grad(y, leaves, dy)
+        for t, g in zip(leaves, grads):
+            assert same(g, full[0 if t is x else 1 if t is w else 2])
+        assert [p is not None for p in made["ns_norm_backward"]] == [
+            any(t is leaf for leaf in leaves) for t in (w, b)]
+
+    x, ids, E, _, w, d = (t.cuda() if isinstance(t, torch.Tensor) else t
+                          for t in expert_inputs(300, 5, 3, 40, "bf16", 7))
+    rows, order = nsp.dispatch(x, ids, E)
+    full = nsp.combine_backward(d, rows, order, w)
+    for leaves in ((rows,), (rows, w), (w,)):
+        for t in (rows, w):
+            t.requires_grad_(any(t is leaf for leaf in leaves))
+        grads = torch.autograd.grad(nsp.combine(rows, order, w), leaves, d)
+        for t, g in zip(leaves, grads):
+            assert same(g, full[0 if t is rows else 1])
+        assert (made["ns_combine_backward"][0] is not None) == (leaves[-1] is w)
+
+
 # ---- all of them ---------------------------------------------------------------------------
 def test_same_bits_every_time_and_on_every_stream(nsp):
     g = gen(3)
