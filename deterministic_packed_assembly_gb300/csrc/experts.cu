@@ -358,7 +358,9 @@ template <class E, int V, int U>
 cudaError_t dispatch_by(ExpertParams &p, void *workspace, cudaStream_t st) {
   set_shape(p, U);
   if (few(p.N, p.k)) {
-    const size_t shared = (p.N * p.k + std::max(p.k, p.E) + 1) * sizeof(uint32_t);
+    // counters of a token's choices, or of the experts: alone where no token is, whatever k
+    const uint32_t counts = p.N ? std::max(p.k, p.E) : p.E;
+    const size_t shared = ((size_t)p.N * p.k + counts + 1) * sizeof(uint32_t);
     ++launch_counter();
     dispatch_few_kernel<E, V, U><<<p.N + 1, kThreads, shared, st>>>(p);
     return cudaGetLastError();
