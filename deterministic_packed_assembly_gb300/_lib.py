@@ -250,6 +250,7 @@ SYMBOLS = ("ns_pack_init", "ns_pack_step", "ns_pack_fingerprint", "ns_pack_batch
            "ns_route_workspace", "ns_route_forward", "ns_route_backward",
            "ns_embed_forward", "ns_embed_workspace", "ns_embed_backward",
            "ns_norm_forward", "ns_norm_workspace", "ns_norm_backward",
+           "ns_norm_probe_forward", "ns_norm_probe_backward",
            "ns_dispatch_workspace", "ns_dispatch", "ns_combine", "ns_combine_backward")
 
 
@@ -316,6 +317,10 @@ def _load() -> C.CDLL:
     L.ns_norm_workspace.argtypes = [u32, u32]
     L.ns_norm_backward.restype = i32
     L.ns_norm_backward.argtypes = [norm, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.ns_norm_probe_forward.restype = i32
+    L.ns_norm_probe_forward.argtypes = [norm, u32, u32, vp, vp, vp, vp]
+    L.ns_norm_probe_backward.restype = i32
+    L.ns_norm_probe_backward.argtypes = [norm, u32, u32, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.ns_dispatch_workspace.restype = u64
     L.ns_dispatch_workspace.argtypes = [u32, u32, u32]
     L.ns_dispatch.restype = i32
@@ -493,6 +498,18 @@ def ns_norm_backward(inputs, mean, rstd, dy, dy_row: int, dx, dweight, dbias,
                      workspace, stream) -> None:
     check(lib.ns_norm_backward(_argument(inputs), mean, rstd, dy, dy_row, dx, dweight, dbias,
                                workspace, stream), "ns_norm_backward")
+
+
+def ns_norm_probe_forward(inputs, fed: int, tries: int, y, mean, rstd, stream) -> None:
+    """ns_norm_forward where only ``fed`` rows come (see include/nstrain_probe.h)."""
+    check(lib.ns_norm_probe_forward(_argument(inputs), fed, tries, y, mean, rstd, stream),
+          "ns_norm_probe_forward")
+
+
+def ns_norm_probe_backward(inputs, fed: int, tries: int, mean, rstd, dy, dy_row: int, dx, dweight,
+                           dbias, workspace, stream) -> None:
+    check(lib.ns_norm_probe_backward(_argument(inputs), fed, tries, mean, rstd, dy, dy_row, dx,
+                                     dweight, dbias, workspace, stream), "ns_norm_probe_backward")
 
 
 def ns_dispatch_workspace(N: int, k: int, E: int) -> int:

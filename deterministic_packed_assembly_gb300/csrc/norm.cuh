@@ -34,6 +34,8 @@ struct NormParams {
   uint32_t N, D;
   uint32_t lanes, warps;  // of a row: lanes of one warp, or warps
   uint32_t stages;        // of the ring
+  uint32_t fed;           // rows that come to it: N, but where a test withholds some
+  uint32_t tries;         // of a wait for them
   float *partial;         // [blocks][2][D]
   void *dweight, *dbias;
   uint32_t blocks;
@@ -209,9 +211,9 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, 
   };
   NormHead head = look(n);
   uint32_t stage = 0, turn = 0;
-  for (; n - lane < p.N; n += every) {
+  for (; n - lane < p.fed; n += every) {
     const NormHead next = look(n + every);
-    if (turn && !barrier_wait(&sh.empty[stage], (turn - 1) & 1)) return;
+    if (turn && !barrier_wait(&sh.empty[stage], (turn - 1) & 1, p.tries)) return;
     sh.head[stage][lane] = head;
     RingSpan x = {0, 0, 0}, dy = x;
     char *xs = ring_row(rows, stage, 0, kArrays, R, lane, slot);
@@ -231,7 +233,9 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, 
   }
 }
 
-// What every output of a batch comes to where a wait for it ran out.
+// What every output of a batch comes to where a wait for it ran out: its sums are this, and its
+// heads, of which nothing is known, count as rows that are there.  A warp that has the batch
+// although another lost it takes its heads as they are, and has these sums.
 __device__ __forceinline__ float norm_lost() { return __int_as_float(0x7fffffff); }
 
 // Barriers, by the first thread; `warps` leave a stage.

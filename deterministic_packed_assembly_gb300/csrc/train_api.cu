@@ -1,11 +1,12 @@
-// C entry points of the training operators (include/nstrain.h): every check of
-// the arguments, then the launches.
+// C entry points of the training operators (include/nstrain.h, nstrain_probe.h): every
+// check of the arguments, then the launches.
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 
 #include "nstrain.h"
+#include "nstrain_probe.h"
 #include "train.h"
 
 namespace {
@@ -239,23 +240,23 @@ static bool check_norm(const ns_norm_inputs *in) {
          usable(in->bias, ws, true) && usable(in->doc, 4, true);
 }
 
-int ns_norm_forward(const ns_norm_inputs *in, void *y, float *mean, float *rstd,
-                    void *cuda_stream) {
+static int run_norm_forward(const ns_norm_inputs *in, nsk::NormWaits waits, void *y, float *mean,
+                            float *rstd, void *cuda_stream) {
   if (!check_norm(in)) return NS_ERR_INVALID_ARG;
   if (in->N == 0) return NS_OK;
   if (!usable(y, size_of(in->dtype)) || !usable(mean, 4, true) || !usable(rstd, 4, true))
     return NS_ERR_INVALID_ARG;
-  return done(
-      nsk::launch_norm_forward(*in, y, mean, rstd, static_cast<cudaStream_t>(cuda_stream)));
+  return done(nsk::launch_norm_forward(*in, y, mean, rstd, static_cast<cudaStream_t>(cuda_stream),
+                                       waits));
 }
 
 uint64_t ns_norm_workspace(uint32_t N, uint32_t D) {
   return N < (1u << 31) && D < (1u << 30) ? nsk::norm_workspace(N, D) : 0;
 }
 
-int ns_norm_backward(const ns_norm_inputs *in, const float *mean, const float *rstd,
-                     const void *dy, int64_t dy_row, void *dx, void *dweight, void *dbias,
-                     void *workspace, void *cuda_stream) {
+static int run_norm_backward(const ns_norm_inputs *in, nsk::NormWaits waits, const float *mean,
+                             const float *rstd, const void *dy, int64_t dy_row, void *dx,
+                             void *dweight, void *dbias, void *workspace, void *cuda_stream) {
   if (!check_norm(in) || !fits_row(dy_row, in->D, in->N)) return NS_ERR_INVALID_ARG;
   const uint64_t es = size_of(in->dtype), ws = size_of(in->weight_dtype);
   const bool none = in->N == 0;
@@ -265,7 +266,34 @@ int ns_norm_backward(const ns_norm_inputs *in, const float *mean, const float *r
     return NS_ERR_INVALID_ARG;
   return done(nsk::launch_norm_backward(*in, mean, rstd, dy, dy_row, dx, dweight, dbias,
                                         static_cast<float *>(workspace),
-                                        static_cast<cudaStream_t>(cuda_stream)));
+                                        static_cast<cudaStream_t>(cuda_stream), waits));
+}
+
+int ns_norm_forward(const ns_norm_inputs *in, void *y, float *mean, float *rstd,
+                    void *cuda_stream) {
+  return run_norm_forward(in, {}, y, mean, rstd, cuda_stream);
+}
+
+int ns_norm_backward(const ns_norm_inputs *in, const float *mean, const float *rstd,
+                     const void *dy, int64_t dy_row, void *dx, void *dweight, void *dbias,
+                     void *workspace, void *cuda_stream) {
+  return run_norm_backward(in, {}, mean, rstd, dy, dy_row, dx, dweight, dbias, workspace,
+                           cuda_stream);
+}
+
+int ns_norm_probe_forward(const ns_norm_inputs *in, uint32_t fed, uint32_t tries, void *y,
+                          float *mean, float *rstd, void *cuda_stream) {
+  if (!in || (fed < in->N && fed % 4)) return NS_ERR_INVALID_ARG;
+  return run_norm_forward(in, {fed, tries}, y, mean, rstd, cuda_stream);
+}
+
+int ns_norm_probe_backward(const ns_norm_inputs *in, uint32_t fed, uint32_t tries,
+                           const float *mean, const float *rstd, const void *dy, int64_t dy_row,
+                           void *dx, void *dweight, void *dbias, void *workspace,
+                           void *cuda_stream) {
+  if (!in || (fed < in->N && fed % 4)) return NS_ERR_INVALID_ARG;
+  return run_norm_backward(in, {fed, tries}, mean, rstd, dy, dy_row, dx, dweight, dbias, workspace,
+                           cuda_stream);
 }
 
 // ---- tokens by expert, and back ----------------------------------------------------

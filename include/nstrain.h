@@ -234,7 +234,9 @@ int ns_embed_backward(const ns_embed_inputs *in, const void *dy, int64_t dy_row,
  * so is the row's gradient; it has no part in those of weight and bias.  x is
  * [N][D], its rows strided (in elements); y, dx are contiguous.  weight and bias
  * ([D], either may be NULL: 1 and 0) are of weight_dtype, which is NS_F32 or
- * dtype. */
+ * dtype.  The kernels' waits for rows that they copy have a limit of about a second;
+ * should one run out, every output of the rows that did not come is NaN, padding
+ * among them, and so are dweight and dbias. */
 typedef struct {
   const void *x;
   int64_t x_row;

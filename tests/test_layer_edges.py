@@ -1,10 +1,67 @@
-"""Edges of embed, layer_norm, dispatch and combine: empty calls."""
+"""Edges of embed, layer_norm, dispatch and combine: empty calls, and waits that run out."""
 import pytest
 import torch
 
-from test_layer_operators import nsp  # noqa: F401
+from test_layer_operators import DTYPES, check_norm, gen, norm_inputs, nsp, same  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+TRIES = 2000  # of a wait: some milliseconds
+
+
+def wide_inputs(N, D, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(N + D)
+    x, dy = (torch.randn(N, D, generator=g, device="cuda").to(DTYPES[dtype]) for _ in range(2))
+    w, b = (torch.randn(D, generator=g, device="cuda") for _ in range(2))
+    return x, dy, w, b
+
+
+def probe(nsp, x, dy, w, b, doc, mean, rstd, fed, tries, weights=True):
+    """Outputs of both passes where only `fed` rows come; filled with 7 before."""
+    from deterministic_packed_assembly_gb300.layers import _norm_inputs
+    N, D = x.shape
+    inputs = _norm_inputs(x, w, b, 1e-5, doc)
+    stream = torch.cuda.current_stream().cuda_stream
+    y, dx = torch.full_like(x, 7), torch.full_like(x, 7)
+    m, r = torch.full_like(mean, 7), torch.full_like(rstd, 7)
+    dw, db = torch.full_like(w, 7), torch.full_like(w, 7)
+    work = torch.empty(nsp.ns_norm_workspace(N, D) // 4, device="cuda")
+    nsp._lib.ns_norm_probe_forward(inputs, fed, tries, y.data_ptr(), m.data_ptr(), r.data_ptr(),
+                                   stream)
+    nsp._lib.ns_norm_probe_backward(inputs, fed, tries, mean.data_ptr(), rstd.data_ptr(),
+                                    dy.data_ptr(), D, dx.data_ptr(),
+                                    dw.data_ptr() if weights else None,
+                                    db.data_ptr() if weights else None,
+                                    work.data_ptr() if weights else None, stream)
+    torch.cuda.synchronize()
+    return y, m, r, dx, dw, db
+
+
+@pytest.mark.parametrize("D,dtype,fed", [
+    (600, "bf16", 20_000), (1280, "f32", 8000), (2560, "bf16", 6000), (2571, "f16", 5000),
+    (5003, "f32", 2400), (9001, "bf16", 2000), (16384, "f16", 1600), (600, "bf16", 0)])
+def test_a_wait_that_runs_out_shows_in_every_output(nsp, D, dtype, fed):
+    """Rows of which nothing comes: y, mean, rstd and dx of them all are NaN, padding among
+    them, whatever their places in the ring held before (padding here, over some turns of
+    it), and so are the weights' gradients; the other rows have their values."""
+    N = fed + 1300
+    x, dy, w, b = wide_inputs(N, D, dtype)
+    doc = torch.zeros(N, dtype=torch.int32, device="cuda")
+    doc[16:fed] = -1
+    doc[fed + 2::3] = -1
+    y, mean, rstd = nsp.layer_norm_forward(x, w, b, doc=doc)
+    dx = nsp.layer_norm_backward(dy, x, w, b, mean, rstd, doc=doc)[0]
+    want = y, mean, rstd, dx
+    for weights in (True, False):
+        got = probe(nsp, x, dy, w, b, doc, mean, rstd, fed, TRIES, weights)
+        for a, e, name in zip(got, want, ("y", "mean", "rstd", "dx")):
+            assert same(a[:fed], e[:fed]), name
+            assert torch.isnan(a[fed:]).all(), (name, int((~torch.isnan(a[fed:])).sum()))
+        for t in got[4:]:
+            assert torch.isnan(t).all() if weights else (t == 7).all()
+    # nothing of it is left
+    assert all(same(a, e) for a, e in zip(probe(nsp, x, dy, w, b, doc, mean, rstd, N, TRIES), want))
 
 
 @pytest.mark.parametrize("k", [1, 12_287, 12_288, 20_000])
