@@ -193,7 +193,9 @@ __device__ __forceinline__ char *ring_row(char *rows, uint32_t stage, uint32_t a
 
 // The warp that copies: lane r has row r of each batch.  Documents and statistics are read a
 // batch ahead, so that their way does not hold up the copies.  If a wait runs out it copies no
-// more, and the others' waits run out too.
+// more, and the others' waits run out too; a warp that has lost a batch leaves no stage any more,
+// so that none is filled again before its copies have arrived.  The block ends after its
+// copies, also where nobody waited for them.
 template <class E, int R, bool kBack>
 __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, char *rows,
                                              uint32_t slot) {
@@ -213,7 +215,7 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, 
   uint32_t stage = 0, turn = 0;
   for (; n - lane < p.fed; n += every) {
     const NormHead next = look(n + every);
-    if (turn && !barrier_wait(&sh.empty[stage], (turn - 1) & 1, p.tries)) return;
+    if (turn && !barrier_wait(&sh.empty[stage], (turn - 1) & 1, p.tries)) break;
     sh.head[stage][lane] = head;
     RingSpan x = {0, 0, 0}, dy = x;
     char *xs = ring_row(rows, stage, 0, kArrays, R, lane, slot);
@@ -231,6 +233,8 @@ __device__ __forceinline__ void produce_rows(const NormParams &p, char *shared, 
     head = next;
     if (++stage == p.stages) stage = 0, ++turn;
   }
+  for (uint32_t i = 0; i < (turn ? p.stages : stage); ++i)
+    barrier_wait(&sh.full[i], (i < stage ? turn : turn - 1) & 1);
 }
 
 // What every output of a batch comes to where a wait for it ran out: its sums are this, and its

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
       }
     }
     __syncwarp();
-    if (lane == 0) barrier_arrive(&sh.empty[stage]);
+    if (lane == 0 && !lost) barrier_arrive(&sh.empty[stage]);
     if (++stage == p.stages) stage = 0, ++turn;
   }
   if (!p.partial) return;

@@ -64,6 +64,30 @@ def test_a_wait_that_runs_out_shows_in_every_output(nsp, D, dtype, fed):
     assert all(same(a, e) for a, e in zip(probe(nsp, x, dy, w, b, doc, mean, rstd, N, TRIES), want))
 
 
+WIDTHS = [(600, "bf16", 20_000), (1280, "f32", 5000), (2560, "bf16", 6000), (2571, "f16", 5000),
+          (5003, "f32", 2400), (9001, "bf16", 2000), (16384, "f16", 1600)]
+
+
+@pytest.mark.parametrize("D,dtype,N", WIDTHS)
+@pytest.mark.parametrize("tries", [0, 1])
+def test_waits_that_run_out_while_rows_are_on_their_way(nsp, D, dtype, N, tries):
+    """No try: every output is NaN, and the next calls find nothing of it.  One: what
+    a batch's warps got in time has its values, the others NaN."""
+    x, dy, w, b = wide_inputs(N, D, dtype)
+    doc = torch.zeros(N, dtype=torch.int32, device="cuda")
+    doc[5::7] = -1
+    y, mean, rstd = nsp.layer_norm_forward(x, w, b, doc=doc)
+    want = y, mean, rstd, *nsp.layer_norm_backward(dy, x, w, b, mean, rstd, doc=doc)
+    for _ in range(3):
+        for weights in (True, False):
+            got = probe(nsp, x, dy, w, b, doc, mean, rstd, N, tries, weights)
+            for a, e in zip(got[:6 if weights else 4], want):
+                assert torch.isnan(a).all() if tries == 0 else (torch.isnan(a) | (a == e)).all()
+        y, m, r = nsp.layer_norm_forward(x, w, b, doc=doc)
+        again = y, m, r, *nsp.layer_norm_backward(dy, x, w, b, m, r, doc=doc)
+        assert all(same(a, e) for a, e in zip(again, want))
+
+
 @pytest.mark.parametrize("k", [1, 12_287, 12_288, 20_000])
 def test_experts_of_no_tokens_with_many_choices(nsp, k):
     x = torch.zeros(0, 5, device="cuda")
