@@ -66,28 +66,43 @@ inline NormShape norm_shape(uint32_t D, bool back) {
 }
 
 // Columns that a row's threads have.
-__host__ __device__ __forceinline__ uint32_t norm_columns(uint32_t nb, uint32_t warps) {
+__host__ __device__ constexpr uint32_t norm_columns(uint32_t nb, uint32_t warps) {
   return nb * warps * 32 * kOct;
 }
-inline uint32_t norm_columns(const NormShape &s) { return norm_columns(s.nb, s.warps); }
 
-// The ring of a pass with `arrays` rows a position: as many blocks an SM as may be, batches
-// as large as leave two stages; or no stages where two rows do not fit.
+// Bytes of a block's weights in shared memory: those of more than three spans a warp, backward
+// (besides their sums three spans' are what the registers hold).
+__host__ __device__ constexpr uint32_t norm_kept(uint32_t nb, uint32_t warps, bool back) {
+  return back && nb > 3 ? norm_columns(nb, warps) * (uint32_t)sizeof(float) : 0;
+}
+
+// The ring of rows of E on `warps` warps, NB spans each: as many of kBlocks blocks an SM as may be,
+// batches of kMost to kLeast rows, as large as leave two stages; or no stages where two rows
+// do not fit.
 struct NormRing {
   uint32_t stages, rows, blocks;  // blocks an SM
   size_t shared;
 };
-inline NormRing norm_ring(const NormShape &shape, uint32_t es, uint32_t arrays, uint32_t most_blocks,
-                          uint32_t most_rows, uint32_t least_rows, uint32_t besides) {
+template <class E, int NB, bool kBack, uint32_t kBlocks, uint32_t kMost, uint32_t kLeast>
+constexpr NormRing norm_ring(uint32_t warps) {
   constexpr uint32_t kShared = 224 * 1024, kHead = 2 * 1024;  // of an SM; of a block besides
-  const uint32_t slot = ring_slot(norm_columns(shape), es) * arrays;
-  for (uint32_t blocks = most_blocks; blocks > 0; --blocks)
-    for (uint32_t rows = most_rows; rows >= least_rows; rows /= 2) {
+  const uint32_t slot = ring_slot(norm_columns(NB, warps), sizeof(E)) * (kBack ? 2 : 1);
+  const uint32_t besides = norm_kept(NB, warps, kBack);
+  for (uint32_t blocks = kBlocks; blocks > 0; --blocks)
+    for (uint32_t rows = kMost; rows >= kLeast; rows /= 2) {
       const uint32_t room = kShared / blocks - 1024 - kHead - besides;
       const uint32_t stages = std::min(kRingStages, room / (slot * rows));
       if (stages >= 2) return {stages, rows, blocks, kHead + besides + (size_t)stages * rows * slot};
     }
   return {0, 0, 0, 0};
+}
+// Whether any of kFew to kWarps warps get batches of R rows: the kernels that are compiled.
+template <class E, int NB, bool kBack, uint32_t kFew, uint32_t kWarps, uint32_t kBlocks,
+          uint32_t kMost, uint32_t kLeast>
+constexpr bool norm_ring_has(uint32_t R) {
+  for (uint32_t warps = kFew; warps <= kWarps; ++warps)
+    if (norm_ring<E, NB, kBack, kBlocks, kMost, kLeast>(warps).rows == R) return true;
+  return false;
 }
 
 // Rows that a lane takes at once where a warp, or a part of one, has whole rows: 16

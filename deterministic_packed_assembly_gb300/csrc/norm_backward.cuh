@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
   // lane's columns beside one another
   constexpr bool kHeld = NB <= 3;
   Ch<2> *kept = reinterpret_cast<Ch<2> *>(shared + kNormRows);
-  char *rows = shared + kNormRows + (kHeld ? 0 : p.warps * NB * 32 * kOct * sizeof(float));
+  char *rows = shared + kNormRows + norm_kept(NB, p.warps, true);
   const uint32_t slot = ring_slot(norm_columns(NB, p.warps), sizeof(E));
   start_ring<R>(shared, p.stages, p.warps);
   if (warp == p.warps) {
@@ -370,21 +370,6 @@ cudaError_t launch_back_ring(NormParams &p, const NormRing &ring, cudaStream_t s
   k<<<p.blocks, 32 * (p.warps + 1), ring.shared, st>>>(p);
   return cudaGetLastError();
 }
-// Batches of kMost rows down to kLeast; false in `done` where the ring has no room.
-template <class E, int NB, int V, int kWarps, int kBlocks, uint32_t kMost, uint32_t kLeast>
-cudaError_t back_ring_of(NormParams &p, bool &done, cudaStream_t st) {
-  const uint32_t besides = NB > 3 ? p.warps * NB * 32 * kOct * (uint32_t)sizeof(float) : 0;
-  const NormRing ring = norm_ring(norm_shape(p.D, true), sizeof(E), 2, kBlocks, kMost, kLeast, besides);
-  done = ring.stages > 0;
-  if constexpr (kMost == 4)
-    if (ring.rows == 4) return launch_back_ring<E, NB, V, 4, kWarps, kBlocks>(p, ring, st);
-  if constexpr (kMost >= 2 && kLeast <= 2)
-    if (ring.rows == 2) return launch_back_ring<E, NB, V, 2, kWarps, kBlocks>(p, ring, st);
-  if constexpr (kLeast == 1)
-    if (ring.rows == 1) return launch_back_ring<E, NB, V, 1, kWarps, kBlocks>(p, ring, st);
-  return cudaSuccess;
-}
-
 template <class E, int V>
 cudaError_t wide_of(NormParams &p, cudaStream_t st) {
   ++launch_counter();
@@ -398,6 +383,20 @@ cudaError_t wide_of(NormParams &p, cudaStream_t st) {
   ++launch_counter();
   norm_columns_kernel<E, V><<<dim3(spans, p.blocks), 32 * kColumnWarps, 0, st>>>(p);
   return cudaGetLastError();
+}
+
+// Batches of kMost rows down to kLeast, or straight from memory where the ring has no room;
+// kFew to kWarps warps a row.
+template <class E, int NB, int V, int kFew, int kWarps, int kBlocks, uint32_t kMost, uint32_t kLeast>
+cudaError_t back_ring_of(NormParams &p, cudaStream_t st) {
+  const NormRing ring = norm_ring<E, NB, true, kBlocks, kMost, kLeast>(p.warps);
+  if constexpr (norm_ring_has<E, NB, true, kFew, kWarps, kBlocks, kMost, kLeast>(4))
+    if (ring.rows == 4) return launch_back_ring<E, NB, V, 4, kWarps, kBlocks>(p, ring, st);
+  if constexpr (norm_ring_has<E, NB, true, kFew, kWarps, kBlocks, kMost, kLeast>(2))
+    if (ring.rows == 2) return launch_back_ring<E, NB, V, 2, kWarps, kBlocks>(p, ring, st);
+  if constexpr (norm_ring_has<E, NB, true, kFew, kWarps, kBlocks, kMost, kLeast>(1))
+    if (ring.rows == 1) return launch_back_ring<E, NB, V, 1, kWarps, kBlocks>(p, ring, st);
+  return wide_of<E, V>(p, st);
 }
 
 template <class E, int NB, int V>
@@ -416,15 +415,12 @@ cudaError_t backward_of(NormParams &p, cudaStream_t st) {
   if (p.D <= kNormNarrow)
     return s.nb == 1 ? narrow_of<E, 1, V>(p, st) : narrow_of<E, 2, V>(p, st);
   if (p.D > kNormKept) return wide_of<E, V>(p, st);
-  bool done = false;
-  const cudaError_t e =
-      s.nb == 1 && s.warps <= 5    ? back_ring_of<E, 1, V, 5, 4, 4, 2>(p, done, st)
-      : s.nb == 1 && s.warps <= 10 ? back_ring_of<E, 1, V, 10, 2, 4, 2>(p, done, st)
-      : s.nb == 1                  ? back_ring_of<E, 1, V, kNormWarps, 1, 4, 2>(p, done, st)
-      : s.nb == 2                  ? back_ring_of<E, 2, V, kNormWarps, 1, 4, 1>(p, done, st)
-      : s.nb == 3                  ? back_ring_of<E, 3, V, kNormWarps, 1, 2, 1>(p, done, st)
-                                   : back_ring_of<E, 5, V, kNormWarps, 1, 1, 1>(p, done, st);
-  return done ? e : wide_of<E, V>(p, st);
+  return s.nb == 1 && s.warps <= 5    ? back_ring_of<E, 1, V, 3, 5, 4, 4, 2>(p, st)
+         : s.nb == 1 && s.warps <= 10 ? back_ring_of<E, 1, V, 6, 10, 2, 4, 2>(p, st)
+         : s.nb == 1                  ? back_ring_of<E, 1, V, 11, kNormWarps, 1, 4, 2>(p, st)
+         : s.nb == 2                  ? back_ring_of<E, 2, V, 8, kNormWarps, 1, 4, 1>(p, st)
+         : s.nb == 3                  ? back_ring_of<E, 3, V, 11, kNormWarps, 1, 2, 1>(p, st)
+                                      : back_ring_of<E, 5, V, 10, kNormWarps, 1, 1, 1>(p, st);
 }
 
 }  // namespace

@@ -368,15 +368,18 @@ cudaError_t launch_ring(NormParams &p, const NormRing &ring, cudaStream_t st) {
   k<<<blocks, 32 * (p.warps + 1), ring.shared, st>>>(p);
   return cudaGetLastError();
 }
-// Batches of four, two or one row, of which the widest rows have the last two.
-template <class E, int NB, int V, int kWarps, int kBlocks>
-cudaError_t ring_of(NormParams &p, bool &done, cudaStream_t st) {
-  constexpr uint32_t kMost = NB > 2 ? 2 : 4;
-  const NormRing ring = norm_ring(norm_shape(p.D, false), sizeof(E), 1, kBlocks, kMost, kMost / 2, 0);
-  done = ring.stages > 0;
-  if (!done) return cudaSuccess;
-  if (ring.rows == kMost) return launch_ring<E, NB, V, kMost, kWarps, kBlocks>(p, ring, st);
-  return launch_ring<E, NB, V, kMost / 2, kWarps, kBlocks>(p, ring, st);
+// Batches of four, two or one row, of which the widest rows have the last two; kFew to kWarps
+// warps a row.
+template <class E, int NB, int V, int kFew, int kWarps, int kBlocks>
+cudaError_t ring_of(NormParams &p, cudaStream_t st) {
+  constexpr uint32_t kMost = NB > 2 ? 2 : 4, kLeast = kMost / 2;
+  const NormRing ring = norm_ring<E, NB, false, kBlocks, kMost, kLeast>(p.warps);
+  if constexpr (norm_ring_has<E, NB, false, kFew, kWarps, kBlocks, kMost, kLeast>(kMost))
+    if (ring.rows == kMost) return launch_ring<E, NB, V, kMost, kWarps, kBlocks>(p, ring, st);
+  if constexpr (norm_ring_has<E, NB, false, kFew, kWarps, kBlocks, kMost, kLeast>(kLeast))
+    if (ring.rows == kLeast) return launch_ring<E, NB, V, kLeast, kWarps, kBlocks>(p, ring, st);
+  static_assert(!norm_ring_has<E, NB, false, kFew, kWarps, kBlocks, kMost, kLeast>(0), "all have one");
+  return cudaErrorInvalidValue;
 }
 
 template <class E, int V>
@@ -401,15 +404,12 @@ cudaError_t forward_of(NormParams &p, cudaStream_t st) {
   }
   // rows that fill the SMs' rings, else straight from memory: a call of 64 rows waits for
   // nothing but its own loads
-  if (p.N > 4 * kNormSMs) {
-    bool done = false;
-    const cudaError_t e = s.nb == 1                   ? ring_of<E, 1, V, 5, 5>(p, done, st)
-                          : s.nb == 2 && s.warps <= 5 ? ring_of<E, 2, V, 5, 4>(p, done, st)
-                          : s.nb == 2                 ? ring_of<E, 2, V, 10, 2>(p, done, st)
-                          : s.warps <= 7              ? ring_of<E, 5, V, 7, 2>(p, done, st)
-                                         : ring_of<E, 5, V, kNormWarps, 1>(p, done, st);
-    if (done) return e;
-  }
+  if (p.N > 4 * kNormSMs)
+    return s.nb == 1                   ? ring_of<E, 1, V, 3, 5, 5>(p, st)
+           : s.nb == 2 && s.warps <= 5 ? ring_of<E, 2, V, 3, 5, 4>(p, st)
+           : s.nb == 2                 ? ring_of<E, 2, V, 6, 10, 2>(p, st)
+           : s.warps <= 7              ? ring_of<E, 5, V, 5, 7, 2>(p, st)
+                                       : ring_of<E, 5, V, 8, kNormWarps, 1>(p, st);
   const uint32_t groups = std::max<uint32_t>(1, kDirectWarps / p.warps);
   const uint32_t threads = groups * p.warps * 32;
   const uint32_t blocks = (uint32_t)(((uint64_t)p.N + groups - 1) / groups);

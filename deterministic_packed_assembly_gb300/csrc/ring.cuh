@@ -46,7 +46,7 @@ __device__ __forceinline__ void bulk_copy(void *smem, const void *gmem, uint32_t
 }
 
 // Bytes of a row's place in the ring, for as many columns as its threads read.
-__host__ __device__ __forceinline__ uint32_t ring_slot(uint32_t columns, uint32_t es) {
+__host__ __device__ constexpr uint32_t ring_slot(uint32_t columns, uint32_t es) {
   return (columns * es + 30) / 16 * 16;
 }
 
