@@ -349,12 +349,13 @@ cudaError_t forward_by(EmbedParams &p, cudaStream_t st) {
   const uint64_t each = kThreads / p.lanes, units = ((uint64_t)p.N + T - 1) / T * p.slices;
   const uint32_t blocks = (uint32_t)((units + each - 1) / each);
   ++launch_counter();
+  constexpr bool kFew = U == 1;  // less than a warp's lanes have one span
   if constexpr (T == 1) {
-    auto *k = p.lanes == 32 ? embed_kernel<W, E, V, U, true> : embed_kernel<W, E, V, U, false>;
+    auto *k = kFew && p.lanes < 32 ? embed_kernel<W, E, V, U, !kFew> : embed_kernel<W, E, V, U, true>;
     k<<<blocks, kThreads, 0, st>>>(p);
   } else {
-    auto *k = p.lanes == 32 ? embed_narrow_kernel<W, E, V, T, U, true>
-                            : embed_narrow_kernel<W, E, V, T, U, false>;
+    auto *k = kFew && p.lanes < 32 ? embed_narrow_kernel<W, E, V, T, U, !kFew>
+                                   : embed_narrow_kernel<W, E, V, T, U, true>;
     k<<<blocks, kThreads, 0, st>>>(p);
   }
   return cudaGetLastError();

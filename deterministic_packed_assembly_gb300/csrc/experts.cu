@@ -370,7 +370,8 @@ cudaError_t dispatch_by(ExpertParams &p, void *workspace, cudaStream_t st) {
   if (e != cudaSuccess || p.D == 0) return e;
   const uint64_t each = kThreads / p.lanes, blocks = ((uint64_t)p.N * p.slices + each - 1) / each;
   ++launch_counter();
-  pdl_launch(p.lanes == 32 ? dispatch_kernel<E, V, U, true> : dispatch_kernel<E, V, U, false>,
+  constexpr bool kFew = U == 1;  // less than a warp's lanes have one span
+  pdl_launch(kFew && p.lanes < 32 ? dispatch_kernel<E, V, U, !kFew> : dispatch_kernel<E, V, U, true>,
              dim3((uint32_t)blocks), dim3(kThreads), 0, st, p);
   return cudaGetLastError();
 }
@@ -408,8 +409,9 @@ template <class E, int V, int T, int U>
 cudaError_t combine_backward_by(ExpertParams &p, cudaStream_t st) {
   const uint64_t units = ((uint64_t)p.N * p.k + T - 1) / T;
   ++launch_counter();
-  auto *k = p.lanes == 32 ? combine_backward_kernel<E, V, T, U, true>
-                          : combine_backward_kernel<E, V, T, U, false>;
+  constexpr bool kFew = U == 1;  // less than a warp's lanes have one span
+  auto *k = kFew && p.lanes < 32 ? combine_backward_kernel<E, V, T, U, !kFew>
+                                 : combine_backward_kernel<E, V, T, U, true>;
   k<<<blocks_for(units, p.lanes, kBackBlocks<E, V>), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
