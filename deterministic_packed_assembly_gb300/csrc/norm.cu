@@ -16,8 +16,8 @@
 // straight from memory.  Backward each thread keeps the sums of its columns' dw and db over
 // all its block's rows; blocks write them out once, and the last kernel adds the blocks'
 // rows in order.  Rows of more than 19200 columns, and backward those that do not fit the ring
-// twice beside their weights (18000 columns of 16 bits, 11520 floats), are read again
-// instead of kept.
+// twice beside their weights (more than 17920 columns of 16 bits, or 11520 floats), are read
+// again instead of kept.
 //
 // 32768 x 2560 bf16: forward 59 us (83 % of the copy's bandwidth), backward 88 (84 %); 9973 x
 // 5003 floats 71 and 96 (82, 92 %).  What keeps them from it is a batch's steps, which

@@ -1,10 +1,33 @@
-"""Edges of embed, layer_norm, dispatch and combine: empty calls, and waits that run out."""
+"""Edges of embed, layer_norm, dispatch and combine: empty calls, the widths at which another
+kernel takes over, and waits that run out."""
 import pytest
 import torch
 
 from test_layer_operators import DTYPES, check_norm, gen, norm_inputs, nsp, same  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+# where a shape of a row's threads ends (norm_shape), batches of the ring become smaller (floats
+# and 16 bits in turn), and the ring ends: 17920 of 16 bits and 11520 floats backward, 19200 forward
+BORDERS = (512, 768, 1280, 1536, 2560, 3328, 3840, 5120, 6400, 6656, 7680, 8960, 11520, 14080, 17920,
+           19200)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [D + more for D in BORDERS for more in (0, 1)])
+def test_layer_norm_at_the_widths_where_kernels_change(nsp, D, dtype):
+    """Rows of the widths on both sides: with enough of them for the ring, the values, and the
+    same bits as of a few (which forward go another way)."""
+    x, w, b, doc, dy = norm_inputs(617, D, dtype, "f32", D)
+    check_norm(nsp, x, w, b, doc, dy)
+    x, w, b, doc, dy = (t.cuda() for t in (x, w, b, doc, dy))
+    y, m, r = nsp.layer_norm_forward(x, w, b, doc=doc)
+    dx = nsp.layer_norm_backward(dy, x, w, b, m, r, doc=doc)[0]
+    n = slice(300, 303)
+    y3, m3, r3 = nsp.layer_norm_forward(x[n], w, b, doc=doc[n])
+    assert same(y3, y[n]) and same(m3, m[n]) and same(r3, r[n])
+    assert same(nsp.layer_norm_backward(dy[n], x[n], w, b, m3, r3, doc=doc[n])[0], dx[n])
+
 
 TRIES = 2000  # of a wait: some milliseconds
 
