@@ -318,9 +318,9 @@ def _load() -> C.CDLL:
     L.ns_norm_backward.restype = i32
     L.ns_norm_backward.argtypes = [norm, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.ns_norm_probe_forward.restype = i32
-    L.ns_norm_probe_forward.argtypes = [norm, u32, u32, vp, vp, vp, vp]
+    L.ns_norm_probe_forward.argtypes = [norm, u32, vp, vp, vp, vp]
     L.ns_norm_probe_backward.restype = i32
-    L.ns_norm_probe_backward.argtypes = [norm, u32, u32, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.ns_norm_probe_backward.argtypes = [norm, u32, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.ns_dispatch_workspace.restype = u64
     L.ns_dispatch_workspace.argtypes = [u32, u32, u32]
     L.ns_dispatch.restype = i32
@@ -500,15 +500,15 @@ def ns_norm_backward(inputs, mean, rstd, dy, dy_row: int, dx, dweight, dbias,
                                workspace, stream), "ns_norm_backward")
 
 
-def ns_norm_probe_forward(inputs, fed: int, tries: int, y, mean, rstd, stream) -> None:
+def ns_norm_probe_forward(inputs, fed: int, y, mean, rstd, stream) -> None:
     """ns_norm_forward where only ``fed`` rows come (see include/nstrain_probe.h)."""
-    check(lib.ns_norm_probe_forward(_argument(inputs), fed, tries, y, mean, rstd, stream),
+    check(lib.ns_norm_probe_forward(_argument(inputs), fed, y, mean, rstd, stream),
           "ns_norm_probe_forward")
 
 
-def ns_norm_probe_backward(inputs, fed: int, tries: int, mean, rstd, dy, dy_row: int, dx, dweight,
+def ns_norm_probe_backward(inputs, fed: int, mean, rstd, dy, dy_row: int, dx, dweight,
                            dbias, workspace, stream) -> None:
-    check(lib.ns_norm_probe_backward(_argument(inputs), fed, tries, mean, rstd, dy, dy_row, dx,
+    check(lib.ns_norm_probe_backward(_argument(inputs), fed, mean, rstd, dy, dy_row, dx,
                                      dweight, dbias, workspace, stream), "ns_norm_probe_backward")
 
 

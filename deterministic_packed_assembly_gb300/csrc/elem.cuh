@@ -191,13 +191,10 @@ __device__ __forceinline__ void barrier_expect(uint64_t *bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
-// Tries of a wait, each of which suspends for some microseconds at most: about a second.
-constexpr uint32_t kWaitTries = 100000;
-// Wait for the phase of this parity; false if it has not come after so many tries.
-__device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity,
-                                             uint32_t tries = kWaitTries) {
+// Wait for the phase of this parity; false if it has not come after about a second.
+__device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity) {
   const uint32_t at = (uint32_t)__cvta_generic_to_shared(bar);
-  for (uint32_t i = 0; i < tries; ++i) {
+  for (int i = 0; i < 100000; ++i) {  // each try suspends for some microseconds at most
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"

@@ -53,11 +53,11 @@ __global__ void __launch_bounds__(32 * kTotalWarps) norm_total_kernel(const Norm
   }
 }
 
-NormParams params_of(const ns_norm_inputs &in, NormWaits waits) {
+NormParams params_of(const ns_norm_inputs &in, uint32_t fed) {
   NormParams p = {};
   p.x = in.x, p.x_row = in.x_row, p.weight = in.weight, p.bias = in.bias, p.doc = in.doc;
   p.N = in.N, p.D = in.D, p.eps = in.eps, p.floats = in.weight_dtype == NS_F32;
-  p.fed = std::min(in.N, waits.fed), p.tries = std::min(kWaitTries, waits.tries);
+  p.fed = std::min(in.N, fed);
   return p;
 }
 // By the rows' type.
@@ -82,8 +82,8 @@ uint64_t norm_workspace(uint32_t N, uint32_t D) {
 }
 
 cudaError_t launch_norm_forward(const ns_norm_inputs &in, void *y, float *mean, float *rstd,
-                                cudaStream_t st, NormWaits waits) {
-  NormParams p = params_of(in, waits);
+                                cudaStream_t st, uint32_t fed) {
+  NormParams p = params_of(in, fed);
   p.y = y, p.mean = mean, p.rstd = rstd;
   const int piece = piece_of_inputs(in, y);
   return by_type(in, [&](auto e) { return norm_forward<decltype(e)>(p, piece, st); });
@@ -91,8 +91,8 @@ cudaError_t launch_norm_forward(const ns_norm_inputs &in, void *y, float *mean, 
 
 cudaError_t launch_norm_backward(const ns_norm_inputs &in, const float *mean, const float *rstd,
                                  const void *dy, int64_t dy_row, void *dx, void *dweight,
-                                 void *dbias, float *partial, cudaStream_t st, NormWaits waits) {
-  NormParams p = params_of(in, waits);
+                                 void *dbias, float *partial, cudaStream_t st, uint32_t fed) {
+  NormParams p = params_of(in, fed);
   p.mean = const_cast<float *>(mean), p.rstd = const_cast<float *>(rstd);
   p.dy = dy, p.dy_row = dy_row, p.y = dx, p.dweight = dweight, p.dbias = dbias;
   p.partial = dweight || dbias ? partial : nullptr;

@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
   bool lost = false;
   uint32_t stage = 0, turn = 0, buffer = 0;
   for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
-    if (!lost && !barrier_wait(&sh.full[stage], turn & 1, p.tries)) lost = true;
+    if (!lost && !barrier_wait(&sh.full[stage], turn & 1)) lost = true;
+    if (lost) lose_batch<R>(sh, stage, lane);
     const char *xr[R], *gr[R];  // this lane's first columns
     float v[2 * R];
 #pragma unroll
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
         const uint32_t c = first + i * kSpan;
         Oct<E, V> x, y;
         clear(x);
-        if (lost || head.there) {
+        if (head.there) {
           Ch<2> f[kOct / 2], g[kOct / 2];
           ring_oct(x, xr[r] + i * kSpan * sizeof(E));
           ring_oct(y, gr[r] + i * kSpan * sizeof(E));

@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
   bool lost = false;
   uint32_t stage = 0, turn = 0;
   for (uint64_t n0 = (uint64_t)blockIdx.x * R; n0 < p.N; n0 += (uint64_t)gridDim.x * R) {
-    if (!lost && !barrier_wait(&sh.full[stage], turn & 1, p.tries)) lost = true;
+    if (!lost && !barrier_wait(&sh.full[stage], turn & 1)) lost = true;
+    if (lost) lose_batch<R>(sh, stage, lane);
     const char *row[R];  // this lane's first columns
     bool there[R];
     float v[R];
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks) norm_ring_kernel(c
         off += (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const E *>(p.x) +
                                                      (int64_t)(n0 + r) * p.x_row) & 15u;
       row[r] = ring_row(shared + kNormRows, stage, 0, 1, R, r, slot) + off;
-      there[r] = lost || sh.head[stage][r].there;  // a lost batch's head is another's: NaN for all
+      there[r] = sh.head[stage][r].there;
       // without a branch, so that the batch's rows are computed side by side: what an absent
       // row's place holds comes to nothing
       Ch<2> two = {0.0f, 0.0f};

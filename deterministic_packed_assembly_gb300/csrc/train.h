@@ -46,16 +46,13 @@ cudaError_t launch_embed_backward(const ns_embed_inputs &in, const void *dy, int
                                   void *dtable, void *workspace, cudaStream_t st);
 
 uint64_t norm_workspace(uint32_t N, uint32_t D);
-// Rows that come to the norm's ring and tries of a wait for them, at most (include/nstrain_probe.h).
-struct NormWaits {
-  uint32_t fed = 0xffffffffu, tries = 0xffffffffu;
-};
+// fed: rows that come to the ring, but for a test (include/nstrain_probe.h) all of them.
 cudaError_t launch_norm_forward(const ns_norm_inputs &in, void *y, float *mean, float *rstd,
-                                cudaStream_t st, NormWaits waits = {});
+                                cudaStream_t st, uint32_t fed = 0xffffffffu);
 cudaError_t launch_norm_backward(const ns_norm_inputs &in, const float *mean, const float *rstd,
                                  const void *dy, int64_t dy_row, void *dx, void *dweight,
                                  void *dbias, float *partial, cudaStream_t st,
-                                 NormWaits waits = {});
+                                 uint32_t fed = 0xffffffffu);
 
 uint64_t dispatch_workspace(uint32_t N, uint32_t k, uint32_t E);
 cudaError_t launch_dispatch(const ns_expert_sizes &s, const int32_t *ids, const void *x,

@@ -240,21 +240,21 @@ static bool check_norm(const ns_norm_inputs *in) {
          usable(in->bias, ws, true) && usable(in->doc, 4, true);
 }
 
-static int run_norm_forward(const ns_norm_inputs *in, nsk::NormWaits waits, void *y, float *mean,
+static int run_norm_forward(const ns_norm_inputs *in, uint32_t fed, void *y, float *mean,
                             float *rstd, void *cuda_stream) {
   if (!check_norm(in)) return NS_ERR_INVALID_ARG;
   if (in->N == 0) return NS_OK;
   if (!usable(y, size_of(in->dtype)) || !usable(mean, 4, true) || !usable(rstd, 4, true))
     return NS_ERR_INVALID_ARG;
   return done(nsk::launch_norm_forward(*in, y, mean, rstd, static_cast<cudaStream_t>(cuda_stream),
-                                       waits));
+                                       fed));
 }
 
 uint64_t ns_norm_workspace(uint32_t N, uint32_t D) {
   return N < (1u << 31) && D < (1u << 30) ? nsk::norm_workspace(N, D) : 0;
 }
 
-static int run_norm_backward(const ns_norm_inputs *in, nsk::NormWaits waits, const float *mean,
+static int run_norm_backward(const ns_norm_inputs *in, uint32_t fed, const float *mean,
                              const float *rstd, const void *dy, int64_t dy_row, void *dx,
                              void *dweight, void *dbias, void *workspace, void *cuda_stream) {
   if (!check_norm(in) || !fits_row(dy_row, in->D, in->N)) return NS_ERR_INVALID_ARG;
@@ -266,33 +266,32 @@ static int run_norm_backward(const ns_norm_inputs *in, nsk::NormWaits waits, con
     return NS_ERR_INVALID_ARG;
   return done(nsk::launch_norm_backward(*in, mean, rstd, dy, dy_row, dx, dweight, dbias,
                                         static_cast<float *>(workspace),
-                                        static_cast<cudaStream_t>(cuda_stream), waits));
+                                        static_cast<cudaStream_t>(cuda_stream), fed));
 }
 
 int ns_norm_forward(const ns_norm_inputs *in, void *y, float *mean, float *rstd,
                     void *cuda_stream) {
-  return run_norm_forward(in, {}, y, mean, rstd, cuda_stream);
+  return run_norm_forward(in, 0xffffffffu, y, mean, rstd, cuda_stream);
 }
 
 int ns_norm_backward(const ns_norm_inputs *in, const float *mean, const float *rstd,
                      const void *dy, int64_t dy_row, void *dx, void *dweight, void *dbias,
                      void *workspace, void *cuda_stream) {
-  return run_norm_backward(in, {}, mean, rstd, dy, dy_row, dx, dweight, dbias, workspace,
+  return run_norm_backward(in, 0xffffffffu, mean, rstd, dy, dy_row, dx, dweight, dbias, workspace,
                            cuda_stream);
 }
 
-int ns_norm_probe_forward(const ns_norm_inputs *in, uint32_t fed, uint32_t tries, void *y,
-                          float *mean, float *rstd, void *cuda_stream) {
+int ns_norm_probe_forward(const ns_norm_inputs *in, uint32_t fed, void *y, float *mean,
+                          float *rstd, void *cuda_stream) {
   if (!in || (fed < in->N && fed % 4)) return NS_ERR_INVALID_ARG;
-  return run_norm_forward(in, {fed, tries}, y, mean, rstd, cuda_stream);
+  return run_norm_forward(in, fed, y, mean, rstd, cuda_stream);
 }
 
-int ns_norm_probe_backward(const ns_norm_inputs *in, uint32_t fed, uint32_t tries,
-                           const float *mean, const float *rstd, const void *dy, int64_t dy_row,
-                           void *dx, void *dweight, void *dbias, void *workspace,
-                           void *cuda_stream) {
+int ns_norm_probe_backward(const ns_norm_inputs *in, uint32_t fed, const float *mean,
+                           const float *rstd, const void *dy, int64_t dy_row, void *dx,
+                           void *dweight, void *dbias, void *workspace, void *cuda_stream) {
   if (!in || (fed < in->N && fed % 4)) return NS_ERR_INVALID_ARG;
-  return run_norm_backward(in, {fed, tries}, mean, rstd, dy, dy_row, dx, dweight, dbias, workspace,
+  return run_norm_backward(in, fed, mean, rstd, dy, dy_row, dx, dweight, dbias, workspace,
                            cuda_stream);
 }
 

@@ -7,7 +7,7 @@ import pytest
 from test_train_host import AT, nsp, refused  # noqa: F401
 
 
-def probe(nsp, back=False, fed=4, tries=10, **kw):
+def probe(nsp, back=False, fed=4, **kw):
     v = dict(x=AT, x_row=8, weight=AT, bias=None, doc=None, N=6, D=8, dtype=nsp.NS_BF16,
              weight_dtype=nsp.NS_F32, eps=1e-5)
     call = dict(mean=AT, rstd=AT, dy=AT, dy_row=8, dx=AT, dweight=AT, dbias=AT, workspace=AT)
@@ -17,7 +17,7 @@ def probe(nsp, back=False, fed=4, tries=10, **kw):
         (v if k in v else call)[k] = x
     s = nsp._lib.ns_norm_inputs(*v.values())
     f = nsp._lib.ns_norm_probe_backward if back else nsp._lib.ns_norm_probe_forward
-    return lambda: f(s, fed, tries, *call.values(), None)
+    return lambda: f(s, fed, *call.values(), None)
 
 
 @pytest.mark.parametrize("back", [False, True])
