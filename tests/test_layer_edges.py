@@ -90,3 +90,74 @@ def test_experts_of_no_tokens_with_many_choices(nsp, k):
     rows, order = nsp.dispatch(x, ids, 3)
     assert rows.shape == (0, 5) and order.place.shape == (0, k) and order.offsets.tolist() == [0] * 4
     assert nsp.combine(rows, order).shape == (0, 5)
+
+
+def chain(nsp, leaves, tokens, ids, doc, dy):
+    """Loss and gradients of all four operators in a row."""
+    table, w, b, gate = leaves
+    x = nsp.layer_norm(nsp.embed(table, tokens, doc=doc), w, b, doc=doc)
+    rows, order = nsp.dispatch(x, ids, 7)
+    out = nsp.combine(torch.tanh(rows), order, gate)
+    loss = (out.float() * dy).sum()
+    return [loss.detach(), *torch.autograd.grad(loss, leaves)]
+
+
+def chain_inputs(N, D, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    leaves = [t.requires_grad_() for t in (
+        torch.randn(90, D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda"),
+        torch.randn(D, generator=g, device="cuda"), torch.rand(N, 3, generator=g, device="cuda"))]
+    tokens = torch.randint(0, 95, (N,), generator=g, device="cuda").int()
+    ids = torch.randint(-1, 7, (N, 3), generator=g, device="cuda").int()
+    doc = torch.randint(-1, 4, (N,), generator=g, device="cuda").int()
+    return leaves, tokens, ids, doc, torch.randn(N, D, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("N,D", [(60, 72), (3000, 640)])
+def test_a_training_step_is_captured_in_a_graph(nsp, N, D):
+    """Forward and backward through PyTorch's autograd, captured and replayed on new inputs."""
+    args = chain_inputs(N, D, 1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(nsp, *args)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(nsp, *args)
+    for seed in (2, 3):
+        new = chain_inputs(N, D, seed)
+        with torch.no_grad():
+            for a, b in zip([*args[0], *args[1:]], [*new[0], *new[1:]]):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, chain(nsp, *new)):
+            assert same(a, b) or a.dim() == 0 and torch.allclose(a, b)
+
+
+def test_calls_of_two_threads(nsp):
+    """Two threads, a stream each: the bits of one alone."""
+    import threading
+    inputs = [chain_inputs(2000, 640, s) for s in (4, 5)]
+    want = [chain(nsp, *i) for i in inputs]
+    got = [[], []]
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[k].append(chain(nsp, *inputs[k]))
+            torch.cuda.current_stream().synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert len(got[k]) == 20
+        for g in got[k]:
+            assert all(same(a, b) for a, b in zip(g[1:], want[k][1:]))
