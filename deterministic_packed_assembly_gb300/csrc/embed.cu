@@ -15,7 +15,11 @@
 //
 // 8 x 4096 tokens of 128256 x 2560 bf16: lookup 40 us (86 % of the copy's bandwidth),
 // gradient 140 (87 %), of which the sort 17 and the join 6.  (Rows of 0 filled beside the
-// sort's kernels slowed those by as much: 143.)
+// sort's kernels slowed those by as much: 143.)  Many positions of narrow rows are far from that:
+// 131072 of 50257 x 512 bf16 83 us of 27, five launches one after the other (by themselves 4, 22 and
+// 7 of the sort, 37 of the sums, of which a warp has one tile with nothing of the next under
+// way, 9 of the join); 4096 of 32000 x 300 24 of 6 (3, 6, 5, 15, 5).  Partial sums have 256 columns
+// a tile at least, and a tile has a whole warp's lanes, whatever the row.
 
 #include <cuda_runtime.h>
 
@@ -365,7 +369,9 @@ cudaError_t forward_of(EmbedParams &p, cudaStream_t st) {
   p.lanes = lanes_for(p.D);
   const uint64_t spans = spans_for(p.D, p.lanes);
   if (spans > 2) return forward_by<W, E, V, 1, 4>(p, st);
-  // several positions at once only where there are enough to fill the SMs
+  // several positions at once only where there are enough to fill the SMs (bf16, 128 columns, one
+  // and four at once: 8192 positions 2.3 and 2.6 us, 16384 2.9 both, 131072 12.1 and 8.9; 512
+  // columns, one and two: 4096 2.3 and 2.4, 8192 2.95 and 3.15, 131072 30.3 and 29.1)
   if ((uint64_t)p.N * p.lanes < 32ull * 32 * 152)
     return spans == 2 ? forward_by<W, E, V, 1, 2>(p, st) : forward_by<W, E, V, 1, 1>(p, st);
   return spans == 2 ? forward_by<W, E, V, 2, 2>(p, st) : forward_by<W, E, V, 4, 1>(p, st);

@@ -22,6 +22,9 @@
 // 32768 x 2560 bf16: forward 59 us (83 % of the copy's bandwidth), backward 88 (84 %); 9973 x
 // 5003 floats 71 and 96 (82, 92 %).  What keeps them from it is a batch's steps, which
 // wait for one another: 48 and 45 % of the issue slots, DRAM 42 and 56 % by the counters.
+// Narrow rows are far from it: 131072 x 64 bf16 11 and 19 us of 5 and 7, 131072 x 512 79 and 89 of 40
+// and 59.  Their kernels wait too, for their own arithmetic and shuffles (40 and 36 % of the issue
+// slots, registers for 31 and 25 % of the warps), and dw and db take a launch of 4 us more.
 
 #include "norm.cuh"
 

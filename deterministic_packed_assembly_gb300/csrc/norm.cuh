@@ -18,7 +18,11 @@ namespace nsk {
 
 constexpr uint32_t kNormSMs = 152;
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr uint32_t kNormNarrow = 512;   // columns up to which rows go without the ring
+// Columns up to which a warp, or a part of one, has a row, without the ring: through it forward
+// 131072 x 512 bf16 take 91 us in place of 79, 384 columns 94 in place of 77, backward 87 and 92
+// in place of 89 and 86.  (Few rows of 512 columns backward are the other way: 700 in 9 us, 7
+// through the ring.)
+constexpr uint32_t kNormNarrow = 512;
 constexpr uint32_t kNormWarps = 15;     // of a row, at most: with the one that copies 512 threads
 constexpr uint32_t kNormKept = 5 * 32 * kOct * kNormWarps;  // columns that they have registers for
 constexpr int kWideThreads = 512;       // of a row of more columns
@@ -44,7 +48,9 @@ struct NormParams {
 // the kernel that takes it.  nb spans a warp.  Forward a row's exchange of sums costs each of
 // its warps the same, so that few are better while blocks are enough (32768 x 2560 bf16: ten
 // warps 90 us, five 71), but weights take registers; backward the sums of the weights'
-// gradients do.
+// gradients do, so that a warp has as few spans as 15 warps allow: 32768 x 2560 bf16 one span 90
+// us, two 96, three 99; 32768 x 3584 one 119, two 127; 16384 x 4096 two 74, three 85; 8192 x
+// 8192 three 78, five 122.
 struct NormShape {
   uint32_t lanes, nb, warps;
 };

@@ -5,8 +5,9 @@
 // column (i L + lane) V of the span, so that neighbouring lanes move neighbouring pieces.  V
 // = 8 moves 16 or 32 bytes at once; rows of an even number of elements are moved by
 // pairs, odd ones by single elements.  (Putting aligned 16 bytes of odd rows together from
-// two loads was measured: its instructions cost more than narrow accesses do.  100 columns in
-// 16 bits, 6 experts: combine 144 us; 1001 columns in 16 bits, 4 experts: 97 us.)
+// two loads was measured once, on the first kernels: 100 columns in 16 bits, 6 experts: combine 144
+// us; 1001 columns, 4 experts: 97.  Narrow pieces, with the distances known and whole spans without
+// bounds, take 54 and 50; the other way was not measured on those.)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -19,8 +19,8 @@ extern "C" {
 
 /* As the calls they are named after, where only the first `fed` rows are copied (a multiple
  * of 4, the largest batch, or at least N): of the others nothing comes, and the call's
- * kernel takes some tenths of a second to give up.  Rows that are read straight from memory do not
- * wait.  Errors: as the calls, and INVALID_ARG for another fed. */
+ * kernel takes some tenths of a second to give up.  Rows that are read straight from
+ * memory do not wait.  Errors: as the calls, and INVALID_ARG for another fed. */
 int ns_norm_probe_forward(const ns_norm_inputs *in, uint32_t fed, void *y, float *mean,
                           float *rstd, void *cuda_stream);
 int ns_norm_probe_backward(const ns_norm_inputs *in, uint32_t fed, const float *mean,
