@@ -157,7 +157,7 @@ def embed(weight: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
           doc: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Rows of a table at tokens, times ``scale``: [*tokens.shape, D].
 
-    ``weight`` [V, D] is float32, bfloat16 or float16 (rows at any distance), ``tokens``
+    ``weight`` [V, D] is float32, bfloat16 or float16 (rows at any distance from D on), ``tokens``
     int32 or int64 of any shape, contiguous, ``doc`` int32 of that shape.  Positions
     whose ``doc`` is below 0, and tokens outside [0, V), have rows of 0 and no part in
     the gradient.  The rows are of ``dtype``, or the weight's.
@@ -285,7 +285,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                doc: Optional[torch.Tensor] = None) -> torch.Tensor:
     """(x - mean) / sqrt(variance + eps) * weight + bias over the last dimension.
 
-    ``x`` [..., D] is float32, bfloat16 or float16, its rows at even distances; ``weight``
+    ``x`` [..., D] is float32, bfloat16 or float16, its rows at even distances from D on; ``weight``
     and ``bias`` [D] are float32 or of x's dtype, 1 and 0 if None; ``doc`` is int32 [...].
     Rows whose ``doc`` is below 0 are not read: they are 0, and have no part in a
     gradient.  Statistics and sums have 32 bits, the variance is that of the values less
@@ -428,7 +428,7 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, experts: int):
 
     ``ids`` (int32 [N, k], as ``route`` returns them; outside [0, experts): none) are the
     experts of each row of ``x`` ([N, D], float32, bfloat16 or float16, rows at any
-    distance).  Expert e's rows are ``rows[order.offsets[e]:order.offsets[e + 1]]``, in
+    distance from D on).  Expert e's rows are ``rows[order.offsets[e]:order.offsets[e + 1]]``, in
     the tokens' order; ``rows[order.place[n, j]]`` is ``x[n]``.  Rows from
     ``order.offsets[experts]`` on, as many as choices without an expert, are 0.
 
